@@ -194,6 +194,28 @@ size_t forward_scratch_bytes(const LinearPlan &p) {
   return std::max(p.off_part + lora_part_floats(p.T, p.r, p.K) * 4, qsplit ? p.off_qpart + qsplit * 4 : 0);
 }
 
+// The shapes the head's loss accepts.
+bool head_shape_ok(int64_t T, int64_t V, int64_t D) {
+  return D >= kBlock && D % kBlock == 0 && D <= kHeadMaxDim && product_ok(T, D) && product_ok(V, D);
+}
+
+// The loss of a bf16 head (w) or a packed one (q), the other one nullptr and both already checked.
+qlora_status head_loss(const uint16_t *h, int64_t T, const uint16_t *w, const QWeight *q, int64_t V, int64_t D,
+                       const int64_t *target, const float *weight, float scale, float *loss, float *lse,
+                       uint16_t *grad_h, void *ws, size_t ws_bytes, void *stream) {
+  if (!head_shape_ok(T, V, D)) return QLORA_ERR_SHAPE;
+  if (!std::isfinite(scale)) return QLORA_ERR_VALUE;
+  if (!h || !target || !loss || !ws) return QLORA_ERR_NULL;
+  if (!aligned16(h) || !aligned16(target) || !aligned16(loss) || !aligned16(ws) || (weight && !aligned16(weight)) ||
+      (lse && !aligned16(lse)) || (grad_h && !aligned16(grad_h)))
+    return QLORA_ERR_ALIGN;
+  const HeadPlan p = plan_head(T, V, D, grad_h != nullptr, q != nullptr);
+  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
+  hipError_t e = launch_head_loss(p, h, w, q, target, weight, scale, loss, lse, grad_h, (char *)ws, tables().cb,
+                                  (hipStream_t)stream);
+  return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -508,6 +530,29 @@ qlora_status qlora_dropout_mask(const uint16_t *x, int64_t T, int64_t K, double 
   return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
 }
 
+size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad, int packed) {
+  if (!head_shape_ok(T, V, D)) return 0;
+  return plan_head(T, V, D, grad != 0, packed != 0).total;
+}
+
+qlora_status qlora_head_loss(const uint16_t *h, int64_t T, const uint16_t *w, int64_t V, int64_t D,
+                             const int64_t *target, const float *weight, float scale, float *loss, float *lse,
+                             uint16_t *grad_h, void *ws, size_t ws_bytes, void *stream) {
+  if (!w) return QLORA_ERR_NULL;
+  if (!aligned16(w)) return QLORA_ERR_ALIGN;
+  return head_loss(h, T, w, nullptr, V, D, target, weight, scale, loss, lse, grad_h, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_weight *q, const int64_t *target,
+                                 const float *weight, float scale, float *loss, float *lse, uint16_t *grad_h,
+                                 void *ws, size_t ws_bytes, void *stream) {
+  const qlora_status s = check_weight(q);
+  if (s != QLORA_OK) return s;
+  const QWeight qw = qweight(q);
+  return head_loss(h, T, nullptr, &qw, q->n_out, q->n_in, target, weight, scale, loss, lse, grad_h, ws, ws_bytes,
+                   stream);
+}
+
 void qlora_kernel_timing_enable(int enable) { kernel_timing_enable(enable != 0); }
 
 qlora_status qlora_kernel_timing_read(int64_t *launches, double *total_ms) {
@@ -527,7 +572,8 @@ qlora_status qlora_status_read(const void *ws, void *stream) {
   if (hipStreamSynchronize((hipStream_t)stream) != hipSuccess) return QLORA_ERR_HIP;
   uint32_t word = 0;
   if (hipMemcpy(&word, ws, sizeof(word), hipMemcpyDeviceToHost) != hipSuccess) return QLORA_ERR_HIP;
-  return (word & 1u) ? QLORA_ERR_NONFINITE : QLORA_OK;
+  if (word & 1u) return QLORA_ERR_NONFINITE;
+  return (word & 2u) ? QLORA_ERR_VALUE : QLORA_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,778 @@
+// The loss of the language-model head over a large vocabulary, with the
+// gradient of the hidden states, without ever holding the logits (gfx950).
+//
+//   l_tv  = sum_d h_td W_vd                      (bf16 operands, fp32 sums)
+//   lse_t = log sum_v exp(l_tv),   loss_t = lse_t - l_t,y(t)
+//   grad_h_t = c_t (sum_v p_tv W_v - W_y(t)),    p_tv = exp(l_tv - lse_t)
+//
+// The head is frozen, as every weight of this library, so there is no
+// gradient for W.  Per piece of the vocabulary:
+//
+//   head_logits   one 256 x 256 tile of l per workgroup; its epilogue takes,
+//                 per token and 128 words, the integer n = ceil(log2 e max l)
+//                 and writes e_tv = 2^(l log2 e - n) in bf16 and s = sum e
+//   head_fold     running N_t = max n and S_t = sum 2^(n - N) s over the
+//                 tiles, and the distance N - n of each tile as a byte
+//   head_grad     G_td += sum_v 2^(n - N) e_tv W_vd: the factor of a tile is a
+//                 power of two, so it is one saturating subtraction from the
+//                 exponent field of the bf16 operand, exact
+//
+// and head_finish forms grad_h = c (G / S - (S - e_y) / S W_y).  So the
+// gradient needs the two products it cannot do without (4 T V D operations)
+// and no second run over the logits.  The target's own term is kept out of e
+// and S and added apart: 1 - p_y = S_others / S has no cancellation, and
+// loss = log1p(S_others / e_y) keeps its relative precision for a token the
+// model is sure of.  e is rounded to bf16 (half a step, 2^-8 of it) because the
+// matrix cores take it in that type; S sums the unrounded fp32 values.
+//
+// Tokens whose target is negative carry no loss.  A scan lists the others, the
+// products gather their rows by that list, and tiles past its end do nothing.
+
+#include <algorithm>
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kTileV = 256;    // words (logits) or hidden columns (gradient) of a workgroup's tile
+constexpr int kTileT = 256;    // tokens of a workgroup's tile
+constexpr int kStatV = 128;    // words that share one exponent n per token
+constexpr int kStep = 64;      // contraction step
+constexpr int kThreads = 512;  // eight waves: 2 along the words or columns, 4 along the tokens
+constexpr int kUnit = 16384;   // bytes of half an operand tile of a step: 128 rows of 128 bytes
+constexpr int kStage = 4 * kUnit;
+constexpr float kLog2eHi = 1.44269502162933349609375f;  // fl32(log2 e), and the rest of it
+constexpr float kLog2eLo = 1.92596299112661746887e-8f;
+constexpr float kLn2 = 0.693147182464599609375f;        // fl32(ln 2), and the rest of it
+constexpr float kLn2Lo = -1.90465429995776804525e-9f;
+// |n| from which a row counts as overflown (its loss and gradient are NaN): below it integers and
+// their differences are exact in fp32 and l log2 e - n is formed to 2^-24 of l
+constexpr float kMaxExponent = 4194304.0f;
+constexpr float kNoExponent = -3.0e38f;  // n of a tile without any word
+
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(lds_void_t *)p; }
+
+// One 16-byte-per-lane copy from global memory to LDS bytes lds + 16 lane.  As asm, since the
+// compiler would otherwise make every later LDS read wait for all copies in flight; it has no
+// register result, and the callers wait for it by count.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16(const char *sbase, uint32_t voff, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1"
+      :
+      : "v"(voff), "s"(sbase), "s"(lds)
+      : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+#define HEAD_WAIT_VM(n) asm volatile("s_waitcnt vmcnt(" #n ")" ::: "memory")
+#define HEAD_WAIT_LDS() asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory")
+
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+// A pointer that is the same in every lane, moved to scalar registers.
+__device__ __forceinline__ const char *uniform(const void *p) {
+  const uint64_t a = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return (const char *)(((uint64_t)hi << 32) | lo);
+}
+
+// LDS layout of an operand tile: rows of 128 bytes, eight 16-byte chunks each, chunk c of row r at
+// position c ^ swizzle(r).  The LDS serves 16-byte reads of 16 lanes at a time from 64 banks (two
+// rows), so row pairs shift the chunks; the transpose reads take 32-byte pieces of rows r..r+3 and
+// r + 8..r + 11 (or + 16), which then fall on different banks too.
+__device__ __forceinline__ int swizzle_rows(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int swizzle_cols(int r) { return (((r >> 1) & 1) | ((((r >> 3) ^ (r >> 4)) & 1) << 1)) << 1; }
+
+// The product shared by both matrix kernels: acc[m][t] over a contraction of `steps` steps of 64.
+// Left operand: 256 rows of a row-major matrix whose contraction index is contiguous (kTrans =
+// false: words of W, contraction over d), or 256 columns of one whose rows are the contraction
+// (kTrans = true: columns d of W, contraction over the words).  Right operand: 256 rows (tokens).
+//
+// Two groups of four waves (one wave of each per SIMD) run half a phase apart: while one group
+// multiplies (16 MFMAs a wave), the other reads its next fragments from LDS and starts the copies
+// that refill it.  A step has four phases, (rows 0..63 of the wave's 128, contraction 0..31), (0..63,
+// 32..63), (64..127, 0..31), (64..127, 32..63); the tokens' fragments are read in the first two.  A
+// stage's tokens and first rows are free after phase 1, its other rows after phase 3, so each is
+// refilled for step k + 2 at once, five to six phases before it is read: two stages (128 KB) are
+// enough to hide the memory's latency.
+//
+// Every wave reads its LDS data completely (lgkmcnt(0)) before the barrier that ends a read phase, so
+// a refill started after that barrier cannot overtake a read; each wave waits for its own copies
+// (vmcnt, in order of issue) before the barrier after which any wave reads them.
+struct Operands {
+  const char *left;    // uniform: the tile's first row (kTrans: first column)
+  const char *right;   // uniform
+  uint32_t left_pitch; // kTrans: bytes between rows of the contraction
+  uint32_t left_off[4];   // per lane: copies of rows 0..63 (0, 1) and 64..127 (2, 3) of both row halves
+  uint32_t right_off[4];
+  int64_t left_step, right_step;  // bytes per contraction step
+  int left_rows;       // kTrans: rows of the contraction that exist (the last one stands for those beyond)
+};
+
+template <bool kTrans>
+__device__ __forceinline__ void copy_left(const Operands &o, int half, int k, int steps, char *stage, int wave,
+                                          int lane) {
+  const int kc = min(k, steps - 1);  // past the end: any valid rows, never read
+  const char *base = o.left + kc * o.left_step;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t off = o.left_off[2 * half + j];
+    if (kTrans) {
+      // row (2 wave + j) * 8 + lane / 8 of the unit: contraction row of a 64-row sub-tile
+      const int row = ((2 * wave + j) * 8 + (lane >> 3)) & 63;
+      off += (uint32_t)__mul24(min(row, o.left_rows - 1 - kc * kStep), (int)o.left_pitch);
+    }
+    dma16(base, off, lds_addr(stage + half * kUnit + (2 * wave + j) * 1024));
+  }
+}
+
+__device__ __forceinline__ void copy_right(const Operands &o, int k, int steps, char *stage, int wave) {
+  const int kc = min(k, steps - 1);
+  const char *base = o.right + kc * o.right_step;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dma16(base, o.right_off[j], lds_addr(stage + 2 * kUnit + (4 * wave + j) * 1024));
+}
+
+template <bool kTrans>
+__device__ __forceinline__ void read_left(const char *stage, int half, int kk, int wm, int lane, u32x4 (&a)[4]) {
+  const char *unit = stage + half * kUnit + wm * 8192;
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    if (!kTrans) {
+      const int r = 16 * f + (lane & 15), c = 4 * kk + (lane >> 4);
+      a[f] = *(const u32x4 *)(unit + r * 128 + ((c ^ swizzle_rows(r)) << 4));
+    } else {
+      // lane s of a 16-lane group points at contraction row .. + s/4 and columns 4 (s%4); it
+      // receives four consecutive contraction rows of column s
+      const int s = lane & 15;
+      uint2 part[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 32 * kk + 8 * (lane >> 4) + 4 * h + (s >> 2);
+        const int c = 2 * f + ((s & 3) >> 1);
+        const char *p = unit + r * 128 + ((c ^ swizzle_cols(r)) << 4) + (s & 1) * 8;
+        part[h] = __builtin_bit_cast(
+            uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((v4s __attribute__((address_space(3))) *)(lds_void_t *)p));
+      }
+      a[f] = u32x4{part[0].x, part[0].y, part[1].x, part[1].y};
+    }
+  }
+}
+
+__device__ __forceinline__ void read_right(const char *stage, int kk, int wn, int lane, u32x4 (&b)[4]) {
+  const char *unit = stage + 2 * kUnit + wn * 8192;
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int r = 16 * f + (lane & 15), c = 4 * kk + (lane >> 4);
+    b[f] = *(const u32x4 *)(unit + r * 128 + ((c ^ swizzle_rows(r)) << 4));
+  }
+}
+
+// Subtracts a power of two from the exponents of eight bf16 values >= 0 (0 where it falls below).
+__device__ __forceinline__ void scale_down(u32x4 &v, uint32_t shift) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t word = v[i];  // a value of its own: a bit cast of a vector's element takes element 0
+    const u16x2 less = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, word),
+                                                     __builtin_bit_cast(u16x2, shift));
+    v[i] = __builtin_bit_cast(uint32_t, less);
+  }
+}
+
+__device__ __forceinline__ void multiply(const u32x4 (&a)[4], const u32x4 (&b)[4], f32x4 (*acc)[4]) {
+  __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m]), as_bf16x8(b[n]), acc[m][n], 0, 0, 0);
+  __builtin_amdgcn_s_setprio(0);
+}
+
+// acc[m][n][q] of lane l: left row 128 wm + 16 m + 4 (l/16) + q, token 64 wn + 16 n + l%16.
+// shifts: the bytes N - n of the tile's tokens, [steps / 2][256] (kTrans only).
+template <bool kTrans>
+__device__ __forceinline__ void product(const Operands &o, int steps, char *lds, const uint8_t *shifts,
+                                        f32x4 (&acc)[8][4]) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave >> 1) & 1, wn = (wave & 1) + 2 * (wave >> 2);
+  const bool late = wave >= 4;
+  copy_right(o, 0, steps, lds, wave);
+  copy_left<kTrans>(o, 0, 0, steps, lds, wave, lane);
+  copy_left<kTrans>(o, 1, 0, steps, lds, wave, lane);
+  copy_right(o, 1, steps, lds + kStage, wave);
+  copy_left<kTrans>(o, 0, 1, steps, lds + kStage, wave, lane);
+  HEAD_WAIT_VM(8);
+  barrier();
+  if (late) barrier();
+  u32x4 a[4], b0[4], b1[4];
+  uint32_t shift[4] = {0u, 0u, 0u, 0u};
+  for (int k = 0; k < steps; ++k) {
+    char *stage = lds + (k & 1) * kStage, *next = lds + ((k + 1) & 1) * kStage;
+    // phase 0
+    if (kTrans && (k & 1) == 0) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        shift[n] = (uint32_t)shifts[(k >> 1) * kTileT + 64 * wn + 16 * n + (lane & 15)] * 0x00800080u;
+    }
+    read_right(stage, 0, wn, lane, b0);
+    read_left<kTrans>(stage, 0, 0, wm, lane, a);
+    copy_left<kTrans>(o, 1, k + 1, steps, next, wave, lane);
+    HEAD_WAIT_LDS();
+    barrier();
+    if (kTrans) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) scale_down(b0[n], shift[n]);
+    }
+    multiply(a, b0, acc);
+    barrier();
+    // phase 1
+    read_right(stage, 1, wn, lane, b1);
+    read_left<kTrans>(stage, 0, 1, wm, lane, a);
+    HEAD_WAIT_LDS();
+    HEAD_WAIT_VM(8);
+    barrier();
+    if (kTrans) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) scale_down(b1[n], shift[n]);
+    }
+    multiply(a, b1, acc);
+    barrier();
+    // phase 2
+    read_left<kTrans>(stage, 1, 0, wm, lane, a);
+    copy_right(o, k + 2, steps, stage, wave);
+    HEAD_WAIT_LDS();
+    barrier();
+    multiply(a, b0, acc + 4);
+    barrier();
+    // phase 3
+    read_left<kTrans>(stage, 1, 1, wm, lane, a);
+    copy_left<kTrans>(o, 0, k + 2, steps, stage, wave, lane);
+    HEAD_WAIT_LDS();
+    HEAD_WAIT_VM(8);
+    barrier();
+    multiply(a, b1, acc + 4);
+    barrier();
+  }
+  if (!late) barrier();
+  HEAD_WAIT_VM(0);  // no copy may outlive the loop: the LDS is reused or given up
+  barrier();
+}
+
+// Tile of a workgroup.  Workgroup ids go round the eight XCDs, so id / 8 counts within one: each XCD
+// takes a contiguous run of tiles, ordered so that 32 neighbours (one per CU) cover 8 left tiles by 4
+// token tiles, whose operands its L2 then serves.
+struct Tile {
+  int64_t left, token;
+};
+__device__ __forceinline__ Tile tile_of(int64_t id, int64_t nleft, int64_t ntoken) {
+  const int64_t total = nleft * ntoken, per = total >> 3, rest = total & 7;
+  const int64_t x = id & 7, j = id >> 3;
+  const int64_t t = x * per + min(x, rest) + j;  // XCDs below `rest` take one tile more
+  const int64_t group = t / (8 * ntoken), first = group * 8;
+  const int64_t width = min((int64_t)8, nleft - first), in = t - first * ntoken;
+  return Tile{first + in % width, in / width};
+}
+
+// ---------------------------------------------------------------------------
+
+// Lists the tokens of a chunk that carry a loss: rows[j] = token, place[token] = j, or -1 (ignored)
+// or -2 (target out of range).  One workgroup; state[0] |= 2 on a bad target, state[1] = the count.
+__global__ __launch_bounds__(1024) void head_scan(const int64_t *__restrict__ target, int T, int64_t V, bool first,
+                                                  int *__restrict__ rows, int *__restrict__ place,
+                                                  uint32_t *__restrict__ state) {
+  __shared__ int wave_sum[16];
+  __shared__ int total;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  bool bad = false;
+  int base = 0;
+  for (int t0 = 0; t0 < T; t0 += 1024) {
+    const int t = t0 + tid;
+    const int64_t y = t < T ? target[t] : -1;
+    const bool live = y >= 0 && y < V;
+    bad |= y >= V;
+    const uint64_t mask = __ballot(live);
+    if (lane == 0) wave_sum[wave] = __popcll(mask);
+    __syncthreads();
+    int before = base, all = 0;
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? wave_sum[w] : 0;
+      all += wave_sum[w];
+    }
+    const int j = before + __popcll(mask & ((1ull << lane) - 1));
+    if (t < T) {
+      if (live) rows[j] = t;
+      place[t] = live ? j : (y >= V ? -2 : -1);
+    }
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) total = 0;
+  __syncthreads();
+  if (bad) total = 1;
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t before = first ? 0u : state[0];
+    state[0] = before | (total ? 2u : 0u);
+    state[1] = (uint32_t)base;
+  }
+}
+
+// One tile of the logits, see the top.  e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
+// [tile of 128 words][tpad].
+__global__ __launch_bounds__(kThreads, 2) void head_logits(
+    const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, const int64_t *__restrict__ target, int64_t v0,
+    int64_t nv, int D, int64_t nleft, int64_t ntoken, const int *__restrict__ rows,
+    const uint32_t *__restrict__ state, uint16_t *__restrict__ e, int64_t pitch, float *__restrict__ exponent,
+    float *__restrict__ sum, int64_t tpad, float *__restrict__ target_logit) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+  const int live = (int)state[1];
+  const Tile tile = tile_of(blockIdx.x, nleft, ntoken);
+  const int t0 = (int)tile.token * kTileT;
+  if (t0 >= live) return;
+  const int64_t vt = tile.left * kTileV;  // within the piece
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave >> 1) & 1, wn = (wave & 1) + 2 * (wave >> 2);
+  const uint32_t row_bytes = (uint32_t)D * 2u;
+
+  Operands o;
+  o.left = uniform(w + vt * D);
+  o.right = uniform(h);
+  o.left_step = o.right_step = 2 * kStep;
+  o.left_pitch = 0;
+  o.left_rows = 0;
+  const int last_v = (int)min((int64_t)kTileV, nv - vt) - 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // unit row (2 wave + i%2) 8 + lane/8: word 128 (row / 64) + 64 (i / 2) + row % 64
+    const int r = (2 * wave + (i & 1)) * 8 + (lane >> 3);
+    const int v = min(128 * (r >> 6) + 64 * (i >> 1) + (r & 63), last_v);
+    o.left_off[i] = (uint32_t)v * row_bytes + (((lane & 7) ^ swizzle_rows(r)) << 4);
+    const int rt = (4 * wave + i) * 8 + (lane >> 3);
+    o.right_off[i] = (uint32_t)rows[min(t0 + rt, live - 1)] * row_bytes + (((lane & 7) ^ swizzle_rows(rt)) << 4);
+  }
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  product<false>(o, D / kStep, lds, nullptr, acc);
+
+  // rows (words) of this lane: 128 wm + 16 m + 4 (lane / 16) + q
+  const int vl = 128 * wm + 4 * (lane >> 4);
+  const int nvt = last_v + 1;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int t = t0 + 64 * wn + 16 * n + (lane & 15);
+    const bool on = t < live;
+    const int64_t place = on ? target[rows[t]] - v0 - vt : -1;  // the target's word, if it is one of this tile's
+    const int y = place >= 0 && place < kTileV ? (int)place : -1;
+    float top = -INFINITY;
+    bool odd = false;  // NaN among the logits
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float l = acc[m][n][q];
+        const bool in = vl + 16 * m + q < nvt;
+        odd |= in && l != l;
+        top = fmaxf(top, in ? l : -INFINITY);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // a finite n whatever the logits are: NaN and infinite sums show in s
+    const float x = fminf(fmaxf(top * kLog2eHi, -2.0f * kMaxExponent), 2.0f * kMaxExponent);
+    const float ex = 128 * wm < nvt ? ceilf(x) : kNoExponent;
+    float s = 0.f;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      float p[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float l = acc[m][n][q];
+        const int v = vl + 16 * m + q;
+        p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2eLo, __builtin_fmaf(l, kLog2eHi, -ex)));
+        if (v >= nvt) p[q] = 0.f;
+        if (v == y) {
+          target_logit[t] = l;
+          p[q] = 0.f;
+        }
+        s += p[q];
+      }
+      if (e && on)
+        *(uint2 *)(e + (int64_t)t * pitch + vt + vl + 16 * m) =
+            make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+    }
+    if (odd) s = NAN;
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16 && on) {
+      const int64_t at = (2 * tile.left + wm) * tpad + t;
+      exponent[at] = ex;
+      sum[at] = s;
+    }
+  }
+}
+
+// Folds the piece's tiles into the running exponent N and sum S of each token: 16 tokens and 16
+// lanes along the tiles a workgroup.  shift: N - n of each tile, at most 255 (which leaves nothing
+// of any bf16 value); factor: 2^(N before - N), for what the pieces before have summed.
+__global__ __launch_bounds__(256) void head_fold(const float *__restrict__ exponent, const float *__restrict__ sum,
+                                                 int64_t tpad, int tiles, bool first,
+                                                 const uint32_t *__restrict__ state, float *__restrict__ N,
+                                                 float *__restrict__ S, uint8_t *__restrict__ shift,
+                                                 float *__restrict__ factor) {
+  __shared__ float part[16][17];
+  const int live = (int)state[1];
+  if ((int)blockIdx.x * 16 >= live) return;
+  const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int t = min((int)blockIdx.x * 16 + c, live - 1);
+  float top = kNoExponent;
+  for (int i = g; i < tiles; i += 16) top = fmaxf(top, exponent[i * tpad + t]);
+  part[g][c] = top;
+  __syncthreads();
+  const float before = first ? kNoExponent : N[t];
+  float now = before;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) now = fmaxf(now, part[i][c]);
+  __syncthreads();
+  float s = 0.f;
+  for (int i = g; i < tiles; i += 16) {
+    const float d = now - exponent[i * tpad + t];
+    s += sum[i * tpad + t] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
+    if (shift) shift[i * tpad + t] = (uint8_t)fminf(d, 255.f);
+  }
+  part[g][c] = s;
+  __syncthreads();
+  if (g == 0 && (int)blockIdx.x * 16 + c < live) {
+    const float f = first ? 0.f : __builtin_amdgcn_exp2f(-fminf(now - before, 300.f));
+    float all = first ? 0.f : S[t] * f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) all += part[i][c];
+    N[t] = now;
+    S[t] = all;
+    factor[t] = f;
+  }
+}
+
+// One tile (256 columns d, 256 tokens) of G over one split of the piece's words, see the top.
+// part: [split][tokens][D] fp32, in units of 2^N.
+__global__ __launch_bounds__(kThreads, 2) void head_grad(
+    const uint16_t *__restrict__ e, int64_t pitch, const uint16_t *__restrict__ w, int64_t nv, int D, int64_t nleft,
+    int64_t ntoken, int64_t split_words, const uint32_t *__restrict__ state, const uint8_t *__restrict__ shift,
+    int64_t tpad, const float *__restrict__ factor, bool first, float *__restrict__ part, int64_t part_stride) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t shifts[kHeadMaxSplit / kStatV * kTileT];
+  const int live = (int)state[1];
+  const int64_t tiles = nleft * ntoken;
+  const int64_t split = blockIdx.x / tiles;
+  const Tile tile = tile_of(blockIdx.x % tiles, nleft, ntoken);
+  const int t0 = (int)tile.token * kTileT;
+  if (t0 >= live) return;
+  const int64_t vb = split * split_words;  // a multiple of 128
+  const int words = (int)max((int64_t)0, min(split_words, nv - vb));  // 0: only the sums before are rescaled
+  const int d0 = (int)tile.left * kTileV;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave >> 1) & 1, wn = (wave & 1) + 2 * (wave >> 2);
+  const int steps = (words + kStep - 1) / kStep;
+
+  {  // the tile's shift bytes (tpad is a multiple of 256, so whole words of four tokens)
+    const int n = (words + kStatV - 1) / kStatV * (kTileT / 4);
+    const uint8_t *src = shift + vb / kStatV * tpad + t0;
+    for (int i = threadIdx.x; i < n; i += kThreads)
+      ((uint32_t *)shifts)[i] = *(const uint32_t *)(src + (i >> 6) * tpad + 4 * (i & 63));
+    __syncthreads();
+  }
+  Operands o;
+  o.left = uniform(w + vb * D + d0);
+  o.right = uniform(e + (int64_t)t0 * pitch + vb);
+  o.left_pitch = (uint32_t)D * 2u;
+  o.left_step = (int64_t)kStep * D * 2;
+  o.right_step = 2 * kStep;
+  o.left_rows = words;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // unit row r: columns 128 (r / 64) + 64 (i / 2) .. + 63, contraction row r % 64
+    const int r = (2 * wave + (i & 1)) * 8 + (lane >> 3);
+    const int d = min(d0 + 128 * (r >> 6) + 64 * (i >> 1), D - 64) - d0;
+    o.left_off[i] = (uint32_t)(2 * d) + (((lane & 7) ^ swizzle_cols(r & 63)) << 4);
+    const int rt = (4 * wave + i) * 8 + (lane >> 3);
+    o.right_off[i] = (uint32_t)min(rt, live - 1 - t0) * (uint32_t)(2 * pitch) + (((lane & 7) ^ swizzle_rows(rt)) << 4);
+  }
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (words > 0) product<true>(o, steps, lds, shifts, acc);
+
+  float *out = part + split * part_stride;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int t = t0 + 64 * wn + 16 * n + (lane & 15);
+    if (t >= live) continue;
+    const float f = first ? 0.f : factor[t];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const int d = d0 + 128 * wm + 16 * m + 4 * (lane >> 4);
+      if (d >= D) continue;
+      f32x4 *p = (f32x4 *)(out + (int64_t)t * D + d);
+      f32x4 v = acc[m][n];
+      if (!first) {
+        const f32x4 old = *p;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(old[q], f, v[q]);
+      }
+      *p = v;
+    }
+  }
+}
+
+// loss, lse and what the gradient needs of one token: 1 / S and S_others / S.
+struct Outcome {
+  float loss, lse, inv, other;
+};
+__device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
+  Outcome r;
+  const float ey = __builtin_amdgcn_exp2f(__builtin_fmaf(ly, kLog2eLo, __builtin_fmaf(ly, kLog2eHi, -N)));
+  const float all = others + ey;
+  const float base = __builtin_fmaf(N, kLn2, N * kLn2Lo);
+  if (others <= ey) {
+    r.loss = log1pf(others / ey);
+    r.lse = ly + r.loss;
+  } else {
+    r.lse = base + logf(all);
+    // N ln 2 - l_y first: the two are close when the loss is small
+    r.loss = (__builtin_fmaf(N, kLn2, -ly) + N * kLn2Lo) + logf(all);
+  }
+  r.inv = 1.0f / all;
+  r.other = others / all;
+  if (!(all > 0.f && all < INFINITY) || !(fabsf(N) < kMaxExponent)) r.loss = r.lse = r.inv = r.other = NAN;
+  return r;
+}
+
+// Loss and lse of every token of the chunk, one thread each.
+__global__ __launch_bounds__(256) void head_losses(int T, const int *__restrict__ place, const float *__restrict__ N,
+                                                   const float *__restrict__ S,
+                                                   const float *__restrict__ target_logit, float *__restrict__ loss,
+                                                   float *__restrict__ lse) {
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= T) return;
+  const int j = place[t];
+  float a = j == -2 ? NAN : 0.f, b = a;
+  if (j >= 0) {
+    const Outcome r = outcome(N[j], S[j], target_logit[j]);
+    a = r.loss;
+    b = r.lse;
+  }
+  loss[t] = a;
+  if (lse) lse[t] = b;
+}
+
+// grad_h of one token a workgroup (and its loss and lse), eight columns a thread and turn.
+__global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place, const float *__restrict__ N,
+                                                   const float *__restrict__ S,
+                                                   const float *__restrict__ target_logit,
+                                                   const int64_t *__restrict__ target,
+                                                   const uint16_t *__restrict__ wy, bool by_token,
+                                                   const float *__restrict__ weight, float scale, const float *__restrict__ part, int splits,
+                                                   int64_t part_stride, int D, float *__restrict__ loss,
+                                                   float *__restrict__ lse, uint16_t *__restrict__ grad) {
+  const int t = blockIdx.x;
+  const int j = place[t];
+  uint16_t *g = grad + (int64_t)t * D;
+  if (j < 0) {
+    const uint32_t fill = j == -2 ? 0x7FC07FC0u : 0u;
+    for (int c = threadIdx.x * 8; c < D; c += 2048) *(u32x4 *)(g + c) = u32x4{fill, fill, fill, fill};
+    if (threadIdx.x == 0) {
+      loss[t] = j == -2 ? NAN : 0.f;
+      if (lse) lse[t] = j == -2 ? NAN : 0.f;
+    }
+    return;
+  }
+  const Outcome r = outcome(N[j], S[j], target_logit[j]);
+  if (threadIdx.x == 0) {
+    loss[t] = r.loss;
+    if (lse) lse[t] = r.lse;
+  }
+  const float c_t = weight ? scale * weight[t] : scale;
+  const float a = c_t * r.inv, b = c_t * r.other;
+  const uint16_t *wr = wy + (by_token ? (int64_t)t : target[t]) * D;  // the target's row of W
+  const float *p = part + (int64_t)j * D;
+  for (int c = threadIdx.x * 8; c < D; c += 2048) {
+    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+    for (int s = 0; s < splits; ++s) {
+      const f32x4 x = *(const f32x4 *)(p + s * part_stride + c), y = *(const f32x4 *)(p + s * part_stride + c + 4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        lo[q] += x[q];
+        hi[q] += y[q];
+      }
+    }
+    const u32x4 wv = *(const u32x4 *)(wr + c);
+    u32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float g0 = q < 2 ? lo[2 * q] : hi[2 * q - 4], g1 = q < 2 ? lo[2 * q + 1] : hi[2 * q - 3];
+      o[q] = pack_bf16x2(__builtin_fmaf(a, g0, -b * bf16_lo(wv[q])), __builtin_fmaf(a, g1, -b * bf16_hi(wv[q])));
+    }
+    *(u32x4 *)(g + c) = o;
+  }
+}
+
+// The decoded rows of the targets of a packed head, [T][D] bf16 in token order (one workgroup a
+// token): the decode of every use of the weight, one value at a time.
+__global__ __launch_bounds__(256) void head_target_rows(QWeight q, Codebook cb, const int *__restrict__ place,
+                                                        const int64_t *__restrict__ target,
+                                                        uint16_t *__restrict__ out) {
+  __shared__ float level[16];
+  if (threadIdx.x < 16) level[threadIdx.x] = cb.v[threadIdx.x];
+  __syncthreads();
+  const int t = blockIdx.x;
+  if (place[t] < 0) return;
+  const int64_t e0 = target[t] * q.n_in;
+  for (int c = threadIdx.x * 2; c < q.n_in; c += 512) {
+    const int64_t el = e0 + c, block = el / kBlock;
+    const float c1 = q.dq ? decode_constant(q.fp8[block], q.s2[block / kGroup], *q.mu) : q.s2[block];
+    const uint32_t byte = q.codes[el >> 1];
+    *(uint32_t *)(out + (int64_t)t * q.n_in + c) =
+        pack_bf16x2(decode_product(level[byte & 15u], c1), decode_product(level[byte >> 4], c1));
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+}  // namespace
+
+HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
+  HeadPlan p;
+  p.T = T;
+  p.V = V;
+  p.D = D;
+  p.grad = grad;
+  p.packed = packed;
+  p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
+  p.tpad = cdiv(p.chunk, kTileT) * kTileT;
+  // Words of a piece: 64 MB of e (grad) and of decoded weight (packed); nothing else grows with it.
+  int64_t vc = cdiv(V, kTileV) * kTileV;
+  // The exponents and sums of its tiles stay within 64 MB too.
+  const int64_t budget = (int64_t)32 << 20;
+  vc = std::min(vc, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
+  if (grad) vc = std::min(vc, std::max<int64_t>(budget / p.tpad / kTileV * kTileV, 8 * kTileV));
+  if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
+  p.pieces = cdiv(V, vc);
+  p.words = cdiv(cdiv(V, p.pieces), kTileV) * kTileV;
+  p.pieces = cdiv(V, p.words);
+  // Splits of the gradient's contraction: one round of 256 workgroups at least, ranges of whole
+  // tiles of 128 words, 512 of them at least, and a range's shift bytes have to fit the LDS.
+  p.splits = 1;
+  if (grad) {
+    const int64_t tiles = cdiv(D, kTileV) * cdiv(p.chunk, kTileT);
+    p.splits = std::max(cdiv(p.words, kHeadMaxSplit), std::min(cdiv(256, tiles), std::max<int64_t>(p.words / 512, 1)));
+    p.split_words = cdiv(cdiv(p.words, p.splits), kStatV) * kStatV;
+    p.splits = cdiv(p.words, p.split_words);
+  } else {
+    p.split_words = 0;
+  }
+  const int64_t stat = p.words / kStatV * p.tpad;
+  size_t off = 256;
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  p.off_rows = take((size_t)p.chunk * 4);
+  p.off_place = take((size_t)p.chunk * 4);
+  p.off_logit = take((size_t)p.chunk * 4);
+  p.off_n = take((size_t)p.chunk * 4);
+  p.off_s = take((size_t)p.chunk * 4);
+  p.off_factor = take((size_t)p.chunk * 4);
+  p.off_exponent = take((size_t)stat * 4);
+  p.off_sum = take((size_t)stat * 4);
+  p.off_shift = grad ? take((size_t)stat) : 0;
+  p.off_e = grad ? take((size_t)p.chunk * p.words * 2) : 0;
+  p.off_part = grad ? take((size_t)p.splits * p.chunk * D * 4) : 0;
+  p.off_w = packed ? take((size_t)p.words * D * 2) : 0;
+  p.off_wy = packed && grad ? take((size_t)p.chunk * D * 2) : 0;
+  p.total = off;
+  return p;
+}
+
+hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t *w, const QWeight *q,
+                            const int64_t *target, const float *weight, float scale, float *loss, float *lse,
+                            uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st) {
+  uint32_t *state = (uint32_t *)ws;
+  int *rows = (int *)(ws + p.off_rows), *place = (int *)(ws + p.off_place);
+  float *logit = (float *)(ws + p.off_logit), *N = (float *)(ws + p.off_n), *S = (float *)(ws + p.off_s);
+  float *factor = (float *)(ws + p.off_factor), *exponent = (float *)(ws + p.off_exponent);
+  float *sum = (float *)(ws + p.off_sum), *part = (float *)(ws + p.off_part);
+  uint8_t *shift = p.grad ? (uint8_t *)(ws + p.off_shift) : nullptr;
+  uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
+  uint16_t *wp = (uint16_t *)(ws + p.off_w), *wy = (uint16_t *)(ws + p.off_wy);
+  const int D = (int)p.D;
+  for (int64_t c0 = 0; c0 < p.T; c0 += p.chunk) {
+    const int T = (int)std::min(p.chunk, p.T - c0);
+    const int64_t ntoken = cdiv(T, kTileT), stride = p.chunk * p.D;
+    const uint16_t *hc = h + c0 * p.D;
+    const int64_t *yc = target + c0;
+    head_scan<<<1, 1024, 0, st>>>(yc, T, p.V, c0 == 0, rows, place, state);
+    for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
+      const int64_t nv = std::min(p.words, p.V - v0), nleft = cdiv(nv, kTileV);
+      const uint16_t *piece = w ? w + v0 * p.D : wp;
+      if (q) {  // rows v0 .. v0 + nv of the packed head; v0 is a multiple of 256, so whole groups lie before it
+        QWeight part_q = *q;
+        const int64_t block = v0 * p.D / kBlock;
+        part_q.n_out = nv;
+        part_q.codes += v0 * p.D / 2;
+        if (part_q.dq) {
+          part_q.fp8 += block;
+          part_q.s2 += block / kGroup;
+        } else {
+          part_q.s2 += block;
+        }
+        const hipError_t err = launch_dequantize(part_q, wp, cb, st);
+        if (err != hipSuccess) return err;
+      }
+      head_logits<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(hc, piece, yc, v0, nv, D, nleft, ntoken, rows,
+                                                                 state, e, p.words, exponent, sum, p.tpad, logit);
+      head_fold<<<(unsigned)cdiv(T, 16), 256, 0, st>>>(exponent, sum, p.tpad, (int)cdiv(nv, kStatV), v0 == 0, state, N,
+                                                      S, shift, factor);
+      if (!p.grad) continue;
+      const int64_t nd = cdiv(p.D, kTileV);
+      head_grad<<<(unsigned)(nd * ntoken * p.splits), kThreads, 0, st>>>(e, p.words, piece, nv, D, nd, ntoken,
+                                                                      p.split_words, state, shift, p.tpad, factor,
+                                                                      v0 == 0, part, stride);
+    }
+    if (!p.grad) {
+      head_losses<<<(unsigned)cdiv(T, 256), 256, 0, st>>>(T, place, N, S, logit, loss + c0, lse ? lse + c0 : nullptr);
+      continue;
+    }
+    if (q) head_target_rows<<<(unsigned)T, 256, 0, st>>>(*q, cb, place, yc, wy);
+    head_finish<<<(unsigned)T, 256, 0, st>>>(place, N, S, logit, yc, q ? wy : w, q != nullptr,
+                                             weight ? weight + c0 : nullptr, scale, part, (int)p.splits, stride, D,
+                                             loss + c0, lse ? lse + c0 : nullptr, grad + c0 * p.D);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -220,6 +220,26 @@ struct AdamwScalars {
 hipError_t launch_adamw(float *param, uint16_t *param_bf16, const float *grad, float *exp_avg, float *exp_avg_sq,
                         int64_t n, const AdamwScalars &s, hipStream_t st);
 
+// Loss of a frozen language-model head with the gradient of the hidden states
+// (head.hip): T tokens in chunks, V words in pieces (byte offsets into the
+// caller's workspace; grad = false: the loss alone; packed: an NF4 head, whose
+// pieces are decoded into the workspace).
+constexpr int64_t kHeadMaxTokens = 16384;  // tokens of a chunk
+constexpr int64_t kHeadMaxDim = 65536;     // D: a chunk's byte offsets stay below 2^32
+constexpr int64_t kHeadMaxSplit = 8192;    // words of one split of the gradient's contraction
+struct HeadPlan {
+  int64_t T, V, D;
+  bool grad, packed;
+  int64_t chunk, tpad, words, pieces, splits, split_words;
+  size_t off_rows, off_place, off_logit, off_n, off_s, off_factor, off_exponent, off_sum, off_shift, off_e, off_part,
+      off_w, off_wy, total;
+};
+HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed);
+// w (bf16 [V x D]) or q (packed), the other one nullptr; weight, lse may be nullptr; grad nullptr iff !p.grad.
+hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t *w, const QWeight *q,
+                            const int64_t *target, const float *weight, float scale, float *loss, float *lse,
+                            uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st);
+
 // Few-token sets (gemv.hip helper): a strided 2-D copy of bf16 rows.
 hipError_t launch_copy_rows(const uint16_t *src, int64_t ld_src, uint16_t *dst, int64_t ld_dst, int64_t rows,
                             int64_t cols, hipStream_t st);

@@ -68,6 +68,9 @@ _SIGNATURES = {
     "qlora_dropout_mask": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_double, ctypes.c_uint64, _P, _P, _P]),
     "qlora_adamw_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, ctypes.c_double, ctypes.c_double,
                                         ctypes.c_double, ctypes.c_double, ctypes.c_double, _P]),
+    "qlora_head_loss": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
+    "qlora_head_loss_nf4": (ctypes.c_int, [_P, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
+    "qlora_head_loss_workspace_bytes": (_SZ, [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int]),
     "qlora_status_read": (ctypes.c_int, [_P, _P]),
     "qlora_kernel_timing_enable": (None, [ctypes.c_int]),
     "qlora_kernel_timing_read": (ctypes.c_int, [_P, _P]),
@@ -172,7 +175,8 @@ _DT = {}  # dtype sets of the checks, filled on first use (torch is imported laz
 def _dtypes():
     if not _DT:
         torch = _torch()
-        _DT.update(tensor=torch.Tensor, bf16=(torch.bfloat16, torch.int16), f32=(torch.float32,))
+        _DT.update(tensor=torch.Tensor, bf16=(torch.bfloat16, torch.int16), f32=(torch.float32,),
+                   i64=(torch.int64,))
     return _DT
 
 
@@ -201,6 +205,9 @@ class _NoChecks:
         pass
 
     def f32(self, t, name, shape):
+        pass
+
+    def i64(self, t, name, shape):
         pass
 
     def done(self):
@@ -242,6 +249,9 @@ class _Args:
 
     def f32(self, t, name: str, shape) -> None:
         self._check(t, name, shape, "f32")
+
+    def i64(self, t, name: str, shape) -> None:
+        self._check(t, name, shape, "i64")
 
     def done(self) -> None:
         dev = self.device
@@ -677,3 +687,62 @@ def linear_set_bwd(dys, x, qs, A_set, Bs, scale: float, u=None, need_grad_x=True
                                       _ptr(u), _ptr(grad_x), _ptr(grad_A_set), _ptrs(grad_Bs), _ptr(ws), wsb,
                                       _stream(stream)), "qlora_linear_set_bwd")
     return grad_x, grad_A_set, grad_Bs
+
+
+# ----------------------------------------------------------- the loss of the head
+def head_loss_workspace_bytes(tokens: int, vocab: int, dim: int, grad: bool = True, packed: bool = False) -> int:
+    return int(lib().qlora_head_loss_workspace_bytes(tokens, vocab, dim, int(grad), int(packed)))
+
+
+def head_loss_workspace(tokens: int, vocab: int, dim: int, grad: bool = True, packed: bool = False, device="cuda"):
+    """A workspace for head_loss (reusable by successive calls on one stream)."""
+    torch = _torch()
+    return torch.empty(max(head_loss_workspace_bytes(tokens, vocab, dim, grad, packed), 1), dtype=torch.uint8,
+                       device=device)
+
+
+def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=None, grad_h=None, need_grad=True,
+              workspace=None, stream=None):
+    """Softmax cross entropy of a frozen language-model head over its vocabulary, the logits never held;
+    returns (loss, lse, grad_h or None).
+
+    h [T x D] bf16; head: a bf16 tensor [V x D] or a packed NF4Weight; target [T] int64, negative where a
+    token carries no loss.  loss and lse [T] fp32 are per token; grad_h [T x D] bf16 is the gradient of
+    sum_t scale weight_t loss_t (weight [T] fp32, default ones).  A target >= V gives NaN, and
+    status_read(workspace) then returns QLORA_ERR_VALUE (8)."""
+    torch = _torch()
+    packed = isinstance(head, NF4Weight)
+    if h.dim() != 2 or not (packed or head.dim() == 2):
+        raise ValueError("h and head must be 2-D")
+    T, D = int(h.shape[0]), int(h.shape[1])
+    V = head.n_out if packed else int(head.shape[0])
+    dev = _weight_device(head) if packed else head.device
+    chk = _Args(dev)
+    chk.bf16(h, "h", (T, head.n_in if packed else D))
+    if not packed:
+        chk.bf16(head, "head", (V, D))
+    chk.i64(target, "target", (T,))
+    if weight is not None:
+        chk.f32(weight, "weight", (T,))
+    loss = loss if loss is not None else torch.empty(T, dtype=torch.float32, device=dev)
+    chk.f32(loss, "loss", (T,))
+    lse = lse if lse is not None else torch.empty(T, dtype=torch.float32, device=dev)
+    chk.f32(lse, "lse", (T,))
+    if not need_grad:
+        grad_h = None
+    elif grad_h is None:
+        grad_h = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    if grad_h is not None:
+        chk.bf16(grad_h, "grad_h", (T, D))
+    chk.done()
+    ws = workspace if workspace is not None else head_loss_workspace(T, V, D, need_grad, packed, dev)
+    wsb = _workspace(ws, dev, lambda: head_loss_workspace_bytes(T, V, D, need_grad, packed))
+    if packed:
+        st = head.struct()
+        _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), _ptr(target), _ptr(weight), float(scale),
+                                         _ptr(loss), _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream(stream)),
+               "qlora_head_loss_nf4")
+    else:
+        _check(lib().qlora_head_loss(_ptr(h), T, _ptr(head), V, D, _ptr(target), _ptr(weight), float(scale), _ptr(loss),
+                                     _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream(stream)), "qlora_head_loss")
+    return loss, lse, grad_h

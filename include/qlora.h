@@ -33,8 +33,9 @@
  *     a workspace must be ordered by the caller.
  *   - Host-checkable problems return a non-zero qlora_status BEFORE anything
  *     is enqueued.  A launch failure returns QLORA_ERR_HIP.  Data-dependent
- *     problems (a NaN or Inf in the weight given to qlora_quantize) set a flag
- *     in the workspace that qlora_status_read reports.  Nothing throws.
+ *     problems (a NaN or Inf in the weight given to qlora_quantize, a target
+ *     past the vocabulary) set a flag in the workspace that qlora_status_read
+ *     reports.  Nothing throws.
  *   - Outputs are overwritten, never accumulated into.
  */
 #ifndef QLORA_H
@@ -326,6 +327,42 @@ qlora_status qlora_adamw_step(float *param, uint16_t *param_bf16, const float *g
                               double lr, double beta1, double beta2, double eps,
                               double weight_decay, void *stream);
 
+/* ---- the loss of the head ---------------------------------------------------- */
+
+/* Softmax cross entropy of a language-model head over V words, with the
+ * gradient of the hidden states, the logits never held (they are formed and
+ * used in pieces of the vocabulary).  The head W [V x D] is frozen, as every
+ * weight here: it receives no gradient.
+ *   l_tv     = sum_d h_td W_vd                    (fp32 sums)
+ *   lse_t    = log sum_v exp(l_tv)
+ *   loss_t   = lse_t - l_t,target(t)
+ *   grad_h_t = bf16( scale weight_t (sum_v exp(l_tv - lse_t) W_v - W_target(t)) )
+ * h [T x D] bf16, target [T] int64, weight [T] fp32 or NULL (all ones), loss
+ * and lse [T] fp32 (lse may be NULL), grad_h [T x D] bf16 (NULL: the loss
+ * alone, for evaluation).  loss and lse are per token, without scale and
+ * weight: the gradient is that of sum_t scale weight_t loss_t.
+ * A negative target marks a token without loss (padding, a prompt): its loss,
+ * lse and gradient are 0, whatever its row of h holds.  A target >= V gives
+ * NaN in that token's loss, lse and gradient, and qlora_status_read on ws
+ * reports QLORA_ERR_VALUE.  A token with a NaN or +Inf logit, or whose largest
+ * logit has a magnitude of 2.9e6 or more, gets NaN in all three.
+ * Requires T >= 1, V >= 1, D % 64 == 0, D <= 65536, T D and V D <= 2^37, a
+ * finite scale.  ws: qlora_head_loss_workspace_bytes, 16-B aligned.          */
+qlora_status qlora_head_loss(const uint16_t *h, int64_t T, const uint16_t *w, int64_t V, int64_t D,
+                             const int64_t *target, const float *weight, float scale, float *loss, float *lse,
+                             uint16_t *grad_h, void *ws, size_t ws_bytes, void *stream);
+
+/* The same with a packed head (V = q->n_out, D = q->n_in): its pieces are
+ * decoded to BFloat16 in the workspace, as every use of the weight decodes it. */
+qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_weight *q, const int64_t *target,
+                                 const float *weight, float scale, float *loss, float *lse, uint16_t *grad_h,
+                                 void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of the two calls (grad: with grad_h; packed: an NF4 head).
+ * 0 on a bad shape.  Bounded whatever V is: tokens are taken 16384 at a time,
+ * words in pieces of about 64 MB of workspace.                                */
+size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad, int packed);
+
 /* ---- diagnostics ---------------------------------------------------------- */
 
 /* Kernel timing for benchmarks.  While enabled (non-zero), every launch of
@@ -349,7 +386,8 @@ void qlora_kernel_timing_enable(int enable);
 qlora_status qlora_kernel_timing_read(int64_t *launches, double *total_ms);
 
 /* Wait for `stream`, then read the status word a previous call left in `ws`:
- * QLORA_OK or QLORA_ERR_NONFINITE (the word is not cleared).                  */
+ * QLORA_OK, QLORA_ERR_NONFINITE (qlora_quantize) or QLORA_ERR_VALUE
+ * (qlora_head_loss: a target past the vocabulary); the word is not cleared.   */
 qlora_status qlora_status_read(const void *ws, void *stream);
 
 #ifdef __cplusplus
