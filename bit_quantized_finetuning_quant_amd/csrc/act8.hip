@@ -1,0 +1,125 @@
+// 8-bit activation checkpoints (gfx950): the input of a linear layer kept in
+// 8.5 instead of 16 bits per value until the backward pass, which needs it for
+// grad_A only.
+//
+//   c1_b  = max |x| over 64 columns of a token,   scale_b = fl32(c1_b / 127)
+//   code  = the integer nearest to the exact 127 x / c1_b, ties to the even one
+//   x_hat = bf16( fl32(code scale_b) )
+//
+// A NaN or Inf makes the scale of its block NaN, so the whole block reads back
+// as NaN: nothing is lost silently.  A block of zeros has scale 0.
+//
+// Both kernels are bound by HBM: 3.06 bytes a value are moved, once.
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRuns = 4;  // runs of 8 values a thread takes, a workgroup's stride apart
+
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+
+// max over the 8 lanes of a block
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+  return v;
+}
+
+// The codes of 8 values of a block with the largest magnitude c1 (finite, > 0).  lift, a power of
+// two, keeps 1 / c1 and 127 x in range.  The quotient is corrected once by its remainder: it is then
+// within 2^-17 of the exact one, and exact where that is a multiple of 1/2, so every tie is seen as
+// one, while all other quotients are at least 1/510 away from a tie (x and c1 have 8 bits).
+__device__ __forceinline__ u32x2v encode(const u32x4 &x, float c1) {
+  const float lift = c1 < 0x1p-60f ? 0x1p64f : c1 > 0x1p60f ? 0x1p-64f : 1.0f;
+  const float c = c1 * lift, inv = __builtin_amdgcn_rcpf(c);
+  u32x2v out;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t packed = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t pair = x[2 * w + (i >> 1)];
+      const float n = ((i & 1) ? bf16_hi(pair) : bf16_lo(pair)) * lift * 127.0f;
+      const float q0 = n * inv;
+      const float q = __builtin_fmaf(__builtin_fmaf(-q0, c, n), inv, q0);
+      packed |= ((uint32_t)(int)__builtin_rintf(q) & 255u) << (8 * i);
+    }
+    out[w] = packed;
+  }
+  return out;
+}
+
+// Values [8 i, 8 i + 8) of x per thread and run; 8 consecutive lanes share a block.
+__global__ __launch_bounds__(kThreads) void act8_encode(const uint16_t *__restrict__ x, int64_t runs,
+                                                       int8_t *__restrict__ codes, float *__restrict__ scale) {
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kRuns) + threadIdx.x;
+  u32x4 v[kRuns];
+#pragma unroll
+  for (int j = 0; j < kRuns; ++j) {
+    const int64_t i = first + j * kThreads;
+    v[j] = i < runs ? *(const u32x4 *)(x + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+  }
+#pragma unroll
+  for (int j = 0; j < kRuns; ++j) {
+    const int64_t i = first + j * kThreads;
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t a = v[j][w] & 0x7FFF7FFFu;
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, a));
+    }
+    const uint32_t top = block_max(max((uint32_t)m[0], (uint32_t)m[1]));
+    const float c1 = __uint_as_float(top << 16);
+    const bool finite = top < 0x7F80u;
+    u32x2v c = {0u, 0u};
+    if (finite && top != 0u) c = encode(v[j], c1);
+    if (i >= runs) continue;
+    *(u32x2v *)(codes + 8 * i) = c;
+    if ((i & 7) == 0) scale[i >> 3] = finite ? c1 / 127.0f : __uint_as_float(0x7FC00000u);
+  }
+}
+
+// 8 codes (an eighth of a block) per thread and run.
+__global__ __launch_bounds__(kThreads) void act8_decode(const int8_t *__restrict__ codes,
+                                                       const float *__restrict__ scale, int64_t runs,
+                                                       uint16_t *__restrict__ x) {
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kRuns) + threadIdx.x;
+  u32x2v c[kRuns];
+  float s[kRuns];
+#pragma unroll
+  for (int j = 0; j < kRuns; ++j) {
+    const int64_t i = first + j * kThreads;
+    c[j] = i < runs ? *(const u32x2v *)(codes + 8 * i) : u32x2v{0u, 0u};
+    s[j] = i < runs ? scale[i >> 3] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < kRuns; ++j) {
+    const int64_t i = first + j * kThreads;
+    if (i < runs) *(u32x4 *)(x + 8 * i) = act8_values(c[j][0], c[j][1], s[j]);
+  }
+}
+
+unsigned grid(int64_t runs) { return (unsigned)((runs + kThreads * kRuns - 1) / (kThreads * kRuns)); }
+
+}  // namespace
+
+hipError_t launch_act8_encode(const uint16_t *x, int64_t T, int64_t K, int8_t *codes, float *scale, hipStream_t st) {
+  const int64_t runs = T * K / 8;
+  act8_encode<<<grid(runs), kThreads, 0, st>>>(x, runs, codes, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_act8_decode(const int8_t *codes, const float *scale, int64_t T, int64_t K, uint16_t *x,
+                              hipStream_t st) {
+  const int64_t runs = T * K / 8;
+  act8_decode<<<grid(runs), kThreads, 0, st>>>(codes, scale, runs, x);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

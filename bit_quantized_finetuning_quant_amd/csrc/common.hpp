@@ -112,6 +112,21 @@ __device__ __forceinline__ void decode_word(uint32_t c, const DecodeTable &t, ui
 __device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
 
+// Eight codes of an 8-bit activation checkpoint (two words, low byte first) -> x_hat = bf16(fl32(code
+// scale)), four words of bf16 pairs.  A code is read as an unsigned byte 128 above it (v_cvt_f32_ubyte).
+__device__ __forceinline__ u32x4 act8_values(uint32_t c0, uint32_t c1, float scale) {
+  u32x4 out;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint32_t u = (w ? c1 : c0) ^ 0x80808080u;
+    const float f0 = ((float)(u & 255u) - 128.0f) * scale, f1 = ((float)((u >> 8) & 255u) - 128.0f) * scale;
+    const float f2 = ((float)((u >> 16) & 255u) - 128.0f) * scale, f3 = ((float)(u >> 24) - 128.0f) * scale;
+    out[2 * w] = pack_bf16x2(f0, f1);
+    out[2 * w + 1] = pack_bf16x2(f2, f3);
+  }
+  return out;
+}
+
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 }  // namespace qlora

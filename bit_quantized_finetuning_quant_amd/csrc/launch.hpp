@@ -220,6 +220,35 @@ struct AdamwScalars {
 hipError_t launch_adamw(float *param, uint16_t *param_bf16, const float *grad, float *exp_avg, float *exp_avg_sq,
                         int64_t n, const AdamwScalars &s, hipStream_t st);
 
+// 8-bit activation checkpoints (act8.hip): codes [T x K], scale [T x K / 64]; K % 64 == 0.
+hipError_t launch_act8_encode(const uint16_t *x, int64_t T, int64_t K, int8_t *codes, float *scale, hipStream_t st);
+hipError_t launch_act8_decode(const int8_t *codes, const float *scale, int64_t T, int64_t K, uint16_t *x,
+                              hipStream_t st);
+
+// Adapter products of a backward pass from a checkpoint (lora.hip).  v [3][T x count r]: v_set as
+// launch_lora_set_v forms it, then what its rounding leaves in two bf16 values; then grad_A_set =
+// scale (v_set + both)^T x_hat and grad_B_i = scale dy_i^T u_i.  `part`: lora_set_part_floats.
+hipError_t launch_lora_set_v_exact(const uint16_t *const *dy, const uint16_t *const *B, const int64_t *N, int count,
+                                   int64_t T, int r, uint16_t *v, float *part, hipStream_t st);
+hipError_t launch_lora_set_grads_act8(const uint16_t *v, const int8_t *codes, const float *code_scale,
+                                      const uint16_t *const *dy, const uint16_t *u_set, const int64_t *N, int count,
+                                      int64_t T, int64_t K, int r, float scale, float *grad_A_set,
+                                      float *const *grad_B, float *part, hipStream_t st);
+
+// Backward of a projection set (or one linear) from the checkpoint of its input (linear.hip).
+struct Act8BwdPlan {
+  int64_t T, K;
+  int r, count;
+  int64_t N[kMaxSetMembers];
+  size_t off_v, off_part, off_qpart, total;  // off_qpart: 0 when grad_x does not split
+};
+Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t K, int r);
+hipError_t launch_linear_set_bwd_act8(const Act8BwdPlan &p, const uint16_t *const *dy, const int8_t *codes,
+                                      const float *code_scale, const QWeight *w, const uint16_t *A_set,
+                                      const uint16_t *const *B, float scale, const uint16_t *u, uint16_t *grad_x,
+                                      float *grad_A_set, float *const *grad_B, char *ws, const Codebook &cb,
+                                      hipStream_t st);
+
 // Loss of a frozen language-model head with the gradient of the hidden states
 // (head.hip): T tokens in chunks, V words in pieces (byte offsets into the
 // caller's workspace; grad = false: the loss alone; packed: an NF4 head, whose

@@ -160,6 +160,16 @@ __device__ __forceinline__ void emit_out(void *out, int64_t idx, float v) {
   }
 }
 
+// What the bf16 rounding of v leaves, in two bf16 values (the differences are exact): out, mid and
+// low then sum to v within 2^-24, its own precision.
+__device__ __forceinline__ void emit_rest(uint16_t *mid, uint16_t *low, int64_t idx, float v) {
+  const float d = v - (float)(__bf16)v;
+  const __bf16 m = (__bf16)d;
+  const __bf16 l = (__bf16)(d - (float)m);
+  mid[idx] = __builtin_bit_cast(uint16_t, m);
+  low[idx] = __builtin_bit_cast(uint16_t, l);
+}
+
 // One adapter product of a launch: C[M x Nc] = scale * Aop Bop over a
 // contraction of Kc, split in chunks of `chunk` (S splits); tiles are numbered
 // column-major (tile = n-tile * tiles_m + m-tile).
@@ -174,13 +184,40 @@ struct LoraProblem {
   void *out;
   int64_t ldo;  // row stride of out (Nc unless the product fills columns of a wider matrix)
   float *part;
+  uint16_t *out_mid, *out_low;  // bf16 outputs: also what their rounding leaves (nullptr: not wanted)
+  // grad_A from a checkpoint: Q holds its codes, P has the remainders P_mid, P_low
+  const uint16_t *P_mid, *P_low;
+  const float *code_scale;  // [Kc x Nc / 64]
 };
+
+// The finished tile: scaled into the output, or as the partial tile of its split.
+template <bool kBf16Out>
+__device__ __forceinline__ void put_tile(const LoraProblem &pr, int64_t tile, int s, const f32x16 &acc) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t m0 = (tile % pr.tiles_m) * LT, n0 = (tile / pr.tiles_m) * LT;
+  // result element q of this lane: tile row wm*32 + 8(q/4) + 4(lane/32) + q%4, column wn*32 + lane%32
+  const int col = wn * 32 + (lane & 31);
+  if (pr.S == 1) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int64_t gm = m0 + wm * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3), gn = n0 + col;
+      if (gm < pr.M && gn < pr.Nc) {
+        emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn, acc[q] * pr.scale);
+        if (kBf16Out && pr.out_mid) emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn, acc[q] * pr.scale);
+      }
+    }
+    return;
+  }
+  // partial tile, row-major 64 x 64, at part[((tile * S) + s) * 4096]
+  float *mine = pr.part + (tile * pr.S + s) * (LT * LT);
+#pragma unroll
+  for (int q = 0; q < 16; ++q) mine[(wm * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * LT + col] = acc[q];
+}
 
 template <bool kAT, bool kBT, bool kBf16Out, int kGroupSteps>
 __device__ __forceinline__ void lora_tile(const LoraProblem &pr, int64_t tile, int s, uint16_t (*sA)[LT * LLD],
                                           uint16_t (*sB)[LT * LLD]) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
   const int64_t m0 = (tile % pr.tiles_m) * LT, n0 = (tile / pr.tiles_m) * LT;
   const int64_t kb = (int64_t)s * pr.chunk, ke = min(pr.Kc, kb + pr.chunk);
 
@@ -198,20 +235,7 @@ __device__ __forceinline__ void lora_tile(const LoraProblem &pr, int64_t tile, i
     lora_body<kAT, kBT, kBf16Out, false, kGroupSteps>(pr.P, pr.ldp, pr.Q, pr.ldq, pr.M, pr.Nc, kb, ke, m0, n0, sA,
                                                        sB, acc);
 
-  // result element q of this lane: tile row wm*32 + 8(q/4) + 4(lane/32) + q%4, column wn*32 + lane%32
-  const int col = wn * 32 + (lane & 31);
-  if (pr.S == 1) {
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int64_t gm = m0 + wm * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3), gn = n0 + col;
-      if (gm < pr.M && gn < pr.Nc) emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn, acc[q] * pr.scale);
-    }
-    return;
-  }
-  // partial tile, row-major 64 x 64, at part[((tile * S) + s) * 4096]
-  float *mine = pr.part + (tile * pr.S + s) * (LT * LT);
-#pragma unroll
-  for (int q = 0; q < 16; ++q) mine[(wm * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * LT + col] = acc[q];
+  put_tile<kBf16Out>(pr, tile, s, acc);
 }
 
 // One or two products of the same operand forms in one launch: workgroups
@@ -256,7 +280,10 @@ __device__ __forceinline__ void reduce_quad(const LoraProblem &pr, int64_t qd) {
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (gn + e < pr.Nc) emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn + e, acc[e] * pr.scale);
+    if (gn + e < pr.Nc) {
+      emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn + e, acc[e] * pr.scale);
+      if (kBf16Out && pr.out_mid) emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn + e, acc[e] * pr.scale);
+    }
 }
 
 template <bool kBf16Out>
@@ -267,6 +294,106 @@ __global__ __launch_bounds__(256) void lora_reduce(LoraProblem a, LoraProblem b,
     else
       reduce_quad<kBf16Out>(b, qd - first);
   }
+}
+
+// ---- grad_A from an 8-bit checkpoint --------------------------------------
+// grad_A = s v^T x_hat: the codes of a 64 x 64 tile (one block of 64 columns a token, so one scale a
+// row) are decoded on their way into LDS, and v = dy B enters as the bf16 value the fused GEMM takes
+// plus the two bf16 values its rounding leaves, three MFMAs per fragment: the fp32 sums of v are then
+// not rounded at all (with one remainder, 2^-16, grad_A was 3 times further from 64 bits than an fp32
+// product; the products are small and their time is their loads').
+constexpr int kActSteps = 2;  // contraction steps fetched at once: four tiles each
+
+struct CodeRegs {
+  uint2 c[2];
+  float s[2];
+};
+
+// Thread t: codes of columns 8 (t%8) .. +7 of rows t/8 and t/8 + 32 of the tile at (r0, c0).
+__device__ __forceinline__ void load_codes(const int8_t *codes, const float *scale, int64_t ld, int64_t nrows, int64_t r0,
+                                           int64_t c0, int tid, CodeRegs &t) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = r0 + (tid >> 3) + 32 * h;
+    const bool in = row < nrows;
+    t.c[h] = in ? *(const uint2 *)(codes + row * ld + c0 + 8 * (tid & 7)) : make_uint2(0u, 0u);
+    t.s[h] = in ? scale[row * (ld / kBlock) + c0 / kBlock] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store_codes(const CodeRegs &t, uint16_t *lds, int tid) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    *(u32x4 *)&lds[((tid >> 3) + 32 * h) * LLD + 8 * (tid & 7)] = act8_values(t.c[h].x, t.c[h].y, t.s[h]);
+}
+
+template <bool kFull>
+__device__ __forceinline__ void act8_body(const LoraProblem &pr, int64_t kb, int64_t ke, int64_t m0, int64_t n0,
+                                          uint16_t (*s)[LT * LLD], f32x16 &acc) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const bool vp = (pr.ldp % 8) == 0;
+  uint16_t(*sh)[LT * LLD] = s, (*sm)[LT * LLD] = s + kActSteps, (*sl)[LT * LLD] = s + 2 * kActSteps;
+  uint16_t(*sq)[LT * LLD] = s + 3 * kActSteps;
+  TileRegs th[kActSteps], tm[kActSteps], tl[kActSteps];
+  CodeRegs tq[kActSteps];
+  auto fetch = [&](int64_t g0) {
+#pragma unroll
+    for (int st = 0; st < kActSteps; ++st) {
+      const int64_t k0 = g0 + LT * st;
+      load_tile<kFull>(pr.P, pr.ldp, ke, pr.M, k0, m0, vp, tid, th[st]);
+      load_tile<kFull>(pr.P_mid, pr.ldp, ke, pr.M, k0, m0, vp, tid, tm[st]);
+      load_tile<kFull>(pr.P_low, pr.ldp, ke, pr.M, k0, m0, vp, tid, tl[st]);
+      load_codes((const int8_t *)pr.Q, pr.code_scale, pr.ldq, ke, k0, n0, tid, tq[st]);
+    }
+  };
+  fetch(kb);
+  for (int64_t g0 = kb; g0 < ke; g0 += LT * kActSteps) {
+#pragma unroll
+    for (int st = 0; st < kActSteps; ++st) {
+      store_tile(th[st], sh[st], tid);
+      store_tile(tm[st], sm[st], tid);
+      store_tile(tl[st], sl[st], tid);
+      store_codes(tq[st], sq[st], tid);
+    }
+    __syncthreads();
+    if (g0 + LT * kActSteps < ke) fetch(g0 + LT * kActSteps);
+#pragma unroll
+    for (int st = 0; st < kActSteps; ++st)
+#pragma unroll
+      for (int kk = 0; kk < LT / 16; ++kk) {
+        const u32x4 h = frag<true>(sh[st], wm * 32, kk, lane), m = frag<true>(sm[st], wm * 32, kk, lane);
+        const u32x4 l = frag<true>(sl[st], wm * 32, kk, lane);
+        const u32x4 q = frag<true>(sq[st], wn * 32, kk, lane);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(h), as_bf16x8(q), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(m), as_bf16x8(q), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(l), as_bf16x8(q), acc, 0, 0, 0);
+      }
+    __syncthreads();
+  }
+}
+
+__device__ __forceinline__ void act8_tile(const LoraProblem &pr, int64_t tile, int s, uint16_t (*lds)[LT * LLD]) {
+  const int64_t m0 = (tile % pr.tiles_m) * LT, n0 = (tile / pr.tiles_m) * LT;
+  const int64_t kb = (int64_t)s * pr.chunk, ke = min(pr.Kc, kb + pr.chunk);
+  f32x16 acc;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) acc[q] = 0.f;
+  if (m0 + LT <= pr.M && (ke - kb) % (LT * kActSteps) == 0 && pr.ldp % 8 == 0)  // rows and planes of whole 16 bytes
+    act8_body<true>(pr, kb, ke, m0, n0, lds, acc);
+  else
+    act8_body<false>(pr, kb, ke, m0, n0, lds, acc);
+  put_tile<false>(pr, tile, s, acc);
+}
+
+// grad_A from the checkpoint (workgroups below `first`) and one grad_B (the rest) in one launch.
+__global__ __launch_bounds__(256) void lora_gemm_act8(LoraProblem a, LoraProblem b, int64_t first) {
+  __shared__ __attribute__((aligned(16))) uint16_t s[8][LT * LLD];
+  const int64_t id = blockIdx.x;
+  if (id < first)
+    act8_tile(a, id / a.S, (int)(id % a.S), s);
+  else
+    lora_tile<true, true, false, 4>(b, (id - first) / b.S, (int)((id - first) % b.S), s, s + 4);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -313,6 +440,9 @@ LoraProblem make_problem(const uint16_t *P, int64_t ldp, const uint16_t *Q, int6
   pr.out = out;
   pr.ldo = Nc;
   pr.part = part;
+  pr.out_mid = pr.out_low = nullptr;
+  pr.P_mid = pr.P_low = nullptr;
+  pr.code_scale = nullptr;
   return pr;
 }
 
@@ -425,6 +555,47 @@ hipError_t launch_lora_set_grads(const uint16_t *v_set, const uint16_t *x, const
     off += lora_part_floats(N[i], r, T);
   }
   return launch_list<true, true, false>(pr, count + 1, st);
+}
+
+// v_set with what its rounding leaves: v [3][T x count r].
+hipError_t launch_lora_set_v_exact(const uint16_t *const *dy, const uint16_t *const *B, const int64_t *N, int count,
+                                   int64_t T, int r, uint16_t *v, float *part, hipStream_t st) {
+  const int64_t plane = T * count * r;
+  LoraProblem pr[kMaxSetMembers];
+  size_t off = 0;
+  for (int i = 0; i < count; ++i) {
+    pr[i] = make_problem(dy[i], N[i], B[i], r, T, r, N[i], 1.0f, v + (int64_t)i * r, part + off);
+    pr[i].ldo = (int64_t)count * r;
+    pr[i].out_mid = v + plane + (int64_t)i * r;
+    pr[i].out_low = v + 2 * plane + (int64_t)i * r;
+    off += lora_part_floats(T, r, N[i]);
+  }
+  return launch_list<false, true, true>(pr, count, st);
+}
+
+// grad_A_set and the first grad_B in one launch, the other grad_B two a launch.
+hipError_t launch_lora_set_grads_act8(const uint16_t *v, const int8_t *codes, const float *code_scale,
+                                      const uint16_t *const *dy, const uint16_t *u_set,
+                                      const int64_t *N, int count, int64_t T, int64_t K, int r, float scale,
+                                      float *grad_A_set, float *const *grad_B, float *part, hipStream_t st) {
+  LoraProblem pr[kMaxSetMembers];
+  const int64_t rt = (int64_t)count * r;
+  LoraProblem a = make_problem(v, rt, (const uint16_t *)codes, K, rt, K, T, scale, grad_A_set, part);
+  a.P_mid = v + T * rt;
+  a.P_low = v + 2 * T * rt;
+  a.code_scale = code_scale;
+  size_t off = lora_part_floats(rt, K, T);
+  for (int i = 0; i < count; ++i) {
+    pr[i] = make_problem(dy[i], N[i], u_set + (int64_t)i * r, rt, N[i], r, T, scale, grad_B[i], part + off);
+    off += lora_part_floats(N[i], r, T);
+  }
+  const int64_t wa = problem_blocks(a), wb = problem_blocks(pr[0]);
+  lora_gemm_act8<<<(unsigned)(wa + wb), 256, 0, st>>>(a, pr[0], wa);
+  const int64_t qa = problem_quads(a), qb = problem_quads(pr[0]);
+  if (qa + qb > 0)
+    lora_reduce<false><<<(unsigned)std::min<int64_t>(cdiv(qa + qb, 256), 2048), 256, 0, st>>>(a, pr[0], qa, qa + qb);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_list<true, true, false>(pr + 1, count - 1, st);
 }
 
 }  // namespace qlora

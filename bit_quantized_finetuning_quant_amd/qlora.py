@@ -33,6 +33,10 @@ class NF4WeightStruct(ctypes.Structure):
                 ("absmax_mean", ctypes.c_void_p), ("flags", ctypes.c_uint32)]
 
 
+class Act8Struct(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -68,6 +72,13 @@ _SIGNATURES = {
     "qlora_dropout_mask": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_double, ctypes.c_uint64, _P, _P, _P]),
     "qlora_adamw_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, ctypes.c_double, ctypes.c_double,
                                         ctypes.c_double, ctypes.c_double, ctypes.c_double, _P]),
+    "qlora_act8_write": (ctypes.c_int, [_P, _P, _P]),
+    "qlora_act8_read": (ctypes.c_int, [_P, _P, _P]),
+    "qlora_linear_bwd_act8": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _P, _SZ,
+                                             _P]),
+    "qlora_linear_set_bwd_act8": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int, ctypes.c_float, _P, _P,
+                                                 _P, _P, _P, _SZ, _P]),
+    "qlora_linear_set_act8_workspace_bytes": (_SZ, [_I64, ctypes.c_int, _P, _I64, ctypes.c_int]),
     "qlora_head_loss": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
     "qlora_head_loss_nf4": (ctypes.c_int, [_P, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
     "qlora_head_loss_workspace_bytes": (_SZ, [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int]),
@@ -176,7 +187,7 @@ def _dtypes():
     if not _DT:
         torch = _torch()
         _DT.update(tensor=torch.Tensor, bf16=(torch.bfloat16, torch.int16), f32=(torch.float32,),
-                   i64=(torch.int64,))
+                   i64=(torch.int64,), i8=(torch.int8,))
     return _DT
 
 
@@ -208,6 +219,9 @@ class _NoChecks:
         pass
 
     def i64(self, t, name, shape):
+        pass
+
+    def i8(self, t, name, shape):
         pass
 
     def done(self):
@@ -252,6 +266,9 @@ class _Args:
 
     def i64(self, t, name: str, shape) -> None:
         self._check(t, name, shape, "i64")
+
+    def i8(self, t, name: str, shape) -> None:
+        self._check(t, name, shape, "i8")
 
     def done(self) -> None:
         dev = self.device
@@ -630,8 +647,9 @@ def _check_list(ts, count: int, name: str) -> None:
         raise ValueError(f"{name} must hold {count} tensors, not {len(ts)}")
 
 
-def _set_dims(x, qs, A_set):
-    """(T, count, r, device, checker) of a projection-set call; A_set must hold count whole [r x n_in] blocks."""
+def _set_dims(x, qs, A_set, act8=None):
+    """(T, count, r, device, checker) of a projection-set call; A_set must hold count whole [r x n_in] blocks.
+    act8: the checkpoint that x is the codes of."""
     count = len(qs)
     if count < 1:
         raise ValueError("a projection set needs at least one member")
@@ -647,7 +665,10 @@ def _set_dims(x, qs, A_set):
         raise ValueError(f"A_set has {A_set.shape[0]} rows, not a multiple of the {count} members")
     T, r = int(x.shape[0]), int(A_set.shape[0]) // count
     chk = _Args(dev)
-    chk.bf16(x, "x", (T, qs[0].n_in))
+    if act8 is None:
+        chk.bf16(x, "x", (T, qs[0].n_in))
+    elif _check_act8(act8, chk)[1] != qs[0].n_in:
+        raise ValueError(f"codes must have {qs[0].n_in} columns, not {x.shape[1]}")
     chk.bf16(A_set, "A_set", (count * r, qs[0].n_in))
     return T, count, r, dev, chk
 
@@ -686,6 +707,130 @@ def linear_set_bwd(dys, x, qs, A_set, Bs, scale: float, u=None, need_grad_x=True
     _check(lib().qlora_linear_set_bwd(_ptrs(dys), _ptr(x), T, count, st, _ptr(A_set), _ptrs(Bs), r, float(scale),
                                       _ptr(u), _ptr(grad_x), _ptr(grad_A_set), _ptrs(grad_Bs), _ptr(ws), wsb,
                                       _stream(stream)), "qlora_linear_set_bwd")
+    return grad_x, grad_A_set, grad_Bs
+
+
+# -------------------------------------------------- 8-bit activation checkpoints
+@dataclass
+class Act8:
+    """An activation [T x K] in 8.5 bits per value: codes int8 [T x K], scale fp32 [T x K / 64]."""
+    codes: "object"
+    scale: "object"
+
+    @classmethod
+    def empty(cls, tokens: int, dim: int, device="cuda"):
+        torch = _torch()
+        if dim % 64:
+            raise ValueError(f"dim must be a multiple of 64, not {dim}")
+        return cls(torch.empty((tokens, dim), dtype=torch.int8, device=device),
+                   torch.empty((tokens, dim // 64), dtype=torch.float32, device=device))
+
+    def struct(self) -> Act8Struct:
+        return Act8Struct(self.codes.shape[0], self.codes.shape[1], _ptr(self.codes), _ptr(self.scale))
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scale.numel()
+
+
+def _check_act8(a: Act8, chk):
+    """(T, K) of a checkpoint whose tensors fit each other."""
+    if a.codes.dim() != 2:
+        raise ValueError("codes must be 2-D")
+    T, K = int(a.codes.shape[0]), int(a.codes.shape[1])
+    if K % 64:
+        raise ValueError(f"codes must have a multiple of 64 columns, not {K}")
+    chk.i8(a.codes, "codes", (T, K))
+    chk.f32(a.scale, "scale", (T, K // 64))
+    return T, K
+
+
+def act8_write(x, out: Act8 = None, stream=None) -> Act8:
+    """Keep a [T x K] bf16 activation (K % 64 == 0) as an 8-bit checkpoint: per 64 columns one fp32 scale,
+    absmax / 127, and the nearest codes."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    T, K = int(x.shape[0]), int(x.shape[1])
+    chk = _Args(x.device)
+    chk.bf16(x, "x", (T, K))
+    a = out if out is not None else Act8.empty(T, K, x.device)
+    if _check_act8(a, chk) != (T, K):
+        raise ValueError(f"out must hold {T} x {K} values, not {a.codes.shape[0]} x {a.codes.shape[1]}")
+    chk.done()
+    st = a.struct()
+    _check(lib().qlora_act8_write(_ptr(x), ctypes.byref(st), _stream(stream)), "qlora_act8_write")
+    return a
+
+
+def act8_read(a: Act8, out=None, stream=None):
+    """The bf16 values a checkpoint stands for."""
+    torch = _torch()
+    chk = _Args(a.codes.device)
+    T, K = _check_act8(a, chk)
+    y = out if out is not None else torch.empty((T, K), dtype=torch.bfloat16, device=a.codes.device)
+    chk.bf16(y, "out", (T, K))
+    chk.done()
+    st = a.struct()
+    _check(lib().qlora_act8_read(ctypes.byref(st), _ptr(y), _stream(stream)), "qlora_act8_read")
+    return y
+
+
+def linear_set_act8_workspace_bytes(tokens: int, n_outs, n_in: int, r: int) -> int:
+    arr = (ctypes.c_int64 * len(n_outs))(*n_outs)
+    return int(lib().qlora_linear_set_act8_workspace_bytes(tokens, len(n_outs), arr, n_in, r))
+
+
+def linear_set_act8_workspace(tokens: int, n_outs, n_in: int, r: int, device="cuda"):
+    """A workspace for linear_set_bwd_act8, and with one n_out for linear_bwd_act8."""
+    torch = _torch()
+    return torch.empty(max(linear_set_act8_workspace_bytes(tokens, n_outs, n_in, r), 1), dtype=torch.uint8,
+                       device=device)
+
+
+def linear_bwd_act8(dy, a: Act8, q: NF4Weight, A, B, scale: float, u, need_grad_x=True, grad_x=None, grad_A=None,
+                    grad_B=None, workspace=None, stream=None):
+    """linear_bwd with the checkpoint `a` of the layer's input in place of x; u is the forward's.
+    Returns (grad_x bf16 or None, grad_A fp32, grad_B fp32)."""
+    grad_x, grad_A, grad_Bs = linear_set_bwd_act8([dy], a, [q], A, [B], scale, u, need_grad_x, grad_x, grad_A,
+                                                  [grad_B] if grad_B is not None else None, workspace, stream)
+    return grad_x, grad_A, grad_Bs[0]
+
+
+def linear_set_bwd_act8(dys, a: Act8, qs, A_set, Bs, scale: float, u, need_grad_x=True, grad_x=None, grad_A_set=None,
+                        grad_Bs=None, workspace=None, stream=None):
+    """linear_set_bwd with the checkpoint `a` of the shared input in place of x; u is the forward's.
+    Returns (grad_x summed over the members or None, grad_A_set, [grad_B_i])."""
+    torch = _torch()
+    T, count, r, dev, chk = _set_dims(a.codes, qs, A_set, act8=a)
+    _check_list(dys, count, "dys")
+    _check_list(Bs, count, "Bs")
+    for i, (q, d, b) in enumerate(zip(qs, dys, Bs)):
+        chk.bf16(d, f"dys[{i}]", (T, q.n_out))
+        chk.bf16(b, f"Bs[{i}]", (q.n_out, r))
+    chk.bf16(u, "u", (T, count * r))
+    n_in = qs[0].n_in
+    if not need_grad_x:
+        grad_x = None
+    elif grad_x is None:
+        grad_x = torch.empty((T, n_in), dtype=torch.bfloat16, device=dev)
+    if grad_x is not None:
+        chk.bf16(grad_x, "grad_x", (T, n_in))
+    if grad_A_set is None:
+        grad_A_set = torch.empty((count * r, n_in), dtype=torch.float32, device=dev)
+    chk.f32(grad_A_set, "grad_A_set", (count * r, n_in))
+    if grad_Bs is None:
+        grad_Bs = [torch.empty((q.n_out, r), dtype=torch.float32, device=dev) for q in qs]
+    _check_list(grad_Bs, count, "grad_Bs")
+    for i, (q, g) in enumerate(zip(qs, grad_Bs)):
+        chk.f32(g, f"grad_Bs[{i}]", (q.n_out, r))
+    chk.done()
+    n_outs = [q.n_out for q in qs]
+    ws = workspace if workspace is not None else linear_set_act8_workspace(T, n_outs, n_in, r, dev)
+    wsb = _workspace(ws, dev, lambda: linear_set_act8_workspace_bytes(T, n_outs, n_in, r))
+    st = (NF4WeightStruct * count)(*[q.struct() for q in qs])
+    sa = a.struct()
+    _check(lib().qlora_linear_set_bwd_act8(_ptrs(dys), ctypes.byref(sa), count, st, _ptr(A_set), _ptrs(Bs), r,
+                                           float(scale), _ptr(u), _ptr(grad_x), _ptr(grad_A_set), _ptrs(grad_Bs),
+                                           _ptr(ws), wsb, _stream(stream)), "qlora_linear_set_bwd_act8")
     return grad_x, grad_A_set, grad_Bs
 
 

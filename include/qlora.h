@@ -327,6 +327,49 @@ qlora_status qlora_adamw_step(float *param, uint16_t *param_bf16, const float *g
                               double lr, double beta1, double beta2, double eps,
                               double weight_decay, void *stream);
 
+/* ---- 8-bit activation checkpoints -------------------------------------------- */
+
+/* Beside its adapters' gradients, a linear layer's backward pass needs the
+ * layer's input only for grad_A = scale v^T x.  A checkpoint keeps that input
+ * between the passes in 8.5 instead of 16 bits per value:
+ *   c1      = max |x| over 64 columns of a token, scale = fl32(c1 / 127)
+ *   code    = integer nearest to the exact 127 x / c1, ties to even
+ *   x_hat   = bf16( fl32(code scale) )
+ * A NaN or Inf makes its block's scale (and so x_hat) NaN; a block of zeros
+ * has scale 0 and codes 0.  T >= 1, K % 64 == 0, T K <= 2^37.
+ * All buffers are device memory owned by the caller, 16-B aligned.            */
+typedef struct {
+  int64_t T, K;
+  int8_t *codes;   /* [T x K]                                                  */
+  float *scale;    /* [T x K / 64]                                             */
+} qlora_act8;
+
+/* x [T x K] bf16 -> *a.                                                        */
+qlora_status qlora_act8_write(const uint16_t *x, const qlora_act8 *a, void *stream);
+
+/* *a -> x_hat [T x K] bf16.                                                    */
+qlora_status qlora_act8_read(const qlora_act8 *a, uint16_t *x, void *stream);
+
+/* qlora_linear_bwd with the checkpoint in place of x (T and n_in are the
+ * checkpoint's): grad_x and grad_B as there, grad_A = scale v^T x_hat with
+ * v = dy B in fp32 (grad_x takes it in bf16, as there).  u is the
+ * forward's u_out and required: from the checkpoint it would come out
+ * different.  grad_x may be NULL.  ws: qlora_linear_set_act8_workspace_bytes
+ * with count = 1.                                                             */
+qlora_status qlora_linear_bwd_act8(const uint16_t *dy, const qlora_act8 *a, const qlora_nf4_weight *q,
+                                   const uint16_t *A, const uint16_t *B, int r, float scale, const uint16_t *u,
+                                   uint16_t *grad_x, float *grad_A, float *grad_B, void *ws, size_t ws_bytes,
+                                   void *stream);
+
+/* qlora_linear_set_bwd with the checkpoint of the shared input in place of x. */
+qlora_status qlora_linear_set_bwd_act8(const uint16_t *const *dy, const qlora_act8 *a, int count,
+                                       const qlora_nf4_weight *q, const uint16_t *A_set, const uint16_t *const *B,
+                                       int r, float scale, const uint16_t *u, uint16_t *grad_x, float *grad_A_set,
+                                       float *const *grad_B, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of the two calls above (0 on a bad shape).                  */
+size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t *n_out, int64_t n_in, int r);
+
 /* ---- the loss of the head ---------------------------------------------------- */
 
 /* Softmax cross entropy of a language-model head over V words, with the

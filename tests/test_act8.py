@@ -1,0 +1,311 @@
+"""8-bit activation checkpoints and the backward pass that reads them.
+
+The codes and the decoded values are compared bit for bit with the definition in exact arithmetic
+(64 bits hold 127 x and decide every tie).  Gradients from the checkpoint are compared with the formula
+in 64 bits on x_hat.  Tolerances of one output value, with S the sum of the absolute terms:
+  grad_A  v = dy B is an fp32 sum (N 2^-24 of its absolute terms), held within 2^-24; then an fp32 sum
+          over the tokens: (N + 3 T + 8) 2^-24 scale |v|'^T |x_hat|, |v|' = |dy| |B| (three addends a token)
+  grad_B  an fp32 sum of exact products: (T + 4) 2^-24 scale |dy|^T |u|
+  grad_x  v in bf16 (2^-8), fp32 sums, the result in bf16:
+          (2^-8 + (N + r) 2^-24) scale |v|' |A| + N 2^-24 |dy| |W| + 2^-8 |grad_x|
+(bf16 has 8 significant bits, so a rounding moves a value by up to 2^-8 of it; the fp32 factor scale
+adds 2^-24, within the + 4 and + 8.)
+"""
+
+import ctypes
+
+import pytest
+
+from bit_quantized_finetuning_quant_amd import qlora
+from helpers import announce, torch_mod
+
+gpu = pytest.mark.gpu
+
+
+def _define(x):
+    """(codes, scale, x_hat) of a bf16 tensor by the definition, in 64 bits on its device."""
+    torch = torch_mod()
+    b = x.double().view(x.shape[0], -1, 64)
+    top = b.abs().amax(2)
+    bad = ~torch.isfinite(b).all(2)
+    safe = torch.where((top > 0) & ~bad, top, torch.ones_like(top))
+    code = torch.where(bad[..., None] | (top == 0)[..., None], 0.0, torch.round(127 * b / safe[..., None]))
+    scale = torch.where(bad, float("nan"), top / 127).float()
+    xh = (code.float() * scale[..., None]).bfloat16()
+    return code.to(torch.int8).view(x.shape), scale, xh.view(x.shape)
+
+
+def _same(a, b):
+    torch = torch_mod()
+    return torch.equal(a.isnan(), b.isnan()) and torch.equal(a[~a.isnan()], b[~b.isnan()])
+
+
+def _write_read(x):
+    torch = torch_mod()
+    a = qlora.act8_write(x)
+    y = qlora.act8_read(a)
+    torch.cuda.synchronize()
+    code, scale, xh = _define(x)
+    assert torch.equal(a.codes, code)
+    assert _same(a.scale, scale)
+    assert _same(y, xh)
+    return a, y
+
+
+@gpu
+@pytest.mark.parametrize("T,K", [(1, 64), (1, 128), (3, 64), (5, 192), (1, 4096), (127, 320), (128, 1024), (129, 2112),
+                                 (1000, 64), (2048, 4096), (509, 22016)])
+def test_codes_and_values(T, K):
+    torch = torch_mod()
+    announce(f"act8 T={T} K={K}")
+    g = torch.Generator(device="cuda").manual_seed(T + K)
+    x = torch.randn(T, K, generator=g, device="cuda") * torch.where(torch.rand(K, generator=g, device="cuda") < 0.01, 30.0, 1.0)
+    _, y = _write_read(x.bfloat16())
+    # no value is further off than half a code and the two roundings of its block's largest value
+    top = x.bfloat16().float().view(T, -1, 64).abs().amax(2, keepdim=True)
+    off = (y.float() - x.bfloat16().float()).view(T, -1, 64).abs()
+    assert bool((off <= top * (0.5 / 127 + 2.0**-8 + 2.0**-22)).all())
+
+
+@gpu
+def test_every_pair_of_significands():
+    """All ties and near ties: every significand of x against every significand of the block's largest
+    value, at the exponents where the codes lie (0 to -8 below it)."""
+    torch = torch_mod()
+    announce("act8 all significands")
+    blocks = []
+    for e in range(0, 9):
+        top = (torch.arange(128, 256).float() / 128)                      # 128 largest values
+        x = torch.arange(128, 256).float() / 128 * 2.0**-e                # 128 values, in runs of 63
+        for part in (x[:63], x[63:126], torch.cat([x[126:], x[:61]])):
+            rows = part.repeat(128, 1).minimum(top[:, None])
+            sign = 1 - 2 * (torch.arange(63) % 2).float()
+            blocks.append(torch.cat([top[:, None], rows * sign], 1))
+    x = torch.cat(blocks)
+    for scale in (1.0, 2.0**-100, 2.0**119, 2.0**-30):
+        _write_read((x * scale).bfloat16().cuda().view(-1, 64 * 128))
+
+
+@gpu
+def test_smallest_and_largest_values():
+    """Blocks of subnormal numbers, zeros of both signs, the largest finite values, one value alone."""
+    torch = torch_mod()
+    announce("act8 ends of the range")
+    bits = torch.zeros(8, 256, dtype=torch.int32)
+    g = torch.Generator().manual_seed(3)
+    bits[0] = torch.randint(0, 128, (256,), generator=g)                  # subnormal
+    bits[1] = torch.randint(0, 2, (256,), generator=g) * 0x8000           # zeros
+    bits[2] = 0x7F7F - torch.randint(0, 64, (256,), generator=g)          # near the largest
+    bits[3, 70] = 1                                                       # the smallest number alone
+    bits[4, 5] = 0xFF7F                                                   # the largest, negative, alone
+    bits[5] = torch.randint(0, 0x7F80, (256,), generator=g)               # all magnitudes
+    bits[6] = torch.randint(0x0080, 0x1000, (256,), generator=g)          # 1e-38 .. 1e-24
+    bits[7] = torch.randint(0x7000, 0x7F80, (256,), generator=g) | 0x8000
+    _write_read(bits.to(torch.int16).view(torch.bfloat16).cuda())
+
+
+@gpu
+def test_nan_and_inf_reach_the_whole_block():
+    torch = torch_mod()
+    announce("act8 non-finite values")
+    x = torch.randn(6, 256, device="cuda").bfloat16()
+    x[1, 70], x[2, 0], x[3, 255] = float("nan"), float("inf"), float("-inf")
+    _, y = _write_read(x)
+    assert y[1, 64:128].isnan().all() and y[2, :64].isnan().all() and y[3, 192:].isnan().all()
+    assert int(y.isnan().sum()) == 3 * 64
+
+
+def _case(T, Ns, K, r, seed, double_quant=True):
+    torch = torch_mod()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = n(T, K).bfloat16()
+    qs = [qlora.quantize(n(N, K) * 0.02, double_quant=double_quant) for N in Ns]
+    A = (n(len(Ns) * r, K) * 0.01).bfloat16()
+    Bs = [(n(N, r) * 0.01).bfloat16() for N in Ns]
+    dys = [n(T, N).bfloat16() for N in Ns]
+    u = (x.float() @ A.float().t()).bfloat16()
+    return x, qs, A, Bs, dys, u
+
+
+def _expect(a, qs, A, Bs, dys, u, scale, r):
+    """(value, tolerance) of grad_x, grad_A_set and every grad_B in 64 bits."""
+    torch = torch_mod()
+    xh = qlora.act8_read(a).double()
+    T = xh.shape[0]
+    mm = torch.mm
+    gx, tx, ga, ta, gb = 0, 0, [], [], []
+    k, e = abs(scale), 2.0**-24
+    for i, (q, B, dy) in enumerate(zip(qs, Bs, dys)):
+        W, B, dy, Ai, ui = (t.double() for t in (qlora.dequantize(q), B, dy, A[i * r:(i + 1) * r], u[:, i * r:(i + 1) * r]))
+        N = W.shape[0]
+        v, va = mm(dy, B), mm(dy.abs(), B.abs())
+        gx = gx + mm(dy, W) + scale * mm(v, Ai)
+        tx = tx + N * e * mm(dy.abs(), W.abs()) + (2.0**-8 + (N + r) * e) * k * mm(va, Ai.abs())
+        ga.append(scale * mm(v.t().contiguous(), xh))
+        ta.append((N + 3 * T + 8) * e * k * mm(va.t().contiguous(), xh.abs()))
+        gb.append((scale * mm(dy.t().contiguous(), ui), (T + 4) * e * k * mm(dy.t().contiguous().abs(), ui.abs())))
+    return (gx, tx + 2.0**-8 * gx.abs()), (torch.cat(ga), torch.cat(ta)), gb
+
+
+def _within(got, want_tol, name):
+    want, tol = want_tol
+    assert not got.isnan().any(), name
+    over = float(((got.double() - want).abs() - tol - 1e-37).max())
+    assert over <= 0, (name, over)
+
+
+def _check(T, Ns, K, r, seed, scale=0.25, double_quant=True):
+    torch = torch_mod()
+    x, qs, A, Bs, dys, u = _case(T, Ns, K, r, seed, double_quant)
+    a = qlora.act8_write(x)
+    gx, ga, gbs = qlora.linear_set_bwd_act8(dys, a, qs, A, Bs, scale, u)
+    none, ga2, gbs2 = qlora.linear_set_bwd_act8(dys, a, qs, A, Bs, scale, u, need_grad_x=False)
+    torch.cuda.synchronize()
+    ex, ea, eb = _expect(a, qs, A, Bs, dys, u, scale, r)
+    _within(gx, ex, "grad_x")
+    _within(ga, ea, "grad_A")
+    for g, e in zip(gbs, eb):
+        _within(g, e, "grad_B")
+    assert none is None and torch.equal(ga, ga2) and all(torch.equal(p, q) for p, q in zip(gbs, gbs2))
+    if len(Ns) == 1:
+        one = qlora.linear_bwd_act8(dys[0], a, qs[0], A, Bs[0], scale, u)
+        assert torch.equal(one[0], gx) and torch.equal(one[1], ga) and torch.equal(one[2], gbs[0])
+
+
+@gpu
+@pytest.mark.parametrize("double_quant", [True, False])
+@pytest.mark.parametrize("T,N,K,r", [(1, 64, 64, 1), (1, 512, 320, 16), (2, 100, 128, 8), (3, 512, 256, 7),
+                                     (63, 257, 192, 100), (64, 128, 64, 64), (65, 384, 320, 256), (128, 256, 512, 65),
+                                     (300, 1000, 448, 16), (513, 256, 1088, 32), (1025, 640, 576, 8)])
+def test_backward_of_one_linear(T, N, K, r, double_quant):
+    announce(f"act8 backward T={T} N={N} K={K} r={r} double_quant={double_quant}")
+    _check(T, [N], K, r, seed=T + N, double_quant=double_quant)
+
+
+@gpu
+@pytest.mark.parametrize("T,Ns,K,r", [(1, (128, 128), 256, 8), (4, (256, 256, 256), 512, 16), (40, (512, 512, 512), 2048, 16),
+                                      (70, (100, 300), 192, 7), (200, (512, 128, 128), 384, 64),
+                                      (509, (256, 384, 512, 640), 320, 33)])
+def test_backward_of_a_set(T, Ns, K, r):
+    announce(f"act8 set backward T={T} Ns={Ns} K={K} r={r}")
+    _check(T, list(Ns), K, r, seed=T)
+
+
+@gpu
+def test_backward_7b_projection():
+    announce("act8 backward T=2048 4096x4096 r=64")
+    _check(2048, [4096], 4096, 64, seed=5)
+
+
+@gpu
+def test_gradient_of_A_against_differences():
+    """grad_A of sum(dy . (scale x_hat A^T B^T)) against central differences of that sum in 64 bits:
+    it is linear in A, so the difference is exact up to 64-bit rounding."""
+    torch = torch_mod()
+    announce("act8 grad_A against differences")
+    T, N, K, r = 50, 128, 192, 8
+    x, qs, A, Bs, dys, u = _case(T, [N], K, r, seed=6)
+    a = qlora.act8_write(x)
+    _, ga, _ = qlora.linear_bwd_act8(dys[0], a, qs[0], A, Bs[0], 0.5, u)
+    xh, dy, B = (t.double() for t in (qlora.act8_read(a), dys[0], Bs[0]))
+    f = lambda At: float((dy * (0.5 * torch.mm(torch.mm(xh, At.t().contiguous()), B.t().contiguous()))).sum())  # noqa: E731
+    d = torch.randn(r, K, device="cuda", dtype=torch.float64)
+    slope = (f(A.double() + d) - f(A.double() - d)) / 2
+    _, (_, tol), _ = _expect(a, qs, A, Bs, dys, u, 0.5, r)
+    assert abs(slope - float((ga.double() * d).sum())) <= float((tol * d.abs()).sum()) + 1e-9 * abs(slope)
+
+
+@gpu
+def test_captured_step_replays_equal_eager():
+    torch = torch_mod()
+    T, N, K, r = 130, 256, 512, 16
+    announce("act8 write and backward under graph capture")
+    x, qs, A, Bs, dys, u = _case(T, [N, N], K, r, seed=7)
+    a = qlora.Act8.empty(T, K)
+    ws = qlora.linear_set_act8_workspace(T, [N, N], K, r)
+    gx = torch.empty(T, K, device="cuda", dtype=torch.bfloat16)
+    ga = torch.empty(2 * r, K, device="cuda")
+    gbs = [torch.empty(N, r, device="cuda") for _ in range(2)]
+
+    def step():
+        qlora.act8_write(x, out=a)
+        qlora.linear_set_bwd_act8(dys, a, qs, A, Bs, 0.5, u, grad_x=gx, grad_A_set=ga, grad_Bs=gbs, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for rep in range(3):
+        x.copy_(torch.randn(T, K, device="cuda") * (rep + 1))
+        dys[0].copy_(torch.randn(T, N, device="cuda"))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (a.codes, a.scale, gx, ga, *gbs)]
+        torch.zeros(1000, device="cuda").add_(1.0)
+        step()
+        torch.cuda.synchronize()
+        for p, q in zip(got, (a.codes, a.scale, gx, ga, *gbs)):
+            assert torch.equal(p, q), rep
+
+
+# ------------------------------------------------------------------- refusals (no GPU)
+def test_refusals_before_any_launch():
+    L = qlora.lib()
+    ok = qlora.Act8Struct(16, 256, 0x10000, 0x20000)
+    ref = ctypes.byref
+    for call in (L.qlora_act8_write, lambda x, a, s: L.qlora_act8_read(a, x, s)):
+        assert call(None, ref(ok), None) == 1 and call(0x30000, None, None) == 1
+        assert call(0x30008, ref(ok), None) == 3
+        for T, K in ((0, 256), (16, 0), (16, 100), (-1, 256), (1 << 36, 64)):
+            assert call(0x30000, ref(qlora.Act8Struct(T, K, 0x10000, 0x20000)), None) == 2, (T, K)
+        assert call(0x30000, ref(qlora.Act8Struct(16, 256, None, 0x20000)), None) == 1
+        assert call(0x30000, ref(qlora.Act8Struct(16, 256, 0x10000, None)), None) == 1
+        assert call(0x30000, ref(qlora.Act8Struct(16, 256, 0x10008, 0x20000)), None) == 3
+        assert call(0x30000, ref(qlora.Act8Struct(16, 256, 0x10000, 0x20004)), None) == 3
+    w = qlora.NF4WeightStruct(512, 256, 0x10000, 0x20000, 0x30000, 0x40000)
+
+    def bwd(a=ok, q=w, dy=0x50000, A=0x60000, B=0x70000, r=8, scale=1.0, u=0x80000, gx=None, ga=0x90000, gb=0xA0000,
+            ws=0xB0000, ws_bytes=0):
+        return L.qlora_linear_bwd_act8(dy, ref(a) if a is not None else None, ref(q), A, B, r, scale, u, gx, ga, gb, ws,
+                                       ws_bytes, None)
+
+    assert bwd(a=None) == 1
+    assert bwd(q=qlora.NF4WeightStruct(512, 320, 0x10000, 0x20000, 0x30000, 0x40000)) == 2  # another n_in
+    assert bwd(r=0) == 2 and bwd(r=257) == 2 and bwd(scale=float("nan")) == 8
+    for name in ("dy", "A", "B", "u", "ga", "gb", "ws"):
+        assert bwd(**{name: None}) == 1, name
+        assert bwd(**{name: 0xC0008}) == 3, name
+    assert bwd(gx=0xC0008) == 3
+    need = qlora.linear_set_act8_workspace_bytes(16, [512], 256, 8)
+    assert need > 0 and bwd(ws_bytes=need - 1) == 4
+    b = qlora.linear_set_act8_workspace_bytes
+    assert b(0, [512], 256, 8) == 0 and b(16, [512], 100, 8) == 0 and b(16, [], 256, 8) == 0
+    assert b(16, [512] * 5, 256, 8) == 0 and b(16, [512, 0], 256, 8) == 0 and b(16, [512], 256, 300) == 0
+
+
+def test_tensor_checks():
+    torch = torch_mod()
+    with pytest.raises(ValueError, match="multiple of 64"):
+        qlora.Act8.empty(4, 100, device="cpu")
+    a = qlora.Act8.empty(4, 128, device="cpu")
+    assert a.nbytes() == 4 * 128 + 4 * 4 * 2
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="must be on"):
+        qlora.act8_write(x, out=a)
+    with pytest.raises(ValueError, match="must be on"):
+        qlora.act8_read(a, out=x)
+    with pytest.raises(ValueError, match="x must be"):
+        qlora.act8_write(x.float(), out=a)
+    with pytest.raises(ValueError, match="out must hold"):
+        qlora.act8_write(x, out=qlora.Act8.empty(4, 64, device="cpu"))
+    with pytest.raises(ValueError, match="scale must have shape"):
+        qlora.act8_read(qlora.Act8(a.codes, a.scale[:, :1].contiguous()))
+    with pytest.raises(ValueError, match="codes must be"):
+        qlora.act8_read(qlora.Act8(a.codes.float(), a.scale))
+    with pytest.raises(ValueError, match="64 columns"):
+        qlora.act8_read(qlora.Act8(a.codes[:, :100].contiguous(), a.scale))
