@@ -11,6 +11,7 @@
 #include "../../include/qlora.h"
 #include "common.hpp"
 #include "launch.hpp"
+#include "validate.hpp"
 
 using namespace qlora;
 
@@ -62,43 +63,6 @@ const Tables &tables() {
   return t;
 }
 
-constexpr int64_t kMaxNumel = (int64_t)1 << 37;
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// a * b <= kMaxNumel for positive a, b, without forming a product that could overflow
-bool product_ok(int64_t a, int64_t b) { return a > 0 && b > 0 && a <= kMaxNumel / b; }
-
-bool shape_ok(int64_t n_out, int64_t n_in) { return product_ok(n_out, n_in); }
-
-bool double_quantized(const qlora_nf4_weight *q) { return (q->flags & QLORA_NF4_FP32_CONSTANTS) == 0u; }
-
-qlora_status check_weight(const qlora_nf4_weight *q) {
-  if (!q) return QLORA_ERR_NULL;
-  if (!shape_ok(q->n_out, q->n_in)) return QLORA_ERR_SHAPE;
-  if ((q->flags & ~QLORA_NF4_FP32_CONSTANTS) != 0u) return QLORA_ERR_VALUE;
-  if (!q->codes || !q->absmax_scale) return QLORA_ERR_NULL;
-  if (!aligned16(q->codes) || !aligned16(q->absmax_scale)) return QLORA_ERR_ALIGN;
-  if (double_quantized(q)) {
-    if (!q->absmax_fp8 || !q->absmax_mean) return QLORA_ERR_NULL;
-    if (!aligned16(q->absmax_fp8) || !aligned16(q->absmax_mean)) return QLORA_ERR_ALIGN;
-  }
-  return QLORA_OK;
-}
-
-QWeight qweight(const qlora_nf4_weight *q) {
-  return QWeight{q->codes, q->absmax_fp8, q->absmax_scale, q->absmax_mean, q->n_out, q->n_in, double_quantized(q)};
-}
-
-qlora_status check_linear(int64_t T, const qlora_nf4_weight *q, int r, float scale) {
-  qlora_status s = check_weight(q);
-  if (s != QLORA_OK) return s;
-  if (T < 1 || T > kMaxNumel || q->n_in % kBlock != 0 || r < 1 || r > 256) return QLORA_ERR_SHAPE;
-  if (!product_ok(T, q->n_in) || !product_ok(T, q->n_out)) return QLORA_ERR_SHAPE;
-  if (!std::isfinite(scale)) return QLORA_ERR_VALUE;
-  return QLORA_OK;
-}
-
 // Dropout arguments: 0 <= p < 1 (finite); thresh = min(2^32 - 1, floor(p 2^32 + 1/2))
 // in fp64, and the fp32 factor 1 / (1 - p) of the kept values.
 bool make_dropout(double p, uint64_t seed, Dropout *d) {
@@ -133,22 +97,6 @@ bool device_address(const void *p, void **dev) {
     default:
       return false;
   }
-}
-
-// A projection set: 1..kMaxSetMembers members sharing n_in and the storage
-// form, adapter rank r per member.
-qlora_status check_set(int64_t T, int count, const qlora_nf4_weight *q, int r, float scale, int64_t *N) {
-  if (!q) return QLORA_ERR_NULL;
-  if (count < 1 || count > kMaxSetMembers) return QLORA_ERR_SHAPE;
-  for (int i = 0; i < count; ++i) {
-    const qlora_status s = check_linear(T, &q[i], r, scale);
-    if (s != QLORA_OK) return s;
-    if (q[i].n_in != q[0].n_in) return QLORA_ERR_SHAPE;
-    if (q[i].flags != q[0].flags) return QLORA_ERR_VALUE;
-    N[i] = q[i].n_out;
-  }
-  if (!product_ok(T, (int64_t)count * r)) return QLORA_ERR_SHAPE;
-  return QLORA_OK;
 }
 
 // ---- scratch of the forward without a caller workspace --------------------
@@ -194,36 +142,9 @@ size_t forward_scratch_bytes(const LinearPlan &p) {
   return std::max(p.off_part + lora_part_floats(p.T, p.r, p.K) * 4, qsplit ? p.off_qpart + qsplit * 4 : 0);
 }
 
-qlora_status check_act8(const qlora_act8 *a) {
-  if (!a) return QLORA_ERR_NULL;
-  if (!product_ok(a->T, a->K) || a->K % kBlock != 0) return QLORA_ERR_SHAPE;
-  if (!a->codes || !a->scale) return QLORA_ERR_NULL;
-  return aligned16(a->codes) && aligned16(a->scale) ? QLORA_OK : QLORA_ERR_ALIGN;
-}
-
-// The shapes the head's loss accepts.
-bool head_shape_ok(int64_t T, int64_t V, int64_t D) {
-  return D >= kBlock && D % kBlock == 0 && D <= kHeadMaxDim && product_ok(T, D) && product_ok(V, D);
-}
-
-// The loss of a bf16 head (w) or a packed one (q), the other one nullptr and both already checked.
-qlora_status head_loss(const uint16_t *h, int64_t T, const uint16_t *w, const QWeight *q, int64_t V, int64_t D,
-                       const int64_t *target, const float *weight, float scale, float *loss, float *lse,
-                       uint16_t *grad_h, void *ws, size_t ws_bytes, void *stream) {
-  if (!head_shape_ok(T, V, D)) return QLORA_ERR_SHAPE;
-  if (!std::isfinite(scale)) return QLORA_ERR_VALUE;
-  if (!h || !target || !loss || !ws) return QLORA_ERR_NULL;
-  if (!aligned16(h) || !aligned16(target) || !aligned16(loss) || !aligned16(ws) || (weight && !aligned16(weight)) ||
-      (lse && !aligned16(lse)) || (grad_h && !aligned16(grad_h)))
-    return QLORA_ERR_ALIGN;
-  const HeadPlan p = plan_head(T, V, D, grad_h != nullptr, q != nullptr);
-  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
-  hipError_t e = launch_head_loss(p, h, w, q, target, weight, scale, loss, lse, grad_h, (char *)ws, tables().cb,
-                                  (hipStream_t)stream);
-  return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
-}
-
 }  // namespace
+
+const Codebook &qlora::nf4_levels() { return tables().cb; }
 
 extern "C" {
 
@@ -257,12 +178,6 @@ size_t qlora_quantize_workspace_bytes(int64_t n_out, int64_t n_in) {
   if (qlora_nf4_sizes(n_out, n_in, nullptr, &nb, nullptr) != QLORA_OK) return 0;
   // status (256 B) + exponent bins + fp32 block absmax
   return 256 + kQuantizeBinBytes + (size_t)nb * 4;
-}
-
-// the shapes every linear call accepts (check_linear), for the size helpers
-bool linear_shape_ok(int64_t T, int64_t n_out, int64_t n_in, int r) {
-  return shape_ok(n_out, n_in) && n_in % kBlock == 0 && r >= 1 && r <= 256 && product_ok(T, n_in) &&
-         product_ok(T, n_out);
 }
 
 size_t qlora_linear_workspace_bytes(int64_t T, int64_t n_out, int64_t n_in, int r) {
@@ -535,89 +450,6 @@ qlora_status qlora_dropout_mask(const uint16_t *x, int64_t T, int64_t K, double 
   if (!aligned16(x) || !aligned16(keep_words) || !aligned16(x_drop)) return QLORA_ERR_ALIGN;
   hipError_t e = launch_dropout_mask(x, T, K, d.thresh, d.seed, keep_words, x_drop, (hipStream_t)stream);
   return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
-}
-
-qlora_status qlora_act8_write(const uint16_t *x, const qlora_act8 *a, void *stream) {
-  const qlora_status s = check_act8(a);
-  if (s != QLORA_OK) return s;
-  if (!x) return QLORA_ERR_NULL;
-  if (!aligned16(x)) return QLORA_ERR_ALIGN;
-  hipError_t e = launch_act8_encode(x, a->T, a->K, a->codes, a->scale, (hipStream_t)stream);
-  return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
-}
-
-qlora_status qlora_act8_read(const qlora_act8 *a, uint16_t *x, void *stream) {
-  const qlora_status s = check_act8(a);
-  if (s != QLORA_OK) return s;
-  if (!x) return QLORA_ERR_NULL;
-  if (!aligned16(x)) return QLORA_ERR_ALIGN;
-  hipError_t e = launch_act8_decode(a->codes, a->scale, a->T, a->K, x, (hipStream_t)stream);
-  return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
-}
-
-size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t *n_out, int64_t n_in, int r) {
-  if (!n_out || count < 1 || count > kMaxSetMembers || r < 1 || r > 256) return 0;
-  for (int i = 0; i < count; ++i)
-    if (!linear_shape_ok(T, n_out[i], n_in, r)) return 0;
-  if (!product_ok(T, (int64_t)count * r)) return 0;
-  return plan_linear_set_act8(T, count, n_out, n_in, r).total;
-}
-
-qlora_status qlora_linear_set_bwd_act8(const uint16_t *const *dy, const qlora_act8 *a, int count,
-                                       const qlora_nf4_weight *q, const uint16_t *A_set, const uint16_t *const *B,
-                                       int r, float scale, const uint16_t *u, uint16_t *grad_x, float *grad_A_set,
-                                       float *const *grad_B, void *ws, size_t ws_bytes, void *stream) {
-  int64_t N[kMaxSetMembers];
-  qlora_status s = check_act8(a);
-  if (s != QLORA_OK) return s;
-  s = check_set(a->T, count, q, r, scale, N);
-  if (s != QLORA_OK) return s;
-  if (q[0].n_in != a->K) return QLORA_ERR_SHAPE;
-  if (!dy || !A_set || !B || !u || !grad_A_set || !grad_B || !ws) return QLORA_ERR_NULL;
-  if (!aligned16(A_set) || !aligned16(u) || !aligned16(grad_A_set) || !aligned16(ws) ||
-      (grad_x && !aligned16(grad_x)))
-    return QLORA_ERR_ALIGN;
-  QWeight w[kMaxSetMembers];
-  for (int i = 0; i < count; ++i) {
-    if (!dy[i] || !B[i] || !grad_B[i]) return QLORA_ERR_NULL;
-    if (!aligned16(dy[i]) || !aligned16(B[i]) || !aligned16(grad_B[i])) return QLORA_ERR_ALIGN;
-    w[i] = qweight(&q[i]);
-  }
-  const Act8BwdPlan p = plan_linear_set_act8(a->T, count, N, a->K, r);
-  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
-  hipError_t e = launch_linear_set_bwd_act8(p, dy, a->codes, a->scale, w, A_set, B, scale, u, grad_x, grad_A_set,
-                                            grad_B, (char *)ws, tables().cb, (hipStream_t)stream);
-  return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
-}
-
-qlora_status qlora_linear_bwd_act8(const uint16_t *dy, const qlora_act8 *a, const qlora_nf4_weight *q,
-                                   const uint16_t *A, const uint16_t *B, int r, float scale, const uint16_t *u,
-                                   uint16_t *grad_x, float *grad_A, float *grad_B, void *ws, size_t ws_bytes,
-                                   void *stream) {
-  return qlora_linear_set_bwd_act8(&dy, a, 1, q, A, &B, r, scale, u, grad_x, grad_A, &grad_B, ws, ws_bytes, stream);
-}
-
-size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad, int packed) {
-  if (!head_shape_ok(T, V, D)) return 0;
-  return plan_head(T, V, D, grad != 0, packed != 0).total;
-}
-
-qlora_status qlora_head_loss(const uint16_t *h, int64_t T, const uint16_t *w, int64_t V, int64_t D,
-                             const int64_t *target, const float *weight, float scale, float *loss, float *lse,
-                             uint16_t *grad_h, void *ws, size_t ws_bytes, void *stream) {
-  if (!w) return QLORA_ERR_NULL;
-  if (!aligned16(w)) return QLORA_ERR_ALIGN;
-  return head_loss(h, T, w, nullptr, V, D, target, weight, scale, loss, lse, grad_h, ws, ws_bytes, stream);
-}
-
-qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_weight *q, const int64_t *target,
-                                 const float *weight, float scale, float *loss, float *lse, uint16_t *grad_h,
-                                 void *ws, size_t ws_bytes, void *stream) {
-  const qlora_status s = check_weight(q);
-  if (s != QLORA_OK) return s;
-  const QWeight qw = qweight(q);
-  return head_loss(h, T, nullptr, &qw, q->n_out, q->n_in, target, weight, scale, loss, lse, grad_h, ws, ws_bytes,
-                   stream);
 }
 
 void qlora_kernel_timing_enable(int enable) { kernel_timing_enable(enable != 0); }

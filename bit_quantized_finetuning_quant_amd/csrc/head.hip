@@ -44,6 +44,8 @@ constexpr int kStep = 64;      // contraction step
 constexpr int kThreads = 512;  // eight waves: 2 along the words or columns, 4 along the tokens
 constexpr int kUnit = 16384;   // bytes of half an operand tile of a step: 128 rows of 128 bytes
 constexpr int kStage = 4 * kUnit;
+constexpr int kFewTokens = 64;  // the few-token form, below
+constexpr int64_t kFewMaxWords = (int64_t)1 << 20;
 constexpr float kLog2eHi = 1.44269502162933349609375f;  // fl32(log2 e), and the rest of it
 constexpr float kLog2eLo = 1.92596299112661746887e-8f;
 constexpr float kLn2 = 0.693147182464599609375f;        // fl32(ln 2), and the rest of it
@@ -337,6 +339,15 @@ __global__ __launch_bounds__(1024) void head_scan(const int64_t *__restrict__ ta
   }
 }
 
+// n of a tile from its largest logit.  Finite whatever the logits are: NaN and infinite sums show in s.
+__device__ __forceinline__ float tile_exponent(float top) {
+  return ceilf(fminf(fmaxf(top * kLog2eHi, -2.0f * kMaxExponent), 2.0f * kMaxExponent));
+}
+// 2^(l log2 e - n)
+__device__ __forceinline__ float relative_exp(float l, float n) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2eLo, __builtin_fmaf(l, kLog2eHi, -n)));
+}
+
 // One tile of the logits, see the top.  e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
 // [tile of 128 words][tpad].
 __global__ __launch_bounds__(kThreads, 2) void head_logits(
@@ -399,9 +410,7 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
       }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    // a finite n whatever the logits are: NaN and infinite sums show in s
-    const float x = fminf(fmaxf(top * kLog2eHi, -2.0f * kMaxExponent), 2.0f * kMaxExponent);
-    const float ex = 128 * wm < nvt ? ceilf(x) : kNoExponent;
+    const float ex = 128 * wm < nvt ? tile_exponent(top) : kNoExponent;
     float s = 0.f;
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
@@ -410,7 +419,7 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
       for (int q = 0; q < 4; ++q) {
         const float l = acc[m][n][q];
         const int v = vl + 16 * m + q;
-        p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2eLo, __builtin_fmaf(l, kLog2eHi, -ex)));
+        p[q] = relative_exp(l, ex);
         if (v >= nvt) p[q] = 0.f;
         if (v == y) {
           target_logit[t] = l;
@@ -553,7 +562,7 @@ struct Outcome {
 };
 __device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
   Outcome r;
-  const float ey = __builtin_amdgcn_exp2f(__builtin_fmaf(ly, kLog2eLo, __builtin_fmaf(ly, kLog2eHi, -N)));
+  const float ey = relative_exp(ly, N);
   const float all = others + ey;
   const float base = __builtin_fmaf(N, kLn2, N * kLn2Lo);
   if (others <= ey) {
@@ -641,15 +650,15 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 
 // The decoded rows of the targets of a packed head, [T][D] bf16 in token order (one workgroup a
 // token): the decode of every use of the weight, one value at a time.
-__global__ __launch_bounds__(256) void head_target_rows(QWeight q, Codebook cb, const int *__restrict__ place,
-                                                        const int64_t *__restrict__ target,
+__global__ __launch_bounds__(256) void head_target_rows(QWeight q, Codebook cb, const int64_t *__restrict__ target,
                                                         uint16_t *__restrict__ out) {
   __shared__ float level[16];
   if (threadIdx.x < 16) level[threadIdx.x] = cb.v[threadIdx.x];
   __syncthreads();
   const int t = blockIdx.x;
-  if (place[t] < 0) return;
-  const int64_t e0 = target[t] * q.n_in;
+  const int64_t y = target[t];
+  if (y < 0 || y >= q.n_out) return;
+  const int64_t e0 = y * q.n_in;
   for (int c = threadIdx.x * 2; c < q.n_in; c += 512) {
     const int64_t el = e0 + c, block = el / kBlock;
     const float c1 = q.dq ? decode_constant(q.fp8[block], q.s2[block / kGroup], *q.mu) : q.s2[block];
@@ -659,10 +668,463 @@ __global__ __launch_bounds__(256) void head_target_rows(QWeight q, Codebook cb, 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Up to 64 tokens: both products are bound by streaming W once, so a
+// workgroup takes 64 words (or 64 columns d) and its four waves take every
+// fourth contraction step each, with no barrier until their sums are added:
+// a wave copies its own 64 x 64 tile of W (8 KB) and the tokens' piece of the
+// other operand into LDS, one or two steps ahead.  The tokens fill NT tiles
+// of 16.  Exponents n are per token and 64 words here, and the gradient's sums
+// of a chunk of words are relative to the chunk's own largest n, which
+// few_finish brings together: no pass over the tiles lies between the two.
+
+constexpr int kFewThreads = 256;
+constexpr int kFewWords = 64;       // words that share an exponent, and a step of the gradient
+constexpr int kFewChunk = 128;      // steps of a chunk at most: its shift bytes are held in LDS
+
+template <int NT>
+constexpr int few_stage() {
+  return 8192 + NT * 2048;
+}
+// Stages of a wave.  The logits of 16 tokens fit two workgroups of two stages on a CU; otherwise one
+// workgroup has the CU to itself and takes three where they fit.
+template <bool kTrans, int NT>
+constexpr int few_stages() {
+  return NT == 4 || (!kTrans && NT == 1) ? 2 : 3;
+}
+
+template <int n>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(n) : "memory");
+}
+
+// acc[m][n][q] of lane l: left row (word or column) 16 m + 4 (l/16) + q, token 16 n + l%16, summed over
+// the wave's steps first, first + 4, ..  mine: the wave's stages.  right_off: per lane, the rows of the
+// tokens.  left_rows: rows that exist, of the tile (words) or of the whole contraction (kTrans).
+template <bool kTrans, int NT>
+__device__ __forceinline__ void few_product(const char *left, uint32_t left_pitch, int left_rows, int64_t left_step,
+                                            const char *right, const uint32_t (&right_off)[2 * NT], int first,
+                                            int steps, char *mine, const uint8_t *shifts, f32x4 (&acc)[4][NT]) {
+  constexpr int kStages = few_stages<kTrans, NT>(), kBytes = few_stage<NT>(), kCopies = 8 + 2 * NT;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (first >= steps) return;
+  auto copy = [&](int step, char *stage) {
+    const int s = min(step, steps - 1);  // past the end: never read
+    const char *lb = left + s * left_step, *rb = right + (int64_t)s * (2 * kStep);
+    const int rows = kTrans ? left_rows - s * kStep : left_rows;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = 8 * j + (lane >> 3);
+      const int sw = kTrans ? swizzle_cols(r) : swizzle_rows(r);
+      dma16(lb, (uint32_t)__mul24(min(r, rows - 1), (int)left_pitch) + (((lane & 7) ^ sw) << 4),
+            lds_addr(stage + 1024 * j));
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) dma16(rb, right_off[j], lds_addr(stage + 8192 + 1024 * j));
+  };
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) copy(first + 4 * i, mine + i * kBytes);
+  char *stage = mine;
+  for (int s = first; s < steps; s += 4) {
+    wait_copies<(kStages - 1) * kCopies>();
+    u32x4 a[2][4], b[2][NT];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      read_left<kTrans>(stage, 0, kk, 0, lane, a[kk]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int r = 16 * n + (lane & 15), c = 4 * kk + (lane >> 4);
+        b[kk][n] = *(const u32x4 *)(stage + 8192 + r * 128 + ((c ^ swizzle_rows(r)) << 4));
+      }
+    }
+    uint32_t shift[NT];
+    if (kTrans) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) shift[n] = (uint32_t)shifts[s * (16 * NT) + 16 * n + (lane & 15)] * 0x00800080u;
+    }
+    HEAD_WAIT_LDS();
+    copy(s + 4 * kStages, stage);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (kTrans) scale_down(b[kk][n], shift[n]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[kk][m]), as_bf16x8(b[kk][n]), acc[m][n], 0,
+                                                             0, 0);
+      }
+    stage = stage == mine + (kStages - 1) * kBytes ? mine : stage + kBytes;
+  }
+  wait_copies<0>();
+}
+
+// The four waves' sums side by side in LDS: [wave][token][68], 64 left rows a token.
+constexpr int kFewPad = 68;
+template <int NT>
+__device__ __forceinline__ void few_put(const f32x4 (&acc)[4][NT], float *red) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __syncthreads();  // every wave is done with its stages
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *(f32x4 *)&red[((wave * NT + n) * 16 + (lane & 15)) * kFewPad + 16 * m + 4 * (lane >> 4)] = acc[m][n];
+  __syncthreads();
+}
+
+// The sum over the waves of four left rows of a token.
+template <int NT>
+__device__ __forceinline__ f32x4 few_sum(const float *red, int token, int row) {
+  f32x4 s = *(const f32x4 *)&red[token * kFewPad + row];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    const f32x4 x = *(const f32x4 *)&red[(w * 16 * NT + token) * kFewPad + row];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[q] += x[q];
+  }
+  return s;
+}
+
+// e (nullptr: the loss alone) [T][pitch], exponent and sum [64 words][64 tokens]; v0: the piece's first word, which is
+// also the first column of e; group0: its first 64 words.
+template <int NT>
+__global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const uint16_t *__restrict__ h,
+                                                             const uint16_t *__restrict__ w,
+                                                             const int64_t *__restrict__ target, int T, int64_t v0,
+                                                             int64_t nv, int D, uint16_t *__restrict__ e, int64_t pitch,
+                                                             float *__restrict__ exponent, float *__restrict__ sum,
+                                                             float *__restrict__ target_logit) {
+  constexpr int kBytes = few_stages<false, NT>() * few_stage<NT>();
+  __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t vt = (int64_t)blockIdx.x * kFewWords;
+  const int words = (int)min((int64_t)kFewWords, nv - vt);
+  uint32_t off[2 * NT];
+#pragma unroll
+  for (int j = 0; j < 2 * NT; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    off[j] = (uint32_t)min(r, T - 1) * (uint32_t)(2 * D) + (((lane & 7) ^ swizzle_rows(r)) << 4);
+  }
+  f32x4 acc[4][NT];
+  few_product<false, NT>(uniform(w + vt * D), (uint32_t)D * 2u, words, 2 * kStep, uniform(h), off, wave, D / kStep,
+                         lds + wave * kBytes, nullptr, acc);
+  float *red = (float *)lds;
+  few_put<NT>(acc, red);
+  // 4 NT tokens a wave, 16 / NT lanes a token, 4 NT words a lane
+  constexpr int kLanes = 16 / NT, kWords = 4 * NT;
+  const int t = wave * 4 * NT + lane / kLanes, first = lane % kLanes * kWords;
+  const bool on = t < T;
+  const int64_t at = on ? target[t] - v0 - vt : -1;
+  const int y = at >= 0 && at < kFewWords ? (int)at : -1;
+  float l[kWords], top = -INFINITY;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < kWords; i += 4) {
+    const f32x4 x = few_sum<NT>(red, t, first + i);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = first + i + q < words;
+      l[i + q] = x[q];
+      odd |= in && x[q] != x[q];
+      top = fmaxf(top, in ? x[q] : -INFINITY);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float ex = tile_exponent(top);
+  float s = 0.f;
+  uint32_t packed[kWords / 2];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    float p = relative_exp(l[i], ex);
+    if (first + i >= words) p = 0.f;
+    if (first + i == y) {
+      target_logit[t] = l[i];
+      p = 0.f;
+    }
+    s += p;
+    l[i] = p;
+  }
+  if (e && on) {
+#pragma unroll
+    for (int i = 0; i < kWords / 2; ++i) packed[i] = pack_bf16x2(l[2 * i], l[2 * i + 1]);
+    uint2 *row = (uint2 *)(e + (int64_t)t * pitch + v0 + vt + first);
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) row[i] = make_uint2(packed[2 * i], packed[2 * i + 1]);
+  }
+  if (odd) s = NAN;
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) s += __shfl_xor(s, d);
+  if (on && lane % kLanes == 0) {
+    const int64_t i = (v0 + vt) / kFewWords * kFewTokens + t;
+    exponent[i] = ex;
+    sum[i] = s;
+  }
+}
+
+// One chunk of words, 64 columns: part[chunk][T][D] relative to 2^N of the chunk, and (first columns) its N and S
+// [chunk][64].  e, exponent and sum start at the piece.
+template <int NT>
+__global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__restrict__ e, int64_t pitch,
+                                                           const uint16_t *__restrict__ w, int T, int64_t nv, int D,
+                                                           int chunk_steps, int chunk0,
+                                                           const float *__restrict__ exponent,
+                                                           const float *__restrict__ sum, float *__restrict__ N,
+                                                           float *__restrict__ S, float *__restrict__ part) {
+  constexpr int kBytes = few_stages<true, NT>() * few_stage<NT>(), kT = 16 * NT, kRows = kFewThreads / kT;
+  __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
+  __shared__ uint8_t shifts[kFewChunk * kT];
+  __shared__ float fold[kFewThreads];
+  const int slices = D / 64;
+  const int chunk = (int)(blockIdx.x / slices), slice = (int)(blockIdx.x % slices);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t vb = (int64_t)chunk * chunk_steps * kFewWords;
+  const int words = (int)min((int64_t)chunk_steps * kFewWords, nv - vb);
+  const int steps = (words + kFewWords - 1) / kFewWords;
+  {  // the chunk's largest exponent of each token, its sum, and every step's distance from it
+    const int t = threadIdx.x % kT, g = threadIdx.x / kT;
+    const float *ex = exponent + vb / kFewWords * kFewTokens + min(t, T - 1);
+    const float *sm = sum + vb / kFewWords * kFewTokens + min(t, T - 1);
+    float top = kNoExponent;
+    for (int i = g; i < steps; i += kRows) top = fmaxf(top, ex[i * kFewTokens]);
+    fold[threadIdx.x] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) top = fmaxf(top, fold[i * kT + t]);
+    __syncthreads();
+    float s = 0.f;
+    for (int i = g; i < steps; i += kRows) {
+      const float d = top - ex[i * kFewTokens];
+      shifts[i * kT + t] = (uint8_t)fminf(d, 255.f);
+      if (slice == 0) s += sm[i * kFewTokens] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
+    }
+    fold[threadIdx.x] = s;
+    __syncthreads();
+    if (slice == 0 && g == 0 && t < T) {
+      for (int i = 1; i < kRows; ++i) s += fold[i * kT + t];
+      N[(chunk0 + chunk) * kFewTokens + t] = top;
+      S[(chunk0 + chunk) * kFewTokens + t] = s;
+    }
+  }
+  uint32_t off[2 * NT];
+#pragma unroll
+  for (int j = 0; j < 2 * NT; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    off[j] = (uint32_t)min(r, T - 1) * (uint32_t)(2 * pitch) + (((lane & 7) ^ swizzle_rows(r)) << 4);
+  }
+  f32x4 acc[4][NT];
+  few_product<true, NT>(uniform(w + vb * D + 64 * slice), (uint32_t)D * 2u, words, (int64_t)kStep * D * 2,
+                        uniform(e + vb), off, wave, steps, lds + wave * kBytes, shifts, acc);
+  float *red = (float *)lds;
+  few_put<NT>(acc, red);
+  // 16 lanes a token, four columns each
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int t = i * 16 + (threadIdx.x >> 4), d = 4 * (threadIdx.x & 15);
+    if (t < T) *(f32x4 *)(part + ((int64_t)(chunk0 + chunk) * T + t) * D + 64 * slice + d) = few_sum<NT>(red, t, d);
+  }
+}
+
+// Notes a target past the vocabulary (T <= 64; the first wave).
+__device__ __forceinline__ void few_state(const int64_t *target, int T, int64_t V, uint32_t *state) {
+  const int lane = threadIdx.x;
+  if (lane >= 64) return;
+  const bool bad = lane < T && target[lane] >= V;
+  const uint64_t any = __ballot(bad);
+  if (lane == 0) state[0] = any ? 2u : 0u;
+}
+
+// Loss and lse of one token a workgroup from the exponents and sums of all its words.
+__global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ target, int T, int64_t V, int groups,
+                                                  const float *__restrict__ exponent, const float *__restrict__ sum,
+                                                  const float *__restrict__ target_logit, uint32_t *__restrict__ state,
+                                                  float *__restrict__ loss, float *__restrict__ lse) {
+  __shared__ float fold[256];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  if (t == 0) few_state(target, T, V, state);
+  const int64_t y = target[t];
+  if (y < 0 || y >= V) {
+    if (tid == 0) {
+      loss[t] = y < 0 ? 0.f : NAN;
+      if (lse) lse[t] = y < 0 ? 0.f : NAN;
+    }
+    return;
+  }
+  float top = kNoExponent;
+  for (int i = tid; i < groups; i += 256) top = fmaxf(top, exponent[i * kFewTokens + t]);
+  fold[tid] = top;
+  __syncthreads();
+  for (int d = 128; d > 0; d >>= 1) {
+    if (tid < d) fold[tid] = fmaxf(fold[tid], fold[tid + d]);
+    __syncthreads();
+  }
+  top = fold[0];
+  __syncthreads();
+  float s = 0.f;
+  for (int i = tid; i < groups; i += 256)
+    s += sum[i * kFewTokens + t] * __builtin_amdgcn_exp2f(-fminf(top - exponent[i * kFewTokens + t], 300.f));
+  fold[tid] = s;
+  __syncthreads();
+  for (int d = 128; d > 0; d >>= 1) {
+    if (tid < d) fold[tid] += fold[tid + d];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    const Outcome r = outcome(top, fold[0], target_logit[t]);
+    loss[t] = r.loss;
+    if (lse) lse[t] = r.lse;
+  }
+}
+
+// grad_h, loss and lse from the chunks: workgroup (token, 1024 columns), four columns a thread.
+__global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ target, int T, int64_t V, int D,
+                                                  int chunks, const float *__restrict__ N, const float *__restrict__ S,
+                                                  const float *__restrict__ target_logit,
+                                                  const uint16_t *__restrict__ wy, bool by_token,
+                                                  const float *__restrict__ weight, float scale,
+                                                  const float *__restrict__ part, uint32_t *__restrict__ state,
+                                                  float *__restrict__ loss, float *__restrict__ lse,
+                                                  uint16_t *__restrict__ grad) {
+  const int t = blockIdx.x, c = (int)blockIdx.y * 1024 + 4 * (int)threadIdx.x;
+  if (t == 0 && blockIdx.y == 0) few_state(target, T, V, state);
+  const int64_t y = target[t];
+  const bool lead = blockIdx.y == 0 && threadIdx.x == 0;
+  uint2 *g = (uint2 *)(grad + (int64_t)t * D + c);
+  if (y < 0 || y >= V) {
+    const uint32_t fill = y < 0 ? 0u : 0x7FC07FC0u;
+    if (c < D) *g = make_uint2(fill, fill);
+    if (lead) {
+      loss[t] = y < 0 ? 0.f : NAN;
+      if (lse) lse[t] = y < 0 ? 0.f : NAN;
+    }
+    return;
+  }
+  float top = kNoExponent, s = 0.f;
+  for (int i = 0; i < chunks; ++i) top = fmaxf(top, N[i * kFewTokens + t]);
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < chunks; ++i) {
+    const float f = __builtin_amdgcn_exp2f(-fminf(top - N[i * kFewTokens + t], 300.f));
+    s += S[i * kFewTokens + t] * f;
+    if (c < D) {
+      const f32x4 x = *(const f32x4 *)(part + ((int64_t)i * T + t) * D + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[q] = __builtin_fmaf(x[q], f, sum[q]);
+    }
+  }
+  const Outcome r = outcome(top, s, target_logit[t]);
+  if (lead) {
+    loss[t] = r.loss;
+    if (lse) lse[t] = r.lse;
+  }
+  if (c >= D) return;
+  const float c_t = weight ? scale * weight[t] : scale;
+  const float a = c_t * r.inv, b = c_t * r.other;
+  const uint2 wv = *(const uint2 *)(wy + (by_token ? (int64_t)t : y) * D + c);
+  *g = make_uint2(pack_bf16x2(__builtin_fmaf(a, sum[0], -b * bf16_lo(wv.x)), __builtin_fmaf(a, sum[1], -b * bf16_hi(wv.x))),
+                  pack_bf16x2(__builtin_fmaf(a, sum[2], -b * bf16_lo(wv.y)), __builtin_fmaf(a, sum[3], -b * bf16_hi(wv.y))));
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
+
+// The few-token form: e [T][V], the sums of every chunk of words.
+static HeadPlan plan_few(HeadPlan p, int64_t piece) {
+  p.pieces = cdiv(p.V, piece);
+  p.words = cdiv(cdiv(p.V, p.pieces), kTileV) * kTileV;
+  p.pieces = cdiv(p.V, p.words);
+  p.splits = p.split_words = 0;
+  const int64_t groups = cdiv(p.V, kFewWords), piece_steps = cdiv(std::min(p.words, p.V), kFewWords);
+  if (p.grad) {
+    // about one workgroup a CU, at least a step for each of its waves, at most kFewChunk steps
+    const int64_t chunks = std::max<int64_t>(1, std::min(256 / (p.D / 64), cdiv(piece_steps, 4)));
+    const int64_t steps = std::min<int64_t>(kFewChunk, cdiv(piece_steps, chunks));
+    p.split_words = steps * kFewWords;
+    for (int64_t v0 = 0; v0 < p.V; v0 += p.words) p.splits += cdiv(std::min(p.words, p.V - v0), p.split_words);
+  }
+  size_t off = 256;
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  p.off_logit = take(kFewTokens * 4);
+  p.off_exponent = take((size_t)groups * kFewTokens * 4);
+  p.off_sum = take((size_t)groups * kFewTokens * 4);
+  p.off_n = take((size_t)p.splits * kFewTokens * 4);
+  p.off_s = take((size_t)p.splits * kFewTokens * 4);
+  p.off_e = p.grad ? take((size_t)p.T * groups * kFewWords * 2) : 0;
+  p.off_part = p.grad ? take((size_t)p.splits * p.T * p.D * 4) : 0;
+  p.off_w = p.packed ? take((size_t)p.words * p.D * 2) : 0;
+  p.off_wy = p.packed && p.grad ? take((size_t)p.T * p.D * 2) : 0;
+  p.off_rows = p.off_place = p.off_factor = p.off_shift = 0;
+  p.total = off;
+  return p;
+}
+
+// Rows v0 .. v0 + nv of a packed head, decoded to out; v0 is a multiple of 256, so whole groups of
+// constants lie before it.
+static hipError_t decode_rows(const QWeight &q, int64_t v0, int64_t nv, uint16_t *out, const Codebook &cb,
+                              hipStream_t st) {
+  QWeight rows = q;
+  const int64_t block = v0 * q.n_in / kBlock;
+  rows.n_out = nv;
+  rows.codes += v0 * q.n_in / 2;
+  if (rows.dq) {
+    rows.fp8 += block;
+    rows.s2 += block / kGroup;
+  } else {
+    rows.s2 += block;
+  }
+  return launch_dequantize(rows, out, cb, st);
+}
+
+template <int NT>
+static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_t *w, const QWeight *q,
+                             const int64_t *target, const float *weight, float scale, float *loss, float *lse,
+                             uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st) {
+  uint32_t *state = (uint32_t *)ws;
+  float *logit = (float *)(ws + p.off_logit), *N = (float *)(ws + p.off_n), *S = (float *)(ws + p.off_s);
+  float *exponent = (float *)(ws + p.off_exponent), *sum = (float *)(ws + p.off_sum);
+  float *part = (float *)(ws + p.off_part);
+  uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
+  uint16_t *wp = (uint16_t *)(ws + p.off_w), *wy = (uint16_t *)(ws + p.off_wy);
+  const int T = (int)p.T, D = (int)p.D, groups = (int)cdiv(p.V, kFewWords);
+  const int64_t pitch = (int64_t)groups * kFewWords;
+  int chunk0 = 0;
+  for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
+    const int64_t nv = std::min(p.words, p.V - v0);
+    const uint16_t *piece = w ? w + v0 * p.D : wp;
+    if (q) {
+      const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
+      if (err != hipSuccess) return err;
+    }
+    few_logits<NT><<<(unsigned)cdiv(nv, kFewWords), kFewThreads, 0, st>>>(h, piece, target, T, v0, nv, D, e, pitch,
+                                                                        exponent, sum, logit);
+    if (!p.grad) continue;
+    const int chunks = (int)cdiv(nv, p.split_words);
+    const int64_t g0 = v0 / kFewWords * kFewTokens;
+    few_grad<NT><<<(unsigned)(chunks * (D / 64)), kFewThreads, 0, st>>>(e + v0, pitch, piece, T, nv, D,
+                                                                      (int)(p.split_words / kFewWords), chunk0,
+                                                                      exponent + g0, sum + g0, N, S, part);
+    chunk0 += chunks;
+  }
+  if (!p.grad) {
+    few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, logit, state, loss, lse);
+    return hipGetLastError();
+  }
+  if (q) head_target_rows<<<(unsigned)T, 256, 0, st>>>(*q, cb, target, wy);
+  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 1024)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, logit,
+                                                                       q ? wy : w, q != nullptr, weight, scale, part,
+                                                                       state, loss, lse, grad);
+  return hipGetLastError();
+}
 
 HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   HeadPlan p;
@@ -671,12 +1133,17 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.D = D;
   p.grad = grad;
   p.packed = packed;
+  p.few = T <= kFewTokens && V <= kFewMaxWords;
   p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
   p.tpad = cdiv(p.chunk, kTileT) * kTileT;
   // Words of a piece: 64 MB of e (grad) and of decoded weight (packed); nothing else grows with it.
   int64_t vc = cdiv(V, kTileV) * kTileV;
   // The exponents and sums of its tiles stay within 64 MB too.
   const int64_t budget = (int64_t)32 << 20;
+  if (p.few) {  // one piece, but for the decoded rows of a packed head
+    if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
+    return plan_few(p, vc);
+  }
   vc = std::min(vc, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
   if (grad) vc = std::min(vc, std::max<int64_t>(budget / p.tpad / kTileV * kTileV, 8 * kTileV));
   if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
@@ -721,6 +1188,9 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
 hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t *w, const QWeight *q,
                             const int64_t *target, const float *weight, float scale, float *loss, float *lse,
                             uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st) {
+  if (p.few && p.T <= 16) return launch_few<1>(p, h, w, q, target, weight, scale, loss, lse, grad, ws, cb, st);
+  if (p.few && p.T <= 32) return launch_few<2>(p, h, w, q, target, weight, scale, loss, lse, grad, ws, cb, st);
+  if (p.few) return launch_few<4>(p, h, w, q, target, weight, scale, loss, lse, grad, ws, cb, st);
   uint32_t *state = (uint32_t *)ws;
   int *rows = (int *)(ws + p.off_rows), *place = (int *)(ws + p.off_place);
   float *logit = (float *)(ws + p.off_logit), *N = (float *)(ws + p.off_n), *S = (float *)(ws + p.off_s);
@@ -739,18 +1209,8 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
     for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
       const int64_t nv = std::min(p.words, p.V - v0), nleft = cdiv(nv, kTileV);
       const uint16_t *piece = w ? w + v0 * p.D : wp;
-      if (q) {  // rows v0 .. v0 + nv of the packed head; v0 is a multiple of 256, so whole groups lie before it
-        QWeight part_q = *q;
-        const int64_t block = v0 * p.D / kBlock;
-        part_q.n_out = nv;
-        part_q.codes += v0 * p.D / 2;
-        if (part_q.dq) {
-          part_q.fp8 += block;
-          part_q.s2 += block / kGroup;
-        } else {
-          part_q.s2 += block;
-        }
-        const hipError_t err = launch_dequantize(part_q, wp, cb, st);
+      if (q) {
+        const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
         if (err != hipSuccess) return err;
       }
       head_logits<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(hc, piece, yc, v0, nv, D, nleft, ntoken, rows,
@@ -767,7 +1227,7 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
       head_losses<<<(unsigned)cdiv(T, 256), 256, 0, st>>>(T, place, N, S, logit, loss + c0, lse ? lse + c0 : nullptr);
       continue;
     }
-    if (q) head_target_rows<<<(unsigned)T, 256, 0, st>>>(*q, cb, place, yc, wy);
+    if (q) head_target_rows<<<(unsigned)T, 256, 0, st>>>(*q, cb, yc, wy);
     head_finish<<<(unsigned)T, 256, 0, st>>>(place, N, S, logit, yc, q ? wy : w, q != nullptr,
                                              weight ? weight + c0 : nullptr, scale, part, (int)p.splits, stride, D,
                                              loss + c0, lse ? lse + c0 : nullptr, grad + c0 * p.D);

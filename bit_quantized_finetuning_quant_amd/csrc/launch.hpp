@@ -8,6 +8,9 @@
 
 namespace qlora {
 
+// The 16 NF4 levels (api.hip).
+const Codebook &nf4_levels();
+
 // Packed weight as the kernels see it.  dq: the block constants are FP8
 // codes (fp8) with fp32 group scales (s2) and a tensor mean (mu); otherwise
 // s2 holds one fp32 constant per block and fp8, mu are unused.
@@ -258,7 +261,7 @@ constexpr int64_t kHeadMaxDim = 65536;     // D: a chunk's byte offsets stay bel
 constexpr int64_t kHeadMaxSplit = 8192;    // words of one split of the gradient's contraction
 struct HeadPlan {
   int64_t T, V, D;
-  bool grad, packed;
+  bool grad, packed, few;  // few: the few-token form (splits: chunks of words in all, split_words: of each)
   int64_t chunk, tpad, words, pieces, splits, split_words;
   size_t off_rows, off_place, off_logit, off_n, off_s, off_factor, off_exponent, off_sum, off_shift, off_e, off_part,
       off_w, off_wy, total;

@@ -168,9 +168,11 @@ def _torch():
 
 
 def _stream(stream=None) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    # the current stream's handle without a Stream object around it (3 us of every call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t) -> int:
@@ -752,10 +754,10 @@ def act8_write(x, out: Act8 = None, stream=None) -> Act8:
     T, K = int(x.shape[0]), int(x.shape[1])
     chk = _Args(x.device)
     chk.bf16(x, "x", (T, K))
-    a = out if out is not None else Act8.empty(T, K, x.device)
-    if _check_act8(a, chk) != (T, K):
-        raise ValueError(f"out must hold {T} x {K} values, not {a.codes.shape[0]} x {a.codes.shape[1]}")
+    if out is not None and _check_act8(out, chk) != (T, K):
+        raise ValueError(f"out must hold {T} x {K} values, not {out.codes.shape[0]} x {out.codes.shape[1]}")
     chk.done()
+    a = out if out is not None else Act8.empty(T, K, x.device)
     st = a.struct()
     _check(lib().qlora_act8_write(_ptr(x), ctypes.byref(st), _stream(stream)), "qlora_act8_write")
     return a
@@ -766,9 +768,10 @@ def act8_read(a: Act8, out=None, stream=None):
     torch = _torch()
     chk = _Args(a.codes.device)
     T, K = _check_act8(a, chk)
-    y = out if out is not None else torch.empty((T, K), dtype=torch.bfloat16, device=a.codes.device)
-    chk.bf16(y, "out", (T, K))
+    if out is not None:
+        chk.bf16(out, "out", (T, K))
     chk.done()
+    y = out if out is not None else torch.empty((T, K), dtype=torch.bfloat16, device=a.codes.device)
     st = a.struct()
     _check(lib().qlora_act8_read(ctypes.byref(st), _ptr(y), _stream(stream)), "qlora_act8_read")
     return y
@@ -810,22 +813,28 @@ def linear_set_bwd_act8(dys, a: Act8, qs, A_set, Bs, scale: float, u, need_grad_
     n_in = qs[0].n_in
     if not need_grad_x:
         grad_x = None
-    elif grad_x is None:
-        grad_x = torch.empty((T, n_in), dtype=torch.bfloat16, device=dev)
-    if grad_x is not None:
+    elif grad_x is not None:
         chk.bf16(grad_x, "grad_x", (T, n_in))
+    if grad_A_set is not None:
+        chk.f32(grad_A_set, "grad_A_set", (count * r, n_in))
+    if grad_Bs is not None:
+        _check_list(grad_Bs, count, "grad_Bs")
+        for i, (q, g) in enumerate(zip(qs, grad_Bs)):
+            chk.f32(g, f"grad_Bs[{i}]", (q.n_out, r))
+    chk.done()
+    if need_grad_x and grad_x is None:
+        grad_x = torch.empty((T, n_in), dtype=torch.bfloat16, device=dev)
     if grad_A_set is None:
         grad_A_set = torch.empty((count * r, n_in), dtype=torch.float32, device=dev)
-    chk.f32(grad_A_set, "grad_A_set", (count * r, n_in))
     if grad_Bs is None:
         grad_Bs = [torch.empty((q.n_out, r), dtype=torch.float32, device=dev) for q in qs]
-    _check_list(grad_Bs, count, "grad_Bs")
-    for i, (q, g) in enumerate(zip(qs, grad_Bs)):
-        chk.f32(g, f"grad_Bs[{i}]", (q.n_out, r))
-    chk.done()
     n_outs = [q.n_out for q in qs]
-    ws = workspace if workspace is not None else linear_set_act8_workspace(T, n_outs, n_in, r, dev)
-    wsb = _workspace(ws, dev, lambda: linear_set_act8_workspace_bytes(T, n_outs, n_in, r))
+    if workspace is None:
+        ws = linear_set_act8_workspace(T, n_outs, n_in, r, dev)
+        wsb = ws.numel()
+    else:
+        ws = workspace
+        wsb = _workspace(ws, dev, lambda: linear_set_act8_workspace_bytes(T, n_outs, n_in, r))
     st = (NF4WeightStruct * count)(*[q.struct() for q in qs])
     sa = a.struct()
     _check(lib().qlora_linear_set_bwd_act8(_ptrs(dys), ctypes.byref(sa), count, st, _ptr(A_set), _ptrs(Bs), r,
@@ -869,19 +878,27 @@ def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=N
     chk.i64(target, "target", (T,))
     if weight is not None:
         chk.f32(weight, "weight", (T,))
-    loss = loss if loss is not None else torch.empty(T, dtype=torch.float32, device=dev)
-    chk.f32(loss, "loss", (T,))
-    lse = lse if lse is not None else torch.empty(T, dtype=torch.float32, device=dev)
-    chk.f32(lse, "lse", (T,))
+    if loss is not None:
+        chk.f32(loss, "loss", (T,))
+    if lse is not None:
+        chk.f32(lse, "lse", (T,))
     if not need_grad:
         grad_h = None
-    elif grad_h is None:
-        grad_h = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
-    if grad_h is not None:
+    elif grad_h is not None:
         chk.bf16(grad_h, "grad_h", (T, D))
     chk.done()
-    ws = workspace if workspace is not None else head_loss_workspace(T, V, D, need_grad, packed, dev)
-    wsb = _workspace(ws, dev, lambda: head_loss_workspace_bytes(T, V, D, need_grad, packed))
+    if loss is None:
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+    if need_grad and grad_h is None:
+        grad_h = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        ws = head_loss_workspace(T, V, D, need_grad, packed, dev)
+        wsb = ws.numel()
+    else:
+        ws = workspace
+        wsb = _workspace(ws, dev, lambda: head_loss_workspace_bytes(T, V, D, need_grad, packed))
     if packed:
         st = head.struct()
         _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), _ptr(target), _ptr(weight), float(scale),

@@ -94,7 +94,10 @@ def _check(h, head, w, y, scale=1.0, weight=None, **kw):
 
 SHAPES = [(1, 64, 1), (1, 64, 2), (1, 128, 300), (2, 64, 255), (3, 192, 257), (16, 256, 1000), (37, 320, 129),
           (63, 128, 700), (64, 448, 2049), (65, 64, 511), (129, 256, 1025), (255, 512, 3001), (257, 192, 4100),
-          (300, 1088, 777), (513, 2112, 1281), (1000, 256, 9001)]
+          (300, 1088, 777), (513, 2112, 1281), (1000, 256, 9001),
+          # up to 64 tokens: one to four tiles of 16, one to many chunks of words, steps shared unevenly by the waves
+          (1, 4096, 32003), (5, 8192, 3000), (16, 64, 16385), (17, 1024, 8193), (32, 2048, 641), (33, 64, 100001),
+          (48, 576, 4097), (64, 1088, 20001), (2, 65536, 300)]
 
 
 @gpu
@@ -144,13 +147,14 @@ def test_packed_head_in_pieces_by_size():
 
 
 @gpu
+@pytest.mark.parametrize("T", [15, 40, 260])
 @pytest.mark.parametrize("order", ["rising", "falling", "far"])
-def test_exponents_of_tiles_and_pieces(order):
+def test_exponents_of_tiles_and_pieces(order, T):
     """Logits whose largest value moves by hundreds between the tiles and the pieces: what a tile
     holds is rescaled by up to 2^-255 and below."""
     torch = torch_mod()
-    T, D, V = 260, 64, 140003
-    announce(f"head loss, {order} logits")
+    D, V = 64, 140003
+    announce(f"head loss, {order} logits T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=11, std=0.05, masked=0.1))
     ramp = torch.linspace(0, 60, V, device="cuda")
     if order == "falling":
@@ -164,11 +168,12 @@ def test_exponents_of_tiles_and_pieces(order):
 
 
 @gpu
-def test_sure_tokens_keep_relative_precision():
+@pytest.mark.parametrize("T", [64, 130])
+def test_sure_tokens_keep_relative_precision(T):
     """Losses down to about 1e-8 (3000 words 26 below the target): loss = log1p(others / e_y) and 1 - p_y are formed without a difference."""
     torch = torch_mod()
-    T, D, V = 64, 256, 3000
-    announce("head loss of sure tokens")
+    D, V = 256, 3000
+    announce(f"head loss of sure tokens T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=12, std=0.02, masked=0.0))
     lean = torch.linspace(5, 28, T, device="cuda")[:, None] / w[y].float().square().sum(1, keepdim=True)
     h = (lean * w[y].float()).bfloat16()
@@ -177,16 +182,17 @@ def test_sure_tokens_keep_relative_precision():
 
 
 @gpu
-def test_tokens_without_loss():
+@pytest.mark.parametrize("T", [20, 64, 600])
+def test_tokens_without_loss(T):
     """Negative targets: zeros, whatever the rows hold; a call without any loss; all rows but one."""
     torch = torch_mod()
-    T, D, V = 600, 128, 900
-    announce("head loss with masked tokens")
+    D, V = 128, 900
+    announce(f"head loss with masked tokens T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=13, std=0.3, masked=0.5))
-    y[300:560] = -1
+    y[T // 2:T - 5] = -1
     dirty = h.clone()
     dirty[y < 0] = float("nan")
-    dirty[310] = float("inf")
+    dirty[T // 2 + 1] = float("inf")
     a, b = _check(h, w, w, y), qlora.head_loss(dirty, w, y)
     for x, z in zip(a, b):
         assert torch.equal(x, z)
@@ -201,12 +207,13 @@ def test_tokens_without_loss():
 
 
 @gpu
+@pytest.mark.parametrize("T", [40, 70])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
-def test_values_past_the_range(value):
+def test_values_past_the_range(value, T):
     """NaN, Inf or an overflow in one token's row: NaN for that token, the others as they were."""
     torch = torch_mod()
-    T, D, V = 70, 128, 1000
-    announce(f"head loss with {value} in a row")
+    D, V = 128, 1000
+    announce(f"head loss with {value} in a row T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=14, std=0.3, masked=0.0))
     want = qlora.head_loss(h, w, y)
     bad = h.clone()
@@ -219,21 +226,24 @@ def test_values_past_the_range(value):
 
 
 @gpu
-def test_target_past_the_vocabulary():
+@pytest.mark.parametrize("T", [63, 70])
+def test_target_past_the_vocabulary(T):
     torch = torch_mod()
-    T, D, V = 70, 128, 1000
-    announce("head loss with a target past the vocabulary")
+    D, V = 128, 1000
+    announce(f"head loss with a target past the vocabulary T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=15, masked=0.2))
     ws = qlora.head_loss_workspace(T, V, D)
     want = qlora.head_loss(h, w, y, workspace=ws)
     assert qlora.status_read(ws) == 0
     bad = y.clone()
     bad[7], bad[60] = V, 2**40
+    bad[8] = -2**40
     got = qlora.head_loss(h, w, bad, workspace=ws)
     assert qlora.status_read(ws) == 8
     keep = torch.ones(T, dtype=torch.bool, device="cuda")
-    keep[7] = keep[60] = False
+    keep[7] = keep[60] = keep[8] = False
     for a, b in zip(got, want):
+        assert not a[8].any()
         assert a[7].isnan().all() and a[60].isnan().all()
         assert torch.equal(a[keep], b[keep])
     qlora.head_loss(h, w, y, workspace=ws)
@@ -266,11 +276,12 @@ def test_gradient_against_differences():
 
 
 @gpu
-def test_captured_call_replays_equal_eager():
+@pytest.mark.parametrize("T", [10, 300])
+def test_captured_call_replays_equal_eager(T):
     """Two captured calls share a workspace; replays after eager work equal the eager results."""
     torch = torch_mod()
-    T, D, V = 300, 256, 2000
-    announce("head loss under graph capture")
+    D, V = 256, 2000
+    announce(f"head loss under graph capture T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=17, std=0.2))
     ws = qlora.head_loss_workspace(T, V, D)
     out = [torch.empty(T, device="cuda"), torch.empty(T, device="cuda"),
@@ -305,10 +316,11 @@ def test_captured_call_replays_equal_eager():
 
 
 @gpu
-def test_two_streams_at_once_and_repeats_are_identical():
+@pytest.mark.parametrize("T", [9, 500])
+def test_two_streams_at_once_and_repeats_are_identical(T):
     torch = torch_mod()
-    T, D, V = 500, 512, 6000
-    announce("head loss on two streams")
+    D, V = 512, 6000
+    announce(f"head loss on two streams T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=18, std=0.1))
     want = qlora.head_loss(h, w, y)
     torch.cuda.synchronize()
