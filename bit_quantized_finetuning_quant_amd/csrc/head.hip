@@ -32,19 +32,14 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "tile.hpp"
 
 namespace qlora {
 
 namespace {
 
-constexpr int kTileV = 256;    // words (logits) or hidden columns (gradient) of a workgroup's tile
-constexpr int kTileT = 256;    // tokens of a workgroup's tile
-constexpr int kStatV = 128;    // words that share one exponent n per token
-constexpr int kStep = 64;      // contraction step
-constexpr int kThreads = 512;  // eight waves: 2 along the words or columns, 4 along the tokens
-constexpr int kUnit = 16384;   // bytes of half an operand tile of a step: 128 rows of 128 bytes
-constexpr int kStage = 4 * kUnit;
-constexpr int kFewTokens = 64;  // the few-token form, below
+constexpr int kStatV = 128;     // words that share one exponent n per token
+constexpr int kShiftV = 8192;   // words whose shift bytes a workgroup holds in LDS at a time
 constexpr int64_t kFewMaxWords = (int64_t)1 << 20;
 constexpr float kLog2eHi = 1.44269502162933349609375f;  // fl32(log2 e), and the rest of it
 constexpr float kLog2eLo = 1.92596299112661746887e-8f;
@@ -54,246 +49,6 @@ constexpr float kLn2Lo = -1.90465429995776804525e-9f;
 // their differences are exact in fp32 and l log2 e - n is formed to 2^-24 of l
 constexpr float kMaxExponent = 4194304.0f;
 constexpr float kNoExponent = -3.0e38f;  // n of a tile without any word
-
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(lds_void_t *)p; }
-
-// One 16-byte-per-lane copy from global memory to LDS bytes lds + 16 lane.  As asm, since the
-// compiler would otherwise make every later LDS read wait for all copies in flight; it has no
-// register result, and the callers wait for it by count.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma16(const char *sbase, uint32_t voff, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %0, %1"
-      :
-      : "v"(voff), "s"(sbase), "s"(lds)
-      : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-#define HEAD_WAIT_VM(n) asm volatile("s_waitcnt vmcnt(" #n ")" ::: "memory")
-#define HEAD_WAIT_LDS() asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory")
-
-__device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-}
-
-// A pointer that is the same in every lane, moved to scalar registers.
-__device__ __forceinline__ const char *uniform(const void *p) {
-  const uint64_t a = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-  return (const char *)(((uint64_t)hi << 32) | lo);
-}
-
-// LDS layout of an operand tile: rows of 128 bytes, eight 16-byte chunks each, chunk c of row r at
-// position c ^ swizzle(r).  The LDS serves 16-byte reads of 16 lanes at a time from 64 banks (two
-// rows), so row pairs shift the chunks; the transpose reads take 32-byte pieces of rows r..r+3 and
-// r + 8..r + 11 (or + 16), which then fall on different banks too.
-__device__ __forceinline__ int swizzle_rows(int r) { return (r >> 1) & 7; }
-__device__ __forceinline__ int swizzle_cols(int r) { return (((r >> 1) & 1) | ((((r >> 3) ^ (r >> 4)) & 1) << 1)) << 1; }
-
-// The product shared by both matrix kernels: acc[m][t] over a contraction of `steps` steps of 64.
-// Left operand: 256 rows of a row-major matrix whose contraction index is contiguous (kTrans =
-// false: words of W, contraction over d), or 256 columns of one whose rows are the contraction
-// (kTrans = true: columns d of W, contraction over the words).  Right operand: 256 rows (tokens).
-//
-// Two groups of four waves (one wave of each per SIMD) run half a phase apart: while one group
-// multiplies (16 MFMAs a wave), the other reads its next fragments from LDS and starts the copies
-// that refill it.  A step has four phases, (rows 0..63 of the wave's 128, contraction 0..31), (0..63,
-// 32..63), (64..127, 0..31), (64..127, 32..63); the tokens' fragments are read in the first two.  A
-// stage's tokens and first rows are free after phase 1, its other rows after phase 3, so each is
-// refilled for step k + 2 at once, five to six phases before it is read: two stages (128 KB) are
-// enough to hide the memory's latency.
-//
-// Every wave reads its LDS data completely (lgkmcnt(0)) before the barrier that ends a read phase, so
-// a refill started after that barrier cannot overtake a read; each wave waits for its own copies
-// (vmcnt, in order of issue) before the barrier after which any wave reads them.
-struct Operands {
-  const char *left;    // uniform: the tile's first row (kTrans: first column)
-  const char *right;   // uniform
-  uint32_t left_pitch; // kTrans: bytes between rows of the contraction
-  uint32_t left_off[4];   // per lane: copies of rows 0..63 (0, 1) and 64..127 (2, 3) of both row halves
-  uint32_t right_off[4];
-  int64_t left_step, right_step;  // bytes per contraction step
-  int left_rows;       // kTrans: rows of the contraction that exist (the last one stands for those beyond)
-};
-
-template <bool kTrans>
-__device__ __forceinline__ void copy_left(const Operands &o, int half, int k, int steps, char *stage, int wave,
-                                          int lane) {
-  const int kc = min(k, steps - 1);  // past the end: any valid rows, never read
-  const char *base = o.left + kc * o.left_step;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t off = o.left_off[2 * half + j];
-    if (kTrans) {
-      // row (2 wave + j) * 8 + lane / 8 of the unit: contraction row of a 64-row sub-tile
-      const int row = ((2 * wave + j) * 8 + (lane >> 3)) & 63;
-      off += (uint32_t)__mul24(min(row, o.left_rows - 1 - kc * kStep), (int)o.left_pitch);
-    }
-    dma16(base, off, lds_addr(stage + half * kUnit + (2 * wave + j) * 1024));
-  }
-}
-
-__device__ __forceinline__ void copy_right(const Operands &o, int k, int steps, char *stage, int wave) {
-  const int kc = min(k, steps - 1);
-  const char *base = o.right + kc * o.right_step;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) dma16(base, o.right_off[j], lds_addr(stage + 2 * kUnit + (4 * wave + j) * 1024));
-}
-
-template <bool kTrans>
-__device__ __forceinline__ void read_left(const char *stage, int half, int kk, int wm, int lane, u32x4 (&a)[4]) {
-  const char *unit = stage + half * kUnit + wm * 8192;
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    if (!kTrans) {
-      const int r = 16 * f + (lane & 15), c = 4 * kk + (lane >> 4);
-      a[f] = *(const u32x4 *)(unit + r * 128 + ((c ^ swizzle_rows(r)) << 4));
-    } else {
-      // lane s of a 16-lane group points at contraction row .. + s/4 and columns 4 (s%4); it
-      // receives four consecutive contraction rows of column s
-      const int s = lane & 15;
-      uint2 part[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 32 * kk + 8 * (lane >> 4) + 4 * h + (s >> 2);
-        const int c = 2 * f + ((s & 3) >> 1);
-        const char *p = unit + r * 128 + ((c ^ swizzle_cols(r)) << 4) + (s & 1) * 8;
-        part[h] = __builtin_bit_cast(
-            uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((v4s __attribute__((address_space(3))) *)(lds_void_t *)p));
-      }
-      a[f] = u32x4{part[0].x, part[0].y, part[1].x, part[1].y};
-    }
-  }
-}
-
-__device__ __forceinline__ void read_right(const char *stage, int kk, int wn, int lane, u32x4 (&b)[4]) {
-  const char *unit = stage + 2 * kUnit + wn * 8192;
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const int r = 16 * f + (lane & 15), c = 4 * kk + (lane >> 4);
-    b[f] = *(const u32x4 *)(unit + r * 128 + ((c ^ swizzle_rows(r)) << 4));
-  }
-}
-
-// Subtracts a power of two from the exponents of eight bf16 values >= 0 (0 where it falls below).
-__device__ __forceinline__ void scale_down(u32x4 &v, uint32_t shift) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t word = v[i];  // a value of its own: a bit cast of a vector's element takes element 0
-    const u16x2 less = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, word),
-                                                     __builtin_bit_cast(u16x2, shift));
-    v[i] = __builtin_bit_cast(uint32_t, less);
-  }
-}
-
-__device__ __forceinline__ void multiply(const u32x4 (&a)[4], const u32x4 (&b)[4], f32x4 (*acc)[4]) {
-  __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-      acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m]), as_bf16x8(b[n]), acc[m][n], 0, 0, 0);
-  __builtin_amdgcn_s_setprio(0);
-}
-
-// acc[m][n][q] of lane l: left row 128 wm + 16 m + 4 (l/16) + q, token 64 wn + 16 n + l%16.
-// shifts: the bytes N - n of the tile's tokens, [steps / 2][256] (kTrans only).
-template <bool kTrans>
-__device__ __forceinline__ void product(const Operands &o, int steps, char *lds, const uint8_t *shifts,
-                                        f32x4 (&acc)[8][4]) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = (wave >> 1) & 1, wn = (wave & 1) + 2 * (wave >> 2);
-  const bool late = wave >= 4;
-  copy_right(o, 0, steps, lds, wave);
-  copy_left<kTrans>(o, 0, 0, steps, lds, wave, lane);
-  copy_left<kTrans>(o, 1, 0, steps, lds, wave, lane);
-  copy_right(o, 1, steps, lds + kStage, wave);
-  copy_left<kTrans>(o, 0, 1, steps, lds + kStage, wave, lane);
-  HEAD_WAIT_VM(8);
-  barrier();
-  if (late) barrier();
-  u32x4 a[4], b0[4], b1[4];
-  uint32_t shift[4] = {0u, 0u, 0u, 0u};
-  for (int k = 0; k < steps; ++k) {
-    char *stage = lds + (k & 1) * kStage, *next = lds + ((k + 1) & 1) * kStage;
-    // phase 0
-    if (kTrans && (k & 1) == 0) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        shift[n] = (uint32_t)shifts[(k >> 1) * kTileT + 64 * wn + 16 * n + (lane & 15)] * 0x00800080u;
-    }
-    read_right(stage, 0, wn, lane, b0);
-    read_left<kTrans>(stage, 0, 0, wm, lane, a);
-    copy_left<kTrans>(o, 1, k + 1, steps, next, wave, lane);
-    HEAD_WAIT_LDS();
-    barrier();
-    if (kTrans) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) scale_down(b0[n], shift[n]);
-    }
-    multiply(a, b0, acc);
-    barrier();
-    // phase 1
-    read_right(stage, 1, wn, lane, b1);
-    read_left<kTrans>(stage, 0, 1, wm, lane, a);
-    HEAD_WAIT_LDS();
-    HEAD_WAIT_VM(8);
-    barrier();
-    if (kTrans) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) scale_down(b1[n], shift[n]);
-    }
-    multiply(a, b1, acc);
-    barrier();
-    // phase 2
-    read_left<kTrans>(stage, 1, 0, wm, lane, a);
-    copy_right(o, k + 2, steps, stage, wave);
-    HEAD_WAIT_LDS();
-    barrier();
-    multiply(a, b0, acc + 4);
-    barrier();
-    // phase 3
-    read_left<kTrans>(stage, 1, 1, wm, lane, a);
-    copy_left<kTrans>(o, 0, k + 2, steps, stage, wave, lane);
-    HEAD_WAIT_LDS();
-    HEAD_WAIT_VM(8);
-    barrier();
-    multiply(a, b1, acc + 4);
-    barrier();
-  }
-  if (!late) barrier();
-  HEAD_WAIT_VM(0);  // no copy may outlive the loop: the LDS is reused or given up
-  barrier();
-}
-
-// Tile of a workgroup.  Workgroup ids go round the eight XCDs, so id / 8 counts within one: each XCD
-// takes a contiguous run of tiles, ordered so that 32 neighbours (one per CU) cover 8 left tiles by 4
-// token tiles, whose operands its L2 then serves.
-struct Tile {
-  int64_t left, token;
-};
-__device__ __forceinline__ Tile tile_of(int64_t id, int64_t nleft, int64_t ntoken) {
-  const int64_t total = nleft * ntoken, per = total >> 3, rest = total & 7;
-  const int64_t x = id & 7, j = id >> 3;
-  const int64_t t = x * per + min(x, rest) + j;  // XCDs below `rest` take one tile more
-  const int64_t group = t / (8 * ntoken), first = group * 8;
-  const int64_t width = min((int64_t)8, nleft - first), in = t - first * ntoken;
-  return Tile{first + in % width, in / width};
-}
 
 // ---------------------------------------------------------------------------
 
@@ -352,15 +107,15 @@ __device__ __forceinline__ float relative_exp(float l, float n) {
 // [tile of 128 words][tpad].
 __global__ __launch_bounds__(kThreads, 2) void head_logits(
     const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, const int64_t *__restrict__ target, int64_t v0,
-    int64_t nv, int D, int64_t nleft, int64_t ntoken, const int *__restrict__ rows,
-    const uint32_t *__restrict__ state, uint16_t *__restrict__ e, int64_t pitch, float *__restrict__ exponent,
+    int64_t nv, int D, int nleft, const int *__restrict__ rows, const uint32_t *__restrict__ state, uint16_t *__restrict__ e, int64_t pitch, float *__restrict__ exponent,
     float *__restrict__ sum, int64_t tpad, float *__restrict__ target_logit) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
   const int live = (int)state[1];
-  const Tile tile = tile_of(blockIdx.x, nleft, ntoken);
-  const int t0 = (int)tile.token * kTileT;
-  if (t0 >= live) return;
-  const int64_t vt = tile.left * kTileV;  // within the piece
+  const int ntoken = (live + kTileT - 1) / kTileT;
+  if ((int)blockIdx.x >= nleft * ntoken) return;
+  const Tile tile = tile_at(place_of(blockIdx.x, nleft * ntoken), nleft, ntoken);
+  const int t0 = tile.token * kTileT;
+  const int64_t vt = (int64_t)tile.left * kTileV;  // within the piece
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = (wave >> 1) & 1, wn = (wave & 1) + 2 * (wave >> 2);
@@ -382,11 +137,8 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
     o.right_off[i] = (uint32_t)rows[min(t0 + rt, live - 1)] * row_bytes + (((lane & 7) ^ swizzle_rows(rt)) << 4);
   }
   f32x4 acc[8][4];
-#pragma unroll
-  for (int m = 0; m < 8; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  product<false>(o, D / kStep, lds, nullptr, acc);
+  tile_zero(acc);
+  product<false, false>(o, D / kStep, lds, nullptr, acc);
 
   // rows (words) of this lane: 128 wm + 16 m + 4 (lane / 16) + q
   const int vl = 128 * wm + 4 * (lane >> 4);
@@ -435,90 +187,106 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (lane < 16 && on) {
-      const int64_t at = (2 * tile.left + wm) * tpad + t;
+      const int64_t at = (int64_t)(2 * tile.left + wm) * tpad + t;
       exponent[at] = ex;
       sum[at] = s;
     }
   }
 }
 
-// Folds the piece's tiles into the running exponent N and sum S of each token: 16 tokens and 16
-// lanes along the tiles a workgroup.  shift: N - n of each tile, at most 255 (which leaves nothing
-// of any bf16 value); factor: 2^(N before - N), for what the pieces before have summed.
+// Folds the piece's tiles into the running exponent N and sum S of each token: 8 tokens and 32 lanes
+// along the tiles a workgroup, eight tiles of a lane in flight at once.  shift: N - n of each tile, at
+// most 255 (which leaves nothing of any bf16 value); factor: 2^(N before - N), for what the pieces
+// before have summed.
 __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ exponent, const float *__restrict__ sum,
                                                  int64_t tpad, int tiles, bool first,
                                                  const uint32_t *__restrict__ state, float *__restrict__ N,
                                                  float *__restrict__ S, uint8_t *__restrict__ shift,
                                                  float *__restrict__ factor) {
-  __shared__ float part[16][17];
+  constexpr int kLanes = 32, kDeep = 8;
+  __shared__ float part[kLanes][9];
   const int live = (int)state[1];
-  if ((int)blockIdx.x * 16 >= live) return;
-  const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int t = min((int)blockIdx.x * 16 + c, live - 1);
-  float top = kNoExponent;
-  for (int i = g; i < tiles; i += 16) top = fmaxf(top, exponent[i * tpad + t]);
+  if ((int)blockIdx.x * 8 >= live) return;
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int t = min((int)blockIdx.x * 8 + c, live - 1);
+  const float before = first ? kNoExponent : N[t], held = first ? 0.f : S[t];
+  float top = before;
+  float ex[kDeep], sm[kDeep];
+  for (int i0 = 0; i0 < tiles; i0 += kLanes * kDeep) {
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) {
+      const int i = i0 + j * kLanes + g;
+      ex[j] = i < tiles ? exponent[i * tpad + t] : kNoExponent;
+      sm[j] = i < tiles ? sum[i * tpad + t] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) top = fmaxf(top, ex[j]);
+  }
   part[g][c] = top;
   __syncthreads();
-  const float before = first ? kNoExponent : N[t];
-  float now = before;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) now = fmaxf(now, part[i][c]);
+  for (int i = 0; i < kLanes; ++i) top = fmaxf(top, part[i][c]);
   __syncthreads();
   float s = 0.f;
-  for (int i = g; i < tiles; i += 16) {
-    const float d = now - exponent[i * tpad + t];
-    s += sum[i * tpad + t] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
-    if (shift) shift[i * tpad + t] = (uint8_t)fminf(d, 255.f);
+  for (int i0 = 0; i0 < tiles; i0 += kLanes * kDeep) {
+    if (tiles > kLanes * kDeep) {  // more than the registers hold: read again
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j) {
+        const int i = i0 + j * kLanes + g;
+        ex[j] = i < tiles ? exponent[i * tpad + t] : kNoExponent;
+        sm[j] = i < tiles ? sum[i * tpad + t] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) {
+      const int i = i0 + j * kLanes + g;
+      const float d = top - ex[j];
+      s += sm[j] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
+      if (shift && i < tiles) shift[i * tpad + t] = (uint8_t)fminf(d, 255.f);
+    }
   }
   part[g][c] = s;
   __syncthreads();
-  if (g == 0 && (int)blockIdx.x * 16 + c < live) {
-    const float f = first ? 0.f : __builtin_amdgcn_exp2f(-fminf(now - before, 300.f));
-    float all = first ? 0.f : S[t] * f;
+  if (g == 0 && (int)blockIdx.x * 8 + c < live) {
+    const float f = first ? 0.f : __builtin_amdgcn_exp2f(-fminf(top - before, 300.f));
+    float all = held * f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) all += part[i][c];
-    N[t] = now;
+    for (int i = 0; i < kLanes; ++i) all += part[i][c];
+    N[t] = top;
     S[t] = all;
     factor[t] = f;
   }
 }
 
-// One tile (256 columns d, 256 tokens) of G over one split of the piece's words, see the top.
-// part: [split][tokens][D] fp32, in units of 2^N.
-__global__ __launch_bounds__(kThreads, 2) void head_grad(
-    const uint16_t *__restrict__ e, int64_t pitch, const uint16_t *__restrict__ w, int64_t nv, int D, int64_t nleft,
-    int64_t ntoken, int64_t split_words, const uint32_t *__restrict__ state, const uint8_t *__restrict__ shift,
-    int64_t tpad, const float *__restrict__ factor, bool first, float *__restrict__ part, int64_t part_stride) {
+// One tile (256 columns d, 256 tokens) of G over one range of the piece's words, see the top.  The tiles and their
+// splits follow from the tokens that carry a loss; `words` is the length of every piece but the last, so that the
+// ranges, and the tiles' places in part, are the same in all.  part: [split][tile][256 tokens][256 d] fp32, in units of
+// 2^N.
+__global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restrict__ e, int64_t pitch,
+                                                         const uint16_t *__restrict__ w, int nv, int words, int D,
+                                                         int nleft, const uint32_t *__restrict__ state,
+                                                         const uint8_t *__restrict__ shift, int64_t tpad,
+                                                         const float *__restrict__ factor, bool first,
+                                                         float *__restrict__ part) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t shifts[kHeadMaxSplit / kStatV * kTileT];
+  __shared__ __attribute__((aligned(16))) uint8_t shifts[kShiftV / kStatV * kTileT];
   const int live = (int)state[1];
-  const int64_t tiles = nleft * ntoken;
-  const int64_t split = blockIdx.x / tiles;
-  const Tile tile = tile_of(blockIdx.x % tiles, nleft, ntoken);
-  const int t0 = (int)tile.token * kTileT;
-  if (t0 >= live) return;
-  const int64_t vb = split * split_words;  // a multiple of 128
-  const int words = (int)max((int64_t)0, min(split_words, nv - vb));  // 0: only the sums before are rescaled
-  const int d0 = (int)tile.left * kTileV;
+  const int ntoken = (live + kTileT - 1) / kTileT, tiles = nleft * ntoken;
+  const Split split = choose_split(tiles, words);
+  if ((int)blockIdx.x >= tiles * split.count) return;
+  const int slot = place_of(blockIdx.x, tiles * split.count), nth = scalar(slot / tiles);
+  const Tile tile = tile_at(slot - nth * tiles, nleft, ntoken);
+  const int t0 = tile.token * kTileT, d0 = tile.left * kTileV;
+  const int first_word = scalar(nth * split.range);
+  const int last_word = scalar(min(min(first_word + split.range, words), nv));  // none: the sums before are rescaled
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = (wave >> 1) & 1, wn = (wave & 1) + 2 * (wave >> 2);
-  const int steps = (words + kStep - 1) / kStep;
 
-  {  // the tile's shift bytes (tpad is a multiple of 256, so whole words of four tokens)
-    const int n = (words + kStatV - 1) / kStatV * (kTileT / 4);
-    const uint8_t *src = shift + vb / kStatV * tpad + t0;
-    for (int i = threadIdx.x; i < n; i += kThreads)
-      ((uint32_t *)shifts)[i] = *(const uint32_t *)(src + (i >> 6) * tpad + 4 * (i & 63));
-    __syncthreads();
-  }
   Operands o;
-  o.left = uniform(w + vb * D + d0);
-  o.right = uniform(e + (int64_t)t0 * pitch + vb);
   o.left_pitch = (uint32_t)D * 2u;
   o.left_step = (int64_t)kStep * D * 2;
   o.right_step = 2 * kStep;
-  o.left_rows = words;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // unit row r: columns 128 (r / 64) + 64 (i / 2) .. + 63, contraction row r % 64
     const int r = (2 * wave + (i & 1)) * 8 + (lane >> 3);
@@ -528,23 +296,30 @@ __global__ __launch_bounds__(kThreads, 2) void head_grad(
     o.right_off[i] = (uint32_t)min(rt, live - 1 - t0) * (uint32_t)(2 * pitch) + (((lane & 7) ^ swizzle_rows(rt)) << 4);
   }
   f32x4 acc[8][4];
-#pragma unroll
-  for (int m = 0; m < 8; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (words > 0) product<true>(o, steps, lds, shifts, acc);
-
-  float *out = part + split * part_stride;
+  tile_zero(acc);
+  for (int vb = first_word; vb < last_word; vb += kShiftV) {
+    const int n = min(kShiftV, last_word - vb);
+    // the tile's shift bytes (tpad is a multiple of 256, so whole words of four tokens)
+    const uint8_t *src = shift + (int64_t)(vb / kStatV) * tpad + t0;
+    for (int i = threadIdx.x; i < (n + kStatV - 1) / kStatV * (kTileT / 4); i += kThreads)
+      ((uint32_t *)shifts)[i] = *(const uint32_t *)(src + (i >> 6) * tpad + 4 * (i & 63));
+    __syncthreads();
+    o.left = uniform(w + (int64_t)vb * D + d0);
+    o.right = uniform(e + (int64_t)t0 * pitch + vb);
+    o.left_rows = n;
+    product<true, true>(o, (n + kStep - 1) / kStep, lds, shifts, acc);
+  }
+  float *out = part + (int64_t)slot * (kTileT * kTileV);
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const int t = t0 + 64 * wn + 16 * n + (lane & 15);
-    if (t >= live) continue;
-    const float f = first ? 0.f : factor[t];
+    const int t = 64 * wn + 16 * n + (lane & 15);
+    if (t0 + t >= live) continue;
+    const float f = first ? 0.f : factor[t0 + t];
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
-      const int d = d0 + 128 * wm + 16 * m + 4 * (lane >> 4);
-      if (d >= D) continue;
-      f32x4 *p = (f32x4 *)(out + (int64_t)t * D + d);
+      const int d = 128 * wm + 16 * m + 4 * (lane >> 4);
+      if (d0 + d >= D) continue;
+      f32x4 *p = (f32x4 *)(out + t * kTileV + d);
       f32x4 v = acc[m][n];
       if (!first) {
         const f32x4 old = *p;
@@ -603,9 +378,11 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
                                                    const float *__restrict__ target_logit,
                                                    const int64_t *__restrict__ target,
                                                    const uint16_t *__restrict__ wy, bool by_token,
-                                                   const float *__restrict__ weight, float scale, const float *__restrict__ part, int splits,
-                                                   int64_t part_stride, int D, float *__restrict__ loss,
-                                                   float *__restrict__ lse, uint16_t *__restrict__ grad) {
+                                                   const float *__restrict__ weight, float scale,
+                                                   const float *__restrict__ part, int words, int nleft,
+                                                   const uint32_t *__restrict__ state, int D,
+                                                   float *__restrict__ loss, float *__restrict__ lse,
+                                                   uint16_t *__restrict__ grad) {
   const int t = blockIdx.x;
   const int j = place[t];
   uint16_t *g = grad + (int64_t)t * D;
@@ -626,11 +403,16 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
   const float c_t = weight ? scale * weight[t] : scale;
   const float a = c_t * r.inv, b = c_t * r.other;
   const uint16_t *wr = wy + (by_token ? (int64_t)t : target[t]) * D;  // the target's row of W
-  const float *p = part + (int64_t)j * D;
+  // the token's row in every split's tiles
+  const int ntoken = ((int)state[1] + kTileT - 1) / kTileT, tiles = nleft * ntoken;
+  const int splits = choose_split(tiles, words).count;
   for (int c = threadIdx.x * 8; c < D; c += 2048) {
+    const int64_t tile = place_at(Tile{c / kTileV, j / kTileT}, nleft, ntoken);
+    const float *p = part + tile * (kTileT * kTileV) + j % kTileT * kTileV + c % kTileV;
     f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
     for (int s = 0; s < splits; ++s) {
-      const f32x4 x = *(const f32x4 *)(p + s * part_stride + c), y = *(const f32x4 *)(p + s * part_stride + c + 4);
+      const f32x4 x = *(const f32x4 *)p, y = *(const f32x4 *)(p + 4);
+      p += (int64_t)tiles * (kTileT * kTileV);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         lo[q] += x[q];
@@ -669,126 +451,14 @@ __global__ __launch_bounds__(256) void head_target_rows(QWeight q, Codebook cb, 
 }
 
 // ---------------------------------------------------------------------------
-// Up to 64 tokens: both products are bound by streaming W once, so a
-// workgroup takes 64 words (or 64 columns d) and its four waves take every
-// fourth contraction step each, with no barrier until their sums are added:
-// a wave copies its own 64 x 64 tile of W (8 KB) and the tokens' piece of the
-// other operand into LDS, one or two steps ahead.  The tokens fill NT tiles
-// of 16.  Exponents n are per token and 64 words here, and the gradient's sums
-// of a chunk of words are relative to the chunk's own largest n, which
-// few_finish brings together: no pass over the tiles lies between the two.
+// Up to 64 tokens: both products are bound by streaming W once and run on the
+// per-wave streams, 64 words (or 64 columns d) a workgroup.  Exponents n are
+// per token and 64 words here, and the gradient's sums of a chunk of words are
+// relative to the chunk's own largest n, which few_finish brings together: no
+// pass over the tiles lies between the two.
 
-constexpr int kFewThreads = 256;
 constexpr int kFewWords = 64;       // words that share an exponent, and a step of the gradient
 constexpr int kFewChunk = 128;      // steps of a chunk at most: its shift bytes are held in LDS
-
-template <int NT>
-constexpr int few_stage() {
-  return 8192 + NT * 2048;
-}
-// Stages of a wave.  The logits of 16 tokens fit two workgroups of two stages on a CU; otherwise one
-// workgroup has the CU to itself and takes three where they fit.
-template <bool kTrans, int NT>
-constexpr int few_stages() {
-  return NT == 4 || (!kTrans && NT == 1) ? 2 : 3;
-}
-
-template <int n>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(n) : "memory");
-}
-
-// acc[m][n][q] of lane l: left row (word or column) 16 m + 4 (l/16) + q, token 16 n + l%16, summed over
-// the wave's steps first, first + 4, ..  mine: the wave's stages.  right_off: per lane, the rows of the
-// tokens.  left_rows: rows that exist, of the tile (words) or of the whole contraction (kTrans).
-template <bool kTrans, int NT>
-__device__ __forceinline__ void few_product(const char *left, uint32_t left_pitch, int left_rows, int64_t left_step,
-                                            const char *right, const uint32_t (&right_off)[2 * NT], int first,
-                                            int steps, char *mine, const uint8_t *shifts, f32x4 (&acc)[4][NT]) {
-  constexpr int kStages = few_stages<kTrans, NT>(), kBytes = few_stage<NT>(), kCopies = 8 + 2 * NT;
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (first >= steps) return;
-  auto copy = [&](int step, char *stage) {
-    const int s = min(step, steps - 1);  // past the end: never read
-    const char *lb = left + s * left_step, *rb = right + (int64_t)s * (2 * kStep);
-    const int rows = kTrans ? left_rows - s * kStep : left_rows;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = 8 * j + (lane >> 3);
-      const int sw = kTrans ? swizzle_cols(r) : swizzle_rows(r);
-      dma16(lb, (uint32_t)__mul24(min(r, rows - 1), (int)left_pitch) + (((lane & 7) ^ sw) << 4),
-            lds_addr(stage + 1024 * j));
-    }
-#pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) dma16(rb, right_off[j], lds_addr(stage + 8192 + 1024 * j));
-  };
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) copy(first + 4 * i, mine + i * kBytes);
-  char *stage = mine;
-  for (int s = first; s < steps; s += 4) {
-    wait_copies<(kStages - 1) * kCopies>();
-    u32x4 a[2][4], b[2][NT];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      read_left<kTrans>(stage, 0, kk, 0, lane, a[kk]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int r = 16 * n + (lane & 15), c = 4 * kk + (lane >> 4);
-        b[kk][n] = *(const u32x4 *)(stage + 8192 + r * 128 + ((c ^ swizzle_rows(r)) << 4));
-      }
-    }
-    uint32_t shift[NT];
-    if (kTrans) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) shift[n] = (uint32_t)shifts[s * (16 * NT) + 16 * n + (lane & 15)] * 0x00800080u;
-    }
-    HEAD_WAIT_LDS();
-    copy(s + 4 * kStages, stage);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (kTrans) scale_down(b[kk][n], shift[n]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[kk][m]), as_bf16x8(b[kk][n]), acc[m][n], 0,
-                                                             0, 0);
-      }
-    stage = stage == mine + (kStages - 1) * kBytes ? mine : stage + kBytes;
-  }
-  wait_copies<0>();
-}
-
-// The four waves' sums side by side in LDS: [wave][token][68], 64 left rows a token.
-constexpr int kFewPad = 68;
-template <int NT>
-__device__ __forceinline__ void few_put(const f32x4 (&acc)[4][NT], float *red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __syncthreads();  // every wave is done with its stages
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      *(f32x4 *)&red[((wave * NT + n) * 16 + (lane & 15)) * kFewPad + 16 * m + 4 * (lane >> 4)] = acc[m][n];
-  __syncthreads();
-}
-
-// The sum over the waves of four left rows of a token.
-template <int NT>
-__device__ __forceinline__ f32x4 few_sum(const float *red, int token, int row) {
-  f32x4 s = *(const f32x4 *)&red[token * kFewPad + row];
-#pragma unroll
-  for (int w = 1; w < 4; ++w) {
-    const f32x4 x = *(const f32x4 *)&red[(w * 16 * NT + token) * kFewPad + row];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) s[q] += x[q];
-  }
-  return s;
-}
 
 // e (nullptr: the loss alone) [T][pitch], exponent and sum [64 words][64 tokens]; v0: the piece's first word, which is
 // also the first column of e; group0: its first 64 words.
@@ -811,7 +481,8 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
     off[j] = (uint32_t)min(r, T - 1) * (uint32_t)(2 * D) + (((lane & 7) ^ swizzle_rows(r)) << 4);
   }
   f32x4 acc[4][NT];
-  few_product<false, NT>(uniform(w + vt * D), (uint32_t)D * 2u, words, 2 * kStep, uniform(h), off, wave, D / kStep,
+  few_zero<NT>(acc);
+  few_product<false, false, NT>(uniform(w + vt * D), (uint32_t)D * 2u, words, 2 * kStep, uniform(h), off, wave, D / kStep,
                          lds + wave * kBytes, nullptr, acc);
   float *red = (float *)lds;
   few_put<NT>(acc, red);
@@ -918,7 +589,8 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
     off[j] = (uint32_t)min(r, T - 1) * (uint32_t)(2 * pitch) + (((lane & 7) ^ swizzle_rows(r)) << 4);
   }
   f32x4 acc[4][NT];
-  few_product<true, NT>(uniform(w + vb * D + 64 * slice), (uint32_t)D * 2u, words, (int64_t)kStep * D * 2,
+  few_zero<NT>(acc);
+  few_product<true, true, NT>(uniform(w + vb * D + 64 * slice), (uint32_t)D * 2u, words, (int64_t)kStep * D * 2,
                         uniform(e + vb), off, wave, steps, lds + wave * kBytes, shifts, acc);
   float *red = (float *)lds;
   few_put<NT>(acc, red);
@@ -1029,9 +701,6 @@ __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ ta
                   pack_bf16x2(__builtin_fmaf(a, sum[2], -b * bf16_lo(wv.y)), __builtin_fmaf(a, sum[3], -b * bf16_hi(wv.y))));
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
-
 }  // namespace
 
 // The few-token form: e [T][V], the sums of every chunk of words.
@@ -1136,7 +805,9 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.few = T <= kFewTokens && V <= kFewMaxWords;
   p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
   p.tpad = cdiv(p.chunk, kTileT) * kTileT;
-  // Words of a piece: 64 MB of e (grad) and of decoded weight (packed); nothing else grows with it.
+  // Words of a piece: 128 MB of e (grad) and 64 MB of decoded weight (packed).  A larger piece leaves less of
+  // the products' last rounds of workgroups empty (2048 tokens, 40% of them masked, V = 32000: 5 tiles of
+  // tokens by 125 of words are three rounds of 256, two pieces of 63 and 62 four).
   int64_t vc = cdiv(V, kTileV) * kTileV;
   // The exponents and sums of its tiles stay within 64 MB too.
   const int64_t budget = (int64_t)32 << 20;
@@ -1145,22 +816,13 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
     return plan_few(p, vc);
   }
   vc = std::min(vc, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
-  if (grad) vc = std::min(vc, std::max<int64_t>(budget / p.tpad / kTileV * kTileV, 8 * kTileV));
+  if (grad) vc = std::min(vc, std::max<int64_t>(2 * budget / p.tpad / kTileV * kTileV, 8 * kTileV));
   if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
   p.pieces = cdiv(V, vc);
   p.words = cdiv(cdiv(V, p.pieces), kTileV) * kTileV;
   p.pieces = cdiv(V, p.words);
-  // Splits of the gradient's contraction: one round of 256 workgroups at least, ranges of whole
-  // tiles of 128 words, 512 of them at least, and a range's shift bytes have to fit the LDS.
-  p.splits = 1;
-  if (grad) {
-    const int64_t tiles = cdiv(D, kTileV) * cdiv(p.chunk, kTileT);
-    p.splits = std::max(cdiv(p.words, kHeadMaxSplit), std::min(cdiv(256, tiles), std::max<int64_t>(p.words / 512, 1)));
-    p.split_words = cdiv(cdiv(p.words, p.splits), kStatV) * kStatV;
-    p.splits = cdiv(p.words, p.split_words);
-  } else {
-    p.split_words = 0;
-  }
+  p.split_words = 0;
+  p.splits = grad ? split_slots((int)cdiv(D, kTileV), (int)cdiv(p.chunk, kTileT), (int)p.words) : 0;
   const int64_t stat = p.words / kStatV * p.tpad;
   size_t off = 256;
   auto take = [&off](size_t bytes) {
@@ -1178,7 +840,7 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.off_sum = take((size_t)stat * 4);
   p.off_shift = grad ? take((size_t)stat) : 0;
   p.off_e = grad ? take((size_t)p.chunk * p.words * 2) : 0;
-  p.off_part = grad ? take((size_t)p.splits * p.chunk * D * 4) : 0;
+  p.off_part = grad ? take((size_t)p.splits * kTileT * kTileV * 4) : 0;
   p.off_w = packed ? take((size_t)p.words * D * 2) : 0;
   p.off_wy = packed && grad ? take((size_t)p.chunk * D * 2) : 0;
   p.total = off;
@@ -1202,26 +864,24 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
   const int D = (int)p.D;
   for (int64_t c0 = 0; c0 < p.T; c0 += p.chunk) {
     const int T = (int)std::min(p.chunk, p.T - c0);
-    const int64_t ntoken = cdiv(T, kTileT), stride = p.chunk * p.D;
+    const int ntoken = (int)cdiv(T, kTileT), nd = (int)cdiv(p.D, kTileV), words = (int)p.words;
     const uint16_t *hc = h + c0 * p.D;
     const int64_t *yc = target + c0;
     head_scan<<<1, 1024, 0, st>>>(yc, T, p.V, c0 == 0, rows, place, state);
     for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
-      const int64_t nv = std::min(p.words, p.V - v0), nleft = cdiv(nv, kTileV);
+      const int nv = (int)std::min(p.words, p.V - v0), nleft = (int)cdiv(nv, kTileV);
       const uint16_t *piece = w ? w + v0 * p.D : wp;
       if (q) {
         const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
         if (err != hipSuccess) return err;
       }
-      head_logits<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(hc, piece, yc, v0, nv, D, nleft, ntoken, rows,
-                                                                 state, e, p.words, exponent, sum, p.tpad, logit);
-      head_fold<<<(unsigned)cdiv(T, 16), 256, 0, st>>>(exponent, sum, p.tpad, (int)cdiv(nv, kStatV), v0 == 0, state, N,
+      head_logits<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(hc, piece, yc, v0, nv, D, nleft, rows, state,
+                                                                 e, p.words, exponent, sum, p.tpad, logit);
+      head_fold<<<(unsigned)cdiv(T, 8), 256, 0, st>>>(exponent, sum, p.tpad, (int)cdiv(nv, kStatV), v0 == 0, state, N,
                                                       S, shift, factor);
       if (!p.grad) continue;
-      const int64_t nd = cdiv(p.D, kTileV);
-      head_grad<<<(unsigned)(nd * ntoken * p.splits), kThreads, 0, st>>>(e, p.words, piece, nv, D, nd, ntoken,
-                                                                      p.split_words, state, shift, p.tpad, factor,
-                                                                      v0 == 0, part, stride);
+      head_grad<<<(unsigned)split_slots(nd, ntoken, words), kThreads, 0, st>>>(
+          e, p.words, piece, nv, words, D, nd, state, shift, p.tpad, factor, v0 == 0, part);
     }
     if (!p.grad) {
       head_losses<<<(unsigned)cdiv(T, 256), 256, 0, st>>>(T, place, N, S, logit, loss + c0, lse ? lse + c0 : nullptr);
@@ -1229,8 +889,8 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
     }
     if (q) head_target_rows<<<(unsigned)T, 256, 0, st>>>(*q, cb, yc, wy);
     head_finish<<<(unsigned)T, 256, 0, st>>>(place, N, S, logit, yc, q ? wy : w, q != nullptr,
-                                             weight ? weight + c0 : nullptr, scale, part, (int)p.splits, stride, D,
-                                             loss + c0, lse ? lse + c0 : nullptr, grad + c0 * p.D);
+                                             weight ? weight + c0 : nullptr, scale, part, words, nd, state, D, loss + c0,
+                                             lse ? lse + c0 : nullptr, grad + c0 * p.D);
   }
   return hipGetLastError();
 }

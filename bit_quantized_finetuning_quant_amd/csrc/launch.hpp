@@ -258,10 +258,10 @@ hipError_t launch_linear_set_bwd_act8(const Act8BwdPlan &p, const uint16_t *cons
 // pieces are decoded into the workspace).
 constexpr int64_t kHeadMaxTokens = 16384;  // tokens of a chunk
 constexpr int64_t kHeadMaxDim = 65536;     // D: a chunk's byte offsets stay below 2^32
-constexpr int64_t kHeadMaxSplit = 8192;    // words of one split of the gradient's contraction
 struct HeadPlan {
   int64_t T, V, D;
-  bool grad, packed, few;  // few: the few-token form (splits: chunks of words in all, split_words: of each)
+  bool grad, packed, few;  // few: the few-token form (splits: chunks of words in all, split_words: of
+  // each); otherwise splits: the gradient's partial tiles
   int64_t chunk, tpad, words, pieces, splits, split_words;
   size_t off_rows, off_place, off_logit, off_n, off_s, off_factor, off_exponent, off_sum, off_shift, off_e, off_part,
       off_w, off_wy, total;
