@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqlora_gfx950.so")
 SOURCES = ["codec.hip", "qgemm.hip", "lora.hip", "gemv.hip", "linear.hip", "optim.hip", "dropout.hip",
-           "act8.hip", "head.hip", "api.hip", "api_train.hip"]
+           "act8.hip", "ragged.hip", "head.hip", "api.hip", "api_train.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

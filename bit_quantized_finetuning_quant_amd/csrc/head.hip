@@ -810,13 +810,13 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   // tokens by 125 of words are three rounds of 256, two pieces of 63 and 62 four).
   int64_t vc = cdiv(V, kTileV) * kTileV;
   // The exponents and sums of its tiles stay within 64 MB too.
-  const int64_t budget = (int64_t)32 << 20;
+  const int64_t budget = (int64_t)64 << 20;
   if (p.few) {  // one piece, but for the decoded rows of a packed head
     if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
     return plan_few(p, vc);
   }
   vc = std::min(vc, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
-  if (grad) vc = std::min(vc, std::max<int64_t>(2 * budget / p.tpad / kTileV * kTileV, 8 * kTileV));
+  if (grad) vc = std::min(vc, std::max<int64_t>(budget / p.tpad / kTileV * kTileV, 8 * kTileV));
   if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
   p.pieces = cdiv(V, vc);
   p.words = cdiv(cdiv(V, p.pieces), kTileV) * kTileV;

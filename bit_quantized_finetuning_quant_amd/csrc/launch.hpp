@@ -238,12 +238,25 @@ hipError_t launch_lora_set_grads_act8(const uint16_t *v, const int8_t *codes, co
                                       int64_t T, int64_t K, int r, float scale, float *grad_A_set,
                                       float *const *grad_B, float *part, hipStream_t st);
 
-// Backward of a projection set (or one linear) from the checkpoint of its input (linear.hip).
+// grad_x of sizes that are not whole tiles of the fused GEMM (ragged.hip): v [T x count r], byte offsets
+// into ws.
+bool ragged_dx_applies(int64_t T, int count, const int64_t *N, int64_t K, int r);
+struct RaggedPlan {
+  size_t off_dy, off_w, off_part, total;
+};
+RaggedPlan plan_ragged_dx(int64_t T, int count, const int64_t *N, int64_t K, int r);
+hipError_t launch_ragged_dx(const RaggedPlan &p, int64_t T, int count, const int64_t *N, int64_t K, int r,
+                            const uint16_t *const *dy, const QWeight *w, const uint16_t *v, const uint16_t *A_set,
+                            float scale, uint16_t *out, char *ws, const Codebook &cb, hipStream_t st);
+
+// Backward of a projection set (or one linear) from the checkpoint of its input (act8.hip).
 struct Act8BwdPlan {
   int64_t T, K;
   int r, count;
   int64_t N[kMaxSetMembers];
-  size_t off_v, off_part, off_qpart, total;  // off_qpart: 0 when grad_x does not split
+  bool ragged;  // grad_x by launch_ragged_dx
+  RaggedPlan rg;
+  size_t off_v, off_part, off_qpart, off_rg, total;  // off_qpart: 0 when grad_x does not split
 };
 Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t K, int r);
 hipError_t launch_linear_set_bwd_act8(const Act8BwdPlan &p, const uint16_t *const *dy, const int8_t *codes,

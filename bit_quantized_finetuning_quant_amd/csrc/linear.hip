@@ -375,62 +375,4 @@ hipError_t launch_linear_set_bwd(const SetPlan &p, const uint16_t *const *dy, co
   return launch_lora_set_grads(v, x, dy, u, p.N, p.count, p.T, p.K, p.r, scale, grad_A_set, grad_B, part, st);
 }
 
-// ---------------------------------------------------------------------------
-// Backward from an 8-bit checkpoint of the input.  Any token count runs on the
-// fused GEMM and the adapter products (a checkpoint of a few tokens saves
-// nothing, so there is no few-token form).
-
-Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t K, int r) {
-  Act8BwdPlan p;
-  p.T = T;
-  p.K = K;
-  p.r = r;
-  p.count = count;
-  bool same_n = true;
-  for (int i = 0; i < kMaxSetMembers; ++i) {
-    p.N[i] = i < count ? N[i] : 0;
-    same_n = same_n && (i >= count || N[i] == N[0]);
-  }
-  size_t off = 256;
-  p.off_v = off;
-  off += align256((size_t)3 * T * count * r * 2);
-  p.off_part = off;
-  off += align256(lora_set_part_floats(T, count, N, K, r) * 4);
-  size_t qsplit = same_n ? qgemm_split_floats(T, K, N[0]) : 0;
-  if (count > 1) qsplit = std::max(qsplit, qgemm_set_dx_member_floats(T, count, N, K));
-  p.off_qpart = qsplit ? off : 0;
-  off += align256(qsplit * 4);
-  p.total = off;
-  return p;
-}
-
-hipError_t launch_linear_set_bwd_act8(const Act8BwdPlan &p, const uint16_t *const *dy, const int8_t *codes,
-                                      const float *code_scale, const QWeight *w, const uint16_t *A_set,
-                                      const uint16_t *const *B, float scale, const uint16_t *u, uint16_t *grad_x,
-                                      float *grad_A_set, float *const *grad_B, char *ws, const Codebook &cb,
-                                      hipStream_t st) {
-  float *part = (float *)(ws + p.off_part);
-  uint16_t *v = (uint16_t *)(ws + p.off_v);
-  const int64_t rt = (int64_t)p.count * p.r;
-  hipError_t e = launch_lora_set_v_exact(dy, B, p.N, p.count, p.T, p.r, v, part, st);
-  if (e != hipSuccess) return e;
-  if (grad_x) {
-    QgemmSet s{};
-    s.count = p.count;
-    s.ld_la = rt;
-    for (int i = 0; i < p.count; ++i) {
-      s.m[i].w = w[i];
-      s.m[i].act = dy[i];
-    }
-    TimedLaunch tl;
-    const bool timed = timing_begin(st, tl, kTimedQgemmDx);
-    e = launch_qgemm_set(true, s, p.T, nullptr, v, A_set, (int)rt, scale, grad_x, cb, st, nullptr,
-                         p.off_qpart ? (float *)(ws + p.off_qpart) : nullptr);
-    if (timed) timing_end(st, tl);
-    if (e != hipSuccess) return e;
-  }
-  return launch_lora_set_grads_act8(v, codes, code_scale, dy, u, p.N, p.count, p.T, p.K, p.r, scale, grad_A_set,
-                                    grad_B, part, st);
-}
-
 }  // namespace qlora

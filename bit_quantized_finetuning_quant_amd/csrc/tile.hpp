@@ -186,53 +186,44 @@ __device__ __forceinline__ void product(const Operands &o, int steps, char *lds,
   TILE_WAIT_VM(8);
   barrier();
   if (late) barrier();
-  u32x4 a[4], b0[4], b1[4];
-  uint32_t shift[4] = {0u, 0u, 0u, 0u};
+  u32x4 a0[4], a1[4], b0[4], b1[4];
   for (int k = 0; k < steps; ++k) {
     char *stage = lds + (k & 1) * kStage, *next = lds + ((k + 1) & 1) * kStage;
-    // phase 0
-    if (kScale && (k & 1) == 0) {
+    // phase 0: rows 0..63
+    uint32_t shift[4];
+    if (kScale) {
 #pragma unroll
       for (int n = 0; n < 4; ++n)
         shift[n] = (uint32_t)shifts[(k >> 1) * kTileT + 64 * wn + 16 * n + (lane & 15)] * 0x00800080u;
     }
     read_right(stage, 0, wn, lane, b0);
-    read_left<kTrans>(stage, 0, 0, wm, lane, a);
+    read_left<kTrans>(stage, 0, 0, wm, lane, a0);
+    read_right(stage, 1, wn, lane, b1);
+    read_left<kTrans>(stage, 0, 1, wm, lane, a1);
     copy_left<kTrans>(o, 1, k + 1, steps, next, wave, lane);
-    TILE_WAIT_LDS();
-    barrier();
     if (kScale) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) scale_down(b0[n], shift[n]);
+      for (int n = 0; n < 4; ++n) {
+        scale_down(b0[n], shift[n]);
+        scale_down(b1[n], shift[n]);
+      }
     }
-    multiply(a, b0, acc);
-    barrier();
-    // phase 1
-    read_right(stage, 1, wn, lane, b1);
-    read_left<kTrans>(stage, 0, 1, wm, lane, a);
     TILE_WAIT_LDS();
     TILE_WAIT_VM(8);
     barrier();
-    if (kScale) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) scale_down(b1[n], shift[n]);
-    }
-    multiply(a, b1, acc);
+    multiply(a0, b0, acc);
+    multiply(a1, b1, acc);
     barrier();
-    // phase 2
-    read_left<kTrans>(stage, 1, 0, wm, lane, a);
+    // phase 1: rows 64..127
+    read_left<kTrans>(stage, 1, 0, wm, lane, a0);
+    read_left<kTrans>(stage, 1, 1, wm, lane, a1);
     copy_right(o, k + 2, steps, stage, wave);
-    TILE_WAIT_LDS();
-    barrier();
-    multiply(a, b0, acc + 4);
-    barrier();
-    // phase 3
-    read_left<kTrans>(stage, 1, 1, wm, lane, a);
     copy_left<kTrans>(o, 0, k + 2, steps, stage, wave, lane);
     TILE_WAIT_LDS();
     TILE_WAIT_VM(8);
     barrier();
-    multiply(a, b1, acc + 4);
+    multiply(a0, b0, acc + 4);
+    multiply(a1, b1, acc + 4);
     barrier();
   }
   if (!late) barrier();

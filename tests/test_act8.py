@@ -8,6 +8,7 @@ in 64 bits on x_hat.  Tolerances of one output value, with S the sum of the abso
   grad_B  an fp32 sum of exact products: (T + 4) 2^-24 scale |dy|^T |u|
   grad_x  v in bf16 (2^-8), fp32 sums, the result in bf16:
           (2^-8 + (N + r) 2^-24) scale |v|' |A| + N 2^-24 |dy| |W| + 2^-8 |grad_x|
+          (both forms of the product: the ragged one adds the same terms in another order)
 (bf16 has 8 significant bits, so a rounding moves a value by up to 2^-8 of it; the fp32 factor scale
 adds 2^-24, within the + 4 and + 8.)
 """
@@ -177,7 +178,12 @@ def _check(T, Ns, K, r, seed, scale=0.25, double_quant=True):
 @pytest.mark.parametrize("double_quant", [True, False])
 @pytest.mark.parametrize("T,N,K,r", [(1, 64, 64, 1), (1, 512, 320, 16), (2, 100, 128, 8), (3, 512, 256, 7),
                                      (63, 257, 192, 100), (64, 128, 64, 64), (65, 384, 320, 256), (128, 256, 512, 65),
-                                     (300, 1000, 448, 16), (513, 256, 1088, 32), (1025, 640, 576, 8)])
+                                     (300, 1000, 448, 16), (513, 256, 1088, 32), (1025, 640, 576, 8),
+                                     # sizes off the fused GEMM's grid: few tokens on each tile count, one and
+                                     # several chunks, one and several splits, a tile of 64 columns
+                                     (16, 77, 64, 3), (17, 4001, 128, 16), (50, 4744, 640, 16), (64, 1, 192, 1),
+                                     (33, 130, 4032, 200), (66, 3, 64, 2), (257, 837, 1152, 33), (2050, 103, 3776, 128),
+                                     (700, 5003, 320, 64)])
 def test_backward_of_one_linear(T, N, K, r, double_quant):
     announce(f"act8 backward T={T} N={N} K={K} r={r} double_quant={double_quant}")
     _check(T, [N], K, r, seed=T + N, double_quant=double_quant)
