@@ -386,14 +386,50 @@ __device__ __forceinline__ void act8_tile(const LoraProblem &pr, int64_t tile, i
   put_tile<false>(pr, tile, s, acc);
 }
 
-// grad_A from the checkpoint (workgroups below `first`) and one grad_B (the rest) in one launch.
-__global__ __launch_bounds__(256) void lora_gemm_act8(LoraProblem a, LoraProblem b, int64_t first) {
+// The products of one step of that backward pass, all in one launch (a launch costs about 4 us of the
+// host and of the GPU, as much as one of these products): problem i takes workgroups first[i] ..
+// first[i + 1] - 1.
+constexpr int kMaxBatch = kMaxSetMembers + 1;
+struct LoraBatch {
+  LoraProblem pr[kMaxBatch];
+  int64_t first[kMaxBatch + 1];
+  int count;
+};
+
+__device__ __forceinline__ int batch_index(const LoraBatch &b, int64_t id) {
+  int i = 0;
+  while (i + 1 < b.count && id >= b.first[i + 1]) ++i;
+  return i;
+}
+
+// v of every member
+__global__ __launch_bounds__(256) void lora_batch_v(LoraBatch b) {
   __shared__ __attribute__((aligned(16))) uint16_t s[8][LT * LLD];
-  const int64_t id = blockIdx.x;
-  if (id < first)
-    act8_tile(a, id / a.S, (int)(id % a.S), s);
+  const int i = batch_index(b, blockIdx.x);
+  const int64_t j = (int64_t)blockIdx.x - b.first[i];
+  lora_tile<false, true, true, 4>(b.pr[i], j / b.pr[i].S, (int)(j % b.pr[i].S), s, s + 4);
+}
+
+// grad_A from the checkpoint (problem 0) and the members' grad_B
+__global__ __launch_bounds__(256) void lora_batch_grads(LoraBatch b) {
+  __shared__ __attribute__((aligned(16))) uint16_t s[8][LT * LLD];
+  const int i = batch_index(b, blockIdx.x);
+  const int64_t j = (int64_t)blockIdx.x - b.first[i];
+  if (i == 0)
+    act8_tile(b.pr[0], j / b.pr[0].S, (int)(j % b.pr[0].S), s);
   else
-    lora_tile<true, true, false, 4>(b, (id - first) / b.S, (int)((id - first) % b.S), s, s + 4);
+    lora_tile<true, true, false, 4>(b.pr[i], j / b.pr[i].S, (int)(j % b.pr[i].S), s, s + 4);
+}
+
+// first counts quads here
+template <bool kBf16Out>
+__global__ __launch_bounds__(256) void lora_batch_reduce(LoraBatch b) {
+  const int64_t quads = b.first[b.count];
+  for (int64_t qd = (int64_t)blockIdx.x * 256 + threadIdx.x; qd < quads; qd += (int64_t)gridDim.x * 256) {
+    int i = 0;
+    while (i + 1 < b.count && qd >= b.first[i + 1]) ++i;
+    reduce_quad<kBf16Out>(b.pr[i], qd - b.first[i]);
+  }
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -557,6 +593,24 @@ hipError_t launch_lora_set_grads(const uint16_t *v_set, const uint16_t *x, const
   return launch_list<true, true, false>(pr, count + 1, st);
 }
 
+static LoraBatch make_batch(const LoraProblem *pr, int count, int64_t (*size)(const LoraProblem &)) {
+  LoraBatch b{};
+  b.count = count;
+  for (int i = 0; i < count; ++i) {
+    b.pr[i] = pr[i];
+    b.first[i + 1] = b.first[i] + size(pr[i]);
+  }
+  return b;
+}
+
+template <bool kBf16Out>
+static hipError_t reduce_batch(const LoraProblem *pr, int count, hipStream_t st) {
+  const LoraBatch b = make_batch(pr, count, problem_quads);
+  if (b.first[count] > 0)
+    lora_batch_reduce<kBf16Out><<<(unsigned)std::min<int64_t>(cdiv(b.first[count], 256), 2048), 256, 0, st>>>(b);
+  return hipGetLastError();
+}
+
 // v_set with what its rounding leaves: v [3][T x count r].
 hipError_t launch_lora_set_v_exact(const uint16_t *const *dy, const uint16_t *const *B, const int64_t *N, int count,
                                    int64_t T, int r, uint16_t *v, float *part, hipStream_t st) {
@@ -570,32 +624,31 @@ hipError_t launch_lora_set_v_exact(const uint16_t *const *dy, const uint16_t *co
     pr[i].out_low = v + 2 * plane + (int64_t)i * r;
     off += lora_part_floats(T, r, N[i]);
   }
-  return launch_list<false, true, true>(pr, count, st);
+  LoraBatch b = make_batch(pr, count, problem_blocks);
+  lora_batch_v<<<(unsigned)b.first[count], 256, 0, st>>>(b);
+  return reduce_batch<true>(pr, count, st);
 }
 
-// grad_A_set and the first grad_B in one launch, the other grad_B two a launch.
+// grad_A_set and every grad_B in one launch.
 hipError_t launch_lora_set_grads_act8(const uint16_t *v, const int8_t *codes, const float *code_scale,
                                       const uint16_t *const *dy, const uint16_t *u_set,
                                       const int64_t *N, int count, int64_t T, int64_t K, int r, float scale,
                                       float *grad_A_set, float *const *grad_B, float *part, hipStream_t st) {
-  LoraProblem pr[kMaxSetMembers];
+  LoraProblem pr[kMaxBatch];
   const int64_t rt = (int64_t)count * r;
-  LoraProblem a = make_problem(v, rt, (const uint16_t *)codes, K, rt, K, T, scale, grad_A_set, part);
+  LoraProblem &a = pr[0];
+  a = make_problem(v, rt, (const uint16_t *)codes, K, rt, K, T, scale, grad_A_set, part);
   a.P_mid = v + T * rt;
   a.P_low = v + 2 * T * rt;
   a.code_scale = code_scale;
   size_t off = lora_part_floats(rt, K, T);
   for (int i = 0; i < count; ++i) {
-    pr[i] = make_problem(dy[i], N[i], u_set + (int64_t)i * r, rt, N[i], r, T, scale, grad_B[i], part + off);
+    pr[i + 1] = make_problem(dy[i], N[i], u_set + (int64_t)i * r, rt, N[i], r, T, scale, grad_B[i], part + off);
     off += lora_part_floats(N[i], r, T);
   }
-  const int64_t wa = problem_blocks(a), wb = problem_blocks(pr[0]);
-  lora_gemm_act8<<<(unsigned)(wa + wb), 256, 0, st>>>(a, pr[0], wa);
-  const int64_t qa = problem_quads(a), qb = problem_quads(pr[0]);
-  if (qa + qb > 0)
-    lora_reduce<false><<<(unsigned)std::min<int64_t>(cdiv(qa + qb, 256), 2048), 256, 0, st>>>(a, pr[0], qa, qa + qb);
-  const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_list<true, true, false>(pr + 1, count - 1, st);
+  LoraBatch b = make_batch(pr, count + 1, problem_blocks);
+  lora_batch_grads<<<(unsigned)b.first[count + 1], 256, 0, st>>>(b);
+  return reduce_batch<false>(pr, count + 1, st);
 }
 
 }  // namespace qlora
