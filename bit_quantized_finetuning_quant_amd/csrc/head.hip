@@ -52,16 +52,26 @@ constexpr float kNoExponent = -3.0e38f;  // n of a tile without any word
 
 // ---------------------------------------------------------------------------
 
+// loss and lse of a token that carries none: 0, or NaN for a target past the vocabulary.
+__device__ __forceinline__ void no_loss(int64_t y, int64_t t, float *loss, float *lse) {
+  const float v = y < 0 ? 0.f : NAN;
+  loss[t] = v;
+  if (lse) lse[t] = v;
+}
+
 // Lists the tokens of a chunk that carry a loss: rows[j] = token, place[token] = j, or -1 (ignored)
-// or -2 (target out of range).  One workgroup; state[0] |= 2 on a bad target, state[1] = the count.
+// or -2 (target out of range); these get their loss here.  One workgroup; state[0] |= 2 on a bad
+// target, state[1] = the count.
 __global__ __launch_bounds__(1024) void head_scan(const int64_t *__restrict__ target, int T, int64_t V, bool first,
                                                   int *__restrict__ rows, int *__restrict__ place,
-                                                  uint32_t *__restrict__ state) {
+                                                  uint32_t *__restrict__ state, float *__restrict__ loss,
+                                                  float *__restrict__ lse) {
   __shared__ int wave_sum[16];
-  __shared__ int total;
+  __shared__ int any;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  bool bad = false;
+  if (tid == 0) any = 0;
   int base = 0;
+  bool bad = false;
   for (int t0 = 0; t0 < T; t0 += 1024) {
     const int t = t0 + tid;
     const int64_t y = t < T ? target[t] : -1;
@@ -78,20 +88,52 @@ __global__ __launch_bounds__(1024) void head_scan(const int64_t *__restrict__ ta
     const int j = before + __popcll(mask & ((1ull << lane) - 1));
     if (t < T) {
       if (live) rows[j] = t;
+      else no_loss(y, t, loss, lse);
       place[t] = live ? j : (y >= V ? -2 : -1);
     }
     base += all;
     __syncthreads();
   }
-  if (tid == 0) total = 0;
-  __syncthreads();
-  if (bad) total = 1;
+  if (bad) any = 1;
   __syncthreads();
   if (tid == 0) {
-    const uint32_t before = first ? 0u : state[0];
-    state[0] = before | (total ? 2u : 0u);
+    state[0] = (first ? 0u : state[0]) | (any ? 2u : 0u);
     state[1] = (uint32_t)base;
   }
+}
+
+// The same for at most 512 tokens by every workgroup of head_logits (512 threads), which spares the
+// launch: returns the count; this thread's token becomes entry j of the list, or j = -1.  The first
+// workgroup writes what the later kernels read.
+__device__ __forceinline__ int list_tokens(const int64_t *target, int T, int64_t V, int *wave_sum, int &j, int *rows,
+                                           int *place, uint32_t *state, float *loss, float *lse) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int64_t y = t < T ? target[t] : -1;
+  const bool live = y >= 0 && y < V;
+  const uint64_t mask = __ballot(live), bad = __ballot(y >= V);
+  if (lane == 0) wave_sum[wave] = __popcll(mask) | (bad ? 1 << 16 : 0);
+  __syncthreads();
+  int before = 0, all = 0, any = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const int n = wave_sum[w] & 0xFFFF;
+    before += w < wave ? n : 0;
+    all += n;
+    any |= wave_sum[w] >> 16;
+  }
+  j = live ? before + __popcll(mask & ((1ull << lane) - 1)) : -1;
+  if (blockIdx.x == 0) {
+    if (t < T) {
+      if (live) rows[j] = t;
+      else no_loss(y, t, loss, lse);
+      place[t] = live ? j : (y >= V ? -2 : -1);
+    }
+    if (t == 0) {
+      state[0] = any ? 2u : 0u;
+      state[1] = (uint32_t)all;
+    }
+  }
+  return all;
 }
 
 // n of a tile from its largest logit.  Finite whatever the logits are: NaN and infinite sums show in s.
@@ -105,16 +147,30 @@ __device__ __forceinline__ float relative_exp(float l, float n) {
 
 // One tile of the logits, see the top.  e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
 // [tile of 128 words][tpad].
+// kList: at most 512 tokens, listed here; otherwise head_scan has.
+template <bool kList>
 __global__ __launch_bounds__(kThreads, 2) void head_logits(
-    const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, const int64_t *__restrict__ target, int64_t v0,
-    int64_t nv, int D, int nleft, const int *__restrict__ rows, const uint32_t *__restrict__ state, uint16_t *__restrict__ e, int64_t pitch, float *__restrict__ exponent,
+    const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, const int64_t *__restrict__ target, int T, int64_t V,
+    int64_t v0, int64_t nv, int D, int nleft, int *__restrict__ rows, int *__restrict__ place,
+    uint32_t *__restrict__ state, float *__restrict__ loss, float *__restrict__ lse, uint16_t *__restrict__ e, int64_t pitch, float *__restrict__ exponent,
     float *__restrict__ sum, int64_t tpad, float *__restrict__ target_logit) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-  const int live = (int)state[1];
+  __shared__ int list[kList ? kTileT : 1];
+  int entry = -1;
+  int live;
+  if (kList)
+    live = scalar(list_tokens(target, T, V, (int *)lds, entry, rows, place, state, loss, lse));
+  else
+    live = (int)state[1];
   const int ntoken = (live + kTileT - 1) / kTileT;
   if ((int)blockIdx.x >= nleft * ntoken) return;
   const Tile tile = tile_at(place_of(blockIdx.x, nleft * ntoken), nleft, ntoken);
   const int t0 = tile.token * kTileT;
+  if (kList) {
+    if (entry >= t0 && entry < t0 + kTileT) list[entry - t0] = threadIdx.x;
+    __syncthreads();
+  }
+  auto token = [&](int j) { return kList ? list[j - t0] : rows[j]; };  // j in the tile
   const int64_t vt = (int64_t)tile.left * kTileV;  // within the piece
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -134,7 +190,7 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
     const int v = min(128 * (r >> 6) + 64 * (i >> 1) + (r & 63), last_v);
     o.left_off[i] = (uint32_t)v * row_bytes + (((lane & 7) ^ swizzle_rows(r)) << 4);
     const int rt = (4 * wave + i) * 8 + (lane >> 3);
-    o.right_off[i] = (uint32_t)rows[min(t0 + rt, live - 1)] * row_bytes + (((lane & 7) ^ swizzle_rows(rt)) << 4);
+    o.right_off[i] = (uint32_t)token(min(t0 + rt, live - 1)) * row_bytes + (((lane & 7) ^ swizzle_rows(rt)) << 4);
   }
   f32x4 acc[8][4];
   tile_zero(acc);
@@ -147,8 +203,8 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
   for (int n = 0; n < 4; ++n) {
     const int t = t0 + 64 * wn + 16 * n + (lane & 15);
     const bool on = t < live;
-    const int64_t place = on ? target[rows[t]] - v0 - vt : -1;  // the target's word, if it is one of this tile's
-    const int y = place >= 0 && place < kTileV ? (int)place : -1;
+    const int64_t at = on ? target[token(t)] - v0 - vt : -1;  // the target's word, if it is one of this tile's
+    const int y = at >= 0 && at < kTileV ? (int)at : -1;
     float top = -INFINITY;
     bool odd = false;  // NaN among the logits
 #pragma unroll
@@ -194,15 +250,40 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
   }
 }
 
+// loss, lse and what the gradient needs of one token: 1 / S and S_others / S.
+struct Outcome {
+  float loss, lse, inv, other;
+};
+__device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
+  Outcome r;
+  const float ey = relative_exp(ly, N);
+  const float all = others + ey;
+  const float base = __builtin_fmaf(N, kLn2, N * kLn2Lo);
+  if (others <= ey) {
+    r.loss = log1pf(others / ey);
+    r.lse = ly + r.loss;
+  } else {
+    r.lse = base + logf(all);
+    // N ln 2 - l_y first: the two are close when the loss is small
+    r.loss = (__builtin_fmaf(N, kLn2, -ly) + N * kLn2Lo) + logf(all);
+  }
+  r.inv = 1.0f / all;
+  r.other = others / all;
+  if (!(all > 0.f && all < INFINITY) || !(fabsf(N) < kMaxExponent)) r.loss = r.lse = r.inv = r.other = NAN;
+  return r;
+}
+
 // Folds the piece's tiles into the running exponent N and sum S of each token: 8 tokens and 32 lanes
 // along the tiles a workgroup, eight tiles of a lane in flight at once.  shift: N - n of each tile, at
 // most 255 (which leaves nothing of any bf16 value); factor: 2^(N before - N), for what the pieces
-// before have summed.
+// before have summed.  loss (nullptr: not yet, or not here): the piece is the last, N and S are final.
 __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ exponent, const float *__restrict__ sum,
                                                  int64_t tpad, int tiles, bool first,
                                                  const uint32_t *__restrict__ state, float *__restrict__ N,
                                                  float *__restrict__ S, uint8_t *__restrict__ shift,
-                                                 float *__restrict__ factor) {
+                                                 float *__restrict__ factor, const int *__restrict__ rows,
+                                                 const float *__restrict__ target_logit, float *__restrict__ loss,
+                                                 float *__restrict__ lse) {
   constexpr int kLanes = 32, kDeep = 8;
   __shared__ float part[kLanes][9];
   const int live = (int)state[1];
@@ -255,17 +336,25 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
     N[t] = top;
     S[t] = all;
     factor[t] = f;
+    if (loss) {
+      const Outcome r = outcome(top, all, target_logit[t]);
+      loss[rows[t]] = r.loss;
+      if (lse) lse[rows[t]] = r.lse;
+    }
   }
 }
 
 // One tile (256 columns d, 256 tokens) of G over one range of the piece's words, see the top.  The tiles and their
 // splits follow from the tokens that carry a loss; `words` is the length of every piece but the last, so that the
-// ranges, and the tiles' places in part, are the same in all.  part: [split][tile][256 tokens][256 d] fp32, in units of
+// ranges, and the tiles' places in part, are the same in all.  kFold: the piece is the only one and has at most
+// kShiftV words; the exponents are folded here, which spares the launch of head_fold (shift is then unused).  part: [split][tile][256 tokens][256 d] fp32, in units of
 // 2^N.
+template <bool kFold>
 __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restrict__ e, int64_t pitch,
                                                          const uint16_t *__restrict__ w, int nv, int words, int D,
                                                          int nleft, const uint32_t *__restrict__ state,
-                                                         const uint8_t *__restrict__ shift, int64_t tpad,
+                                                         const uint8_t *__restrict__ shift,
+                                                         const float *__restrict__ exponent, int64_t tpad,
                                                          const float *__restrict__ factor, bool first,
                                                          float *__restrict__ part) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
@@ -299,10 +388,26 @@ __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restr
   tile_zero(acc);
   for (int vb = first_word; vb < last_word; vb += kShiftV) {
     const int n = min(kShiftV, last_word - vb);
-    // the tile's shift bytes (tpad is a multiple of 256, so whole words of four tokens)
-    const uint8_t *src = shift + (int64_t)(vb / kStatV) * tpad + t0;
-    for (int i = threadIdx.x; i < (n + kStatV - 1) / kStatV * (kTileT / 4); i += kThreads)
-      ((uint32_t *)shifts)[i] = *(const uint32_t *)(src + (i >> 6) * tpad + 4 * (i & 63));
+    if (kFold) {  // two threads a token
+      const float *ex = exponent + t0 + (threadIdx.x & 255);
+      const int half = threadIdx.x >> 8, all = (nv + kStatV - 1) / kStatV;
+      float top = kNoExponent;
+#pragma unroll 8
+      for (int i = half; i < all; i += 2) top = fmaxf(top, ex[i * tpad]);
+      float *fold = (float *)lds;
+      fold[threadIdx.x] = top;
+      __syncthreads();
+      top = fmaxf(top, fold[threadIdx.x ^ 256]);
+      const int g0 = vb / kStatV;
+#pragma unroll 8
+      for (int i = half; i < (n + kStatV - 1) / kStatV; i += 2)
+        shifts[i * kTileT + (threadIdx.x & 255)] = (uint8_t)fminf(top - ex[(g0 + i) * tpad], 255.f);
+    } else {
+      // the tile's shift bytes (tpad is a multiple of 256, so whole words of four tokens)
+      const uint8_t *src = shift + (int64_t)(vb / kStatV) * tpad + t0;
+      for (int i = threadIdx.x; i < (n + kStatV - 1) / kStatV * (kTileT / 4); i += kThreads)
+        ((uint32_t *)shifts)[i] = *(const uint32_t *)(src + (i >> 6) * tpad + 4 * (i & 63));
+    }
     __syncthreads();
     o.left = uniform(w + (int64_t)vb * D + d0);
     o.right = uniform(e + (int64_t)t0 * pitch + vb);
@@ -331,55 +436,38 @@ __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restr
   }
 }
 
-// loss, lse and what the gradient needs of one token: 1 / S and S_others / S.
-struct Outcome {
-  float loss, lse, inv, other;
-};
-__device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
-  Outcome r;
-  const float ey = relative_exp(ly, N);
-  const float all = others + ey;
-  const float base = __builtin_fmaf(N, kLn2, N * kLn2Lo);
-  if (others <= ey) {
-    r.loss = log1pf(others / ey);
-    r.lse = ly + r.loss;
-  } else {
-    r.lse = base + logf(all);
-    // N ln 2 - l_y first: the two are close when the loss is small
-    r.loss = (__builtin_fmaf(N, kLn2, -ly) + N * kLn2Lo) + logf(all);
-  }
-  r.inv = 1.0f / all;
-  r.other = others / all;
-  if (!(all > 0.f && all < INFINITY) || !(fabsf(N) < kMaxExponent)) r.loss = r.lse = r.inv = r.other = NAN;
-  return r;
+// Eight values of row y of W from column c on (c % 8 == 0), as bf16 pairs: a bf16 head's (q.codes nullptr), or a
+// packed one's by the decode of every use of the weight.
+__device__ __forceinline__ u32x4 row_values(const uint16_t *w, const QWeight &q, const Codebook &cb, int64_t y, int D,
+                                            int c) {
+  const int64_t e = y * D + c;
+  if (w) return *(const u32x4 *)(w + e);
+  const int64_t block = e / kBlock;
+  const float c1 = q.dq ? decode_constant(q.fp8[block], q.s2[block / kGroup], *q.mu) : q.s2[block];
+  const uint32_t codes = *(const uint32_t *)(q.codes + e / 2);
+  auto level = [&](uint32_t k) {  // a register each: the levels are in the kernel's arguments
+    float v = cb.v[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v = k == (uint32_t)i ? cb.v[i] : v;
+    return decode_product(v, c1);
+  };
+  u32x4 out;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    out[i] = pack_bf16x2(level((codes >> (8 * i)) & 15u), level((codes >> (8 * i + 4)) & 15u));
+  return out;
 }
 
-// Loss and lse of every token of the chunk, one thread each.
-__global__ __launch_bounds__(256) void head_losses(int T, const int *__restrict__ place, const float *__restrict__ N,
-                                                   const float *__restrict__ S,
-                                                   const float *__restrict__ target_logit, float *__restrict__ loss,
-                                                   float *__restrict__ lse) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= T) return;
-  const int j = place[t];
-  float a = j == -2 ? NAN : 0.f, b = a;
-  if (j >= 0) {
-    const Outcome r = outcome(N[j], S[j], target_logit[j]);
-    a = r.loss;
-    b = r.lse;
-  }
-  loss[t] = a;
-  if (lse) lse[t] = b;
-}
-
-// grad_h of one token a workgroup (and its loss and lse), eight columns a thread and turn.
+// grad_h of one token a workgroup (and its loss and lse), eight columns a thread and turn.  kFold: as in head_grad, N
+// and S come from the tiles' exponents and sums.
+template <bool kFold>
 __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place, const float *__restrict__ N,
-                                                   const float *__restrict__ S,
+                                                   const float *__restrict__ S, const float *__restrict__ exponent,
+                                                   const float *__restrict__ sum, int64_t tpad, int stat_tiles,
                                                    const float *__restrict__ target_logit,
-                                                   const int64_t *__restrict__ target,
-                                                   const uint16_t *__restrict__ wy, bool by_token,
-                                                   const float *__restrict__ weight, float scale,
-                                                   const float *__restrict__ part, int words, int nleft,
+                                                   const int64_t *__restrict__ target, const uint16_t *__restrict__ w,
+                                                   QWeight q, Codebook cb, const float *__restrict__ weight,
+                                                   float scale, const float *__restrict__ part, int words, int nleft,
                                                    const uint32_t *__restrict__ state, int D,
                                                    float *__restrict__ loss, float *__restrict__ lse,
                                                    uint16_t *__restrict__ grad) {
@@ -389,20 +477,30 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
   if (j < 0) {
     const uint32_t fill = j == -2 ? 0x7FC07FC0u : 0u;
     for (int c = threadIdx.x * 8; c < D; c += 2048) *(u32x4 *)(g + c) = u32x4{fill, fill, fill, fill};
-    if (threadIdx.x == 0) {
-      loss[t] = j == -2 ? NAN : 0.f;
-      if (lse) lse[t] = j == -2 ? NAN : 0.f;
-    }
     return;
   }
-  const Outcome r = outcome(N[j], S[j], target_logit[j]);
+  float n, s;
+  if (kFold) {  // at most 64 tiles, one a lane, every wave for itself
+    const int i = threadIdx.x & 63;
+    const float ex = i < stat_tiles ? exponent[i * tpad + j] : kNoExponent, sm = i < stat_tiles ? sum[i * tpad + j] : 0.f;
+    n = ex;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) n = fmaxf(n, __shfl_xor(n, d));
+    s = sm * __builtin_amdgcn_exp2f(-fminf(n - ex, 300.f));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+  } else {
+    n = N[j];
+    s = S[j];
+  }
+  const Outcome r = outcome(n, s, target_logit[j]);
   if (threadIdx.x == 0) {
     loss[t] = r.loss;
     if (lse) lse[t] = r.lse;
   }
   const float c_t = weight ? scale * weight[t] : scale;
   const float a = c_t * r.inv, b = c_t * r.other;
-  const uint16_t *wr = wy + (by_token ? (int64_t)t : target[t]) * D;  // the target's row of W
+  const int64_t y = target[t];
   // the token's row in every split's tiles
   const int ntoken = ((int)state[1] + kTileT - 1) / kTileT, tiles = nleft * ntoken;
   const int splits = choose_split(tiles, words).count;
@@ -410,43 +508,24 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
     const int64_t tile = place_at(Tile{c / kTileV, j / kTileT}, nleft, ntoken);
     const float *p = part + tile * (kTileT * kTileV) + j % kTileT * kTileV + c % kTileV;
     f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-    for (int s = 0; s < splits; ++s) {
-      const f32x4 x = *(const f32x4 *)p, y = *(const f32x4 *)(p + 4);
+    for (int k = 0; k < splits; ++k) {
+      const f32x4 x = *(const f32x4 *)p, z = *(const f32x4 *)(p + 4);
       p += (int64_t)tiles * (kTileT * kTileV);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        lo[q] += x[q];
-        hi[q] += y[q];
+      for (int i = 0; i < 4; ++i) {
+        lo[i] += x[i];
+        hi[i] += z[i];
       }
     }
-    const u32x4 wv = *(const u32x4 *)(wr + c);
+    const u32x4 wv = row_values(w, q, cb, y, D, c);
     u32x4 o;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float g0 = q < 2 ? lo[2 * q] : hi[2 * q - 4], g1 = q < 2 ? lo[2 * q + 1] : hi[2 * q - 3];
-      o[q] = pack_bf16x2(__builtin_fmaf(a, g0, -b * bf16_lo(wv[q])), __builtin_fmaf(a, g1, -b * bf16_hi(wv[q])));
+    for (int i = 0; i < 4; ++i) {
+      const float g0 = i < 2 ? lo[2 * i] : hi[2 * i - 4], g1 = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+      const uint32_t pair = wv[i];
+      o[i] = pack_bf16x2(__builtin_fmaf(a, g0, -b * bf16_lo(pair)), __builtin_fmaf(a, g1, -b * bf16_hi(pair)));
     }
     *(u32x4 *)(g + c) = o;
-  }
-}
-
-// The decoded rows of the targets of a packed head, [T][D] bf16 in token order (one workgroup a
-// token): the decode of every use of the weight, one value at a time.
-__global__ __launch_bounds__(256) void head_target_rows(QWeight q, Codebook cb, const int64_t *__restrict__ target,
-                                                        uint16_t *__restrict__ out) {
-  __shared__ float level[16];
-  if (threadIdx.x < 16) level[threadIdx.x] = cb.v[threadIdx.x];
-  __syncthreads();
-  const int t = blockIdx.x;
-  const int64_t y = target[t];
-  if (y < 0 || y >= q.n_out) return;
-  const int64_t e0 = y * q.n_in;
-  for (int c = threadIdx.x * 2; c < q.n_in; c += 512) {
-    const int64_t el = e0 + c, block = el / kBlock;
-    const float c1 = q.dq ? decode_constant(q.fp8[block], q.s2[block / kGroup], *q.mu) : q.s2[block];
-    const uint32_t byte = q.codes[el >> 1];
-    *(uint32_t *)(out + (int64_t)t * q.n_in + c) =
-        pack_bf16x2(decode_product(level[byte & 15u], c1), decode_product(level[byte >> 4], c1));
   }
 }
 
@@ -621,10 +700,7 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
   if (t == 0) few_state(target, T, V, state);
   const int64_t y = target[t];
   if (y < 0 || y >= V) {
-    if (tid == 0) {
-      loss[t] = y < 0 ? 0.f : NAN;
-      if (lse) lse[t] = y < 0 ? 0.f : NAN;
-    }
+    if (tid == 0) no_loss(y, t, loss, lse);
     return;
   }
   float top = kNoExponent;
@@ -653,39 +729,42 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
   }
 }
 
-// grad_h, loss and lse from the chunks: workgroup (token, 1024 columns), four columns a thread.
-__global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ target, int T, int64_t V, int D,
+// grad_h, loss and lse from the chunks: workgroup (token, 1024 columns) of 128 threads, eight columns each.
+__global__ __launch_bounds__(128) void few_finish(const int64_t *__restrict__ target, int T, int64_t V, int D,
                                                   int chunks, const float *__restrict__ N, const float *__restrict__ S,
                                                   const float *__restrict__ target_logit,
-                                                  const uint16_t *__restrict__ wy, bool by_token,
+                                                  const uint16_t *__restrict__ w, QWeight q, Codebook cb,
                                                   const float *__restrict__ weight, float scale,
                                                   const float *__restrict__ part, uint32_t *__restrict__ state,
                                                   float *__restrict__ loss, float *__restrict__ lse,
                                                   uint16_t *__restrict__ grad) {
-  const int t = blockIdx.x, c = (int)blockIdx.y * 1024 + 4 * (int)threadIdx.x;
+  const int t = blockIdx.x, c = (int)blockIdx.y * 1024 + 8 * (int)threadIdx.x;
   if (t == 0 && blockIdx.y == 0) few_state(target, T, V, state);
   const int64_t y = target[t];
   const bool lead = blockIdx.y == 0 && threadIdx.x == 0;
-  uint2 *g = (uint2 *)(grad + (int64_t)t * D + c);
+  u32x4 *g = (u32x4 *)(grad + (int64_t)t * D + c);
   if (y < 0 || y >= V) {
     const uint32_t fill = y < 0 ? 0u : 0x7FC07FC0u;
-    if (c < D) *g = make_uint2(fill, fill);
-    if (lead) {
-      loss[t] = y < 0 ? 0.f : NAN;
-      if (lse) lse[t] = y < 0 ? 0.f : NAN;
-    }
+    if (c < D) *g = u32x4{fill, fill, fill, fill};
+    if (lead) no_loss(y, t, loss, lse);
     return;
   }
   float top = kNoExponent, s = 0.f;
+#pragma unroll 8
   for (int i = 0; i < chunks; ++i) top = fmaxf(top, N[i * kFewTokens + t]);
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll 4
   for (int i = 0; i < chunks; ++i) {
     const float f = __builtin_amdgcn_exp2f(-fminf(top - N[i * kFewTokens + t], 300.f));
     s += S[i * kFewTokens + t] * f;
     if (c < D) {
-      const f32x4 x = *(const f32x4 *)(part + ((int64_t)i * T + t) * D + c);
+      const float *p = part + ((int64_t)i * T + t) * D + c;
+      const f32x4 x = *(const f32x4 *)p, z = *(const f32x4 *)(p + 4);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) sum[q] = __builtin_fmaf(x[q], f, sum[q]);
+      for (int k = 0; k < 4; ++k) {
+        lo[k] = __builtin_fmaf(x[k], f, lo[k]);
+        hi[k] = __builtin_fmaf(z[k], f, hi[k]);
+      }
     }
   }
   const Outcome r = outcome(top, s, target_logit[t]);
@@ -696,9 +775,15 @@ __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ ta
   if (c >= D) return;
   const float c_t = weight ? scale * weight[t] : scale;
   const float a = c_t * r.inv, b = c_t * r.other;
-  const uint2 wv = *(const uint2 *)(wy + (by_token ? (int64_t)t : y) * D + c);
-  *g = make_uint2(pack_bf16x2(__builtin_fmaf(a, sum[0], -b * bf16_lo(wv.x)), __builtin_fmaf(a, sum[1], -b * bf16_hi(wv.x))),
-                  pack_bf16x2(__builtin_fmaf(a, sum[2], -b * bf16_lo(wv.y)), __builtin_fmaf(a, sum[3], -b * bf16_hi(wv.y))));
+  const u32x4 wv = row_values(w, q, cb, y, D, c);
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float g0 = i < 2 ? lo[2 * i] : hi[2 * i - 4], g1 = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+    const uint32_t pair = wv[i];
+    o[i] = pack_bf16x2(__builtin_fmaf(a, g0, -b * bf16_lo(pair)), __builtin_fmaf(a, g1, -b * bf16_hi(pair)));
+  }
+  *g = o;
 }
 
 }  // namespace
@@ -731,7 +816,6 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
   p.off_e = p.grad ? take((size_t)p.T * groups * kFewWords * 2) : 0;
   p.off_part = p.grad ? take((size_t)p.splits * p.T * p.D * 4) : 0;
   p.off_w = p.packed ? take((size_t)p.words * p.D * 2) : 0;
-  p.off_wy = p.packed && p.grad ? take((size_t)p.T * p.D * 2) : 0;
   p.off_rows = p.off_place = p.off_factor = p.off_shift = 0;
   p.total = off;
   return p;
@@ -763,7 +847,7 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
   float *exponent = (float *)(ws + p.off_exponent), *sum = (float *)(ws + p.off_sum);
   float *part = (float *)(ws + p.off_part);
   uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
-  uint16_t *wp = (uint16_t *)(ws + p.off_w), *wy = (uint16_t *)(ws + p.off_wy);
+  uint16_t *wp = (uint16_t *)(ws + p.off_w);
   const int T = (int)p.T, D = (int)p.D, groups = (int)cdiv(p.V, kFewWords);
   const int64_t pitch = (int64_t)groups * kFewWords;
   int chunk0 = 0;
@@ -788,9 +872,8 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
     few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, logit, state, loss, lse);
     return hipGetLastError();
   }
-  if (q) head_target_rows<<<(unsigned)T, 256, 0, st>>>(*q, cb, target, wy);
-  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 1024)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, logit,
-                                                                       q ? wy : w, q != nullptr, weight, scale, part,
+  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 1024)), 128, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, logit, w,
+                                                                       q ? *q : QWeight{}, cb, weight, scale, part,
                                                                        state, loss, lse, grad);
   return hipGetLastError();
 }
@@ -842,7 +925,6 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.off_e = grad ? take((size_t)p.chunk * p.words * 2) : 0;
   p.off_part = grad ? take((size_t)p.splits * kTileT * kTileV * 4) : 0;
   p.off_w = packed ? take((size_t)p.words * D * 2) : 0;
-  p.off_wy = packed && grad ? take((size_t)p.chunk * D * 2) : 0;
   p.total = off;
   return p;
 }
@@ -860,37 +942,42 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
   float *sum = (float *)(ws + p.off_sum), *part = (float *)(ws + p.off_part);
   uint8_t *shift = p.grad ? (uint8_t *)(ws + p.off_shift) : nullptr;
   uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
-  uint16_t *wp = (uint16_t *)(ws + p.off_w), *wy = (uint16_t *)(ws + p.off_wy);
+  uint16_t *wp = (uint16_t *)(ws + p.off_w);
   const int D = (int)p.D;
   for (int64_t c0 = 0; c0 < p.T; c0 += p.chunk) {
     const int T = (int)std::min(p.chunk, p.T - c0);
     const int ntoken = (int)cdiv(T, kTileT), nd = (int)cdiv(p.D, kTileV), words = (int)p.words;
     const uint16_t *hc = h + c0 * p.D;
     const int64_t *yc = target + c0;
-    head_scan<<<1, 1024, 0, st>>>(yc, T, p.V, c0 == 0, rows, place, state);
+    float *lc = loss + c0, *ec = lse ? lse + c0 : nullptr;
+    const bool list = p.T <= kThreads;                            // head_logits lists the tokens itself
+    const bool fold = p.grad && p.pieces == 1 && words <= kShiftV;  // head_grad and head_finish fold the tiles themselves
+    if (!list) head_scan<<<1, 1024, 0, st>>>(yc, T, p.V, c0 == 0, rows, place, state, lc, ec);
     for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
       const int nv = (int)std::min(p.words, p.V - v0), nleft = (int)cdiv(nv, kTileV);
+      const bool last = v0 + nv == p.V;
       const uint16_t *piece = w ? w + v0 * p.D : wp;
       if (q) {
         const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
         if (err != hipSuccess) return err;
       }
-      head_logits<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(hc, piece, yc, v0, nv, D, nleft, rows, state,
-                                                                 e, p.words, exponent, sum, p.tpad, logit);
-      head_fold<<<(unsigned)cdiv(T, 8), 256, 0, st>>>(exponent, sum, p.tpad, (int)cdiv(nv, kStatV), v0 == 0, state, N,
-                                                      S, shift, factor);
+      const auto logits = list ? head_logits<true> : head_logits<false>;
+      logits<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(hc, piece, yc, T, p.V, v0, nv, D, nleft, rows, place, state,
+                                                            lc, ec, e, p.words, exponent, sum, p.tpad, logit);
+      if (!fold)
+        head_fold<<<(unsigned)cdiv(T, 8), 256, 0, st>>>(exponent, sum, p.tpad, (int)cdiv(nv, kStatV), v0 == 0, state, N,
+                                                        S, shift, factor, rows, logit, last && !p.grad ? lc : nullptr,
+                                                        ec);
       if (!p.grad) continue;
-      head_grad<<<(unsigned)split_slots(nd, ntoken, words), kThreads, 0, st>>>(
-          e, p.words, piece, nv, words, D, nd, state, shift, p.tpad, factor, v0 == 0, part);
+      const auto product = fold ? head_grad<true> : head_grad<false>;
+      product<<<(unsigned)split_slots(nd, ntoken, words), kThreads, 0, st>>>(
+          e, p.words, piece, nv, words, D, nd, state, shift, exponent, p.tpad, factor, v0 == 0, part);
     }
-    if (!p.grad) {
-      head_losses<<<(unsigned)cdiv(T, 256), 256, 0, st>>>(T, place, N, S, logit, loss + c0, lse ? lse + c0 : nullptr);
-      continue;
-    }
-    if (q) head_target_rows<<<(unsigned)T, 256, 0, st>>>(*q, cb, yc, wy);
-    head_finish<<<(unsigned)T, 256, 0, st>>>(place, N, S, logit, yc, q ? wy : w, q != nullptr,
-                                             weight ? weight + c0 : nullptr, scale, part, words, nd, state, D, loss + c0,
-                                             lse ? lse + c0 : nullptr, grad + c0 * p.D);
+    if (!p.grad) continue;
+    const auto finish = fold ? head_finish<true> : head_finish<false>;
+    finish<<<(unsigned)T, 256, 0, st>>>(place, N, S, exponent, sum, p.tpad, (int)cdiv(p.V, kStatV), logit, yc, w,
+                                        q ? *q : QWeight{}, cb, weight ? weight + c0 : nullptr, scale, part, words, nd,
+                                        state, D, lc, ec, grad + c0 * p.D);
   }
   return hipGetLastError();
 }

@@ -277,7 +277,7 @@ struct HeadPlan {
   // each); otherwise splits: the gradient's partial tiles
   int64_t chunk, tpad, words, pieces, splits, split_words;
   size_t off_rows, off_place, off_logit, off_n, off_s, off_factor, off_exponent, off_sum, off_shift, off_e, off_part,
-      off_w, off_wy, total;
+      off_w, total;
 };
 HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed);
 // w (bf16 [V x D]) or q (packed), the other one nullptr; weight, lse may be nullptr; grad nullptr iff !p.grad.

@@ -97,7 +97,9 @@ SHAPES = [(1, 64, 1), (1, 64, 2), (1, 128, 300), (2, 64, 255), (3, 192, 257), (1
           (300, 1088, 777), (513, 2112, 1281), (1000, 256, 9001),
           # up to 64 tokens: one to four tiles of 16, one to many chunks of words, steps shared unevenly by the waves
           (1, 4096, 32003), (5, 8192, 3000), (16, 64, 16385), (17, 1024, 8193), (32, 2048, 641), (33, 64, 100001),
-          (48, 576, 4097), (64, 1088, 20001), (2, 65536, 300)]
+          (48, 576, 4097), (64, 1088, 20001), (2, 65536, 300),
+          # lists of tokens and folds inside the products, and on either side of where they end
+          (511, 64, 8192), (512, 128, 8193), (513, 64, 8192), (514, 128, 8193), (512, 192, 100), (70, 4096, 419)]
 
 
 @gpu
@@ -124,6 +126,14 @@ def test_several_chunks_of_tokens():
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=8, std=0.3))
     y[16384:16400] = -1
     _check(h, w, w, y, weight=torch_mod().rand(T, device="cuda"))
+    ws = qlora.head_loss_workspace(T, V, D)
+    for at in (5, T - 5):  # a bad target in either chunk is reported
+        bad = y.clone()
+        bad[at] = V
+        qlora.head_loss(h, w, bad, workspace=ws)
+        assert qlora.status_read(ws) == 8
+    T = 16384 + 300  # a last chunk short enough for another form
+    _check(h[:T].contiguous(), w, w, y[:T].contiguous())
 
 
 @gpu
@@ -226,7 +236,7 @@ def test_values_past_the_range(value, T):
 
 
 @gpu
-@pytest.mark.parametrize("T", [63, 70])
+@pytest.mark.parametrize("T", [63, 70, 600])
 def test_target_past_the_vocabulary(T):
     torch = torch_mod()
     D, V = 128, 1000
