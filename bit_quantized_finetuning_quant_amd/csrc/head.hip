@@ -41,12 +41,11 @@ namespace {
 constexpr int kStatV = 128;     // words that share one exponent n per token
 constexpr int kShiftV = 8192;   // words whose shift bytes a workgroup holds in LDS at a time
 constexpr int64_t kFewMaxWords = (int64_t)1 << 20;
-constexpr float kLog2eHi = 1.44269502162933349609375f;  // fl32(log2 e), and the rest of it
-constexpr float kLog2eLo = 1.92596299112661746887e-8f;
+constexpr float kLog2e = 1.44269502162933349609375f;    // fl32(log2 e)
 constexpr float kLn2 = 0.693147182464599609375f;        // fl32(ln 2), and the rest of it
 constexpr float kLn2Lo = -1.90465429995776804525e-9f;
 // |n| from which a row counts as overflown (its loss and gradient are NaN): below it integers and
-// their differences are exact in fp32 and l log2 e - n is formed to 2^-24 of l
+// their differences are exact in fp32, and l log2 e - n is rounded once
 constexpr float kMaxExponent = 4194304.0f;
 constexpr float kNoExponent = -3.0e38f;  // n of a tile without any word
 
@@ -138,11 +137,56 @@ __device__ __forceinline__ int list_tokens(const int64_t *target, int T, int64_t
 
 // n of a tile from its largest logit.  Finite whatever the logits are: NaN and infinite sums show in s.
 __device__ __forceinline__ float tile_exponent(float top) {
-  return ceilf(fminf(fmaxf(top * kLog2eHi, -2.0f * kMaxExponent), 2.0f * kMaxExponent));
+  return ceilf(fminf(fmaxf(top * kLog2e, -2.0f * kMaxExponent), 2.0f * kMaxExponent));
 }
-// 2^(l log2 e - n)
+// 2^(l log2 e - n).  log2 e is its fp32 value everywhere, 1.3e-8 of it too small, so that all exponentials
+// of a token belong to logits scaled by that much: 1.3e-8 of l - l_y in the loss.
 __device__ __forceinline__ float relative_exp(float l, float n) {
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2eLo, __builtin_fmaf(l, kLog2eHi, -n)));
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -n));
+}
+
+// 16 tokens (fragment n) by the wave's 128 words of a tile of the logits: e, n and s.  A NaN logit shows in
+// s.  kTest: words past nvt are left out, and the token's target y (of this tile, or -1) goes to
+// target_logit.  out, exponent, sum, target_logit: this lane's token (out: its first word, too).
+template <bool kTest>
+__device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool on, int y, int vl, int nvt,
+                                           uint16_t *out, float *exponent, float *sum, float *target_logit) {
+  const int lane = threadIdx.x & 63;
+  float top = -INFINITY;
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float l = acc[m][n][q];
+      top = fmaxf(top, !kTest || vl + 16 * m + q < nvt ? l : -INFINITY);
+    }
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  const float ex = !kTest || (vl & ~127) < nvt ? tile_exponent(top) : kNoExponent;
+  float s = 0.f, ly = 0.f;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    float p[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float l = acc[m][n][q];
+      p[q] = relative_exp(l, ex);
+      if (kTest) {
+        const int v = vl + 16 * m + q;
+        ly = v == y ? l : ly;
+        p[q] = v == y || v >= nvt ? 0.f : p[q];
+      }
+      s += p[q];
+    }
+    if (out && on) *(uint2 *)(out + 16 * m) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+  }
+  if (kTest && y >= 0 && (y & ~127) == (vl & ~127) && ((y >> 2) & 3) == (lane >> 4)) *target_logit = ly;
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  if (lane < 16 && on) {
+    *exponent = ex;
+    *sum = s;
+  }
 }
 
 // One tile of the logits, see the top.  e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
@@ -197,56 +241,22 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
   product<false, false>(o, D / kStep, lds, nullptr, acc);
 
   // rows (words) of this lane: 128 wm + 16 m + 4 (lane / 16) + q
-  const int vl = 128 * wm + 4 * (lane >> 4);
-  const int nvt = last_v + 1;
+  const int vl = 128 * wm + 4 * (lane >> 4), nvt = last_v + 1;
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
     const int t = t0 + 64 * wn + 16 * n + (lane & 15);
     const bool on = t < live;
     const int64_t at = on ? target[token(t)] - v0 - vt : -1;  // the target's word, if it is one of this tile's
     const int y = at >= 0 && at < kTileV ? (int)at : -1;
-    float top = -INFINITY;
-    bool odd = false;  // NaN among the logits
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float l = acc[m][n][q];
-        const bool in = vl + 16 * m + q < nvt;
-        odd |= in && l != l;
-        top = fmaxf(top, in ? l : -INFINITY);
-      }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float ex = 128 * wm < nvt ? tile_exponent(top) : kNoExponent;
-    float s = 0.f;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      float p[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float l = acc[m][n][q];
-        const int v = vl + 16 * m + q;
-        p[q] = relative_exp(l, ex);
-        if (v >= nvt) p[q] = 0.f;
-        if (v == y) {
-          target_logit[t] = l;
-          p[q] = 0.f;
-        }
-        s += p[q];
-      }
-      if (e && on)
-        *(uint2 *)(e + (int64_t)t * pitch + vt + vl + 16 * m) =
-            make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
-    }
-    if (odd) s = NAN;
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (lane < 16 && on) {
-      const int64_t at = (int64_t)(2 * tile.left + wm) * tpad + t;
-      exponent[at] = ex;
-      sum[at] = s;
-    }
+    // most waves hold no word past the vocabulary and no token's target: their values need no test
+    if (nvt == kTileV && !__any(y >> 7 == wm))
+      put_logits<false>(acc, n, on, -1, vl, nvt, e ? e + (int64_t)t * pitch + vt + vl : nullptr,
+                        exponent + (int64_t)(2 * tile.left + wm) * tpad + t, sum + (int64_t)(2 * tile.left + wm) * tpad + t,
+                        nullptr);
+    else
+      put_logits<true>(acc, n, on, y, vl, nvt, e ? e + (int64_t)t * pitch + vt + vl : nullptr,
+                       exponent + (int64_t)(2 * tile.left + wm) * tpad + t, sum + (int64_t)(2 * tile.left + wm) * tpad + t,
+                       target_logit + t);
   }
 }
 
@@ -572,7 +582,6 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
   const int64_t at = on ? target[t] - v0 - vt : -1;
   const int y = at >= 0 && at < kFewWords ? (int)at : -1;
   float l[kWords], top = -INFINITY;
-  bool odd = false;
 #pragma unroll
   for (int i = 0; i < kWords; i += 4) {
     const f32x4 x = few_sum<NT>(red, t, first + i);
@@ -580,7 +589,6 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
     for (int q = 0; q < 4; ++q) {
       const bool in = first + i + q < words;
       l[i + q] = x[q];
-      odd |= in && x[q] != x[q];
       top = fmaxf(top, in ? x[q] : -INFINITY);
     }
   }
@@ -607,7 +615,6 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) row[i] = make_uint2(packed[2 * i], packed[2 * i + 1]);
   }
-  if (odd) s = NAN;
 #pragma unroll
   for (int d = 1; d < kLanes; d <<= 1) s += __shfl_xor(s, d);
   if (on && lane % kLanes == 0) {
@@ -729,8 +736,9 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
   }
 }
 
-// grad_h, loss and lse from the chunks: workgroup (token, 1024 columns) of 128 threads, eight columns each.
-__global__ __launch_bounds__(128) void few_finish(const int64_t *__restrict__ target, int T, int64_t V, int D,
+// grad_h, loss and lse from the chunks: workgroup (token, 512 columns), eight columns and every fourth
+// chunk a thread, so that the chunks' sums (from the caches of other XCDs) arrive in few round trips.
+__global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ target, int T, int64_t V, int D,
                                                   int chunks, const float *__restrict__ N, const float *__restrict__ S,
                                                   const float *__restrict__ target_logit,
                                                   const uint16_t *__restrict__ w, QWeight q, Codebook cb,
@@ -738,41 +746,69 @@ __global__ __launch_bounds__(128) void few_finish(const int64_t *__restrict__ ta
                                                   const float *__restrict__ part, uint32_t *__restrict__ state,
                                                   float *__restrict__ loss, float *__restrict__ lse,
                                                   uint16_t *__restrict__ grad) {
-  const int t = blockIdx.x, c = (int)blockIdx.y * 1024 + 8 * (int)threadIdx.x;
+  __shared__ f32x4 half[3][64][2];
+  const int t = blockIdx.x, lane = threadIdx.x & 63, group = threadIdx.x >> 6;
+  const int c = (int)blockIdx.y * 512 + 8 * lane;
   if (t == 0 && blockIdx.y == 0) few_state(target, T, V, state);
   const int64_t y = target[t];
   const bool lead = blockIdx.y == 0 && threadIdx.x == 0;
   u32x4 *g = (u32x4 *)(grad + (int64_t)t * D + c);
   if (y < 0 || y >= V) {
     const uint32_t fill = y < 0 ? 0u : 0x7FC07FC0u;
-    if (c < D) *g = u32x4{fill, fill, fill, fill};
+    if (c < D && group == 0) *g = u32x4{fill, fill, fill, fill};
     if (lead) no_loss(y, t, loss, lse);
     return;
   }
+  // N and S: the chunks one a lane, every wave for itself
   float top = kNoExponent, s = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < chunks; ++i) top = fmaxf(top, N[i * kFewTokens + t]);
+  for (int i = lane; i < chunks; i += 64) top = fmaxf(top, N[i * kFewTokens + t]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  for (int i = lane; i < chunks; i += 64)
+    s += S[i * kFewTokens + t] * __builtin_amdgcn_exp2f(-fminf(top - N[i * kFewTokens + t], 300.f));
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
   f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-#pragma unroll 4
-  for (int i = 0; i < chunks; ++i) {
-    const float f = __builtin_amdgcn_exp2f(-fminf(top - N[i * kFewTokens + t], 300.f));
-    s += S[i * kFewTokens + t] * f;
-    if (c < D) {
-      const float *p = part + ((int64_t)i * T + t) * D + c;
-      const f32x4 x = *(const f32x4 *)p, z = *(const f32x4 *)(p + 4);
+  const float *p = part + (int64_t)t * D + min(c, D - 8);
+  for (int i0 = group; i0 < chunks; i0 += 16) {
+    f32x4 x[4], z[4];
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = min(i0 + 4 * j, chunks - 1);
+      x[j] = *(const f32x4 *)(p + (int64_t)i * T * D);
+      z[j] = *(const f32x4 *)(p + (int64_t)i * T * D + 4);
+      f[j] = i0 + 4 * j < chunks ? __builtin_amdgcn_exp2f(-fminf(top - N[i * kFewTokens + t], 300.f)) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        lo[k] = __builtin_fmaf(x[k], f, lo[k]);
-        hi[k] = __builtin_fmaf(z[k], f, hi[k]);
+        if (i0 + 4 * j >= chunks) continue;  // a factor of 0 would not keep a NaN out
+        lo[k] = __builtin_fmaf(x[j][k], f[j], lo[k]);
+        hi[k] = __builtin_fmaf(z[j][k], f[j], hi[k]);
       }
-    }
   }
+  if (group > 0) {
+    half[group - 1][lane][0] = lo;
+    half[group - 1][lane][1] = hi;
+  }
+  __syncthreads();
   const Outcome r = outcome(top, s, target_logit[t]);
   if (lead) {
     loss[t] = r.loss;
     if (lse) lse[t] = r.lse;
   }
-  if (c >= D) return;
+  if (group > 0 || c >= D) return;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const f32x4 x = half[j][lane][0], z = half[j][lane][1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lo[k] += x[k];
+      hi[k] += z[k];
+    }
+  }
   const float c_t = weight ? scale * weight[t] : scale;
   const float a = c_t * r.inv, b = c_t * r.other;
   const u32x4 wv = row_values(w, q, cb, y, D, c);
@@ -872,7 +908,7 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
     few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, logit, state, loss, lse);
     return hipGetLastError();
   }
-  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 1024)), 128, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, logit, w,
+  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, logit, w,
                                                                        q ? *q : QWeight{}, cb, weight, scale, part,
                                                                        state, loss, lse, grad);
   return hipGetLastError();
