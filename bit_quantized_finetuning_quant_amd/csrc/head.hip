@@ -371,7 +371,7 @@ __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restr
   __shared__ __attribute__((aligned(16))) uint8_t shifts[kShiftV / kStatV * kTileT];
   const int live = (int)state[1];
   const int ntoken = (live + kTileT - 1) / kTileT, tiles = nleft * ntoken;
-  const Split split = choose_split(tiles, words);
+  const Split split = split_of(tiles, words);
   if ((int)blockIdx.x >= tiles * split.count) return;
   const int slot = place_of(blockIdx.x, tiles * split.count), nth = scalar(slot / tiles);
   const Tile tile = tile_at(slot - nth * tiles, nleft, ntoken);
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
   const int64_t y = target[t];
   // the token's row in every split's tiles
   const int ntoken = ((int)state[1] + kTileT - 1) / kTileT, tiles = nleft * ntoken;
-  const int splits = choose_split(tiles, words).count;
+  const int splits = split_of(tiles, words).count;
   for (int c = threadIdx.x * 8; c < D; c += 2048) {
     const int64_t tile = place_at(Tile{c / kTileV, j / kTileT}, nleft, ntoken);
     const float *p = part + tile * (kTileT * kTileV) + j % kTileT * kTileV + c % kTileV;
@@ -540,8 +540,10 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 }
 
 // ---------------------------------------------------------------------------
-// Up to 64 tokens: both products are bound by streaming W once and run on the
-// per-wave streams, 64 words (or 64 columns d) a workgroup.  Exponents n are
+// Few tokens or few words: the products run on the per-wave streams, 64 words
+// (or 64 columns d) by up to 64 tokens a workgroup.  Up to 64 tokens both are
+// bound by streaming W once; beyond, this form is for problems with too few
+// 256 x 256 tiles to occupy the CUs (few_pays).  Exponents n are
 // per token and 64 words here, and the gradient's sums of a chunk of words are
 // relative to the chunk's own largest n, which few_finish brings together: no
 // pass over the tiles lies between the two.
@@ -549,25 +551,27 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 constexpr int kFewWords = 64;       // words that share an exponent, and a step of the gradient
 constexpr int kFewChunk = 128;      // steps of a chunk at most: its shift bytes are held in LDS
 
-// e (nullptr: the loss alone) [T][pitch], exponent and sum [64 words][64 tokens]; v0: the piece's first word, which is
-// also the first column of e; group0: its first 64 words.
+// e (nullptr: the loss alone) [T][pitch], exponent and sum [64 words][tpad]; v0: the piece's first word, which is
+// also the first column of e.  Workgroups: the token groups of 64 words, then the next words'.
 template <int NT>
 __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const uint16_t *__restrict__ h,
                                                              const uint16_t *__restrict__ w,
                                                              const int64_t *__restrict__ target, int T, int64_t v0,
                                                              int64_t nv, int D, uint16_t *__restrict__ e, int64_t pitch,
                                                              float *__restrict__ exponent, float *__restrict__ sum,
-                                                             float *__restrict__ target_logit) {
+                                                             int tpad, float *__restrict__ target_logit) {
   constexpr int kBytes = few_stages<false, NT>() * few_stage<NT>();
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t vt = (int64_t)blockIdx.x * kFewWords;
+  const int groups = tpad / kFewTokens, place = place_of(blockIdx.x, gridDim.x), block = scalar(place / groups);
+  const int t0 = (place - block * groups) * kFewTokens;
+  const int64_t vt = (int64_t)block * kFewWords;
   const int words = (int)min((int64_t)kFewWords, nv - vt);
   uint32_t off[2 * NT];
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
     const int r = 8 * j + (lane >> 3);
-    off[j] = (uint32_t)min(r, T - 1) * (uint32_t)(2 * D) + (((lane & 7) ^ swizzle_rows(r)) << 4);
+    off[j] = (uint32_t)min(t0 + r, T - 1) * (uint32_t)(2 * D) + (((lane & 7) ^ swizzle_rows(r)) << 4);
   }
   f32x4 acc[4][NT];
   few_zero<NT>(acc);
@@ -577,14 +581,14 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
   few_put<NT>(acc, red);
   // 4 NT tokens a wave, 16 / NT lanes a token, 4 NT words a lane
   constexpr int kLanes = 16 / NT, kWords = 4 * NT;
-  const int t = wave * 4 * NT + lane / kLanes, first = lane % kLanes * kWords;
+  const int tl = wave * 4 * NT + lane / kLanes, t = t0 + tl, first = lane % kLanes * kWords;
   const bool on = t < T;
   const int64_t at = on ? target[t] - v0 - vt : -1;
   const int y = at >= 0 && at < kFewWords ? (int)at : -1;
   float l[kWords], top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kWords; i += 4) {
-    const f32x4 x = few_sum<NT>(red, t, first + i);
+    const f32x4 x = few_sum<NT>(red, tl, first + i);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bool in = first + i + q < words;
@@ -618,37 +622,40 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
 #pragma unroll
   for (int d = 1; d < kLanes; d <<= 1) s += __shfl_xor(s, d);
   if (on && lane % kLanes == 0) {
-    const int64_t i = (v0 + vt) / kFewWords * kFewTokens + t;
+    const int64_t i = (v0 + vt) / kFewWords * tpad + t;
     exponent[i] = ex;
     sum[i] = s;
   }
 }
 
 // One chunk of words, 64 columns: part[chunk][T][D] relative to 2^N of the chunk, and (first columns) its N and S
-// [chunk][64].  e, exponent and sum start at the piece.
+// [chunk][tpad].  e, exponent and sum start at the piece.
 template <int NT>
 __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__restrict__ e, int64_t pitch,
                                                            const uint16_t *__restrict__ w, int T, int64_t nv, int D,
                                                            int chunk_steps, int chunk0,
                                                            const float *__restrict__ exponent,
-                                                           const float *__restrict__ sum, float *__restrict__ N,
-                                                           float *__restrict__ S, float *__restrict__ part) {
+                                                           const float *__restrict__ sum, int tpad,
+                                                           float *__restrict__ N, float *__restrict__ S,
+                                                           float *__restrict__ part) {
   constexpr int kBytes = few_stages<true, NT>() * few_stage<NT>(), kT = 16 * NT, kRows = kFewThreads / kT;
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   __shared__ uint8_t shifts[kFewChunk * kT];
   __shared__ float fold[kFewThreads];
-  const int slices = D / 64;
-  const int chunk = (int)(blockIdx.x / slices), slice = (int)(blockIdx.x % slices);
+  // places: the slices of a chunk for one token group, then its other token groups, then the next chunk
+  const int slices = D / 64, groups = tpad / kFewTokens, place = place_of(blockIdx.x, gridDim.x);
+  const int over = scalar(place / slices), slice = scalar(place - over * slices);
+  const int chunk = scalar(over / groups), t0 = (over - chunk * groups) * kFewTokens;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t vb = (int64_t)chunk * chunk_steps * kFewWords;
   const int words = (int)min((int64_t)chunk_steps * kFewWords, nv - vb);
   const int steps = (words + kFewWords - 1) / kFewWords;
   {  // the chunk's largest exponent of each token, its sum, and every step's distance from it
     const int t = threadIdx.x % kT, g = threadIdx.x / kT;
-    const float *ex = exponent + vb / kFewWords * kFewTokens + min(t, T - 1);
-    const float *sm = sum + vb / kFewWords * kFewTokens + min(t, T - 1);
+    const float *ex = exponent + vb / kFewWords * tpad + min(t0 + t, T - 1);
+    const float *sm = sum + vb / kFewWords * tpad + min(t0 + t, T - 1);
     float top = kNoExponent;
-    for (int i = g; i < steps; i += kRows) top = fmaxf(top, ex[i * kFewTokens]);
+    for (int i = g; i < steps; i += kRows) top = fmaxf(top, ex[i * tpad]);
     fold[threadIdx.x] = top;
     __syncthreads();
 #pragma unroll
@@ -656,51 +663,56 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
     __syncthreads();
     float s = 0.f;
     for (int i = g; i < steps; i += kRows) {
-      const float d = top - ex[i * kFewTokens];
+      const float d = top - ex[i * tpad];
       shifts[i * kT + t] = (uint8_t)fminf(d, 255.f);
-      if (slice == 0) s += sm[i * kFewTokens] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
+      if (slice == 0) s += sm[i * tpad] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
     }
     fold[threadIdx.x] = s;
     __syncthreads();
-    if (slice == 0 && g == 0 && t < T) {
+    if (slice == 0 && g == 0 && t0 + t < T) {
       for (int i = 1; i < kRows; ++i) s += fold[i * kT + t];
-      N[(chunk0 + chunk) * kFewTokens + t] = top;
-      S[(chunk0 + chunk) * kFewTokens + t] = s;
+      N[(int64_t)(chunk0 + chunk) * tpad + t0 + t] = top;
+      S[(int64_t)(chunk0 + chunk) * tpad + t0 + t] = s;
     }
   }
   uint32_t off[2 * NT];
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
     const int r = 8 * j + (lane >> 3);
-    off[j] = (uint32_t)min(r, T - 1) * (uint32_t)(2 * pitch) + (((lane & 7) ^ swizzle_rows(r)) << 4);
+    off[j] = (uint32_t)min(r, T - 1 - t0) * (uint32_t)(2 * pitch) + (((lane & 7) ^ swizzle_rows(r)) << 4);
   }
   f32x4 acc[4][NT];
   few_zero<NT>(acc);
   few_product<true, true, NT>(uniform(w + vb * D + 64 * slice), (uint32_t)D * 2u, words, (int64_t)kStep * D * 2,
-                        uniform(e + vb), off, wave, steps, lds + wave * kBytes, shifts, acc);
+                        uniform(e + (int64_t)t0 * pitch + vb), off, wave, steps, lds + wave * kBytes, shifts, acc);
   float *red = (float *)lds;
   few_put<NT>(acc, red);
   // 16 lanes a token, four columns each
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int t = i * 16 + (threadIdx.x >> 4), d = 4 * (threadIdx.x & 15);
-    if (t < T) *(f32x4 *)(part + ((int64_t)(chunk0 + chunk) * T + t) * D + 64 * slice + d) = few_sum<NT>(red, t, d);
+    if (t0 + t < T)
+      *(f32x4 *)(part + ((int64_t)(chunk0 + chunk) * T + t0 + t) * D + 64 * slice + d) = few_sum<NT>(red, t, d);
   }
 }
 
-// Notes a target past the vocabulary (T <= 64; the first wave).
+// Notes a target past the vocabulary (one workgroup of 256 threads).
 __device__ __forceinline__ void few_state(const int64_t *target, int T, int64_t V, uint32_t *state) {
-  const int lane = threadIdx.x;
-  if (lane >= 64) return;
-  const bool bad = lane < T && target[lane] >= V;
-  const uint64_t any = __ballot(bad);
-  if (lane == 0) state[0] = any ? 2u : 0u;
+  __shared__ int any;
+  if (threadIdx.x == 0) any = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int t = threadIdx.x; t < T; t += 256) bad |= target[t] >= V;
+  if (bad) any = 1;
+  __syncthreads();
+  if (threadIdx.x == 0) state[0] = any ? 2u : 0u;
 }
 
 // Loss and lse of one token a workgroup from the exponents and sums of all its words.
 __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ target, int T, int64_t V, int groups,
                                                   const float *__restrict__ exponent, const float *__restrict__ sum,
-                                                  const float *__restrict__ target_logit, uint32_t *__restrict__ state,
+                                                  int tpad, const float *__restrict__ target_logit,
+                                                  uint32_t *__restrict__ state,
                                                   float *__restrict__ loss, float *__restrict__ lse) {
   __shared__ float fold[256];
   const int t = blockIdx.x, tid = threadIdx.x;
@@ -711,7 +723,7 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
     return;
   }
   float top = kNoExponent;
-  for (int i = tid; i < groups; i += 256) top = fmaxf(top, exponent[i * kFewTokens + t]);
+  for (int i = tid; i < groups; i += 256) top = fmaxf(top, exponent[(int64_t)i * tpad + t]);
   fold[tid] = top;
   __syncthreads();
   for (int d = 128; d > 0; d >>= 1) {
@@ -722,7 +734,7 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
   __syncthreads();
   float s = 0.f;
   for (int i = tid; i < groups; i += 256)
-    s += sum[i * kFewTokens + t] * __builtin_amdgcn_exp2f(-fminf(top - exponent[i * kFewTokens + t], 300.f));
+    s += sum[(int64_t)i * tpad + t] * __builtin_amdgcn_exp2f(-fminf(top - exponent[(int64_t)i * tpad + t], 300.f));
   fold[tid] = s;
   __syncthreads();
   for (int d = 128; d > 0; d >>= 1) {
@@ -740,7 +752,7 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
 // chunk a thread, so that the chunks' sums (from the caches of other XCDs) arrive in few round trips.
 __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ target, int T, int64_t V, int D,
                                                   int chunks, const float *__restrict__ N, const float *__restrict__ S,
-                                                  const float *__restrict__ target_logit,
+                                                  int tpad, const float *__restrict__ target_logit,
                                                   const uint16_t *__restrict__ w, QWeight q, Codebook cb,
                                                   const float *__restrict__ weight, float scale,
                                                   const float *__restrict__ part, uint32_t *__restrict__ state,
@@ -761,11 +773,11 @@ __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ ta
   }
   // N and S: the chunks one a lane, every wave for itself
   float top = kNoExponent, s = 0.f;
-  for (int i = lane; i < chunks; i += 64) top = fmaxf(top, N[i * kFewTokens + t]);
+  for (int i = lane; i < chunks; i += 64) top = fmaxf(top, N[(int64_t)i * tpad + t]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
   for (int i = lane; i < chunks; i += 64)
-    s += S[i * kFewTokens + t] * __builtin_amdgcn_exp2f(-fminf(top - N[i * kFewTokens + t], 300.f));
+    s += S[(int64_t)i * tpad + t] * __builtin_amdgcn_exp2f(-fminf(top - N[(int64_t)i * tpad + t], 300.f));
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
   f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
@@ -778,7 +790,7 @@ __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ ta
       const int i = min(i0 + 4 * j, chunks - 1);
       x[j] = *(const f32x4 *)(p + (int64_t)i * T * D);
       z[j] = *(const f32x4 *)(p + (int64_t)i * T * D + 4);
-      f[j] = i0 + 4 * j < chunks ? __builtin_amdgcn_exp2f(-fminf(top - N[i * kFewTokens + t], 300.f)) : 0.f;
+      f[j] = i0 + 4 * j < chunks ? __builtin_amdgcn_exp2f(-fminf(top - N[(int64_t)i * tpad + t], 300.f)) : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -830,10 +842,12 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
   p.words = cdiv(cdiv(p.V, p.pieces), kTileV) * kTileV;
   p.pieces = cdiv(p.V, p.words);
   p.splits = p.split_words = 0;
+  p.tpad = cdiv(p.T, kFewTokens) * kFewTokens;
   const int64_t groups = cdiv(p.V, kFewWords), piece_steps = cdiv(std::min(p.words, p.V), kFewWords);
   if (p.grad) {
     // about one workgroup a CU, at least a step for each of its waves, at most kFewChunk steps
-    const int64_t chunks = std::max<int64_t>(1, std::min(256 / (p.D / 64), cdiv(piece_steps, 4)));
+    const int64_t chunks =
+        std::max<int64_t>(1, std::min(256 / (p.D / 64 * (p.tpad / kFewTokens)), cdiv(piece_steps, 4)));
     const int64_t steps = std::min<int64_t>(kFewChunk, cdiv(piece_steps, chunks));
     p.split_words = steps * kFewWords;
     for (int64_t v0 = 0; v0 < p.V; v0 += p.words) p.splits += cdiv(std::min(p.words, p.V - v0), p.split_words);
@@ -844,11 +858,11 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
     off += align256(bytes);
     return at;
   };
-  p.off_logit = take(kFewTokens * 4);
-  p.off_exponent = take((size_t)groups * kFewTokens * 4);
-  p.off_sum = take((size_t)groups * kFewTokens * 4);
-  p.off_n = take((size_t)p.splits * kFewTokens * 4);
-  p.off_s = take((size_t)p.splits * kFewTokens * 4);
+  p.off_logit = take((size_t)p.tpad * 4);
+  p.off_exponent = take((size_t)groups * p.tpad * 4);
+  p.off_sum = take((size_t)groups * p.tpad * 4);
+  p.off_n = take((size_t)p.splits * p.tpad * 4);
+  p.off_s = take((size_t)p.splits * p.tpad * 4);
   p.off_e = p.grad ? take((size_t)p.T * groups * kFewWords * 2) : 0;
   p.off_part = p.grad ? take((size_t)p.splits * p.T * p.D * 4) : 0;
   p.off_w = p.packed ? take((size_t)p.words * p.D * 2) : 0;
@@ -884,7 +898,8 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
   float *part = (float *)(ws + p.off_part);
   uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
   uint16_t *wp = (uint16_t *)(ws + p.off_w);
-  const int T = (int)p.T, D = (int)p.D, groups = (int)cdiv(p.V, kFewWords);
+  const int T = (int)p.T, D = (int)p.D, groups = (int)cdiv(p.V, kFewWords), tpad = (int)p.tpad;
+  const int token_groups = tpad / kFewTokens;
   const int64_t pitch = (int64_t)groups * kFewWords;
   int chunk0 = 0;
   for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
@@ -894,24 +909,42 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
       const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
       if (err != hipSuccess) return err;
     }
-    few_logits<NT><<<(unsigned)cdiv(nv, kFewWords), kFewThreads, 0, st>>>(h, piece, target, T, v0, nv, D, e, pitch,
-                                                                        exponent, sum, logit);
+    few_logits<NT><<<(unsigned)(cdiv(nv, kFewWords) * token_groups), kFewThreads, 0, st>>>(
+        h, piece, target, T, v0, nv, D, e, pitch, exponent, sum, tpad, logit);
     if (!p.grad) continue;
     const int chunks = (int)cdiv(nv, p.split_words);
-    const int64_t g0 = v0 / kFewWords * kFewTokens;
-    few_grad<NT><<<(unsigned)(chunks * (D / 64)), kFewThreads, 0, st>>>(e + v0, pitch, piece, T, nv, D,
-                                                                      (int)(p.split_words / kFewWords), chunk0,
-                                                                      exponent + g0, sum + g0, N, S, part);
+    const int64_t g0 = v0 / kFewWords * tpad;
+    few_grad<NT><<<(unsigned)(chunks * token_groups * (D / 64)), kFewThreads, 0, st>>>(
+        e + v0, pitch, piece, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0, tpad, N, S,
+        part);
     chunk0 += chunks;
   }
   if (!p.grad) {
-    few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, logit, state, loss, lse);
+    few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, tpad, logit, state, loss, lse);
     return hipGetLastError();
   }
-  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, logit, w,
-                                                                       q ? *q : QWeight{}, cb, weight, scale, part,
+  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, tpad, logit,
+                                                                       w, q ? *q : QWeight{}, cb, weight, scale, part,
                                                                        state, loss, lse, grad);
   return hipGetLastError();
+}
+
+// Whether the streamed form is taken: always up to 64 tokens, and where its time, estimated in us from
+// runs of both forms at 66 to 2048 tokens, 256 to 4096 columns and 300 to 32000 words, is below that of
+// the tiles.  A stream's unit is 64 tokens, 64 columns, 4096 words; a workgroup of the logits costs about
+// 2.6 us besides.  The tiles have launches and first copies, the chain of a tile's steps, the sums of a
+// vocabulary spread over splits, and the operations.  Measured, with the gradient (tiles / streams): 256 x
+// 1024 x 4000 63 / 25 us, 1024 x 1024 x 4000 70 / 63, 512 x 1024 x 16000 80 / 108, 66 x 4096 x 16000
+// 122 / 95, 256 x 4096 x 16000 135 / 173; the loss alone: 512 x 4096 x 4000 73 / 35, 1024 x 4096 x 4000
+// 75 / 67, 200 x 1024 x 32000 31 / 55.
+static bool few_pays(int64_t T, int64_t V, int64_t D, bool grad) {
+  if (V > kFewMaxWords || T > kHeadMaxTokens) return false;
+  if (T <= kFewTokens) return true;
+  const double groups = (double)cdiv(T, kFewTokens), units = groups * (D / 64) * (V / 4096.0);
+  const double blocks = groups * cdiv(V, kFewWords), ops = 2.0 * T * V * D;
+  const double few = grad ? 18 + 0.155 * units + 0.010 * blocks : 12 + 0.055 * units + 0.010 * blocks;
+  const double tile = grad ? 34 + 0.0155 * D + 0.0008 * V + ops / 1.0e9 : 16 + std::max(0.0145 * D, ops / 1.35e9);
+  return few < tile;
 }
 
 HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
@@ -921,7 +954,7 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.D = D;
   p.grad = grad;
   p.packed = packed;
-  p.few = T <= kFewTokens && V <= kFewMaxWords;
+  p.few = few_pays(T, V, D, grad);
   p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
   p.tpad = cdiv(p.chunk, kTileT) * kTileT;
   // Words of a piece: 128 MB of e (grad) and 64 MB of decoded weight (packed).  A larger piece leaves less of

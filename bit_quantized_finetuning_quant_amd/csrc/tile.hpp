@@ -260,27 +260,45 @@ __device__ __forceinline__ int place_at(const Tile &tile, int nleft, int ntoken)
 }
 
 // Splits of the contraction (`length` long, in ranges of whole 128s) of `tiles` output tiles: the count
-// with the least rounds of 256 workgroups times range, where a range costs about 256 more (its first
-// copies and its result) and every partial tile about 2 (256 KB written and read again).  At most
-// kMaxSlots workgroups unless the tiles alone are more.
-constexpr int kMaxSplits = 8, kMaxSlots = 512;
+// with the least rounds of 256 workgroups times range, where a range costs about 512 more (its first
+// copies and its result: 12 us against 1.4 us a step) and every partial tile about 2 (256 KB written and
+// read again).  At most kMaxSlots workgroups unless the tiles alone are more.
+constexpr int kMaxSplits = 64, kMaxSlots = 512;
 struct Split {
   int count, range;
 };
-__host__ __device__ inline Split choose_split(int tiles, int length) {
-  Split best{1, (length + 127) / 128 * 128};
-  int64_t cost = (int64_t)(tiles + 255) / 256 * (best.range + 256) + 2 * tiles;
-  for (int s = 2; s <= kMaxSplits; ++s) {
-    const int range = ((length + s - 1) / s + 127) / 128 * 128;
-    if (tiles * s > kMaxSlots || range < 256) break;
-    const int n = (length + range - 1) / range;  // ranges that are not empty
-    const int64_t c = (int64_t)(tiles * n + 255) / 256 * (range + 256) + 2 * tiles * n;
+// The cost of `s` splits, 2^40 and more where they are not possible; their count without empty ranges and the range.
+__host__ __device__ inline int64_t split_cost(int tiles, int length, int s, Split &out) {
+  const int range = ((length + s - 1) / s + 127) / 128 * 128;
+  const int n = (length + range - 1) / range;
+  out = Split{n, range};
+  if (s > 1 && (tiles * n > kMaxSlots || range < 256)) return (int64_t)1 << 40;
+  return (int64_t)((tiles * n + 255) / 256) * (range + 512) + 2 * tiles * n;
+}
+inline Split choose_split(int tiles, int length) {
+  Split best{}, one{};
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= kMaxSplits; ++s) {
+    const int64_t c = split_cost(tiles, length, s, one);
     if (c < cost) {
       cost = c;
-      best = Split{n, range};
+      best = one;
     }
   }
   return best;
+}
+// The same on the device, one count a lane.
+__device__ __forceinline__ Split split_of(int tiles, int length) {
+  Split mine;
+  const int lane = threadIdx.x & 63;
+  int64_t key = split_cost(tiles, length, lane + 1, mine) * 64 + lane;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t other = ((int64_t)__shfl_xor((int)(key >> 32), d) << 32) | (uint32_t)__shfl_xor((int)key, d);
+    key = other < key ? other : key;
+  }
+  const int s = (int)(key & 63);
+  return Split{scalar(__shfl(mine.count, s)), scalar(__shfl(mine.range, s))};
 }
 
 // Workgroups (and partial tiles) that `nleft` by up to `ntoken` tiles need at most.

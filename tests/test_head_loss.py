@@ -98,7 +98,11 @@ SHAPES = [(1, 64, 1), (1, 64, 2), (1, 128, 300), (2, 64, 255), (3, 192, 257), (1
           # up to 64 tokens: one to four tiles of 16, one to many chunks of words, steps shared unevenly by the waves
           (1, 4096, 32003), (5, 8192, 3000), (16, 64, 16385), (17, 1024, 8193), (32, 2048, 641), (33, 64, 100001),
           (48, 576, 4097), (64, 1088, 20001), (2, 65536, 300),
-          # lists of tokens and folds inside the products, and on either side of where they end
+          # the 256 x 256 tiles: lists of tokens and folds inside the products or in kernels of their own, the
+          # last column tile of 64, one and many splits of the contraction
+          (400, 4096, 8190), (512, 4096, 8192), (513, 4096, 8192), (520, 4032, 8193), (300, 1024, 33000),
+          (257, 4096, 17001), (512, 704, 31999), (1100, 512, 9000), (2050, 192, 9001), (1300, 320, 12345),
+          (2048, 256, 8192), (700, 128, 70000), (2300, 64, 16390),
           (511, 64, 8192), (512, 128, 8193), (513, 64, 8192), (514, 128, 8193), (512, 192, 100), (70, 4096, 419)]
 
 
@@ -178,17 +182,17 @@ def test_exponents_of_tiles_and_pieces(order, T):
 
 
 @gpu
-@pytest.mark.parametrize("T", [64, 130])
+@pytest.mark.parametrize("T", [64, 130, 600])
 def test_sure_tokens_keep_relative_precision(T):
-    """Losses down to about 1e-8 (3000 words 26 below the target): loss = log1p(others / e_y) and 1 - p_y are formed without a difference."""
+    """Losses down to about 1e-8 (3000 words 26 below the target, at 20003 words 1e-7): loss = log1p(others / e_y) and 1 - p_y are formed without a difference."""
     torch = torch_mod()
-    D, V = 256, 3000
+    D, V = 256, 3000 if T < 550 else 20003  # streams, tiles
     announce(f"head loss of sure tokens T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=12, std=0.02, masked=0.0))
     lean = torch.linspace(5, 28, T, device="cuda")[:, None] / w[y].float().square().sum(1, keepdim=True)
     h = (lean * w[y].float()).bfloat16()
     loss, _, _ = _check(h, w, w, y)
-    assert float(loss.min()) < 1e-7 and float(loss.min()) > 0
+    assert float(loss.min()) < 1e-6 and float(loss.min()) > 0
 
 
 @gpu
@@ -196,7 +200,7 @@ def test_sure_tokens_keep_relative_precision(T):
 def test_tokens_without_loss(T):
     """Negative targets: zeros, whatever the rows hold; a call without any loss; all rows but one."""
     torch = torch_mod()
-    D, V = 128, 900
+    D, V = 128, 900 if T < 550 else 20003  # streams, tiles
     announce(f"head loss with masked tokens T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=13, std=0.3, masked=0.5))
     y[T // 2:T - 5] = -1
@@ -217,12 +221,12 @@ def test_tokens_without_loss(T):
 
 
 @gpu
-@pytest.mark.parametrize("T", [40, 70])
+@pytest.mark.parametrize("T", [40, 70, 600])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
 def test_values_past_the_range(value, T):
     """NaN, Inf or an overflow in one token's row: NaN for that token, the others as they were."""
     torch = torch_mod()
-    D, V = 128, 1000
+    D, V = 128, 1000 if T < 550 else 20003  # streams, tiles
     announce(f"head loss with {value} in a row T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=14, std=0.3, masked=0.0))
     want = qlora.head_loss(h, w, y)
@@ -239,7 +243,7 @@ def test_values_past_the_range(value, T):
 @pytest.mark.parametrize("T", [63, 70, 600])
 def test_target_past_the_vocabulary(T):
     torch = torch_mod()
-    D, V = 128, 1000
+    D, V = 128, 1000 if T < 550 else 20003  # streams, tiles
     announce(f"head loss with a target past the vocabulary T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=15, masked=0.2))
     ws = qlora.head_loss_workspace(T, V, D)
@@ -286,11 +290,11 @@ def test_gradient_against_differences():
 
 
 @gpu
-@pytest.mark.parametrize("T", [10, 300])
+@pytest.mark.parametrize("T", [10, 300, 600])
 def test_captured_call_replays_equal_eager(T):
     """Two captured calls share a workspace; replays after eager work equal the eager results."""
     torch = torch_mod()
-    D, V = 256, 2000
+    D, V = 256, 2000 if T < 550 else 20003  # streams, tiles
     announce(f"head loss under graph capture T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=17, std=0.2))
     ws = qlora.head_loss_workspace(T, V, D)
@@ -326,10 +330,10 @@ def test_captured_call_replays_equal_eager(T):
 
 
 @gpu
-@pytest.mark.parametrize("T", [9, 500])
+@pytest.mark.parametrize("T", [9, 500, 600])
 def test_two_streams_at_once_and_repeats_are_identical(T):
     torch = torch_mod()
-    D, V = 512, 6000
+    D, V = 512, 6000 if T < 550 else 20003  # streams, tiles
     announce(f"head loss on two streams T={T}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=18, std=0.1))
     want = qlora.head_loss(h, w, y)
