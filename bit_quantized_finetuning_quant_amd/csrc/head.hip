@@ -655,6 +655,7 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
     const float *ex = exponent + vb / kFewWords * tpad + min(t0 + t, T - 1);
     const float *sm = sum + vb / kFewWords * tpad + min(t0 + t, T - 1);
     float top = kNoExponent;
+#pragma unroll 8
     for (int i = g; i < steps; i += kRows) top = fmaxf(top, ex[i * tpad]);
     fold[threadIdx.x] = top;
     __syncthreads();
@@ -662,6 +663,7 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
     for (int i = 0; i < kRows; ++i) top = fmaxf(top, fold[i * kT + t]);
     __syncthreads();
     float s = 0.f;
+#pragma unroll 8
     for (int i = g; i < steps; i += kRows) {
       const float d = top - ex[i * tpad];
       shifts[i * kT + t] = (uint8_t)fminf(d, 255.f);

@@ -161,10 +161,16 @@ def nf4_codebook():
 
 
 # ------------------------------------------------------------- device helpers
-def _torch():
-    import torch
+_TORCH = None
 
-    return torch
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(stream=None) -> int:
@@ -173,6 +179,21 @@ def _stream(stream=None) -> int:
     torch = _torch()
     # the current stream's handle without a Stream object around it (3 us of every call)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _stream_on(dev, stream=None) -> int:
+    """The stream's handle for a call on tensors of `dev`, which must be the current device (a launch goes
+    to the current one, whatever device the pointers belong to)."""
+    torch = _torch()
+    current = torch.cuda.current_device()
+    if dev.index != current:
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{current}: call it under "
+                         f"torch.cuda.device({dev.index})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(current)
+    if stream.device != dev:
+        raise ValueError(f"the tensors are on {dev}, the stream on {stream.device}")
+    return int(stream.cuda_stream)
 
 
 def _ptr(t) -> int:
@@ -728,7 +749,7 @@ class Act8:
                    torch.empty((tokens, dim // 64), dtype=torch.float32, device=device))
 
     def struct(self) -> Act8Struct:
-        return Act8Struct(self.codes.shape[0], self.codes.shape[1], _ptr(self.codes), _ptr(self.scale))
+        return Act8Struct(*self.codes.shape, self.codes.data_ptr(), self.scale.data_ptr())
 
     def nbytes(self) -> int:
         return self.codes.numel() + 4 * self.scale.numel()
@@ -738,7 +759,7 @@ def _check_act8(a: Act8, chk):
     """(T, K) of a checkpoint whose tensors fit each other."""
     if a.codes.dim() != 2:
         raise ValueError("codes must be 2-D")
-    T, K = int(a.codes.shape[0]), int(a.codes.shape[1])
+    T, K = a.codes.shape
     if K % 64:
         raise ValueError(f"codes must have a multiple of 64 columns, not {K}")
     chk.i8(a.codes, "codes", (T, K))
@@ -751,7 +772,7 @@ def act8_write(x, out: Act8 = None, stream=None) -> Act8:
     absmax / 127, and the nearest codes."""
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
-    T, K = int(x.shape[0]), int(x.shape[1])
+    T, K = x.shape
     chk = _Args(x.device)
     chk.bf16(x, "x", (T, K))
     if out is not None and _check_act8(out, chk) != (T, K):
@@ -759,7 +780,7 @@ def act8_write(x, out: Act8 = None, stream=None) -> Act8:
     chk.done()
     a = out if out is not None else Act8.empty(T, K, x.device)
     st = a.struct()
-    _check(lib().qlora_act8_write(_ptr(x), ctypes.byref(st), _stream(stream)), "qlora_act8_write")
+    _check(lib().qlora_act8_write(x.data_ptr(), ctypes.byref(st), _stream_on(x.device, stream)), "qlora_act8_write")
     return a
 
 
@@ -773,7 +794,7 @@ def act8_read(a: Act8, out=None, stream=None):
     chk.done()
     y = out if out is not None else torch.empty((T, K), dtype=torch.bfloat16, device=a.codes.device)
     st = a.struct()
-    _check(lib().qlora_act8_read(ctypes.byref(st), _ptr(y), _stream(stream)), "qlora_act8_read")
+    _check(lib().qlora_act8_read(ctypes.byref(st), y.data_ptr(), _stream_on(y.device, stream)), "qlora_act8_read")
     return y
 
 
@@ -839,7 +860,7 @@ def linear_set_bwd_act8(dys, a: Act8, qs, A_set, Bs, scale: float, u, need_grad_
     sa = a.struct()
     _check(lib().qlora_linear_set_bwd_act8(_ptrs(dys), ctypes.byref(sa), count, st, _ptr(A_set), _ptrs(Bs), r,
                                            float(scale), _ptr(u), _ptr(grad_x), _ptr(grad_A_set), _ptrs(grad_Bs),
-                                           _ptr(ws), wsb, _stream(stream)), "qlora_linear_set_bwd_act8")
+                                           _ptr(ws), wsb, _stream_on(dev, stream)), "qlora_linear_set_bwd_act8")
     return grad_x, grad_A_set, grad_Bs
 
 
@@ -902,9 +923,10 @@ def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=N
     if packed:
         st = head.struct()
         _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), _ptr(target), _ptr(weight), float(scale),
-                                         _ptr(loss), _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream(stream)),
+                                         _ptr(loss), _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream_on(dev, stream)),
                "qlora_head_loss_nf4")
     else:
         _check(lib().qlora_head_loss(_ptr(h), T, _ptr(head), V, D, _ptr(target), _ptr(weight), float(scale), _ptr(loss),
-                                     _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream(stream)), "qlora_head_loss")
+                                     _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream_on(dev, stream)),
+               "qlora_head_loss")
     return loss, lse, grad_h
