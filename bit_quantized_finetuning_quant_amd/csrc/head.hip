@@ -9,13 +9,18 @@
 // gradient for W.  Per piece of the vocabulary:
 //
 //   head_logits   one 256 x 256 tile of l per workgroup; its epilogue takes,
-//                 per token and 128 words, the integer n = ceil(log2 e max l)
+//                 per token and 128 words, an integer n above log2 e max l
 //                 and writes e_tv = 2^(l log2 e - n) in bf16 and s = sum e
 //   head_fold     running N_t = max n and S_t = sum 2^(n - N) s over the
-//                 tiles, and the distance N - n of each tile as a byte
+//                 tiles, and the distance (N - n) / 64 of each tile, 0 to 3
 //   head_grad     G_td += sum_v 2^(n - N) e_tv W_vd: the factor of a tile is a
 //                 power of two, so it is one saturating subtraction from the
 //                 exponent field of the bf16 operand, exact
+//
+// n is one of 44 + 64 i: bf16 has the exponents of fp32, so e loses nothing by
+// lying up to 2^64 below 1, and the tiles of a token nearly always have the
+// same n (where the largest logits of all its tiles lie between -13.8 and
+// 30.5).  A workgroup of head_grad whose distances are all 0 subtracts nothing.
 //
 // and head_finish forms grad_h = c (G / S - (S - e_y) / S W_y).  So the
 // gradient needs the two products it cannot do without (4 T V D operations)
@@ -39,7 +44,8 @@ namespace qlora {
 namespace {
 
 constexpr int kStatV = 128;     // words that share one exponent n per token
-constexpr int kShiftV = 8192;   // words whose shift bytes a workgroup holds in LDS at a time
+constexpr int kMaxPiece = 32768;  // words of a piece: a range's distances fit 16 KB of LDS
+constexpr int kFoldV = 8192;    // words up to which the products fold the tiles themselves
 constexpr int64_t kFewMaxWords = (int64_t)1 << 20;
 constexpr float kLog2e = 1.44269502162933349609375f;    // fl32(log2 e)
 constexpr float kLn2 = 0.693147182464599609375f;        // fl32(ln 2), and the rest of it
@@ -139,6 +145,12 @@ __device__ __forceinline__ int list_tokens(const int64_t *target, int T, int64_t
 __device__ __forceinline__ float tile_exponent(float top) {
   return ceilf(fminf(fmaxf(top * kLog2e, -2.0f * kMaxExponent), 2.0f * kMaxExponent));
 }
+// The one of 44 + 64 i at or above m, and 2^(m - that).
+__device__ __forceinline__ float coarse_exponent(float m, float &factor) {
+  const float n = 64.0f * ceilf((m - 44.0f) * 0.015625f) + 44.0f;
+  factor = __builtin_ldexpf(1.0f, (int)(m - n));
+  return n;
+}
 // 2^(l log2 e - n).  log2 e is its fp32 value everywhere, 1.3e-8 of it too small, so that all exponentials
 // of a token belong to logits scaled by that much: 1.3e-8 of l - l_y in the loss.
 __device__ __forceinline__ float relative_exp(float l, float n) {
@@ -162,7 +174,10 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
     }
   top = fmaxf(top, __shfl_xor(top, 16));
   top = fmaxf(top, __shfl_xor(top, 32));
-  const float ex = !kTest || (vl & ~127) < nvt ? tile_exponent(top) : kNoExponent;
+  // the exponentials are formed next to 1, where they are exact to 2^-24, and moved from there
+  const float ex = tile_exponent(top);
+  float factor, n_tile = coarse_exponent(ex, factor);
+  if (kTest && (vl & ~127) >= nvt) n_tile = kNoExponent;
   float s = 0.f, ly = 0.f;
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
@@ -170,7 +185,7 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float l = acc[m][n][q];
-      p[q] = relative_exp(l, ex);
+      p[q] = relative_exp(l, ex) * factor;
       if (kTest) {
         const int v = vl + 16 * m + q;
         ly = v == y ? l : ly;
@@ -184,7 +199,7 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
   s += __shfl_xor(s, 16);
   s += __shfl_xor(s, 32);
   if (lane < 16 && on) {
-    *exponent = ex;
+    *exponent = n_tile;
     *sum = s;
   }
 }
@@ -238,7 +253,7 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
   }
   f32x4 acc[8][4];
   tile_zero(acc);
-  product<false, false>(o, D / kStep, lds, nullptr, acc);
+  product<false, false>(o, D / kStep, lds, nullptr, false, acc);
 
   // rows (words) of this lane: 128 wm + 16 m + 4 (lane / 16) + q
   const int vl = 128 * wm + 4 * (lane >> 4), nvt = last_v + 1;
@@ -283,10 +298,19 @@ __device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
   return r;
 }
 
+// (N - n) / 64, at most 3 (192 leaves nothing of a bf16 value up to 1).
+__device__ __forceinline__ int distance(float d) { return (int)fminf(d * 0.015625f, 3.0f); }
+// The distances of the tokens of four neighbouring lanes, two bits each, in all of them.
+__device__ __forceinline__ int pack_distances(int d) {
+  d <<= 2 * (threadIdx.x & 3);
+  d |= __shfl_xor(d, 1);
+  return d | __shfl_xor(d, 2);
+}
+
 // Folds the piece's tiles into the running exponent N and sum S of each token: 8 tokens and 32 lanes
-// along the tiles a workgroup, eight tiles of a lane in flight at once.  shift: N - n of each tile, at
-// most 255 (which leaves nothing of any bf16 value); factor: 2^(N before - N), for what the pieces
-// before have summed.  loss (nullptr: not yet, or not here): the piece is the last, N and S are final.
+// along the tiles a workgroup, eight tiles of a lane in flight at once.  shift [tile][tpad / 4]: the
+// distances of four tokens a byte (0 for tokens past the last); factor: 2^(N before - N), for what the
+// pieces before have summed.  loss (nullptr: not yet, or not here): the piece is the last, N and S are final.
 __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ exponent, const float *__restrict__ sum,
                                                  int64_t tpad, int tiles, bool first,
                                                  const uint32_t *__restrict__ state, float *__restrict__ N,
@@ -333,7 +357,10 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
       const int i = i0 + j * kLanes + g;
       const float d = top - ex[j];
       s += sm[j] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
-      if (shift && i < tiles) shift[i * tpad + t] = (uint8_t)fminf(d, 255.f);
+      if (shift) {
+        const int four = pack_distances((int)blockIdx.x * 8 + c < live ? distance(d) : 0);
+        if (i < tiles && (c & 3) == 0) shift[i * (tpad >> 2) + (int)blockIdx.x * 2 + (c >> 2)] = (uint8_t)four;
+      }
     }
   }
   part[g][c] = s;
@@ -357,7 +384,7 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
 // One tile (256 columns d, 256 tokens) of G over one range of the piece's words, see the top.  The tiles and their
 // splits follow from the tokens that carry a loss; `words` is the length of every piece but the last, so that the
 // ranges, and the tiles' places in part, are the same in all.  kFold: the piece is the only one and has at most
-// kShiftV words; the exponents are folded here, which spares the launch of head_fold (shift is then unused).  part: [split][tile][256 tokens][256 d] fp32, in units of
+// kFoldV words; the exponents are folded here, which spares the launch of head_fold (shift is then unused).  part: [split][tile][256 tokens][256 d] fp32, in units of
 // 2^N.
 template <bool kFold>
 __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restrict__ e, int64_t pitch,
@@ -368,7 +395,7 @@ __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restr
                                                          const float *__restrict__ factor, bool first,
                                                          float *__restrict__ part) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t shifts[kShiftV / kStatV * kTileT];
+  __shared__ __attribute__((aligned(16))) uint8_t shifts[kMaxPiece / kStatV * kTileT / 4];
   const int live = (int)state[1];
   const int ntoken = (live + kTileT - 1) / kTileT, tiles = nleft * ntoken;
   const Split split = split_of(tiles, words);
@@ -396,11 +423,12 @@ __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restr
   }
   f32x4 acc[8][4];
   tile_zero(acc);
-  for (int vb = first_word; vb < last_word; vb += kShiftV) {
-    const int n = min(kShiftV, last_word - vb);
+  if (first_word < last_word) {
+    const int groups = (last_word - first_word + kStatV - 1) / kStatV, g0 = first_word / kStatV;
+    int moved = 0;  // any distance of the tile's tokens
     if (kFold) {  // two threads a token
-      const float *ex = exponent + t0 + (threadIdx.x & 255);
-      const int half = threadIdx.x >> 8, all = (nv + kStatV - 1) / kStatV;
+      const int token = threadIdx.x & 255, half = threadIdx.x >> 8, all = (nv + kStatV - 1) / kStatV;
+      const float *ex = exponent + min(t0 + token, live - 1);
       float top = kNoExponent;
 #pragma unroll 8
       for (int i = half; i < all; i += 2) top = fmaxf(top, ex[i * tpad]);
@@ -408,21 +436,27 @@ __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restr
       fold[threadIdx.x] = top;
       __syncthreads();
       top = fmaxf(top, fold[threadIdx.x ^ 256]);
-      const int g0 = vb / kStatV;
+      for (int i = half; i < groups; i += 2) {
+        const int four = pack_distances(distance(top - ex[(g0 + i) * tpad]));
+        if ((token & 3) == 0) shifts[i * (kTileT / 4) + (token >> 2)] = (uint8_t)four;
+        moved |= four;
+      }
+    } else {  // head_fold's; a group's bytes of the tile's tokens are 16 words
+      const uint8_t *src = shift + (int64_t)g0 * (tpad >> 2) + (t0 >> 2);
 #pragma unroll 8
-      for (int i = half; i < (n + kStatV - 1) / kStatV; i += 2)
-        shifts[i * kTileT + (threadIdx.x & 255)] = (uint8_t)fminf(top - ex[(g0 + i) * tpad], 255.f);
-    } else {
-      // the tile's shift bytes (tpad is a multiple of 256, so whole words of four tokens)
-      const uint8_t *src = shift + (int64_t)(vb / kStatV) * tpad + t0;
-      for (int i = threadIdx.x; i < (n + kStatV - 1) / kStatV * (kTileT / 4); i += kThreads)
-        ((uint32_t *)shifts)[i] = *(const uint32_t *)(src + (i >> 6) * tpad + 4 * (i & 63));
+      for (int i = threadIdx.x; i < groups * 16; i += kThreads) {
+        int four = *(const int *)(src + (i >> 4) * (tpad >> 2) + 4 * (i & 15));
+        const int bytes = (live - t0 + 3) / 4 - 4 * (i & 15);  // the others are not written
+        if (bytes < 4) four = bytes > 0 ? four & (int)(0xFFFFFFFFu >> (32 - 8 * bytes)) : 0;
+        ((int *)shifts)[i] = four;
+        moved |= four;
+      }
     }
-    __syncthreads();
-    o.left = uniform(w + (int64_t)vb * D + d0);
-    o.right = uniform(e + (int64_t)t0 * pitch + vb);
-    o.left_rows = n;
-    product<true, true>(o, (n + kStep - 1) / kStep, lds, shifts, acc);
+    const bool scaled = scalar(__syncthreads_or(moved)) != 0;
+    o.left = uniform(w + (int64_t)first_word * D + d0);
+    o.right = uniform(e + (int64_t)t0 * pitch + first_word);
+    o.left_rows = last_word - first_word;
+    product<true, true>(o, (last_word - first_word + kStep - 1) / kStep, lds, shifts, scaled, acc);
   }
   float *out = part + (int64_t)slot * (kTileT * kTileV);
 #pragma unroll
@@ -970,6 +1004,7 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
     return plan_few(p, vc);
   }
   vc = std::min(vc, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
+  if (grad) vc = std::min<int64_t>(vc, kMaxPiece);
   if (grad) vc = std::min(vc, std::max<int64_t>(budget / p.tpad / kTileV * kTileV, 8 * kTileV));
   if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
   p.pieces = cdiv(V, vc);
@@ -992,7 +1027,7 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.off_factor = take((size_t)p.chunk * 4);
   p.off_exponent = take((size_t)stat * 4);
   p.off_sum = take((size_t)stat * 4);
-  p.off_shift = grad ? take((size_t)stat) : 0;
+  p.off_shift = grad ? take((size_t)stat / 4) : 0;
   p.off_e = grad ? take((size_t)p.chunk * p.words * 2) : 0;
   p.off_part = grad ? take((size_t)p.splits * kTileT * kTileV * 4) : 0;
   p.off_w = packed ? take((size_t)p.words * D * 2) : 0;
@@ -1022,7 +1057,7 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
     const int64_t *yc = target + c0;
     float *lc = loss + c0, *ec = lse ? lse + c0 : nullptr;
     const bool list = p.T <= kThreads;                            // head_logits lists the tokens itself
-    const bool fold = p.grad && p.pieces == 1 && words <= kShiftV;  // head_grad and head_finish fold the tiles themselves
+    const bool fold = p.grad && p.pieces == 1 && words <= kFoldV;  // head_grad and head_finish fold the tiles themselves
     if (!list) head_scan<<<1, 1024, 0, st>>>(yc, T, p.V, c0 == 0, rows, place, state, lc, ec);
     for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
       const int nv = (int)std::min(p.words, p.V - v0), nleft = (int)cdiv(nv, kTileV);

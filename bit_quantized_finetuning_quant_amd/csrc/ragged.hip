@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kThreads, 2) void ragged_tiles(const uint16_t *__re
       o.left = uniform(wp + (int64_t)a * K + d0);
       o.right = uniform(dyp + (int64_t)t0 * rows + a);
       o.left_rows = b - a;
-      product<true, false>(o, (b - a) / kStep, lds, nullptr, acc);
+      product<true, false>(o, (b - a) / kStep, lds, nullptr, false, acc);
     }
     if (half == 0 && a < b) {
 #pragma unroll

@@ -168,11 +168,26 @@ __device__ __forceinline__ void multiply(const u32x4 (&a)[4], const u32x4 (&b)[4
   __builtin_amdgcn_s_setprio(0);
 }
 
+// The 256 tokens' rows of a stage times 2^(-64 d), a token a thread (the first 256); d: two bits a token.
+__device__ __forceinline__ void scale_tokens(char *stage, const uint8_t *distances) {
+  const int r = threadIdx.x;
+  const uint32_t d = (distances[r >> 2] >> (2 * (r & 3))) & 3u;
+  if (d == 0) return;
+  u32x4 *row = (u32x4 *)(stage + 2 * kUnit + r * 128);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    u32x4 v = row[c];
+    scale_down(v, d * 0x20002000u);
+    row[c] = v;
+  }
+}
+
 // acc[m][n][q] of lane l: left row 128 wm + 16 m + 4 (l/16) + q, token 64 wn + 16 n + l%16.
-// kScale: the tokens' operand holds values >= 0, multiplied by 2^-shift; shifts: a byte per token and two steps,
-// [steps / 2][256].
+// kScale: the tokens' operand holds values >= 0, multiplied by 2^(-64 d); shifts: d of 0 to 3 per token and two steps,
+// four neighbouring tokens a byte, [steps / 2][64]; scaled: whether any of them is not 0.  (Scaled in the
+// fragments' registers, every step paid for it: 859 against 820 us for 2048 tokens by 4096 by 32000.)
 template <bool kTrans, bool kScale>
-__device__ __forceinline__ void product(const Operands &o, int steps, char *lds, const uint8_t *shifts,
+__device__ __forceinline__ void product(const Operands &o, int steps, char *lds, const uint8_t *shifts, bool scaled,
                                         f32x4 (&acc)[8][4]) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -189,25 +204,17 @@ __device__ __forceinline__ void product(const Operands &o, int steps, char *lds,
   u32x4 a0[4], a1[4], b0[4], b1[4];
   for (int k = 0; k < steps; ++k) {
     char *stage = lds + (k & 1) * kStage, *next = lds + ((k + 1) & 1) * kStage;
-    // phase 0: rows 0..63
-    uint32_t shift[4];
-    if (kScale) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        shift[n] = (uint32_t)shifts[(k >> 1) * kTileT + 64 * wn + 16 * n + (lane & 15)] * 0x00800080u;
+    if (kScale && scaled) {  // a phase of its own, rarely taken: the first group scales the tokens' tile in place
+      if (!late) scale_tokens(stage, shifts + (k >> 1) * (kTileT / 4));
+      TILE_WAIT_LDS();
+      barrier();
     }
+    // phase 0: rows 0..63
     read_right(stage, 0, wn, lane, b0);
     read_left<kTrans>(stage, 0, 0, wm, lane, a0);
     read_right(stage, 1, wn, lane, b1);
     read_left<kTrans>(stage, 0, 1, wm, lane, a1);
     copy_left<kTrans>(o, 1, k + 1, steps, next, wave, lane);
-    if (kScale) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        scale_down(b0[n], shift[n]);
-        scale_down(b1[n], shift[n]);
-      }
-    }
     TILE_WAIT_LDS();
     TILE_WAIT_VM(8);
     barrier();

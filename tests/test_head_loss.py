@@ -161,7 +161,7 @@ def test_packed_head_in_pieces_by_size():
 
 
 @gpu
-@pytest.mark.parametrize("T", [15, 40, 260])
+@pytest.mark.parametrize("T", [15, 40, 260, 600])
 @pytest.mark.parametrize("order", ["rising", "falling", "far"])
 def test_exponents_of_tiles_and_pieces(order, T):
     """Logits whose largest value moves by hundreds between the tiles and the pieces: what a tile
