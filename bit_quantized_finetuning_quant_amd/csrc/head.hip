@@ -1076,7 +1076,7 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
                                                         ec);
       if (!p.grad) continue;
       const auto product = fold ? head_grad<true> : head_grad<false>;
-      product<<<(unsigned)split_slots(nd, ntoken, words), kThreads, 0, st>>>(
+      product<<<(unsigned)p.splits, kThreads, 0, st>>>(  // enough for any number of live tokens
           e, p.words, piece, nv, words, D, nd, state, shift, exponent, p.tpad, factor, v0 == 0, part);
     }
     if (!p.grad) continue;

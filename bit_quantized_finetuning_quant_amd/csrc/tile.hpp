@@ -287,6 +287,7 @@ inline Split choose_split(int tiles, int length) {
   int64_t cost = INT64_MAX;
   for (int s = 1; s <= kMaxSplits; ++s) {
     const int64_t c = split_cost(tiles, length, s, one);
+    if (c >= (int64_t)1 << 40) break;  // nor are more splits possible
     if (c < cost) {
       cost = c;
       best = one;
