@@ -21,6 +21,7 @@
 // the result is deterministic) and writes the scaled output.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -184,15 +185,19 @@ struct LoraProblem {
   void *out;
   int64_t ldo;  // row stride of out (Nc unless the product fills columns of a wider matrix)
   float *part;
-  uint16_t *out_mid, *out_low;  // bf16 outputs: also what their rounding leaves (nullptr: not wanted)
-  // grad_A from a checkpoint: Q holds its codes, P has the remainders P_mid, P_low
+};
+
+// A product of the backward pass from an 8-bit checkpoint.
+struct Act8Problem : LoraProblem {
+  uint16_t *out_mid, *out_low;  // v: also what its bf16 rounding leaves
+  // grad_A: Q holds the checkpoint's codes, P has the remainders P_mid, P_low
   const uint16_t *P_mid, *P_low;
   const float *code_scale;  // [Kc x Nc / 64]
 };
 
 // The finished tile: scaled into the output, or as the partial tile of its split.
-template <bool kBf16Out>
-__device__ __forceinline__ void put_tile(const LoraProblem &pr, int64_t tile, int s, const f32x16 &acc) {
+template <bool kBf16Out, class Problem>
+__device__ __forceinline__ void put_tile(const Problem &pr, int64_t tile, int s, const f32x16 &acc) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const int64_t m0 = (tile % pr.tiles_m) * LT, n0 = (tile / pr.tiles_m) * LT;
@@ -204,7 +209,8 @@ __device__ __forceinline__ void put_tile(const LoraProblem &pr, int64_t tile, in
       const int64_t gm = m0 + wm * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3), gn = n0 + col;
       if (gm < pr.M && gn < pr.Nc) {
         emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn, acc[q] * pr.scale);
-        if (kBf16Out && pr.out_mid) emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn, acc[q] * pr.scale);
+        if constexpr (kBf16Out && std::is_same_v<Problem, Act8Problem>)
+          emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn, acc[q] * pr.scale);
       }
     }
     return;
@@ -215,8 +221,8 @@ __device__ __forceinline__ void put_tile(const LoraProblem &pr, int64_t tile, in
   for (int q = 0; q < 16; ++q) mine[(wm * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * LT + col] = acc[q];
 }
 
-template <bool kAT, bool kBT, bool kBf16Out, int kGroupSteps>
-__device__ __forceinline__ void lora_tile(const LoraProblem &pr, int64_t tile, int s, uint16_t (*sA)[LT * LLD],
+template <bool kAT, bool kBT, bool kBf16Out, int kGroupSteps, class Problem>
+__device__ __forceinline__ void lora_tile(const Problem &pr, int64_t tile, int s, uint16_t (*sA)[LT * LLD],
                                           uint16_t (*sB)[LT * LLD]) {
   const int64_t m0 = (tile % pr.tiles_m) * LT, n0 = (tile / pr.tiles_m) * LT;
   const int64_t kb = (int64_t)s * pr.chunk, ke = min(pr.Kc, kb + pr.chunk);
@@ -255,8 +261,8 @@ __global__ __launch_bounds__(256) void lora_gemm(LoraProblem a, LoraProblem b, i
 // out = scale * (sum over splits, in split order) of the partial tiles; one
 // thread per 4 consecutive columns of a tile row.  Quads below `first` belong
 // to problem a, the rest to problem b.
-template <bool kBf16Out>
-__device__ __forceinline__ void reduce_quad(const LoraProblem &pr, int64_t qd) {
+template <bool kBf16Out, class Problem>
+__device__ __forceinline__ void reduce_quad(const Problem &pr, int64_t qd) {
   const int64_t tile = qd / (LT * LT / 4);
   const int local = (int)(qd % (LT * LT / 4)) * 4;
   const int64_t gm = (tile % pr.tiles_m) * LT + local / LT;
@@ -282,7 +288,8 @@ __device__ __forceinline__ void reduce_quad(const LoraProblem &pr, int64_t qd) {
   for (int e = 0; e < 4; ++e)
     if (gn + e < pr.Nc) {
       emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn + e, acc[e] * pr.scale);
-      if (kBf16Out && pr.out_mid) emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn + e, acc[e] * pr.scale);
+      if constexpr (kBf16Out && std::is_same_v<Problem, Act8Problem>)
+        emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn + e, acc[e] * pr.scale);
     }
 }
 
@@ -328,7 +335,7 @@ __device__ __forceinline__ void store_codes(const CodeRegs &t, uint16_t *lds, in
 }
 
 template <bool kFull>
-__device__ __forceinline__ void act8_body(const LoraProblem &pr, int64_t kb, int64_t ke, int64_t m0, int64_t n0,
+__device__ __forceinline__ void act8_body(const Act8Problem &pr, int64_t kb, int64_t ke, int64_t m0, int64_t n0,
                                           uint16_t (*s)[LT * LLD], f32x16 &acc) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
@@ -373,7 +380,7 @@ __device__ __forceinline__ void act8_body(const LoraProblem &pr, int64_t kb, int
   }
 }
 
-__device__ __forceinline__ void act8_tile(const LoraProblem &pr, int64_t tile, int s, uint16_t (*lds)[LT * LLD]) {
+__device__ __forceinline__ void act8_tile(const Act8Problem &pr, int64_t tile, int s, uint16_t (*lds)[LT * LLD]) {
   const int64_t m0 = (tile % pr.tiles_m) * LT, n0 = (tile / pr.tiles_m) * LT;
   const int64_t kb = (int64_t)s * pr.chunk, ke = min(pr.Kc, kb + pr.chunk);
   f32x16 acc;
@@ -391,7 +398,7 @@ __device__ __forceinline__ void act8_tile(const LoraProblem &pr, int64_t tile, i
 // first[i + 1] - 1.
 constexpr int kMaxBatch = kMaxSetMembers + 1;
 struct LoraBatch {
-  LoraProblem pr[kMaxBatch];
+  Act8Problem pr[kMaxBatch];
   int64_t first[kMaxBatch + 1];
   int count;
 };
@@ -476,9 +483,6 @@ LoraProblem make_problem(const uint16_t *P, int64_t ldp, const uint16_t *Q, int6
   pr.out = out;
   pr.ldo = Nc;
   pr.part = part;
-  pr.out_mid = pr.out_low = nullptr;
-  pr.P_mid = pr.P_low = nullptr;
-  pr.code_scale = nullptr;
   return pr;
 }
 
@@ -593,7 +597,7 @@ hipError_t launch_lora_set_grads(const uint16_t *v_set, const uint16_t *x, const
   return launch_list<true, true, false>(pr, count + 1, st);
 }
 
-static LoraBatch make_batch(const LoraProblem *pr, int count, int64_t (*size)(const LoraProblem &)) {
+static LoraBatch make_batch(const Act8Problem *pr, int count, int64_t (*size)(const LoraProblem &)) {
   LoraBatch b{};
   b.count = count;
   for (int i = 0; i < count; ++i) {
@@ -604,7 +608,7 @@ static LoraBatch make_batch(const LoraProblem *pr, int count, int64_t (*size)(co
 }
 
 template <bool kBf16Out>
-static hipError_t reduce_batch(const LoraProblem *pr, int count, hipStream_t st) {
+static hipError_t reduce_batch(const Act8Problem *pr, int count, hipStream_t st) {
   const LoraBatch b = make_batch(pr, count, problem_quads);
   if (b.first[count] > 0)
     lora_batch_reduce<kBf16Out><<<(unsigned)std::min<int64_t>(cdiv(b.first[count], 256), 2048), 256, 0, st>>>(b);
@@ -615,10 +619,10 @@ static hipError_t reduce_batch(const LoraProblem *pr, int count, hipStream_t st)
 hipError_t launch_lora_set_v_exact(const uint16_t *const *dy, const uint16_t *const *B, const int64_t *N, int count,
                                    int64_t T, int r, uint16_t *v, float *part, hipStream_t st) {
   const int64_t plane = T * count * r;
-  LoraProblem pr[kMaxSetMembers];
+  Act8Problem pr[kMaxSetMembers] = {};
   size_t off = 0;
   for (int i = 0; i < count; ++i) {
-    pr[i] = make_problem(dy[i], N[i], B[i], r, T, r, N[i], 1.0f, v + (int64_t)i * r, part + off);
+    (LoraProblem &)pr[i] = make_problem(dy[i], N[i], B[i], r, T, r, N[i], 1.0f, v + (int64_t)i * r, part + off);
     pr[i].ldo = (int64_t)count * r;
     pr[i].out_mid = v + plane + (int64_t)i * r;
     pr[i].out_low = v + 2 * plane + (int64_t)i * r;
@@ -634,16 +638,16 @@ hipError_t launch_lora_set_grads_act8(const uint16_t *v, const int8_t *codes, co
                                       const uint16_t *const *dy, const uint16_t *u_set,
                                       const int64_t *N, int count, int64_t T, int64_t K, int r, float scale,
                                       float *grad_A_set, float *const *grad_B, float *part, hipStream_t st) {
-  LoraProblem pr[kMaxBatch];
+  Act8Problem pr[kMaxBatch] = {};
   const int64_t rt = (int64_t)count * r;
-  LoraProblem &a = pr[0];
-  a = make_problem(v, rt, (const uint16_t *)codes, K, rt, K, T, scale, grad_A_set, part);
+  Act8Problem &a = pr[0];
+  (LoraProblem &)a = make_problem(v, rt, (const uint16_t *)codes, K, rt, K, T, scale, grad_A_set, part);
   a.P_mid = v + T * rt;
   a.P_low = v + 2 * T * rt;
   a.code_scale = code_scale;
   size_t off = lora_part_floats(rt, K, T);
   for (int i = 0; i < count; ++i) {
-    pr[i + 1] = make_problem(dy[i], N[i], u_set + (int64_t)i * r, rt, N[i], r, T, scale, grad_B[i], part + off);
+    (LoraProblem &)pr[i + 1] = make_problem(dy[i], N[i], u_set + (int64_t)i * r, rt, N[i], r, T, scale, grad_B[i], part + off);
     off += lora_part_floats(N[i], r, T);
   }
   LoraBatch b = make_batch(pr, count + 1, problem_blocks);
