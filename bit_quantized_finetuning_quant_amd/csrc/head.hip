@@ -43,12 +43,12 @@ namespace qlora {
 
 namespace {
 
-constexpr int kStatV = 128;     // words that share one exponent n per token
+constexpr int kStatV = 128;       // words that share one exponent n per token
 constexpr int kMaxPiece = 32768;  // words of a piece: a range's distances fit 16 KB of LDS
-constexpr int kFoldV = 8192;    // words up to which the products fold the tiles themselves
+constexpr int kFoldV = 8192;      // words up to which the products fold the tiles themselves
 constexpr int64_t kFewMaxWords = (int64_t)1 << 20;
-constexpr float kLog2e = 1.44269502162933349609375f;    // fl32(log2 e)
-constexpr float kLn2 = 0.693147182464599609375f;        // fl32(ln 2), and the rest of it
+constexpr float kLog2e = 1.44269502162933349609375f;  // fl32(log2 e)
+constexpr float kLn2 = 0.693147182464599609375f;      // fl32(ln 2), and the rest of it
 constexpr float kLn2Lo = -1.90465429995776804525e-9f;
 // |n| from which a row counts as overflown (its loss and gradient are NaN): below it integers and
 // their differences are exact in fp32, and l log2 e - n is rounded once
@@ -151,8 +151,8 @@ __device__ __forceinline__ float coarse_exponent(float m, float &factor) {
   factor = __builtin_ldexpf(1.0f, (int)(m - n));
   return n;
 }
-// 2^(l log2 e - n).  log2 e is its fp32 value everywhere, 1.3e-8 of it too small, so that all exponentials
-// of a token belong to logits scaled by that much: 1.3e-8 of l - l_y in the loss.
+// 2^(l log2 e - n).  log2 e is its fp32 value, 1.3e-8 of it too small, so all exponentials of a token belong
+// to logits smaller by that much: 1.3e-8 of l - l_y in the ratios, of l in lse (fp32 has 6e-8).
 __device__ __forceinline__ float relative_exp(float l, float n) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -n));
 }
@@ -205,14 +205,14 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
 }
 
 // One tile of the logits, see the top.  e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
-// [tile of 128 words][tpad].
-// kList: at most 512 tokens, listed here; otherwise head_scan has.
+// [tile of 128 words][tpad].  kList: at most 512 tokens, listed here; otherwise head_scan has.
 template <bool kList>
 __global__ __launch_bounds__(kThreads, 2) void head_logits(
     const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, const int64_t *__restrict__ target, int T, int64_t V,
     int64_t v0, int64_t nv, int D, int nleft, int *__restrict__ rows, int *__restrict__ place,
-    uint32_t *__restrict__ state, float *__restrict__ loss, float *__restrict__ lse, uint16_t *__restrict__ e, int64_t pitch, float *__restrict__ exponent,
-    float *__restrict__ sum, int64_t tpad, float *__restrict__ target_logit) {
+    uint32_t *__restrict__ state, float *__restrict__ loss, float *__restrict__ lse, uint16_t *__restrict__ e,
+    int64_t pitch, float *__restrict__ exponent, float *__restrict__ sum, int64_t tpad,
+    float *__restrict__ target_logit) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
   __shared__ int list[kList ? kTileT : 1];
   int entry = -1;
@@ -263,15 +263,13 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
     const bool on = t < live;
     const int64_t at = on ? target[token(t)] - v0 - vt : -1;  // the target's word, if it is one of this tile's
     const int y = at >= 0 && at < kTileV ? (int)at : -1;
+    const int64_t stat = (int64_t)(2 * tile.left + wm) * tpad + t;
+    uint16_t *out = e ? e + (int64_t)t * pitch + vt + vl : nullptr;
     // most waves hold no word past the vocabulary and no token's target: their values need no test
     if (nvt == kTileV && !__any(y >> 7 == wm))
-      put_logits<false>(acc, n, on, -1, vl, nvt, e ? e + (int64_t)t * pitch + vt + vl : nullptr,
-                        exponent + (int64_t)(2 * tile.left + wm) * tpad + t, sum + (int64_t)(2 * tile.left + wm) * tpad + t,
-                        nullptr);
+      put_logits<false>(acc, n, on, -1, vl, nvt, out, exponent + stat, sum + stat, nullptr);
     else
-      put_logits<true>(acc, n, on, y, vl, nvt, e ? e + (int64_t)t * pitch + vt + vl : nullptr,
-                       exponent + (int64_t)(2 * tile.left + wm) * tpad + t, sum + (int64_t)(2 * tile.left + wm) * tpad + t,
-                       target_logit + t);
+      put_logits<true>(acc, n, on, y, vl, nvt, out, exponent + stat, sum + stat, target_logit + t);
   }
 }
 
@@ -383,9 +381,9 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
 
 // One tile (256 columns d, 256 tokens) of G over one range of the piece's words, see the top.  The tiles and their
 // splits follow from the tokens that carry a loss; `words` is the length of every piece but the last, so that the
-// ranges, and the tiles' places in part, are the same in all.  kFold: the piece is the only one and has at most
-// kFoldV words; the exponents are folded here, which spares the launch of head_fold (shift is then unused).  part: [split][tile][256 tokens][256 d] fp32, in units of
-// 2^N.
+// ranges, and the tiles' places in part, are the same in all.  part: [split][tile][256 tokens][256 d] fp32, in units of
+// 2^N.  kFold: the piece is the only one and has at most kFoldV words; the exponents are folded here, which spares the
+// launch of head_fold (shift is then unused).
 template <bool kFold>
 __global__ __launch_bounds__(kThreads, 2) void head_grad(const uint16_t *__restrict__ e, int64_t pitch,
                                                          const uint16_t *__restrict__ w, int nv, int words, int D,
@@ -577,10 +575,12 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 // Few tokens or few words: the products run on the per-wave streams, 64 words
 // (or 64 columns d) by up to 64 tokens a workgroup.  Up to 64 tokens both are
 // bound by streaming W once; beyond, this form is for problems with too few
-// 256 x 256 tiles to occupy the CUs (few_pays).  Exponents n are
-// per token and 64 words here, and the gradient's sums of a chunk of words are
-// relative to the chunk's own largest n, which few_finish brings together: no
-// pass over the tiles lies between the two.
+// 256 x 256 tiles to occupy the CUs (few_pays).  Exponents n are the integers
+// next above, per token and 64 words, and the gradient's sums of a chunk of
+// words are relative to the chunk's own largest n, which few_finish brings
+// together: no pass over the tiles lies between the two products.
+//   16 x 4096 x 32000 (W 262 MB): few_logits 43 us (6.1 TB/s), with the gradient
+//   89 us, the call's launches included; a plain copy reaches 5.2 TB/s.
 
 constexpr int kFewWords = 64;       // words that share an exponent, and a step of the gradient
 constexpr int kFewChunk = 128;      // steps of a chunk at most: its shift bytes are held in LDS
@@ -993,7 +993,7 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.few = few_pays(T, V, D, grad);
   p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
   p.tpad = cdiv(p.chunk, kTileT) * kTileT;
-  // Words of a piece: 128 MB of e (grad) and 64 MB of decoded weight (packed).  A larger piece leaves less of
+  // Words of a piece: 128 MB of e (grad) and of decoded weight (packed).  A larger piece leaves less of
   // the products' last rounds of workgroups empty (2048 tokens, 40% of them masked, V = 32000: 5 tiles of
   // tokens by 125 of words are three rounds of 256, two pieces of 63 and 62 four).
   int64_t vc = cdiv(V, kTileV) * kTileV;
@@ -1056,7 +1056,7 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
     const uint16_t *hc = h + c0 * p.D;
     const int64_t *yc = target + c0;
     float *lc = loss + c0, *ec = lse ? lse + c0 : nullptr;
-    const bool list = p.T <= kThreads;                            // head_logits lists the tokens itself
+    const bool list = p.T <= kThreads;  // head_logits lists the tokens itself
     const bool fold = p.grad && p.pieces == 1 && words <= kFoldV;  // head_grad and head_finish fold the tiles themselves
     if (!list) head_scan<<<1, 1024, 0, st>>>(yc, T, p.V, c0 == 0, rows, place, state, lc, ec);
     for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
