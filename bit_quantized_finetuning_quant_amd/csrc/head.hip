@@ -279,16 +279,19 @@ struct Outcome {
 };
 __device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
   Outcome r;
-  const float ey = relative_exp(ly, N);
+  const float m = tile_exponent(ly);
+  const float ey = __builtin_ldexpf(relative_exp(ly, m), (int)fmaxf(m - N, -300.f));  // formed next to 1, as every e
   const float all = others + ey;
-  const float base = __builtin_fmaf(N, kLn2, N * kLn2Lo);
   if (others <= ey) {
     r.loss = log1pf(others / ey);
     r.lse = ly + r.loss;
   } else {
-    r.lse = base + logf(all);
-    // N ln 2 - l_y first: the two are close when the loss is small
-    r.loss = (__builtin_fmaf(N, kLn2, -ly) + N * kLn2Lo) + logf(all);
+    // S = f 2^k and N + k are taken apart: their logarithms would cancel where N is far above log2 S
+    int k;
+    const float f = __builtin_frexpf(all, &k), n = N + (float)k;
+    r.lse = __builtin_fmaf(n, kLn2, __builtin_fmaf(n, kLn2Lo, logf(f)));
+    // n ln 2 - l_y first: the two are close when the loss is small
+    r.loss = (__builtin_fmaf(n, kLn2, -ly) + n * kLn2Lo) + logf(f);
   }
   r.inv = 1.0f / all;
   r.other = others / all;

@@ -354,8 +354,9 @@ qlora_status qlora_act8_read(const qlora_act8 *a, uint16_t *x, void *stream);
  * checkpoint's): grad_x and grad_B as there, grad_A = scale v^T x_hat with
  * v = dy B in fp32 (grad_x takes it in bf16, as there).  u is the
  * forward's u_out and required: from the checkpoint it would come out
- * different.  grad_x may be NULL.  ws: qlora_linear_set_act8_workspace_bytes
- * with count = 1.                                                             */
+ * different.  grad_x may be NULL.  (Where the adapter's input is dropped out,
+ * qlora_act8_read gives the x that qlora_linear_bwd_dropout takes.)
+ * ws: qlora_linear_set_act8_workspace_bytes with count = 1.                   */
 qlora_status qlora_linear_bwd_act8(const uint16_t *dy, const qlora_act8 *a, const qlora_nf4_weight *q,
                                    const uint16_t *A, const uint16_t *B, int r, float scale, const uint16_t *u,
                                    uint16_t *grad_x, float *grad_A, float *grad_B, void *ws, size_t ws_bytes,
@@ -389,6 +390,7 @@ size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t
  * NaN in that token's loss, lse and gradient, and qlora_status_read on ws
  * reports QLORA_ERR_VALUE.  A token with a NaN or +Inf logit, or whose largest
  * logit has a magnitude of 2.9e6 or more, gets NaN in all three.
+ * Words more than 2^-60 below a token's most likely one may be left out.
  * Requires T >= 1, V >= 1, D % 64 == 0, D <= 65536, T D and V D <= 2^37, a
  * finite scale.  ws: qlora_head_loss_workspace_bytes, 16-B aligned.          */
 qlora_status qlora_head_loss(const uint16_t *h, int64_t T, const uint16_t *w, int64_t V, int64_t D,
@@ -403,7 +405,8 @@ qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_w
 
 /* Workspace bytes of the two calls (grad: with grad_h; packed: an NF4 head).
  * 0 on a bad shape.  Bounded whatever V is: tokens are taken 16384 at a time,
- * words in pieces of about 64 MB of workspace.                                */
+ * words in pieces of at most 128 MB of exponentials (with grad), 128 MB of
+ * decoded rows (packed) and 128 MB of fp32 partial sums (with grad).          */
 size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad, int packed);
 
 /* ---- diagnostics ---------------------------------------------------------- */
