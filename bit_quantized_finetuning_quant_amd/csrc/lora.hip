@@ -162,9 +162,9 @@ __device__ __forceinline__ void emit_out(void *out, int64_t idx, float v) {
 }
 
 // What the bf16 rounding of v leaves, in two bf16 values (the differences are exact): out, mid and
-// low then sum to v within 2^-24, its own precision.
+// low then sum to v within 2^-24, its own precision.  Nothing is left of an infinity.
 __device__ __forceinline__ void emit_rest(uint16_t *mid, uint16_t *low, int64_t idx, float v) {
-  const float d = v - (float)(__bf16)v;
+  const float h = (float)(__bf16)v, d = __builtin_isinf(h) ? 0.f : v - h;
   const __bf16 m = (__bf16)d;
   const __bf16 l = (__bf16)(d - (float)m);
   mid[idx] = __builtin_bit_cast(uint16_t, m);

@@ -259,6 +259,50 @@ def test_captured_step_replays_equal_eager():
             assert torch.equal(p, q), rep
 
 
+@gpu
+def test_a_given_streams_memory_is_its_own():
+    """What a call on another stream than the current one allocates lies in that stream's memory pool: the
+    workspace is given back when the call returns, before the kernels have run."""
+    torch = torch_mod()
+    announce("act8 on a given stream")
+    x, qs, A, Bs, dys, u = _case(40, [128], 192, 8, seed=9)
+    a = qlora.act8_write(x)
+    y = qlora.act8_read(a)
+    want = [a.codes, a.scale, y, *qlora.linear_bwd_act8(dys[0], a, qs[0], A, Bs[0], 0.5, u)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b = qlora.act8_write(x, stream=side)
+    y = qlora.act8_read(b, stream=side)
+    got = [b.codes, b.scale, y, *qlora.linear_bwd_act8(dys[0], b, qs[0], A, Bs[0], 0.5, u, stream=side)]
+    pools = [(s["address"], s["address"] + s["total_size"], s["stream"]) for s in torch.cuda.memory_snapshot()]
+    for t in got:
+        assert [p[2] for p in pools if p[0] <= t.data_ptr() < p[1]] == [side.cuda_stream]
+    side.synchronize()
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+
+
+@gpu
+@pytest.mark.parametrize("T", [40, 1200])
+def test_infinite_gradients(T):
+    """An infinite v = dy B has no remainder beside its bf16 value: grad_A is infinite (NaN where both signs meet)
+    where the formula is, not NaN throughout."""
+    torch = torch_mod()
+    announce(f"act8 backward of an infinite gradient T={T}")
+    x, qs, A, Bs, dys, u = _case(T, [128], 192, 8, seed=10)
+    dys[0][T // 2, 3] = float("inf")
+    dys[0][T - 1, 5] = float("inf")
+    a = qlora.act8_write(x)
+    _, ga, _ = qlora.linear_bwd_act8(dys[0], a, qs[0], A, Bs[0], 0.5, u)
+    xh, dy, B = (t.double().cpu() for t in (qlora.act8_read(a), dys[0], Bs[0]))
+    want = 0.5 * torch.mm(torch.mm(dy, B).t().contiguous(), xh)
+    assert want.isinf().any() and want.isnan().any()
+    ga = ga.cpu()
+    assert torch.equal(ga.isnan(), want.isnan())
+    assert torch.equal(ga[~want.isnan()].double(), want[~want.isnan()])
+
+
 # ------------------------------------------------------------------- refusals (no GPU)
 def test_refusals_before_any_launch():
     L = qlora.lib()
