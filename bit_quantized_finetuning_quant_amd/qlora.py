@@ -9,6 +9,7 @@ fallback: if the library is missing, every call raises.
 import ctypes
 import os
 import threading
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -194,6 +195,12 @@ def _stream_on(dev, stream=None) -> int:
     if stream.device != dev:
         raise ValueError(f"the tensors are on {dev}, the stream on {stream.device}")
     return int(stream.cuda_stream)
+
+
+def _alloc_on(stream):
+    """The context in which a call allocates what its caller did not give: the memory then belongs to the stream
+    that the call runs on, where it may be given back as soon as the call returns."""
+    return nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
 def _ptr(t) -> int:
@@ -778,9 +785,13 @@ def act8_write(x, out: Act8 = None, stream=None) -> Act8:
     if out is not None and _check_act8(out, chk) != (T, K):
         raise ValueError(f"out must hold {T} x {K} values, not {out.codes.shape[0]} x {out.codes.shape[1]}")
     chk.done()
-    a = out if out is not None else Act8.empty(T, K, x.device)
+    handle = _stream_on(x.device, stream)
+    a = out
+    if a is None:
+        with _alloc_on(stream):
+            a = Act8.empty(T, K, x.device)
     st = a.struct()
-    _check(lib().qlora_act8_write(x.data_ptr(), ctypes.byref(st), _stream_on(x.device, stream)), "qlora_act8_write")
+    _check(lib().qlora_act8_write(x.data_ptr(), ctypes.byref(st), handle), "qlora_act8_write")
     return a
 
 
@@ -792,9 +803,13 @@ def act8_read(a: Act8, out=None, stream=None):
     if out is not None:
         chk.bf16(out, "out", (T, K))
     chk.done()
-    y = out if out is not None else torch.empty((T, K), dtype=torch.bfloat16, device=a.codes.device)
+    handle = _stream_on(a.codes.device, stream)
+    y = out
+    if y is None:
+        with _alloc_on(stream):
+            y = torch.empty((T, K), dtype=torch.bfloat16, device=a.codes.device)
     st = a.struct()
-    _check(lib().qlora_act8_read(ctypes.byref(st), y.data_ptr(), _stream_on(y.device, stream)), "qlora_act8_read")
+    _check(lib().qlora_act8_read(ctypes.byref(st), y.data_ptr(), handle), "qlora_act8_read")
     return y
 
 
@@ -843,24 +858,26 @@ def linear_set_bwd_act8(dys, a: Act8, qs, A_set, Bs, scale: float, u, need_grad_
         for i, (q, g) in enumerate(zip(qs, grad_Bs)):
             chk.f32(g, f"grad_Bs[{i}]", (q.n_out, r))
     chk.done()
-    if need_grad_x and grad_x is None:
-        grad_x = torch.empty((T, n_in), dtype=torch.bfloat16, device=dev)
-    if grad_A_set is None:
-        grad_A_set = torch.empty((count * r, n_in), dtype=torch.float32, device=dev)
-    if grad_Bs is None:
-        grad_Bs = [torch.empty((q.n_out, r), dtype=torch.float32, device=dev) for q in qs]
+    handle = _stream_on(dev, stream)
     n_outs = [q.n_out for q in qs]
-    if workspace is None:
-        ws = linear_set_act8_workspace(T, n_outs, n_in, r, dev)
-        wsb = ws.numel()
-    else:
-        ws = workspace
-        wsb = _workspace(ws, dev, lambda: linear_set_act8_workspace_bytes(T, n_outs, n_in, r))
+    with _alloc_on(stream):
+        if need_grad_x and grad_x is None:
+            grad_x = torch.empty((T, n_in), dtype=torch.bfloat16, device=dev)
+        if grad_A_set is None:
+            grad_A_set = torch.empty((count * r, n_in), dtype=torch.float32, device=dev)
+        if grad_Bs is None:
+            grad_Bs = [torch.empty((q.n_out, r), dtype=torch.float32, device=dev) for q in qs]
+        if workspace is None:
+            ws = linear_set_act8_workspace(T, n_outs, n_in, r, dev)
+            wsb = ws.numel()
+        else:
+            ws = workspace
+            wsb = _workspace(ws, dev, lambda: linear_set_act8_workspace_bytes(T, n_outs, n_in, r))
     st = (NF4WeightStruct * count)(*[q.struct() for q in qs])
     sa = a.struct()
     _check(lib().qlora_linear_set_bwd_act8(_ptrs(dys), ctypes.byref(sa), count, st, _ptr(A_set), _ptrs(Bs), r,
                                            float(scale), _ptr(u), _ptr(grad_x), _ptr(grad_A_set), _ptrs(grad_Bs),
-                                           _ptr(ws), wsb, _stream_on(dev, stream)), "qlora_linear_set_bwd_act8")
+                                           _ptr(ws), wsb, handle), "qlora_linear_set_bwd_act8")
     return grad_x, grad_A_set, grad_Bs
 
 
@@ -908,25 +925,27 @@ def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=N
     elif grad_h is not None:
         chk.bf16(grad_h, "grad_h", (T, D))
     chk.done()
-    if loss is None:
-        loss = torch.empty(T, dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
-    if need_grad and grad_h is None:
-        grad_h = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
-    if workspace is None:
-        ws = head_loss_workspace(T, V, D, need_grad, packed, dev)
-        wsb = ws.numel()
-    else:
-        ws = workspace
-        wsb = _workspace(ws, dev, lambda: head_loss_workspace_bytes(T, V, D, need_grad, packed))
+    handle = _stream_on(dev, stream)
+    with _alloc_on(stream):
+        if loss is None:
+            loss = torch.empty(T, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(T, dtype=torch.float32, device=dev)
+        if need_grad and grad_h is None:
+            grad_h = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            ws = head_loss_workspace(T, V, D, need_grad, packed, dev)
+            wsb = ws.numel()
+        else:
+            ws = workspace
+            wsb = _workspace(ws, dev, lambda: head_loss_workspace_bytes(T, V, D, need_grad, packed))
     if packed:
         st = head.struct()
         _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), _ptr(target), _ptr(weight), float(scale),
-                                         _ptr(loss), _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream_on(dev, stream)),
+                                         _ptr(loss), _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, handle),
                "qlora_head_loss_nf4")
     else:
         _check(lib().qlora_head_loss(_ptr(h), T, _ptr(head), V, D, _ptr(target), _ptr(weight), float(scale), _ptr(loss),
-                                     _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, _stream_on(dev, stream)),
+                                     _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, handle),
                "qlora_head_loss")
     return loss, lse, grad_h

@@ -174,7 +174,8 @@ def test_exponents_of_tiles_and_pieces(order, T):
     if order == "falling":
         ramp = ramp.flip(0)
     if order == "far":
-        ramp = torch.where(torch.arange(V, device="cuda") % 128 == 5, 600.0, -600.0) * (torch.arange(V, device="cuda") > 70000)
+        ids = torch.arange(V, device="cuda")
+        ramp = torch.where(ids % 128 == 5, 600.0, -600.0) * (ids > 70000)
     h[:, 0] = 1.0
     w[:, 0] = ramp.bfloat16()
     y[::3] = V - 1 if order == "rising" else 3  # also tokens the model is sure of, and sure against
@@ -184,7 +185,8 @@ def test_exponents_of_tiles_and_pieces(order, T):
 @gpu
 @pytest.mark.parametrize("T", [64, 130, 600])
 def test_sure_tokens_keep_relative_precision(T):
-    """Losses down to about 1e-8 (3000 words 26 below the target, at 20003 words 1e-7): loss = log1p(others / e_y) and 1 - p_y are formed without a difference."""
+    """Losses down to about 1e-8 (3000 words 26 below the target, at 20003 words 1e-7): loss = log1p(others / e_y)
+    and 1 - p_y are formed without a difference."""
     torch = torch_mod()
     D, V = 256, 3000 if T < 550 else 20003  # streams, tiles
     announce(f"head loss of sure tokens T={T}")
@@ -349,6 +351,26 @@ def test_two_streams_at_once_and_repeats_are_identical(T):
         for r in calls:
             for a, b in zip(r, want):
                 assert torch.equal(a, b)
+
+
+@gpu
+def test_a_given_streams_memory_is_its_own():
+    """What a call on another stream than the current one allocates lies in that stream's memory pool: the
+    workspace is given back when the call returns, before the kernels have run."""
+    torch = torch_mod()
+    announce("head loss on a given stream")
+    h, w, y = (t.cuda() for t in _inputs(40, 256, 3000, seed=21, std=0.1))
+    want = qlora.head_loss(h, w, y)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = qlora.head_loss(h, w, y, stream=side)
+    pools = [(s["address"], s["address"] + s["total_size"], s["stream"]) for s in torch.cuda.memory_snapshot()]
+    for t in got:
+        assert [p[2] for p in pools if p[0] <= t.data_ptr() < p[1]] == [side.cuda_stream]
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------- refusals (no GPU)
