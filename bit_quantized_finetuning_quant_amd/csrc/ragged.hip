@@ -1,5 +1,5 @@
 // grad_x of linears whose sizes are not whole tiles of the fused GEMM (n_out not
-// a multiple of 64 or n_in not of 128), gfx950.
+// a multiple of 64 or n_in not of 128), or whose products are long, gfx950.
 //
 //   grad_x = sum_i dy_i W_hat_i + s v A
 //
@@ -11,7 +11,10 @@
 // and beside them [v | dy_0 | dy_1 ..] with zero columns in the same places.
 // Then the sum is one product over all rows on plain full tiles: the adapter
 // steps come first and their sum is scaled in fp32.
-// Decoding costs 2.5 bytes a weight at HBM speed, read again by the product.
+// Decoding costs 2.5 bytes a weight at HBM speed, read again by the product; the
+// product then runs at 1.36 PFLOP/s where its tiles fill the CUs, against 0.9 to
+// 1.0 with the decode inside.  So long products on whole tiles are taken here too
+// (long_pays).
 
 #include <algorithm>
 
@@ -248,6 +251,21 @@ int few_chunk_steps(const RaggedLayout &l) {
 
 }  // namespace
 
+// Whether a product on whole tiles is faster here than in the fused GEMM, both estimated in us.  Here: the rounds
+// of 256 workgroups (25 ns a row of a tile's range, 512 rows' worth of start), the decode and the packed
+// gradients at 5.2 TB/s; there: 970 TFLOP/s.  Measured, the whole backward pass of T x n_out x n_in (here / there):
+// 4096 x 8192 x 22016 1439 / 1618 us, 4096 x 8192 x 8192 571 / 622, 4096 x (3 of 4096) x 4096 466 / 483, 2048 x
+// 8192 x 8192 307 / 325; left to the fused GEMM: 2048 x 4096 x 4096 139 / 111, 2048 x 4096 x 11008 275 / 248, 1024 x
+// 8192 x 22016 510 / 422 (and, below the estimate's precision, 4096 x 4096 x 11008 437 / 481).
+static bool long_pays(int64_t T, int64_t K, int64_t rows) {
+  if (T < 1024) return false;
+  const int tiles = (int)(cdiv(K, kTileV) * cdiv(T, kTileT));
+  Split s = choose_split(tiles, (int)rows);
+  const double product = 0.025 * (double)split_cost(tiles, (int)rows, s.count, s);
+  const double layout = (2.5 * rows * K + 4.0 * T * rows) / 5.2e6;
+  return product + layout < 2.0 * T * K * rows / 0.97e9;
+}
+
 bool ragged_dx_applies(int64_t T, int count, const int64_t *N, int64_t K, int r) {
   bool whole = K % 128 == 0;
   int64_t rows = pad64((int64_t)count * r);
@@ -259,7 +277,8 @@ bool ragged_dx_applies(int64_t T, int count, const int64_t *N, int64_t K, int r)
   // a few tokens and rows: its own launches cost more than the masks (6 tokens, 2 x 100 x 512: 41 against
   // 47 us; 1 token, 4 x 200 x 512: 62 against 57)
   if (T <= kFewTokens && rows <= 512) return false;
-  return !whole && rows <= kMaxDecoded / K && T <= (int64_t)1 << 24 && rows * T <= (int64_t)1 << 32;
+  if (rows > kMaxDecoded / K || T > (int64_t)1 << 24 || rows * T > (int64_t)1 << 32) return false;
+  return !whole || long_pays(T, K, rows);
 }
 
 // dyp, the weights' rows, and the partial sums, each 256-byte aligned

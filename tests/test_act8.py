@@ -205,6 +205,14 @@ def test_backward_7b_projection():
 
 
 @gpu
+@pytest.mark.parametrize("T,Ns,K,r", [(2048, (8192,), 8192, 16), (1100, (4096, 1024, 1024), 8192, 8)])
+def test_long_products_on_whole_tiles(T, Ns, K, r):
+    """Long enough for the decoded weights' product, and a set that stays on the fused GEMM."""
+    announce(f"act8 long backward T={T} Ns={Ns} K={K} r={r}")
+    _check(T, list(Ns), K, r, seed=22)
+
+
+@gpu
 def test_gradient_of_A_against_differences():
     """grad_A of sum(dy . (scale x_hat A^T B^T)) against central differences of that sum in 64 bits:
     it is linear in A, so the difference is exact up to 64-bit rounding."""
