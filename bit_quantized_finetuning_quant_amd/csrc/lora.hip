@@ -615,6 +615,11 @@ static hipError_t reduce_batch(const Act8Problem *pr, int count, hipStream_t st)
   return hipGetLastError();
 }
 
+// Rows of a member up to which v is not split over them: the reduction is a launch more, of 3 us on the host (16 tokens,
+// 512 x 1024: 37 -> 33 us; 1000 tokens the same; at 1024 rows, or for the gradients' sums over the tokens, the longer
+// loop costs more than it spares: 500 tokens, 1000 x 512 52 -> 61 us).
+constexpr int64_t kWholeRows = 512;
+
 // v_set with what its rounding leaves: v [3][T x count r].
 hipError_t launch_lora_set_v_exact(const uint16_t *const *dy, const uint16_t *const *B, const int64_t *N, int count,
                                    int64_t T, int r, uint16_t *v, float *part, hipStream_t st) {
@@ -623,6 +628,10 @@ hipError_t launch_lora_set_v_exact(const uint16_t *const *dy, const uint16_t *co
   size_t off = 0;
   for (int i = 0; i < count; ++i) {
     (LoraProblem &)pr[i] = make_problem(dy[i], N[i], B[i], r, T, r, N[i], 1.0f, v + (int64_t)i * r, part + off);
+    if (N[i] <= kWholeRows) {
+      pr[i].chunk = cdiv(N[i], 4 * LT) * (4 * LT);
+      pr[i].S = 1;
+    }
     pr[i].ldo = (int64_t)count * r;
     pr[i].out_mid = v + plane + (int64_t)i * r;
     pr[i].out_low = v + 2 * plane + (int64_t)i * r;

@@ -7,6 +7,7 @@ fallback: if the library is missing, every call raises.
 """
 
 import ctypes
+import functools
 import os
 import threading
 from contextlib import nullcontext
@@ -177,21 +178,21 @@ def _torch():
 def _stream(stream=None) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
-    torch = _torch()
+    c = _torch()._C
     # the current stream's handle without a Stream object around it (3 us of every call)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _stream_on(dev, stream=None) -> int:
     """The stream's handle for a call on tensors of `dev`, which must be the current device (a launch goes
     to the current one, whatever device the pointers belong to)."""
-    torch = _torch()
-    current = torch.cuda.current_device()
+    c = _torch()._C
+    current = c._cuda_getDevice()
     if dev.index != current:
         raise ValueError(f"the tensors are on {dev}, the current device is cuda:{current}: call it under "
                          f"torch.cuda.device({dev.index})")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(current)
+        return c._cuda_getCurrentRawStream(current)
     if stream.device != dev:
         raise ValueError(f"the tensors are on {dev}, the stream on {stream.device}")
     return int(stream.cuda_stream)
@@ -204,7 +205,7 @@ def _alloc_on(stream):
 
 
 def _ptr(t) -> int:
-    return 0 if t is None else int(t.data_ptr())
+    return 0 if t is None else t.data_ptr()
 
 
 # The C ABI takes plain pointers and cannot check the extent of a buffer, so every tensor is
@@ -277,16 +278,17 @@ class _Args:
         self.named = []
 
     def _check(self, t, name: str, shape, kind: str) -> None:
-        dt = _dtypes()
+        dt = _DT or _dtypes()
+        if isinstance(t, dt["tensor"]) and t.dtype in dt[kind] and t.shape == shape and t.is_contiguous():
+            self.named.append((name, t))
+            return
         if not isinstance(t, dt["tensor"]):
             raise ValueError(f"{name} must be a tensor")
         if t.dtype not in dt[kind]:
             raise ValueError(f"{name} must be {' or '.join(str(d) for d in dt[kind])}, not {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        self.named.append((name, t))
+        raise ValueError(f"{name} must be contiguous")
 
     def bf16(self, t, name: str, shape) -> None:
         self._check(t, name, shape, "bf16")
@@ -302,8 +304,9 @@ class _Args:
 
     def done(self) -> None:
         dev = self.device
+        cuda = dev.type == "cuda"
         for name, t in self.named:
-            if t.device != dev or dev.type != "cuda":
+            if not cuda or t.device != dev:
                 raise ValueError(f"{name} must be on {dev}, not {t.device}")
 
 
@@ -813,9 +816,14 @@ def act8_read(a: Act8, out=None, stream=None):
     return y
 
 
-def linear_set_act8_workspace_bytes(tokens: int, n_outs, n_in: int, r: int) -> int:
+@functools.lru_cache(maxsize=1024)
+def _act8_bytes(tokens: int, n_outs: tuple, n_in: int, r: int) -> int:
     arr = (ctypes.c_int64 * len(n_outs))(*n_outs)
     return int(lib().qlora_linear_set_act8_workspace_bytes(tokens, len(n_outs), arr, n_in, r))
+
+
+def linear_set_act8_workspace_bytes(tokens: int, n_outs, n_in: int, r: int) -> int:
+    return _act8_bytes(tokens, tuple(n_outs), n_in, r)
 
 
 def linear_set_act8_workspace(tokens: int, n_outs, n_in: int, r: int, device="cuda"):
@@ -882,6 +890,7 @@ def linear_set_bwd_act8(dys, a: Act8, qs, A_set, Bs, scale: float, u, need_grad_
 
 
 # ----------------------------------------------------------- the loss of the head
+@functools.lru_cache(maxsize=1024)
 def head_loss_workspace_bytes(tokens: int, vocab: int, dim: int, grad: bool = True, packed: bool = False) -> int:
     return int(lib().qlora_head_loss_workspace_bytes(tokens, vocab, dim, int(grad), int(packed)))
 
