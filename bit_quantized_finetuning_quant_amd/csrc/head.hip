@@ -584,20 +584,21 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 // together: no pass over the tiles lies between the two products.
 //   16 x 4096 x 32000 (W 262 MB): few_logits 43 us (6.1 TB/s), with the gradient
 //   89 us, the call's launches included; a plain copy reaches 5.2 TB/s.
+// A packed head is decoded inside both products up to 64 tokens (one group);
+// beyond, every group would decode it again, and it is decoded once before.
 
 constexpr int kFewWords = 64;       // words that share an exponent, and a step of the gradient
 constexpr int kFewChunk = 128;      // steps of a chunk at most: its shift bytes are held in LDS
 
 // e (nullptr: the loss alone) [T][pitch], exponent and sum [64 words][tpad]; v0: the piece's first word, which is
 // also the first column of e.  Workgroups: the token groups of 64 words, then the next words'.
-template <int NT>
-__global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const uint16_t *__restrict__ h,
-                                                             const uint16_t *__restrict__ w,
-                                                             const int64_t *__restrict__ target, int T, int64_t v0,
-                                                             int64_t nv, int D, uint16_t *__restrict__ e, int64_t pitch,
-                                                             float *__restrict__ exponent, float *__restrict__ sum,
-                                                             int tpad, float *__restrict__ target_logit) {
-  constexpr int kBytes = few_stages<false, NT>() * few_stage<NT>();
+// kPacked: the rows are decoded from q on their way in (w unused, v0 = 0).
+template <int NT, bool kPacked>
+__global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
+    const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, QWeight q, Codebook cb,
+    const int64_t *__restrict__ target, int T, int64_t v0, int64_t nv, int D, uint16_t *__restrict__ e, int64_t pitch,
+    float *__restrict__ exponent, float *__restrict__ sum, int tpad, float *__restrict__ target_logit) {
+  constexpr int kBytes = (kPacked ? 2 : few_stages<false, NT>()) * few_stage<NT>();
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int groups = tpad / kFewTokens, place = place_of(blockIdx.x, gridDim.x), block = scalar(place / groups);
@@ -612,8 +613,12 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
   }
   f32x4 acc[4][NT];
   few_zero<NT>(acc);
-  few_product<false, false, NT>(uniform(w + vt * D), (uint32_t)D * 2u, words, 2 * kStep, uniform(h), off, wave, D / kStep,
-                         lds + wave * kBytes, nullptr, acc);
+  if constexpr (kPacked)
+    few_product_packed<false, false, NT>(q, cb, vt, words, D / kBlock, 0, uniform(h), off, wave, D / kStep,
+                                         lds + wave * kBytes, nullptr, acc);
+  else
+    few_product<false, false, NT>(uniform(w + vt * D), (uint32_t)D * 2u, words, 2 * kStep, uniform(h), off, wave,
+                                  D / kStep, lds + wave * kBytes, nullptr, acc);
   float *red = (float *)lds;
   few_put<NT>(acc, red);
   // 4 NT tokens a wave, 16 / NT lanes a token, 4 NT words a lane
@@ -667,15 +672,15 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(const
 
 // One chunk of words, 64 columns: part[chunk][T][D] relative to 2^N of the chunk, and (first columns) its N and S
 // [chunk][tpad].  e, exponent and sum start at the piece.
-template <int NT>
+template <int NT, bool kPacked>
 __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__restrict__ e, int64_t pitch,
-                                                           const uint16_t *__restrict__ w, int T, int64_t nv, int D,
-                                                           int chunk_steps, int chunk0,
+                                                           const uint16_t *__restrict__ w, QWeight q, Codebook cb,
+                                                           int T, int64_t nv, int D, int chunk_steps, int chunk0,
                                                            const float *__restrict__ exponent,
                                                            const float *__restrict__ sum, int tpad,
                                                            float *__restrict__ N, float *__restrict__ S,
                                                            float *__restrict__ part) {
-  constexpr int kBytes = few_stages<true, NT>() * few_stage<NT>(), kT = 16 * NT, kRows = kFewThreads / kT;
+  constexpr int kBytes = (kPacked ? 2 : few_stages<true, NT>()) * few_stage<NT>(), kT = 16 * NT, kRows = kFewThreads / kT;
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   __shared__ uint8_t shifts[kFewChunk * kT];
   __shared__ float fold[kFewThreads];
@@ -722,8 +727,13 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
   }
   f32x4 acc[4][NT];
   few_zero<NT>(acc);
-  few_product<true, true, NT>(uniform(w + vb * D + 64 * slice), (uint32_t)D * 2u, words, (int64_t)kStep * D * 2,
-                        uniform(e + (int64_t)t0 * pitch + vb), off, wave, steps, lds + wave * kBytes, shifts, acc);
+  const char *right = uniform(e + (int64_t)t0 * pitch + vb);
+  if constexpr (kPacked)
+    few_product_packed<true, true, NT>(q, cb, vb, words, D / kBlock, slice, right, off, wave, steps, lds + wave * kBytes,
+                                       shifts, acc);
+  else
+    few_product<true, true, NT>(uniform(w + vb * D + 64 * slice), (uint32_t)D * 2u, words, (int64_t)kStep * D * 2,
+                                right, off, wave, steps, lds + wave * kBytes, shifts, acc);
   float *red = (float *)lds;
   few_put<NT>(acc, red);
   // 16 lanes a token, four columns each
@@ -904,7 +914,7 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
   p.off_s = take((size_t)p.splits * p.tpad * 4);
   p.off_e = p.grad ? take((size_t)p.T * groups * kFewWords * 2) : 0;
   p.off_part = p.grad ? take((size_t)p.splits * p.T * p.D * 4) : 0;
-  p.off_w = p.packed ? take((size_t)p.words * p.D * 2) : 0;
+  p.off_w = p.decode ? take((size_t)p.words * p.D * 2) : 0;
   p.off_rows = p.off_place = p.off_factor = p.off_shift = 0;
   p.total = off;
   return p;
@@ -927,7 +937,7 @@ static hipError_t decode_rows(const QWeight &q, int64_t v0, int64_t nv, uint16_t
   return launch_dequantize(rows, out, cb, st);
 }
 
-template <int NT>
+template <int NT, bool kPacked>
 static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_t *w, const QWeight *q,
                              const int64_t *target, const float *weight, float scale, float *loss, float *lse,
                              uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st) {
@@ -939,22 +949,23 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
   uint16_t *wp = (uint16_t *)(ws + p.off_w);
   const int T = (int)p.T, D = (int)p.D, groups = (int)cdiv(p.V, kFewWords), tpad = (int)p.tpad;
   const int token_groups = tpad / kFewTokens;
+  const QWeight qw = q ? *q : QWeight{};
   const int64_t pitch = (int64_t)groups * kFewWords;
   int chunk0 = 0;
   for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
     const int64_t nv = std::min(p.words, p.V - v0);
     const uint16_t *piece = w ? w + v0 * p.D : wp;
-    if (q) {
+    if (p.decode) {
       const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
       if (err != hipSuccess) return err;
     }
-    few_logits<NT><<<(unsigned)(cdiv(nv, kFewWords) * token_groups), kFewThreads, 0, st>>>(
-        h, piece, target, T, v0, nv, D, e, pitch, exponent, sum, tpad, logit);
+    few_logits<NT, kPacked><<<(unsigned)(cdiv(nv, kFewWords) * token_groups), kFewThreads, 0, st>>>(
+        h, piece, qw, cb, target, T, v0, nv, D, e, pitch, exponent, sum, tpad, logit);
     if (!p.grad) continue;
     const int chunks = (int)cdiv(nv, p.split_words);
     const int64_t g0 = v0 / kFewWords * tpad;
-    few_grad<NT><<<(unsigned)(chunks * token_groups * (D / 64)), kFewThreads, 0, st>>>(
-        e + v0, pitch, piece, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0, tpad, N, S,
+    few_grad<NT, kPacked><<<(unsigned)(chunks * token_groups * (D / 64)), kFewThreads, 0, st>>>(
+        e + v0, pitch, piece, qw, cb, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0, tpad, N, S,
         part);
     chunk0 += chunks;
   }
@@ -963,8 +974,8 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
     return hipGetLastError();
   }
   few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, tpad, logit,
-                                                                       w, q ? *q : QWeight{}, cb, weight, scale, part,
-                                                                       state, loss, lse, grad);
+                                                                       w, qw, cb, weight, scale, part, state, loss,
+                                                                       lse, grad);
   return hipGetLastError();
 }
 
@@ -992,7 +1003,7 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.V = V;
   p.D = D;
   p.grad = grad;
-  p.packed = packed;
+  p.packed = p.decode = packed;
   p.few = few_pays(T, V, D, grad);
   p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
   p.tpad = cdiv(p.chunk, kTileT) * kTileT;
@@ -1003,7 +1014,8 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   // The exponents and sums of its tiles stay within 64 MB too.
   const int64_t budget = (int64_t)64 << 20;
   if (p.few) {  // one piece, but for the decoded rows of a packed head
-    if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
+    p.decode = packed && T > kFewTokens;  // up to 64 tokens the streams decode the rows themselves
+    if (p.decode) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
     return plan_few(p, vc);
   }
   vc = std::min(vc, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
@@ -1041,9 +1053,14 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
 hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t *w, const QWeight *q,
                             const int64_t *target, const float *weight, float scale, float *loss, float *lse,
                             uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st) {
-  if (p.few && p.T <= 16) return launch_few<1>(p, h, w, q, target, weight, scale, loss, lse, grad, ws, cb, st);
-  if (p.few && p.T <= 32) return launch_few<2>(p, h, w, q, target, weight, scale, loss, lse, grad, ws, cb, st);
-  if (p.few) return launch_few<4>(p, h, w, q, target, weight, scale, loss, lse, grad, ws, cb, st);
+  if (p.few) {
+    const bool packed = q && !p.decode;
+    const auto run = p.T <= 16   ? packed ? launch_few<1, true> : launch_few<1, false>
+                     : p.T <= 32 ? packed ? launch_few<2, true> : launch_few<2, false>
+                     : packed    ? launch_few<4, true>
+                                 : launch_few<4, false>;
+    return run(p, h, w, q, target, weight, scale, loss, lse, grad, ws, cb, st);
+  }
   uint32_t *state = (uint32_t *)ws;
   int *rows = (int *)(ws + p.off_rows), *place = (int *)(ws + p.off_place);
   float *logit = (float *)(ws + p.off_logit), *N = (float *)(ws + p.off_n), *S = (float *)(ws + p.off_s);

@@ -397,8 +397,9 @@ qlora_status qlora_head_loss(const uint16_t *h, int64_t T, const uint16_t *w, in
                              const int64_t *target, const float *weight, float scale, float *loss, float *lse,
                              uint16_t *grad_h, void *ws, size_t ws_bytes, void *stream);
 
-/* The same with a packed head (V = q->n_out, D = q->n_in): its pieces are
- * decoded to BFloat16 in the workspace, as every use of the weight decodes it. */
+/* The same with a packed head (V = q->n_out, D = q->n_in), whose rows are
+ * decoded to BFloat16 as every use of the weight decodes them: inside the
+ * products up to 64 tokens, piece by piece in the workspace above.            */
 qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_weight *q, const int64_t *target,
                                  const float *weight, float scale, float *loss, float *lse, uint16_t *grad_h,
                                  void *ws, size_t ws_bytes, void *stream);

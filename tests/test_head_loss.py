@@ -151,9 +151,23 @@ def test_packed_head(T, D, V, double_quant):
 
 
 @gpu
-def test_packed_head_in_pieces_by_size():
+@pytest.mark.parametrize("double_quant", [True, False])
+@pytest.mark.parametrize("T,D,V", [(1, 128, 1), (1, 4096, 32003), (2, 64, 63), (5, 192, 65), (16, 1024, 8193),
+                                   (17, 320, 4100), (32, 448, 20001), (48, 64, 100001), (64, 1088, 2049), (65, 1088, 2049)])
+def test_packed_head_decoded_in_the_streams(T, D, V, double_quant):
+    """Up to 64 tokens the rows are decoded inside the products: one to four tiles of tokens, a tile with fewer
+    than 64 rows, waves with none, one and many steps."""
+    announce(f"packed head, few tokens, T={T} D={D} V={V} double_quant={double_quant}")
+    h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=23, std=2 / math.sqrt(D)))
+    q = qlora.quantize(w, double_quant=double_quant)
+    _check(h, q, qlora.dequantize(q), y, scale=0.25)
+
+
+@gpu
+@pytest.mark.parametrize("T", [40, 70, 1030])
+def test_packed_head_in_pieces_by_size(T):
     """V D above a piece's decoded bytes: pieces also without the gradient."""
-    T, D, V = 40, 8192, 9001
+    D, V = 8192, 9001
     announce(f"packed head in pieces T={T} D={D} V={V}")
     h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=10, std=0.02))
     q = qlora.quantize(w)
