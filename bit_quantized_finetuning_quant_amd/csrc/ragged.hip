@@ -53,10 +53,14 @@ __global__ __launch_bounds__(256) void ragged_pack(RaggedLayout l, const uint16_
           c = c0 - l.first[i];
         }
       u32x4 x = {0u, 0u, 0u, 0u};
+      if (c + 8 <= n) {
+        x = load8(src + c);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t value = c + j < n ? src[c + j] : 0u;
-        x[j >> 1] |= value << (16 * (j & 1));
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t value = c + j < n ? src[c + j] : 0u;
+          x[j >> 1] |= value << (16 * (j & 1));
+        }
       }
       *(u32x4 *)(dyp + t * l.total + c0) = x;
     }
@@ -81,7 +85,8 @@ __global__ __launch_bounds__(256) void ragged_pack(RaggedLayout l, const uint16_
 }
 
 // One 256 x 256 tile (columns of grad_x, tokens) over one range of the rows: grad_x itself, or with more than one range
-// part [range][tile][256 tokens][256 columns] fp32.
+// part [range][tile][256 tokens][256 columns] fp32.  Bound by the matrix cores: 3284 tokens, 4 x 837 x 6144, 169 us (0.80
+// PFLOP/s of the unpadded sizes, 1.2 rounds of workgroups); 4096 x 8192 x 22016, 1166 us (1.27).
 __global__ __launch_bounds__(kThreads, 2) void ragged_tiles(const uint16_t *__restrict__ dyp,
                                                             const uint16_t *__restrict__ wp, int T, int K, int rows,
                                                             int adapter, float scale, int nleft, int ntoken,
@@ -344,8 +349,8 @@ hipError_t launch_ragged_dx(const RaggedPlan &p, int64_t T, int count, const int
     ragged_tiles<<<(unsigned)(nleft * ntoken * split.count), kThreads, 0, st>>>(
         dyp, wp, l.T, l.K, l.total, l.rank_pad, scale, nleft, ntoken, split, part, out);
     if (split.count > 1)
-      ragged_reduce<<<(unsigned)std::min<int64_t>(cdiv(T * K / 4, 256), 2048), 256, 0, st>>>(part, l.T, l.K, nleft, ntoken,
-                                                                                          split.count, out);
+      ragged_reduce<<<(unsigned)std::min<int64_t>(cdiv(T * K / 4, 256), 2048), 256, 0, st>>>(
+          part, l.T, l.K, nleft, ntoken, split.count, out);
   }
   return hipGetLastError();
 }
