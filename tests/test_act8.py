@@ -199,6 +199,17 @@ def test_backward_of_a_set(T, Ns, K, r):
 
 
 @gpu
+@pytest.mark.parametrize("T,N,K,r", [(1, 1, 64, 1), (1, 7, 64, 1), (2, 3, 64, 1), (2, 5, 64, 3), (9, 7, 64, 1),
+                                     (3, 9, 128, 7), (70, 8, 64, 8), (71, 9, 192, 9), (300, 65, 64, 7), (515, 129, 128, 63),
+                                     (1030, 1031, 64, 5), (1025, 7, 64, 2), (600, 71, 320, 65)])
+def test_narrow_and_odd_rows(T, N, K, r):
+    """Adapter products whose operands have rows of fewer than eight values, fewer than eight values in all, and
+    rows at every alignment."""
+    announce(f"act8 backward of narrow rows T={T} N={N} K={K} r={r}")
+    _check(T, [N], K, r, seed=24)
+
+
+@gpu
 def test_backward_7b_projection():
     announce("act8 backward T=2048 4096x4096 r=64")
     _check(2048, [4096], 4096, 64, seed=5)
