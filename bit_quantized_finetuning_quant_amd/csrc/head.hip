@@ -565,6 +565,7 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
     const int64_t tile = place_at(Tile{c / kTileV, j / kTileT}, nleft, ntoken);
     const float *p = part + tile * (kTileT * kTileV) + j % kTileT * kTileV + c % kTileV;
     f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll 4
     for (int k = 0; k < splits; ++k) {
       const f32x4 x = *(const f32x4 *)p, z = *(const f32x4 *)(p + 4);
       p += (int64_t)tiles * (kTileT * kTileV);

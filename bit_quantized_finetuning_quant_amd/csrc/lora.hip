@@ -52,19 +52,14 @@ __device__ __forceinline__ u32x4 ld8(const uint16_t *row, int64_t c, int64_t nco
   return drop(load8(row + at), (int)min(c - at, (int64_t)8));
 }
 
-// The same of element `at` of a matrix of `all` values with fewer than eight columns, `keep` of them from here on: the
-// load goes on into the next rows, whose values are cleared, and at the matrix's end starts before.
+// The same of element `at` of a matrix of `all` >= 8 values with fewer than eight columns, `keep` of them from here on:
+// the load goes on into the next rows, whose values are cleared, and at the matrix's end starts before.
 __device__ __forceinline__ u32x4 ld8_narrow(const uint16_t *src, int64_t at, int64_t all, int64_t keep) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (keep <= 0) return v;
-  if (all < 8) {
-    for (int i = 0; i < keep; ++i) v[i >> 1] |= (uint32_t)src[at + i] << (16 * (i & 1));
-    return v;
-  }
   const int64_t from = min(at, all - 8);
-  v = drop(load8(src + from), (int)(at - from));
+  const int k = (int)max(keep, (int64_t)0);
+  u32x4 v = drop(load8(src + from), (int)min(at - from, (int64_t)8));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = keep > 2 * i + 1 ? v[i] : keep == 2 * i + 1 ? v[i] & 0xFFFFu : 0u;
+  for (int i = 0; i < 4; ++i) v[i] = k > 2 * i + 1 ? v[i] : k == 2 * i + 1 ? v[i] & 0xFFFFu : 0u;
   return v;
 }
 
@@ -73,8 +68,8 @@ __device__ __forceinline__ u32x4 ld8_narrow(const uint16_t *src, int64_t at, int
 // fetches columns 8 (t%8) .. +7 of rows t/8 and t/8 + 32, so that each wave's
 // load covers 8 whole 128-byte rows (a load that covers half of each of 16
 // lines moves about half as many bytes per cycle from L2).  kWhole: the tile
-// is known to be in range; kNarrow: ncols < 8.
-enum Edge { kWhole, kMasked, kNarrow };
+// is known to be in range; kNarrow: ncols < 8; kTiny: fewer than eight values in all.
+enum Edge { kWhole, kMasked, kNarrow, kTiny };
 struct TileRegs {
   u32x4 v[2];
 };
@@ -96,6 +91,10 @@ __device__ __forceinline__ void load_tile(const uint16_t *src, int64_t ld, int64
     const int64_t at = in ? row + 32 * h : nrows - 1;
     if (kEdge == kNarrow) {
       t.v[h] = ld8_narrow(src, at * ld + col, (nrows - 1) * ld + ncols, in ? ncols - col : 0);
+    } else if (kEdge == kTiny) {
+      t.v[h] = u32x4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < 8; ++i)
+        if (in && col + i < ncols) t.v[h][i >> 1] |= (uint32_t)src[at * ld + col + i] << (16 * (i & 1));
     } else {
       const u32x4 v = ld8(src + at * ld, col, ncols);
       t.v[h] = in ? v : u32x4{0u, 0u, 0u, 0u};
@@ -160,8 +159,10 @@ __device__ __forceinline__ void lora_body(const uint16_t *__restrict__ P, int64_
       all(std::integral_constant<Edge, kWhole>{});
     else if ((trans.value ? outs : ke) >= 8)
       all(std::integral_constant<Edge, kMasked>{});
-    else
+    else if ((trans.value ? (ke - 1) * ld + outs : (outs - 1) * ld + ke) >= 8)
       all(std::integral_constant<Edge, kNarrow>{});
+    else
+      all(std::integral_constant<Edge, kTiny>{});
   };
   auto fetch = [&](int64_t g0) {
     fetch_one(std::bool_constant<kAT>{}, P, ldp, M, m0, g0, ta);
@@ -426,8 +427,10 @@ __device__ __forceinline__ void act8_tile(const Act8Problem &pr, int64_t tile, i
     act8_body<kWhole>(pr, kb, ke, m0, n0, lds, acc);
   else if (pr.M >= 8)
     act8_body<kMasked>(pr, kb, ke, m0, n0, lds, acc);
-  else
+  else if ((ke - 1) * pr.ldp + pr.M >= 8)
     act8_body<kNarrow>(pr, kb, ke, m0, n0, lds, acc);
+  else
+    act8_body<kTiny>(pr, kb, ke, m0, n0, lds, acc);
   put_tile<false>(pr, tile, s, acc);
 }
 

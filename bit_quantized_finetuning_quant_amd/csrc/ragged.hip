@@ -150,21 +150,37 @@ __global__ __launch_bounds__(kThreads, 2) void ragged_tiles(const uint16_t *__re
   }
 }
 
-// grad_x from the ranges' tiles, in range order; four columns a thread.
+// grad_x from the ranges' tiles, four columns a thread.  kWaves = 4: every wave takes a fourth of the ranges, so that the
+// partial sums, from the caches of other XCDs, arrive in few round trips (109 tokens by 256 columns, 60 ranges: 19 ->
+// 4.5 us; where one wave a quad fills the CUs it loses, 1500 by 1024, ten ranges: 80 -> 82 us in all).
+template <int kWaves>
 __global__ __launch_bounds__(256) void ragged_reduce(const float *__restrict__ part, int T, int K, int nleft,
                                                      int ntoken, int splits, uint16_t *__restrict__ out) {
+  constexpr int kQuads = 256 / kWaves, kDeep = kWaves > 1 ? 8 : 1;
+  __shared__ f32x4 sums[kWaves][kQuads];
   const int64_t quads = (int64_t)T * K / 4, stride = (int64_t)nleft * ntoken * kTileT * kTileV;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+  const int own = threadIdx.x % kQuads, wave = threadIdx.x / kQuads;
+  for (int64_t i0 = (int64_t)blockIdx.x * kQuads; i0 < quads; i0 += (int64_t)gridDim.x * kQuads) {
+    const int64_t i = min(i0 + own, quads - 1);
     const int t = (int)(i / (K / 4)), c = (int)(i % (K / 4)) * 4;
     const float *p = part + (int64_t)place_at(Tile{c / kTileV, t / kTileT}, nleft, ntoken) * (kTileT * kTileV) +
                      t % kTileT * kTileV + c % kTileV;
-    f32x4 s = *(const f32x4 *)p;
-    for (int k = 1; k < splits; ++k) {
-      const f32x4 x = *(const f32x4 *)(p + k * stride);
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&s](const f32x4 &x) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) s[q] += x[q];
+    };
+#pragma unroll kDeep
+    for (int k = wave; k < splits; k += kWaves) add(*(const f32x4 *)(p + k * stride));
+    if constexpr (kWaves > 1) {
+      sums[wave][own] = s;
+      __syncthreads();
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) add(sums[w][own]);  // of use in the first wave
+      __syncthreads();
     }
-    *(uint2 *)(out + (int64_t)t * K + c) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    if (wave == 0 && i0 + own < quads)
+      *(uint2 *)(out + (int64_t)t * K + c) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
   }
 }
 
@@ -223,6 +239,7 @@ __global__ __launch_bounds__(256) void ragged_few_reduce(const float *__restrict
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;
   f32x4 s = *(const f32x4 *)(part + i);
+#pragma unroll 8
   for (int k = 1; k < chunks; ++k) {
     const f32x4 x = *(const f32x4 *)(part + k * n + i);
 #pragma unroll
@@ -348,9 +365,13 @@ hipError_t launch_ragged_dx(const RaggedPlan &p, int64_t T, int count, const int
     const Split split = choose_split(nleft * ntoken, l.total);
     ragged_tiles<<<(unsigned)(nleft * ntoken * split.count), kThreads, 0, st>>>(
         dyp, wp, l.T, l.K, l.total, l.rank_pad, scale, nleft, ntoken, split, part, out);
-    if (split.count > 1)
-      ragged_reduce<<<(unsigned)std::min<int64_t>(cdiv(T * K / 4, 256), 2048), 256, 0, st>>>(
-          part, l.T, l.K, nleft, ntoken, split.count, out);
+    const int64_t quads = T * K / 4;
+    if (split.count >= 8 && quads <= 65536)
+      ragged_reduce<4><<<(unsigned)std::min<int64_t>(cdiv(quads, 64), 4096), 256, 0, st>>>(part, l.T, l.K, nleft, ntoken,
+                                                                                       split.count, out);
+    else if (split.count > 1)
+      ragged_reduce<1><<<(unsigned)std::min<int64_t>(cdiv(quads, 256), 2048), 256, 0, st>>>(part, l.T, l.K, nleft, ntoken,
+                                                                                        split.count, out);
   }
   return hipGetLastError();
 }
