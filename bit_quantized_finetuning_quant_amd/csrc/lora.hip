@@ -63,20 +63,31 @@ __device__ __forceinline__ u32x4 ld8_narrow(const uint16_t *src, int64_t at, int
   return v;
 }
 
+// Columns c .. c + 7 of a row, zero from ncols on: value by value, or (vec: the rows are 16-byte aligned) in one load
+// where the row goes on.
+__device__ __forceinline__ u32x4 ld8_by_one(const uint16_t *row, int64_t c, int64_t ncols, bool vec) {
+  if (vec && c + 8 <= ncols) return *(const u32x4 *)(row + c);
+  u32x4 v = {0u, 0u, 0u, 0u};
+  for (int i = 0; i < 8; ++i)
+    if (c + i < ncols) v[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+  return v;
+}
+
 // Tile rows [r0, r0 + 64) x columns [c0, c0 + 64) of a row-major [nrows x ld]
 // bf16 matrix (columns >= ncols and rows >= nrows read as zero); thread t
 // fetches columns 8 (t%8) .. +7 of rows t/8 and t/8 + 32, so that each wave's
 // load covers 8 whole 128-byte rows (a load that covers half of each of 16
 // lines moves about half as many bytes per cycle from L2).  kWhole: the tile
-// is known to be in range; kNarrow: ncols < 8; kTiny: fewer than eight values in all.
-enum Edge { kWhole, kMasked, kNarrow, kTiny };
+// is known to be in range; kNarrow: ncols < 8; kTiny: fewer than eight values in all;
+// kByLoad: decided load by load (vec: the rows are 16-byte aligned).
+enum Edge { kWhole, kMasked, kNarrow, kTiny, kByLoad };
 struct TileRegs {
   u32x4 v[2];
 };
 
 template <Edge kEdge>
 __device__ __forceinline__ void load_tile(const uint16_t *src, int64_t ld, int64_t nrows, int64_t ncols,
-                                          int64_t r0, int64_t c0, int tid, TileRegs &t) {
+                                          int64_t r0, int64_t c0, bool vec, int tid, TileRegs &t) {
   const int64_t row = r0 + (tid >> 3);
   const int64_t col = c0 + 8 * (tid & 7);
   if (kEdge == kWhole) {
@@ -91,10 +102,8 @@ __device__ __forceinline__ void load_tile(const uint16_t *src, int64_t ld, int64
     const int64_t at = in ? row + 32 * h : nrows - 1;
     if (kEdge == kNarrow) {
       t.v[h] = ld8_narrow(src, at * ld + col, (nrows - 1) * ld + ncols, in ? ncols - col : 0);
-    } else if (kEdge == kTiny) {
-      t.v[h] = u32x4{0u, 0u, 0u, 0u};
-      for (int i = 0; i < 8; ++i)
-        if (in && col + i < ncols) t.v[h][i >> 1] |= (uint32_t)src[at * ld + col + i] << (16 * (i & 1));
+    } else if (kEdge == kTiny || kEdge == kByLoad) {
+      t.v[h] = in ? ld8_by_one(src + (row + 32 * h) * ld, col, ncols, kEdge == kByLoad && vec) : u32x4{0u, 0u, 0u, 0u};
     } else {
       const u32x4 v = ld8(src + at * ld, col, ncols);
       t.v[h] = in ? v : u32x4{0u, 0u, 0u, 0u};
@@ -130,7 +139,7 @@ __device__ __forceinline__ u32x4 frag(const uint16_t *lds, int base, int kk, int
 // so that the whole split arrives in one round trip (128 KB per workgroup in
 // flight, 147 KB of LDS).
 
-template <bool kAT, bool kBT, bool kBf16Out, bool kFull, int kGroupSteps>
+template <bool kAT, bool kBT, bool kFull, bool kSorted, int kGroupSteps>
 __device__ __forceinline__ void lora_body(const uint16_t *__restrict__ P, int64_t ldp,
                                           const uint16_t *__restrict__ Q, int64_t ldq, int64_t M, int64_t Nc,
                                           int64_t kb, int64_t ke, int64_t m0, int64_t n0, uint16_t (*sA)[LT * LLD],
@@ -143,21 +152,21 @@ __device__ __forceinline__ void lora_body(const uint16_t *__restrict__ P, int64_
   // registers as soon as the current group is in LDS, so they overlap with its
   // MFMAs.
   TileRegs ta[kGroupSteps], tb[kGroupSteps];
-  // One operand's tiles: rows (its output index) or, kTrans, columns.  Which form loads them is decided once for all.
+  const bool vp = (ldp % 8) == 0 && ((uintptr_t)P & 15u) == 0, vq = (ldq % 8) == 0 && ((uintptr_t)Q & 15u) == 0;
+  // kSorted: which form loads an operand's tiles, rows (its output index) or columns, is decided once for all of them;
+  // three forms more and the operands one after the other, which costs kernels that are all whole tiles 0.5 to 1 us.
   auto fetch_one = [&](auto trans, const uint16_t *src, int64_t ld, int64_t outs, int64_t o0, int64_t g0, TileRegs *t) {
     auto all = [&](auto edge) {
 #pragma unroll
       for (int st = 0; st < kGroupSteps; ++st) {
         const int64_t k0 = g0 + LT * st;
         if constexpr (!trans.value)
-          load_tile<edge.value>(src, ld, outs, ke, o0, k0, tid, t[st]);
+          load_tile<edge.value>(src, ld, outs, ke, o0, k0, false, tid, t[st]);
         else
-          load_tile<edge.value>(src, ld, ke, outs, k0, o0, tid, t[st]);
+          load_tile<edge.value>(src, ld, ke, outs, k0, o0, false, tid, t[st]);
       }
     };
-    if constexpr (kFull)
-      all(std::integral_constant<Edge, kWhole>{});
-    else if ((trans.value ? outs : ke) >= 8)
+    if ((trans.value ? outs : ke) >= 8)
       all(std::integral_constant<Edge, kMasked>{});
     else if ((trans.value ? (ke - 1) * ld + outs : (outs - 1) * ld + ke) >= 8)
       all(std::integral_constant<Edge, kNarrow>{});
@@ -165,8 +174,24 @@ __device__ __forceinline__ void lora_body(const uint16_t *__restrict__ P, int64_
       all(std::integral_constant<Edge, kTiny>{});
   };
   auto fetch = [&](int64_t g0) {
-    fetch_one(std::bool_constant<kAT>{}, P, ldp, M, m0, g0, ta);
-    fetch_one(std::bool_constant<kBT>{}, Q, ldq, Nc, n0, g0, tb);
+    if constexpr (kSorted && !kFull) {
+      fetch_one(std::bool_constant<kAT>{}, P, ldp, M, m0, g0, ta);
+      fetch_one(std::bool_constant<kBT>{}, Q, ldq, Nc, n0, g0, tb);
+      return;
+    }
+    constexpr Edge kEdge = kFull ? kWhole : kByLoad;
+#pragma unroll
+    for (int st = 0; st < kGroupSteps; ++st) {
+      const int64_t k0 = g0 + LT * st;
+      if (!kAT)
+        load_tile<kEdge>(P, ldp, M, ke, m0, k0, vp, tid, ta[st]);
+      else
+        load_tile<kEdge>(P, ldp, ke, M, k0, m0, vp, tid, ta[st]);
+      if (!kBT)
+        load_tile<kEdge>(Q, ldq, Nc, ke, n0, k0, vq, tid, tb[st]);
+      else
+        load_tile<kEdge>(Q, ldq, ke, Nc, k0, n0, vq, tid, tb[st]);
+    }
   };
   fetch(kb);
   for (int64_t g0 = kb; g0 < ke; g0 += LT * kGroupSteps) {
@@ -266,6 +291,7 @@ __device__ __forceinline__ void lora_tile(const Problem &pr, int64_t tile, int s
                                           uint16_t (*sB)[LT * LLD]) {
   const int64_t m0 = (tile % pr.tiles_m) * LT, n0 = (tile / pr.tiles_m) * LT;
   const int64_t kb = (int64_t)s * pr.chunk, ke = min(pr.Kc, kb + pr.chunk);
+  constexpr bool kSorted = std::is_same_v<Problem, Act8Problem>;
 
   f32x16 acc;
 #pragma unroll
@@ -273,10 +299,10 @@ __device__ __forceinline__ void lora_tile(const Problem &pr, int64_t tile, int s
   // full: both operand tiles in range, and the chunk is whole groups
   const bool full = (m0 + LT <= pr.M) && (n0 + LT <= pr.Nc) && ((ke - kb) % (LT * kGroupSteps) == 0);
   if (full)
-    lora_body<kAT, kBT, kBf16Out, true, kGroupSteps>(pr.P, pr.ldp, pr.Q, pr.ldq, pr.M, pr.Nc, kb, ke, m0, n0, sA, sB,
+    lora_body<kAT, kBT, true, kSorted, kGroupSteps>(pr.P, pr.ldp, pr.Q, pr.ldq, pr.M, pr.Nc, kb, ke, m0, n0, sA, sB,
                                                       acc);
   else
-    lora_body<kAT, kBT, kBf16Out, false, kGroupSteps>(pr.P, pr.ldp, pr.Q, pr.ldq, pr.M, pr.Nc, kb, ke, m0, n0, sA,
+    lora_body<kAT, kBT, false, kSorted, kGroupSteps>(pr.P, pr.ldp, pr.Q, pr.ldq, pr.M, pr.Nc, kb, ke, m0, n0, sA,
                                                        sB, acc);
 
   put_tile<kBf16Out>(pr, tile, s, acc);
@@ -385,9 +411,9 @@ __device__ __forceinline__ void act8_body(const Act8Problem &pr, int64_t kb, int
 #pragma unroll
     for (int st = 0; st < kActSteps; ++st) {
       const int64_t k0 = g0 + LT * st;
-      load_tile<kEdge>(pr.P, pr.ldp, ke, pr.M, k0, m0, tid, th[st]);
-      load_tile<kEdge>(pr.P_mid, pr.ldp, ke, pr.M, k0, m0, tid, tm[st]);
-      load_tile<kEdge>(pr.P_low, pr.ldp, ke, pr.M, k0, m0, tid, tl[st]);
+      load_tile<kEdge>(pr.P, pr.ldp, ke, pr.M, k0, m0, false, tid, th[st]);
+      load_tile<kEdge>(pr.P_mid, pr.ldp, ke, pr.M, k0, m0, false, tid, tm[st]);
+      load_tile<kEdge>(pr.P_low, pr.ldp, ke, pr.M, k0, m0, false, tid, tl[st]);
       load_codes((const int8_t *)pr.Q, pr.code_scale, pr.ldq, ke, k0, n0, tid, tq[st]);
     }
   };
