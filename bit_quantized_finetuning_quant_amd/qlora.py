@@ -827,7 +827,8 @@ def linear_set_act8_workspace_bytes(tokens: int, n_outs, n_in: int, r: int) -> i
 
 
 def linear_set_act8_workspace(tokens: int, n_outs, n_in: int, r: int, device="cuda"):
-    """A workspace for linear_set_bwd_act8, and with one n_out for linear_bwd_act8."""
+    """A workspace for linear_set_bwd_act8, and with one n_out for linear_bwd_act8, of exactly these sizes (fewer
+    tokens may need more)."""
     torch = _torch()
     return torch.empty(max(linear_set_act8_workspace_bytes(tokens, n_outs, n_in, r), 1), dtype=torch.uint8,
                        device=device)
@@ -896,7 +897,8 @@ def head_loss_workspace_bytes(tokens: int, vocab: int, dim: int, grad: bool = Tr
 
 
 def head_loss_workspace(tokens: int, vocab: int, dim: int, grad: bool = True, packed: bool = False, device="cuda"):
-    """A workspace for head_loss (reusable by successive calls on one stream)."""
+    """A workspace for head_loss of exactly these sizes (reusable by successive calls on one stream; fewer tokens
+    may need more)."""
     torch = _torch()
     return torch.empty(max(head_loss_workspace_bytes(tokens, vocab, dim, grad, packed), 1), dtype=torch.uint8,
                        device=device)

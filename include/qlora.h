@@ -368,7 +368,8 @@ qlora_status qlora_linear_set_bwd_act8(const uint16_t *const *dy, const qlora_ac
                                        int r, float scale, const uint16_t *u, uint16_t *grad_x, float *grad_A_set,
                                        float *const *grad_B, void *ws, size_t ws_bytes, void *stream);
 
-/* Workspace bytes of the two calls above (0 on a bad shape).                  */
+/* Workspace bytes of the two calls above (0 on a bad shape), for these sizes:
+ * fewer tokens may take another form and need more.                           */
 size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t *n_out, int64_t n_in, int r);
 
 /* ---- the loss of the head ---------------------------------------------------- */
@@ -407,7 +408,8 @@ qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_w
 /* Workspace bytes of the two calls (grad: with grad_h; packed: an NF4 head).
  * 0 on a bad shape.  Bounded whatever V is: tokens are taken 16384 at a time,
  * words in pieces of at most 128 MB of exponentials (with grad), 128 MB of
- * decoded rows (packed) and 128 MB of fp32 partial sums (with grad).          */
+ * decoded rows (packed) and 128 MB of fp32 partial sums (with grad).  For
+ * these sizes: fewer tokens may take another form and need more.              */
 size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad, int packed);
 
 /* ---- diagnostics ---------------------------------------------------------- */
