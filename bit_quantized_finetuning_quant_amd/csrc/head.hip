@@ -10,9 +10,10 @@
 //
 //   head_logits   one 256 x 256 tile of l per workgroup; its epilogue takes,
 //                 per token and 128 words, an integer n above log2 e max l
-//                 and writes e_tv = 2^(l log2 e - n) in bf16 and s = sum e
-//   head_fold     running N_t = max n and S_t = sum 2^(n - N) s over the
-//                 tiles, and the distance (N - n) / 64 of each tile, 0 to 3
+//                 and writes e_tv = 2^(l log2 e - n) in bf16, s = sum e and
+//                 r = sum of the written (rounded) e
+//   head_fold     running N_t = max n, S_t = sum 2^(n - N) s and R_t likewise of r
+//                 over the tiles, and the distance (N - n) / 64 of each tile, 0 to 3
 //   head_grad     G_td += sum_v 2^(n - N) e_tv W_vd: the factor of a tile is a
 //                 power of two, so it is one saturating subtraction from the
 //                 exponent field of the bf16 operand, exact
@@ -25,13 +26,18 @@
 // the range (its share of the loss is below the rounding of any other term,
 // unless every other word is that unlikely).
 //
-// and head_finish forms grad_h = c (G / S - (S - e_y) / S W_y).  So the
+// and head_finish forms grad_h = c (G - R W_y) / (R + e_y).  So the
 // gradient needs the two products it cannot do without (4 T V D operations)
-// and no second run over the logits.  The target's own term is kept out of e
-// and S and added apart: 1 - p_y = S_others / S has no cancellation, and
-// loss = log1p(S_others / e_y) keeps its relative precision for a token the
+// and no second run over the logits.  The target's own term is kept out of e,
+// S and R and added apart: 1 - p_y has no cancellation, and
+// loss = log1p(S / e_y) keeps its relative precision for a token the
 // model is sure of.  e is rounded to bf16 (half a step, 2^-8 of it) because the
-// matrix cores take it in that type; S sums the unrounded fp32 values.
+// matrix cores take it in that type; S, of which loss and lse are made, sums the
+// unrounded fp32 values.  The gradient takes R, so that its words' weights sum
+// to what W_y is subtracted with: a token sure of another word than its target
+// gets c p (W_word - W_y) within the rounding of that difference, also where the
+// two rows are alike and most of it cancels (with S in R's place it was off by up
+// to 2^-8 of W_word: 0.013 of the gradient at a cosine of 0.9, now 0.002).
 //
 // Tokens whose target is negative carry no loss.  A scan lists the others, the
 // products gather their rows by that list, and tiles past its end do nothing.
@@ -160,12 +166,19 @@ __device__ __forceinline__ float relative_exp(float l, float n) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -n));
 }
 
-// 16 tokens (fragment n) by the wave's 128 words of a tile of the logits: e, n and s.  A NaN logit shows in
+// r + the two bf16 values of a word.
+__device__ __forceinline__ float add_pair(uint32_t pair, float r) {
+  constexpr uint32_t kOnes = 0x3F803F80u;
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, kOnes), r, false);
+}
+
+// 16 tokens (fragment n) by the wave's 128 words of a tile of the logits: e, n, s and r.  A NaN logit shows in
 // s.  kTest: words past nvt are left out, and the token's target y (of this tile, or -1) goes to
 // target_logit.  out, exponent, sum, target_logit: this lane's token (out: its first word, too).
 template <bool kTest>
 __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool on, int y, int vl, int nvt,
-                                           uint16_t *out, float *exponent, float *sum, float *target_logit) {
+                                           uint16_t *out, float *exponent, float *sum, float *rounded,
+                                           float *target_logit) {
   const int lane = threadIdx.x & 63;
   float top = -INFINITY;
 #pragma unroll
@@ -181,7 +194,7 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
   const float ex = tile_exponent(top);
   float factor, n_tile = coarse_exponent(ex, factor);
   if (kTest && (vl & ~127) >= nvt) n_tile = kNoExponent;
-  float s = 0.f, ly = 0.f;
+  float s = 0.f, r = 0.f, ly = 0.f;
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
     float p[4];
@@ -196,14 +209,23 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
       }
       s += p[q];
     }
-    if (out && on) *(uint2 *)(out + 16 * m) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+    if (out) {
+      const uint2 v = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+      if (on) *(uint2 *)(out + 16 * m) = v;
+      r = add_pair(v.y, add_pair(v.x, r));
+    }
   }
   if (kTest && y >= 0 && (y & ~127) == (vl & ~127) && ((y >> 2) & 3) == (lane >> 4)) *target_logit = ly;
   s += __shfl_xor(s, 16);
   s += __shfl_xor(s, 32);
+  if (out) {
+    r += __shfl_xor(r, 16);
+    r += __shfl_xor(r, 32);
+  }
   if (lane < 16 && on) {
     *exponent = n_tile;
     *sum = s;
+    if (out) *rounded = r;
   }
 }
 
@@ -212,14 +234,14 @@ __device__ __forceinline__ void put_logits(const f32x4 (&acc)[8][4], int n, bool
 // library product of these operands alone reaches 1.45).  256 x 256 tiles, since a tile's operands then take a quarter
 // of the LDS bandwidth that 128 x 128 would; the epilogue works on the accumulators where they are, so that the logits
 // never leave the registers.
-// e: [tokens][pitch] bf16 (nullptr: the loss alone); exponent and sum:
+// e: [tokens][pitch] bf16 (nullptr: the loss alone, and no rounded); exponent, sum and rounded:
 // [tile of 128 words][tpad].  kList: at most 512 tokens, listed here; otherwise head_scan has.
 template <bool kList>
 __global__ __launch_bounds__(kThreads, 2) void head_logits(
     const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, const int64_t *__restrict__ target, int T, int64_t V,
     int64_t v0, int64_t nv, int D, int nleft, int *__restrict__ rows, int *__restrict__ place,
     uint32_t *__restrict__ state, float *__restrict__ loss, float *__restrict__ lse, uint16_t *__restrict__ e,
-    int64_t pitch, float *__restrict__ exponent, float *__restrict__ sum, int64_t tpad,
+    int64_t pitch, float *__restrict__ exponent, float *__restrict__ sum, float *__restrict__ rounded, int64_t tpad,
     float *__restrict__ target_logit) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
   __shared__ int list[kList ? kTileT : 1];
@@ -275,17 +297,18 @@ __global__ __launch_bounds__(kThreads, 2) void head_logits(
     uint16_t *out = e ? e + (int64_t)t * pitch + vt + vl : nullptr;
     // most waves hold no word past the vocabulary and no token's target: their values need no test
     if (nvt == kTileV && !__any(y >> 7 == wm))
-      put_logits<false>(acc, n, on, -1, vl, nvt, out, exponent + stat, sum + stat, nullptr);
+      put_logits<false>(acc, n, on, -1, vl, nvt, out, exponent + stat, sum + stat, rounded + stat, nullptr);
     else
-      put_logits<true>(acc, n, on, y, vl, nvt, out, exponent + stat, sum + stat, target_logit + t);
+      put_logits<true>(acc, n, on, y, vl, nvt, out, exponent + stat, sum + stat, rounded + stat,
+                       target_logit + t);
   }
 }
 
-// loss, lse and what the gradient needs of one token: 1 / S and S_others / S.
+// loss, lse and what the gradient needs of one token: 1 / (R + e_y) and R / (R + e_y).
 struct Outcome {
   float loss, lse, inv, other;
 };
-__device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
+__device__ __forceinline__ Outcome outcome(float N, float others, float R, float ly) {
   Outcome r;
   const float m = tile_exponent(ly);
   const float ey = __builtin_ldexpf(relative_exp(ly, m), (int)fmaxf(m - N, -300.f));  // formed next to 1, as every e
@@ -301,8 +324,8 @@ __device__ __forceinline__ Outcome outcome(float N, float others, float ly) {
     // n ln 2 - l_y first: the two are close when the loss is small
     r.loss = (__builtin_fmaf(n, kLn2, -ly) + n * kLn2Lo) + logf(f);
   }
-  r.inv = 1.0f / all;
-  r.other = others / all;
+  r.inv = 1.0f / (R + ey);
+  r.other = R / (R + ey);
   if (!(all > 0.f && all < INFINITY) || !(fabsf(N) < kMaxExponent)) r.loss = r.lse = r.inv = r.other = NAN;
   return r;
 }
@@ -316,33 +339,37 @@ __device__ __forceinline__ int pack_distances(int d) {
   return d | __shfl_xor(d, 2);
 }
 
-// Folds the piece's tiles into the running exponent N and sum S of each token: 8 tokens and 32 lanes
+// Folds the piece's tiles into the running exponent N and sums S and R of each token: 8 tokens and 32 lanes
 // along the tiles a workgroup, eight tiles of a lane in flight at once.  shift [tile][tpad / 4]: the
 // distances of four tokens a byte (0 for tokens past the last); factor: 2^(N before - N), for what the
 // pieces before have summed.  loss (nullptr: not yet, or not here): the piece is the last, N and S are final.
 // 7.9 us for 4096 tokens by 126 tiles: the tiles' statistics are 8 bytes per token and 128 words, so this is latency.
+// kGrad: with rounded, R, shift and factor.
+template <bool kGrad>
 __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ exponent, const float *__restrict__ sum,
-                                                 int64_t tpad, int tiles, bool first,
+                                                 const float *__restrict__ rounded, int64_t tpad, int tiles, bool first,
                                                  const uint32_t *__restrict__ state, float *__restrict__ N,
-                                                 float *__restrict__ S, uint8_t *__restrict__ shift,
+                                                 float *__restrict__ S, float *__restrict__ R,
+                                                 uint8_t *__restrict__ shift,
                                                  float *__restrict__ factor, const int *__restrict__ rows,
                                                  const float *__restrict__ target_logit, float *__restrict__ loss,
                                                  float *__restrict__ lse) {
   constexpr int kLanes = 32, kDeep = 8;
-  __shared__ float part[kLanes][9];
+  __shared__ float part[kLanes][9], part_r[kGrad ? kLanes : 1][9];
   const int live = (int)state[1];
   if ((int)blockIdx.x * 8 >= live) return;
   const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
   const int t = min((int)blockIdx.x * 8 + c, live - 1);
-  const float before = first ? kNoExponent : N[t], held = first ? 0.f : S[t];
+  const float before = first ? kNoExponent : N[t], held = first ? 0.f : S[t], held_r = kGrad && !first ? R[t] : 0.f;
   float top = before;
-  float ex[kDeep], sm[kDeep];
+  float ex[kDeep], sm[kDeep], rm[kDeep];
   for (int i0 = 0; i0 < tiles; i0 += kLanes * kDeep) {
 #pragma unroll
     for (int j = 0; j < kDeep; ++j) {
       const int i = i0 + j * kLanes + g;
       ex[j] = i < tiles ? exponent[i * tpad + t] : kNoExponent;
       sm[j] = i < tiles ? sum[i * tpad + t] : 0.f;
+      if (kGrad) rm[j] = i < tiles ? rounded[i * tpad + t] : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < kDeep; ++j) top = fmaxf(top, ex[j]);
@@ -352,7 +379,7 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
 #pragma unroll
   for (int i = 0; i < kLanes; ++i) top = fmaxf(top, part[i][c]);
   __syncthreads();
-  float s = 0.f;
+  float s = 0.f, r = 0.f;
   for (int i0 = 0; i0 < tiles; i0 += kLanes * kDeep) {
     if (tiles > kLanes * kDeep) {  // more than the registers hold: read again
 #pragma unroll
@@ -360,20 +387,24 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
         const int i = i0 + j * kLanes + g;
         ex[j] = i < tiles ? exponent[i * tpad + t] : kNoExponent;
         sm[j] = i < tiles ? sum[i * tpad + t] : 0.f;
+        if (kGrad) rm[j] = i < tiles ? rounded[i * tpad + t] : 0.f;
       }
     }
 #pragma unroll
     for (int j = 0; j < kDeep; ++j) {
       const int i = i0 + j * kLanes + g;
       const float d = top - ex[j];
-      s += sm[j] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
-      if (shift) {
+      const float f = __builtin_amdgcn_exp2f(-fminf(d, 300.f));
+      s += sm[j] * f;
+      if (kGrad) {
+        r += rm[j] * f;
         const int four = pack_distances((int)blockIdx.x * 8 + c < live ? distance(d) : 0);
         if (i < tiles && (c & 3) == 0) shift[i * (tpad >> 2) + (int)blockIdx.x * 2 + (c >> 2)] = (uint8_t)four;
       }
     }
   }
   part[g][c] = s;
+  if (kGrad) part_r[g][c] = r;
   __syncthreads();
   if (g == 0 && (int)blockIdx.x * 8 + c < live) {
     const float f = first ? 0.f : __builtin_amdgcn_exp2f(-fminf(top - before, 300.f));
@@ -382,11 +413,17 @@ __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ expon
     for (int i = 0; i < kLanes; ++i) all += part[i][c];
     N[t] = top;
     S[t] = all;
-    factor[t] = f;
+    if (kGrad) {
+      float all_r = held_r * f;
+#pragma unroll
+      for (int i = 0; i < kLanes; ++i) all_r += part_r[i][c];
+      R[t] = all_r;
+      factor[t] = f;
+    }
     if (loss) {
-      const Outcome r = outcome(top, all, target_logit[t]);
-      loss[rows[t]] = r.loss;
-      if (lse) lse[rows[t]] = r.lse;
+      const Outcome o = outcome(top, all, all, target_logit[t]);
+      loss[rows[t]] = o.loss;
+      if (lse) lse[rows[t]] = o.lse;
     }
   }
 }
@@ -515,12 +552,13 @@ __device__ __forceinline__ u32x4 row_values(const uint16_t *w, const QWeight &q,
 }
 
 // grad_h of one token a workgroup (and its loss and lse), eight columns a thread and turn.  Bound by HBM: 45 us for 4096
-// x 8192 (fp32 sums and W's rows read, bf16 written: 5.7 TB/s).  kFold: as in head_grad, N
-// and S come from the tiles' exponents and sums.
+// x 8192 (fp32 sums and W's rows read, bf16 written: 5.7 TB/s).  kFold: as in head_grad, N,
+// S and R come from the tiles' exponents and sums.
 template <bool kFold>
 __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place, const float *__restrict__ N,
-                                                   const float *__restrict__ S, const float *__restrict__ exponent,
-                                                   const float *__restrict__ sum, int64_t tpad, int stat_tiles,
+                                                   const float *__restrict__ S, const float *__restrict__ R,
+                                                   const float *__restrict__ exponent, const float *__restrict__ sum,
+                                                   const float *__restrict__ rounded, int64_t tpad, int stat_tiles,
                                                    const float *__restrict__ target_logit,
                                                    const int64_t *__restrict__ target, const uint16_t *__restrict__ w,
                                                    QWeight q, Codebook cb, const float *__restrict__ weight,
@@ -536,21 +574,28 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
     for (int c = threadIdx.x * 8; c < D; c += 2048) *(u32x4 *)(g + c) = u32x4{fill, fill, fill, fill};
     return;
   }
-  float n, s;
+  float n, s, rs;
   if (kFold) {  // at most 64 tiles, one a lane, every wave for itself
     const int i = threadIdx.x & 63;
-    const float ex = i < stat_tiles ? exponent[i * tpad + j] : kNoExponent, sm = i < stat_tiles ? sum[i * tpad + j] : 0.f;
+    const float ex = i < stat_tiles ? exponent[i * tpad + j] : kNoExponent;
+    const float sm = i < stat_tiles ? sum[i * tpad + j] : 0.f, rm = i < stat_tiles ? rounded[i * tpad + j] : 0.f;
     n = ex;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) n = fmaxf(n, __shfl_xor(n, d));
-    s = sm * __builtin_amdgcn_exp2f(-fminf(n - ex, 300.f));
+    const float f = __builtin_amdgcn_exp2f(-fminf(n - ex, 300.f));
+    s = sm * f;
+    rs = rm * f;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+    for (int d = 1; d < 64; d <<= 1) {
+      s += __shfl_xor(s, d);
+      rs += __shfl_xor(rs, d);
+    }
   } else {
     n = N[j];
     s = S[j];
+    rs = R[j];
   }
-  const Outcome r = outcome(n, s, target_logit[j]);
+  const Outcome r = outcome(n, s, rs, target_logit[j]);
   if (threadIdx.x == 0) {
     loss[t] = r.loss;
     if (lse) lse[t] = r.lse;
@@ -603,14 +648,15 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 constexpr int kFewWords = 64;       // words that share an exponent, and a step of the gradient
 constexpr int kFewChunk = 128;      // steps of a chunk at most: its shift bytes are held in LDS
 
-// e (nullptr: the loss alone) [T][pitch], exponent and sum [64 words][tpad]; v0: the piece's first word, which is
+// e (nullptr: the loss alone, and no rounded) [T][pitch], exponent, sum and rounded [64 words][tpad]; v0: the piece's first word, which is
 // also the first column of e.  Workgroups: the token groups of 64 words, then the next words'.
 // kPacked: the rows are decoded from q on their way in (w unused, v0 = 0).
 template <int NT, bool kPacked>
 __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
     const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, QWeight q, Codebook cb,
     const int64_t *__restrict__ target, int T, int64_t v0, int64_t nv, int D, uint16_t *__restrict__ e, int64_t pitch,
-    float *__restrict__ exponent, float *__restrict__ sum, int tpad, float *__restrict__ target_logit) {
+    float *__restrict__ exponent, float *__restrict__ sum, float *__restrict__ rounded, int tpad,
+    float *__restrict__ target_logit) {
   constexpr int kBytes = (kPacked ? 2 : few_stages<false, NT>()) * few_stage<NT>();
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -654,8 +700,7 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
 #pragma unroll
   for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
   const float ex = tile_exponent(top);
-  float s = 0.f;
-  uint32_t packed[kWords / 2];
+  float s = 0.f, r = 0.f;
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
     float p = relative_exp(l[i], ex);
@@ -667,36 +712,43 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
     s += p;
     l[i] = p;
   }
-  if (e && on) {
-#pragma unroll
-    for (int i = 0; i < kWords / 2; ++i) packed[i] = pack_bf16x2(l[2 * i], l[2 * i + 1]);
+  if (e) {
     uint2 *row = (uint2 *)(e + (int64_t)t * pitch + v0 + vt + first);
 #pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) row[i] = make_uint2(packed[2 * i], packed[2 * i + 1]);
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint2 v = make_uint2(pack_bf16x2(l[4 * i], l[4 * i + 1]), pack_bf16x2(l[4 * i + 2], l[4 * i + 3]));
+      if (on) row[i] = v;
+      r = add_pair(v.y, add_pair(v.x, r));
+    }
   }
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) s += __shfl_xor(s, d);
+  for (int d = 1; d < kLanes; d <<= 1) {
+    s += __shfl_xor(s, d);
+    r += __shfl_xor(r, d);
+  }
   if (on && lane % kLanes == 0) {
     const int64_t i = (v0 + vt) / kFewWords * tpad + t;
     exponent[i] = ex;
     sum[i] = s;
+    if (e) rounded[i] = r;
   }
 }
 
 // One chunk of words, 64 columns; few_logits' statistics of the chunk are folded on the way.  part[chunk][T][D] relative
-// to 2^N of the chunk, and (first columns) its N and S [chunk][tpad].  e, exponent and sum start at the piece.
+// to 2^N of the chunk, and (first columns) its N, S and R [chunk][tpad].  e, exponent and the sums start at the piece.
 template <int NT, bool kPacked>
 __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__restrict__ e, int64_t pitch,
                                                            const uint16_t *__restrict__ w, QWeight q, Codebook cb,
                                                            int T, int64_t nv, int D, int chunk_steps, int chunk0,
                                                            const float *__restrict__ exponent,
-                                                           const float *__restrict__ sum, int tpad,
+                                                           const float *__restrict__ sum,
+                                                           const float *__restrict__ rounded, int tpad,
                                                            float *__restrict__ N, float *__restrict__ S,
-                                                           float *__restrict__ part) {
+                                                           float *__restrict__ R, float *__restrict__ part) {
   constexpr int kBytes = (kPacked ? 2 : few_stages<true, NT>()) * few_stage<NT>(), kT = 16 * NT, kRows = kFewThreads / kT;
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   __shared__ uint8_t shifts[kFewChunk * kT];
-  __shared__ float fold[kFewThreads];
+  __shared__ float fold[kFewThreads], fold_r[kFewThreads];
   // places: the slices of a chunk for one token group, then its other token groups, then the next chunk
   const int slices = D / 64, groups = tpad / kFewTokens, place = place_of(blockIdx.x, gridDim.x);
   const int over = scalar(place / slices), slice = scalar(place - over * slices);
@@ -709,6 +761,7 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
     const int t = threadIdx.x % kT, g = threadIdx.x / kT;
     const float *ex = exponent + vb / kFewWords * tpad + min(t0 + t, T - 1);
     const float *sm = sum + vb / kFewWords * tpad + min(t0 + t, T - 1);
+    const float *rm = rounded + vb / kFewWords * tpad + min(t0 + t, T - 1);
     float top = kNoExponent;
 #pragma unroll 8
     for (int i = g; i < steps; i += kRows) top = fmaxf(top, ex[i * tpad]);
@@ -717,19 +770,29 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
 #pragma unroll
     for (int i = 0; i < kRows; ++i) top = fmaxf(top, fold[i * kT + t]);
     __syncthreads();
-    float s = 0.f;
+    float s = 0.f, r = 0.f;
 #pragma unroll 8
     for (int i = g; i < steps; i += kRows) {
       const float d = top - ex[i * tpad];
       shifts[i * kT + t] = (uint8_t)fminf(d, 255.f);
-      if (slice == 0) s += sm[i * tpad] * __builtin_amdgcn_exp2f(-fminf(d, 300.f));
+      if (slice == 0) {
+        const float f = __builtin_amdgcn_exp2f(-fminf(d, 300.f));
+        s += sm[i * tpad] * f;
+        r += rm[i * tpad] * f;
+      }
     }
     fold[threadIdx.x] = s;
+    fold_r[threadIdx.x] = r;
     __syncthreads();
     if (slice == 0 && g == 0 && t0 + t < T) {
-      for (int i = 1; i < kRows; ++i) s += fold[i * kT + t];
-      N[(int64_t)(chunk0 + chunk) * tpad + t0 + t] = top;
-      S[(int64_t)(chunk0 + chunk) * tpad + t0 + t] = s;
+      for (int i = 1; i < kRows; ++i) {
+        s += fold[i * kT + t];
+        r += fold_r[i * kT + t];
+      }
+      const int64_t at = (int64_t)(chunk0 + chunk) * tpad + t0 + t;
+      N[at] = top;
+      S[at] = s;
+      R[at] = r;
     }
   }
   uint32_t off[2 * NT];
@@ -804,7 +867,7 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
     __syncthreads();
   }
   if (tid == 0) {
-    const Outcome r = outcome(top, fold[0], target_logit[t]);
+    const Outcome r = outcome(top, fold[0], fold[0], target_logit[t]);
     loss[t] = r.loss;
     if (lse) lse[t] = r.lse;
   }
@@ -814,7 +877,7 @@ __global__ __launch_bounds__(256) void few_losses(const int64_t *__restrict__ ta
 // chunk a thread, so that the chunks' sums (from the caches of other XCDs) arrive in few round trips.
 __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ target, int T, int64_t V, int D,
                                                   int chunks, const float *__restrict__ N, const float *__restrict__ S,
-                                                  int tpad, const float *__restrict__ target_logit,
+                                                  const float *__restrict__ R, int tpad, const float *__restrict__ target_logit,
                                                   const uint16_t *__restrict__ w, QWeight q, Codebook cb,
                                                   const float *__restrict__ weight, float scale,
                                                   const float *__restrict__ part, uint32_t *__restrict__ state,
@@ -833,15 +896,21 @@ __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ ta
     if (lead) no_loss(y, t, loss, lse);
     return;
   }
-  // N and S: the chunks one a lane, every wave for itself
-  float top = kNoExponent, s = 0.f;
+  // N, S and R: the chunks one a lane, every wave for itself
+  float top = kNoExponent, s = 0.f, rs = 0.f;
   for (int i = lane; i < chunks; i += 64) top = fmaxf(top, N[(int64_t)i * tpad + t]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-  for (int i = lane; i < chunks; i += 64)
-    s += S[(int64_t)i * tpad + t] * __builtin_amdgcn_exp2f(-fminf(top - N[(int64_t)i * tpad + t], 300.f));
+  for (int i = lane; i < chunks; i += 64) {
+    const float f = __builtin_amdgcn_exp2f(-fminf(top - N[(int64_t)i * tpad + t], 300.f));
+    s += S[(int64_t)i * tpad + t] * f;
+    rs += R[(int64_t)i * tpad + t] * f;
+  }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+  for (int d = 1; d < 64; d <<= 1) {
+    s += __shfl_xor(s, d);
+    rs += __shfl_xor(rs, d);
+  }
   f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
   const float *p = part + (int64_t)t * D + min(c, D - 8);
   for (int i0 = group; i0 < chunks; i0 += 16) {
@@ -868,7 +937,7 @@ __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ ta
     half[group - 1][lane][1] = hi;
   }
   __syncthreads();
-  const Outcome r = outcome(top, s, target_logit[t]);
+  const Outcome r = outcome(top, s, rs, target_logit[t]);
   if (lead) {
     loss[t] = r.loss;
     if (lse) lse[t] = r.lse;
@@ -923,8 +992,10 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
   p.off_logit = take((size_t)p.tpad * 4);
   p.off_exponent = take((size_t)groups * p.tpad * 4);
   p.off_sum = take((size_t)groups * p.tpad * 4);
+  p.off_rounded = p.grad ? take((size_t)groups * p.tpad * 4) : 0;
   p.off_n = take((size_t)p.splits * p.tpad * 4);
   p.off_s = take((size_t)p.splits * p.tpad * 4);
+  p.off_r = take((size_t)p.splits * p.tpad * 4);
   p.off_e = p.grad ? take((size_t)p.T * groups * kFewWords * 2) : 0;
   p.off_part = p.grad ? take((size_t)p.splits * p.T * p.D * 4) : 0;
   p.off_w = p.decode ? take((size_t)p.words * p.D * 2) : 0;
@@ -956,6 +1027,7 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
                              uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st) {
   uint32_t *state = (uint32_t *)ws;
   float *logit = (float *)(ws + p.off_logit), *N = (float *)(ws + p.off_n), *S = (float *)(ws + p.off_s);
+  float *R = (float *)(ws + p.off_r), *rounded = (float *)(ws + p.off_rounded);
   float *exponent = (float *)(ws + p.off_exponent), *sum = (float *)(ws + p.off_sum);
   float *part = (float *)(ws + p.off_part);
   uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
@@ -973,20 +1045,20 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
       if (err != hipSuccess) return err;
     }
     few_logits<NT, kPacked><<<(unsigned)(cdiv(nv, kFewWords) * token_groups), kFewThreads, 0, st>>>(
-        h, piece, qw, cb, target, T, v0, nv, D, e, pitch, exponent, sum, tpad, logit);
+        h, piece, qw, cb, target, T, v0, nv, D, e, pitch, exponent, sum, rounded, tpad, logit);
     if (!p.grad) continue;
     const int chunks = (int)cdiv(nv, p.split_words);
     const int64_t g0 = v0 / kFewWords * tpad;
     few_grad<NT, kPacked><<<(unsigned)(chunks * token_groups * (D / 64)), kFewThreads, 0, st>>>(
-        e + v0, pitch, piece, qw, cb, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0, tpad,
-        N, S, part);
+        e + v0, pitch, piece, qw, cb, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0,
+        rounded + g0, tpad, N, S, R, part);
     chunk0 += chunks;
   }
   if (!p.grad) {
     few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, tpad, logit, state, loss, lse);
     return hipGetLastError();
   }
-  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, tpad,
+  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, R, tpad,
                                                                        logit, w, qw, cb, weight, scale, part, state,
                                                                        loss, lse, grad);
   return hipGetLastError();
@@ -1052,9 +1124,11 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.off_logit = take((size_t)p.chunk * 4);
   p.off_n = take((size_t)p.chunk * 4);
   p.off_s = take((size_t)p.chunk * 4);
+  p.off_r = take((size_t)p.chunk * 4);
   p.off_factor = take((size_t)p.chunk * 4);
   p.off_exponent = take((size_t)stat * 4);
   p.off_sum = take((size_t)stat * 4);
+  p.off_rounded = grad ? take((size_t)stat * 4) : 0;
   p.off_shift = grad ? take((size_t)stat / 4) : 0;
   p.off_e = grad ? take((size_t)p.chunk * p.words * 2) : 0;
   p.off_part = grad ? take((size_t)p.splits * kTileT * kTileV * 4) : 0;
@@ -1079,6 +1153,7 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
   float *logit = (float *)(ws + p.off_logit), *N = (float *)(ws + p.off_n), *S = (float *)(ws + p.off_s);
   float *factor = (float *)(ws + p.off_factor), *exponent = (float *)(ws + p.off_exponent);
   float *sum = (float *)(ws + p.off_sum), *part = (float *)(ws + p.off_part);
+  float *R = (float *)(ws + p.off_r), *rounded = (float *)(ws + p.off_rounded);
   uint8_t *shift = p.grad ? (uint8_t *)(ws + p.off_shift) : nullptr;
   uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
   uint16_t *wp = (uint16_t *)(ws + p.off_w);
@@ -1102,11 +1177,13 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
       }
       const auto logits = list ? head_logits<true> : head_logits<false>;
       logits<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(hc, piece, yc, T, p.V, v0, nv, D, nleft, rows, place, state,
-                                                            lc, ec, e, p.words, exponent, sum, p.tpad, logit);
-      if (!fold)
-        head_fold<<<(unsigned)cdiv(T, 8), 256, 0, st>>>(exponent, sum, p.tpad, (int)cdiv(nv, kStatV), v0 == 0, state, N,
-                                                        S, shift, factor, rows, logit, last && !p.grad ? lc : nullptr,
-                                                        ec);
+                                                            lc, ec, e, p.words, exponent, sum, rounded, p.tpad, logit);
+      if (!fold) {
+        const auto collect = p.grad ? head_fold<true> : head_fold<false>;
+        collect<<<(unsigned)cdiv(T, 8), 256, 0, st>>>(exponent, sum, rounded, p.tpad, (int)cdiv(nv, kStatV), v0 == 0,
+                                                      state, N, S, R, shift, factor, rows, logit,
+                                                      last && !p.grad ? lc : nullptr, ec);
+      }
       if (!p.grad) continue;
       const auto product = fold ? head_grad<true> : head_grad<false>;
       product<<<(unsigned)p.splits, kThreads, 0, st>>>(  // enough for any number of live tokens
@@ -1114,7 +1191,7 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
     }
     if (!p.grad) continue;
     const auto finish = fold ? head_finish<true> : head_finish<false>;
-    finish<<<(unsigned)T, 256, 0, st>>>(place, N, S, exponent, sum, p.tpad, (int)cdiv(p.V, kStatV), logit, yc, w,
+    finish<<<(unsigned)T, 256, 0, st>>>(place, N, S, R, exponent, sum, rounded, p.tpad, (int)cdiv(p.V, kStatV), logit, yc, w,
                                         q ? *q : QWeight{}, cb, weight ? weight + c0 : nullptr, scale, part, words, nd,
                                         state, D, lc, ec, grad + c0 * p.D);
   }

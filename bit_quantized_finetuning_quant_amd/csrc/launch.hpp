@@ -278,8 +278,8 @@ struct HeadPlan {
   bool few;     // few: the few-token form (splits: chunks of words in all, split_words: of
   // each); otherwise splits: the gradient's partial tiles
   int64_t chunk, tpad, words, pieces, splits, split_words;
-  size_t off_rows, off_place, off_logit, off_n, off_s, off_factor, off_exponent, off_sum, off_shift, off_e, off_part,
-      off_w, total;
+  size_t off_rows, off_place, off_logit, off_n, off_s, off_r, off_factor, off_exponent, off_sum, off_rounded, off_shift,
+      off_e, off_part, off_w, total;
 };
 HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed);
 // w (bf16 [V x D]) or q (packed), the other one nullptr; weight, lse may be nullptr; grad nullptr iff !p.grad.

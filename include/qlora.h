@@ -385,7 +385,9 @@ size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t
  * h [T x D] bf16, target [T] int64, weight [T] fp32 or NULL (all ones), loss
  * and lse [T] fp32 (lse may be NULL), grad_h [T x D] bf16 (NULL: the loss
  * alone, for evaluation).  loss and lse are per token, without scale and
- * weight: the gradient is that of sum_t scale weight_t loss_t.
+ * weight: the gradient is that of sum_t scale weight_t loss_t.  Its product
+ * takes the exponentials in bf16 (2^-8 of each) and divides by the sum of these
+ * rounded values, so the words' weights and the target's sum to zero.
  * A negative target marks a token without loss (padding, a prompt): its loss,
  * lse and gradient are 0, whatever its row of h holds.  A target >= V gives
  * NaN in that token's loss, lse and gradient, and qlora_status_read on ws

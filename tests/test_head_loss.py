@@ -387,6 +387,56 @@ def test_a_given_streams_memory_is_its_own():
         assert torch.equal(a, b)
 
 
+def _exact_inputs(T, D, V, seed, similar):
+    """h and W of multiples of 2^-3 and 2^-5 below 16 and 2: every partial sum of a logit is a multiple of 2^-8 below
+    2^14, so the logits are exact in fp32.  Token t leans by 20 to 60 logits to a word that is not its target and
+    whose row is `similar` to the target's row (the cosine between them)."""
+    torch = torch_mod()
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    w = torch.round(n(V, D) * 8).clamp(-63, 63) / 32
+    order = torch.randperm(V, generator=g)
+    wrong, y = order[:T], order[T:2 * T]
+    w[wrong] = torch.round((similar * w[y] + (1 - similar**2) ** 0.5 * 0.25 * n(T, D)) * 32).clamp(-63, 63) / 32
+    lean = torch.linspace(20, 60, T)[:, None] / w[wrong].square().sum(1, keepdim=True)
+    h = (torch.round(lean * w[wrong] * 8) / 8).clamp(-15, 15)
+    assert float((h.abs() @ w.abs().t()).max()) < 2**14
+    y[3::7] = -100
+    return h.bfloat16(), w.bfloat16(), y
+
+
+@gpu
+@pytest.mark.parametrize("similar", [0.0, 0.9])
+@pytest.mark.parametrize("T,D,V", [(1, 256, 300), (16, 512, 5000), (30, 256, 4000), (64, 256, 9000), (200, 256, 3000),
+                                   (300, 1024, 7000), (512, 512, 8192), (512, 256, 17000), (700, 256, 9001),
+                                   (2050, 256, 33000)])
+def test_sure_of_a_wrong_word(T, D, V, similar):
+    """The gradient of a token that is sure of a word other than its target is c p (W_word - W_target), however
+    much of it cancels where the two rows are alike: the weights of the words sum to what the target's row is
+    subtracted with.  With e_v (1 + d_v) in place of e_v, |d_v| <= 2^-8, in the product AND in the sum, and
+    x the p-weighted sum of d over v != y, the gradient is off by
+      sum_{v != y} p_v (d_v - x) (W_v - W_y) / (1 + x),   |d_v - x| <= 2^-8 min(2 (1 - p_v), 1 + (1 - p_y)),
+    then V 2^-24 of the absolute terms of the product and of the sum, 2^-19 for exp2 and the factors, and 2^-8 of
+    the result for its own rounding.  (No term for the logits: they are exact here.)"""
+    torch = torch_mod()
+    announce(f"head loss sure of a wrong word T={T} D={D} V={V} similar={similar}")
+    h, w, y = (t.cuda() for t in _exact_inputs(T, D, V, seed=T + V, similar=similar))
+    _, _, grad = qlora.head_loss(h, w, y, scale=0.5)
+    torch.cuda.synchronize()
+    hd, wd = h.double(), w.double()
+    live = torch.nonzero(y >= 0)[:, 0]
+    for t in live.tolist()[::max(1, live.numel() // 60)]:
+        p = torch.softmax(torch.mv(wd, hd[t]), 0)
+        diff = wd - wd[y[t]]
+        p[y[t]] = 0  # its own term: (p_y - p_y - (1 - p_y)) W_y is in the difference
+        rest = float(p.sum())
+        want = 0.5 * torch.mv(diff.t(), p)
+        spread = p * torch.minimum(2 * (1 - p), torch.full_like(p, 1 + rest))
+        tol = 0.5 * (2.0**-8 / (1 - 2.0**-8) * torch.mv(diff.abs().t(), spread)
+                     + (V * 2.0**-24 + 2.0**-19) * (torch.mv(wd.abs().t(), p) + rest * wd[y[t]].abs())) + 2.0**-8 * want.abs()
+        _close(grad[t], want, tol, f"grad_h of token {t}")
+
+
 # ------------------------------------------------------------------- refusals (no GPU)
 def _call(h=0x10000, T=4, w=0x20000, V=100, D=128, y=0x30000, weight=None, scale=1.0, loss=0x40000, lse=None,
           grad=0x50000, ws=0x60000, ws_bytes=0):
