@@ -648,9 +648,9 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 constexpr int kFewWords = 64;       // words that share an exponent, and a step of the gradient
 constexpr int kFewChunk = 128;      // steps of a chunk at most: its shift bytes are held in LDS
 
-// e (nullptr: the loss alone, and no rounded) [T][pitch], exponent, sum and rounded [64 words][tpad]; v0: the piece's first word, which is
-// also the first column of e.  Workgroups: the token groups of 64 words, then the next words'.
-// kPacked: the rows are decoded from q on their way in (w unused, v0 = 0).
+// e (nullptr: the loss alone, and no rounded) [T][pitch] of the piece, exponent, sum and rounded [64 words][tpad] of
+// all words; v0: the piece's first word.  Workgroups: the token groups of 64 words, then the next words'.
+// kPacked: the rows are decoded from q, the piece's, on their way in (w unused).
 template <int NT, bool kPacked>
 __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
     const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, QWeight q, Codebook cb,
@@ -713,7 +713,7 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
     l[i] = p;
   }
   if (e) {
-    uint2 *row = (uint2 *)(e + (int64_t)t * pitch + v0 + vt + first);
+    uint2 *row = (uint2 *)(e + (int64_t)t * pitch + vt + first);
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
       const uint2 v = make_uint2(pack_bf16x2(l[4 * i], l[4 * i + 1]), pack_bf16x2(l[4 * i + 2], l[4 * i + 3]));
@@ -734,21 +734,27 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) void few_logits(
   }
 }
 
+// What a chunk's slot holds beside its sums: N, S and R [chunk][tpad].
+struct FewSlots {
+  float *N, *S, *R;
+};
+
 // One chunk of words, 64 columns; few_logits' statistics of the chunk are folded on the way.  part[chunk][T][D] relative
-// to 2^N of the chunk, and (first columns) its N, S and R [chunk][tpad].  e, exponent and the sums start at the piece.
+// to 2^N of the chunk, and (first columns) its N, S and R in `now`.  exponent and the sums start at the piece.  The
+// pieces of a vocabulary share the slots: from the second on (first = false) a chunk's sums are added to what part
+// and `before` hold of the pieces before, also where the last piece has no words for it.
 template <int NT, bool kPacked>
 __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__restrict__ e, int64_t pitch,
                                                            const uint16_t *__restrict__ w, QWeight q, Codebook cb,
-                                                           int T, int64_t nv, int D, int chunk_steps, int chunk0,
+                                                           int T, int64_t nv, int D, int chunk_steps, bool first,
                                                            const float *__restrict__ exponent,
                                                            const float *__restrict__ sum,
                                                            const float *__restrict__ rounded, int tpad,
-                                                           float *__restrict__ N, float *__restrict__ S,
-                                                           float *__restrict__ R, float *__restrict__ part) {
+                                                           FewSlots before, FewSlots now, float *__restrict__ part) {
   constexpr int kBytes = (kPacked ? 2 : few_stages<true, NT>()) * few_stage<NT>(), kT = 16 * NT, kRows = kFewThreads / kT;
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   __shared__ uint8_t shifts[kFewChunk * kT];
-  __shared__ float fold[kFewThreads], fold_r[kFewThreads];
+  __shared__ float fold[kFewThreads], fold_r[kFewThreads], factor[kT][2];  // factors: of the sums before and of these
   // places: the slices of a chunk for one token group, then its other token groups, then the next chunk
   const int slices = D / 64, groups = tpad / kFewTokens, place = place_of(blockIdx.x, gridDim.x);
   const int over = scalar(place / slices), slice = scalar(place - over * slices);
@@ -784,15 +790,25 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
     fold[threadIdx.x] = s;
     fold_r[threadIdx.x] = r;
     __syncthreads();
-    if (slice == 0 && g == 0 && t0 + t < T) {
-      for (int i = 1; i < kRows; ++i) {
-        s += fold[i * kT + t];
-        r += fold_r[i * kT + t];
+    if (g == 0 && t0 + t < T) {
+      const int64_t at = (int64_t)chunk * tpad + t0 + t;
+      float n = top, f = 1.f;
+      if (!first) {
+        const float old = before.N[at];
+        n = fmaxf(top, old);
+        f = __builtin_amdgcn_exp2f(-fminf(n - top, 300.f));
+        factor[t][0] = __builtin_amdgcn_exp2f(-fminf(n - old, 300.f));
+        factor[t][1] = f;
       }
-      const int64_t at = (int64_t)(chunk0 + chunk) * tpad + t0 + t;
-      N[at] = top;
-      S[at] = s;
-      R[at] = r;
+      if (slice == 0) {
+        for (int i = 1; i < kRows; ++i) {
+          s += fold[i * kT + t];
+          r += fold_r[i * kT + t];
+        }
+        now.N[at] = n;
+        now.S[at] = first ? s : before.S[at] * factor[t][0] + s * f;
+        now.R[at] = first ? r : before.R[at] * factor[t][0] + r * f;
+      }
     }
   }
   uint32_t off[2 * NT];
@@ -816,8 +832,14 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int t = i * 16 + (threadIdx.x >> 4), d = 4 * (threadIdx.x & 15);
-    if (t0 + t < T)
-      *(f32x4 *)(part + ((int64_t)(chunk0 + chunk) * T + t0 + t) * D + 64 * slice + d) = few_sum<NT>(red, t, d);
+    if (t0 + t >= T) continue;
+    f32x4 sums = few_sum<NT>(red, t, d), *p = (f32x4 *)(part + ((int64_t)chunk * T + t0 + t) * D + 64 * slice + d);
+    if (!first) {
+      const f32x4 old = *p;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sums[q] = __builtin_fmaf(old[q], factor[t][0], sums[q] * factor[t][1]);
+    }
+    *p = sums;
   }
 }
 
@@ -967,7 +989,10 @@ __global__ __launch_bounds__(256) void few_finish(const int64_t *__restrict__ ta
 
 }  // namespace
 
-// The few-token form: e [T][V], the sums of every chunk of words.
+// What a workspace holds of e, of decoded rows (values of two bytes) and of fp32 sums (bytes) at most, see plan_head.
+constexpr int64_t kPieceValues = (int64_t)64 << 20, kPartBytes = (int64_t)128 << 20, kStatBytes = (int64_t)64 << 20;
+
+// The few-token form in pieces of up to `piece` words: e of a piece, the sums of every chunk of words.
 static HeadPlan plan_few(HeadPlan p, int64_t piece) {
   p.pieces = cdiv(p.V, piece);
   p.words = cdiv(cdiv(p.V, p.pieces), kTileV) * kTileV;
@@ -981,7 +1006,7 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
         std::max<int64_t>(1, std::min(256 / (p.D / 64 * (p.tpad / kFewTokens)), cdiv(piece_steps, 4)));
     const int64_t steps = std::min<int64_t>(kFewChunk, cdiv(piece_steps, chunks));
     p.split_words = steps * kFewWords;
-    for (int64_t v0 = 0; v0 < p.V; v0 += p.words) p.splits += cdiv(std::min(p.words, p.V - v0), p.split_words);
+    p.splits = cdiv(std::min(p.words, p.V), p.split_words);  // of a piece; the next pieces' are added to them
   }
   size_t off = 256;
   auto take = [&off](size_t bytes) {
@@ -993,10 +1018,11 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
   p.off_exponent = take((size_t)groups * p.tpad * 4);
   p.off_sum = take((size_t)groups * p.tpad * 4);
   p.off_rounded = p.grad ? take((size_t)groups * p.tpad * 4) : 0;
-  p.off_n = take((size_t)p.splits * p.tpad * 4);
-  p.off_s = take((size_t)p.splits * p.tpad * 4);
-  p.off_r = take((size_t)p.splits * p.tpad * 4);
-  p.off_e = p.grad ? take((size_t)p.T * groups * kFewWords * 2) : 0;
+  const int64_t sides = p.pieces > 1 ? 2 : 1;  // a piece's slots and those of the piece before
+  p.off_n = take((size_t)sides * p.splits * p.tpad * 4);
+  p.off_s = take((size_t)sides * p.splits * p.tpad * 4);
+  p.off_r = take((size_t)sides * p.splits * p.tpad * 4);
+  p.off_e = p.grad ? take((size_t)p.T * piece_steps * kFewWords * 2) : 0;
   p.off_part = p.grad ? take((size_t)p.splits * p.T * p.D * 4) : 0;
   p.off_w = p.decode ? take((size_t)p.words * p.D * 2) : 0;
   p.off_rows = p.off_place = p.off_factor = p.off_shift = 0;
@@ -1004,10 +1030,8 @@ static HeadPlan plan_few(HeadPlan p, int64_t piece) {
   return p;
 }
 
-// Rows v0 .. v0 + nv of a packed head, decoded to out; v0 is a multiple of 256, so whole groups of
-// constants lie before it.
-static hipError_t decode_rows(const QWeight &q, int64_t v0, int64_t nv, uint16_t *out, const Codebook &cb,
-                              hipStream_t st) {
+// Rows v0 .. v0 + nv of a packed head; v0 is a multiple of 256, so whole groups of constants lie before it.
+static QWeight rows_of(const QWeight &q, int64_t v0, int64_t nv) {
   QWeight rows = q;
   const int64_t block = v0 * q.n_in / kBlock;
   rows.n_out = nv;
@@ -1018,7 +1042,7 @@ static hipError_t decode_rows(const QWeight &q, int64_t v0, int64_t nv, uint16_t
   } else {
     rows.s2 += block;
   }
-  return launch_dequantize(rows, out, cb, st);
+  return rows;
 }
 
 template <int NT, bool kPacked>
@@ -1026,39 +1050,44 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
                              const int64_t *target, const float *weight, float scale, float *loss, float *lse,
                              uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st) {
   uint32_t *state = (uint32_t *)ws;
-  float *logit = (float *)(ws + p.off_logit), *N = (float *)(ws + p.off_n), *S = (float *)(ws + p.off_s);
-  float *R = (float *)(ws + p.off_r), *rounded = (float *)(ws + p.off_rounded);
+  float *logit = (float *)(ws + p.off_logit), *rounded = (float *)(ws + p.off_rounded);
   float *exponent = (float *)(ws + p.off_exponent), *sum = (float *)(ws + p.off_sum);
+  auto slots = [&](bool odd) {
+    const int64_t side = odd ? p.splits * p.tpad : 0;
+    return FewSlots{(float *)(ws + p.off_n) + side, (float *)(ws + p.off_s) + side, (float *)(ws + p.off_r) + side};
+  };
+  FewSlots before{}, now{};
   float *part = (float *)(ws + p.off_part);
   uint16_t *e = p.grad ? (uint16_t *)(ws + p.off_e) : nullptr;
   uint16_t *wp = (uint16_t *)(ws + p.off_w);
   const int T = (int)p.T, D = (int)p.D, groups = (int)cdiv(p.V, kFewWords), tpad = (int)p.tpad;
   const int token_groups = tpad / kFewTokens;
   const QWeight qw = q ? *q : QWeight{};
-  const int64_t pitch = (int64_t)groups * kFewWords;
-  int chunk0 = 0;
+  const int64_t pitch = cdiv(std::min(p.words, p.V), kFewWords) * kFewWords;
   for (int64_t v0 = 0; v0 < p.V; v0 += p.words) {
     const int64_t nv = std::min(p.words, p.V - v0);
     const uint16_t *piece = w ? w + v0 * p.D : wp;
     if (p.decode) {
-      const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
+      const hipError_t err = launch_dequantize(rows_of(*q, v0, nv), wp, cb, st);
       if (err != hipSuccess) return err;
     }
+    const QWeight rows = kPacked ? rows_of(*q, v0, nv) : QWeight{};
     few_logits<NT, kPacked><<<(unsigned)(cdiv(nv, kFewWords) * token_groups), kFewThreads, 0, st>>>(
-        h, piece, qw, cb, target, T, v0, nv, D, e, pitch, exponent, sum, rounded, tpad, logit);
+        h, piece, rows, cb, target, T, v0, nv, D, e, pitch, exponent, sum, rounded, tpad, logit);
     if (!p.grad) continue;
-    const int chunks = (int)cdiv(nv, p.split_words);
     const int64_t g0 = v0 / kFewWords * tpad;
-    few_grad<NT, kPacked><<<(unsigned)(chunks * token_groups * (D / 64)), kFewThreads, 0, st>>>(
-        e + v0, pitch, piece, qw, cb, T, nv, D, (int)(p.split_words / kFewWords), chunk0, exponent + g0, sum + g0,
-        rounded + g0, tpad, N, S, R, part);
-    chunk0 += chunks;
+    before = now;
+    now = slots((v0 / p.words & 1) != 0);
+    few_grad<NT, kPacked><<<(unsigned)(p.splits * token_groups * (D / 64)), kFewThreads, 0, st>>>(
+        e, pitch, piece, rows, cb, T, nv, D, (int)(p.split_words / kFewWords), v0 == 0, exponent + g0, sum + g0,
+        rounded + g0, tpad, before, now, part);
   }
   if (!p.grad) {
     few_losses<<<(unsigned)T, 256, 0, st>>>(target, T, p.V, groups, exponent, sum, tpad, logit, state, loss, lse);
     return hipGetLastError();
   }
-  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, N, S, R, tpad,
+  few_finish<<<dim3((unsigned)T, (unsigned)cdiv(D, 512)), 256, 0, st>>>(target, T, p.V, D, (int)p.splits, now.N, now.S,
+                                                                       now.R, tpad,
                                                                        logit, w, qw, cb, weight, scale, part, state,
                                                                        loss, lse, grad);
   return hipGetLastError();
@@ -1089,24 +1118,30 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.D = D;
   p.grad = grad;
   p.packed = p.decode = packed;
-  p.few = few_pays(T, V, D, grad);
   p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
-  p.tpad = cdiv(p.chunk, kTileT) * kTileT;
   // Words of a piece: 128 MB of e (grad) and of decoded weight (packed).  A larger piece leaves less of
   // the products' last rounds of workgroups empty (2048 tokens, 40% of them masked, V = 32000: 5 tiles of
   // tokens by 125 of words are three rounds of 256, two pieces of 63 and 62 four).
-  int64_t vc = cdiv(V, kTileV) * kTileV;
-  // The exponents and sums of its tiles stay within 64 MB too.
-  const int64_t budget = (int64_t)64 << 20;
-  if (p.few) {  // one piece, but for the decoded rows of a packed head
+  auto fit = [](int64_t per_word, int64_t least) {  // words of a piece, `least` tiles at least
+    return std::max(kPieceValues / per_word / kTileV, least) * kTileV;
+  };
+  const int64_t whole = cdiv(V, kTileV) * kTileV;
+  p.few = few_pays(T, V, D, grad);
+  if (p.few) {
     p.decode = packed && T > kFewTokens;  // up to 64 tokens the streams decode the rows themselves
-    if (p.decode) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
-    return plan_few(p, vc);
+    int64_t vc = whole;
+    if (grad)  // also: as many chunks' sums as fit
+      vc = std::min({vc, fit(T, 4), std::max<int64_t>(kPartBytes / (T * D * 4), 1) * kFewChunk * kFewWords});
+    if (p.decode) vc = std::min(vc, fit(D, 4));
+    const HeadPlan few = plan_few(p, vc);
+    if ((cdiv(V, kFewWords) * (grad ? 12 : 8) + few.splits * 24) * few.tpad <= kStatBytes) return few;
+    p.few = false;
+    p.decode = packed;
   }
-  vc = std::min(vc, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
-  if (grad) vc = std::min<int64_t>(vc, kMaxPiece);
-  if (grad) vc = std::min(vc, std::max<int64_t>(budget / p.tpad / kTileV * kTileV, 8 * kTileV));
-  if (packed) vc = std::min(vc, std::max<int64_t>(budget / D / kTileV * kTileV, 4 * kTileV));
+  p.tpad = cdiv(p.chunk, kTileT) * kTileT;
+  int64_t vc = std::min(whole, std::max<int64_t>(((int64_t)1 << 30) / p.tpad / kTileV * kTileV, 8 * kTileV));
+  if (grad) vc = std::min<int64_t>(std::min<int64_t>(vc, kMaxPiece), fit(p.tpad, 8));
+  if (packed) vc = std::min(vc, fit(D, 4));
   p.pieces = cdiv(V, vc);
   p.words = cdiv(cdiv(V, p.pieces), kTileV) * kTileV;
   p.pieces = cdiv(V, p.words);
@@ -1172,7 +1207,7 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
       const bool last = v0 + nv == p.V;
       const uint16_t *piece = w ? w + v0 * p.D : wp;
       if (q) {
-        const hipError_t err = decode_rows(*q, v0, nv, wp, cb, st);
+        const hipError_t err = launch_dequantize(rows_of(*q, v0, nv), wp, cb, st);
         if (err != hipSuccess) return err;
       }
       const auto logits = list ? head_logits<true> : head_logits<false>;

@@ -408,10 +408,12 @@ qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_w
                                  void *ws, size_t ws_bytes, void *stream);
 
 /* Workspace bytes of the two calls (grad: with grad_h; packed: an NF4 head).
- * 0 on a bad shape.  Bounded whatever V is: tokens are taken 16384 at a time,
- * words in pieces of at most 128 MB of exponentials (with grad), 128 MB of
- * decoded rows (packed) and 128 MB of fp32 partial sums (with grad).  For
- * these sizes: fewer tokens may take another form and need more.              */
+ * 0 on a bad shape.  Bounded whatever T and V are: tokens are taken 16384 at a
+ * time, words in pieces.  At most 128 MB of exponentials (with grad), 128 MB of
+ * decoded rows (packed), 64 MB of exponents and sums, forty bytes a token taken,
+ * and (with grad) of fp32 partial sums 128 MB, or 4 T D bytes of the tokens taken
+ * where that is more (T and D in whole 256s).  For these sizes: fewer tokens may
+ * take another form and need more.                                            */
 size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad, int packed);
 
 /* ---- diagnostics ---------------------------------------------------------- */

@@ -124,6 +124,44 @@ def test_several_pieces_of_the_vocabulary(T, D, V):
 
 
 @gpu
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,D,V", [(100, 64, 1 << 20), (256, 64, (1 << 20) - 3), (40, 64, (1 << 20) + 77), (1, 128, 1100000),
+                                   (64, 65536, 65600)])
+def test_few_tokens_of_a_very_large_vocabulary(T, D, V, packed):
+    """The streams in several pieces, of exponentials or of chunks' sums, and the tiles for a few tokens of more words
+    than the streams take."""
+    torch = torch_mod()
+    announce(f"head loss of a very large vocabulary T={T} D={D} V={V} packed={packed}")
+    h, _, y = (t.cuda() for t in _inputs(T, D, V if D < 1000 else 4, seed=26))
+    w = torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(26)
+    for at in range(0, V, 1 << 16):
+        part = w[at:at + (1 << 16)]
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda") * (2 / math.sqrt(D)))
+    y[y >= 0] = torch.randint(0, V, (int((y >= 0).sum()),), generator=g, device="cuda")
+    y[0] = V - 1
+    q = qlora.quantize(w) if packed else w
+    _check(h, q, qlora.dequantize(q) if packed else w, y, scale=0.5)
+
+
+@gpu
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_exponents_of_the_streams_pieces(order):
+    """Logits that rise or fall by 120 over four pieces of the streams: the sums of the pieces before and the piece's
+    own are brought to one exponent."""
+    torch = torch_mod()
+    T, D, V = 256, 64, 1 << 20
+    announce(f"head loss, {order} logits over the pieces of the streams")
+    h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=27, std=0.05, masked=0.1))
+    ramp = torch.linspace(-60, 60, V, device="cuda")
+    h[:, 0] = 1.0
+    w[:, 0] = (ramp if order == "rising" else ramp.flip(0)).bfloat16()
+    y[::3] = V - 1
+    y[1::3] = 5
+    _check(h, w, w, y)
+
+
+@gpu
 def test_several_chunks_of_tokens():
     T, D, V = 16384 + 700, 64, 515
     announce(f"head loss in chunks T={T} D={D} V={V}")
@@ -470,6 +508,29 @@ def test_workspace_sizes():
     # and far below the fp32 logits
     assert b(16384, 128000, 4096) < 16384 * 128000 * 4 / 8
     assert b(1 << 20, 32000, 4096) == b(16384, 32000, 4096)
+
+
+def test_workspace_limits():
+    """The limits that the header states, over both forms: 128 MB of exponentials, 64 MB of exponents and sums, 128 MB
+    of partial sums or fp32 sums of the tokens taken at a time where these are more, 128 MB of decoded rows, and up to
+    forty bytes a token."""
+    MB = 1 << 20
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    for T in (1, 16, 33, 64, 65, 128, 256, 300, 512, 513, 1000, 4096, 16384, 100000):
+        for D in (64, 1024, 4096, 8192, 65536):
+            for V in (1, 300, 32000, 131072, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, 1 << 22, 1 << 31):
+                if V * D > 1 << 37:
+                    continue
+                tokens = min(T, 16384)
+                for grad in (False, True):
+                    for packed in (False, True):
+                        limit = 64 * MB + 40 * up(tokens) + 4096
+                        if grad:
+                            limit += 128 * MB + max(128 * MB, up(tokens) * up(D) * 4)
+                        if packed:
+                            limit += 128 * MB
+                        got = qlora.head_loss_workspace_bytes(T, V, D, grad, packed)
+                        assert 0 < got <= limit, (T, V, D, grad, packed, got / MB, limit / MB)
 
 
 def test_tensor_checks():
