@@ -204,6 +204,11 @@ def _alloc_on(stream):
     return nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
+def _on_boundary(t) -> bool:
+    """Whether a tensor may go to the C ABI as it is (None may)."""
+    return t is None or t.data_ptr() % 16 == 0
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -910,7 +915,8 @@ def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=N
     returns (loss, lse, grad_h or None).
 
     h [T x D] bf16; head: a bf16 tensor [V x D] or a packed NF4Weight; target [T] int64, negative where a
-    token carries no loss.  loss and lse [T] fp32 are per token; grad_h [T x D] bf16 is the gradient of
+    token carries no loss.  loss and lse [T] fp32 are per token (target, weight, loss and lse may be views at any
+    offset, which are copied; the matrices lie on 16-byte boundaries); grad_h [T x D] bf16 is the gradient of
     sum_t scale weight_t loss_t (weight [T] fp32, default ones).  A target >= V gives NaN, and
     status_read(workspace) then returns QLORA_ERR_VALUE (8)."""
     torch = _torch()
@@ -950,13 +956,21 @@ def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=N
         else:
             ws = workspace
             wsb = _workspace(ws, dev, lambda: head_loss_workspace_bytes(T, V, D, need_grad, packed))
-    if packed:
-        st = head.struct()
-        _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), _ptr(target), _ptr(weight), float(scale),
-                                         _ptr(loss), _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, handle),
-               "qlora_head_loss_nf4")
-    else:
-        _check(lib().qlora_head_loss(_ptr(h), T, _ptr(head), V, D, _ptr(target), _ptr(weight), float(scale), _ptr(loss),
-                                     _ptr(lse), _ptr(grad_h), _ptr(ws), wsb, handle),
-               "qlora_head_loss")
+        # the C ABI takes 16-byte aligned pointers; labels[1:] and the like go through copies of T values
+        y = target if _on_boundary(target) else target.clone()
+        wt = weight if _on_boundary(weight) else weight.clone()
+        to_loss, to_lse = (t if _on_boundary(t) else torch.empty_like(t) for t in (loss, lse))
+        if packed:
+            st = head.struct()
+            _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), _ptr(y), _ptr(wt), float(scale),
+                                             _ptr(to_loss), _ptr(to_lse), _ptr(grad_h), _ptr(ws), wsb, handle),
+                   "qlora_head_loss_nf4")
+        else:
+            _check(lib().qlora_head_loss(_ptr(h), T, _ptr(head), V, D, _ptr(y), _ptr(wt), float(scale), _ptr(to_loss),
+                                         _ptr(to_lse), _ptr(grad_h), _ptr(ws), wsb, handle),
+                   "qlora_head_loss")
+        if to_loss is not loss:
+            loss.copy_(to_loss)
+        if to_lse is not lse:
+            lse.copy_(to_lse)
     return loss, lse, grad_h

@@ -395,7 +395,9 @@ size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t
  * logit has a magnitude of 2.9e6 or more, gets NaN in all three.
  * Words more than 2^-60 below a token's most likely one may be left out.
  * Requires T >= 1, V >= 1, D % 64 == 0, D <= 65536, T D and V D <= 2^37, a
- * finite scale.  ws: qlora_head_loss_workspace_bytes, 16-B aligned.          */
+ * finite scale.  ws: qlora_head_loss_workspace_bytes.  target, weight, loss and
+ * lse are 16-byte aligned as every tensor here is (the Python binding copies
+ * views of them that are not).                                               */
 qlora_status qlora_head_loss(const uint16_t *h, int64_t T, const uint16_t *w, int64_t V, int64_t D,
                              const int64_t *target, const float *weight, float scale, float *loss, float *lse,
                              uint16_t *grad_h, void *ws, size_t ws_bytes, void *stream);

@@ -406,6 +406,61 @@ def test_two_streams_at_once_and_repeats_are_identical(T):
 
 
 @gpu
+@pytest.mark.parametrize("T", [9, 64, 511, 700])
+@pytest.mark.parametrize("side", [False, True])
+def test_views_of_per_token_vectors(T, side):
+    """Next-token targets are labels[1:], eight bytes off a 16-byte boundary; weights, losses and lse may be views of
+    longer buffers too.  The results are the aligned call's, and what lies beside the views stays as it was."""
+    torch = torch_mod()
+    D, V = 128, 900 if T < 550 else 20003
+    announce(f"head loss of views T={T} side={side}")
+    h, w, labels = (t.cuda() for t in _inputs(T + 1, D, V, seed=28, std=0.2))
+    h = h[:T]
+    weights = torch.rand(T + 3, device="cuda")
+    want = qlora.head_loss(h, w, labels[1:].clone(), weight=weights[3:].clone())
+    held = [torch.full((T + 5,), 7.0, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream() if side else None
+    got = qlora.head_loss(h, w, labels[1:], weight=weights[3:], loss=held[0][1:T + 1], lse=held[1][2:T + 2], stream=stream)
+    torch.cuda.synchronize()
+    assert got[0].data_ptr() == held[0].data_ptr() + 4 and got[1].data_ptr() == held[1].data_ptr() + 8
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for t, at in zip(held, (1, 2)):
+        assert (t[:at] == 7).all() and (t[at + T:] == 7).all()
+
+
+@gpu
+def test_captured_call_with_views():
+    """The copies of views are part of a captured call: replays read the targets of the day."""
+    torch = torch_mod()
+    T, D, V = 300, 128, 900
+    announce("head loss of views under graph capture")
+    h, w, labels = (t.cuda() for t in _inputs(T + 1, D, V, seed=29, std=0.2))
+    h = h[:T]
+    held = torch.zeros(T + 1, device="cuda")
+    ws = qlora.head_loss_workspace(T, V, D)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        qlora.head_loss(h, w, labels[1:], loss=held[1:], workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _, lse, grad = qlora.head_loss(h, w, labels[1:], loss=held[1:], workspace=ws)
+    for rep in range(3):
+        labels.copy_(_inputs(T + 1, D, V, seed=40 + rep)[2].cuda())
+        g.replay()
+        torch.cuda.synchronize()
+        got = [held[1:].clone(), lse.clone(), grad.clone()]
+        torch.zeros(1000, device="cuda").add_(1.0)
+        want = qlora.head_loss(h, w, labels[1:])
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), rep
+
+
+@gpu
 def test_a_given_streams_memory_is_its_own():
     """What a call on another stream than the current one allocates lies in that stream's memory pool: the
     workspace is given back when the call returns, before the kernels have run."""
