@@ -155,7 +155,13 @@ hipError_t launch_act8_decode(const int8_t *codes, const float *scale, int64_t T
 // fused GEMM and the adapter products (a checkpoint of a few tokens saves
 // nothing, so there is no few-token form).
 
-Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t K, int r) {
+// v's three planes, and the partial tiles of the products: those of one step are at most count + 1 products (grad_A and
+// every grad_B), of which one splits only with fewer than 256 tiles, in about 256 workgroups (510 at most).
+size_t act8_bound(int64_t T, int count, int r) {
+  return 256 + aligned((size_t)6 * T * count * r) + (size_t)(count + 1) * 510 * 64 * 64 * 4;
+}
+
+Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t K, int r, bool lean) {
   Act8BwdPlan p;
   p.T = T;
   p.K = K;
@@ -171,8 +177,12 @@ Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t
   off += aligned((size_t)3 * T * count * r * 2);
   p.off_part = off;
   off += aligned(lora_set_part_floats(T, count, N, K, r) * 4);
-  p.ragged = ragged_dx_applies(T, count, N, K, r);
+  p.ragged = !lean && ragged_dx_applies(T, count, N, K, r);
   p.off_qpart = p.off_rg = 0;
+  if (lean) {
+    p.total = off;
+    return p;
+  }
   if (p.ragged) {
     p.rg = plan_ragged_dx(T, count, N, K, r);
     p.off_rg = off;

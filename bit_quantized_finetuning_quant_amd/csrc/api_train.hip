@@ -64,7 +64,12 @@ size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t
   for (int i = 0; i < count; ++i)
     if (!linear_shape_ok(T, n_out[i], n_in, r)) return 0;
   if (!product_ok(T, (int64_t)count * r)) return 0;
-  return plan_linear_set_act8(T, count, n_out, n_in, r).total;
+  return plan_linear_set_act8(T, count, n_out, n_in, r, false).total;
+}
+
+size_t qlora_linear_set_act8_workspace_bound(int64_t T, int count, int r) {
+  if (count < 1 || count > kMaxSetMembers || r < 1 || r > 256 || !product_ok(T, (int64_t)count * r)) return 0;
+  return act8_bound(T, count, r);
 }
 
 qlora_status qlora_linear_set_bwd_act8(const uint16_t *const *dy, const qlora_act8 *a, int count,
@@ -87,8 +92,11 @@ qlora_status qlora_linear_set_bwd_act8(const uint16_t *const *dy, const qlora_ac
     if (!aligned16(dy[i]) || !aligned16(B[i]) || !aligned16(grad_B[i])) return QLORA_ERR_ALIGN;
     w[i] = qweight(&q[i]);
   }
-  const Act8BwdPlan p = plan_linear_set_act8(a->T, count, N, a->K, r);
-  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
+  Act8BwdPlan p = plan_linear_set_act8(a->T, count, N, a->K, r, false);
+  if (ws_bytes < p.total) {
+    if (ws_bytes < act8_bound(a->T, count, r)) return QLORA_ERR_WORKSPACE;
+    p = plan_linear_set_act8(a->T, count, N, a->K, r, true);
+  }
   hipError_t e = launch_linear_set_bwd_act8(p, dy, a->codes, a->scale, w, A_set, B, scale, u, grad_x, grad_A_set,
                                             grad_B, (char *)ws, nf4_levels(), (hipStream_t)stream);
   return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;

@@ -258,7 +258,10 @@ struct Act8BwdPlan {
   RaggedPlan rg;
   size_t off_v, off_part, off_qpart, off_rg, total;  // off_qpart: 0 when grad_x does not split
 };
-Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t K, int r);
+// lean: grad_x on the fused GEMM without splits, which needs no workspace; the plan's total is then at most
+// act8_bound(T, count, r), whatever the sizes of the weights, and that of fewer tokens too.
+Act8BwdPlan plan_linear_set_act8(int64_t T, int count, const int64_t *N, int64_t K, int r, bool lean);
+size_t act8_bound(int64_t T, int count, int r);
 hipError_t launch_linear_set_bwd_act8(const Act8BwdPlan &p, const uint16_t *const *dy, const int8_t *codes,
                                       const float *code_scale, const QWeight *w, const uint16_t *A_set,
                                       const uint16_t *const *B, float scale, const uint16_t *u, uint16_t *grad_x,

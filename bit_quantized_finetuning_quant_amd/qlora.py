@@ -81,6 +81,7 @@ _SIGNATURES = {
     "qlora_linear_set_bwd_act8": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int, ctypes.c_float, _P, _P,
                                                  _P, _P, _P, _SZ, _P]),
     "qlora_linear_set_act8_workspace_bytes": (_SZ, [_I64, ctypes.c_int, _P, _I64, ctypes.c_int]),
+    "qlora_linear_set_act8_workspace_bound": (_SZ, [_I64, ctypes.c_int, ctypes.c_int]),
     "qlora_head_loss": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
     "qlora_head_loss_nf4": (ctypes.c_int, [_P, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
     "qlora_head_loss_workspace_bytes": (_SZ, [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int]),
@@ -831,9 +832,16 @@ def linear_set_act8_workspace_bytes(tokens: int, n_outs, n_in: int, r: int) -> i
     return _act8_bytes(tokens, tuple(n_outs), n_in, r)
 
 
+@functools.lru_cache(maxsize=1024)
+def linear_set_act8_workspace_bound(tokens: int, members: int, r: int) -> int:
+    """Bytes of a workspace that serves every linear_set_bwd_act8 (members = 1: linear_bwd_act8) of up to `tokens`
+    tokens, whatever the weights' sizes; where it is less than linear_set_act8_workspace_bytes, grad_x may take longer."""
+    return int(lib().qlora_linear_set_act8_workspace_bound(tokens, members, r))
+
+
 def linear_set_act8_workspace(tokens: int, n_outs, n_in: int, r: int, device="cuda"):
     """A workspace for linear_set_bwd_act8, and with one n_out for linear_bwd_act8, of exactly these sizes (fewer
-    tokens may need more)."""
+    tokens may need more; linear_set_act8_workspace_bound has the bytes that serve them all)."""
     torch = _torch()
     return torch.empty(max(linear_set_act8_workspace_bytes(tokens, n_outs, n_in, r), 1), dtype=torch.uint8,
                        device=device)
@@ -882,11 +890,14 @@ def linear_set_bwd_act8(dys, a: Act8, qs, A_set, Bs, scale: float, u, need_grad_
         if grad_Bs is None:
             grad_Bs = [torch.empty((q.n_out, r), dtype=torch.float32, device=dev) for q in qs]
         if workspace is None:
-            ws = linear_set_act8_workspace(T, n_outs, n_in, r, dev)
-            wsb = ws.numel()
+            wsb = linear_set_act8_workspace_bytes(T, n_outs, n_in, r)
+            if not need_grad_x:  # what only grad_x needs is left out
+                wsb = min(wsb, linear_set_act8_workspace_bound(T, count, r))
+            ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
         else:
             ws = workspace
-            wsb = _workspace(ws, dev, lambda: linear_set_act8_workspace_bytes(T, n_outs, n_in, r))
+            wsb = _workspace(ws, dev, lambda: min(linear_set_act8_workspace_bytes(T, n_outs, n_in, r),
+                                                  linear_set_act8_workspace_bound(T, count, r)))
     st = (NF4WeightStruct * count)(*[q.struct() for q in qs])
     sa = a.struct()
     _check(lib().qlora_linear_set_bwd_act8(_ptrs(dys), ctypes.byref(sa), count, st, _ptr(A_set), _ptrs(Bs), r,

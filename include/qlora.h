@@ -369,8 +369,17 @@ qlora_status qlora_linear_set_bwd_act8(const uint16_t *const *dy, const qlora_ac
                                        float *const *grad_B, void *ws, size_t ws_bytes, void *stream);
 
 /* Workspace bytes of the two calls above (0 on a bad shape), for these sizes:
- * fewer tokens may take another form and need more.                           */
+ * fewer tokens may take another form and need more.  Where grad_x is formed from
+ * decoded weights (long products, and sizes off the fused GEMM's tiles) they hold
+ * the weights and the gradients in bf16, with fp32 partial sums of up to 128 MB.  */
 size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t *n_out, int64_t n_in, int r);
+
+/* Workspace bytes that serve every call of up to T tokens, `count` members and
+ * rank r, whatever n_out and n_in are (0 on a bad shape): 6 T count r and 8.4 MB
+ * a member, once more.  A workspace of at least these bytes, but fewer than the
+ * helper above names, is taken too: grad_x then stays on the fused GEMM without
+ * splits, which may take longer (a call without grad_x loses nothing).           */
+size_t qlora_linear_set_act8_workspace_bound(int64_t T, int count, int r);
 
 /* ---- the loss of the head ---------------------------------------------------- */
 

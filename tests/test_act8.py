@@ -224,6 +224,41 @@ def test_long_products_on_whole_tiles(T, Ns, K, r):
 
 
 @gpu
+@pytest.mark.parametrize("Ns,K,r,Ts", [((8192,), 8192, 16, (2048, 2047, 1024, 300, 64, 1)),
+                                       ((1000,), 448, 16, (1500, 700, 100, 17, 2)),
+                                       ((11008, 11008), 4096, 64, (1024, 700, 128, 5)),
+                                       ((512, 100, 7), 512, 33, (900, 513, 40, 1)),
+                                       ((128, 128, 128, 128), 256, 256, (2000, 90))])
+def test_one_workspace_for_up_to_many_tokens(Ns, K, r, Ts):
+    """A workspace of the bound for the most tokens serves every call of fewer, also where the exact size is larger
+    (grad_x then without the forms that need it) and where grad_x is not asked for; nothing behind it is written."""
+    torch = torch_mod()
+    count = len(Ns)
+    size = qlora.linear_set_act8_workspace_bound(max(Ts), count, r)
+    held = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = held[:size]
+    less = 0
+    for T in Ts:
+        announce(f"act8 backward in the bound of {max(Ts)} tokens T={T} Ns={Ns} K={K} r={r}")
+        less += qlora.linear_set_act8_workspace_bytes(T, Ns, K, r) > size
+        x, qs, A, Bs, dys, u = _case(T, Ns, K, r, seed=25 + T)
+        a = qlora.act8_write(x)
+        gx, ga, gbs = qlora.linear_set_bwd_act8(dys, a, qs, A, Bs, 0.25, u, workspace=ws)
+        _, ga2, gbs2 = qlora.linear_set_bwd_act8(dys, a, qs, A, Bs, 0.25, u, need_grad_x=False, workspace=ws)
+        _, ga3, gbs3 = qlora.linear_set_bwd_act8(dys, a, qs, A, Bs, 0.25, u)
+        torch.cuda.synchronize()
+        ex, ea, eb = _expect(a, qs, A, Bs, dys, u, 0.25, r)
+        _within(gx, ex, "grad_x")
+        _within(ga, ea, "grad_A")
+        for g, e in zip(gbs, eb):
+            _within(g, e, "grad_B")
+        assert torch.equal(ga, ga2) and torch.equal(ga, ga3)
+        assert all(torch.equal(p, q) and torch.equal(p, s) for p, q, s in zip(gbs, gbs2, gbs3))
+        assert (held[size:] == 0xA5).all()
+    assert less or K < 4096  # the wide cases hold at least one call that needs more by its exact size
+
+
+@gpu
 def test_gradient_of_A_against_differences():
     """grad_A of sum(dy . (scale x_hat A^T B^T)) against central differences of that sum in 64 bits:
     it is linear in A, so the difference is exact up to 64-bit rounding."""
@@ -355,6 +390,18 @@ def test_refusals_before_any_launch():
     b = qlora.linear_set_act8_workspace_bytes
     assert b(0, [512], 256, 8) == 0 and b(16, [512], 100, 8) == 0 and b(16, [], 256, 8) == 0
     assert b(16, [512] * 5, 256, 8) == 0 and b(16, [512, 0], 256, 8) == 0 and b(16, [512], 256, 300) == 0
+
+
+def test_bound_of_the_workspace():
+    """Grows with the tokens, and is below the exact size where that holds decoded weights."""
+    b, exact = qlora.linear_set_act8_workspace_bound, qlora.linear_set_act8_workspace_bytes
+    assert b(0, 1, 8) == 0 and b(16, 0, 8) == 0 and b(16, 5, 8) == 0 and b(16, 1, 0) == 0 and b(16, 1, 257) == 0
+    assert b(1 << 40, 1, 8) == 0 and b(-1, 1, 8) == 0
+    for count, r in ((1, 1), (1, 64), (2, 64), (4, 256)):
+        sizes = [b(T, count, r) for T in (1, 2, 63, 64, 65, 1000, 2048, 2049, 100000)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    assert b(2048, 1, 64) < 20 << 20 < exact(2048, [22016], 8192, 64)
+    assert b(2048, 2, 64) < 30 << 20 < exact(1024, [11008] * 2, 4096, 64)
 
 
 def test_tensor_checks():
