@@ -273,19 +273,33 @@ int few_chunk_steps(const RaggedLayout &l) {
 
 }  // namespace
 
-// Whether a product on whole tiles is faster here than in the fused GEMM, both estimated in us.  Here: the rounds
-// of 256 workgroups (25 ns a row of a tile's range, 512 rows' worth of start), the decode and the packed
-// gradients at 5.2 TB/s; there: 970 TFLOP/s.  Measured, the whole backward pass of T x n_out x n_in (here / there):
-// 4096 x 8192 x 22016 1439 / 1618 us, 4096 x 8192 x 8192 571 / 622, 4096 x (3 of 4096) x 4096 466 / 483, 2048 x
-// 8192 x 8192 307 / 325; left to the fused GEMM: 2048 x 4096 x 4096 139 / 111, 2048 x 4096 x 11008 275 / 248, 1024 x
-// 8192 x 22016 510 / 422 (and, below the estimate's precision, 4096 x 4096 x 11008 437 / 481).
-static bool long_pays(int64_t T, int64_t K, int64_t rows) {
+// Whether a product on whole tiles is faster here than in the fused GEMM, both estimated in us from the rounds of 256
+// workgroups that each takes: here 17.6 a round and 12.6 ns a row of a tile's range, the partial tiles, and the decode
+// with the packed gradients at 4.1 TB/s; there 5.2 a round and 0.70 a step of 64 rows, and the splits' partial sums
+// (fitted to the 81 shapes of 1024 to 8192 tokens by the linears and sets of 4096, 8192, 11008 and 22016).  This
+// form holds the decoded weights in the workspace, so it is taken for a gain of 5% only.  Of the 81 none is then
+// slower than in the fused GEMM, and the mean is 0.3% above the faster form's.  Measured, the whole backward pass
+// of T x n_out x n_in (here / there): 4096 x 8192 x 22016 1354 / 1556 us, 4096 x 8192 x 8192 510 / 558, 4096 x 4096 x 11008
+// 397 / 436, 2049 x 11008 x 4096 289 / 318, 2048 x 22016 x 8192 689 / 712; left to the fused GEMM: 2048 x (2 of 11008) x
+// 4096 419 / 393, 2049 x (3 of 8192) x 8192 1210 / 1137, 2048 x 4096 x 4096 122 / 98, 1024 x 22016 x 8192 422 / 372.
+static bool long_pays(int64_t T, int count, const int64_t *N, int64_t K, int64_t rows) {
   if (T < 1024) return false;
   const int tiles = (int)(cdiv(K, kTileV) * cdiv(T, kTileT));
-  Split s = choose_split(tiles, (int)rows);
-  const double product = 0.025 * (double)split_cost(tiles, (int)rows, s.count, s);
-  const double layout = (2.5 * rows * K + 4.0 * T * rows) / 5.2e6;
-  return product + layout < 2.0 * T * K * rows / 0.97e9;
+  const Split s = choose_split(tiles, (int)rows);
+  const double here = (double)cdiv((int64_t)tiles * s.count, 256) * (17.6 + 0.0126 * s.range) +
+                      (s.count > 1 ? 0.051 * tiles * s.count : 0.0) + (2.5 * rows * K + 4.0 * T * rows) / 4.1e6;
+  int64_t steps = 0;
+  bool same_n = true;
+  for (int i = 0; i < count; ++i) {
+    steps += N[i] / kStep;
+    same_n = same_n && N[i] == N[0];
+  }
+  QgemmSplit f{1, 0};  // a split takes the same range of steps of every member
+  if (same_n) f = qgemm_split(T, K, N[0]);
+  if (f.splits > 1) steps = f.steps * count;
+  const double rounds = (double)cdiv(cdiv(T, 256) * (K / 128) * f.splits, 256);
+  const double partial = f.splits > 1 ? 1.3 * (f.splits * (double)T * K / 1e6 + 3.0) : 0.0;
+  return 1.05 * here < rounds * (5.2 + 0.70 * steps) + partial;
 }
 
 bool ragged_dx_applies(int64_t T, int count, const int64_t *N, int64_t K, int r) {
@@ -300,7 +314,7 @@ bool ragged_dx_applies(int64_t T, int count, const int64_t *N, int64_t K, int r)
   // 47 us; 1 token, 4 x 200 x 512: 62 against 57)
   if (T <= kFewTokens && rows <= 512) return false;
   if (rows > kMaxDecoded / K || T > (int64_t)1 << 24 || rows * T > (int64_t)1 << 32) return false;
-  return !whole || long_pays(T, K, rows);
+  return !whole || long_pays(T, count, N, K, rows);
 }
 
 // dyp, the weights' rows, and the partial sums, each 256-byte aligned

@@ -404,6 +404,19 @@ def test_bound_of_the_workspace():
     assert b(2048, 2, 64) < 30 << 20 < exact(1024, [11008] * 2, 4096, 64)
 
 
+def test_form_of_long_products():
+    """Weights are decoded into the workspace (which then holds n_out n_in bf16 values at least) where that was measured
+    to be faster by a margin, and not where it was slower."""
+    size = qlora.linear_set_act8_workspace_bytes
+    for T, Ns, K, r in ((4096, [4096], 11008, 64), (4096, [8192], 22016, 64), (4096, [11008] * 2, 4096, 64),
+                        (2049, [11008], 4096, 64), (2048, [8192], 8192, 64), (8192, [4096] * 3, 4096, 16)):
+        assert size(T, Ns, K, r) > 2 * sum(Ns) * K, (T, Ns, K)
+    for T, Ns, K, r in ((2048, [11008] * 2, 4096, 64), (2047, [11008] * 2, 4096, 64), (2048, [11008] * 2, 4096, 16),
+                        (2048, [4096], 4096, 64), (2048, [11008], 4096, 64), (2049, [8192] * 3, 8192, 16),
+                        (1024, [22016], 8192, 64), (2048, [4096], 11008, 64)):
+        assert size(T, Ns, K, r) < 2 * sum(Ns) * K, (T, Ns, K)
+
+
 def test_tensor_checks():
     torch = torch_mod()
     with pytest.raises(ValueError, match="multiple of 64"):
