@@ -313,7 +313,8 @@ bool ragged_dx_applies(int64_t T, int count, const int64_t *N, int64_t K, int r)
   // a few tokens and rows: its own launches cost more than the masks (6 tokens, 2 x 100 x 512: 41 against
   // 47 us; 1 token, 4 x 200 x 512: 62 against 57)
   if (T <= kFewTokens && rows <= 512) return false;
-  if (rows > kMaxDecoded / K || T > (int64_t)1 << 24 || rows * T > (int64_t)1 << 32) return false;
+  // T: ragged_pack takes a workgroup of 256 threads a token and a few more, and a launch holds fewer than 2^32 threads
+  if (rows > kMaxDecoded / K || T > (int64_t)1 << 23 || rows * T > (int64_t)1 << 32) return false;
   return !whole || long_pays(T, count, N, K, rows);
 }
 

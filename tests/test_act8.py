@@ -259,6 +259,25 @@ def test_one_workspace_for_up_to_many_tokens(Ns, K, r, Ts):
 
 
 @gpu
+def test_very_many_tokens():
+    """More tokens than the form of decoded weights may launch: the first and last rows of grad_x, in 64 bits."""
+    torch = torch_mod()
+    T, N, K, r = (1 << 24) + 70, 64, 64, 1
+    announce(f"act8 backward T={T} N={N} K={K} r={r}")
+    g = torch.Generator(device="cuda").manual_seed(30)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    q = qlora.quantize(n(N, K) * 0.02)
+    A, B, dy, u = n(r, K), n(N, r), n(T, N), n(T, r)
+    a = qlora.act8_write(n(T, K))
+    gx, ga, gb = qlora.linear_bwd_act8(dy, a, q, A, B, 0.25, u)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 500), slice(T - 500, T)):
+        part = qlora.Act8(a.codes[rows].clone(), a.scale[rows].clone())  # on 16-byte boundaries
+        _within(gx[rows], _expect(part, [q], A, [B], [dy[rows]], u[rows], 0.25, r)[0], "grad_x")
+    assert ga.isfinite().all() and gb.isfinite().all()
+
+
+@gpu
 def test_gradient_of_A_against_differences():
     """grad_A of sum(dy . (scale x_hat A^T B^T)) against central differences of that sum in 64 bits:
     it is linear in A, so the difference is exact up to 64-bit rounding."""
@@ -402,6 +421,15 @@ def test_bound_of_the_workspace():
         assert sizes == sorted(sizes) and sizes[0] > 0
     assert b(2048, 1, 64) < 20 << 20 < exact(2048, [22016], 8192, 64)
     assert b(2048, 2, 64) < 30 << 20 < exact(1024, [11008] * 2, 4096, 64)
+
+
+def test_launch_of_very_many_tokens():
+    """A launch holds fewer than 2^32 threads: a form that takes a workgroup of 256 a token stops in time.  (The
+    workspace of that form holds the gradients, so that its size tells the forms apart.)"""
+    size = qlora.linear_set_act8_workspace_bytes
+    for T in ((1 << 24) - 100, 1 << 24, 1 << 25):
+        assert size(T, [64], 64, 1) < 2 * 128 * T
+    assert size(1 << 22, [64], 64, 1) > 2 * 128 << 22
 
 
 def test_form_of_long_products():
