@@ -134,6 +134,33 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *p) {
   return v;
 }
 
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// The LDS byte address of a pointer into LDS.
+__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(lds_void_t *)p; }
+
+// One 16-byte-per-lane LDS-DMA: lane l reads 16 bytes at sbase + voff and
+// writes them at LDS byte address lds + 16 l.  Written as inline asm so that
+// the compiler does not treat the whole LDS as possibly being written by it:
+// the builtin makes every later LDS read of the wave wait for all outstanding
+// loads, including stages that are meant to stay in flight.  The instruction
+// has no register result; its waits are issued explicitly by the caller, and
+// voff must stay unmodified until they have been.
+// m0 is named as clobbered: nothing else in these kernels uses it (checked in
+// the generated code), and every DMA sets it right before use.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16(const char *sbase, uint32_t voff, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1"
+      :
+      : "v"(voff), "s"(sbase), "s"(lds)
+      : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 }  // namespace qlora

@@ -1117,7 +1117,7 @@ HeadPlan plan_head(int64_t T, int64_t V, int64_t D, bool grad, bool packed) {
   p.V = V;
   p.D = D;
   p.grad = grad;
-  p.packed = p.decode = packed;
+  p.decode = packed;
   p.chunk = std::min<int64_t>(T, kHeadMaxTokens);
   // Words of a piece: 128 MB of e (grad) and of decoded weight (packed).  A larger piece leaves less of
   // the products' last rounds of workgroups empty (2048 tokens, 40% of them masked, V = 32000: 5 tiles of

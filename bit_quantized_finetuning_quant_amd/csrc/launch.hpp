@@ -276,10 +276,10 @@ constexpr int64_t kHeadMaxTokens = 16384;  // tokens of a chunk
 constexpr int64_t kHeadMaxDim = 65536;     // D: a chunk's byte offsets stay below 2^32
 struct HeadPlan {
   int64_t T, V, D;
-  bool grad, packed;
+  bool grad;
   bool decode;  // the packed head's pieces are decoded into the workspace first
-  bool few;     // few: the few-token form (splits: chunks of words in all, split_words: of
-  // each); otherwise splits: the gradient's partial tiles
+  bool few;     // few: the few-token form (splits: chunks of words of a piece, split_words: words
+  // of each); otherwise splits: the gradient's partial tiles
   int64_t chunk, tpad, words, pieces, splits, split_words;
   size_t off_rows, off_place, off_logit, off_n, off_s, off_r, off_factor, off_exponent, off_sum, off_rounded, off_shift,
       off_e, off_part, off_w, total;

@@ -33,7 +33,6 @@ namespace {
 constexpr int LT = 64;   // output tile (M and N) and contraction step
 constexpr int LLD = 72;  // LDS row length (bf16), padded
 
-typedef __attribute__((address_space(3))) void lds_void_t;
 typedef short v4s __attribute__((ext_vector_type(4)));
 
 // Eight values of which the first `past` are dropped.

@@ -51,8 +51,6 @@ static_assert(128 * QLD == 64 * TLD, "both weight-tile layouts fill the same LDS
 constexpr int kActStages = 3;                            // activation tile LDS ring
 constexpr int kWStages = 3;                              // weight tile LDS ring
 
-typedef __attribute__((address_space(1))) const void gptr_t;
-typedef __attribute__((address_space(3))) void lptr_t;
 
 __device__ __forceinline__ u32x4 ld8(const uint16_t *row, int64_t c, int64_t ncols, bool vec) {
   if (vec && c + 8 <= ncols) return *(const u32x4 *)(row + c);
@@ -88,34 +86,10 @@ __device__ __forceinline__ void wg_barrier() {
 // 6:4 (left at its maximum), lgkmcnt in 11:8.
 constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 15) | (7 << 4) | ((lgkm & 15) << 8) | ((vm >> 4) << 14); }
 
-// One 16-byte-per-lane LDS-DMA: lane l reads 16 bytes at sbase + voff and
-// writes them at LDS byte address lds + 16 l.  Written as inline asm so that
-// the compiler does not treat the whole LDS as possibly being written by it:
-// the builtin makes every later LDS read of the wave wait for all outstanding
-// loads, including stages that are meant to stay in flight.  The instruction
-// has no register result; its waits are issued explicitly by the caller, and
-// voff must stay unmodified until they have been.
-// m0 is named as clobbered: nothing else in these kernels uses it (checked in
-// the generated code), and every DMA sets it right before use.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma16(const char *sbase, uint32_t voff, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %0, %1"
-      :
-      : "v"(voff), "s"(sbase), "s"(lds)
-      : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
 // The value held by the other lane of an adjacent pair (DPP quad_perm [1, 0, 3, 2]).
 __device__ __forceinline__ uint32_t pair_swap(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
 }
-
-__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(lptr_t *)p; }
 
 // Full tiles: consumer wave cw (0..3) moves rows [64 cw, 64 cw + 64) of the
 // activation tile of stage kt into LDS buffer dst with 8 DMA instructions of 8
@@ -495,9 +469,9 @@ __device__ __forceinline__ void consumer_slices(const uint16_t *A, const uint16_
         const int ncol = wn * 64 + j * 32 + 16 * (g & 1) + 4 * (sl & 3);
         typedef short v4s __attribute__((ext_vector_type(4)));
         const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (v4s __attribute__((address_space(3))) *)(lptr_t *)&B[nrow * TLD + ncol]);
+            (v4s __attribute__((address_space(3))) *)(lds_void_t *)&B[nrow * TLD + ncol]);
         const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (v4s __attribute__((address_space(3))) *)(lptr_t *)&B[(nrow + 4) * TLD + ncol]);
+            (v4s __attribute__((address_space(3))) *)(lds_void_t *)&B[(nrow + 4) * TLD + ncol]);
         const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
         b[j] = u32x4{l2.x, l2.y, h2.x, h2.y};
       }
@@ -533,9 +507,9 @@ __device__ __forceinline__ u32x4 load_b_frag(const uint16_t *B, int wn, int lane
   const int ncol = wn * 64 + j * 32 + 16 * (g & 1) + 4 * (sl & 3);
   typedef short v4s __attribute__((ext_vector_type(4)));
   const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (v4s __attribute__((address_space(3))) *)(lptr_t *)&B[nrow * TLD + ncol]);
+      (v4s __attribute__((address_space(3))) *)(lds_void_t *)&B[nrow * TLD + ncol]);
   const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (v4s __attribute__((address_space(3))) *)(lptr_t *)&B[(nrow + 4) * TLD + ncol]);
+      (v4s __attribute__((address_space(3))) *)(lds_void_t *)&B[(nrow + 4) * TLD + ncol]);
   const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
   return u32x4{l2.x, l2.y, h2.x, h2.y};
 }

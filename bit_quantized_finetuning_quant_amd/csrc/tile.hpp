@@ -18,25 +18,6 @@ constexpr int kStage = 4 * kUnit;
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(lds_void_t *)p; }
-
-// One 16-byte-per-lane copy from global memory to LDS bytes lds + 16 lane.  As asm, since the
-// compiler would otherwise make every later LDS read wait for all copies in flight; it has no
-// register result, and the callers wait for it by count.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma16(const char *sbase, uint32_t voff, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %0, %1"
-      :
-      : "v"(voff), "s"(sbase), "s"(lds)
-      : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 #define TILE_WAIT_VM(n) asm volatile("s_waitcnt vmcnt(" #n ")" ::: "memory")
 #define TILE_WAIT_LDS() asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory")
