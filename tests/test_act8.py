@@ -17,8 +17,9 @@ import ctypes
 
 import pytest
 
-from bit_quantized_finetuning_quant_amd import qlora
-from helpers import announce, torch_mod
+from bit_quantized_finetuning_quant_amd import qlora, workloads
+from helpers import NORMWISE_TOL, announce, bf16_to_f64, dev_bf16, dev_f32, host, host_bits, normwise_rel, torch_mod
+from oracle import dropout
 
 gpu = pytest.mark.gpu
 
@@ -256,6 +257,28 @@ def test_one_workspace_for_up_to_many_tokens(Ns, K, r, Ts):
         assert all(torch.equal(p, q) and torch.equal(p, s) for p, q, s in zip(gbs, gbs2, gbs3))
         assert (held[size:] == 0xA5).all()
     assert less or K < 4096  # the wide cases hold at least one call that needs more by its exact size
+
+
+@gpu
+@pytest.mark.parametrize("n_out,n_in,T,r,p", [(300, 320, 300, 24, 0.05), (1024, 1024, 700, 64, 0.3), (130, 2112, 3, 13, 0.05)])
+def test_dropout_from_a_checkpoint(n_out, n_in, T, r, p):
+    """An adapter with dropout reads the checkpoint back: grad_A is that of x_hat under the forward's mask, grad_B
+    that of the forward's own u, within the bar of the linear layer."""
+    torch = torch_mod()
+    announce(f"act8 with dropout n_out={n_out} n_in={n_in} T={T} r={r} p={p}")
+    case = workloads.custom_case(n_out, n_in, T, r, 16.0, seed=n_out + T)
+    q = qlora.quantize(dev_f32(case.w))
+    x, A, B, dy = (dev_bf16(t) for t in (case.x, case.a, case.b, case.dy))
+    _, u = qlora.linear_fwd_dropout(x, q, A, B, case.scale, p, 77)
+    xh = qlora.act8_read(qlora.act8_write(x))
+    gx, ga, gb = qlora.linear_bwd_dropout(dy, xh, q, A, B, case.scale, p, 77, u=u)
+    torch.cuda.synchronize()
+    wh = host_bits(qlora.dequantize(q))
+    gx_ref, ga_ref, _ = dropout.backward(case.dy, host_bits(xh), wh, case.a, case.b, case.scale, p, 77)
+    _, _, gb_ref = dropout.backward(case.dy, case.x, wh, case.a, case.b, case.scale, p, 77)
+    assert normwise_rel(bf16_to_f64(host_bits(gx)), gx_ref) <= NORMWISE_TOL
+    assert normwise_rel(host(ga), ga_ref) <= NORMWISE_TOL
+    assert normwise_rel(host(gb), gb_ref) <= NORMWISE_TOL
 
 
 @gpu
