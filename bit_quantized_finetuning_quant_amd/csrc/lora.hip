@@ -225,12 +225,16 @@ __device__ __forceinline__ void emit_out(void *out, int64_t idx, float v) {
   }
 }
 
-// What the bf16 rounding of v leaves, in two bf16 values (the differences are exact): out, mid and
-// low then sum to v within 2^-24, its own precision.  Nothing is left of an infinity.
-__device__ __forceinline__ void emit_rest(uint16_t *mid, uint16_t *low, int64_t idx, float v) {
-  const float h = (float)(__bf16)v, d = __builtin_isinf(h) ? 0.f : v - h;
+// v in three bf16 values: its rounding and what that leaves, twice (the differences are exact), which sum to v
+// within 2^-24, its own precision.  A finite v that would round to infinity takes bf16's largest value first;
+// nothing is left of an infinity.
+__device__ __forceinline__ void emit_parts(uint16_t *out, uint16_t *mid, uint16_t *low, int64_t idx, float v) {
+  const float top = __uint_as_float(0x7F7F0000u);
+  const __bf16 h = (__bf16)(fabsf(v) > top && !__builtin_isinf(v) ? copysignf(top, v) : v);
+  const float d = __builtin_isinf(v) ? 0.f : v - (float)h;
   const __bf16 m = (__bf16)d;
   const __bf16 l = (__bf16)(d - (float)m);
+  out[idx] = __builtin_bit_cast(uint16_t, h);
   mid[idx] = __builtin_bit_cast(uint16_t, m);
   low[idx] = __builtin_bit_cast(uint16_t, l);
 }
@@ -253,7 +257,7 @@ struct LoraProblem {
 
 // A product of the backward pass from an 8-bit checkpoint.
 struct Act8Problem : LoraProblem {
-  uint16_t *out_mid, *out_low;  // v: also what its bf16 rounding leaves
+  uint16_t *out_mid, *out_low;  // v: what its bf16 rounding leaves
   // grad_A: Q holds the checkpoint's codes, P has the remainders P_mid, P_low
   const uint16_t *P_mid, *P_low;
   const float *code_scale;  // [Kc x Nc / 64]
@@ -272,9 +276,10 @@ __device__ __forceinline__ void put_tile(const Problem &pr, int64_t tile, int s,
     for (int q = 0; q < 16; ++q) {
       const int64_t gm = m0 + wm * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3), gn = n0 + col;
       if (gm < pr.M && gn < pr.Nc) {
-        emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn, acc[q] * pr.scale);
         if constexpr (kBf16Out && std::is_same_v<Problem, Act8Problem>)
-          emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn, acc[q] * pr.scale);
+          emit_parts((uint16_t *)pr.out, pr.out_mid, pr.out_low, gm * pr.ldo + gn, acc[q] * pr.scale);
+        else
+          emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn, acc[q] * pr.scale);
       }
     }
     return;
@@ -350,9 +355,10 @@ __device__ __forceinline__ void reduce_quad(const Problem &pr, int64_t qd) {
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (gn + e < pr.Nc) {
-      emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn + e, acc[e] * pr.scale);
       if constexpr (kBf16Out && std::is_same_v<Problem, Act8Problem>)
-        emit_rest(pr.out_mid, pr.out_low, gm * pr.ldo + gn + e, acc[e] * pr.scale);
+        emit_parts((uint16_t *)pr.out, pr.out_mid, pr.out_low, gm * pr.ldo + gn + e, acc[e] * pr.scale);
+      else
+        emit_out<kBf16Out>(pr.out, gm * pr.ldo + gn + e, acc[e] * pr.scale);
     }
 }
 

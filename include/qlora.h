@@ -352,9 +352,9 @@ qlora_status qlora_act8_read(const qlora_act8 *a, uint16_t *x, void *stream);
 
 /* qlora_linear_bwd with the checkpoint in place of x (T and n_in are the
  * checkpoint's): grad_x and grad_B as there, grad_A = scale v^T x_hat with
- * v = dy B in fp32 (grad_x takes it in bf16, as there).  u is the
- * forward's u_out and required: from the checkpoint it would come out
- * different.  grad_x may be NULL.  (Where the adapter's input is dropped out,
+ * v = dy B in fp32 (grad_x takes it in bf16, as there, but a finite v as a
+ * finite one).  u is the forward's u_out and required: from the checkpoint it
+ * would come out different.  grad_x may be NULL.  (Where the adapter's input is dropped out,
  * qlora_act8_read gives the x that qlora_linear_bwd_dropout takes.)
  * ws: qlora_linear_set_act8_workspace_bytes with count = 1.                   */
 qlora_status qlora_linear_bwd_act8(const uint16_t *dy, const qlora_act8 *a, const qlora_nf4_weight *q,

@@ -399,6 +399,53 @@ def test_infinite_gradients(T):
     assert torch.equal(ga[~want.isnan()].double(), want[~want.isnan()])
 
 
+@gpu
+@pytest.mark.parametrize("T,N", [(40, 128), (40, 2000), (1200, 128)])
+def test_gradients_past_the_range_of_bf16(T, N):
+    """A finite v = dy B above bf16's largest value by more than half a step (here 1.003 of it) is held as finite
+    parts: grad_A and grad_x are the formula's."""
+    torch = torch_mod()
+    announce(f"act8 backward of a gradient next to the end of the range T={T} N={N}")
+    x, qs, A, Bs, dys, u = _case(T, [N], 192, 8, seed=31)
+    x = (x.float() * 2.0**-30).bfloat16()
+    A = (A.float() * 2.0**-30).bfloat16()
+    top = torch.finfo(torch.bfloat16).max
+    B = torch.zeros_like(Bs[0])
+    B[:2] = 1.0
+    dy = torch.zeros_like(dys[0])
+    for t, sign in ((T // 2, 1.0), (T - 1, -1.0)):
+        dy[t, 0] = sign * top
+        dy[t, 1] = sign * 2.0**-9 * 1.5 * top
+    v = dy.float() @ B.float()
+    assert v.isfinite().all() and v.bfloat16().isinf().any()
+    a = qlora.act8_write(x)
+    q = qlora.quantize(torch.zeros(N, 192, device="cuda"))
+    gx, ga, gbs = qlora.linear_bwd_act8(dy, a, q, A, B, 0.25, u)
+    torch.cuda.synchronize()
+    ex, ea, _ = _expect(a, [q], A, [B], [dy], u, 0.25, 8)
+    _within(ga, ea, "grad_A")
+    _within(gx, ex, "grad_x")
+
+
+@gpu
+@pytest.mark.parametrize("T,N", [(40, 128), (40, 2000), (1200, 128)])
+def test_nan_gradients(T, N):
+    """A NaN in dy reaches its token's row of grad_x, every row of grad_A and its row of grad_B, and nothing else."""
+    torch = torch_mod()
+    announce(f"act8 backward of a NaN gradient T={T} N={N}")
+    x, qs, A, Bs, dys, u = _case(T, [N], 192, 8, seed=32)
+    a = qlora.act8_write(x)
+    want = qlora.linear_bwd_act8(dys[0], a, qs[0], A, Bs[0], 0.25, u)
+    dys[0][T // 2, 3] = float("nan")
+    gx, ga, gbs = qlora.linear_bwd_act8(dys[0], a, qs[0], A, Bs[0], 0.25, u)
+    torch.cuda.synchronize()
+    rows = torch.arange(T, device="cuda") != T // 2
+    outs = torch.arange(N, device="cuda") != 3
+    assert gx[T // 2].isnan().all() and torch.equal(gx[rows], want[0][rows])
+    assert ga.isnan().all()
+    assert gbs[3].isnan().all() and torch.equal(gbs[outs], want[2][outs])
+
+
 # ------------------------------------------------------------------- refusals (no GPU)
 def test_refusals_before_any_launch():
     L = qlora.lib()
