@@ -754,7 +754,7 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
   constexpr int kBytes = (kPacked ? 2 : few_stages<true, NT>()) * few_stage<NT>(), kT = 16 * NT, kRows = kFewThreads / kT;
   __shared__ __attribute__((aligned(1024))) char lds[4 * kBytes];
   __shared__ uint8_t shifts[kFewChunk * kT];
-  __shared__ float fold[kFewThreads], fold_r[kFewThreads], factor[kT][2];  // factors: of the sums before and of these
+  __shared__ float fold[kFewThreads], factor[kT][2];  // factors: of the sums before and of these
   // places: the slices of a chunk for one token group, then its other token groups, then the next chunk
   const int slices = D / 64, groups = tpad / kFewTokens, place = place_of(blockIdx.x, gridDim.x);
   const int over = scalar(place / slices), slice = scalar(place - over * slices);
@@ -763,11 +763,11 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
   const int64_t vb = (int64_t)chunk * chunk_steps * kFewWords;
   const int words = (int)min((int64_t)chunk_steps * kFewWords, nv - vb);
   const int steps = (words + kFewWords - 1) / kFewWords;
-  {  // the chunk's largest exponent of each token, its sum, and every step's distance from it
+  {  // the chunk's largest exponent of each token, every step's distance from it, and its sums: S by the workgroup of
+     // the first columns, R by that of the second (both in one delay the launch: 64 tokens, packed, 109 against 119 us)
     const int t = threadIdx.x % kT, g = threadIdx.x / kT;
-    const float *ex = exponent + vb / kFewWords * tpad + min(t0 + t, T - 1);
-    const float *sm = sum + vb / kFewWords * tpad + min(t0 + t, T - 1);
-    const float *rm = rounded + vb / kFewWords * tpad + min(t0 + t, T - 1);
+    const int64_t from = vb / kFewWords * tpad + min(t0 + t, T - 1);
+    const float *ex = exponent + from;
     float top = kNoExponent;
 #pragma unroll 8
     for (int i = g; i < steps; i += kRows) top = fmaxf(top, ex[i * tpad]);
@@ -776,40 +776,34 @@ __global__ __launch_bounds__(kFewThreads, 1) void few_grad(const uint16_t *__res
 #pragma unroll
     for (int i = 0; i < kRows; ++i) top = fmaxf(top, fold[i * kT + t]);
     __syncthreads();
-    float s = 0.f, r = 0.f;
 #pragma unroll 8
-    for (int i = g; i < steps; i += kRows) {
-      const float d = top - ex[i * tpad];
-      shifts[i * kT + t] = (uint8_t)fminf(d, 255.f);
-      if (slice == 0) {
-        const float f = __builtin_amdgcn_exp2f(-fminf(d, 300.f));
-        s += sm[i * tpad] * f;
-        r += rm[i * tpad] * f;
-      }
+    for (int i = g; i < steps; i += kRows) shifts[i * kT + t] = (uint8_t)fminf(top - ex[i * tpad], 255.f);
+    const int64_t at = (int64_t)chunk * tpad + t0 + t;
+    const bool on = g == 0 && t0 + t < T;
+    float n = top, f = 1.f, f_old = 0.f;
+    if (on && !first) {
+      const float old = before.N[at];
+      n = fmaxf(top, old);
+      factor[t][0] = f_old = __builtin_amdgcn_exp2f(-fminf(n - old, 300.f));
+      factor[t][1] = f = __builtin_amdgcn_exp2f(-fminf(n - top, 300.f));
     }
-    fold[threadIdx.x] = s;
-    fold_r[threadIdx.x] = r;
+    if (on && slice == 0) now.N[at] = n;
+    for (int kind = slice; kind < 2; kind += slices) {
+      const float *src = (kind ? rounded : sum) + from;
+      float s = 0.f;
+#pragma unroll 8
+      for (int i = g; i < steps; i += kRows)
+        s += src[i * tpad] * __builtin_amdgcn_exp2f(-fminf(top - ex[i * tpad], 300.f));
+      fold[threadIdx.x] = s;
+      __syncthreads();
+      if (on) {
+        for (int i = 1; i < kRows; ++i) s += fold[i * kT + t];
+        const float held = first ? 0.f : (kind ? before.R : before.S)[at] * f_old;
+        (kind ? now.R : now.S)[at] = held + s * f;
+      }
+      __syncthreads();
+    }
     __syncthreads();
-    if (g == 0 && t0 + t < T) {
-      const int64_t at = (int64_t)chunk * tpad + t0 + t;
-      float n = top, f = 1.f;
-      if (!first) {
-        const float old = before.N[at];
-        n = fmaxf(top, old);
-        f = __builtin_amdgcn_exp2f(-fminf(n - top, 300.f));
-        factor[t][0] = __builtin_amdgcn_exp2f(-fminf(n - old, 300.f));
-        factor[t][1] = f;
-      }
-      if (slice == 0) {
-        for (int i = 1; i < kRows; ++i) {
-          s += fold[i * kT + t];
-          r += fold_r[i * kT + t];
-        }
-        now.N[at] = n;
-        now.S[at] = first ? s : before.S[at] * factor[t][0] + s * f;
-        now.R[at] = first ? r : before.R[at] * factor[t][0] + r * f;
-      }
-    }
   }
   uint32_t off[2 * NT];
 #pragma unroll
