@@ -343,7 +343,7 @@ __device__ __forceinline__ int pack_distances(int d) {
 // along the tiles a workgroup, eight tiles of a lane in flight at once.  shift [tile][tpad / 4]: the
 // distances of four tokens a byte (0 for tokens past the last); factor: 2^(N before - N), for what the
 // pieces before have summed.  loss (nullptr: not yet, or not here): the piece is the last, N and S are final.
-// 7.9 us for 4096 tokens by 126 tiles: the tiles' statistics are 8 bytes per token and 128 words, so this is latency.
+// 9.5 us for 4096 tokens by 126 tiles: the tiles' statistics are 12 bytes per token and 128 words, so this is latency.
 // kGrad: with rounded, R, shift and factor.
 template <bool kGrad>
 __global__ __launch_bounds__(256) void head_fold(const float *__restrict__ exponent, const float *__restrict__ sum,
@@ -641,7 +641,7 @@ __global__ __launch_bounds__(256) void head_finish(const int *__restrict__ place
 // words are relative to the chunk's own largest n, which few_finish brings
 // together: no pass over the tiles lies between the two products.
 //   16 x 4096 x 32000 (W 262 MB): few_logits 43 us (6.1 TB/s), with the gradient
-//   89 us, the call's launches included; a plain copy reaches 5.2 TB/s.
+//   91 us, the call's launches included; a plain copy reaches 5.2 TB/s.
 // A packed head is decoded inside both products up to 64 tokens (one group);
 // beyond, every group would decode it again, and it is decoded once before.
 
@@ -1089,7 +1089,8 @@ static hipError_t launch_few(const HeadPlan &p, const uint16_t *h, const uint16_
 
 // Whether the streamed form is taken: always up to 64 tokens, and where its time, estimated in us from
 // runs of both forms at 66 to 2048 tokens, 256 to 4096 columns and 300 to 32000 words, is below that of
-// the tiles.  A stream's unit is 64 tokens, 64 columns, 4096 words; a workgroup of the logits costs about
+// the tiles.  (The host does not know which tokens carry no loss: every token counts, and the streams compute
+// them all, where the tiles skip them.)  A stream's unit is 64 tokens, 64 columns, 4096 words; a workgroup of the logits costs about
 // 2.6 us besides.  The tiles have launches and first copies, the chain of a tile's steps, the sums of a
 // vocabulary spread over splits, and the operations.  Measured, with the gradient (tiles / streams): 256 x
 // 1024 x 4000 63 / 25 us, 1024 x 1024 x 4000 70 / 63, 512 x 1024 x 16000 80 / 108, 66 x 4096 x 16000

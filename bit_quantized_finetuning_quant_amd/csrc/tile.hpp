@@ -387,10 +387,12 @@ __device__ __forceinline__ void few_product(const char *left, uint32_t left_pitc
 }
 
 // The same with a packed left operand, decoded on its way into LDS: a lane takes one row of the tile, which is one NF4
-// block (32 bytes of codes, one constant), builds the block's 16 values in registers and selects them by code (about
-// 270 vector instructions a step, which bound it).  The codes of a step are loaded two steps ahead.  Against decoded
-// rows in the workspace, W of 32000 x 4096: one token's loss 114 -> 32 us, with the gradient (each product decodes) 165
-// -> 74 us; 64 tokens 119 -> 55 and 181 -> 116 us.
+// block (32 bytes of codes, one constant), builds the block's 16 values in registers and selects them by code, about
+// 270 vector instructions a step.  These issue in 63% of the busy cycles of one token's logits (two waves a SIMD) and in
+// 45% of its gradient's (one wave a SIMD; both products of 64 tokens: 45 and 47%); the rest is a wave's chain of
+// decode, LDS write, wait, LDS read and multiply.  The codes of a step are loaded two steps ahead.  Against
+// decoded rows in the workspace, W of 32000 x 4096: one token's loss 114 -> 32 us, with the gradient (each product
+// decodes) 165 -> 72 us; 64 tokens 119 -> 54 and 181 -> 109 us.
 struct PackedRow {
   u32x4 codes[2];
   uint32_t q;
