@@ -205,11 +205,6 @@ def _alloc_on(stream):
     return nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
-def _on_boundary(t) -> bool:
-    """Whether a tensor may go to the C ABI as it is (None may)."""
-    return t is None or t.data_ptr() % 16 == 0
-
-
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -967,21 +962,23 @@ def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=N
         else:
             ws = workspace
             wsb = _workspace(ws, dev, lambda: head_loss_workspace_bytes(T, V, D, need_grad, packed))
-        # the C ABI takes 16-byte aligned pointers; labels[1:] and the like go through copies of T values
-        y = target if _on_boundary(target) else target.clone()
-        wt = weight if _on_boundary(weight) else weight.clone()
-        to_loss, to_lse = (t if _on_boundary(t) else torch.empty_like(t) for t in (loss, lse))
+        vectors = [target, weight, loss, lse]
+        ptrs = [target.data_ptr(), _ptr(weight), loss.data_ptr(), lse.data_ptr()]
+        if (ptrs[0] | ptrs[1] | ptrs[2] | ptrs[3]) & 15:
+            # the C ABI takes 16-byte aligned pointers; labels[1:] and the like go through copies of T values
+            for i in range(4):
+                if ptrs[i] & 15:
+                    vectors[i] = vectors[i].clone() if i < 2 else torch.empty_like(vectors[i])
+                    ptrs[i] = vectors[i].data_ptr()
         if packed:
             st = head.struct()
-            _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), _ptr(y), _ptr(wt), float(scale),
-                                             _ptr(to_loss), _ptr(to_lse), _ptr(grad_h), _ptr(ws), wsb, handle),
-                   "qlora_head_loss_nf4")
+            _check(lib().qlora_head_loss_nf4(_ptr(h), T, ctypes.byref(st), ptrs[0], ptrs[1], float(scale), ptrs[2], ptrs[3],
+                                             _ptr(grad_h), _ptr(ws), wsb, handle), "qlora_head_loss_nf4")
         else:
-            _check(lib().qlora_head_loss(_ptr(h), T, _ptr(head), V, D, _ptr(y), _ptr(wt), float(scale), _ptr(to_loss),
-                                         _ptr(to_lse), _ptr(grad_h), _ptr(ws), wsb, handle),
-                   "qlora_head_loss")
-        if to_loss is not loss:
-            loss.copy_(to_loss)
-        if to_lse is not lse:
-            lse.copy_(to_lse)
+            _check(lib().qlora_head_loss(_ptr(h), T, _ptr(head), V, D, ptrs[0], ptrs[1], float(scale), ptrs[2], ptrs[3],
+                                         _ptr(grad_h), _ptr(ws), wsb, handle), "qlora_head_loss")
+        if vectors[2] is not loss:
+            loss.copy_(vectors[2])
+        if vectors[3] is not lse:
+            lse.copy_(vectors[3])
     return loss, lse, grad_h
