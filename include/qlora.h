@@ -375,10 +375,10 @@ qlora_status qlora_linear_set_bwd_act8(const uint16_t *const *dy, const qlora_ac
 size_t qlora_linear_set_act8_workspace_bytes(int64_t T, int count, const int64_t *n_out, int64_t n_in, int r);
 
 /* Workspace bytes that serve every call of up to T tokens, `count` members and
- * rank r, whatever n_out and n_in are (0 on a bad shape): 6 T count r and 8.4 MB
- * a member, once more.  A workspace of at least these bytes, but fewer than the
- * helper above names, is taken too: grad_x then stays on the fused GEMM without
- * splits, which may take longer (a call without grad_x loses nothing).           */
+ * rank r, whatever n_out and n_in are (0 on a bad shape): 6 T count r bytes, and
+ * 8.4 MB for each member and one more.  A workspace of at least these bytes, but
+ * fewer than the helper above names, is taken too: grad_x then stays on the fused
+ * GEMM without splits, which may take longer (a call without grad_x loses nothing). */
 size_t qlora_linear_set_act8_workspace_bound(int64_t T, int count, int r);
 
 /* ---- the loss of the head ---------------------------------------------------- */
