@@ -145,6 +145,17 @@ def test_few_tokens_of_a_very_large_vocabulary(T, D, V, packed):
 
 
 @gpu
+@pytest.mark.parametrize("T,D,V", [(64, 65536, 65600), (200, 64, 1 << 20), (1030, 8192, 9001)])
+def test_packed_pieces_with_fp32_constants(T, D, V):
+    """Pieces of a packed head without double quantization: streams that decode the rows themselves and that read
+    decoded ones, and the tiles."""
+    announce(f"head loss of pieces with fp32 constants T={T} D={D} V={V}")
+    h, w, y = (t.cuda() for t in _inputs(T, D, V, seed=33, std=1 / math.sqrt(D)))
+    q = qlora.quantize(w, double_quant=False)
+    _check(h, q, qlora.dequantize(q), y)
+
+
+@gpu
 @pytest.mark.parametrize("order", ["rising", "falling"])
 def test_exponents_of_the_streams_pieces(order):
     """Logits that rise or fall by 120 over four pieces of the streams: the sums of the pieces before and the piece's
