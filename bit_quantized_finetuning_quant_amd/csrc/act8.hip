@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "act8.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -27,59 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRuns = 4;  // runs of 8 values a thread takes, a workgroup's stride apart
 
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
-
-// max over the 8 lanes of a block
-__device__ __forceinline__ uint32_t block_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-  return v;
-}
-
-// The codes of 8 values of a block with the largest magnitude c1 (finite, > 0): the quotients Q = 127 x / c1
-// rounded to the nearest integer, ties to the even one.  x and c1 have 8 significant bits, so Q either is
-// a multiple of 1/2 or differs from every odd one by at least Q / (127 255), 259 units of its last place.
-// q = x (127 / c1) is within 4 of them; rounded to 18 significant bits (by up to 32) it is a tie where Q is
-// one, and on Q's side otherwise.  Adding 1.5 2^23 rounds that to the integer, which is then the low byte.
-__device__ __forceinline__ u32x2v encode(u32x4 x, float c1) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t pair = x[i];
-    v[2 * i] = bf16_lo(pair);
-    v[2 * i + 1] = bf16_hi(pair);
-  }
-  if (c1 < 0x1p-100f || c1 > 0x1p100f) {  // 127 / c1 or 1 / c1 would leave the range
-    const float lift = c1 < 1.0f ? 0x1p64f : 0x1p-64f;
-    c1 *= lift;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= lift;
-  }
-  const float inv = 127.0f * __builtin_amdgcn_rcpf(c1);
-  uint32_t n[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t q = (__float_as_uint(v[i] * inv) + 32u) & ~63u;
-    n[i] = __float_as_uint(__uint_as_float(q) + 12582912.0f);
-  }
-  u32x2v out;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint32_t lo = __builtin_amdgcn_perm(n[4 * w + 1], n[4 * w], 0x0C0C0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(n[4 * w + 3], n[4 * w + 2], 0x04000C0Cu);
-    out[w] = lo | hi;
-  }
-  return out;
-}
-
-// fl32(c1 / 127) of a bf16 c1 >= 0: the product with fl32(1 / 127), corrected by its remainder (right for all 128
-// significands; below 2^-100, where the remainder would be subnormal, the division itself).
-__device__ __forceinline__ float block_scale(float c1) {
-  if (c1 < 0x1p-100f) return c1 / 127.0f;
-  const float r = 1.0f / 127.0f, q = c1 * r;
-  return __builtin_fmaf(__builtin_fmaf(-q, 127.0f, c1), r, q);
-}
 
 // Values [8 i, 8 i + 8) of x per thread and run; 8 consecutive lanes share a block.
 __global__ __launch_bounds__(kThreads) void act8_encode(const uint16_t *__restrict__ x, int64_t runs,
@@ -94,20 +43,11 @@ __global__ __launch_bounds__(kThreads) void act8_encode(const uint16_t *__restri
 #pragma unroll
   for (int j = 0; j < kRuns; ++j) {
     const int64_t i = first + j * kThreads;
-    u16x2 m = {0, 0};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t a = v[j][w] & 0x7FFF7FFFu;
-      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, a));
-    }
-    const uint32_t top = block_max(max((uint32_t)m[0], (uint32_t)m[1]));
-    const float c1 = __uint_as_float(top << 16);
-    const bool finite = top < 0x7F80u;
-    u32x2v c = {0u, 0u};
-    if (finite && top != 0u) c = encode(v[j], c1);
+    float block;
+    const u32x2v c = encode_block(v[j], block);
     if (i >= runs) continue;
     __builtin_nontemporal_store(c, (u32x2v *)(codes + 8 * i));
-    if ((i & 7) == 0) scale[i >> 3] = finite ? block_scale(c1) : __uint_as_float(0x7FC00000u);
+    if ((i & 7) == 0) scale[i >> 3] = block;
   }
 }
 

@@ -290,6 +290,46 @@ hipError_t launch_head_loss(const HeadPlan &p, const uint16_t *h, const uint16_t
                             const int64_t *target, const float *weight, float scale, float *loss, float *lse,
                             uint16_t *grad, char *ws, const Codebook &cb, hipStream_t st);
 
+// Root-mean-square norm with the residual's addition (norm.hip): D % 64 == 0, D <= kNormMaxDim; weight
+// [D] fp32 or bf16.  residual and sum both or neither; y, (codes, scale), or both.
+constexpr int64_t kNormMaxDim = 65536;
+hipError_t launch_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int64_t T, int64_t D, const void *weight,
+                               bool w_fp32, float eps, uint16_t *sum, uint16_t *y, int8_t *codes, float *scale,
+                               hipStream_t st);
+// dres, grad_weight may be nullptr; part: rms_norm_part_floats with grad_weight, else nullptr.
+size_t rms_norm_part_floats(int64_t T, int64_t D);
+hipError_t launch_rms_norm_bwd(const uint16_t *dy, const uint16_t *s, const uint16_t *dres, int64_t T, int64_t D,
+                               const void *weight, bool w_fp32, float eps, uint16_t *grad_s, float *grad_weight,
+                               float *part, hipStream_t st);
+
+// The gated product h = act(gate) up (gated.hip): elementwise, and behind the projections of a gate and an
+// up weight that share x.
+enum class Activation : int { kSilu = 0, kGeluTanh = 1 };
+hipError_t launch_gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_t T, int64_t N, Activation act,
+                                uint16_t *h, int8_t *codes, float *scale, hipStream_t st);
+hipError_t launch_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const uint16_t *up, int64_t T, int64_t N,
+                                Activation act, uint16_t *dgate, uint16_t *dup, hipStream_t st);
+// What the projections leave: h, its codes with their scales, or both; gate and up both or neither.
+struct GatedOut {
+  Activation act;
+  uint16_t *h;
+  int8_t *codes;
+  float *scale;
+  uint16_t *gate, *up;
+};
+// Fused GEMM of both projections (qgemm.hip): set holds gate and up, la = u_set [M x 2 r]; every n_out % 64 == 0.
+hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
+                              const GatedOut &out, const Codebook &cb, hipStream_t st);
+struct GatedPlan {
+  int64_t T, N, K;
+  int r;
+  size_t off_u, off_part, total;
+};
+GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r);
+hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
+                                   const uint16_t *const *B, float scale, const GatedOut &out, uint16_t *u_out,
+                                   char *ws, const Codebook &cb, hipStream_t st);
+
 // Few-token sets (gemv.hip helper): a strided 2-D copy of bf16 rows.
 hipError_t launch_copy_rows(const uint16_t *src, int64_t ld_src, uint16_t *dst, int64_t ld_dst, int64_t rows,
                             int64_t cols, hipStream_t st);

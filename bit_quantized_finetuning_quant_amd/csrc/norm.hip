@@ -1,0 +1,350 @@
+// Root-mean-square norm with the residual's addition, and its backward pass
+// (gfx950).
+//
+//   s    = bf16(x + residual)                          the residual stream's next value
+//   rstd = 1 / sqrt(mean_d s_td^2 + eps)
+//   y    = bf16(w_d (s_td rstd_t))                     and / or y as an 8-bit checkpoint
+//
+//   xhat = s rstd,   c_t = mean_d(w_d dy_td xhat_td)
+//   grad_s = bf16(dres + rstd (w dy - xhat c)),        grad_w_d = sum_t dy_td xhat_td
+//
+// A row stays in registers between its sums and its results, so every value
+// crosses HBM once.  The backward pass forms rstd again from s, which it
+// reads anyway, in the same reduction as c: nothing is kept for it.
+// Sums and statistics are fp32; s, y and grad_s round once.
+//
+// Squares past fp32 (a row with |s| > 1.8e19) make the sum infinite; the row is
+// then summed again with s scaled by 2^-96, which is exact.
+
+#include <algorithm>
+
+#include "act8.hpp"
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace qlora {
+
+namespace {
+
+// w[8 i .. 8 i + 7]
+__device__ __forceinline__ void weight8(const void *w, bool wide, int i, float (&out)[8]) {
+  if (wide) {
+    const f32x4 a = ((const f32x4 *)w)[2 * i], b = ((const f32x4 *)w)[2 * i + 1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      out[j] = a[j];
+      out[4 + j] = b[j];
+    }
+  } else {
+    const u32x4 a = ((const u32x4 *)w)[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t p = a[j];
+      out[2 * j] = bf16_lo(p);
+      out[2 * j + 1] = bf16_hi(p);
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack8(const u32x4 &v, float (&out)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t p = v[j];
+    out[2 * j] = bf16_lo(p);
+    out[2 * j + 1] = bf16_hi(p);
+  }
+}
+
+// The sums of N values over the kRow threads of a row, the same in all of them.  red: a row's slots.
+template <int kRow, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N]) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], d);
+  if constexpr (kRow > 64) {
+    constexpr int kWaves = kRow / 64;
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();  // the slots' last values have been read
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) red[wave][k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      v[k] = red[0][k];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v[k] += red[w][k];
+    }
+  }
+}
+
+constexpr float kLift = 0x1p-96f;  // of s, for rows whose squares pass fp32
+
+template <int kRow>
+constexpr int block_threads() {
+  return kRow < 256 ? 256 : kRow;
+}
+
+struct NormFwd {
+  const uint16_t *x, *residual;
+  int64_t T;
+  int D;
+  const void *weight;
+  bool wide;
+  float eps;
+  uint16_t *sum, *y;
+  int8_t *codes;
+  float *scale;
+};
+
+// kRow threads a row, V runs of 8 values a thread, a row's threads apart.
+template <int kRow, int V>
+__global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_fwd(NormFwd p) {
+  constexpr int kRows = block_threads<kRow>() / kRow;
+  __shared__ float red[block_threads<kRow>() / 64][1];
+  const int lane = threadIdx.x % kRow, runs = p.D / 8;
+  for (int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow; t < p.T; t += (int64_t)gridDim.x * kRows) {
+    u32x4 s[V];
+    const int64_t row = t * p.D;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = lane + v * kRow;
+      s[v] = i < runs ? *(const u32x4 *)(p.x + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+    }
+    if (p.residual) {
+      u32x4 r[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = lane + v * kRow;
+        r[v] = i < runs ? *(const u32x4 *)(p.residual + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = lane + v * kRow;
+        float a[8], b[8];
+        unpack8(s[v], a);
+        unpack8(r[v], b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[v][j] = pack_bf16x2(a[2 * j] + b[2 * j], a[2 * j + 1] + b[2 * j + 1]);
+        if (i < runs) *(u32x4 *)(p.sum + row + 8 * i) = s[v];
+      }
+    }
+    float lift = 1.0f, rstd;
+    for (;;) {
+      float sq[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float a[8];
+        unpack8(s[v], a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float l = a[j] * lift;
+          sq[0] = __builtin_fmaf(l, l, sq[0]);
+        }
+      }
+      row_sum<kRow>(sq, red);
+      rstd = 1.0f / sqrtf(sq[0] / (float)p.D + p.eps * lift * lift);
+      if (lift != 1.0f || sq[0] < __builtin_inff()) break;  // (a NaN's sum is summed again, to the same)
+      lift = kLift;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = lane + v * kRow;
+      if (i >= runs) continue;
+      float a[8], w[8];
+      unpack8(s[v], a);
+      weight8(p.weight, p.wide, i, w);
+      u32x4 y;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        y[j] = pack_bf16x2(w[2 * j] * (a[2 * j] * lift * rstd), w[2 * j + 1] * (a[2 * j + 1] * lift * rstd));
+      if (p.y) *(u32x4 *)(p.y + row + 8 * i) = y;
+      if (p.codes) {
+        float block;
+        const act8_u32x2 c = encode_block(y, block);
+        *(act8_u32x2 *)(p.codes + row + 8 * i) = c;
+        if ((i & 7) == 0) p.scale[(row >> 6) + (i >> 3)] = block;
+      }
+    }
+  }
+}
+
+struct NormBwd {
+  const uint16_t *dy, *s, *dres;
+  int64_t T;
+  int D;
+  const void *weight;
+  bool wide;
+  float eps;
+  uint16_t *grad;
+  float *part;  // with the weight's gradient: [row groups of the grid][D]
+};
+
+template <int kRow, int V, bool kWeight>
+__global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_bwd(NormBwd p) {
+  constexpr int kRows = block_threads<kRow>() / kRow;
+  __shared__ float red[block_threads<kRow>() / 64][2];
+  const int lane = threadIdx.x % kRow, runs = p.D / 8;
+  const int64_t group = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow;
+  float gw[kWeight ? V : 1][8];
+#pragma unroll
+  for (int v = 0; v < (kWeight ? V : 1); ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[v][j] = 0.f;
+  for (int64_t t = group; t < p.T; t += (int64_t)gridDim.x * kRows) {
+    u32x4 s[V], g[V];
+    const int64_t row = t * p.D;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = lane + v * kRow;
+      s[v] = i < runs ? *(const u32x4 *)(p.s + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      g[v] = i < runs ? *(const u32x4 *)(p.dy + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+    }
+    float lift = 1.0f, rstd, c;
+    for (;;) {
+      float sum[2] = {0.f, 0.f};  // of s^2 and of w dy s
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = lane + v * kRow;
+        float a[8], b[8], w[8];
+        unpack8(s[v], a);
+        unpack8(g[v], b);
+        if (i < runs) weight8(p.weight, p.wide, i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float l = a[j] * lift;
+          sum[0] = __builtin_fmaf(l, l, sum[0]);
+          if (i < runs) sum[1] = __builtin_fmaf(w[j] * b[j], l, sum[1]);
+        }
+      }
+      row_sum<kRow>(sum, red);
+      rstd = 1.0f / sqrtf(sum[0] / (float)p.D + p.eps * lift * lift);
+      c = sum[1] * rstd / (float)p.D;
+      if (lift != 1.0f || sum[0] < __builtin_inff()) break;
+      lift = kLift;
+    }
+    const float outer = rstd * lift;  // 1 / the root of the mean square
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = lane + v * kRow;
+      if (i >= runs) continue;
+      float a[8], b[8], w[8], o[8];
+      unpack8(s[v], a);
+      unpack8(g[v], b);
+      weight8(p.weight, p.wide, i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xhat = a[j] * lift * rstd;
+        o[j] = outer * (w[j] * b[j] - xhat * c);
+        if constexpr (kWeight) gw[v][j] = __builtin_fmaf(b[j], xhat, gw[v][j]);
+      }
+      if (p.dres) {
+        float d[8];
+        unpack8(*(const u32x4 *)(p.dres + row + 8 * i), d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += d[j];
+      }
+      *(u32x4 *)(p.grad + row + 8 * i) = u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                              pack_bf16x2(o[6], o[7])};
+    }
+  }
+  if constexpr (kWeight) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = lane + v * kRow;
+      if (i >= runs) continue;
+      float *dst = p.part + group * p.D + 8 * i;
+      *(f32x4 *)dst = f32x4{gw[v][0], gw[v][1], gw[v][2], gw[v][3]};
+      *(f32x4 *)(dst + 4) = f32x4{gw[v][4], gw[v][5], gw[v][6], gw[v][7]};
+    }
+  }
+}
+
+// grad_w from the row groups' sums: 64 columns a workgroup, its 16 waves every 16th group each, in a fixed order.
+__global__ __launch_bounds__(1024) void rms_norm_weight(const float *__restrict__ part, int groups, int D,
+                                                       float *__restrict__ grad) {
+  __shared__ float sums[16][64];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63), wave = threadIdx.x >> 6;
+  float s = 0.f;
+#pragma unroll 8
+  for (int g = wave; g < groups; g += 16) s += part[(int64_t)g * D + col];
+  sums[wave][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) s += sums[w][threadIdx.x];
+  grad[col] = s;
+}
+
+// Row groups of the launch with the weight's gradient: each holds partial sums of a row's length, written and read
+// again, so they are few; two workgroups a CU.
+constexpr int kWeightBlocks = 512;
+
+// A row's threads and runs: every run in registers.
+template <typename F>
+void with_shape(int64_t D, const F &f) {
+  const int64_t runs = D / 8;
+  if (runs <= 64)
+    f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+  else if (runs <= 128)
+    f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+  else if (runs <= 256)
+    f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
+  else if (runs <= 512)
+    f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+  else if (runs <= 1024)
+    f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
+  else if (runs <= 2048)
+    f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
+  else if (runs <= 4096)
+    f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
+  else
+    f(std::integral_constant<int, 1024>(), std::integral_constant<int, 8>());
+}
+
+int rows_of_block(int64_t D) { return D <= 1024 ? 4 : 1; }
+
+int64_t weight_blocks(int64_t T, int64_t D) {
+  const int rows = rows_of_block(D);
+  return std::min<int64_t>((T + rows - 1) / rows, kWeightBlocks);
+}
+
+// Workgroups of a launch of one row (or four) each; past 2^20 they take several in turn.
+int64_t row_blocks(int64_t T, int64_t D) {
+  const int rows = rows_of_block(D);
+  return std::min<int64_t>((T + rows - 1) / rows, (int64_t)1 << 20);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int64_t T, int64_t D, const void *weight,
+                               bool w_fp32, float eps, uint16_t *sum, uint16_t *y, int8_t *codes, float *scale,
+                               hipStream_t st) {
+  const NormFwd p{x, residual, T, (int)D, weight, w_fp32, eps, sum, y, codes, scale};
+  with_shape(D, [&](auto row, auto runs) {
+    rms_norm_fwd<row(), runs()><<<(unsigned)row_blocks(T, D), block_threads<row()>(), 0, st>>>(p);
+  });
+  return hipGetLastError();
+}
+
+size_t rms_norm_part_floats(int64_t T, int64_t D) { return (size_t)(weight_blocks(T, D) * rows_of_block(D) * D); }
+
+hipError_t launch_rms_norm_bwd(const uint16_t *dy, const uint16_t *s, const uint16_t *dres, int64_t T, int64_t D,
+                               const void *weight, bool w_fp32, float eps, uint16_t *grad_s, float *grad_weight,
+                               float *part, hipStream_t st) {
+  const NormBwd p{dy, s, dres, T, (int)D, weight, w_fp32, eps, grad_s, part};
+  with_shape(D, [&](auto row, auto runs) {
+    constexpr int kThreads = block_threads<row()>();
+    if (grad_weight)
+      rms_norm_bwd<row(), runs(), true><<<(unsigned)weight_blocks(T, D), kThreads, 0, st>>>(p);
+    else
+      rms_norm_bwd<row(), runs(), false><<<(unsigned)row_blocks(T, D), kThreads, 0, st>>>(p);
+  });
+  if (grad_weight)
+    rms_norm_weight<<<(unsigned)(D / 64), 1024, 0, st>>>(part, (int)(weight_blocks(T, D) * rows_of_block(D)), (int)D,
+                                                        grad_weight);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

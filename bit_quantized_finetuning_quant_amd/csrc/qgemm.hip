@@ -34,7 +34,9 @@
 // B operand lane l holds B[8(l/32)..+7][l%32], result register q of lane l is
 // D[8(q/4) + 4(l/32) + q%4][l%32].
 
+#include "act8.hpp"
 #include "common.hpp"
+#include "gated.hpp"
 #include "launch.hpp"
 
 namespace qlora {
@@ -220,8 +222,10 @@ struct Producer {
   const uint8_t *code0;
   int64_t code_step, blk0, blk_step;
 
-  __device__ __forceinline__ void init_addressing() {
-    const int64_t n = kTransW ? (ptid >> 2) : c0 + (ptid >> 1);
+  __device__ __forceinline__ void init_addressing() { init_row(kTransW ? (ptid >> 2) : c0 + (ptid >> 1)); }
+
+  // n: the lane's weight row of stage 0
+  __device__ __forceinline__ void init_row(int64_t n) {
     const int64_t col = kTransW ? c0 + 32 * (ptid & 3) : 32 * (ptid & 1);
     code_step = kTransW ? QBK * (K / 2) : QBK / 2;
     blk_step = kTransW ? QBK * kblk_row : 1;
@@ -594,6 +598,70 @@ __device__ __forceinline__ QgemmMember set_member(const QgemmSet &s, int i) {
   return i == 0 ? s.m[0] : i == 1 ? s.m[1] : i == 2 ? s.m[2] : s.m[3];
 }
 
+// Gated tiles (forward of a gate and an up weight): a tile's 128 weight rows are 64 of each, 32 by 32 in turn, so
+// that of a consumer wave's two 32-column fragments one is gate and the other up, and both values of a column
+// are in the same lane.  Row rho of the tile is column c0 + 32 (rho / 64) + rho % 32 of member (rho / 32) % 2.
+__device__ __forceinline__ int64_t gated_row(int64_t c0, int rho) { return c0 + 32 * (rho >> 6) + (rho & 31); }
+__device__ __forceinline__ int gated_sb_row(int member, int col) { return 64 * (col >> 5) + 32 * member + (col & 31); }
+
+template <bool kDQ>
+__device__ __forceinline__ Producer<false, kDQ> gated_producer(const QgemmSet &set, int64_t c0, int ptid, float mu,
+                                                               int64_t kstep0) {
+  const bool up = (__builtin_amdgcn_readfirstlane(ptid >> 6) & 1) != 0;
+  const QWeight &g = set.m[0].w, &u = set.m[1].w;
+  Producer<false, kDQ> p{};
+  p.Kc = p.K = g.n_in;
+  p.N = g.n_out;
+  p.kblk_row = g.n_in / kBlock;
+  p.w = g;
+  if (up) {
+    p.w.codes = u.codes;
+    p.w.fp8 = u.fp8;
+    p.w.s2 = u.s2;
+  }
+  p.mu = mu;
+  p.ptid = ptid;
+  p.kstep0 = kstep0;
+  p.init_row(gated_row(c0, ptid >> 1));
+  return p;
+}
+
+// One 64-wide chunk of one member's adapter term: la's columns of that member as the activation tile, and its 64
+// rows of B (zero past r) where its weight rows lie.
+__device__ __forceinline__ void stage_lora_gated(const uint16_t *la, int64_t ld_la, const uint16_t *B, int member, int r,
+                                                 int j0, int64_t M, int64_t m0, int64_t c0, int tid, uint16_t *sa_dst,
+                                                 uint16_t *sb_dst) {
+  const bool vec = (r % 8) == 0;
+  constexpr int kA = QBM * 8 / 512;
+  u32x4 va[kA];
+#pragma unroll
+  for (int it = 0; it < kA; ++it) {
+    const int idx = tid + 512 * it, row = idx >> 3, ch = idx & 7;
+    const int64_t grow = m0 + row;
+    va[it] = grow < M ? ld8(la + grow * ld_la + (int64_t)member * r, j0 + 8 * ch, r, vec) : u32x4{0u, 0u, 0u, 0u};
+  }
+  const int col = tid >> 3, bch = tid & 7;
+  const u32x4 vb = ld8(B + (c0 + col) * r, j0 + 8 * bch, r, vec);
+#pragma unroll
+  for (int it = 0; it < kA; ++it) {
+    const int idx = tid + 512 * it;
+    *(u32x4 *)&sa_dst[act_off(idx >> 3, idx & 7)] = va[it];
+  }
+  *(u32x4 *)&sb_dst[gated_sb_row(member, col) * QLD + 8 * bch] = vb;
+}
+
+// The four slices of such a chunk: the member's fragments only.
+template <int kMember>
+__device__ __forceinline__ void consumer_slices_gated(const uint16_t *A, const uint16_t *B, int wm, int wn, int lane,
+                                                      f32x16 (&acc)[4][2]) {
+#pragma unroll
+  for (int kk = 0; kk < QBK / 16; ++kk) {
+    const u32x4 b = load_b_frag<false>(B, wn, lane, kk, kMember);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i][kMember] = mfma(load_a_frag(A, wm, lane, kk, i), b, acc[i][kMember]);
+  }
+}
+
 // One launch covers a projection set (members sharing n_in; one member for a
 // single linear):
 //   forward: the grid's column tiles run over the members in order; tile y
@@ -615,13 +683,18 @@ __device__ __forceinline__ QgemmMember set_member(const QgemmSet &s, int i) {
 // member and writes its fp32 tile to part[z][M][set.part_cols] (forward: a
 // member's column c at column 128 tile0 + c); split 0 also carries the adapter
 // term; qgemm_split_reduce adds the splits in order.
-template <bool kTransW, bool kDQ, bool kDrop, bool kClamp, bool kFull>
+// gated_out (a GatedOut; forward, kFull): the two members are gate and up, the tiles as above (grid: n_out / 64
+// columns of tiles); the epilogue forms h = act(gate) up from the fp32 accumulators and writes what it names.
+// Splits go to part[z][M][2 n_out], gate before up.
+template <bool kTransW, bool kDQ, bool kDrop, bool kClamp, bool kFull, typename... Gated>
 __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const uint16_t *__restrict__ x,
                                                 const uint16_t *__restrict__ la, const uint16_t *__restrict__ lb,
                                                 int r, float scale, uint16_t *__restrict__ gx, Codebook cb,
                                                 const uint32_t *__restrict__ keep, float *__restrict__ part,
-                                                int64_t split_steps) {
+                                                int64_t split_steps, Gated... gated_out) {
+  constexpr bool kGated = sizeof...(Gated) > 0;
   static_assert(kFull || !kClamp, "clamped rows only on grids of full tiles");
+  static_assert(!kGated || (kFull && !kTransW && !kDrop), "gated tiles are full tiles of a forward");
   __shared__ __attribute__((aligned(16))) uint16_t sa[kActStages][QBM * 64];
   __shared__ __attribute__((aligned(16))) uint16_t sb[kWStages][QBN * QLD];  // = 64 * TLD
   __shared__ float lut[16];
@@ -644,12 +717,12 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
   }
   const int64_t m0 = bx * QBM;
   int mf = 0;  // forward: the member of this column tile
-  if (!kTransW)
+  if (!kTransW && !kGated)
     for (int i = 1; i < set.count; ++i)
       if (by >= set_member(set, i).tile0) mf = i;
   const QgemmMember fm = set_member(set, mf);
   const int64_t Ncols = kTransW ? set.m[0].w.n_in : fm.w.n_out;
-  const int64_t c0 = (by - (kTransW ? 0 : fm.tile0)) * QBN;
+  const int64_t c0 = kGated ? by * (QBN / 2) : (by - (kTransW ? 0 : fm.tile0)) * QBN;
   const uint16_t *la_t = kTransW ? la : la + (int64_t)mf * r;
   const uint16_t *lb_t = kTransW ? lb : fm.lb;
   uint16_t *out = kTransW ? gx : fm.out;
@@ -691,13 +764,17 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
   // every member's tensor mean, fetched with the first codes
   float mu0 = 0.f, mu1 = 0.f, mu2 = 0.f, mu3 = 0.f;
   if (tid >= 256) {
-    if (kDQ) {
+    if (kDQ && kGated) {
+      mu0 = *set.m[(cw & 1) ? 1 : 0].w.mu;  // as gated_producer: producer wave cw - 4
+    } else if (kDQ) {
       mu0 = *set_member(set, m_begin).w.mu;
       if (m_begin + 1 < m_end) mu1 = *set_member(set, m_begin + 1).w.mu;
       if (m_begin + 2 < m_end) mu2 = *set_member(set, m_begin + 2).w.mu;
       if (m_begin + 3 < m_end) mu3 = *set_member(set, m_begin + 3).w.mu;
     }
-    if (full_first)
+    if constexpr (kGated)
+      fetch_first_codes(gated_producer<kDQ>(set, c0, tid - 256, 0.f, kstep0), nk_first, pre0, pre1, pre2);
+    else if (full_first)
       fetch_first_codes(member_producer<kTransW, kDQ>(m_first, x, M, m0, c0, tid - 256, 0.f, kstep0), nk_first, pre0, pre1,
                         pre2);
   } else if (full_first) {
@@ -721,7 +798,24 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-  for (int j0 = 0; j0 < r_eff; j0 += QBK) {
+  if constexpr (kGated) {
+    for (int member = 0; member < (r_eff > 0 ? 2 : 0); ++member)
+      for (int j0 = 0; j0 < r; j0 += QBK) {
+        stage_lora_gated(la, set.ld_la, set.m[member].lb, member, r, j0, M, m0, c0, tid, sa[2], sb[1]);
+        if (tid < 256) dma_first.wait_all();
+        __syncthreads();
+        if (tid < 256) {
+          if (member == 0)
+            consumer_slices_gated<0>(sa[2], sb[1], wm, wn, lane, acc);
+          else
+            consumer_slices_gated<1>(sa[2], sb[1], wm, wn, lane, acc);
+          __syncthreads();
+        } else if (member == 0 || j0 + QBK < r) {
+          __syncthreads();
+        }
+      }
+  }
+  for (int j0 = 0; j0 < (kGated ? 0 : r_eff); j0 += QBK) {
     stage_lora<kTransW>(la_t, set.ld_la, lb_t, r, j0, M, Ncols, m0, c0, tid, sa[2], sb[1]);
     // every wave's early DMA of stages 0 and 1 has landed before the barrier
     // (the staging's loads, issued after them, have returned already); naming
@@ -777,7 +871,11 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
       if (mi > m_begin) wg_barrier();  // the previous member's pipeline has drained
       const int mo = mi - m_begin;
       const float mu = mo == 0 ? mu0 : mo == 1 ? mu1 : mo == 2 ? mu2 : mu3;
-      const Producer<kTransW, kDQ> p = member_producer<kTransW, kDQ>(mm, x, M, m0, c0, tid - 256, mu, kstep0);
+      Producer<kTransW, kDQ> p;
+      if constexpr (kGated)
+        p = gated_producer<kDQ>(set, c0, tid - 256, mu, kstep0);
+      else
+        p = member_producer<kTransW, kDQ>(mm, x, M, m0, c0, tid - 256, mu, kstep0);
       if (full) {
         if (mi > m_begin) fetch_first_codes(p, nk, pre0, pre1, pre2);  // the first member's went out early
         producer_loop_full(p, nk, sb, pre0, pre1, pre2, cb);
@@ -891,13 +989,55 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int64_t col = c0 + wn * 64 + j * 32 + l32;
+        const int64_t col = kGated ? j * Ncols + c0 + wn * 32 + l32 : c0 + wn * 64 + j * 32 + l32;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const int64_t row = m0 + wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3);
-          if (row < M && col < Ncols) pz[row * pcols + col] = acc[i][j][q];
+          if (row < M && (kGated || col < Ncols)) pz[row * pcols + col] = acc[i][j][q];
         }
       }
+    return;
+  }
+
+  if constexpr (kGated) {
+    // The product in fp32, then up to three tiles of [256][64] bf16 through LDS ([256][72]: h and gate in the
+    // activation ring, up in the weight ring), written as 16-byte row chunks; 8 lanes hold a block of the codes.
+    const GatedOut gated = [](const GatedOut &out) { return out; }(gated_out...);
+    __syncthreads();
+    constexpr int GLD = QBN / 2 + 8;
+    static_assert(2 * QBM * GLD <= kActStages * QBM * 64 && QBM * GLD <= kWStages * QBN * QLD, "the tiles fit");
+    uint16_t *ht = &sa[0][0], *gt = ht + QBM * GLD, *ut = &sb[0][0];
+    const bool kept = gated.gate != nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int at = (wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3)) * GLD + wn * 32 + l32;
+        const float g = acc[i][0][q], u = acc[i][1][q];
+        ht[at] = __builtin_bit_cast(uint16_t, (__bf16)(gate_act(g, gated.act) * u));
+        if (kept) {
+          gt[at] = __builtin_bit_cast(uint16_t, (__bf16)g);
+          ut[at] = __builtin_bit_cast(uint16_t, (__bf16)u);
+        }
+      }
+    __syncthreads();
+    for (int idx = tid; idx < QBM * (QBN / 16); idx += 256) {
+      const int row = idx >> 3, ch = idx & 7, at = row * GLD + 8 * ch;
+      if (m0 + row >= M) continue;
+      const int64_t to = (m0 + row) * Ncols + c0 + 8 * ch;
+      const u32x4 v = *(const u32x4 *)&ht[at];
+      if (gated.h) *(u32x4 *)&gated.h[to] = v;
+      if (gated.codes) {
+        float block;
+        const act8_u32x2 c = encode_block(v, block);
+        *(act8_u32x2 *)&gated.codes[to] = c;
+        if (ch == 0) gated.scale[to >> 6] = block;
+      }
+      if (kept) {
+        *(u32x4 *)&gated.gate[to] = *(const u32x4 *)&gt[at];
+        *(u32x4 *)&gated.up[to] = *(const u32x4 *)&ut[at];
+      }
+    }
     return;
   }
 
@@ -1514,6 +1654,33 @@ hipError_t launch_qgemm_set(bool trans_w, const QgemmSet &set, int64_t M, const 
     int64_t blocks = (M * pcols / 8 + 255) / 256;
     if (blocks > 2048) blocks = 2048;
     qgemm_split_reduce<<<(unsigned)blocks, 256, 0, st>>>(pz, sp.splits, M, pcols, so);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
+                              const GatedOut &out, const Codebook &cb, hipStream_t st) {
+  QgemmSet s = set;
+  s.count = 2;
+  s.ld_la = 2 * r;
+  s.m[2] = s.m[3] = s.m[0];
+  s.part_cols = 2 * s.m[0].w.n_out;
+  const dim3 g((unsigned)((M + QBM - 1) / QBM), (unsigned)(s.m[0].w.n_out / (QBN / 2)), 1);
+  const bool clamp = M % QBM != 0;
+  if (s.m[0].w.dq) {
+    if (clamp)
+      qgemm_ws<false, true, false, true, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr,
+                                                                  nullptr, 0, out);
+    else
+      qgemm_ws<false, true, false, false, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr,
+                                                                   nullptr, 0, out);
+  } else {
+    if (clamp)
+      qgemm_ws<false, false, false, true, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr,
+                                                                   nullptr, 0, out);
+    else
+      qgemm_ws<false, false, false, false, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb,
+                                                                    nullptr, nullptr, 0, out);
   }
   return hipGetLastError();
 }

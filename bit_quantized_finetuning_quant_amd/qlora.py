@@ -12,6 +12,7 @@ import os
 import threading
 from contextlib import nullcontext
 from dataclasses import dataclass
+from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqlora_gfx950.so")
@@ -85,6 +86,15 @@ _SIGNATURES = {
     "qlora_head_loss": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
     "qlora_head_loss_nf4": (ctypes.c_int, [_P, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
     "qlora_head_loss_workspace_bytes": (_SZ, [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int]),
+    "qlora_rms_norm_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, ctypes.c_int, ctypes.c_float, _P, _P, _P, _P]),
+    "qlora_rms_norm_bwd_workspace_bytes": (_SZ, [_I64, _I64]),
+    "qlora_rms_norm_bwd": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P, ctypes.c_int, ctypes.c_float, _P, _P, _P, _SZ,
+                                          _P]),
+    "qlora_gated_act_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, ctypes.c_int, _P, _P, _P]),
+    "qlora_gated_act_bwd": (ctypes.c_int, [_P, _P, _P, _I64, _I64, ctypes.c_int, _P, _P, _P]),
+    "qlora_linear_gated_workspace_bytes": (_SZ, [_I64, _I64, _I64, ctypes.c_int]),
+    "qlora_linear_gated_fwd": (ctypes.c_int, [_P, _I64, _P, _P, _P, ctypes.c_int, ctypes.c_float, ctypes.c_int, _P, _P,
+                                              _P, _P, _P, _P, _SZ, _P]),
     "qlora_status_read": (ctypes.c_int, [_P, _P]),
     "qlora_kernel_timing_enable": (None, [ctypes.c_int]),
     "qlora_kernel_timing_read": (ctypes.c_int, [_P, _P]),
@@ -982,3 +992,277 @@ def head_loss(h, head, target, scale: float = 1.0, weight=None, loss=None, lse=N
         if vectors[3] is not lse:
             lse.copy_(vectors[3])
     return loss, lse, grad_h
+
+
+# ------------------------------------- around the linears of a feed-forward block
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _activation(name: str) -> int:
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, not {name!r}")
+    return code
+
+
+def _rows(x, name: str):
+    """(T, K) of an activation that a call may keep as an 8-bit checkpoint."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    T, K = x.shape
+    if K % 64:
+        raise ValueError(f"{name} must have a multiple of 64 columns, not {K}")
+    return T, K
+
+
+def _norm_weight(weight, chk, D: int) -> int:
+    """The dtype code of a norm's weight [D]."""
+    if weight.dtype == _torch().float32:
+        chk.f32(weight, "weight", (D,))
+        return QLORA_F32
+    chk.bf16(weight, "weight", (D,))
+    return QLORA_BF16
+
+
+def _out8(act8, T: int, K: int, chk) -> None:
+    if act8 is not None and _check_act8(act8, chk) != (T, K):
+        raise ValueError(f"act8 must hold {T} x {K} values, not {act8.codes.shape[0]} x {act8.codes.shape[1]}")
+
+
+def _ref8(act8):
+    return None if act8 is None else ctypes.byref(act8.struct())
+
+
+def rms_norm_fwd(x, weight, eps: float = 1e-6, residual=None, s=None, y=None, need_y=True, act8: Act8 = None,
+                 need_act8=False, stream=None):
+    """Root-mean-square norm of a [T x D] bf16 activation, D % 64 == 0: s = bf16(x + residual) (x itself without
+    residual) and y = bf16(weight (s / sqrt(mean s^2 + eps))), with weight [D] bf16 or fp32.  Returns (y, s, act8):
+    y is None with need_y=False, act8 the 8-bit checkpoint of y where it is given or need_act8.  s may be the
+    residual or x, which the sum then replaces."""
+    torch = _torch()
+    T, D = _rows(x, "x")
+    dev = x.device
+    chk = _Args(dev)
+    chk.bf16(x, "x", (T, D))
+    dtype = _norm_weight(weight, chk, D)
+    if residual is not None:
+        chk.bf16(residual, "residual", (T, D))
+        if s is not None:
+            chk.bf16(s, "s", (T, D))
+    elif s is not None:
+        raise ValueError("s is the sum with a residual: without one it is x")
+    need_act8 = need_act8 or act8 is not None
+    if not need_y:
+        y = None
+        if not need_act8:
+            raise ValueError("need_y=False needs an 8-bit result")
+    elif y is not None:
+        chk.bf16(y, "y", (T, D))
+    _out8(act8, T, D, chk)
+    chk.done()
+    handle = _stream_on(dev, stream)
+    with _alloc_on(stream):
+        if residual is not None and s is None:
+            s = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+        if need_y and y is None:
+            y = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+        if need_act8 and act8 is None:
+            act8 = Act8.empty(T, D, dev)
+    _check(lib().qlora_rms_norm_fwd(x.data_ptr(), _ptr(residual), T, D, weight.data_ptr(), dtype, float(eps), _ptr(s),
+                                    _ptr(y), _ref8(act8), handle), "qlora_rms_norm_fwd")
+    return y, x if s is None else s, act8
+
+
+@functools.lru_cache(maxsize=1024)
+def rms_norm_bwd_workspace_bytes(tokens: int, dim: int) -> int:
+    return int(lib().qlora_rms_norm_bwd_workspace_bytes(tokens, dim))
+
+
+def rms_norm_bwd_workspace(tokens: int, dim: int, device="cuda"):
+    """A workspace for rms_norm_bwd with the weight's gradient (one without it needs none)."""
+    torch = _torch()
+    return torch.empty(max(rms_norm_bwd_workspace_bytes(tokens, dim), 1), dtype=torch.uint8, device=device)
+
+
+def rms_norm_bwd(dy, s, weight, eps: float = 1e-6, dres=None, grad_s=None, need_grad_weight=False, grad_weight=None,
+                 workspace=None, stream=None):
+    """Backward of rms_norm_fwd from s (its second result): (grad_s bf16 [T x D], grad_weight fp32 [D] or None).
+    grad_s, the gradient of x and of residual alike, includes dres, the gradient that reaches s past the norm;
+    grad_s may be dres or dy.  grad_weight is formed where it is given or need_grad_weight."""
+    torch = _torch()
+    T, D = _rows(s, "s")
+    dev = s.device
+    chk = _Args(dev)
+    chk.bf16(dy, "dy", (T, D))
+    chk.bf16(s, "s", (T, D))
+    dtype = _norm_weight(weight, chk, D)
+    if dres is not None:
+        chk.bf16(dres, "dres", (T, D))
+    if grad_s is not None:
+        chk.bf16(grad_s, "grad_s", (T, D))
+    need_grad_weight = need_grad_weight or grad_weight is not None
+    if grad_weight is not None:
+        chk.f32(grad_weight, "grad_weight", (D,))
+    chk.done()
+    handle = _stream_on(dev, stream)
+    wsb = 0
+    with _alloc_on(stream):
+        if grad_s is None:
+            grad_s = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+        if need_grad_weight:
+            if grad_weight is None:
+                grad_weight = torch.empty(D, dtype=torch.float32, device=dev)
+            if workspace is None:
+                workspace = rms_norm_bwd_workspace(T, D, dev)
+                wsb = workspace.numel()
+            else:
+                wsb = _workspace(workspace, dev, lambda: rms_norm_bwd_workspace_bytes(T, D))
+    _check(lib().qlora_rms_norm_bwd(dy.data_ptr(), s.data_ptr(), _ptr(dres), T, D, weight.data_ptr(), dtype, float(eps),
+                                    grad_s.data_ptr(), _ptr(grad_weight), _ptr(workspace) if wsb else None, wsb, handle),
+           "qlora_rms_norm_bwd")
+    return grad_s, grad_weight
+
+
+def gated_act_fwd(gate, up, activation: str = "silu", h=None, need_h=True, act8: Act8 = None, need_act8=False,
+                  stream=None):
+    """The gated product alone: (h, act8) with h = bf16(act(gate) up) [T x N], N % 64 == 0, and its 8-bit checkpoint
+    where it is given or need_act8 (h is None with need_h=False).  activation: "silu" or "gelu_tanh".  h may be gate
+    or up."""
+    torch = _torch()
+    code = _activation(activation)
+    T, N = _rows(gate, "gate")
+    dev = gate.device
+    chk = _Args(dev)
+    chk.bf16(gate, "gate", (T, N))
+    chk.bf16(up, "up", (T, N))
+    need_act8 = need_act8 or act8 is not None
+    if not need_h:
+        h = None
+        if not need_act8:
+            raise ValueError("need_h=False needs an 8-bit result")
+    elif h is not None:
+        chk.bf16(h, "h", (T, N))
+    _out8(act8, T, N, chk)
+    chk.done()
+    handle = _stream_on(dev, stream)
+    with _alloc_on(stream):
+        if need_h and h is None:
+            h = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        if need_act8 and act8 is None:
+            act8 = Act8.empty(T, N, dev)
+    _check(lib().qlora_gated_act_fwd(gate.data_ptr(), up.data_ptr(), T, N, code, _ptr(h), _ref8(act8), handle),
+           "qlora_gated_act_fwd")
+    return h, act8
+
+
+def gated_act_bwd(dh, gate, up, activation: str = "silu", dgate=None, dup=None, stream=None):
+    """Backward of the gated product: (dgate, dup) = (bf16(dh up act'(gate)), bf16(dh act(gate))), which
+    linear_set_bwd, linear_set_bwd_act8 and linear_bwd_dropout take as the projections' dy.  dgate and dup may
+    each be any one of dh, gate and up."""
+    torch = _torch()
+    code = _activation(activation)
+    T, N = _rows(gate, "gate")
+    dev = gate.device
+    chk = _Args(dev)
+    chk.bf16(dh, "dh", (T, N))
+    chk.bf16(gate, "gate", (T, N))
+    chk.bf16(up, "up", (T, N))
+    if dgate is not None:
+        chk.bf16(dgate, "dgate", (T, N))
+    if dup is not None:
+        chk.bf16(dup, "dup", (T, N))
+    chk.done()
+    handle = _stream_on(dev, stream)
+    with _alloc_on(stream):
+        if dgate is None:
+            dgate = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        if dup is None:
+            dup = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    _check(lib().qlora_gated_act_bwd(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), T, N, code, dgate.data_ptr(),
+                                     dup.data_ptr(), handle), "qlora_gated_act_bwd")
+    return dgate, dup
+
+
+class Gated(NamedTuple):
+    """Results of linear_gated_fwd; None where a call was not asked for one."""
+    h: "object"
+    act8: "Act8"
+    gate: "object"
+    up: "object"
+    u: "object"
+
+
+@functools.lru_cache(maxsize=1024)
+def linear_gated_workspace_bytes(tokens: int, n_ff: int, n_in: int, r: int) -> int:
+    return int(lib().qlora_linear_gated_workspace_bytes(tokens, n_ff, n_in, r))
+
+
+def linear_gated_workspace(tokens: int, n_ff: int, n_in: int, r: int, device="cuda"):
+    """A workspace for linear_gated_fwd of exactly these sizes (reusable by successive calls on one stream; fewer
+    tokens may need more)."""
+    torch = _torch()
+    return torch.empty(max(linear_gated_workspace_bytes(tokens, n_ff, n_in, r), 1), dtype=torch.uint8, device=device)
+
+
+def linear_gated_fwd(x, qs, A_set, Bs, scale: float, activation: str = "silu", keep=True, h=None, need_h=True,
+                     act8: Act8 = None, need_act8=False, gate=None, up=None, u_out=None, workspace=None,
+                     stream=None) -> Gated:
+    """The gated product of a feed-forward block behind its projections: h = bf16(act(gate) up) with gate and up the
+    linear_set_fwd of qs = [gate, up] (both [n_ff x n_in], n_ff % 64 == 0), taken in fp32.  keep: gate, up and u,
+    which the backward pass reads (gated_act_bwd, then linear_set_bwd or linear_set_bwd_act8), are returned too.
+    act8: h's 8-bit checkpoint, where it is given or need_act8; need_h=False leaves out h itself."""
+    torch = _torch()
+    code = _activation(activation)
+    if len(qs) != 2:
+        raise ValueError(f"qs must hold the gate and the up weight, not {len(qs)}")
+    T, count, r, dev, chk = _set_dims(x, qs, A_set)
+    N, K = qs[0].n_out, qs[0].n_in
+    if qs[1].n_out != N:
+        raise ValueError(f"up has n_out {qs[1].n_out}, gate has {N}")
+    if N % 64:
+        raise ValueError(f"n_out must be a multiple of 64, not {N}")
+    _check_list(Bs, 2, "Bs")
+    chk.bf16(Bs[0], "Bs[0]", (N, r))
+    chk.bf16(Bs[1], "Bs[1]", (N, r))
+    need_act8 = need_act8 or act8 is not None
+    if not need_h:
+        h = None
+        if not need_act8:
+            raise ValueError("need_h=False needs an 8-bit result")
+    elif h is not None:
+        chk.bf16(h, "h", (T, N))
+    _out8(act8, T, N, chk)
+    if not keep and (gate is not None or up is not None):
+        raise ValueError("gate and up are written with keep=True")
+    if gate is not None:
+        chk.bf16(gate, "gate", (T, N))
+    if up is not None:
+        chk.bf16(up, "up", (T, N))
+    if u_out is not None:
+        chk.bf16(u_out, "u_out", (T, 2 * r))
+    chk.done()
+    handle = _stream_on(dev, stream)
+    with _alloc_on(stream):
+        bf16 = torch.bfloat16
+        if need_h and h is None:
+            h = torch.empty((T, N), dtype=bf16, device=dev)
+        if need_act8 and act8 is None:
+            act8 = Act8.empty(T, N, dev)
+        if keep:
+            if gate is None:
+                gate = torch.empty((T, N), dtype=bf16, device=dev)
+            if up is None:
+                up = torch.empty((T, N), dtype=bf16, device=dev)
+            if u_out is None:
+                u_out = torch.empty((T, 2 * r), dtype=bf16, device=dev)
+        if workspace is None:
+            ws = linear_gated_workspace(T, N, K, r, dev)
+            wsb = ws.numel()
+        else:
+            ws = workspace
+            wsb = _workspace(ws, dev, lambda: linear_gated_workspace_bytes(T, N, K, r))
+    st = (NF4WeightStruct * 2)(qs[0].struct(), qs[1].struct())
+    _check(lib().qlora_linear_gated_fwd(_ptr(x), T, st, _ptr(A_set), _ptrs(Bs), r, float(scale), code, _ptr(h),
+                                        _ref8(act8), _ptr(gate), _ptr(up), _ptr(u_out), _ptr(ws), wsb, handle),
+           "qlora_linear_gated_fwd")
+    return Gated(h, act8, gate, up, u_out)

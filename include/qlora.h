@@ -427,6 +427,75 @@ qlora_status qlora_head_loss_nf4(const uint16_t *h, int64_t T, const qlora_nf4_w
  * take another form and need more.                                            */
 size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad, int packed);
 
+/* ---- around the linears of a feed-forward block ------------------------------ */
+
+/* Root-mean-square norm of T rows of D values, with the residual's addition
+ * before it and an 8-bit checkpoint of its result:
+ *   s    = bf16( x + residual )                     the residual stream's next value
+ *   rstd = 1 / sqrt( mean_d s_td^2 + eps )          (fp32)
+ *   y    = bf16( weight_d (s_td rstd_t) )           [T x D]
+ *   *y8  = y as qlora_act8_write keeps it, code for code
+ * x, residual, sum and y [T x D] bf16, weight [D] fp32 or bf16.  residual and
+ * sum are both given or both NULL (then s = x); sum may be residual or x.  At
+ * least one of y and y8 is given; y8's T and K are T and D.
+ * Requires T >= 1, D % 64 == 0, D <= 65536, T D <= 2^37, a finite eps > 0.
+ * A NaN in a row of s makes its row of y NaN; an Inf makes it NaN there and 0
+ * elsewhere.  Finite rows of any magnitude give finite results.               */
+qlora_status qlora_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int64_t T, int64_t D, const void *weight,
+                                qlora_dtype w_dtype, float eps, uint16_t *sum, uint16_t *y, const qlora_act8 *y8,
+                                void *stream);
+
+/* Its backward pass from s (the forward's sum, or x); rstd is formed again:
+ *   xhat        = s rstd,   c_t = mean_d( weight_d dy_td xhat_td )
+ *   grad_s      = bf16( dres + rstd (weight dy - xhat c) )     [T x D]
+ *   grad_weight = sum_t dy_td xhat_td                          [D] fp32
+ * grad_s is the gradient of x and of residual alike.  dres (the gradient that
+ * reaches s past the norm; bf16) may be NULL, and grad_s may be dres or dy.
+ * grad_weight may be NULL (a frozen weight); only with it a workspace is needed
+ * (qlora_rms_norm_bwd_workspace_bytes(T, D), at most 2048 rows of D fp32 sums),
+ * whose sums are added in a fixed order.                                      */
+size_t qlora_rms_norm_bwd_workspace_bytes(int64_t T, int64_t D);
+qlora_status qlora_rms_norm_bwd(const uint16_t *dy, const uint16_t *s, const uint16_t *dres, int64_t T, int64_t D,
+                                const void *weight, qlora_dtype w_dtype, float eps, uint16_t *grad_s,
+                                float *grad_weight, void *ws, size_t ws_bytes, void *stream);
+
+/* The activation of a gated product (another code is QLORA_ERR_VALUE):
+ *   QLORA_SILU       g / (1 + exp(-g))
+ *   QLORA_GELU_TANH  g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2          */
+typedef enum { QLORA_SILU = 0, QLORA_GELU_TANH = 1 } qlora_activation;
+
+/* The gated product alone, h = bf16( act(gate) up ) [T x N] and / or its 8-bit
+ * checkpoint *h8 (as qlora_act8_write keeps h): behind projections with dropout,
+ * or to form h again in the backward pass.  gate, up [T x N] bf16; h may be
+ * either of them.  T >= 1, N % 64 == 0, T N <= 2^37.                          */
+qlora_status qlora_gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_t T, int64_t N, qlora_activation act,
+                                 uint16_t *h, const qlora_act8 *h8, void *stream);
+
+/* Its backward pass: dgate = bf16( dh up act'(gate) ), dup = bf16( dh act(gate) ),
+ * the dy of the two projections (qlora_linear_set_bwd and its like).  dgate and
+ * dup may each be any one of dh, gate and up.                                 */
+qlora_status qlora_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const uint16_t *up, int64_t T, int64_t N,
+                                 qlora_activation act, uint16_t *dgate, uint16_t *dup, void *stream);
+
+/* The gated product behind its projections, for T tokens: the projection set
+ * q[0] (gate), q[1] (up) of qlora_linear_set_fwd, with the product formed from
+ * the fp32 sums inside it:
+ *   u_set = x A_set^T
+ *   gate  = x W_hat_0^T + scale u_0 B_0^T,   up = x W_hat_1^T + scale u_1 B_1^T
+ *   h     = bf16( act(gate) up )             [T x n_ff] and / or its checkpoint *h8
+ * gate and up [T x n_ff] are also written, in bf16, where they are given (both
+ * or neither): the backward pass, qlora_gated_act_bwd, reads them.  (h is formed
+ * before they are rounded, so qlora_gated_act_fwd on them differs from h by
+ * their roundings.)  Both weights are [n_ff x n_in] and of one storage form,
+ * n_ff % 64 == 0, n_ff and n_in < 2^22; the rest as qlora_linear_set_fwd with two
+ * members.  ws: qlora_linear_gated_workspace_bytes, for these sizes (fewer
+ * tokens may take another form and need more).                                */
+size_t qlora_linear_gated_workspace_bytes(int64_t T, int64_t n_ff, int64_t n_in, int r);
+qlora_status qlora_linear_gated_fwd(const uint16_t *x, int64_t T, const qlora_nf4_weight *q, const uint16_t *A_set,
+                                    const uint16_t *const *B, int r, float scale, qlora_activation act, uint16_t *h,
+                                    const qlora_act8 *h8, uint16_t *gate, uint16_t *up, uint16_t *u_out, void *ws,
+                                    size_t ws_bytes, void *stream);
+
 /* ---- diagnostics ---------------------------------------------------------- */
 
 /* Kernel timing for benchmarks.  While enabled (non-zero), every launch of
