@@ -317,13 +317,23 @@ struct GatedOut {
   float *scale;
   uint16_t *gate, *up;
 };
-// Fused GEMM of both projections (qgemm.hip): set holds gate and up, la = u_set [M x 2 r]; every n_out % 64 == 0.
+// Fused GEMM of both projections (qgemm.hip): set holds gate and up, la = u_set [M x 2 r], n_out % 64 == 0.  Where
+// qgemm_gated_parts gives a count, that many fp32 partial tiles part[z][M][2 n_out] (gate before up) are left for
+// the caller to add; else `out` is written.
+int qgemm_gated_parts(int64_t M, int64_t N, int64_t K);
 hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
-                              const GatedOut &out, const Codebook &cb, hipStream_t st);
+                              const GatedOut &out, float *part, const Codebook &cb, hipStream_t st);
+// The few-token form (gemv.hip), where gemv_fwd_applies over both weights' rows: w holds gate and up, u_set
+// [T x 2 r] is written, part: gemv_set_fwd_part_floats of the two.
+hipError_t launch_gemv_gated(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
+                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u_set,
+                             float *part, const Codebook &cb, hipStream_t st);
 struct GatedPlan {
   int64_t T, N, K;
   int r;
-  size_t off_u, off_part, total;
+  bool few;   // the few-token form
+  int parts;  // otherwise: partial tiles of the fused GEMM (0: none)
+  size_t off_u, off_part, off_qpart, total;
 };
 GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r);
 hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const QWeight *w, const uint16_t *A_set,

@@ -626,31 +626,43 @@ __device__ __forceinline__ Producer<false, kDQ> gated_producer(const QgemmSet &s
   return p;
 }
 
-// One 64-wide chunk of one member's adapter term: la's columns of that member as the activation tile, and its 64
-// rows of B (zero past r) where its weight rows lie.
-__device__ __forceinline__ void stage_lora_gated(const uint16_t *la, int64_t ld_la, const uint16_t *B, int member, int r,
-                                                 int j0, int64_t M, int64_t m0, int64_t c0, int tid, uint16_t *sa_dst,
-                                                 uint16_t *sb_dst) {
+// One 64-wide chunk of the adapter term, which contracts over the ranks of both members in turn: la's columns j0 ..
+// (zero past 2 r) as the activation tile, and as the weight tile B of each member's columns at its own ranks, zero
+// at the other's.
+__device__ __forceinline__ void stage_lora_gated(const QgemmSet &set, const uint16_t *la, int r, int j0, int64_t M,
+                                                 int64_t m0, int64_t c0, int tid, uint16_t *sa_dst, uint16_t *sb_dst) {
   const bool vec = (r % 8) == 0;
-  constexpr int kA = QBM * 8 / 512;
-  u32x4 va[kA];
+  constexpr int kA = QBM * 8 / 512, kB = 2;
+  u32x4 va[kA], vb[kB];
 #pragma unroll
   for (int it = 0; it < kA; ++it) {
     const int idx = tid + 512 * it, row = idx >> 3, ch = idx & 7;
     const int64_t grow = m0 + row;
-    va[it] = grow < M ? ld8(la + grow * ld_la + (int64_t)member * r, j0 + 8 * ch, r, vec) : u32x4{0u, 0u, 0u, 0u};
+    va[it] = grow < M ? ld8(la + grow * set.ld_la, j0 + 8 * ch, 2 * r, vec) : u32x4{0u, 0u, 0u, 0u};
   }
-  const int col = tid >> 3, bch = tid & 7;
-  const u32x4 vb = ld8(B + (c0 + col) * r, j0 + 8 * bch, r, vec);
+#pragma unroll
+  for (int it = 0; it < kB; ++it) {  // the 64 columns of gate, then those of up, 8 chunks of the ranks each
+    const int col = tid >> 3, j = j0 + 8 * (tid & 7) - it * r;
+    const uint16_t *row = set.m[it].lb + (c0 + col) * r;
+    vb[it] = u32x4{0u, 0u, 0u, 0u};
+    if (vec) {
+      if (j >= 0 && j < r) vb[it] = *(const u32x4 *)(row + j);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j + i >= 0 && j + i < r) vb[it][i >> 1] |= (uint32_t)row[j + i] << (16 * (i & 1));
+    }
+  }
 #pragma unroll
   for (int it = 0; it < kA; ++it) {
     const int idx = tid + 512 * it;
     *(u32x4 *)&sa_dst[act_off(idx >> 3, idx & 7)] = va[it];
   }
-  *(u32x4 *)&sb_dst[gated_sb_row(member, col) * QLD + 8 * bch] = vb;
+#pragma unroll
+  for (int it = 0; it < kB; ++it) *(u32x4 *)&sb_dst[gated_sb_row(it, tid >> 3) * QLD + 8 * (tid & 7)] = vb[it];
 }
 
-// The four slices of such a chunk: the member's fragments only.
+// The four slices of a chunk that holds one member's ranks only.
 template <int kMember>
 __device__ __forceinline__ void consumer_slices_gated(const uint16_t *A, const uint16_t *B, int wm, int wn, int lane,
                                                       f32x16 (&acc)[4][2]) {
@@ -799,21 +811,22 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
   if constexpr (kGated) {
-    for (int member = 0; member < (r_eff > 0 ? 2 : 0); ++member)
-      for (int j0 = 0; j0 < r; j0 += QBK) {
-        stage_lora_gated(la, set.ld_la, set.m[member].lb, member, r, j0, M, m0, c0, tid, sa[2], sb[1]);
-        if (tid < 256) dma_first.wait_all();
+    for (int j0 = 0; j0 < 2 * r_eff; j0 += QBK) {
+      stage_lora_gated(set, la, r, j0, M, m0, c0, tid, sa[2], sb[1]);
+      if (tid < 256) dma_first.wait_all();
+      __syncthreads();
+      if (tid < 256) {
+        if (j0 + QBK <= r)
+          consumer_slices_gated<0>(sa[2], sb[1], wm, wn, lane, acc);
+        else if (j0 >= r)
+          consumer_slices_gated<1>(sa[2], sb[1], wm, wn, lane, acc);
+        else
+          consumer_slices<false>(sa[2], sb[1], wm, wn, lane, acc);
         __syncthreads();
-        if (tid < 256) {
-          if (member == 0)
-            consumer_slices_gated<0>(sa[2], sb[1], wm, wn, lane, acc);
-          else
-            consumer_slices_gated<1>(sa[2], sb[1], wm, wn, lane, acc);
-          __syncthreads();
-        } else if (member == 0 || j0 + QBK < r) {
-          __syncthreads();
-        }
+      } else if (j0 + QBK < 2 * r_eff) {
+        __syncthreads();
       }
+    }
   }
   for (int j0 = 0; j0 < (kGated ? 0 : r_eff); j0 += QBK) {
     stage_lora<kTransW>(la_t, set.ld_la, lb_t, r, j0, M, Ncols, m0, c0, tid, sa[2], sb[1]);
@@ -1008,35 +1021,33 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
     static_assert(2 * QBM * GLD <= kActStages * QBM * 64 && QBM * GLD <= kWStages * QBN * QLD, "the tiles fit");
     uint16_t *ht = &sa[0][0], *gt = ht + QBM * GLD, *ut = &sb[0][0];
     const bool kept = gated.gate != nullptr;
+    with_activation(gated.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int at = (wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3)) * GLD + wn * 32 + l32;
-        const float g = acc[i][0][q], u = acc[i][1][q];
-        ht[at] = __builtin_bit_cast(uint16_t, (__bf16)(gate_act(g, gated.act) * u));
-        if (kept) {
-          gt[at] = __builtin_bit_cast(uint16_t, (__bf16)g);
-          ut[at] = __builtin_bit_cast(uint16_t, (__bf16)u);
+        for (int q = 0; q < 16; ++q) {
+          const int at = (wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3)) * GLD + wn * 32 + l32;
+          ht[at] = __builtin_bit_cast(uint16_t, (__bf16)(gate_act<act()>(acc[i][0][q]) * acc[i][1][q]));
         }
-      }
+    });
+    if (kept) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int at = (wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3)) * GLD + wn * 32 + l32;
+          gt[at] = __builtin_bit_cast(uint16_t, (__bf16)acc[i][0][q]);
+          ut[at] = __builtin_bit_cast(uint16_t, (__bf16)acc[i][1][q]);
+        }
+    }
     __syncthreads();
     for (int idx = tid; idx < QBM * (QBN / 16); idx += 256) {
       const int row = idx >> 3, ch = idx & 7, at = row * GLD + 8 * ch;
       if (m0 + row >= M) continue;
       const int64_t to = (m0 + row) * Ncols + c0 + 8 * ch;
-      const u32x4 v = *(const u32x4 *)&ht[at];
-      if (gated.h) *(u32x4 *)&gated.h[to] = v;
-      if (gated.codes) {
-        float block;
-        const act8_u32x2 c = encode_block(v, block);
-        *(act8_u32x2 *)&gated.codes[to] = c;
-        if (ch == 0) gated.scale[to >> 6] = block;
-      }
-      if (kept) {
-        *(u32x4 *)&gated.gate[to] = *(const u32x4 *)&gt[at];
-        *(u32x4 *)&gated.up[to] = *(const u32x4 *)&ut[at];
-      }
+      const u32x4 none = {0u, 0u, 0u, 0u};
+      store_gated(gated, to, *(const u32x4 *)&ht[at], kept ? *(const u32x4 *)&gt[at] : none,
+                  kept ? *(const u32x4 *)&ut[at] : none);
     }
     return;
   }
@@ -1194,11 +1205,17 @@ __device__ __forceinline__ void sm_stage_mfma(const uint16_t *A, const uint16_t 
   }
 }
 
-template <bool kTransW, bool kDQ, int kRows>
+//
+// GatedTiles (forward): the tiles of a gate and an up weight as in qgemm_ws, 64 columns of each; waves 0 and 2
+// hold gate, 1 and 3 up.  Every workgroup writes its fp32 tile to part[z][M][2 n_out].
+struct GatedTiles {};
+template <bool kTransW, bool kDQ, int kRows, typename... Gated>
 __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, const uint16_t *__restrict__ x,
                                                    const uint16_t *__restrict__ la, const uint16_t *__restrict__ lb,
                                                    int r, float scale, uint16_t *__restrict__ gx, Codebook cb,
                                                    float *__restrict__ part, int64_t split_steps) {
+  constexpr bool kGated = sizeof...(Gated) > 0;
+  static_assert(!kGated || !kTransW, "gated tiles are a forward's");
   constexpr int kSt = kRows == 64 ? 3 : 2;  // LDS stages
   constexpr int kTiles = kRows / 32;        // 32-row MFMA tiles; also 16-byte activation chunks per thread
   __shared__ __attribute__((aligned(16))) uint16_t sa[kSt][kRows * 64];
@@ -1207,15 +1224,20 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
   const int l32 = lane & 31, lhi = lane >> 5;
   const QgemmMember mm = set.m[0];
   const int64_t Ncols = kTransW ? mm.w.n_in : mm.w.n_out, Kc = kTransW ? mm.w.n_out : mm.w.n_in;
-  const int64_t m0 = (int64_t)blockIdx.x * kRows, c0 = (int64_t)blockIdx.y * QBN;
+  const int64_t m0 = (int64_t)blockIdx.x * kRows, c0 = (int64_t)blockIdx.y * (kGated ? QBN / 2 : QBN);
   const uint16_t *act = kTransW ? mm.act : x;
   const uint16_t *lb_t = kTransW ? lb : mm.lb;
   uint16_t *out = kTransW ? gx : mm.out;
   const int64_t kstep0 = part ? (int64_t)blockIdx.z * split_steps : 0;
   const int64_t nk = part ? min(split_steps, Kc / QBK - kstep0) : Kc / QBK;
   const int r_eff = blockIdx.z == 0 ? r : 0;
-  const float mu = kDQ ? *mm.w.mu : 0.f;
-  const Producer<kTransW, kDQ> p = member_producer<kTransW, kDQ>(mm, x, M, m0, c0, tid, mu, kstep0);
+  const int own = __builtin_amdgcn_readfirstlane(w) & 1;  // kGated: the wave's member
+  const float mu = !kDQ ? 0.f : kGated && own ? *set.m[1].w.mu : *mm.w.mu;
+  Producer<kTransW, kDQ> p;
+  if constexpr (kGated)
+    p = gated_producer<kDQ>(set, c0, tid, mu, kstep0);
+  else
+    p = member_producer<kTransW, kDQ>(mm, x, M, m0, c0, tid, mu, kstep0);
 
   // this lane's activation rows (clamped) and chunk pair
   const int arow = tid >> 2, ach = 2 * (tid & 3);
@@ -1255,18 +1277,24 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
   // rank at a time through the last LDS stage (zero past r and past M)
   constexpr int kL = kSt - 1;
   const bool lvec = (r % 8) == 0 && (set.ld_la % 8) == 0;
-  for (int j0 = 0; j0 < r_eff; j0 += QBK) {
+  // kGated: gate's chunks, then up's
+  const int r_chunks = (r + QBK - 1) / QBK * QBK, rank_end = kGated && r_eff > 0 ? 2 * r_chunks : r_eff;
+  for (int jall = 0; jall < rank_end; jall += QBK) {
+    const int member = kGated && jall >= r_chunks ? 1 : 0, j0 = kGated ? jall - member * r_chunks : jall;
     u32x4 va[kTiles], vb[4];
 #pragma unroll
     for (int it = 0; it < kTiles; ++it) {  // kRows rows x 8 chunks of the rank
       const int idx = tid + 256 * it, row = idx >> 3, ch = idx & 7;
       const int64_t grow = m0 + row;
-      va[it] = grow < M ? ld8(la + grow * set.ld_la, j0 + 8 * ch, r, lvec) : u32x4{0u, 0u, 0u, 0u};
+      va[it] = grow < M ? ld8(la + grow * set.ld_la + (int64_t)member * r, j0 + 8 * ch, r, lvec) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int idx = tid + 256 * it;
-      if (!kTransW) {  // 128 output columns x 8 chunks of the rank
+      if (kGated) {  // 64 columns of the member x 8 chunks of the rank
+        const int row = idx >> 3, ch = idx & 7;
+        if (it < 2) vb[it] = ld8(set.m[member].lb + (c0 + row) * r, j0 + 8 * ch, r, lvec);
+      } else if (!kTransW) {  // 128 output columns x 8 chunks of the rank
         const int row = idx >> 3, ch = idx & 7;
         vb[it] = ld8(lb_t + (c0 + row) * r, j0 + 8 * ch, r, lvec);
       } else {  // 64 rank rows x 16 chunks of 8 columns
@@ -1283,14 +1311,16 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int idx = tid + 256 * it;
-      if (!kTransW)
+      if (kGated) {
+        if (it < 2) *(u32x4 *)&sb[kL][gated_sb_row(member, idx >> 3) * QLD + 8 * (idx & 7)] = vb[it];
+      } else if (!kTransW)
         *(u32x4 *)&sb[kL][(idx >> 3) * QLD + 8 * (idx & 7)] = vb[it];
       else
         *(u32x4 *)&sb[kL][(idx >> 4) * TLD + 8 * (idx & 15)] = vb[it];
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
     wg_barrier();
-    sm_stage_mfma<kTransW>(sa[kL], sb[kL], w, lane, acc);
+    if (!kGated || own == member) sm_stage_mfma<kTransW>(sa[kL], sb[kL], w, lane, acc);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
     wg_barrier();  // the last stage is free again
   }
@@ -1351,15 +1381,16 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
   }
 
   // element q of acc[i]: tile row 32 i + 8 (q / 4) + 4 (lane / 32) + q % 4, column 32 w + lane % 32
-  const int64_t col = c0 + 32 * w + l32;
-  if (part) {
-    float *pz = part + (int64_t)blockIdx.z * M * Ncols;
+  const int64_t col = kGated ? own * Ncols + c0 + 32 * (w >> 1) + l32 : c0 + 32 * w + l32;
+  if (kGated || part) {
+    const int64_t pcols = kGated ? 2 * Ncols : Ncols;
+    float *pz = part + (int64_t)blockIdx.z * M * pcols;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         const int64_t row = m0 + 32 * i + 8 * (q >> 2) + 4 * lhi + (q & 3);
-        if (row < M) pz[row * Ncols + col] = acc[i][q];
+        if (row < M) pz[row * pcols + col] = acc[i][q];
       }
     return;
   }
@@ -1658,30 +1689,59 @@ hipError_t launch_qgemm_set(bool trans_w, const QgemmSet &set, int64_t M, const 
   return hipGetLastError();
 }
 
+// A gated launch: few tokens on the few-token tiles, always through fp32 partial tiles; else 256-row tiles, split
+// where that fills the CUs better.
+static QgemmSplit gated_split(int64_t M, int64_t N, int64_t K) {
+  return M <= kSmMaxRows ? qgemm_sm_split(M, 2 * N, K) : qgemm_split(M, 2 * N, K);
+}
+
+int qgemm_gated_parts(int64_t M, int64_t N, int64_t K) {
+  const int splits = gated_split(M, N, K).splits;
+  return M <= kSmMaxRows || splits > 1 ? splits : 0;
+}
+
+template <bool kDQ, bool kClamp>
+static void launch_gated_ws(dim3 g, hipStream_t st, const QgemmSet &s, int64_t M, const uint16_t *x, const uint16_t *la,
+                            int r, float scale, const Codebook &cb, float *part, int64_t steps, const GatedOut &out) {
+  qgemm_ws<false, kDQ, false, kClamp, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr, part,
+                                                               steps, out);
+}
+
+template <bool kDQ, int kRows>
+static void launch_gated_sm(dim3 g, hipStream_t st, const QgemmSet &s, int64_t M, const uint16_t *x, const uint16_t *la,
+                            int r, float scale, const Codebook &cb, float *part, int64_t steps) {
+  qgemm_sm<false, kDQ, kRows, GatedTiles><<<g, 256, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, part, steps);
+}
+
 hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
-                              const GatedOut &out, const Codebook &cb, hipStream_t st) {
+                              const GatedOut &out, float *part, const Codebook &cb, hipStream_t st) {
   QgemmSet s = set;
   s.count = 2;
   s.ld_la = 2 * r;
   s.m[2] = s.m[3] = s.m[0];
-  s.part_cols = 2 * s.m[0].w.n_out;
-  const dim3 g((unsigned)((M + QBM - 1) / QBM), (unsigned)(s.m[0].w.n_out / (QBN / 2)), 1);
-  const bool clamp = M % QBM != 0;
-  if (s.m[0].w.dq) {
-    if (clamp)
-      qgemm_ws<false, true, false, true, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr,
-                                                                  nullptr, 0, out);
+  const int64_t N = s.m[0].w.n_out, K = s.m[0].w.n_in;
+  s.part_cols = 2 * N;
+  const bool dq = s.m[0].w.dq;
+  const QgemmSplit sp = gated_split(M, N, K);
+  const int64_t steps = sp.splits > 1 ? sp.steps : K / QBK;
+  if (M <= kSmMaxRows) {
+    const dim3 g(1, (unsigned)(N / (QBN / 2)), (unsigned)sp.splits);
+    if (sm_rows(M) == 64)
+      dq ? launch_gated_sm<true, 64>(g, st, s, M, x, la, r, scale, cb, part, steps)
+         : launch_gated_sm<false, 64>(g, st, s, M, x, la, r, scale, cb, part, steps);
     else
-      qgemm_ws<false, true, false, false, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr,
-                                                                   nullptr, 0, out);
-  } else {
-    if (clamp)
-      qgemm_ws<false, false, false, true, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr,
-                                                                   nullptr, 0, out);
-    else
-      qgemm_ws<false, false, false, false, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb,
-                                                                    nullptr, nullptr, 0, out);
+      dq ? launch_gated_sm<true, 128>(g, st, s, M, x, la, r, scale, cb, part, steps)
+         : launch_gated_sm<false, 128>(g, st, s, M, x, la, r, scale, cb, part, steps);
+    return hipGetLastError();
   }
+  float *pz = sp.splits > 1 ? part : nullptr;
+  const dim3 g((unsigned)((M + QBM - 1) / QBM), (unsigned)(N / (QBN / 2)), (unsigned)sp.splits);
+  if (M % QBM != 0)
+    dq ? launch_gated_ws<true, true>(g, st, s, M, x, la, r, scale, cb, pz, steps, out)
+       : launch_gated_ws<false, true>(g, st, s, M, x, la, r, scale, cb, pz, steps, out);
+  else
+    dq ? launch_gated_ws<true, false>(g, st, s, M, x, la, r, scale, cb, pz, steps, out)
+       : launch_gated_ws<false, false>(g, st, s, M, x, la, r, scale, cb, pz, steps, out);
   return hipGetLastError();
 }
 
