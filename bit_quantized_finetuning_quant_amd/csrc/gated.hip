@@ -14,12 +14,13 @@
 #include "common.hpp"
 #include "gated.hpp"
 #include "launch.hpp"
+#include "tile.hpp"
 
 namespace qlora {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWide = 256;  // threads of the elementwise kernels
 constexpr int kRuns = 2;  // runs of 8 values a thread takes, a workgroup's stride apart
 
 template <Activation kAct>
@@ -35,20 +36,20 @@ __device__ __forceinline__ u32x4 product8(const u32x4 &g, const u32x4 &u) {
 
 // 8 consecutive lanes share a block of the codes (N is a multiple of 64, so no block crosses a row).
 template <Activation kAct>
-__global__ __launch_bounds__(kThreads) void gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_t runs,
+__global__ __launch_bounds__(kWide) void gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_t runs,
                                                          uint16_t *h, int8_t *codes, float *scale) {
-  const int64_t step = (int64_t)gridDim.x * (kThreads * kRuns);
-  for (int64_t first = (int64_t)blockIdx.x * (kThreads * kRuns) + threadIdx.x; first < runs; first += step) {
+  const int64_t step = (int64_t)gridDim.x * (kWide * kRuns);
+  for (int64_t first = (int64_t)blockIdx.x * (kWide * kRuns) + threadIdx.x; first < runs; first += step) {
     u32x4 g[kRuns], u[kRuns];
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
-      const int64_t i = first + j * kThreads;
+      const int64_t i = first + j * kWide;
       g[j] = i < runs ? *(const u32x4 *)(gate + 8 * i) : u32x4{0u, 0u, 0u, 0u};
       u[j] = i < runs ? *(const u32x4 *)(up + 8 * i) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
-      const int64_t i = first + j * kThreads;
+      const int64_t i = first + j * kWide;
       if (i >= runs) continue;
       const u32x4 v = product8<kAct>(g[j], u[j]);
       if (h) *(u32x4 *)(h + 8 * i) = v;
@@ -63,21 +64,21 @@ __global__ __launch_bounds__(kThreads) void gated_act_fwd(const uint16_t *gate, 
 }
 
 template <Activation kAct>
-__global__ __launch_bounds__(kThreads) void gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const uint16_t *up,
+__global__ __launch_bounds__(kWide) void gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const uint16_t *up,
                                                          int64_t runs, uint16_t *dgate, uint16_t *dup) {
-  const int64_t step = (int64_t)gridDim.x * (kThreads * kRuns);
-  for (int64_t first = (int64_t)blockIdx.x * (kThreads * kRuns) + threadIdx.x; first < runs; first += step) {
+  const int64_t step = (int64_t)gridDim.x * (kWide * kRuns);
+  for (int64_t first = (int64_t)blockIdx.x * (kWide * kRuns) + threadIdx.x; first < runs; first += step) {
     u32x4 d[kRuns], g[kRuns], u[kRuns];
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
-      const int64_t i = first + j * kThreads;
+      const int64_t i = first + j * kWide;
       d[j] = i < runs ? *(const u32x4 *)(dh + 8 * i) : u32x4{0u, 0u, 0u, 0u};
       g[j] = i < runs ? *(const u32x4 *)(gate + 8 * i) : u32x4{0u, 0u, 0u, 0u};
       u[j] = i < runs ? *(const u32x4 *)(up + 8 * i) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
-      const int64_t i = first + j * kThreads;
+      const int64_t i = first + j * kWide;
       if (i >= runs) continue;
       u32x4 dg, du;
 #pragma unroll
@@ -97,10 +98,10 @@ __global__ __launch_bounds__(kThreads) void gated_act_bwd(const uint16_t *dh, co
 
 // h (and what else `out` names) from the fused GEMM's partial tiles part[z][T][2 N], added in order; 8 columns a thread.
 template <Activation kAct>
-__global__ __launch_bounds__(kThreads) void gated_reduce(const float *__restrict__ part, int parts, int64_t T, int64_t N,
+__global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ part, int parts, int64_t T, int64_t N,
                                                         GatedOut out) {
   const int64_t runs = T * N / 8, zs = 2 * T * N;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < runs; i += (int64_t)gridDim.x * kThreads) {
+  for (int64_t i = (int64_t)blockIdx.x * kWide + threadIdx.x; i < runs; i += (int64_t)gridDim.x * kWide) {
     const int64_t row = 8 * i / N, col = 8 * i - row * N;
     const float *p = part + row * (2 * N) + col;
     f32x4 v[4] = {};
@@ -126,12 +127,140 @@ __global__ __launch_bounds__(kThreads) void gated_reduce(const float *__restrict
   }
 }
 
-// One pass of a workgroup each, up to 2^22 of them.
-unsigned grid(int64_t runs) {
-  return (unsigned)std::min<int64_t>((runs + kThreads * kRuns - 1) / (kThreads * kRuns), (int64_t)1 << 22);
+// ---- many tokens: decoded weights in the workspace, plain tiles ------------------------------------------------
+// The fused GEMM decodes a weight tile once for every 256 tokens; from some thousand tokens on, decoding each
+// weight once (2.5 bytes a weight at HBM speed) and multiplying on plain 256 x 256 tiles is faster.
+
+// The adapter's operands with their contraction, the ranks of both members in turn, padded with zeros to `pad`
+// columns: bp [2 N][pad] (gate's rows hold B_0 at columns 0 .., up's B_1 at r ..), and up [T][pad] from u [T][2 r].
+__global__ __launch_bounds__(kWide) void gated_pack(const uint16_t *__restrict__ b0, const uint16_t *__restrict__ b1,
+                                                   const uint16_t *__restrict__ u, int64_t N, int64_t T, int r, int pad,
+                                                   uint16_t *__restrict__ bp, uint16_t *__restrict__ up) {
+  const int chunks = pad / 8;
+  const int64_t brows = 2 * N * chunks, all = brows + (up ? T * chunks : 0);
+  for (int64_t i = (int64_t)blockIdx.x * kWide + threadIdx.x; i < all; i += (int64_t)gridDim.x * kWide) {
+    const bool token = i >= brows;
+    const int64_t k = token ? i - brows : i, row = k / chunks;
+    const int c = (int)(k - row * chunks) * 8;
+    const int member = !token && row >= N ? 1 : 0, width = token ? 2 * r : r, first = c - member * r;
+    const uint16_t *src = token ? u + row * 2 * r : (member ? b1 + (row - N) * r : b0 + row * r);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (first >= 0 && first + 8 <= width) {
+      v = load8(src + first);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (first + j >= 0 && first + j < width) v[j >> 1] |= (uint32_t)src[first + j] << (16 * (j & 1));
+    }
+    *(u32x4 *)((token ? up : bp) + row * pad + c) = v;
+  }
 }
 
-size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+constexpr int kGatedPitch = 144;  // bytes of a token's 64 columns in LDS, with 16 of padding
+struct GatedTilesArgs {
+  const uint16_t *x, *u, *w, *b;  // u [T][pad]; decoded w [2 N][K], b [2 N][pad]: gate's rows, then up's
+  int64_t T, N, K;
+  int pad, nleft, ntoken;
+  float scale;
+};
+
+// One 256 x 256 tile: 128 columns of gate and of up, 16 rows of each in turn, by 256 tokens.  Of a lane's
+// accumulators acc[2 j] is gate and acc[2 j + 1] up of the same token and 4 columns, and a wave's 64 columns are
+// one block of the codes.
+__global__ __launch_bounds__(kThreads, 2) void gated_tiles(GatedTilesArgs a, GatedOut out) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+  const Tile tile = tile_at(place_of(blockIdx.x, a.nleft * a.ntoken), a.nleft, a.ntoken);
+  const int64_t t0 = (int64_t)tile.token * kTileT, d0 = (int64_t)tile.left * (kTileV / 2);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave >> 1) & 1, wn = (wave & 1) + 2 * (wave >> 2);
+  const int last_col = (int)min((int64_t)(kTileV / 2), a.N - d0) - 1, last_token = (int)min((int64_t)kTileT, a.T - t0) - 1;
+  f32x4 acc[8][4];
+  tile_zero(acc);
+  for (int half = 0; half < 2; ++half) {  // the adapter's ranks, then n_in
+    const uint32_t row_bytes = 2u * (uint32_t)(half ? a.K : (int64_t)a.pad);
+    Operands o;
+    o.left = uniform(half ? a.w + d0 * a.K : a.b + d0 * a.pad);
+    o.right = uniform(half ? a.x + t0 * a.K : a.u + t0 * a.pad);
+    o.left_step = o.right_step = 2 * kStep;
+    o.left_pitch = 0;
+    o.left_rows = 0;
+    const uint32_t up = (uint32_t)a.N * row_bytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (2 * wave + (i & 1)) * 8 + (lane >> 3), v = 128 * (r >> 6) + 64 * (i >> 1) + (r & 63);
+      const int col = min(64 * (v >> 7) + 16 * ((v >> 5) & 3) + (v & 15), last_col);
+      o.left_off[i] = (uint32_t)col * row_bytes + ((v >> 4) & 1 ? up : 0u) + (((lane & 7) ^ swizzle_rows(r)) << 4);
+      const int rt = (4 * wave + i) * 8 + (lane >> 3);
+      o.right_off[i] = (uint32_t)min(rt, last_token) * row_bytes + (((lane & 7) ^ swizzle_rows(rt)) << 4);
+    }
+    product<false, false>(o, (int)((half ? a.K : a.pad) / kStep), lds, nullptr, false, acc);
+    if (half == 0) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[m][n][q] *= a.scale;
+    }
+  }
+  if (d0 + 64 * wm >= a.N) return;
+  // A wave's 64 tokens by 64 columns go through its own part of the LDS, so that rows are written 128 bytes at a
+  // time: first h, then gate and up.
+  char *mine = lds + wave * (2 * kStage / 8);
+  auto put = [&](auto value) {  // value(m pair, n, q): bf16 pairs of columns 16 j + 4 (lane / 16) + 2 p ..
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *(uint2 *)(mine + (16 * n + (lane & 15)) * kGatedPitch + 32 * j + 8 * (lane >> 4)) =
+            make_uint2(value(j, n, 0), value(j, n, 2));
+  };
+  auto each_row = [&](auto f) {  // f(element of the outputs, the run's 8 values), 8 lanes a token
+    TILE_WAIT_LDS();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = 8 * i + (lane >> 3);
+      const u32x4 v = *(const u32x4 *)(mine + t * kGatedPitch + 16 * (lane & 7));
+      if (64 * wn + t <= last_token) f((t0 + 64 * wn + t) * a.N + d0 + 64 * wm + 8 * (lane & 7), v);
+    }
+    TILE_WAIT_LDS();
+  };
+  with_activation(out.act, [&](auto act) {
+    put([&](int j, int n, int q) {
+      return pack_bf16x2(gate_act<act()>(acc[2 * j][n][q]) * acc[2 * j + 1][n][q],
+                         gate_act<act()>(acc[2 * j][n][q + 1]) * acc[2 * j + 1][n][q + 1]);
+    });
+  });
+  each_row([&](int64_t to, const u32x4 &v) {
+    if (out.h) *(u32x4 *)(out.h + to) = v;
+    if (out.codes) {
+      float block;
+      const act8_u32x2 c = encode_block(v, block);
+      *(act8_u32x2 *)(out.codes + to) = c;
+      if ((lane & 7) == 0) out.scale[to >> 6] = block;
+    }
+  });
+  if (!out.gate) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    put([&](int j, int n, int q) { return pack_bf16x2(acc[2 * j + k][n][q], acc[2 * j + k][n][q + 1]); });
+    uint16_t *dst = k ? out.up : out.gate;
+    each_row([&](int64_t to, const u32x4 &v) { *(u32x4 *)(dst + to) = v; });
+  }
+}
+
+// Whether the decoded form is taken.
+bool decode_pays(int64_t T, int64_t N, int64_t K) {
+  // offsets within a tile, from its first row of gate to its last of up, stay below 2^32; a launch's threads too
+  if (N * K > (int64_t)1 << 29 || K > 65536 || cdiv(N, kTileV / 2) * cdiv(T, kTileT) > (int64_t)1 << 22) return false;
+  return T >= 512;
+}
+
+// One pass of a workgroup each, up to 2^22 of them.
+unsigned grid(int64_t runs) {
+  return (unsigned)std::min<int64_t>((runs + kWide * kRuns - 1) / (kWide * kRuns), (int64_t)1 << 22);
+}
 
 }  // namespace
 
@@ -139,7 +268,7 @@ hipError_t launch_gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_
                                 uint16_t *h, int8_t *codes, float *scale, hipStream_t st) {
   const int64_t runs = T * N / 8;
   with_activation(act, [&](auto a) {
-    gated_act_fwd<a()><<<grid(runs), kThreads, 0, st>>>(gate, up, runs, h, codes, scale);
+    gated_act_fwd<a()><<<grid(runs), kWide, 0, st>>>(gate, up, runs, h, codes, scale);
   });
   return hipGetLastError();
 }
@@ -148,7 +277,7 @@ hipError_t launch_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const 
                                 Activation act, uint16_t *dgate, uint16_t *dup, hipStream_t st) {
   const int64_t runs = T * N / 8;
   with_activation(act, [&](auto a) {
-    gated_act_bwd<a()><<<grid(runs), kThreads, 0, st>>>(dh, gate, up, runs, dgate, dup);
+    gated_act_bwd<a()><<<grid(runs), kWide, 0, st>>>(dh, gate, up, runs, dgate, dup);
   });
   return hipGetLastError();
 }
@@ -160,7 +289,8 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   p.K = K;
   p.r = r;
   p.few = gemv_fwd_applies(T, 2 * N, K);
-  p.parts = p.few ? 0 : qgemm_gated_parts(T, N, K);
+  p.decode = !p.few && decode_pays(T, N, K);
+  p.parts = p.few || p.decode ? 0 : qgemm_gated_parts(T, N, K);
   const int64_t both[2] = {N, N};
   size_t off = 256;
   p.off_u = off;
@@ -169,6 +299,14 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   off += align256((p.few ? gemv_set_fwd_part_floats(T, both, 2, K, r) : lora_part_floats(T, 2 * r, K)) * 4);
   p.off_qpart = off;
   off += align256((size_t)p.parts * T * 2 * N * 4);
+  // the decoded form: both weights, the adapter's operands (u as it is where its ranks need no padding)
+  const size_t pad = (size_t)(2 * r + 63) / 64 * 64;
+  p.off_w = off;
+  off += p.decode ? align256((size_t)2 * N * K * 2) : 0;
+  p.off_b = off;
+  off += p.decode ? align256((size_t)2 * N * pad * 2) : 0;
+  p.off_up = off;
+  off += p.decode && pad != (size_t)2 * r ? align256((size_t)T * pad * 2) : 0;
   p.total = off;
   return p;
 }
@@ -181,6 +319,26 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
   if (p.few) return launch_gemv_gated(p.T, x, w, A_set, B, p.r, scale, out, u, part, cb, st);
   hipError_t e = launch_lora(LoraKind::kU, x, p.K, A_set, p.K, p.T, 2 * p.r, p.K, 1.0f, u, part, st);
   if (e != hipSuccess) return e;
+  if (p.decode) {
+    const int pad = (2 * p.r + 63) / 64 * 64;
+    uint16_t *wd = (uint16_t *)(ws + p.off_w), *bp = (uint16_t *)(ws + p.off_b);
+    uint16_t *up = pad != 2 * p.r ? (uint16_t *)(ws + p.off_up) : nullptr;
+    DequantSet set{};
+    set.count = 2;
+    for (int i = 0; i < 2; ++i) {
+      set.w[i] = w[i];
+      set.out[i] = wd + i * p.N * p.K;
+    }
+    e = launch_dequantize_set(set, cb, st);
+    if (e != hipSuccess) return e;
+    const int64_t chunks = (2 * p.N + (up ? p.T : 0)) * (pad / 8);
+    gated_pack<<<(unsigned)std::min<int64_t>(cdiv(chunks, kWide), 2048), kWide, 0, st>>>(B[0], B[1], u, p.N, p.T, p.r, pad,
+                                                                                     bp, up);
+    const int nleft = (int)cdiv(p.N, kTileV / 2), ntoken = (int)cdiv(p.T, kTileT);
+    const GatedTilesArgs a{x, up ? up : u, wd, bp, p.T, p.N, p.K, pad, nleft, ntoken, scale};
+    gated_tiles<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(a, out);
+    return hipGetLastError();
+  }
   QgemmSet s{};
   for (int i = 0; i < 2; ++i) {
     s.m[i].w = w[i];
@@ -188,9 +346,9 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
   }
   e = launch_qgemm_gated(s, p.T, x, u, p.r, scale, out, qpart, cb, st);
   if (e != hipSuccess || p.parts == 0) return e;
-  const int64_t blocks = (p.T * p.N / 8 + kThreads - 1) / kThreads;
+  const int64_t blocks = (p.T * p.N / 8 + kWide - 1) / kWide;
   with_activation(out.act, [&](auto a) {
-    gated_reduce<a()><<<(unsigned)std::min<int64_t>(blocks, 2048), kThreads, 0, st>>>(qpart, p.parts, p.T, p.N, out);
+    gated_reduce<a()><<<(unsigned)std::min<int64_t>(blocks, 2048), kWide, 0, st>>>(qpart, p.parts, p.T, p.N, out);
   });
   return hipGetLastError();
 }

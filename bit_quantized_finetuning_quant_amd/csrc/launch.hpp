@@ -331,9 +331,10 @@ hipError_t launch_gemv_gated(int64_t T, const uint16_t *x, const QWeight *w, con
 struct GatedPlan {
   int64_t T, N, K;
   int r;
-  bool few;   // the few-token form
-  int parts;  // otherwise: partial tiles of the fused GEMM (0: none)
-  size_t off_u, off_part, off_qpart, total;
+  bool few;     // the few-token form
+  bool decode;  // decoded weights on plain tiles
+  int parts;    // otherwise: partial tiles of the fused GEMM (0: none)
+  size_t off_u, off_part, off_qpart, off_w, off_b, off_up, total;
 };
 GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r);
 hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
