@@ -14,8 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqlora_gfx950.so")
 SOURCES = ["codec.hip", "qgemm.hip", "lora.hip", "gemv.hip", "linear.hip", "optim.hip", "dropout.hip",
-           "act8.hip", "ragged.hip", "head.hip", "norm.hip", "gated.hip", "api.hip", "api_train.hip",
-           "api_mlp.hip"]
+           "act8.hip", "ragged.hip", "head.hip", "norm.hip", "gated.hip", "gated_few.hip", "api.hip",
+           "api_train.hip", "api_mlp.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

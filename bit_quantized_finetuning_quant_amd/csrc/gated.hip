@@ -288,15 +288,16 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   p.N = N;
   p.K = K;
   p.r = r;
-  p.few = gemv_fwd_applies(T, 2 * N, K);
+  p.few = gated_few_applies(T, N, K);
   p.decode = !p.few && decode_pays(T, N, K);
   p.parts = p.few || p.decode ? 0 : qgemm_gated_parts(T, N, K);
-  const int64_t both[2] = {N, N};
   size_t off = 256;
   p.off_u = off;
   off += align256((size_t)T * 2 * r * 2);
   p.off_part = off;
-  off += align256((p.few ? gemv_set_fwd_part_floats(T, both, 2, K, r) : lora_part_floats(T, 2 * r, K)) * 4);
+  off += align256(p.few ? gated_few_xp_values(T, K) * 2 : lora_part_floats(T, 2 * r, K) * 4);
+  p.off_h = off;  // the few-token form's h where only its codes are wanted
+  off += p.few ? align256((size_t)T * N * 2) : 0;
   p.off_qpart = off;
   off += align256((size_t)p.parts * T * 2 * N * 4);
   // the decoded form: both weights, the adapter's operands (u as it is where its ranks need no padding)
@@ -316,7 +317,14 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
                                    char *ws, const Codebook &cb, hipStream_t st) {
   uint16_t *u = u_out ? u_out : (uint16_t *)(ws + p.off_u);
   float *part = (float *)(ws + p.off_part), *qpart = (float *)(ws + p.off_qpart);
-  if (p.few) return launch_gemv_gated(p.T, x, w, A_set, B, p.r, scale, out, u, part, cb, st);
+  if (p.few) {
+    GatedOut plain = out;
+    plain.codes = nullptr;
+    if (!out.h) plain.h = (uint16_t *)(ws + p.off_h);
+    const hipError_t e = launch_gated_few(p.T, x, w, A_set, B, p.r, scale, plain, u, (uint16_t *)part, cb, st);
+    if (e != hipSuccess || !out.codes) return e;
+    return launch_act8_encode(plain.h, p.T, p.N, out.codes, out.scale, st);
+  }
   hipError_t e = launch_lora(LoraKind::kU, x, p.K, A_set, p.K, p.T, 2 * p.r, p.K, 1.0f, u, part, st);
   if (e != hipSuccess) return e;
   if (p.decode) {

@@ -328,13 +328,21 @@ hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x,
 hipError_t launch_gemv_gated(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
                              const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u_set,
                              float *part, const Codebook &cb, hipStream_t st);
+// Up to kGatedFewTokens tokens in one pass (gated_few.hip): u [T x 2 r] is written, xp holds x laid out for the
+// products; out.h is given and out.codes is not.
+constexpr int64_t kGatedFewTokens = 128;
+bool gated_few_applies(int64_t T, int64_t N, int64_t K);
+size_t gated_few_xp_values(int64_t T, int64_t K);
+hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
+                            const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
+                            const Codebook &cb, hipStream_t st);
 struct GatedPlan {
   int64_t T, N, K;
   int r;
   bool few;     // the few-token form
   bool decode;  // decoded weights on plain tiles
   int parts;    // otherwise: partial tiles of the fused GEMM (0: none)
-  size_t off_u, off_part, off_qpart, off_w, off_b, off_up, total;
+  size_t off_u, off_part, off_qpart, off_w, off_b, off_up, off_h, total;
 };
 GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r);
 hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
