@@ -96,7 +96,23 @@ __global__ __launch_bounds__(kWide) void gated_act_bwd(const uint16_t *dh, const
   }
 }
 
-// h (and what else `out` names) from the fused GEMM's partial tiles part[z][T][2 N], added in order; 8 columns a thread.
+// Eight values of gate (v[0], v[1]) and of up (v[2], v[3]) to `out`.
+template <Activation kAct>
+__device__ __forceinline__ void finish8(const GatedOut &out, int64_t to, const f32x4 (&v)[4]) {
+  u32x4 h, g, u;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float g0 = v[k][2 * q], g1 = v[k][2 * q + 1], u0 = v[2 + k][2 * q], u1 = v[2 + k][2 * q + 1];
+      h[2 * k + q] = pack_bf16x2(gate_act<kAct>(g0) * u0, gate_act<kAct>(g1) * u1);
+      g[2 * k + q] = pack_bf16x2(g0, g1);
+      u[2 * k + q] = pack_bf16x2(u0, u1);
+    }
+  store_gated(out, to, h, g, u);
+}
+
+// The same from the few-token tiles' fp32 results part[z][T][2 N], added in order; 8 columns a thread.
 template <Activation kAct>
 __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ part, int parts, int64_t T, int64_t N,
                                                         GatedOut out) {
@@ -113,17 +129,7 @@ __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ 
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[k][q] += a[q];
       }
-    u32x4 h, g, u;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float g0 = v[k][2 * q], g1 = v[k][2 * q + 1], u0 = v[2 + k][2 * q], u1 = v[2 + k][2 * q + 1];
-        h[2 * k + q] = pack_bf16x2(gate_act<kAct>(g0) * u0, gate_act<kAct>(g1) * u1);
-        g[2 * k + q] = pack_bf16x2(g0, g1);
-        u[2 * k + q] = pack_bf16x2(u0, u1);
-      }
-    store_gated(out, 8 * i, h, g, u);
+    finish8<kAct>(out, 8 * i, v);
   }
 }
 
@@ -160,8 +166,9 @@ constexpr int kGatedPitch = 144;  // bytes of a token's 64 columns in LDS, with 
 struct GatedTilesArgs {
   const uint16_t *x, *u, *w, *b;  // u [T][pad]; decoded w [2 N][K], b [2 N][pad]: gate's rows, then up's
   int64_t T, N, K;
-  int pad, nleft, ntoken;
+  int pad, nleft, ntoken, full, tail, steps;  // steps: of a tail tile's range
   float scale;
+  float *part;  // [range][tail tile][256 tokens][256]
 };
 
 // One 256 x 256 tile: 128 columns of gate and of up, 16 rows of each in turn, by 256 tokens.  Of a lane's
@@ -169,7 +176,10 @@ struct GatedTilesArgs {
 // one block of the codes.
 __global__ __launch_bounds__(kThreads, 2) void gated_tiles(GatedTilesArgs a, GatedOut out) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-  const Tile tile = tile_at(place_of(blockIdx.x, a.nleft * a.ntoken), a.nleft, a.ntoken);
+  const int id = blockIdx.x, over = id - a.full;
+  const bool split = over >= 0;
+  const int tail_tile = split ? over % a.tail : 0, range = split ? over / a.tail : 0;
+  const Tile tile = tile_at(split ? a.full + tail_tile : place_of(id, a.full), a.nleft, a.ntoken);
   const int64_t t0 = (int64_t)tile.token * kTileT, d0 = (int64_t)tile.left * (kTileV / 2);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -177,11 +187,13 @@ __global__ __launch_bounds__(kThreads, 2) void gated_tiles(GatedTilesArgs a, Gat
   const int last_col = (int)min((int64_t)(kTileV / 2), a.N - d0) - 1, last_token = (int)min((int64_t)kTileT, a.T - t0) - 1;
   f32x4 acc[8][4];
   tile_zero(acc);
-  for (int half = 0; half < 2; ++half) {  // the adapter's ranks, then n_in
+  const int all_steps = (int)(a.K / kStep), first = split ? range * a.steps : 0;
+  const int steps = split ? min(a.steps, all_steps - first) : all_steps;
+  for (int half = range == 0 ? 0 : 1; half < 2; ++half) {  // the adapter's ranks (the first range's), then n_in
     const uint32_t row_bytes = 2u * (uint32_t)(half ? a.K : (int64_t)a.pad);
     Operands o;
-    o.left = uniform(half ? a.w + d0 * a.K : a.b + d0 * a.pad);
-    o.right = uniform(half ? a.x + t0 * a.K : a.u + t0 * a.pad);
+    o.left = uniform(half ? a.w + d0 * a.K + first * kStep : a.b + d0 * a.pad);
+    o.right = uniform(half ? a.x + t0 * a.K + first * kStep : a.u + t0 * a.pad);
     o.left_step = o.right_step = 2 * kStep;
     o.left_pitch = 0;
     o.left_rows = 0;
@@ -194,7 +206,7 @@ __global__ __launch_bounds__(kThreads, 2) void gated_tiles(GatedTilesArgs a, Gat
       const int rt = (4 * wave + i) * 8 + (lane >> 3);
       o.right_off[i] = (uint32_t)min(rt, last_token) * row_bytes + (((lane & 7) ^ swizzle_rows(rt)) << 4);
     }
-    product<false, false>(o, (int)((half ? a.K : a.pad) / kStep), lds, nullptr, false, acc);
+    product<false, false>(o, half ? steps : a.pad / kStep, lds, nullptr, false, acc);
     if (half == 0) {
 #pragma unroll
       for (int m = 0; m < 8; ++m)
@@ -203,6 +215,15 @@ __global__ __launch_bounds__(kThreads, 2) void gated_tiles(GatedTilesArgs a, Gat
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[m][n][q] *= a.scale;
     }
+  }
+  if (split) {
+    float *dst = a.part + ((int64_t)range * a.tail + tail_tile) * (kTileT * kTileV);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+        *(f32x4 *)(dst + (64 * wn + 16 * n + (lane & 15)) * kTileV + 128 * wm + 16 * m + 4 * (lane >> 4)) = acc[m][n];
+    return;
   }
   if (d0 + 64 * wm >= a.N) return;
   // A wave's 64 tokens by 64 columns go through its own part of the LDS, so that rows are written 128 bytes at a
@@ -250,11 +271,72 @@ __global__ __launch_bounds__(kThreads, 2) void gated_tiles(GatedTilesArgs a, Gat
   }
 }
 
+// h (and what else `out` names) of tail tiles from their ranges' fp32 tiles, added in order; 8 columns a thread.  kPlain:
+// tiles of gated_tiles (128 columns, 16 of gate and 16 of up in turn), otherwise of the fused GEMM (64 columns of gate,
+// then of up).
+template <Activation kAct, bool kPlain>
+__global__ __launch_bounds__(kWide) void gated_tail(const float *__restrict__ part, GatedRounds rounds, int nleft,
+                                                   int ntoken, int64_t T, int64_t N, GatedOut out) {
+  constexpr int kCols = kPlain ? 128 : 64, kRow = 2 * kCols, kRunsRow = kCols / 8;
+  constexpr int kTile = 256 * kRow;
+  const int64_t i = (int64_t)blockIdx.x * kWide + threadIdx.x;
+  const int tail_tile = (int)(i / (256 * kRunsRow)), in = (int)(i % (256 * kRunsRow));
+  const int t = in / kRunsRow, c = 8 * (in % kRunsRow);
+  int64_t token, col;
+  if (kPlain) {
+    const Tile tile = tile_at(rounds.full + tail_tile, nleft, ntoken);
+    token = (int64_t)tile.token * 256 + t;
+    col = (int64_t)tile.left * kCols + c;
+  } else {
+    const int tile = rounds.full + tail_tile, left = tile / ntoken;
+    token = (int64_t)(tile - left * ntoken) * 256 + t;
+    col = (int64_t)left * kCols + c;
+  }
+  if (token >= T || col >= N) return;
+  const int at = kPlain ? 128 * (c >> 6) + 32 * ((c >> 4) & 3) + (c & 15) : c, up = kPlain ? 16 : kCols;
+  const float *p = part + (int64_t)tail_tile * kTile + t * kRow + at;
+  f32x4 v[4] = {};
+#pragma unroll 2
+  for (int z = 0; z < rounds.splits; ++z)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f32x4 a = *(const f32x4 *)(p + (int64_t)z * rounds.tail * kTile + (k >> 1) * up + 4 * (k & 1));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[k][q] += a[q];
+    }
+  finish8<kAct>(out, token * N + col, v);
+}
+
+template <bool kPlain>
+void launch_tail(const float *part, const GatedRounds &rounds, int nleft, int ntoken, int64_t T, int64_t N,
+                 const GatedOut &out, hipStream_t st) {
+  with_activation(out.act, [&](auto a) {
+    gated_tail<a(), kPlain><<<(unsigned)(rounds.tail * (kPlain ? 16 : 8)), kWide, 0, st>>>(part, rounds, nleft, ntoken, T, N,
+                                                                                        out);
+  });
+}
+
+// The two forms' times in us (fitted to 512 to 4096 tokens of n_ff x n_in = 5504 x 2048, 11008 x 4096 and 22016 x 8192,
+// within 5%).
+constexpr double kFusedRound = 5.0, kFusedStep = 0.98, kPlainRound = 7.0, kPlainStep = 1.235;
+constexpr int64_t kFusedTile = 256 * 128 * 4, kPlainTile = 256 * 256 * 4;
+double fused_us(int64_t T, int64_t N, int64_t K, GatedRounds *rounds) {
+  double us;
+  *rounds = gated_rounds(cdiv(T, 256) * (N / 64), K / 64, kFusedRound, kFusedStep, kFusedTile, &us);
+  return 14.0 + us;
+}
+double plain_us(int64_t T, int64_t N, int64_t K, GatedRounds *rounds) {
+  double us;
+  *rounds = gated_rounds(cdiv(N, kTileV / 2) * cdiv(T, kTileT), K / 64, kPlainRound, kPlainStep, kPlainTile, &us);
+  return 20.0 + us + 5.0 * (double)N * K / 5.1e6;
+}
+
 // Whether the decoded form is taken.
 bool decode_pays(int64_t T, int64_t N, int64_t K) {
   // offsets within a tile, from its first row of gate to its last of up, stay below 2^32; a launch's threads too
   if (N * K > (int64_t)1 << 29 || K > 65536 || cdiv(N, kTileV / 2) * cdiv(T, kTileT) > (int64_t)1 << 22) return false;
-  return T >= 512;
+  GatedRounds r;
+  return 1.03 * plain_us(T, N, K, &r) < fused_us(T, N, K, &r);
 }
 
 // One pass of a workgroup each, up to 2^22 of them.
@@ -282,6 +364,24 @@ hipError_t launch_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const 
   return hipGetLastError();
 }
 
+GatedRounds gated_rounds(int64_t tiles, int64_t steps, double round_us, double step_us, int64_t tile_bytes, double *us) {
+  GatedRounds best{(int)tiles, 0, 0, 0};
+  *us = (double)cdiv(tiles, 256) * (round_us + step_us * steps);
+  const int64_t full = tiles / 256 * 256, tail = tiles - full;
+  for (int64_t s = 2; tail && s <= 16 && steps / s >= 4; ++s) {
+    const int64_t range = cdiv(steps, s), splits = cdiv(steps, range);
+    // an fp32 tile is written and read at about 4 bytes a ps, by one launch more
+    const double t = (double)(full / 256) * (round_us + step_us * steps) +
+                     (double)cdiv(tail * splits, 256) * (round_us + step_us * range) +
+                     2.0 * tail * splits * tile_bytes / 4e6 + 4.0;
+    if (t < *us) {
+      *us = t;
+      best = GatedRounds{(int)full, (int)tail, (int)splits, range};
+    }
+  }
+  return best;
+}
+
 GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   GatedPlan p{};
   p.T = T;
@@ -289,8 +389,13 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   p.K = K;
   p.r = r;
   p.few = gated_few_applies(T, N, K);
-  p.decode = !p.few && decode_pays(T, N, K);
-  p.parts = p.few || p.decode ? 0 : qgemm_gated_parts(T, N, K);
+  p.parts = p.few || T > kGatedSmTokens ? 0 : qgemm_gated_parts(T, N, K);
+  p.decode = !p.few && p.parts == 0 && decode_pays(T, N, K);
+  size_t tail = 0;
+  if (!p.few && p.parts == 0) {
+    p.decode ? plain_us(T, N, K, &p.rounds) : fused_us(T, N, K, &p.rounds);
+    tail = (size_t)p.rounds.tail * p.rounds.splits * (p.decode ? kPlainTile : kFusedTile);
+  }
   size_t off = 256;
   p.off_u = off;
   off += align256((size_t)T * 2 * r * 2);
@@ -299,7 +404,7 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   p.off_h = off;  // the few-token form's h where only its codes are wanted
   off += p.few ? align256((size_t)T * N * 2) : 0;
   p.off_qpart = off;
-  off += align256((size_t)p.parts * T * 2 * N * 4);
+  off += align256(std::max((size_t)p.parts * T * 2 * N * 4, tail));
   // the decoded form: both weights, the adapter's operands (u as it is where its ranks need no padding)
   const size_t pad = (size_t)(2 * r + 63) / 64 * 64;
   p.off_w = off;
@@ -343,8 +448,11 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
     gated_pack<<<(unsigned)std::min<int64_t>(cdiv(chunks, kWide), 2048), kWide, 0, st>>>(B[0], B[1], u, p.N, p.T, p.r, pad,
                                                                                      bp, up);
     const int nleft = (int)cdiv(p.N, kTileV / 2), ntoken = (int)cdiv(p.T, kTileT);
-    const GatedTilesArgs a{x, up ? up : u, wd, bp, p.T, p.N, p.K, pad, nleft, ntoken, scale};
-    gated_tiles<<<(unsigned)(nleft * ntoken), kThreads, 0, st>>>(a, out);
+    const GatedRounds &g = p.rounds;
+    const GatedTilesArgs a{x,  up ? up : u, wd,     bp,     p.T,          p.N,   p.K,  pad,
+                           nleft, ntoken,      g.full, g.tail, (int)g.steps, scale, qpart};
+    gated_tiles<<<(unsigned)(g.full + g.tail * g.splits), kThreads, 0, st>>>(a, out);
+    if (g.tail) launch_tail<true>(qpart, g, nleft, ntoken, p.T, p.N, out, st);
     return hipGetLastError();
   }
   QgemmSet s{};
@@ -352,12 +460,15 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
     s.m[i].w = w[i];
     s.m[i].lb = B[i];
   }
-  e = launch_qgemm_gated(s, p.T, x, u, p.r, scale, out, qpart, cb, st);
-  if (e != hipSuccess || p.parts == 0) return e;
-  const int64_t blocks = (p.T * p.N / 8 + kWide - 1) / kWide;
-  with_activation(out.act, [&](auto a) {
-    gated_reduce<a()><<<(unsigned)std::min<int64_t>(blocks, 2048), kWide, 0, st>>>(qpart, p.parts, p.T, p.N, out);
-  });
+  e = launch_qgemm_gated(s, p.T, x, u, p.r, scale, p.rounds, out, qpart, cb, st);
+  if (e != hipSuccess) return e;
+  if (p.rounds.tail) launch_tail<false>(qpart, p.rounds, (int)(p.N / 64), (int)cdiv(p.T, 256), p.T, p.N, out, st);
+  if (p.parts) {
+    const int64_t blocks = cdiv(p.T * p.N / 8, kWide);
+    with_activation(out.act, [&](auto a) {
+      gated_reduce<a()><<<(unsigned)std::min<int64_t>(blocks, 2048), kWide, 0, st>>>(qpart, p.parts, p.T, p.N, out);
+    });
+  }
   return hipGetLastError();
 }
 

@@ -1,4 +1,4 @@
-// The gated product behind its projections for up to 128 tokens (gfx950).
+// The gated product behind its projections for up to 64 tokens (gfx950).
 //
 // Reading and decoding the 4-bit weights is the work here, so every code is read once, decoded once in the
 // registers of the lane that multiplies it, and used for all tokens; nothing of W goes through LDS.
@@ -27,7 +27,7 @@ namespace {
 constexpr int kChunkBlocks = 4;            // NF4 blocks of a row in a chunk
 constexpr int kChunk = 64 * kChunkBlocks;  // n_in of a chunk
 constexpr int kWaves = 4;                  // waves of a workgroup
-constexpr int kPrepWaves = 16;
+constexpr int kPrepWaves = 8, kPrepRows = 4, kPrepTokens = 4;
 
 __device__ __forceinline__ f32x4 mfma16(const u32x4 &a, const u32x4 &b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
@@ -46,56 +46,92 @@ __device__ __forceinline__ u32x4 ranks8(const uint16_t *row, int j, int r) {
   return v;
 }
 
-// Workgroups below `utiles`: 16 rows of A_set by 16 tokens of u, the waves every 16th step of 32 each.  The others: x
-// [T][K] into xp, 8 values a thread, zero past n_in.
+__device__ __forceinline__ float dot8(const u32x4 &a, const u32x4 &b, float c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = a[i], y = b[i];
+    c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), __builtin_bit_cast(bf16x2, y), c, false);
+  }
+  return c;
+}
+
+// Workgroups below `utiles`: kPrepRows rows of A_set by kPrepTokens tokens of u, the lanes along n_in (a matrix
+// instruction's operand would take rows from neighbouring lanes: 64 accesses a load).  The others: x [T][K] into xp, 8
+// values a thread, zero past n_in.
 __global__ __launch_bounds__(64 * kPrepWaves) void gated_few_prep(const uint16_t *__restrict__ x,
                                                                   const uint16_t *__restrict__ A, int T, int K,
                                                                   int rows, int utiles, uint16_t *__restrict__ u,
                                                                   uint16_t *__restrict__ xp) {
-  __shared__ float red[kPrepWaves][16][17];
+  __shared__ float red[kPrepWaves][kPrepRows * kPrepTokens];
   if ((int)blockIdx.x >= utiles) {
-    const int64_t i = (int64_t)((int)blockIdx.x - utiles) * (64 * kPrepWaves) + threadIdx.x;
-    const int64_t runs = (int64_t)((K + kChunk - 1) / kChunk) * (kChunk / 8) * T;
+    const uint32_t i = ((uint32_t)blockIdx.x - utiles) * (64 * kPrepWaves) + threadIdx.x;
+    const uint32_t runs = (uint32_t)((K + kChunk - 1) / kChunk) * (kChunk / 8) * T;
     if (i >= runs) return;
-    const int64_t rest = i / T, t = i - rest * T, sj = rest >> 2;
-    const int g = (int)(rest & 3);
-    const int k = 64 * (kChunkBlocks * (int)(sj >> 3) + g) + 8 * (int)(sj & 7);
+    const uint32_t rest = i / T, t = i - rest * T, sj = rest >> 2, g = rest & 3;
+    const int k = 64 * (kChunkBlocks * (int)(sj >> 3) + (int)g) + 8 * (int)(sj & 7);
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (k < K) v = *(const u32x4 *)(x + t * K + k);
+    if (k < K) v = *(const u32x4 *)(x + (int64_t)t * K + k);
     // 0 2 | 4 6 | 1 3 | 5 7
-    *(u32x4 *)(xp + 8 * i) =
+    *(u32x4 *)(xp + 8 * (int64_t)i) =
         u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
               __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
     return;
   }
-  const int row_tiles = (rows + 15) / 16;
-  const int r0 = 16 * ((int)blockIdx.x % row_tiles), t0 = 16 * ((int)blockIdx.x / row_tiles);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const uint16_t *xr = x + (int64_t)min(t0 + n, T - 1) * K + 8 * g, *ar = A + (int64_t)min(r0 + n, rows - 1) * K + 8 * g;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int k = 32 * wave; k < K; k += 32 * kPrepWaves)
-    acc = mfma16(*(const u32x4 *)(xr + k), *(const u32x4 *)(ar + k), acc);
+  const int row_tiles = (rows + kPrepRows - 1) / kPrepRows;
+  const int r0 = kPrepRows * ((int)blockIdx.x % row_tiles), t0 = kPrepTokens * ((int)blockIdx.x / row_tiles);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint16_t *xr[kPrepTokens], *ar[kPrepRows];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[wave][4 * g + i][n] = acc[i];
+  for (int i = 0; i < kPrepTokens; ++i) xr[i] = x + (int64_t)min(t0 + i, T - 1) * K;
+#pragma unroll
+  for (int i = 0; i < kPrepRows; ++i) ar[i] = A + (int64_t)min(r0 + i, rows - 1) * K;
+  float acc[kPrepRows][kPrepTokens] = {};
+  for (int k0 = 512 * wave; k0 < K; k0 += 512 * kPrepWaves) {
+    const int k = k0 + 8 * lane;
+    const bool in = k < K;
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    u32x4 av[kPrepRows], xv[kPrepTokens];
+#pragma unroll
+    for (int i = 0; i < kPrepRows; ++i) av[i] = in ? *(const u32x4 *)(ar[i] + k) : none;
+#pragma unroll
+    for (int i = 0; i < kPrepTokens; ++i) xv[i] = in ? *(const u32x4 *)(xr[i] + k) : none;
+#pragma unroll
+    for (int i = 0; i < kPrepRows; ++i)
+#pragma unroll
+      for (int h = 0; h < kPrepTokens; ++h) acc[i][h] = dot8(av[i], xv[h], acc[i][h]);
+  }
+#pragma unroll
+  for (int i = 0; i < kPrepRows; ++i)
+#pragma unroll
+    for (int h = 0; h < kPrepTokens; ++h) {
+      float v = acc[i][h];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+      if (lane == 0) red[wave][i * kPrepTokens + h] = v;
+    }
   __syncthreads();
-  const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
-  if (threadIdx.x >= 256 || t0 + t >= T || r0 + c >= rows) return;
+  const int i = threadIdx.x / kPrepTokens, h = threadIdx.x % kPrepTokens;
+  if (i >= kPrepRows || t0 + h >= T || r0 + i >= rows) return;
   float s = 0.f;
 #pragma unroll
-  for (int w = 0; w < kPrepWaves; ++w) s += red[w][t][c];
-  u[(int64_t)(t0 + t) * rows + r0 + c] = __builtin_bit_cast(uint16_t, (__bf16)s);
+  for (int w = 0; w < kPrepWaves; ++w) s += red[w][threadIdx.x];
+  u[(int64_t)(t0 + h) * rows + r0 + i] = __builtin_bit_cast(uint16_t, (__bf16)s);
 }
 
-// Eight codes (low nibble first) -> four bf16 pairs, (0, 2), (4, 6), (1, 3), (5, 7): decode_word without its last
-// step.
+// Four of the bytes that a table of 16 holds, for four codes given by their low 3 bits (sel) and by the place of each
+// in the lookups of the two halves, byte i of the lower or (bit 3) of the upper one (pick).
+__device__ __forceinline__ uint32_t four_bytes(const uint32_t (&tb)[4], uint32_t sel, uint32_t pick) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(tb[3], tb[2], sel), __builtin_amdgcn_perm(tb[1], tb[0], sel), pick);
+}
+
+// Eight codes (low nibble first) -> four bf16 pairs, (0, 2), (4, 6), (1, 3), (5, 7).
 __device__ __forceinline__ u32x4 decode_split(uint32_t c, const DecodeTable &t) {
-  const uint32_t c4 = c >> 4;
-  const uint32_t se = c & 0x07070707u, so = c4 & 0x07070707u;
-  const uint32_t me = __builtin_amdgcn_perm(c << 4, c << 12, 0x0B090A08u);
-  const uint32_t mo = __builtin_amdgcn_perm(c, c << 8, 0x0B090A08u);
-  const uint32_t le = table_bytes(t.lo, se, me), he = table_bytes(t.hi, se, me);
-  const uint32_t lq = table_bytes(t.lo, so, mo), hq = table_bytes(t.hi, so, mo);
+  uint32_t own = 0x03020100u, upper = 0x04040404u;
+  asm("" : "+v"(own), "+s"(upper));  // in registers: as literals they would keep the and and the or apart
+  const uint32_t se = c & 0x07070707u, so = (c >> 4) & 0x07070707u;
+  const uint32_t pe = ((c >> 1) & upper) | own, po = ((c >> 5) & upper) | own;
+  const uint32_t le = four_bytes(t.lo, se, pe), he = four_bytes(t.hi, se, pe);
+  const uint32_t lq = four_bytes(t.lo, so, po), hq = four_bytes(t.hi, so, po);
   return u32x4{__builtin_amdgcn_perm(he, le, 0x05010400u), __builtin_amdgcn_perm(he, le, 0x07030602u),
                __builtin_amdgcn_perm(hq, lq, 0x05010400u), __builtin_amdgcn_perm(hq, lq, 0x07030602u)};
 }
@@ -149,23 +185,21 @@ __global__ __launch_bounds__(64 * kWaves) void gated_few(GatedFewArgs a, Codeboo
   const int n = lane & 15, g = lane >> 4;
   const int64_t row = 16 * (int64_t)blockIdx.x + n;
   const int blocks = a.K / kBlock, chunks = (blocks + kChunkBlocks - 1) / kChunkBlocks;
-  const int pieces = a.K / 32;  // of a row
-  const int64_t row0 = 16 * (int64_t)blockIdx.x;
+  // Uniform bases and 32-bit lane offsets: the tile's rows of each weight (fewer than 2^31 blocks in all).
+  const uint32_t pitch = (uint32_t)a.K / 2, tile0 = blockIdx.x * 16u * (uint32_t)blocks;
+  const uint32_t code_row = (uint32_t)(lane >> 3) * pitch, block_row = (uint32_t)n * (uint32_t)blocks;
   auto load = [&](int s, Pieces (&b)[2]) {  // past the row's end: any of it, x is 0 there
     const int c = min(s, chunks - 1);
-    const int piece = min(2 * kChunkBlocks * c + (lane & 7), pieces - 1);
-    const int64_t block = row * blocks + min(kChunkBlocks * c + g, blocks - 1);
+    const uint32_t code = code_row + min(128u * (uint32_t)c + 16u * (lane & 7), pitch - 16u);
+    const uint32_t block = block_row + min((uint32_t)(kChunkBlocks * c + g), (uint32_t)blocks - 1u);
+    const uint32_t constant = kDQ ? (tile0 + block) >> 8 : tile0 + block;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        b[m].codes[i] = *(const u32x4 *)(a.w[m].codes + ((row0 + 8 * i + (lane >> 3)) * pieces + piece) * 16);
-      if (kDQ) {
-        b[m].q = a.w[m].fp8[block];
-        b[m].s2 = a.w[m].s2[block >> 8];
-      } else {
-        b[m].s2 = a.w[m].s2[block];
-      }
+      const uint8_t *codes = a.w[m].codes + (int64_t)blockIdx.x * 16 * pitch;
+      b[m].codes[0] = *(const u32x4 *)(codes + code);
+      b[m].codes[1] = *(const u32x4 *)(codes + (code + 8u * pitch));
+      if (kDQ) b[m].q = *(a.w[m].fp8 + tile0 + block);
+      b[m].s2 = a.w[m].s2[constant];
     }
   };
   Pieces next[2];
@@ -203,7 +237,8 @@ __global__ __launch_bounds__(64 * kWaves) void gated_few(GatedFewArgs a, Codeboo
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int h = 0; h < TT; ++h) xf[j][h] = xp[((8 * s + j) * 4 + g) * a.T + token[h]];
+      for (int h = 0; h < TT; ++h) xf[j][h] = (xp + (int64_t)(8 * s + j) * 4 * a.T)[(uint32_t)(g * a.T + token[h])];
+    if (TT == 1) __builtin_amdgcn_sched_barrier(0);  // (more tiles' loads together would take too many registers)
     DecodeTable t[2];
     u32x4 codes[2][2];
 #pragma unroll
@@ -218,6 +253,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_few(GatedFewArgs a, Codeboo
 #pragma unroll
       for (int i = 0; i < 2; ++i) codes[m][i] = *(const u32x4 *)(mine + 2048 * m + piece_at(n, 2 * g + i));
     load(s + kWaves, next);
+    if (TT == 1) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const u32x4 wg = decode_split(codes[0][j >> 2][j & 3], t[0]), wu = decode_split(codes[1][j >> 2][j & 3], t[1]);
@@ -271,7 +307,7 @@ hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, cons
                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
                             const Codebook &cb, hipStream_t st) {
   const int64_t N = w[0].n_out, K = w[0].n_in;
-  const int utiles = (int)((2 * r + 15) / 16 * ((T + 15) / 16));
+  const int utiles = (int)((2 * r + kPrepRows - 1) / kPrepRows * ((T + kPrepTokens - 1) / kPrepTokens));
   const int64_t runs = (int64_t)gated_few_xp_values(T, K) / 8;
   gated_few_prep<<<(unsigned)(utiles + (runs + 64 * kPrepWaves - 1) / (64 * kPrepWaves)), 64 * kPrepWaves, 0, st>>>(
       x, A_set, (int)T, (int)K, 2 * r, utiles, u, xp);
@@ -288,12 +324,8 @@ hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, cons
     run(std::integral_constant<int, 2>());
   else if (T <= 48)
     run(std::integral_constant<int, 3>());
-  else if (T <= 64)
-    run(std::integral_constant<int, 4>());
-  else if (T <= 96)
-    run(std::integral_constant<int, 6>());
   else
-    run(std::integral_constant<int, 8>());
+    run(std::integral_constant<int, 4>());
   return hipGetLastError();
 }
 

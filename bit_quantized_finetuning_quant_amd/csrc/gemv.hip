@@ -33,7 +33,6 @@
 #include <algorithm>
 
 #include "common.hpp"
-#include "gated.hpp"
 #include "launch.hpp"
 
 namespace qlora {
@@ -320,28 +319,22 @@ __device__ __forceinline__ float strided_sum(const float *p, int64_t stride, int
 // s u B^T; the four quarters are added in order.  Every load that does not
 // need u is issued before u is reduced, so that one memory round trip covers
 // them.  Tokens of the last group past T read token T - 1 and are never stored.
-// With a GatedOut the members are gate and up and a workgroup has 256 threads for each: they finish the same 64
-// rows of both, whose sums then meet in LDS.
-template <int TG, typename... Gated>
-__global__ __launch_bounds__(sizeof...(Gated) ? 512 : 256) void gemv_fwd_finish(const float *__restrict__ y_part,
+template <int TG>
+__global__ __launch_bounds__(256) void gemv_fwd_finish(const float *__restrict__ y_part,
                                                        const float *__restrict__ u_part, int64_t spans,
                                                        GemvFwdSet set, int r, int ld_u, float scale,
                                                        float u_scale, int64_t Ntot, int T,
-                                                       uint16_t *__restrict__ u_out, Gated... gated_out) {
-  constexpr bool kGated = sizeof...(Gated) > 0;
-  __shared__ float us_[kGated ? 2 : 1][TG * 256];
-  __shared__ float tmp_[kGated ? 2 : 1][1024];  // E S <= max(E, 256) entries, E = TG r <= 1024
-  __shared__ float red_[kGated ? 2 : 1][4][TG][64];
-  const int half = kGated ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
-  float *us = us_[half], *tmp = tmp_[half];
-  float (*red)[TG][64] = red_[half];
-  const int tid = kGated ? threadIdx.x & 255 : threadIdx.x;
+                                                       uint16_t *__restrict__ u_out) {
+  __shared__ float us[TG * 256];
+  __shared__ float tmp[1024];  // E S <= max(E, 256) entries, E = TG r <= 1024
+  __shared__ float red[4][TG][64];
+  const int tid = threadIdx.x;
   const int q = __builtin_amdgcn_readfirstlane(tid >> 6), c = tid & 63;
   const int t0 = TG * (int)blockIdx.y;
   auto tok = [&](int t) { return min(t0 + t, T - 1); };  // token of group position t (clamped)
   // this workgroup's member (Ntot = 0: u only, member 0) and its 64 rows
-  const int m = kGated ? half : Ntot > 0 ? fwd_member(set, blockIdx.x) : 0;
-  const int64_t pl = kGated ? (int64_t)blockIdx.x : (int64_t)blockIdx.x - set.block0[m];
+  const int m = Ntot > 0 ? fwd_member(set, blockIdx.x) : 0;
+  const int64_t pl = (int64_t)blockIdx.x - set.block0[m];
   const int64_t N = Ntot > 0 ? set.w[m].n_out : 0;
   const uint16_t *__restrict__ B = set.B[m];
   uint16_t *__restrict__ y = set.y[m];
@@ -435,25 +428,6 @@ __global__ __launch_bounds__(sizeof...(Gated) ? 512 : 256) void gemv_fwd_finish(
 #pragma unroll
   for (int t = 0; t < TG; ++t) red[q][t][c] = ys[t] + scale * lora[t];
   __syncthreads();
-  if constexpr (kGated) {
-    // wave t forms token t's 64 values, then 8 lanes of a token 8 values each (TG <= 4)
-    const GatedOut out = [](const GatedOut &o) { return o; }(gated_out...);
-    __shared__ __attribute__((aligned(16))) uint16_t row[3][TG][64];
-    const int t = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (t < TG) {
-      const float g = red_[0][0][t][c] + red_[0][1][t][c] + red_[0][2][t][c] + red_[0][3][t][c];
-      const float up = red_[1][0][t][c] + red_[1][1][t][c] + red_[1][2][t][c] + red_[1][3][t][c];
-      with_activation(out.act, [&](auto a) { row[0][t][c] = to_bf16(gate_act<a()>(g) * up); });
-      row[1][t][c] = to_bf16(g);
-      row[2][t][c] = to_bf16(up);
-    }
-    __syncthreads();
-    const int mine = threadIdx.x >> 3, ch = threadIdx.x & 7;
-    if (mine < TG && t0 + mine < T)
-      store_gated(out, (int64_t)(t0 + mine) * N + pl * 64 + 8 * ch, *(const u32x4 *)&row[0][mine][8 * ch],
-                  *(const u32x4 *)&row[1][mine][8 * ch], *(const u32x4 *)&row[2][mine][8 * ch]);
-    return;
-  }
   if (q == 0 && n < N) {
 #pragma unroll
     for (int t = 0; t < TG; ++t)
@@ -1096,67 +1070,6 @@ size_t gemv_set_part_floats(int64_t T, const int64_t *N, int count, int64_t K, i
   const BwdSplit b = bwd_split(T, set, K, r);
   const size_t bwd = (size_t)(b.chunks * T * K + b.parts * T * r);
   return std::max(gemv_set_fwd_part_floats(T, N, count, K, r), bwd);
-}
-
-// The products of the gated forward: one pass over both weights' rows.
-template <int kUnits>
-static hipError_t gemv_gated_main(int64_t T, const uint16_t *x, const GemvFwdSet &set, int64_t Ntot,
-                                  const uint16_t *A_set, int r_total, float *y_part, float *u_part,
-                                  const GemvGeometry &g, size_t lds, const Codebook &cb, hipStream_t st) {
-  const unsigned grid = (unsigned)(g.fblocks + g.ablocks);
-  const int t = (int)T;
-  auto run = [&](auto tiles) {
-    gemv_fwd_main<kUnits, tiles()><<<grid, 256, lds, st>>>(x, x, t, set, Ntot, A_set, r_total, y_part, u_part, g.fspans,
-                                                          g.ablocks, cb);
-  };
-  if (T <= 16)
-    run(std::integral_constant<int, 1>());
-  else if (T <= 32)
-    run(std::integral_constant<int, 2>());
-  else if (kUnits == kFwdUnitsLarge)
-    return hipErrorInvalidValue;  // long spans hold at most 19 tokens in 40 KB
-  else if (T <= 48)
-    run(std::integral_constant<int, kUnits == kFwdUnitsLarge ? 2 : 3>());
-  else
-    run(std::integral_constant<int, kUnits == kFwdUnitsLarge ? 2 : 4>());
-  return hipGetLastError();
-}
-
-hipError_t launch_gemv_gated(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
-                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u_set,
-                             float *part, const Codebook &cb, hipStream_t st) {
-  const int64_t N = w[0].n_out, Ntot = 2 * N;
-  GemvFwdSet set{};
-  set.count = 2;
-  for (int i = 0; i < kMaxSetMembers; ++i) {
-    set.w[i] = w[i & 1];
-    set.B[i] = B[i & 1];
-    set.block0[i] = i == 0 ? 0 : i == 1 ? N / kFwdRows : kNoBlock;
-  }
-  set.block0[kMaxSetMembers] = kNoBlock;
-  const GemvGeometry g = geometry(T, Ntot, w[0].n_in, 2 * r);
-  float *y_part = part, *u_part = part + g.fspans * T * Ntot;
-  const size_t lds = (size_t)T * (g.funits * 32 + 8) * 2;
-  if (lds > kFwdMultiTileMaxLds && T > 16) return hipErrorInvalidValue;  // see gemv_fwd_applies
-  const hipError_t e =
-      g.funits == kFwdUnitsSmall
-          ? gemv_gated_main<kFwdUnitsSmall>(T, x, set, Ntot, A_set, 2 * r, y_part, u_part, g, lds, cb, st)
-          : gemv_gated_main<kFwdUnitsLarge>(T, x, set, Ntot, A_set, 2 * r, y_part, u_part, g, lds, cb, st);
-  if (e != hipSuccess) return e;
-  auto finish = [&](auto tokens) {
-    constexpr int TG = tokens();
-    gemv_fwd_finish<TG><<<dim3((unsigned)(N / 64), (unsigned)((T + TG - 1) / TG)), 512, 0, st>>>(
-        y_part, u_part, g.fspans, set, r, 2 * r, scale, 1.0f, Ntot, (int)T, u_set, out);
-  };
-  if (T == 1)
-    finish(std::integral_constant<int, 1>());
-  else if (T == 2)
-    finish(std::integral_constant<int, 2>());
-  else if (T == 3)
-    finish(std::integral_constant<int, 3>());
-  else
-    finish(std::integral_constant<int, 4>());
-  return hipGetLastError();
 }
 
 size_t gemv_set_fwd_part_floats(int64_t T, const int64_t *N, int count, int64_t K, int r) {

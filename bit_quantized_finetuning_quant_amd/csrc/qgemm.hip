@@ -695,15 +695,19 @@ __device__ __forceinline__ void consumer_slices_gated(const uint16_t *A, const u
 // member and writes its fp32 tile to part[z][M][set.part_cols] (forward: a
 // member's column c at column 128 tile0 + c); split 0 also carries the adapter
 // term; qgemm_split_reduce adds the splits in order.
-// gated_out (a GatedOut; forward, kFull): the two members are gate and up, the tiles as above (grid: n_out / 64
-// columns of tiles); the epilogue forms h = act(gate) up from the fp32 accumulators and writes what it names.
-// Splits go to part[z][M][2 n_out], gate before up.
+// gated_args (a GatedArgs; forward, kFull): the two members are gate and up, the tiles as above, a workgroup each
+// in one dimension; the epilogue forms h = act(gate) up from the fp32 accumulators and writes what it names, or
+// for a range of a tail tile part[range][tail tile][256][128], gate's 64 columns before up's.
+struct GatedArgs {
+  GatedOut out;
+  int full, tail;
+};
 template <bool kTransW, bool kDQ, bool kDrop, bool kClamp, bool kFull, typename... Gated>
 __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const uint16_t *__restrict__ x,
                                                 const uint16_t *__restrict__ la, const uint16_t *__restrict__ lb,
                                                 int r, float scale, uint16_t *__restrict__ gx, Codebook cb,
                                                 const uint32_t *__restrict__ keep, float *__restrict__ part,
-                                                int64_t split_steps, Gated... gated_out) {
+                                                int64_t split_steps, Gated... gated_args) {
   constexpr bool kGated = sizeof...(Gated) > 0;
   static_assert(kFull || !kClamp, "clamped rows only on grids of full tiles");
   static_assert(!kGated || (kFull && !kTransW && !kDrop), "gated tiles are full tiles of a forward");
@@ -727,6 +731,25 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
       by = (xcd % 2) * (C / 2) + slot / rb;
     }
   }
+  int range = 0, tail_tile = 0;  // kGated: of the contraction, and of the tail
+  bool split = false;
+  if constexpr (kGated) {
+    // Tokens fastest, and each XCD a run of neighbouring tiles: a weight tile is then read by one XCD.
+    const GatedArgs g = [](const GatedArgs &v) { return v; }(gated_args...);
+    const int id = blockIdx.x, R = (int)((M + QBM - 1) / QBM);
+    int tile;
+    split = id >= g.full;
+    if (!split) {
+      const int per = g.full >> 3, rest = g.full & 7, xcd = id & 7;
+      tile = xcd * per + min(xcd, rest) + (id >> 3);
+    } else {
+      tail_tile = (id - g.full) % g.tail;
+      range = (id - g.full) / g.tail;
+      tile = g.full + tail_tile;
+    }
+    by = tile / R;
+    bx = tile - by * R;
+  }
   const int64_t m0 = bx * QBM;
   int mf = 0;  // forward: the member of this column tile
   if (!kTransW && !kGated)
@@ -744,10 +767,11 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
   const bool rows_ok = kFull || m0 + QBM <= M;
   // this workgroup's contraction steps (a split, or all of them) and its rank
   // of the adapter term (only split 0 adds it)
-  const int64_t kstep0 = part ? (int64_t)blockIdx.z * split_steps : 0;
-  const int r_eff = blockIdx.z == 0 ? r : 0;
+  const int64_t kstep0 = kGated ? range * split_steps : part ? (int64_t)blockIdx.z * split_steps : 0;
+  const int r_eff = kGated ? (range == 0 ? r : 0) : blockIdx.z == 0 ? r : 0;
   auto member_steps = [&](int64_t Kc) {
     const int64_t nk = (Kc + QBK - 1) / QBK;
+    if constexpr (kGated) return split ? min(split_steps, nk - kstep0) : nk;
     return part ? min(split_steps, nk - kstep0) : nk;
   };
 
@@ -993,7 +1017,21 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
   dma.wait_all();
   }  // members
 
-  if (part) {
+  if constexpr (kGated) {
+    if (split) {
+      const GatedArgs args = [](const GatedArgs &v) { return v; }(gated_args...);
+      float *dst = part + ((int64_t)range * args.tail + tail_tile) * (QBM * QBN);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            dst[(wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3)) * QBN + 64 * j + 32 * wn + l32] = acc[i][j][q];
+      return;
+    }
+  }
+  if (!kGated && part) {
     // a split: the fp32 tile goes straight from the accumulators to part[z]
     // (each store instruction covers 32 consecutive columns of two rows)
     const int64_t pcols = set.part_cols;
@@ -1002,11 +1040,11 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int64_t col = kGated ? j * Ncols + c0 + wn * 32 + l32 : c0 + wn * 64 + j * 32 + l32;
+        const int64_t col = c0 + wn * 64 + j * 32 + l32;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const int64_t row = m0 + wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3);
-          if (row < M && (kGated || col < Ncols)) pz[row * pcols + col] = acc[i][j][q];
+          if (row < M && col < Ncols) pz[row * pcols + col] = acc[i][j][q];
         }
       }
     return;
@@ -1015,7 +1053,7 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
   if constexpr (kGated) {
     // The product in fp32, then up to three tiles of [256][64] bf16 through LDS ([256][72]: h and gate in the
     // activation ring, up in the weight ring), written as 16-byte row chunks; 8 lanes hold a block of the codes.
-    const GatedOut gated = [](const GatedOut &out) { return out; }(gated_out...);
+    const GatedOut gated = [](const GatedArgs &v) { return v.out; }(gated_args...);
     __syncthreads();
     constexpr int GLD = QBN / 2 + 8;
     static_assert(2 * QBM * GLD <= kActStages * QBM * 64 && QBM * GLD <= kWStages * QBN * QLD, "the tiles fit");
@@ -1689,22 +1727,14 @@ hipError_t launch_qgemm_set(bool trans_w, const QgemmSet &set, int64_t M, const 
   return hipGetLastError();
 }
 
-// A gated launch: few tokens on the few-token tiles, always through fp32 partial tiles; else 256-row tiles, split
-// where that fills the CUs better.
-static QgemmSplit gated_split(int64_t M, int64_t N, int64_t K) {
-  return M <= kSmMaxRows ? qgemm_sm_split(M, 2 * N, K) : qgemm_split(M, 2 * N, K);
-}
-
-int qgemm_gated_parts(int64_t M, int64_t N, int64_t K) {
-  const int splits = gated_split(M, N, K).splits;
-  return M <= kSmMaxRows || splits > 1 ? splits : 0;
-}
+static_assert(kGatedSmTokens == kSmMaxRows, "gated launches of as many tokens run on the few-token tiles");
+int qgemm_gated_parts(int64_t M, int64_t N, int64_t K) { return qgemm_sm_split(M, 2 * N, K).splits; }
 
 template <bool kDQ, bool kClamp>
 static void launch_gated_ws(dim3 g, hipStream_t st, const QgemmSet &s, int64_t M, const uint16_t *x, const uint16_t *la,
-                            int r, float scale, const Codebook &cb, float *part, int64_t steps, const GatedOut &out) {
+                            int r, float scale, const Codebook &cb, float *part, int64_t steps, const GatedArgs &args) {
   qgemm_ws<false, kDQ, false, kClamp, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr, part,
-                                                               steps, out);
+                                                               steps, args);
 }
 
 template <bool kDQ, int kRows>
@@ -1714,17 +1744,17 @@ static void launch_gated_sm(dim3 g, hipStream_t st, const QgemmSet &s, int64_t M
 }
 
 hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
-                              const GatedOut &out, float *part, const Codebook &cb, hipStream_t st) {
+                              const GatedRounds &rounds, const GatedOut &out, float *part, const Codebook &cb,
+                              hipStream_t st) {
   QgemmSet s = set;
   s.count = 2;
   s.ld_la = 2 * r;
   s.m[2] = s.m[3] = s.m[0];
   const int64_t N = s.m[0].w.n_out, K = s.m[0].w.n_in;
-  s.part_cols = 2 * N;
   const bool dq = s.m[0].w.dq;
-  const QgemmSplit sp = gated_split(M, N, K);
-  const int64_t steps = sp.splits > 1 ? sp.steps : K / QBK;
   if (M <= kSmMaxRows) {
+    const QgemmSplit sp = qgemm_sm_split(M, 2 * N, K);
+    const int64_t steps = sp.splits > 1 ? sp.steps : K / QBK;
     const dim3 g(1, (unsigned)(N / (QBN / 2)), (unsigned)sp.splits);
     if (sm_rows(M) == 64)
       dq ? launch_gated_sm<true, 64>(g, st, s, M, x, la, r, scale, cb, part, steps)
@@ -1734,14 +1764,14 @@ hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x,
          : launch_gated_sm<false, 128>(g, st, s, M, x, la, r, scale, cb, part, steps);
     return hipGetLastError();
   }
-  float *pz = sp.splits > 1 ? part : nullptr;
-  const dim3 g((unsigned)((M + QBM - 1) / QBM), (unsigned)(N / (QBN / 2)), (unsigned)sp.splits);
+  const GatedArgs args{out, rounds.full, rounds.tail};
+  const dim3 g((unsigned)(rounds.full + rounds.tail * rounds.splits));
   if (M % QBM != 0)
-    dq ? launch_gated_ws<true, true>(g, st, s, M, x, la, r, scale, cb, pz, steps, out)
-       : launch_gated_ws<false, true>(g, st, s, M, x, la, r, scale, cb, pz, steps, out);
+    dq ? launch_gated_ws<true, true>(g, st, s, M, x, la, r, scale, cb, part, rounds.steps, args)
+       : launch_gated_ws<false, true>(g, st, s, M, x, la, r, scale, cb, part, rounds.steps, args);
   else
-    dq ? launch_gated_ws<true, false>(g, st, s, M, x, la, r, scale, cb, pz, steps, out)
-       : launch_gated_ws<false, false>(g, st, s, M, x, la, r, scale, cb, pz, steps, out);
+    dq ? launch_gated_ws<true, false>(g, st, s, M, x, la, r, scale, cb, part, rounds.steps, args)
+       : launch_gated_ws<false, false>(g, st, s, M, x, la, r, scale, cb, part, rounds.steps, args);
   return hipGetLastError();
 }
 
