@@ -35,7 +35,7 @@ __device__ __forceinline__ u32x4 product8(const u32x4 &g, const u32x4 &u) {
 }
 
 // 8 consecutive lanes share a block of the codes (N is a multiple of 64, so no block crosses a row).
-template <Activation kAct>
+template <Activation kAct, bool kStream>
 __global__ __launch_bounds__(kWide) void gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_t runs,
                                                          uint16_t *h, int8_t *codes, float *scale) {
   const int64_t step = (int64_t)gridDim.x * (kWide * kRuns);
@@ -44,8 +44,8 @@ __global__ __launch_bounds__(kWide) void gated_act_fwd(const uint16_t *gate, con
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
       const int64_t i = first + j * kWide;
-      g[j] = i < runs ? *(const u32x4 *)(gate + 8 * i) : u32x4{0u, 0u, 0u, 0u};
-      u[j] = i < runs ? *(const u32x4 *)(up + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      g[j] = i < runs ? load_run<kStream>(gate + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      u[j] = i < runs ? load_run<kStream>(up + 8 * i) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(kWide) void gated_act_fwd(const uint16_t *gate, con
   }
 }
 
-template <Activation kAct>
+template <Activation kAct, bool kStream>
 __global__ __launch_bounds__(kWide) void gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const uint16_t *up,
                                                          int64_t runs, uint16_t *dgate, uint16_t *dup) {
   const int64_t step = (int64_t)gridDim.x * (kWide * kRuns);
@@ -72,9 +72,9 @@ __global__ __launch_bounds__(kWide) void gated_act_bwd(const uint16_t *dh, const
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
       const int64_t i = first + j * kWide;
-      d[j] = i < runs ? *(const u32x4 *)(dh + 8 * i) : u32x4{0u, 0u, 0u, 0u};
-      g[j] = i < runs ? *(const u32x4 *)(gate + 8 * i) : u32x4{0u, 0u, 0u, 0u};
-      u[j] = i < runs ? *(const u32x4 *)(up + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      d[j] = i < runs ? load_run<kStream>(dh + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      g[j] = i < runs ? load_run<kStream>(gate + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      u[j] = i < runs ? load_run<kStream>(up + 8 * i) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
@@ -350,7 +350,10 @@ hipError_t launch_gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_
                                 uint16_t *h, int8_t *codes, float *scale, hipStream_t st) {
   const int64_t runs = T * N / 8;
   with_activation(act, [&](auto a) {
-    gated_act_fwd<a()><<<grid(runs), kWide, 0, st>>>(gate, up, runs, h, codes, scale);
+    if (T * N * 4 >= kStreamBytes)
+      gated_act_fwd<a(), true><<<grid(runs), kWide, 0, st>>>(gate, up, runs, h, codes, scale);
+    else
+      gated_act_fwd<a(), false><<<grid(runs), kWide, 0, st>>>(gate, up, runs, h, codes, scale);
   });
   return hipGetLastError();
 }
@@ -359,7 +362,10 @@ hipError_t launch_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const 
                                 Activation act, uint16_t *dgate, uint16_t *dup, hipStream_t st) {
   const int64_t runs = T * N / 8;
   with_activation(act, [&](auto a) {
-    gated_act_bwd<a()><<<grid(runs), kWide, 0, st>>>(dh, gate, up, runs, dgate, dup);
+    if (T * N * 6 >= kStreamBytes)
+      gated_act_bwd<a(), true><<<grid(runs), kWide, 0, st>>>(dh, gate, up, runs, dgate, dup);
+    else
+      gated_act_bwd<a(), false><<<grid(runs), kWide, 0, st>>>(dh, gate, up, runs, dgate, dup);
   });
   return hipGetLastError();
 }

@@ -99,7 +99,7 @@ struct NormFwd {
 };
 
 // kRow threads a row, V runs of 8 values a thread, a row's threads apart.
-template <int kRow, int V>
+template <int kRow, int V, bool kStream>
 __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_fwd(NormFwd p) {
   constexpr int kRows = block_threads<kRow>() / kRow;
   __shared__ float red[block_threads<kRow>() / 64][1];
@@ -110,14 +110,14 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_fwd(NormFwd p)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = lane + v * kRow;
-      s[v] = i < runs ? *(const u32x4 *)(p.x + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      s[v] = i < runs ? load_run<kStream>(p.x + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
     }
     if (p.residual) {
       u32x4 r[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int i = lane + v * kRow;
-        r[v] = i < runs ? *(const u32x4 *)(p.residual + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+        r[v] = i < runs ? load_run<kStream>(p.residual + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -178,90 +178,135 @@ struct NormBwd {
   bool wide;
   float eps;
   uint16_t *grad;
-  float *part;  // with the weight's gradient: [row groups of the grid][D]
+  float *part;  // with the weight's gradient: [workgroup][D]
 };
 
-template <int kRow, int V, bool kWeight>
+// One row: rstd (of s lifted) and c from the sums of s^2 and w dy s.  false: the squares pass fp32.
+template <int kRow, int V, bool kLifted, typename W>
+__device__ __forceinline__ bool norm_sums(const NormBwd &p, const u32x4 (&s)[V], const u32x4 (&g)[V], const W &weight,
+                                          float (*red)[2], float &rstd, float &c) {
+  const float lift = kLifted ? kLift : 1.0f;
+  float sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float a[8], b[8], w[8];
+    unpack8(s[v], a);
+    unpack8(g[v], b);
+    weight(v, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float l = kLifted ? a[j] * lift : a[j];
+      sum[0] = __builtin_fmaf(l, l, sum[0]);
+      sum[1] = __builtin_fmaf(w[j] * b[j], l, sum[1]);
+    }
+  }
+  row_sum<kRow>(sum, red);
+  rstd = 1.0f / sqrtf(sum[0] / (float)p.D + p.eps * lift * lift);
+  c = sum[1] * rstd / (float)p.D;
+  return sum[0] < __builtin_inff();
+}
+
+// The weight stays in registers over a workgroup's rows where it has room there.
+template <int kRow, int V, bool kWeight, bool kStream>
 __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_bwd(NormBwd p) {
   constexpr int kRows = block_threads<kRow>() / kRow;
+  constexpr bool kHeld = V <= 2;
   __shared__ float red[block_threads<kRow>() / 64][2];
   const int lane = threadIdx.x % kRow, runs = p.D / 8;
-  const int64_t group = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow;
+  float held[kHeld ? V : 1][8];
+  if constexpr (kHeld)
+#pragma unroll
+    for (int v = 0; v < V; ++v) weight8(p.weight, p.wide, min(lane + v * kRow, runs - 1), held[v]);
+  auto weight = [&](int v, float (&w)[8]) {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = held[v][j];
+    } else {
+      weight8(p.weight, p.wide, min(lane + v * kRow, runs - 1), w);
+    }
+  };
   float gw[kWeight ? V : 1][8];
 #pragma unroll
   for (int v = 0; v < (kWeight ? V : 1); ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) gw[v][j] = 0.f;
-  for (int64_t t = group; t < p.T; t += (int64_t)gridDim.x * kRows) {
-    u32x4 s[V], g[V];
+  const int64_t first = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow, step = (int64_t)gridDim.x * kRows;
+  auto load = [&](int64_t t, u32x4 (&s)[V], u32x4 (&g)[V], u32x4 (&d)[V]) {
     const int64_t row = t * p.D;
+    const u32x4 none = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = lane + v * kRow;
-      s[v] = i < runs ? *(const u32x4 *)(p.s + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
-      g[v] = i < runs ? *(const u32x4 *)(p.dy + row + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+      s[v] = i < runs ? load_run<kStream>(p.s + row + 8 * i) : none;
+      g[v] = i < runs ? load_run<kStream>(p.dy + row + 8 * i) : none;
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = lane + v * kRow;
+      d[v] = p.dres && i < runs ? load_run<kStream>(p.dres + row + 8 * i) : none;
+    }
+  };
+  for (int64_t t = first; t < p.T; t += step) {
+    const int64_t row = t * p.D;
+    u32x4 s[V], g[V], d[V];
+    load(t, s, g, d);
     float lift = 1.0f, rstd, c;
-    for (;;) {
-      float sum[2] = {0.f, 0.f};  // of s^2 and of w dy s
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int i = lane + v * kRow;
-        float a[8], b[8], w[8];
-        unpack8(s[v], a);
-        unpack8(g[v], b);
-        if (i < runs) weight8(p.weight, p.wide, i, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float l = a[j] * lift;
-          sum[0] = __builtin_fmaf(l, l, sum[0]);
-          if (i < runs) sum[1] = __builtin_fmaf(w[j] * b[j], l, sum[1]);
-        }
-      }
-      row_sum<kRow>(sum, red);
-      rstd = 1.0f / sqrtf(sum[0] / (float)p.D + p.eps * lift * lift);
-      c = sum[1] * rstd / (float)p.D;
-      if (lift != 1.0f || sum[0] < __builtin_inff()) break;
+    if (!norm_sums<kRow, V, false>(p, s, g, weight, red, rstd, c)) {  // (a NaN's row too, to the same end)
       lift = kLift;
+      norm_sums<kRow, V, true>(p, s, g, weight, red, rstd, c);
     }
     const float outer = rstd * lift;  // 1 / the root of the mean square
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = lane + v * kRow;
-      if (i >= runs) continue;
-      float a[8], b[8], w[8], o[8];
+      float a[8], b[8], w[8], o[8], past[8];
       unpack8(s[v], a);
       unpack8(g[v], b);
-      weight8(p.weight, p.wide, i, w);
+      unpack8(d[v], past);
+      weight(v, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float xhat = a[j] * lift * rstd;
         o[j] = outer * (w[j] * b[j] - xhat * c);
+        if (p.dres) o[j] += past[j];
         if constexpr (kWeight) gw[v][j] = __builtin_fmaf(b[j], xhat, gw[v][j]);
       }
-      if (p.dres) {
-        float d[8];
-        unpack8(*(const u32x4 *)(p.dres + row + 8 * i), d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += d[j];
-      }
-      *(u32x4 *)(p.grad + row + 8 * i) = u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                              pack_bf16x2(o[6], o[7])};
+      if (i < runs)
+        *(u32x4 *)(p.grad + row + 8 * i) = u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                                pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
     }
   }
   if constexpr (kWeight) {
+    // the workgroup's rows side by side are added first
+    __shared__ __attribute__((aligned(16))) float sums[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? V * kRow * 8 : 1];
+    if constexpr (kRows > 1) {
+      const int mine = threadIdx.x / kRow;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (mine > 0) sums[mine - 1][j * V * kRow + lane + v * kRow] = gw[v][j];
+      __syncthreads();
+      if (mine > 0) return;
+#pragma unroll
+      for (int k = 0; k < kRows - 1; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gw[v][j] += sums[k][j * V * kRow + lane + v * kRow];
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = lane + v * kRow;
       if (i >= runs) continue;
-      float *dst = p.part + group * p.D + 8 * i;
+      float *dst = p.part + (int64_t)blockIdx.x * p.D + 8 * i;
       *(f32x4 *)dst = f32x4{gw[v][0], gw[v][1], gw[v][2], gw[v][3]};
       *(f32x4 *)(dst + 4) = f32x4{gw[v][4], gw[v][5], gw[v][6], gw[v][7]};
     }
   }
 }
 
-// grad_w from the row groups' sums: 64 columns a workgroup, its 16 waves every 16th group each, in a fixed order.
+// grad_w from the workgroups' sums: 64 columns a workgroup, its 16 waves every 16th of them each, in a fixed order.
 __global__ __launch_bounds__(1024) void rms_norm_weight(const float *__restrict__ part, int groups, int D,
                                                        float *__restrict__ grad) {
   __shared__ float sums[16][64];
@@ -277,30 +322,34 @@ __global__ __launch_bounds__(1024) void rms_norm_weight(const float *__restrict_
   grad[col] = s;
 }
 
-// Row groups of the launch with the weight's gradient: each holds partial sums of a row's length, written and read
-// again, so they are few; two workgroups a CU.
+// Workgroups of the launch with the weight's gradient: each holds partial sums of a row's length, written and read
+// again, so they are few; two a CU.
 constexpr int kWeightBlocks = 512;
 
-// A row's threads and runs: every run in registers.
-template <typename F>
+// A row's threads and runs, every run in registers.  The backward pass holds three rows' worth and takes at most two
+// runs a thread up to 16384 columns (4096 x 8192: four runs 73.6 us, two 64.7, one 72.7).
+template <bool kBackward, typename F>
 void with_shape(int64_t D, const F &f) {
   const int64_t runs = D / 8;
+  auto shape = [&](auto row, auto per) { f(row, per); };
+#define NORM_SHAPE(ROW, RUNS) shape(std::integral_constant<int, ROW>(), std::integral_constant<int, RUNS>())
   if (runs <= 64)
-    f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+    NORM_SHAPE(64, 1);
   else if (runs <= 128)
-    f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+    NORM_SHAPE(64, 2);
   else if (runs <= 256)
-    f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
+    NORM_SHAPE(256, 1);
   else if (runs <= 512)
-    f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+    NORM_SHAPE(256, 2);
   else if (runs <= 1024)
-    f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
+    kBackward ? NORM_SHAPE(512, 2) : NORM_SHAPE(256, 4);
   else if (runs <= 2048)
-    f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
+    kBackward ? NORM_SHAPE(1024, 2) : NORM_SHAPE(512, 4);
   else if (runs <= 4096)
-    f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
+    NORM_SHAPE(1024, 4);
   else
-    f(std::integral_constant<int, 1024>(), std::integral_constant<int, 8>());
+    NORM_SHAPE(1024, 8);
+#undef NORM_SHAPE
 }
 
 int rows_of_block(int64_t D) { return D <= 1024 ? 4 : 1; }
@@ -322,28 +371,37 @@ hipError_t launch_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int6
                                bool w_fp32, float eps, uint16_t *sum, uint16_t *y, int8_t *codes, float *scale,
                                hipStream_t st) {
   const NormFwd p{x, residual, T, (int)D, weight, w_fp32, eps, sum, y, codes, scale};
-  with_shape(D, [&](auto row, auto runs) {
-    rms_norm_fwd<row(), runs()><<<(unsigned)row_blocks(T, D), block_threads<row()>(), 0, st>>>(p);
+  with_shape<false>(D, [&](auto row, auto runs) {
+    constexpr int kThreads = block_threads<row()>();
+    if (T * D * (residual ? 4 : 2) >= kStreamBytes)
+      rms_norm_fwd<row(), runs(), true><<<(unsigned)row_blocks(T, D), kThreads, 0, st>>>(p);
+    else
+      rms_norm_fwd<row(), runs(), false><<<(unsigned)row_blocks(T, D), kThreads, 0, st>>>(p);
   });
   return hipGetLastError();
 }
 
-size_t rms_norm_part_floats(int64_t T, int64_t D) { return (size_t)(weight_blocks(T, D) * rows_of_block(D) * D); }
+size_t rms_norm_part_floats(int64_t T, int64_t D) { return (size_t)(weight_blocks(T, D) * D); }
 
 hipError_t launch_rms_norm_bwd(const uint16_t *dy, const uint16_t *s, const uint16_t *dres, int64_t T, int64_t D,
                                const void *weight, bool w_fp32, float eps, uint16_t *grad_s, float *grad_weight,
                                float *part, hipStream_t st) {
   const NormBwd p{dy, s, dres, T, (int)D, weight, w_fp32, eps, grad_s, part};
-  with_shape(D, [&](auto row, auto runs) {
+  with_shape<true>(D, [&](auto row, auto runs) {
     constexpr int kThreads = block_threads<row()>();
-    if (grad_weight)
-      rms_norm_bwd<row(), runs(), true><<<(unsigned)weight_blocks(T, D), kThreads, 0, st>>>(p);
+    const bool stream = T * D * (dres ? 6 : 4) >= kStreamBytes;
+    const unsigned blocks = (unsigned)(grad_weight ? weight_blocks(T, D) : row_blocks(T, D));
+    if (grad_weight && stream)
+      rms_norm_bwd<row(), runs(), true, true><<<blocks, kThreads, 0, st>>>(p);
+    else if (grad_weight)
+      rms_norm_bwd<row(), runs(), true, false><<<blocks, kThreads, 0, st>>>(p);
+    else if (stream)
+      rms_norm_bwd<row(), runs(), false, true><<<blocks, kThreads, 0, st>>>(p);
     else
-      rms_norm_bwd<row(), runs(), false><<<(unsigned)row_blocks(T, D), kThreads, 0, st>>>(p);
+      rms_norm_bwd<row(), runs(), false, false><<<blocks, kThreads, 0, st>>>(p);
   });
   if (grad_weight)
-    rms_norm_weight<<<(unsigned)(D / 64), 1024, 0, st>>>(part, (int)(weight_blocks(T, D) * rows_of_block(D)), (int)D,
-                                                        grad_weight);
+    rms_norm_weight<<<(unsigned)(D / 64), 1024, 0, st>>>(part, (int)weight_blocks(T, D), (int)D, grad_weight);
   return hipGetLastError();
 }
 
