@@ -137,28 +137,76 @@ __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ 
 // The fused GEMM decodes a weight tile once for every 256 tokens; from some thousand tokens on, decoding each
 // weight once (2.5 bytes a weight at HBM speed) and multiplying on plain 256 x 256 tiles is faster.
 
-// The adapter's operands with their contraction, the ranks of both members in turn, padded with zeros to `pad`
-// columns: bp [2 N][pad] (gate's rows hold B_0 at columns 0 .., up's B_1 at r ..), and up [T][pad] from u [T][2 r].
-__global__ __launch_bounds__(kWide) void gated_pack(const uint16_t *__restrict__ b0, const uint16_t *__restrict__ b1,
-                                                   const uint16_t *__restrict__ u, int64_t N, int64_t T, int r, int pad,
-                                                   uint16_t *__restrict__ bp, uint16_t *__restrict__ up) {
-  const int chunks = pad / 8;
-  const int64_t brows = 2 * N * chunks, all = brows + (up ? T * chunks : 0);
-  for (int64_t i = (int64_t)blockIdx.x * kWide + threadIdx.x; i < all; i += (int64_t)gridDim.x * kWide) {
-    const bool token = i >= brows;
-    const int64_t k = token ? i - brows : i, row = k / chunks;
-    const int c = (int)(k - row * chunks) * 8;
-    const int member = !token && row >= N ? 1 : 0, width = token ? 2 * r : r, first = c - member * r;
-    const uint16_t *src = token ? u + row * 2 * r : (member ? b1 + (row - N) * r : b0 + row * r);
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (first >= 0 && first + 8 <= width) {
-      v = load8(src + first);
-    } else {
+// What the tiles need beside x, in one launch, whose workgroups take one of two parts:
+//   the adapter's operands, whose contraction is the ranks of both members in turn, padded with zeros to `pad`:
+//     bp [2 N][pad] (gate's rows hold B_0 at columns 0 .., up's B_1 at r ..), and where 2 r is not whole 64s
+//     up [T][pad] from u [T][2 r];
+//   the weights, 8 values a thread and pass.
+// (u = x A_set^T beside the decode gains nothing: its loads then wait for the decode's stores, 43 + 21 us apart
+// and 68 together at 2048 tokens of 2 x 11008 x 4096.)
+struct GatedPrep {
+  const uint16_t *u, *B[2];
+  QWeight w[2];
+  int64_t T, N, chunks;  // chunks: of 8 values of a weight
+  int r, pad, packs;     // packs: workgroups of the first part
+  uint16_t *up, *bp, *wd;
+};
+
+__device__ __forceinline__ void prep_pack(const GatedPrep &a) {
+  const int per = a.pad / 8;
+  const int64_t i = (int64_t)blockIdx.x * kWide + threadIdx.x, row = i / per;
+  if (row >= 2 * a.N + (a.up ? a.T : 0)) return;
+  const bool token = row >= 2 * a.N;
+  const int member = !token && row >= a.N ? 1 : 0;
+  const int c = (int)(i - row * per) * 8, width = token ? 2 * a.r : a.r, first = c - member * a.r;
+  const uint16_t *src = token ? a.u + (row - 2 * a.N) * width : a.B[member] + (row - member * a.N) * a.r;
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (first >= 0 && first + 8 <= width) {
+    v = load8(src + first);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (first + j >= 0 && first + j < width) v[j >> 1] |= (uint32_t)src[first + j] << (16 * (j & 1));
+    for (int j = 0; j < 8; ++j)
+      if (first + j >= 0 && first + j < width) v[j >> 1] |= (uint32_t)src[first + j] << (16 * (j & 1));
+  }
+  *(u32x4 *)((token ? a.up + (row - 2 * a.N) * a.pad : a.bp + row * a.pad) + c) = v;
+}
+
+template <bool kDQ>
+__global__ __launch_bounds__(kWide) void gated_prep(GatedPrep a, Codebook cb) {
+  __shared__ float lut[16];
+  if ((int)blockIdx.x < a.packs) {
+    prep_pack(a);
+    return;
+  }
+  if (threadIdx.x < 16) lut[threadIdx.x] = cb.v[threadIdx.x];
+  __syncthreads();
+  const int64_t id = (int64_t)blockIdx.x - a.packs, groups = (int64_t)gridDim.x - a.packs;
+  constexpr int kDeep = 4;
+  const int64_t passes = (a.chunks + kDeep * kWide - 1) / (kDeep * kWide);  // of one weight
+  const float mu0 = kDQ ? *a.w[0].mu : 0.f, mu1 = kDQ ? *a.w[1].mu : 0.f;
+  for (int64_t pass = id; pass < 2 * passes; pass += groups) {
+    const int m = pass >= passes ? 1 : 0;
+    const QWeight &w = a.w[m];
+    const float mu = m ? mu1 : mu0;
+    const int64_t first = (pass - m * passes) * (kDeep * kWide) + threadIdx.x;
+    uint32_t code[kDeep];
+    float c1[kDeep];
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) {
+      const int64_t c = min(first + j * kWide, a.chunks - 1);
+      code[j] = ((const uint32_t *)w.codes)[c];
+      c1[j] = kDQ ? decode_constant(w.fp8[c >> 3], w.s2[c >> 11], mu) : w.s2[c >> 3];
     }
-    *(u32x4 *)((token ? up : bp) + row * pad + c) = v;
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) {
+      const int64_t c = first + j * kWide;
+      u32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = pack_bf16x2(decode_product(lut[(code[j] >> (8 * i)) & 15u], c1[j]),
+                           decode_product(lut[(code[j] >> (8 * i + 4)) & 15u], c1[j]));
+      if (c < a.chunks) *(u32x4 *)(a.wd + ((int64_t)m * a.chunks + c) * 8) = v;
+    }
   }
 }
 
@@ -440,25 +488,32 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
   if (e != hipSuccess) return e;
   if (p.decode) {
     const int pad = (2 * p.r + 63) / 64 * 64;
-    uint16_t *wd = (uint16_t *)(ws + p.off_w), *bp = (uint16_t *)(ws + p.off_b);
-    uint16_t *up = pad != 2 * p.r ? (uint16_t *)(ws + p.off_up) : nullptr;
-    DequantSet set{};
-    set.count = 2;
+    GatedPrep g{};
+    g.u = u;
     for (int i = 0; i < 2; ++i) {
-      set.w[i] = w[i];
-      set.out[i] = wd + i * p.N * p.K;
+      g.B[i] = B[i];
+      g.w[i] = w[i];
     }
-    e = launch_dequantize_set(set, cb, st);
-    if (e != hipSuccess) return e;
-    const int64_t chunks = (2 * p.N + (up ? p.T : 0)) * (pad / 8);
-    gated_pack<<<(unsigned)std::min<int64_t>(cdiv(chunks, kWide), 2048), kWide, 0, st>>>(B[0], B[1], u, p.N, p.T, p.r, pad,
-                                                                                     bp, up);
+    g.T = p.T;
+    g.N = p.N;
+    g.chunks = p.N * p.K / 8;
+    g.r = p.r;
+    g.pad = pad;
+    g.up = pad != 2 * p.r ? (uint16_t *)(ws + p.off_up) : nullptr;
+    g.bp = (uint16_t *)(ws + p.off_b);
+    g.wd = (uint16_t *)(ws + p.off_w);
+    g.packs = (int)cdiv((2 * p.N + (g.up ? p.T : 0)) * (pad / 8), kWide);
+    const unsigned blocks = (unsigned)(g.packs + std::min<int64_t>(cdiv(2 * g.chunks, 4 * kWide), 4096));
+    if (w[0].dq)
+      gated_prep<true><<<blocks, kWide, 0, st>>>(g, cb);
+    else
+      gated_prep<false><<<blocks, kWide, 0, st>>>(g, cb);
     const int nleft = (int)cdiv(p.N, kTileV / 2), ntoken = (int)cdiv(p.T, kTileT);
-    const GatedRounds &g = p.rounds;
-    const GatedTilesArgs a{x,  up ? up : u, wd,     bp,     p.T,          p.N,   p.K,  pad,
-                           nleft, ntoken,      g.full, g.tail, (int)g.steps, scale, qpart};
-    gated_tiles<<<(unsigned)(g.full + g.tail * g.splits), kThreads, 0, st>>>(a, out);
-    if (g.tail) launch_tail<true>(qpart, g, nleft, ntoken, p.T, p.N, out, st);
+    const GatedRounds &n = p.rounds;
+    const GatedTilesArgs a{x,     g.up ? g.up : u, g.wd,   g.bp,   p.T,          p.N,   p.K,  pad,
+                           nleft, ntoken,          n.full, n.tail, (int)n.steps, scale, qpart};
+    gated_tiles<<<(unsigned)(n.full + n.tail * n.splits), kThreads, 0, st>>>(a, out);
+    if (n.tail) launch_tail<true>(qpart, n, nleft, ntoken, p.T, p.N, out, st);
     return hipGetLastError();
   }
   QgemmSet s{};
