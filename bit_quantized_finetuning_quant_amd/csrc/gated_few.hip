@@ -28,6 +28,7 @@ constexpr int kChunkBlocks = 4;            // NF4 blocks of a row in a chunk
 constexpr int kChunk = 64 * kChunkBlocks;  // n_in of a chunk
 constexpr int kWaves = 4;                  // waves of a workgroup
 constexpr int kPrepWaves = 8, kPrepRows = 4, kPrepTokens = 4;
+static_assert(kPrepRows * kPrepTokens == 16, "the lanes' exchange holds 16 sums");
 
 __device__ __forceinline__ f32x4 mfma16(const u32x4 &a, const u32x4 &b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
@@ -100,15 +101,23 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gated_few_prep(const uint16_t
 #pragma unroll
       for (int h = 0; h < kPrepTokens; ++h) acc[i][h] = dot8(av[i], xv[h], acc[i][h]);
   }
+  // The 16 sums over the lanes: four exchanges that halve the values a lane holds leave one in each of 16 lanes.
+  float v[16];
 #pragma unroll
-  for (int i = 0; i < kPrepRows; ++i)
+  for (int i = 0; i < 16; ++i) v[i] = acc[i / kPrepTokens][i % kPrepTokens];
 #pragma unroll
-    for (int h = 0; h < kPrepTokens; ++h) {
-      float v = acc[i][h];
+  for (int e = 0; e < 4; ++e) {
+    const bool upper = (lane >> e) & 1;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-      if (lane == 0) red[wave][i * kPrepTokens + h] = v;
+    for (int i = 0; i < (8 >> e); ++i) {
+      const float keep = upper ? v[i + (8 >> e)] : v[i], give = upper ? v[i] : v[i + (8 >> e)];
+      v[i] = keep + __shfl_xor(give, 1 << e);
     }
+  }
+  v[0] += __shfl_xor(v[0], 16);
+  v[0] += __shfl_xor(v[0], 32);
+  // lane l < 16 holds value 8 l0 + 4 l1 + 2 l2 + l3 of its bits
+  if (lane < 16) red[wave][((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | (lane >> 3)] = v[0];
   __syncthreads();
   const int i = threadIdx.x / kPrepTokens, h = threadIdx.x % kPrepTokens;
   if (i >= kPrepRows || t0 + h >= T || r0 + i >= rows) return;
