@@ -185,9 +185,11 @@ struct GatedFewArgs {
   float scale;
 };
 
-// TT tiles of 16 tokens.
+// TT tiles of 16 tokens.  Four of them fit three waves a SIMD, so that the 2.7 that 11008 x 4096 has run at once (64
+// tokens: 38.6 -> 32.1 us); with fewer tiles the compiler's own choice is faster (33 tokens of 22016 x 8192: 102
+// against 129 us).
 template <int TT, bool kDQ>
-__global__ __launch_bounds__(64 * kWaves) void gated_few(GatedFewArgs a, Codebook cb, GatedOut out) {
+__global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedFewArgs a, Codebook cb, GatedOut out) {
   __shared__ float red[kWaves][16 * TT][17];
   __shared__ __attribute__((aligned(16))) char turn[kWaves][2][2048];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
