@@ -29,24 +29,20 @@ qlora_status check_out8(const qlora_act8 *a, int64_t T, int64_t K) {
   return aligned16(a->codes) && aligned16(a->scale) ? QLORA_OK : QLORA_ERR_ALIGN;
 }
 
-qlora_status check_norm(int64_t T, int64_t D, qlora_dtype w_dtype, float eps) {
+qlora_status check_norm(int64_t T, int64_t D, int dtype, float eps) {
   if (!norm_shape_ok(T, D)) return QLORA_ERR_SHAPE;
-  const int dtype = code_of(w_dtype);
   if (dtype != QLORA_F32 && dtype != QLORA_BF16) return QLORA_ERR_DTYPE;
   return std::isfinite(eps) && eps > 0.f ? QLORA_OK : QLORA_ERR_VALUE;
 }
 
-bool activation_ok(qlora_activation act) {
-  const int a = code_of(act);
-  return a == QLORA_SILU || a == QLORA_GELU_TANH;
-}
+bool activation_ok(int act) { return act == QLORA_SILU || act == QLORA_GELU_TANH; }
 
-// n_in: byte offsets within a row tile of x stay below 2^32; n_ff: its tiles are the grid's second dimension.
-constexpr int64_t kGatedMaxDim = (int64_t)1 << 22;
+// n_in: byte offsets within a row tile of x stay below 2^32; n_ff, and its tiles with the tokens': a launch's grid.
+constexpr int64_t kGatedMaxDim = (int64_t)1 << 22, kGatedMaxTiles = (int64_t)1 << 22;
 
 bool gated_shape_ok(int64_t T, int64_t N, int64_t K, int r) {
-  return linear_shape_ok(T, N, K, r) && N % kBlock == 0 && N < kGatedMaxDim && K < kGatedMaxDim && product_ok(T, 2 * (int64_t)r) &&
-         (T + 255) / 256 <= INT32_MAX / 512;
+  return linear_shape_ok(T, N, K, r) && N % kBlock == 0 && N < kGatedMaxDim && K < kGatedMaxDim &&
+         product_ok(T, 2 * (int64_t)r) && (T / 256 + 1) * (N / 64) <= kGatedMaxTiles;
 }
 
 }  // namespace
@@ -56,7 +52,7 @@ extern "C" {
 qlora_status qlora_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int64_t T, int64_t D, const void *weight,
                                 qlora_dtype w_dtype, float eps, uint16_t *sum, uint16_t *y, const qlora_act8 *y8,
                                 void *stream) {
-  qlora_status s = check_norm(T, D, w_dtype, eps);
+  qlora_status s = check_norm(T, D, code_of(w_dtype), eps);
   if (s != QLORA_OK) return s;
   if (!x || !weight || (!y && !y8) || (residual == nullptr) != (sum == nullptr)) return QLORA_ERR_NULL;
   s = check_out8(y8, T, D);
@@ -75,7 +71,7 @@ size_t qlora_rms_norm_bwd_workspace_bytes(int64_t T, int64_t D) {
 qlora_status qlora_rms_norm_bwd(const uint16_t *dy, const uint16_t *s, const uint16_t *dres, int64_t T, int64_t D,
                                 const void *weight, qlora_dtype w_dtype, float eps, uint16_t *grad_s,
                                 float *grad_weight, void *ws, size_t ws_bytes, void *stream) {
-  const qlora_status st = check_norm(T, D, w_dtype, eps);
+  const qlora_status st = check_norm(T, D, code_of(w_dtype), eps);
   if (st != QLORA_OK) return st;
   if (!dy || !s || !weight || !grad_s || (grad_weight && !ws)) return QLORA_ERR_NULL;
   if (!aligned16(dy) || !aligned16(s) || !aligned16(dres) || !aligned16(weight) || !aligned16(grad_s) ||
@@ -90,7 +86,7 @@ qlora_status qlora_rms_norm_bwd(const uint16_t *dy, const uint16_t *s, const uin
 qlora_status qlora_gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64_t T, int64_t N, qlora_activation act,
                                  uint16_t *h, const qlora_act8 *h8, void *stream) {
   if (!act_shape_ok(T, N)) return QLORA_ERR_SHAPE;
-  if (!activation_ok(act)) return QLORA_ERR_VALUE;
+  if (!activation_ok(code_of(act))) return QLORA_ERR_VALUE;
   if (!gate || !up || (!h && !h8)) return QLORA_ERR_NULL;
   const qlora_status s = check_out8(h8, T, N);
   if (s != QLORA_OK) return s;
@@ -103,7 +99,7 @@ qlora_status qlora_gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64
 qlora_status qlora_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const uint16_t *up, int64_t T, int64_t N,
                                  qlora_activation act, uint16_t *dgate, uint16_t *dup, void *stream) {
   if (!act_shape_ok(T, N)) return QLORA_ERR_SHAPE;
-  if (!activation_ok(act)) return QLORA_ERR_VALUE;
+  if (!activation_ok(code_of(act))) return QLORA_ERR_VALUE;
   if (!dh || !gate || !up || !dgate || !dup) return QLORA_ERR_NULL;
   if (!aligned16(dh) || !aligned16(gate) || !aligned16(up) || !aligned16(dgate) || !aligned16(dup))
     return QLORA_ERR_ALIGN;
@@ -124,7 +120,7 @@ qlora_status qlora_linear_gated_fwd(const uint16_t *x, int64_t T, const qlora_nf
   qlora_status s = check_set(T, 2, q, r, scale, N);
   if (s != QLORA_OK) return s;
   if (N[0] != N[1] || !gated_shape_ok(T, N[0], q[0].n_in, r)) return QLORA_ERR_SHAPE;
-  if (!activation_ok(act)) return QLORA_ERR_VALUE;
+  if (!activation_ok(code_of(act))) return QLORA_ERR_VALUE;
   if (!x || !A_set || !B || !B[0] || !B[1] || !ws || (!h && !h8) || (gate == nullptr) != (up == nullptr))
     return QLORA_ERR_NULL;
   s = check_out8(h8, T, N[0]);

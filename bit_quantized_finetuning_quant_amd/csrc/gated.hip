@@ -381,8 +381,9 @@ double plain_us(int64_t T, int64_t N, int64_t K, GatedRounds *rounds) {
 
 // Whether the decoded form is taken.
 bool decode_pays(int64_t T, int64_t N, int64_t K) {
-  // offsets within a tile, from its first row of gate to its last of up, stay below 2^32; a launch's threads too
-  if (N * K > (int64_t)1 << 29 || K > 65536 || cdiv(N, kTileV / 2) * cdiv(T, kTileT) > (int64_t)1 << 22) return false;
+  // offsets within a tile, from its first row of gate to its last of up, stay below 2^32, and the threads of the
+  // launches; the decoded weights below 2 GB
+  if (N * K > (int64_t)1 << 29 || K > 65536 || T > (int64_t)1 << 22) return false;
   GatedRounds r;
   return 1.03 * plain_us(T, N, K, &r) < fused_us(T, N, K, &r);
 }

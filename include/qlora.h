@@ -487,9 +487,11 @@ qlora_status qlora_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const
  * or neither): the backward pass, qlora_gated_act_bwd, reads them.  (h is formed
  * before they are rounded, so qlora_gated_act_fwd on them differs from h by
  * their roundings.)  Both weights are [n_ff x n_in] and of one storage form,
- * n_ff % 64 == 0, n_ff and n_in < 2^22; the rest as qlora_linear_set_fwd with two
- * members.  ws: qlora_linear_gated_workspace_bytes, for these sizes (fewer
- * tokens may take another form and need more).                                */
+ * n_ff % 64 == 0, n_ff and n_in < 2^22, (T / 256 + 1) n_ff / 64 <= 2^22; the rest
+ * as qlora_linear_set_fwd with two members.
+ * ws: qlora_linear_gated_workspace_bytes, for these sizes (fewer tokens may take
+ * another form and need more).  From about a thousand tokens on it holds both
+ * decoded weights (4 n_ff n_in bytes, at most 2 GB; longer ones stay packed).  */
 size_t qlora_linear_gated_workspace_bytes(int64_t T, int64_t n_ff, int64_t n_in, int r);
 qlora_status qlora_linear_gated_fwd(const uint16_t *x, int64_t T, const qlora_nf4_weight *q, const uint16_t *A_set,
                                     const uint16_t *const *B, int r, float scale, qlora_activation act, uint16_t *h,
