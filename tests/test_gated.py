@@ -223,33 +223,49 @@ def test_block_of_the_7b_and_65b_mlp(T, K, N, r):
     _check_block(last, qlora.Gated(out.h[-40:], None, out.gate[-40:], out.up[-40:], out.u[-40:]), "silu")
 
 
+# where the weights are decoded first: whole rounds of tiles, and a last one in ranges of K; ranks with and without
+# padding, output tiles that end inside, one step of K
+DECODED = [(4096, 64, 5568, 32), (1500, 256, 8256, 7), (2049, 320, 5568, 100), (5000, 256, 2752, 64),
+           (3000, 1024, 5568, 31), (4096, 1024, 4160, 16), (2049, 2048, 4160, 200)]
+
+
 @gpu
-def test_block_rows_and_members_do_not_mix():
-    """A NaN or Inf in one token stays in its row; a gate far below zero leaves 0, whatever up is."""
+@pytest.mark.parametrize("T,K,N,r", DECODED)
+def test_block_of_decoded_weights(T, K, N, r):
+    announce(f"gated block of decoded weights T={T} K={K} N={N} r={r}")
+    assert qlora.linear_gated_workspace_bytes(T, N, K, r) > 4 * N * K
+    test_block(T, K, N, r)
+
+
+@gpu
+@pytest.mark.parametrize("T,K,N", [(5, 256, 320), (40, 256, 320), (100, 256, 320), (300, 256, 320), (4096, 64, 5568),
+                                   (3000, 1024, 5568)])
+def test_block_rows_and_members_do_not_mix(T, K, N):
+    """A NaN or Inf in one token stays in its row, and a row of zeros is 0."""
     torch = torch_mod()
-    for T in (5, 40, 100, 300):
-        announce(f"gated block special values T={T}")
-        p = _block(T, 256, 320, 8, T)
-        args = (p["qs"], p["A"], p["Bs"], p["scale"])
-        base = qlora.linear_gated_fwd(p["x"], *args)
-        x = p["x"].clone()
-        x[1, 7], x[3] = float("nan"), 0
-        out = qlora.linear_gated_fwd(x, *args, need_act8=True)
-        rest = torch.ones(T, dtype=torch.bool)
-        rest[[1, 3]] = False
-        for k in ("h", "gate", "up", "u"):
-            assert torch.equal(getattr(out, k)[rest], getattr(base, k)[rest])
-            assert bool(getattr(out, k)[1].isnan().all()) and bool((getattr(out, k)[3] == 0).all())
-        assert bool(out.act8.scale[1].isnan().all()) and bool((out.act8.codes[3] == 0).all())
+    announce(f"gated block special values T={T}")
+    p = _block(T, K, N, 8, T)
+    args = (p["qs"], p["A"], p["Bs"], p["scale"])
+    base = qlora.linear_gated_fwd(p["x"], *args)
+    x = p["x"].clone()
+    x[1, 7], x[3] = float("nan"), 0
+    out = qlora.linear_gated_fwd(x, *args, need_act8=True)
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[[1, 3]] = False
+    for k in ("h", "gate", "up", "u"):
+        assert torch.equal(getattr(out, k)[rest], getattr(base, k)[rest])
+        assert bool(getattr(out, k)[1].isnan().all()) and bool((getattr(out, k)[3] == 0).all())
+    assert bool(out.act8.scale[1].isnan().all()) and bool((out.act8.codes[3] == 0).all())
 
 
 @gpu
-@pytest.mark.parametrize("T", [1, 20, 100, 300, 700])
-def test_block_outputs_workspace_stream_and_graph(T):
+@pytest.mark.parametrize("T,K,N", [(1, 512, 704), (20, 512, 704), (64, 512, 704), (100, 512, 704), (300, 512, 704),
+                                   (700, 512, 704), (4096, 64, 5568), (3000, 1024, 5568)])
+def test_block_outputs_workspace_stream_and_graph(T, K, N):
     """Given outputs and workspace, rows behind the last one, a stream of its own, and a captured graph."""
     torch = torch_mod()
     announce(f"gated block graph T={T}")
-    K, N, r = 512, 704, 16
+    r = 16
     p = _block(T, K, N, r, T)
     args = (p["x"], p["qs"], p["A"], p["Bs"], p["scale"])
     want = qlora.linear_gated_fwd(*args, need_act8=True)
