@@ -112,7 +112,7 @@ __device__ __forceinline__ void finish8(const GatedOut &out, int64_t to, const f
   store_gated(out, to, h, g, u);
 }
 
-// The same from the few-token tiles' fp32 results part[z][T][2 N], added in order; 8 columns a thread.
+// The same from the few-token form's fp32 results part[z][T][2 N], added in order; 8 columns a thread.
 template <Activation kAct>
 __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ part, int parts, int64_t T, int64_t N,
                                                         GatedOut out) {
@@ -443,21 +443,24 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   p.N = N;
   p.K = K;
   p.r = r;
-  p.few = gated_few_applies(T, N, K);
-  p.parts = p.few || T > kGatedSmTokens ? 0 : qgemm_gated_parts(T, N, K);
-  p.decode = !p.few && p.parts == 0 && decode_pays(T, N, K);
+  p.few = T <= kGatedFewTokens;
+  p.parts = p.few ? gated_few_parts(T, N, K) : 0;
+  p.decode = !p.few && decode_pays(T, N, K);
   size_t tail = 0;
-  if (!p.few && p.parts == 0) {
+  if (!p.few) {
     p.decode ? plain_us(T, N, K, &p.rounds) : fused_us(T, N, K, &p.rounds);
     tail = (size_t)p.rounds.tail * p.rounds.splits * (p.decode ? kPlainTile : kFusedTile);
   }
   size_t off = 256;
   p.off_u = off;
   off += align256((size_t)T * 2 * r * 2);
+  p.own_u = p.few && gated_few_own_u(T, r);
   p.off_part = off;
-  off += align256(p.few ? gated_few_xp_values(T, K) * 2 : lora_part_floats(T, 2 * r, K) * 4);
-  p.off_h = off;  // the few-token form's h where only its codes are wanted
-  off += p.few ? align256((size_t)T * N * 2) : 0;
+  off += p.own_u ? 0 : align256(lora_part_floats(T, 2 * r, K) * 4);
+  p.off_xp = off;
+  off += p.few ? align256(gated_few_xp_values(T, K) * 2) : 0;
+  p.off_h = off;  // h, where the one pass writes it and only its codes are wanted
+  off += p.few && !p.parts ? align256((size_t)T * N * 2) : 0;
   p.off_qpart = off;
   off += align256(std::max((size_t)p.parts * T * 2 * N * 4, tail));
   // the decoded form: both weights, the adapter's operands (u as it is where its ranks need no padding)
@@ -477,16 +480,28 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
                                    char *ws, const Codebook &cb, hipStream_t st) {
   uint16_t *u = u_out ? u_out : (uint16_t *)(ws + p.off_u);
   float *part = (float *)(ws + p.off_part), *qpart = (float *)(ws + p.off_qpart);
-  if (p.few) {
-    GatedOut plain = out;
-    plain.codes = nullptr;
-    if (!out.h) plain.h = (uint16_t *)(ws + p.off_h);
-    const hipError_t e = launch_gated_few(p.T, x, w, A_set, B, p.r, scale, plain, u, (uint16_t *)part, cb, st);
-    if (e != hipSuccess || !out.codes) return e;
-    return launch_act8_encode(plain.h, p.T, p.N, out.codes, out.scale, st);
+  hipError_t e;
+  if (!p.own_u) {
+    e = launch_lora(LoraKind::kU, x, p.K, A_set, p.K, p.T, 2 * p.r, p.K, 1.0f, u, part, st);
+    if (e != hipSuccess) return e;
   }
-  hipError_t e = launch_lora(LoraKind::kU, x, p.K, A_set, p.K, p.T, 2 * p.r, p.K, 1.0f, u, part, st);
-  if (e != hipSuccess) return e;
+  if (p.few) {
+    GatedOut first = out;
+    if (!p.parts) {
+      first.codes = nullptr;
+      if (!out.h) first.h = (uint16_t *)(ws + p.off_h);
+    }
+    e = launch_gated_few(p.T, x, w, A_set, B, p.r, scale, first, u, (uint16_t *)(ws + p.off_xp), qpart, cb, st);
+    if (e != hipSuccess) return e;
+    if (p.parts) {
+      const int64_t blocks = cdiv(p.T * p.N / 8, kWide);
+      with_activation(out.act, [&](auto a) {
+        gated_reduce<a()><<<(unsigned)std::min<int64_t>(blocks, 2048), kWide, 0, st>>>(qpart, p.parts, p.T, p.N, out);
+      });
+      return hipGetLastError();
+    }
+    return out.codes ? launch_act8_encode(first.h, p.T, p.N, out.codes, out.scale, st) : hipSuccess;
+  }
   if (p.decode) {
     const int pad = (2 * p.r + 63) / 64 * 64;
     GatedPrep g{};
@@ -525,12 +540,6 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
   e = launch_qgemm_gated(s, p.T, x, u, p.r, scale, p.rounds, out, qpart, cb, st);
   if (e != hipSuccess) return e;
   if (p.rounds.tail) launch_tail<false>(qpart, p.rounds, (int)(p.N / 64), (int)cdiv(p.T, 256), p.T, p.N, out, st);
-  if (p.parts) {
-    const int64_t blocks = cdiv(p.T * p.N / 8, kWide);
-    with_activation(out.act, [&](auto a) {
-      gated_reduce<a()><<<(unsigned)std::min<int64_t>(blocks, 2048), kWide, 0, st>>>(qpart, p.parts, p.T, p.N, out);
-    });
-  }
   return hipGetLastError();
 }
 

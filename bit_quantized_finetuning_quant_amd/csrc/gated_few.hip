@@ -1,11 +1,14 @@
-// The gated product behind its projections for up to 64 tokens (gfx950).
+// The gated product behind its projections for up to 128 tokens (gfx950).
 //
 // Reading and decoding the 4-bit weights is the work here, so every code is read once, decoded once in the
-// registers of the lane that multiplies it, and used for all tokens; nothing of W goes through LDS.
+// registers of the lane that multiplies it, and used for all tokens.
 //
 //   gated_few_prep   u = x A_set^T (bf16), and x laid out as the products take it
-//   gated_few        16 columns of gate and of up a workgroup, its waves every KS-th chunk of 256 of n_in each;
-//                    their sums meet in LDS and the workgroup writes its columns of h (gate, up)
+//   gated_few        16 columns of gate and of up a workgroup, its waves every fourth chunk of 256 of n_in each; their
+//                    sums meet in LDS and the workgroup writes its columns of h (gate, up)
+//   gated_split      more than 64 tokens, or 16 of large weights: 64 columns of each a workgroup, 16 a wave, over a range
+//                    of the chunks; x comes through LDS, once for the four waves, and the ranges' fp32 results are
+//                    added by a launch more
 //
 // v_mfma_f32_16x16x32_bf16: A lane l holds A[l % 16][8 (l / 16) + 0..7], B lane l holds B[8 (l / 16) + 0..7][l % 16],
 // D register i of lane l is D[4 (l / 16) + i][l % 16].  Which 32 values of the contraction a product takes, and in what
@@ -19,6 +22,7 @@
 #include "common.hpp"
 #include "gated.hpp"
 #include "launch.hpp"
+#include "tile.hpp"
 
 namespace qlora {
 
@@ -61,7 +65,7 @@ __device__ __forceinline__ float dot8(const u32x4 &a, const u32x4 &b, float c) {
 // values a thread, zero past n_in.
 __global__ __launch_bounds__(64 * kPrepWaves) void gated_few_prep(const uint16_t *__restrict__ x,
                                                                   const uint16_t *__restrict__ A, int T, int K,
-                                                                  int rows, int utiles, uint16_t *__restrict__ u,
+                                                                  int ld, int rows, int utiles, uint16_t *__restrict__ u,
                                                                   uint16_t *__restrict__ xp) {
   __shared__ float red[kPrepWaves][kPrepRows * kPrepTokens];
   if ((int)blockIdx.x >= utiles) {
@@ -73,7 +77,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gated_few_prep(const uint16_t
     u32x4 v = {0u, 0u, 0u, 0u};
     if (k < K) v = *(const u32x4 *)(x + (int64_t)t * K + k);
     // 0 2 | 4 6 | 1 3 | 5 7
-    *(u32x4 *)(xp + 8 * (int64_t)i) =
+    *(u32x4 *)(xp + 8 * ((int64_t)rest * ld + t)) =
         u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
               __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
     return;
@@ -181,12 +185,12 @@ struct GatedFewArgs {
   const uint16_t *xp, *u;
   QWeight w[2];
   const uint16_t *B[2];
-  int T, N, K, r;
+  int T, ld, N, K, r;  // ld: tokens from one eight of xp to the next
   float scale;
 };
 
 // TT tiles of 16 tokens.  Four of them fit three waves a SIMD, so that the 2.7 that 11008 x 4096 has run at once (64
-// tokens: 38.6 -> 32.1 us); with fewer tiles the compiler's own choice is faster (33 tokens of 22016 x 8192: 102
+// tokens: 38.6 -> 32.1 us); with fewer tiles the compiler's own choice is faster (48 tokens of 22016 x 8192: 102
 // against 129 us).
 template <int TT, bool kDQ>
 __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedFewArgs a, Codebook cb, GatedOut out) {
@@ -248,7 +252,7 @@ __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedF
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int h = 0; h < TT; ++h) xf[j][h] = (xp + (int64_t)(8 * s + j) * 4 * a.T)[(uint32_t)(g * a.T + token[h])];
+      for (int h = 0; h < TT; ++h) xf[j][h] = (xp + (int64_t)(8 * s + j) * 4 * a.ld)[(uint32_t)(g * a.ld + token[h])];
     if (TT == 1) __builtin_amdgcn_sched_barrier(0);  // (more tiles' loads together would take too many registers)
     DecodeTable t[2];
     u32x4 codes[2][2];
@@ -308,35 +312,203 @@ __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedF
   }
 }
 
+// TT tiles of 16 tokens, `range` chunks of n_in, z-th of them: part[z][T][2 N].  With x in registers more than two tiles
+// leave a SIMD two waves, and each operand comes from L2 once for 32 columns; here it comes once for 128, half a chunk
+// (four products) ahead, and the codes a chunk ahead, all by copies into LDS that no register holds.
+//   xs   half chunks [4 j][g][token] of 16 bytes as they lie in xp, two in turn
+//   cs   a wave's codes of a chunk, in the places that piece_at gives: read to registers at the chunk's start, then
+//        refilled
+// A wave's waits: at a chunk's start for all of its copies, in its middle for those of x, all but the four copies of
+// codes issued after them; each before the barrier behind which other waves read what it has copied, and with
+// lgkmcnt(0), so that what it has read is in registers before others overwrite it.
+template <int TT, bool kDQ>
+__global__ __launch_bounds__(64 * kWaves, TT <= 4 ? 3 : 2) void gated_split(GatedFewArgs a, Codebook cb, int range,
+                                                                            float *__restrict__ part) {
+  __shared__ __attribute__((aligned(1024))) char xs[2][TT * 4096];
+  __shared__ __attribute__((aligned(1024))) char cs[kWaves][2][2048];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int tiles = a.N / 64, tile = (int)blockIdx.x % tiles, z = (int)blockIdx.x / tiles;
+  const int blocks = a.K / kBlock, chunks = (blocks + kChunkBlocks - 1) / kChunkBlocks;
+  const int c0 = z * range, c1 = min(c0 + range, chunks);
+  const int64_t row0 = 64 * (int64_t)tile + 16 * wave;
+  const uint32_t pitch = (uint32_t)a.K / 2, block0 = (uint32_t)row0 * (uint32_t)blocks;
+  const uint32_t block_row = (uint32_t)n * (uint32_t)blocks;
+  const char *codes[2] = {uniform(a.w[0].codes + row0 * pitch), uniform(a.w[1].codes + row0 * pitch)};
+  // the lane's pieces of a chunk from the scalar base; in the last chunk none past its row's end (x is 0 there)
+  uint32_t from[2];
+  const uint32_t x_from = 16u * lane;
+  auto place = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * i + (lane >> 3);
+      from[i] = (uint32_t)r * pitch + min(16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7)), pitch - 16u - 128u * (uint32_t)c);
+    }
+  };
+  uint32_t q[2] = {};
+  float s2[2];
+  auto load = [&](int c) {  // `from` may change: nothing that it addresses is in flight
+    const uint32_t block = block_row + min((uint32_t)(kChunkBlocks * c + g), (uint32_t)blocks - 1u);
+    const uint32_t constant = kDQ ? (block0 + block) >> 8 : block0 + block;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (kDQ) q[m] = *(a.w[m].fp8 + block0 + block);
+      s2[m] = a.w[m].s2[constant];
+    }
+    if (c == chunks - 1) place(c);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) dma16(codes[m] + 128 * (int64_t)c, from[i], lds_addr(cs[wave][m] + 1024 * i));
+  };
+  const char *xp = uniform(a.xp);
+  auto load_x = [&](int h, int buf) {  // half chunk h: ld / 4 KB, the waves in turn
+    const char *src = xp + (int64_t)h * 256 * a.ld;
+    for (int p = wave; p < a.ld / 4; p += kWaves) dma16(src + 1024 * p, x_from, lds_addr(xs[buf] + 1024 * p));
+  };
+  place(0);
+  load(c0);
+  load_x(2 * c0, 0);
+  const float mu0 = kDQ ? *a.w[0].mu : 0.f, mu1 = kDQ ? *a.w[1].mu : 0.f;
+  // the adapter term, 32 ranks a product, the ranges in turn; D's rows are the weight's here: a lane holds four
+  // neighbouring columns of one token
+  f32x4 acc[2][TT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int h = 0; h < TT; ++h) acc[m][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 32 * z; j < a.r; j += 32 * (int)(gridDim.x / tiles))
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const u32x4 b = ranks8(a.B[m] + (row0 + n) * a.r, j + 8 * g, a.r);
+#pragma unroll
+      for (int h = 0; h < TT; ++h)
+        acc[m][h] = mfma16(
+            b, ranks8(a.u + (int64_t)min(16 * h + n, a.T - 1) * (2 * a.r) + m * a.r, j + 8 * g, a.r), acc[m][h]);
+    }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int h = 0; h < TT; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][h][i] *= a.scale;
+
+  for (int c = c0; c < c1; ++c) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::"v"(from[0]), "v"(from[1]), "v"(x_from) : "memory");
+    barrier();
+    load_x(2 * c + 1, 1);
+    u32x4 w[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[m][i] = *(const u32x4 *)(cs[wave][m] + piece_at(n, 2 * g + i));
+    DecodeTable t[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) build_table<kDQ>(Pieces{{}, q[m], s2[m]}, m ? mu1 : mu0, cb, t[m]);
+    asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(w[0][0]), "+v"(w[0][1]), "+v"(w[1][0]), "+v"(w[1][1])::"memory");
+    const bool more = c + 1 < c1;
+    if (more) load(c + 1);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half) {
+        if (more)
+          asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)" ::: "memory");
+        else
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        barrier();
+        if (more) load_x(2 * c + 2, 0);
+      }
+      const char *xh = xs[half] + 16 * (g * a.ld + n);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const u32x4 wg = decode_split(w[0][half][j], t[0]), wu = decode_split(w[1][half][j], t[1]);
+#pragma unroll
+        for (int h = 0; h < TT; ++h) {
+          const u32x4 xf = *(const u32x4 *)(xh + 64 * j * a.ld + 256 * h);
+          acc[0][h] = mfma16(wg, xf, acc[0][h]);
+          acc[1][h] = mfma16(wu, xf, acc[1][h]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < TT; ++h) {
+    const int t = 16 * h + n;
+    if (t < a.T)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        *(f32x4 *)(part + ((int64_t)z * a.T + t) * (2 * (int64_t)a.N) + m * a.N + row0 + 4 * g) = acc[m][h];
+  }
+}
+
 }  // namespace
 
-bool gated_few_applies(int64_t T, int64_t N, int64_t K) { return T <= kGatedFewTokens && N <= INT32_MAX && K <= 65536; }
+static int64_t chunk_count(int64_t K) { return (K + kChunk - 1) / kChunk; }
+// About two workgroups a CU, which hold three of them up to 64 tokens and two of more: with one the copies' latency shows
+// (64 tokens of two 22016 x 8192 weights: 131 us, with two 96), with four the results cost more than they gain (103).
+static int64_t range_chunks(int64_t T, int64_t N, int64_t K) {
+  const int64_t tiles = N / 64, want = T <= 64 ? (512 + tiles - 1) / tiles : std::max<int64_t>(512 / tiles, 2);
+  const int64_t splits = std::min(want, chunk_count(K));
+  return (chunk_count(K) + splits - 1) / splits;
+}
 
-size_t gated_few_xp_values(int64_t T, int64_t K) { return (size_t)((K + kChunk - 1) / kChunk * kChunk * T); }
+// In ranges where x in registers costs more than the launch that adds them.  One pass against ranges, us: 17 tokens of
+// two 11008 x 4096 weights 30 and 34, 64 tokens 38 and 40; 33 tokens of 14336 x 4096 42 and 40, 64 tokens 54 and 44; 20 tokens of
+// 22016 x 8192 83 and 77, 33 tokens 102 and 84.
+int gated_few_parts(int64_t T, int64_t N, int64_t K) {
+  if (T <= 16 || (T <= 64 && N * K < (int64_t)48 << 20)) return 0;
+  const int64_t range = range_chunks(T, N, K);
+  return (int)((chunk_count(K) + range - 1) / range);
+}
+
+// Tiles of u.  Each reads its rows and tokens whole, so from some number on the two launches of the adapters' product are
+// faster (two 11008 x 4096 weights: 128 tokens at rank 16, 256 tiles, 58 against 63 us; at rank 64, 1024 tiles, 71
+// against 66; 64 tokens at rank 64, 512 tiles, even).
+static int64_t u_tiles(int64_t T, int r) {
+  return (2 * r + kPrepRows - 1) / kPrepRows * ((T + kPrepTokens - 1) / kPrepTokens);
+}
+bool gated_few_own_u(int64_t T, int r) {
+  return u_tiles(T, r) <= 512;
+}
+
+size_t gated_few_xp_values(int64_t T, int64_t K) { return (size_t)(chunk_count(K) * kChunk * ((T + 3) / 4 * 4)); }
 
 hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
-                            const Codebook &cb, hipStream_t st) {
+                            float *part, const Codebook &cb, hipStream_t st) {
   const int64_t N = w[0].n_out, K = w[0].n_in;
-  const int utiles = (int)((2 * r + kPrepRows - 1) / kPrepRows * ((T + kPrepTokens - 1) / kPrepTokens));
-  const int64_t runs = (int64_t)gated_few_xp_values(T, K) / 8;
+  const int utiles = gated_few_own_u(T, r) ? (int)u_tiles(T, r) : 0;
+  const int ld = (int)(T + 3) / 4 * 4;
+  const int64_t runs = chunk_count(K) * (kChunk / 8) * T;
   gated_few_prep<<<(unsigned)(utiles + (runs + 64 * kPrepWaves - 1) / (64 * kPrepWaves)), 64 * kPrepWaves, 0, st>>>(
-      x, A_set, (int)T, (int)K, 2 * r, utiles, u, xp);
-  const GatedFewArgs a{xp, u, {w[0], w[1]}, {B[0], B[1]}, (int)T, (int)N, (int)K, r, scale};
-  auto run = [&](auto tiles) {
-    if (w[0].dq)
-      gated_few<tiles(), true><<<(unsigned)(N / 16), 64 * kWaves, 0, st>>>(a, cb, out);
-    else
-      gated_few<tiles(), false><<<(unsigned)(N / 16), 64 * kWaves, 0, st>>>(a, cb, out);
+      x, A_set, (int)T, (int)K, ld, 2 * r, utiles, u, xp);
+  const GatedFewArgs a{xp, u, {w[0], w[1]}, {B[0], B[1]}, (int)T, ld, (int)N, (int)K, r, scale};
+  const int parts = gated_few_parts(T, N, K), range = (int)range_chunks(T, N, K);
+  auto run = [&](auto tiles, auto dq) {
+    if (tiles() > 4 || parts) {
+      gated_split<tiles(), dq()><<<(unsigned)(N / 64 * parts), 64 * kWaves, 0, st>>>(a, cb, range, part);
+      return;
+    }
+    if constexpr (tiles() <= 4) gated_few<tiles(), dq()><<<(unsigned)(N / 16), 64 * kWaves, 0, st>>>(a, cb, out);
   };
-  if (T <= 16)
-    run(std::integral_constant<int, 1>());
-  else if (T <= 32)
-    run(std::integral_constant<int, 2>());
-  else if (T <= 48)
-    run(std::integral_constant<int, 3>());
+  auto with_tiles = [&](auto dq) {
+    if (T <= 16)
+      run(std::integral_constant<int, 1>(), dq);
+    else if (T <= 32)
+      run(std::integral_constant<int, 2>(), dq);
+    else if (T <= 48)
+      run(std::integral_constant<int, 3>(), dq);
+    else if (T <= 64)
+      run(std::integral_constant<int, 4>(), dq);
+    else if (T <= 96)
+      run(std::integral_constant<int, 6>(), dq);
+    else
+      run(std::integral_constant<int, 8>(), dq);
+  };
+  if (w[0].dq)
+    with_tiles(std::true_type());
   else
-    run(std::integral_constant<int, 4>());
+    with_tiles(std::false_type());
   return hipGetLastError();
 }
 

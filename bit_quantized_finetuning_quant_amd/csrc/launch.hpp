@@ -326,30 +326,30 @@ struct GatedRounds {
 // round_us + step_us * steps: a workgroup's time; tile_bytes: an fp32 tile's.
 GatedRounds gated_rounds(int64_t tiles, int64_t steps, double round_us, double step_us, int64_t tile_bytes, double *us);
 // Fused GEMM of both projections (qgemm.hip): set holds gate and up, la = u_set [M x 2 r], n_out % 64 == 0.
-// More than kGatedSmTokens tokens: tiles of 256 tokens by 64 columns of each, tokens fastest; whole tiles are written to
-// `out`, the ranges of the others to part[range][tail tile][256][128] (gate's columns, then up's).
-// Up to kGatedSmTokens: part[z][M][2 n_out] (gate before up), qgemm_gated_parts of them.
-constexpr int64_t kGatedSmTokens = 128;
-int qgemm_gated_parts(int64_t M, int64_t N, int64_t K);
+// Tiles of 256 tokens by 64 columns of each, tokens fastest; whole tiles are written to `out`, the ranges of the others
+// to part[range][tail tile][256][128] (gate's columns, then up's).
 hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
                               const GatedRounds &rounds, const GatedOut &out, float *part, const Codebook &cb,
                               hipStream_t st);
-// Up to kGatedFewTokens tokens in one pass (gated_few.hip): u [T x 2 r] is written, xp holds x laid out for the
-// products; out.h is given and out.codes is not.
-constexpr int64_t kGatedFewTokens = 64;
-bool gated_few_applies(int64_t T, int64_t N, int64_t K);
+// Up to kGatedFewTokens tokens (gated_few.hip): u [T x 2 r] is written, xp holds x laid out for the products.
+// gated_few_parts = 0: in one pass, out.h is given and out.codes is not.  Otherwise only the fp32 results of that
+// many ranges of n_in are written, part[range][T][2 n_out] (gate before up).
+constexpr int64_t kGatedFewTokens = 128;
+int gated_few_parts(int64_t T, int64_t N, int64_t K);
+bool gated_few_own_u(int64_t T, int r);  // u is written here; otherwise it is there
 size_t gated_few_xp_values(int64_t T, int64_t K);
 hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
-                            const Codebook &cb, hipStream_t st);
+                            float *part, const Codebook &cb, hipStream_t st);
 struct GatedPlan {
   int64_t T, N, K;
   int r;
   bool few;            // the few-token form
+  int parts;           // its fp32 results of all tokens (0: it writes the product itself)
+  bool own_u;          // it writes u
   bool decode;         // decoded weights on plain tiles
-  int parts;           // fp32 results of all tokens (the fused GEMM's few-token tiles; otherwise 0)
   GatedRounds rounds;  // of the 256-row tiles of either form
-  size_t off_u, off_part, off_qpart, off_w, off_b, off_up, off_h, total;
+  size_t off_u, off_xp, off_part, off_qpart, off_w, off_b, off_up, off_h, total;
 };
 GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r);
 hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const QWeight *w, const uint16_t *A_set,

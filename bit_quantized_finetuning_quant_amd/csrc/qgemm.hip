@@ -1243,17 +1243,11 @@ __device__ __forceinline__ void sm_stage_mfma(const uint16_t *A, const uint16_t 
   }
 }
 
-//
-// GatedTiles (forward): the tiles of a gate and an up weight as in qgemm_ws, 64 columns of each; waves 0 and 2
-// hold gate, 1 and 3 up.  Every workgroup writes its fp32 tile to part[z][M][2 n_out].
-struct GatedTiles {};
-template <bool kTransW, bool kDQ, int kRows, typename... Gated>
+template <bool kTransW, bool kDQ, int kRows>
 __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, const uint16_t *__restrict__ x,
                                                    const uint16_t *__restrict__ la, const uint16_t *__restrict__ lb,
                                                    int r, float scale, uint16_t *__restrict__ gx, Codebook cb,
                                                    float *__restrict__ part, int64_t split_steps) {
-  constexpr bool kGated = sizeof...(Gated) > 0;
-  static_assert(!kGated || !kTransW, "gated tiles are a forward's");
   constexpr int kSt = kRows == 64 ? 3 : 2;  // LDS stages
   constexpr int kTiles = kRows / 32;        // 32-row MFMA tiles; also 16-byte activation chunks per thread
   __shared__ __attribute__((aligned(16))) uint16_t sa[kSt][kRows * 64];
@@ -1262,20 +1256,15 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
   const int l32 = lane & 31, lhi = lane >> 5;
   const QgemmMember mm = set.m[0];
   const int64_t Ncols = kTransW ? mm.w.n_in : mm.w.n_out, Kc = kTransW ? mm.w.n_out : mm.w.n_in;
-  const int64_t m0 = (int64_t)blockIdx.x * kRows, c0 = (int64_t)blockIdx.y * (kGated ? QBN / 2 : QBN);
+  const int64_t m0 = (int64_t)blockIdx.x * kRows, c0 = (int64_t)blockIdx.y * QBN;
   const uint16_t *act = kTransW ? mm.act : x;
   const uint16_t *lb_t = kTransW ? lb : mm.lb;
   uint16_t *out = kTransW ? gx : mm.out;
   const int64_t kstep0 = part ? (int64_t)blockIdx.z * split_steps : 0;
   const int64_t nk = part ? min(split_steps, Kc / QBK - kstep0) : Kc / QBK;
   const int r_eff = blockIdx.z == 0 ? r : 0;
-  const int own = __builtin_amdgcn_readfirstlane(w) & 1;  // kGated: the wave's member
-  const float mu = !kDQ ? 0.f : kGated && own ? *set.m[1].w.mu : *mm.w.mu;
-  Producer<kTransW, kDQ> p;
-  if constexpr (kGated)
-    p = gated_producer<kDQ>(set, c0, tid, mu, kstep0);
-  else
-    p = member_producer<kTransW, kDQ>(mm, x, M, m0, c0, tid, mu, kstep0);
+  const float mu = kDQ ? *mm.w.mu : 0.f;
+  const Producer<kTransW, kDQ> p = member_producer<kTransW, kDQ>(mm, x, M, m0, c0, tid, mu, kstep0);
 
   // this lane's activation rows (clamped) and chunk pair
   const int arow = tid >> 2, ach = 2 * (tid & 3);
@@ -1315,24 +1304,18 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
   // rank at a time through the last LDS stage (zero past r and past M)
   constexpr int kL = kSt - 1;
   const bool lvec = (r % 8) == 0 && (set.ld_la % 8) == 0;
-  // kGated: gate's chunks, then up's
-  const int r_chunks = (r + QBK - 1) / QBK * QBK, rank_end = kGated && r_eff > 0 ? 2 * r_chunks : r_eff;
-  for (int jall = 0; jall < rank_end; jall += QBK) {
-    const int member = kGated && jall >= r_chunks ? 1 : 0, j0 = kGated ? jall - member * r_chunks : jall;
+  for (int j0 = 0; j0 < r_eff; j0 += QBK) {
     u32x4 va[kTiles], vb[4];
 #pragma unroll
     for (int it = 0; it < kTiles; ++it) {  // kRows rows x 8 chunks of the rank
       const int idx = tid + 256 * it, row = idx >> 3, ch = idx & 7;
       const int64_t grow = m0 + row;
-      va[it] = grow < M ? ld8(la + grow * set.ld_la + (int64_t)member * r, j0 + 8 * ch, r, lvec) : u32x4{0u, 0u, 0u, 0u};
+      va[it] = grow < M ? ld8(la + grow * set.ld_la, j0 + 8 * ch, r, lvec) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int idx = tid + 256 * it;
-      if (kGated) {  // 64 columns of the member x 8 chunks of the rank
-        const int row = idx >> 3, ch = idx & 7;
-        if (it < 2) vb[it] = ld8(set.m[member].lb + (c0 + row) * r, j0 + 8 * ch, r, lvec);
-      } else if (!kTransW) {  // 128 output columns x 8 chunks of the rank
+      if (!kTransW) {  // 128 output columns x 8 chunks of the rank
         const int row = idx >> 3, ch = idx & 7;
         vb[it] = ld8(lb_t + (c0 + row) * r, j0 + 8 * ch, r, lvec);
       } else {  // 64 rank rows x 16 chunks of 8 columns
@@ -1349,16 +1332,14 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int idx = tid + 256 * it;
-      if (kGated) {
-        if (it < 2) *(u32x4 *)&sb[kL][gated_sb_row(member, idx >> 3) * QLD + 8 * (idx & 7)] = vb[it];
-      } else if (!kTransW)
+      if (!kTransW)
         *(u32x4 *)&sb[kL][(idx >> 3) * QLD + 8 * (idx & 7)] = vb[it];
       else
         *(u32x4 *)&sb[kL][(idx >> 4) * TLD + 8 * (idx & 15)] = vb[it];
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
     wg_barrier();
-    if (!kGated || own == member) sm_stage_mfma<kTransW>(sa[kL], sb[kL], w, lane, acc);
+    sm_stage_mfma<kTransW>(sa[kL], sb[kL], w, lane, acc);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
     wg_barrier();  // the last stage is free again
   }
@@ -1419,16 +1400,15 @@ __global__ __launch_bounds__(256, 2) void qgemm_sm(QgemmSet set, int64_t M, cons
   }
 
   // element q of acc[i]: tile row 32 i + 8 (q / 4) + 4 (lane / 32) + q % 4, column 32 w + lane % 32
-  const int64_t col = kGated ? own * Ncols + c0 + 32 * (w >> 1) + l32 : c0 + 32 * w + l32;
-  if (kGated || part) {
-    const int64_t pcols = kGated ? 2 * Ncols : Ncols;
-    float *pz = part + (int64_t)blockIdx.z * M * pcols;
+  const int64_t col = c0 + 32 * w + l32;
+  if (part) {
+    float *pz = part + (int64_t)blockIdx.z * M * Ncols;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         const int64_t row = m0 + 32 * i + 8 * (q >> 2) + 4 * lhi + (q & 3);
-        if (row < M) pz[row * pcols + col] = acc[i][q];
+        if (row < M) pz[row * Ncols + col] = acc[i][q];
       }
     return;
   }
@@ -1727,20 +1707,11 @@ hipError_t launch_qgemm_set(bool trans_w, const QgemmSet &set, int64_t M, const 
   return hipGetLastError();
 }
 
-static_assert(kGatedSmTokens == kSmMaxRows, "gated launches of as many tokens run on the few-token tiles");
-int qgemm_gated_parts(int64_t M, int64_t N, int64_t K) { return qgemm_sm_split(M, 2 * N, K).splits; }
-
 template <bool kDQ, bool kClamp>
 static void launch_gated_ws(dim3 g, hipStream_t st, const QgemmSet &s, int64_t M, const uint16_t *x, const uint16_t *la,
                             int r, float scale, const Codebook &cb, float *part, int64_t steps, const GatedArgs &args) {
   qgemm_ws<false, kDQ, false, kClamp, true><<<g, 512, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, nullptr, part,
                                                                steps, args);
-}
-
-template <bool kDQ, int kRows>
-static void launch_gated_sm(dim3 g, hipStream_t st, const QgemmSet &s, int64_t M, const uint16_t *x, const uint16_t *la,
-                            int r, float scale, const Codebook &cb, float *part, int64_t steps) {
-  qgemm_sm<false, kDQ, kRows, GatedTiles><<<g, 256, 0, st>>>(s, M, x, la, nullptr, r, scale, nullptr, cb, part, steps);
 }
 
 hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
@@ -1750,20 +1721,7 @@ hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x,
   s.count = 2;
   s.ld_la = 2 * r;
   s.m[2] = s.m[3] = s.m[0];
-  const int64_t N = s.m[0].w.n_out, K = s.m[0].w.n_in;
   const bool dq = s.m[0].w.dq;
-  if (M <= kSmMaxRows) {
-    const QgemmSplit sp = qgemm_sm_split(M, 2 * N, K);
-    const int64_t steps = sp.splits > 1 ? sp.steps : K / QBK;
-    const dim3 g(1, (unsigned)(N / (QBN / 2)), (unsigned)sp.splits);
-    if (sm_rows(M) == 64)
-      dq ? launch_gated_sm<true, 64>(g, st, s, M, x, la, r, scale, cb, part, steps)
-         : launch_gated_sm<false, 64>(g, st, s, M, x, la, r, scale, cb, part, steps);
-    else
-      dq ? launch_gated_sm<true, 128>(g, st, s, M, x, la, r, scale, cb, part, steps)
-         : launch_gated_sm<false, 128>(g, st, s, M, x, la, r, scale, cb, part, steps);
-    return hipGetLastError();
-  }
   const GatedArgs args{out, rounds.full, rounds.tail};
   const dim3 g((unsigned)(rounds.full + rounds.tail * rounds.splits));
   if (M % QBM != 0)

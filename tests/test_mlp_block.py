@@ -80,7 +80,7 @@ def test_a_block_forward_and_backward(T, D, F, r, act):
     torch.cuda.current_stream().wait_stream(side)
     for name, want in _reference(p, act).items():
         for g, w in zip(*(([t] if not isinstance(t, list) else t) for t in (got[name], want))):
-            off = float((g.double() - w.detach()).norm() / w.norm())
+            off = float((g.double() - w.detach()).norm() / w.detach().norm())
             # what is read back in 8 bits is off by half a code, absmax / 254 of its 64 values
             assert off <= (NORMWISE_TOL if name not in ("gAd", "gA") else 2 * NORMWISE_TOL), (name, off)
 
