@@ -444,10 +444,12 @@ __global__ __launch_bounds__(64 * kWaves, TT <= 4 ? 3 : 2) void gated_split(Gate
 }  // namespace
 
 static int64_t chunk_count(int64_t K) { return (K + kChunk - 1) / kChunk; }
-// About two workgroups a CU, which hold three of them up to 64 tokens and two of more: with one the copies' latency shows
-// (64 tokens of two 22016 x 8192 weights: 131 us, with two 96), with four the results cost more than they gain (103).
+// About two workgroups a CU, which holds three of them up to 64 tokens and two of more: with one the copies' latency shows
+// (64 tokens of two 22016 x 8192 weights: 131 us, with two 96), with four the results cost more than they gain (103).  Past 64
+// tokens the results are longer, so from 384 tiles on there is one range (128 tokens of 28672 x 4096: two 109 us, one 101;
+// 22016 x 8192, 344 tiles: two 161, one 174).
 static int64_t range_chunks(int64_t T, int64_t N, int64_t K) {
-  const int64_t tiles = N / 64, want = T <= 64 ? (512 + tiles - 1) / tiles : std::max<int64_t>(512 / tiles, 2);
+  const int64_t tiles = N / 64, want = T <= 64 ? (512 + tiles - 1) / tiles : std::max<int64_t>(512 / tiles, tiles < 384 ? 2 : 1);
   const int64_t splits = std::min(want, chunk_count(K));
   return (chunk_count(K) + splits - 1) / splits;
 }
