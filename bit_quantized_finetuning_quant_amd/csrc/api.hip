@@ -209,7 +209,8 @@ const char *qlora_status_string(qlora_status s) {
     case QLORA_ERR_DTYPE: return "unknown dtype";
     case QLORA_ERR_HIP: return "HIP runtime error at launch";
     case QLORA_ERR_NONFINITE: return "NaN or Inf in the quantized weight";
-    case QLORA_ERR_VALUE: return "a scalar argument is not finite or out of range";
+    case QLORA_ERR_VALUE:
+      return "a scalar argument is not finite or out of range, or a buffer is named for two results";
     case QLORA_ERR_MEMORY: return "a buffer is not reachable by the GPU (pageable host memory?)";
     case QLORA_ERR_SCRATCH: return "the call needs more scratch than the library's fixed array holds";
   }

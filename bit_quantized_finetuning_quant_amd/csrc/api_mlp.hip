@@ -4,6 +4,8 @@
 
 #include <string.h>
 
+#include <initializer_list>
+
 #include "validate.hpp"
 
 using namespace qlora;
@@ -37,6 +39,14 @@ qlora_status check_norm(int64_t T, int64_t D, int dtype, float eps) {
 
 bool activation_ok(int act) { return act == QLORA_SILU || act == QLORA_GELU_TANH; }
 
+// Whether a buffer is named for two results (or for one and the input that every workgroup reads).
+bool named_twice(std::initializer_list<const void *> buffers) {
+  for (const void *const *a = buffers.begin(); a != buffers.end(); ++a)
+    for (const void *const *b = a + 1; b != buffers.end(); ++b)
+      if (*a && *a == *b) return true;
+  return false;
+}
+
 // n_in: byte offsets within a row tile of x stay below 2^32; n_ff, and its tiles with the tokens': a launch's grid.
 constexpr int64_t kGatedMaxDim = (int64_t)1 << 22, kGatedMaxTiles = (int64_t)1 << 22;
 
@@ -59,6 +69,7 @@ qlora_status qlora_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int
   if (s != QLORA_OK) return s;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum) || !aligned16(y))
     return QLORA_ERR_ALIGN;
+  if (named_twice({sum, y})) return QLORA_ERR_VALUE;
   const hipError_t e = launch_rms_norm_fwd(x, residual, T, D, weight, code_of(w_dtype) == QLORA_F32, eps, sum, y,
                                            y8 ? y8->codes : nullptr, y8 ? y8->scale : nullptr, (hipStream_t)stream);
   return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
@@ -103,6 +114,7 @@ qlora_status qlora_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const
   if (!dh || !gate || !up || !dgate || !dup) return QLORA_ERR_NULL;
   if (!aligned16(dh) || !aligned16(gate) || !aligned16(up) || !aligned16(dgate) || !aligned16(dup))
     return QLORA_ERR_ALIGN;
+  if (named_twice({dgate, dup})) return QLORA_ERR_VALUE;
   const hipError_t e =
       launch_gated_act_bwd(dh, gate, up, T, N, (Activation)code_of(act), dgate, dup, (hipStream_t)stream);
   return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
@@ -130,6 +142,7 @@ qlora_status qlora_linear_gated_fwd(const uint16_t *x, int64_t T, const qlora_nf
     return QLORA_ERR_ALIGN;
   const GatedPlan p = plan_linear_gated(T, N[0], q[0].n_in, r);
   if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
+  if (named_twice({x, h, gate, up, u_out})) return QLORA_ERR_VALUE;
   const QWeight w[2] = {qweight(&q[0]), qweight(&q[1])};
   const GatedOut out{(Activation)code_of(act), h, h8 ? h8->codes : nullptr, h8 ? h8->scale : nullptr, gate, up};
   const hipError_t e = launch_linear_gated_fwd(p, x, w, A_set, B, scale, out, u_out, (char *)ws, nf4_levels(),

@@ -1162,7 +1162,7 @@ def gated_act_fwd(gate, up, activation: str = "silu", h=None, need_h=True, act8:
 def gated_act_bwd(dh, gate, up, activation: str = "silu", dgate=None, dup=None, stream=None):
     """Backward of the gated product: (dgate, dup) = (bf16(dh up act'(gate)), bf16(dh act(gate))), which
     linear_set_bwd, linear_set_bwd_act8 and linear_bwd_dropout take as the projections' dy.  dgate and dup may
-    each be any one of dh, gate and up."""
+    each be any one of dh, gate and up, but not both the same."""
     code = _activation(activation)
     T, N = _rows(gate, "gate")
     dev = gate.device

@@ -57,7 +57,8 @@ typedef enum {
   QLORA_ERR_DTYPE = 5,      /* unknown dtype code                                   */
   QLORA_ERR_HIP = 6,        /* the HIP runtime reported an error at launch          */
   QLORA_ERR_NONFINITE = 7,  /* (deferred) NaN or Inf met while quantizing           */
-  QLORA_ERR_VALUE = 8,      /* a scalar argument is not finite or out of range      */
+  QLORA_ERR_VALUE = 8,      /* a scalar argument is not finite or out of range, or a
+                               buffer is named for two results                     */
   QLORA_ERR_MEMORY = 9,     /* a buffer is neither device nor pinned host memory    */
   QLORA_ERR_SCRATCH = 10    /* the call needs more than the fixed scratch array     */
 } qlora_status;
@@ -436,8 +437,8 @@ size_t qlora_head_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad
  *   y    = bf16( weight_d (s_td rstd_t) )           [T x D]
  *   *y8  = y as qlora_act8_write keeps it, code for code
  * x, residual, sum and y [T x D] bf16, weight [D] fp32 or bf16.  residual and
- * sum are both given or both NULL (then s = x); sum may be residual or x.  At
- * least one of y and y8 is given; y8's T and K are T and D.
+ * sum are both given or both NULL (then s = x); sum may be residual or x (y being
+ * sum is QLORA_ERR_VALUE).  At least one of y and y8 is given; y8's T and K are T and D.
  * Requires T >= 1, D % 64 == 0, D <= 65536, T D <= 2^37, a finite eps > 0.
  * A NaN in a row of s makes its row of y NaN; an Inf makes it NaN there and 0
  * elsewhere.  Finite rows of any magnitude give finite results.               */
@@ -452,7 +453,7 @@ qlora_status qlora_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int
  * grad_s is the gradient of x and of residual alike.  dres (the gradient that
  * reaches s past the norm; bf16) may be NULL, and grad_s may be dres or dy.
  * grad_weight may be NULL (a frozen weight); only with it a workspace is needed
- * (qlora_rms_norm_bwd_workspace_bytes(T, D), at most 2048 rows of D fp32 sums),
+ * (qlora_rms_norm_bwd_workspace_bytes(T, D), at most 512 rows of D fp32 sums),
  * whose sums are added in a fixed order.                                      */
 size_t qlora_rms_norm_bwd_workspace_bytes(int64_t T, int64_t D);
 qlora_status qlora_rms_norm_bwd(const uint16_t *dy, const uint16_t *s, const uint16_t *dres, int64_t T, int64_t D,
@@ -473,7 +474,8 @@ qlora_status qlora_gated_act_fwd(const uint16_t *gate, const uint16_t *up, int64
 
 /* Its backward pass: dgate = bf16( dh up act'(gate) ), dup = bf16( dh act(gate) ),
  * the dy of the two projections (qlora_linear_set_bwd and its like).  dgate and
- * dup may each be any one of dh, gate and up.                                 */
+ * dup may each be any one of dh, gate and up, but not both the same
+ * (QLORA_ERR_VALUE).                                                          */
 qlora_status qlora_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const uint16_t *up, int64_t T, int64_t N,
                                  qlora_activation act, uint16_t *dgate, uint16_t *dup, void *stream);
 
@@ -488,7 +490,8 @@ qlora_status qlora_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const
  * before they are rounded, so qlora_gated_act_fwd on them differs from h by
  * their roundings.)  Both weights are [n_ff x n_in] and of one storage form,
  * n_ff % 64 == 0, n_ff and n_in < 2^22, (T / 256 + 1) n_ff / 64 <= 2^22; the rest
- * as qlora_linear_set_fwd with two members.
+ * as qlora_linear_set_fwd with two members.  x, h, gate, up and u_out are buffers
+ * of their own (two the same: QLORA_ERR_VALUE).
  * ws: qlora_linear_gated_workspace_bytes, for these sizes (fewer tokens may take
  * another form and need more).  From about a thousand tokens on it holds both
  * decoded weights (4 n_ff n_in bytes, at most 2 GB; longer ones stay packed).  */

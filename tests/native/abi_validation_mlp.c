@@ -18,7 +18,7 @@ static int failures;
   } while (0)
 
 int main(void) {
-  _Alignas(16) static unsigned char mem[256];
+  _Alignas(16) static unsigned char mem[512];
   uint16_t *h = (uint16_t *)mem;
   float *f = (float *)mem;
   const uint16_t *B[2] = {h, h};
@@ -83,7 +83,13 @@ int main(void) {
   EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, INFINITY, QLORA_SILU, h, 0, 0, 0, 0, mem, 0, 0), QLORA_ERR_VALUE);
   EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, 1.f, odd_act, h, 0, 0, 0, 0, mem, 0, 0), QLORA_ERR_VALUE);
   EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, 1.f, QLORA_SILU, 0, 0, 0, 0, 0, mem, 0, 0), QLORA_ERR_NULL);
-  EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, 1.f, QLORA_SILU, h, &a, h, h, h, mem, 0, 0), QLORA_ERR_WORKSPACE);
+  EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, 1.f, QLORA_SILU, h + 8, &a, h + 16, h + 24, h + 32, mem, 0, 0), QLORA_ERR_WORKSPACE);
+  /* a buffer named for two results */
+  EXPECT(qlora_rms_norm_fwd(h, h, 4, 8 * 16, f, QLORA_F32, 1e-6f, h + 8, h + 8, 0, 0), QLORA_ERR_VALUE);
+  EXPECT(qlora_gated_act_bwd(h, h, h, 4, 128, QLORA_SILU, h, h, 0), QLORA_ERR_VALUE);
+  EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, 1.f, QLORA_SILU, h + 8, 0, h + 8, h + 16, 0, mem, 1 << 24, 0), QLORA_ERR_VALUE);
+  EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, 1.f, QLORA_SILU, h + 8, 0, h + 16, h + 16, 0, mem, 1 << 24, 0), QLORA_ERR_VALUE);
+  EXPECT(qlora_linear_gated_fwd(h, 4, q, h, B, 8, 1.f, QLORA_SILU, h, 0, 0, 0, 0, mem, 1 << 24, 0), QLORA_ERR_VALUE);
   if (failures) {
     printf("%d failures\n", failures);
     return 1;

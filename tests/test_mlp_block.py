@@ -136,3 +136,20 @@ def test_two_streams_at_once():
         for g, a in zip(got, alone):
             for k in ("z", "ds", "gw", "gA", "gAd"):
                 assert torch.equal(g[k], a[k]), k
+
+
+def test_a_buffer_named_for_two_results_is_refused():
+    torch = torch_mod()
+    announce("feed-forward operators: a buffer named twice")
+    p = _layer(4, 128, 128, 8, 1)
+    x, r, q = p["x"], p["res"], p["q"]
+    t = torch.zeros_like(x)
+    for call in (lambda: qlora.rms_norm_fwd(x, p["w"], EPS, residual=r, s=t, y=t),
+                 lambda: qlora.gated_act_bwd(x, r, r, dgate=t, dup=t),
+                 lambda: qlora.linear_gated_fwd(x, q, p["A"], p["B"], 1.0, h=t, gate=t),
+                 lambda: qlora.linear_gated_fwd(x, q, p["A"], p["B"], 1.0, gate=t, up=t),
+                 lambda: qlora.linear_gated_fwd(x, q, p["A"], p["B"], 1.0, h=x)):
+        with pytest.raises(qlora.QloraError, match="named for two results"):
+            call()
+    torch.cuda.synchronize()
+    assert bool((t == 0).all())
