@@ -10,6 +10,12 @@
 //                    of the chunks; x comes through LDS, once for the four waves, and the ranges' fp32 results are
 //                    added by a launch more
 //
+// What bounds them: the decode's vector instructions and, next to them, HBM.  Two 11008 x 4096 weights (46.5 MB), 1 token:
+// prep 7.0 us, gated_few 17.1 (2.7 TB/s; 12.9 with the decode's lookups left out), two 22016 x 8192 (186 MB) 53.7 (3.5
+// TB/s; 39); the decode is 23 instructions for 8 codes of a lane and 5 for their share of the table, 38 us of the 53.7 on
+// all SIMDs.  Codes or x a chunk further ahead cost a wave a SIMD and gain nothing (53.7 -> 57 us).  gated_split, 64
+// tokens of 22016 x 8192: 85 us, of which 43 are the decode's instructions and 21 the products.
+//
 // v_mfma_f32_16x16x32_bf16: A lane l holds A[l % 16][8 (l / 16) + 0..7], B lane l holds B[8 (l / 16) + 0..7][l % 16],
 // D register i of lane l is D[4 (l / 16) + i][l % 16].  Which 32 values of the contraction a product takes, and in what
 // order, is free as long as A and B agree.  Here lane (n, g) = (l % 16, l / 16) decodes one whole NF4 block of row
@@ -253,7 +259,6 @@ __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedF
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int h = 0; h < TT; ++h) xf[j][h] = (xp + (int64_t)(8 * s + j) * 4 * a.ld)[(uint32_t)(g * a.ld + token[h])];
-    if (TT == 1) __builtin_amdgcn_sched_barrier(0);  // (more tiles' loads together would take too many registers)
     DecodeTable t[2];
     u32x4 codes[2][2];
 #pragma unroll
@@ -268,7 +273,6 @@ __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedF
 #pragma unroll
       for (int i = 0; i < 2; ++i) codes[m][i] = *(const u32x4 *)(mine + 2048 * m + piece_at(n, 2 * g + i));
     load(s + kWaves, next);
-    if (TT == 1) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const u32x4 wg = decode_split(codes[0][j >> 2][j & 3], t[0]), wu = decode_split(codes[1][j >> 2][j & 3], t[1]);
