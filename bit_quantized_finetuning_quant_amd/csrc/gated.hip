@@ -7,6 +7,14 @@
 //
 // Behind the projections the product takes gate and up in fp32; the bf16 copies
 // of both are what the backward pass reads, and need not be written.
+//
+// The product alone and its backward pass are bound by HBM: 2048 x 11008 with h and its codes written (158 MB) 25 us,
+// 6.3 TB/s (part of it from the last-level cache); the gradients of 4096 x 22016 (902 MB) 135 us, 6.7 TB/s.
+//
+// Behind the projections there are three forms.  Up to 128 tokens the decode is the work (gated_few.hip).  Then the fused
+// GEMM (qgemm.hip) decodes a weight tile for 256 tokens beside the matrix instructions: 509 tokens of two 11008 x 4096
+// weights 115 us, 0.80 PFLOP/s, bound by the two roles of its waves.  From where that costs less (the forms' times are
+// estimated in plan_linear_gated) the weights are decoded first.
 
 #include <algorithm>
 
@@ -21,7 +29,7 @@ namespace qlora {
 namespace {
 
 constexpr int kWide = 256;  // threads of the elementwise kernels
-constexpr int kRuns = 2;  // runs of 8 values a thread takes, a workgroup's stride apart
+constexpr int kRuns = 2;    // runs of 8 values a thread takes, a workgroup's stride apart
 
 template <Activation kAct>
 __device__ __forceinline__ u32x4 product8(const u32x4 &g, const u32x4 &u) {
@@ -135,7 +143,10 @@ __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ 
 
 // ---- many tokens: decoded weights in the workspace, plain tiles ------------------------------------------------
 // The fused GEMM decodes a weight tile once for every 256 tokens; from some thousand tokens on, decoding each
-// weight once (2.5 bytes a weight at HBM speed) and multiplying on plain 256 x 256 tiles is faster.
+// weight once (2.5 bytes a weight at HBM speed) and multiplying on plain 256 x 256 tiles is faster: 2048 tokens of two
+// 11008 x 4096 weights 312 us (the decode 42, 5.4 TB/s), fused 407; 4096 tokens of 22016 x 8192 2.13 ms (164 us; the tiles
+// 2.06 ms at best, 1.43 PFLOP/s), fused 2.98.  Matrix instructions bound the tiles, at the clock that the card's
+// power leaves them (a library product of 4096 x 8192 x 44032 runs at 1.5 PFLOP/s).
 
 // What the tiles need beside x, in one launch, whose workgroups take one of two parts:
 //   the adapter's operands, whose contraction is the ranks of both members in turn, padded with zeros to `pad`:
@@ -364,18 +375,43 @@ void launch_tail(const float *part, const GatedRounds &rounds, int nleft, int nt
   });
 }
 
-// The two forms' times in us (fitted to 512 to 4096 tokens of n_ff x n_in = 5504 x 2048, 11008 x 4096 and 22016 x 8192,
-// within 5%).
+// Tiles of `steps` steps in rounds of 256 workgroups: whole ones and, where that is faster, the last in ranges.
+// round_us + step_us steps: a workgroup's time, of which `fixed` stays in a round that leaves CUs idle.
+GatedRounds gated_rounds(int64_t tiles, int64_t steps, double round_us, double step_us, double fixed,
+                         int64_t tile_bytes, double *us) {
+  auto rounds_us = [&](int64_t groups, int64_t n) {
+    const double idle = groups % 256 ? 1.0 - (double)(groups % 256) / 256 : 0.0;
+    return ((double)cdiv(groups, 256) - idle * (1.0 - fixed)) * (round_us + step_us * n);
+  };
+  GatedRounds best{(int)tiles, 0, 0, 0};
+  *us = rounds_us(tiles, steps);
+  const int64_t full = tiles / 256 * 256, tail = tiles - full;
+  for (int64_t s = 2; tail && s <= 16 && steps / s >= 4; ++s) {
+    const int64_t range = cdiv(steps, s), splits = cdiv(steps, range);
+    // the fp32 tiles are written beside the other ranges' products and read at 6 TB/s, by one launch more
+    const double t = rounds_us(full, steps) + rounds_us(tail * splits, range) +
+                     (double)(tail * splits * tile_bytes) / 6e6 + 4.0;
+    if (t < *us) {
+      *us = t;
+      best = GatedRounds{(int)full, (int)tail, (int)splits, range};
+    }
+  }
+  return best;
+}
+
+// The two forms' times in us, fitted to 509 to 4096 tokens of n_ff x n_in = 5504 x 2048, 11008 x 4096 and 22016 x 8192:
+// within 10%, and the faster form everywhere.  (The plain tiles run at the card's power limit: a round of fewer is faster.)  Fused and decoded: 5504 x 2048 1024 tokens 76 and 62, 2048 tokens 123 and 110;
+// 11008 x 4096 509 tokens 124 and 127, 1024 tokens 210 and 199; 22016 x 8192 509 tokens 386 and 488, 1024 tokens 740 and 722.
 constexpr double kFusedRound = 5.0, kFusedStep = 0.98, kPlainRound = 7.0, kPlainStep = 1.235;
 constexpr int64_t kFusedTile = 256 * 128 * 4, kPlainTile = 256 * 256 * 4;
 double fused_us(int64_t T, int64_t N, int64_t K, GatedRounds *rounds) {
   double us;
-  *rounds = gated_rounds(cdiv(T, 256) * (N / 64), K / 64, kFusedRound, kFusedStep, kFusedTile, &us);
+  *rounds = gated_rounds(cdiv(T, 256) * (N / 64), K / 64, kFusedRound, kFusedStep, 1.0, kFusedTile, &us);
   return 14.0 + us;
 }
 double plain_us(int64_t T, int64_t N, int64_t K, GatedRounds *rounds) {
   double us;
-  *rounds = gated_rounds(cdiv(N, kTileV / 2) * cdiv(T, kTileT), K / 64, kPlainRound, kPlainStep, kPlainTile, &us);
+  *rounds = gated_rounds(cdiv(N, kTileV / 2) * cdiv(T, kTileT), K / 64, kPlainRound, kPlainStep, 0.3, kPlainTile, &us);
   return 20.0 + us + 5.0 * (double)N * K / 5.1e6;
 }
 
@@ -417,24 +453,6 @@ hipError_t launch_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const 
       gated_act_bwd<a(), false><<<grid(runs), kWide, 0, st>>>(dh, gate, up, runs, dgate, dup);
   });
   return hipGetLastError();
-}
-
-GatedRounds gated_rounds(int64_t tiles, int64_t steps, double round_us, double step_us, int64_t tile_bytes, double *us) {
-  GatedRounds best{(int)tiles, 0, 0, 0};
-  *us = (double)cdiv(tiles, 256) * (round_us + step_us * steps);
-  const int64_t full = tiles / 256 * 256, tail = tiles - full;
-  for (int64_t s = 2; tail && s <= 16 && steps / s >= 4; ++s) {
-    const int64_t range = cdiv(steps, s), splits = cdiv(steps, range);
-    // an fp32 tile is written and read at about 4 bytes a ps, by one launch more
-    const double t = (double)(full / 256) * (round_us + step_us * steps) +
-                     (double)cdiv(tail * splits, 256) * (round_us + step_us * range) +
-                     2.0 * tail * splits * tile_bytes / 4e6 + 4.0;
-    if (t < *us) {
-      *us = t;
-      best = GatedRounds{(int)full, (int)tail, (int)splits, range};
-    }
-  }
-  return best;
 }
 
 GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {

@@ -323,8 +323,6 @@ struct GatedRounds {
   int full, tail, splits;
   int64_t steps;  // of 64, of a range
 };
-// round_us + step_us * steps: a workgroup's time; tile_bytes: an fp32 tile's.
-GatedRounds gated_rounds(int64_t tiles, int64_t steps, double round_us, double step_us, int64_t tile_bytes, double *us);
 // Fused GEMM of both projections (qgemm.hip): set holds gate and up, la = u_set [M x 2 r], n_out % 64 == 0.
 // Tiles of 256 tokens by 64 columns of each, tokens fastest; whole tiles are written to `out`, the ranges of the others
 // to part[range][tail tile][256][128] (gate's columns, then up's).
