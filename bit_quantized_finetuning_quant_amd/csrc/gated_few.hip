@@ -13,7 +13,7 @@
 // What bounds them: the decode's vector instructions and, next to them, HBM.  Two 11008 x 4096 weights (46.5 MB), 1 token:
 // prep 7.0 us, gated_few 17.1 (2.7 TB/s; 12.9 with the decode's lookups left out), two 22016 x 8192 (186 MB) 53.7 (3.5
 // TB/s; 39); the decode is 23 instructions for 8 codes of a lane and 5 for their share of the table, 38 us of the 53.7 on
-// all SIMDs.  Codes or x a chunk further ahead cost a wave a SIMD and gain nothing (53.7 -> 57 us).  gated_split, 64
+// all SIMDs.  Codes or x a chunk further ahead cost a wave a SIMD and more than they gain (with prep 62 -> 65 us).  gated_split, 64
 // tokens of 22016 x 8192: 85 us, of which 43 are the decode's instructions and 21 the products.
 //
 // v_mfma_f32_16x16x32_bf16: A lane l holds A[l % 16][8 (l / 16) + 0..7], B lane l holds B[8 (l / 16) + 0..7][l % 16],
