@@ -66,6 +66,20 @@ __device__ __forceinline__ float dot8(const u32x4 &a, const u32x4 &b, float c) {
   return c;
 }
 
+// Lanes 0..31 (or even rows of 16) the sum of a and its other half (row), the others that of b.
+template <int kLanes>
+__device__ __forceinline__ float fold(float a, float b) {
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  const auto r = kLanes == 32 ? __builtin_amdgcn_permlane32_swap(x, y, false, false)
+                              : __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// The value kBy lanes away in the row of 16.
+template <int kBy>
+__device__ __forceinline__ float rotated(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + kBy, 0xF, 0xF, true));
+}
+
 // Workgroups below `utiles`: kPrepRows rows of A_set by kPrepTokens tokens of u, the lanes along n_in (a matrix
 // instruction's operand would take rows from neighbouring lanes: 64 accesses a load).  The others: x [T][K] into xp, 8
 // values a thread, zero past n_in.
@@ -73,7 +87,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gated_few_prep(const uint16_t
                                                                   const uint16_t *__restrict__ A, int T, int K,
                                                                   int ld, int rows, int utiles, uint16_t *__restrict__ u,
                                                                   uint16_t *__restrict__ xp) {
-  __shared__ float red[kPrepWaves][kPrepRows * kPrepTokens];
+  __shared__ __attribute__((aligned(16))) float red[kPrepWaves][kPrepRows * kPrepTokens];
   if ((int)blockIdx.x >= utiles) {
     const uint32_t i = ((uint32_t)blockIdx.x - utiles) * (64 * kPrepWaves) + threadIdx.x;
     const uint32_t runs = (uint32_t)((K + kChunk - 1) / kChunk) * (kChunk / 8) * T;
@@ -111,23 +125,22 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gated_few_prep(const uint16_t
 #pragma unroll
       for (int h = 0; h < kPrepTokens; ++h) acc[i][h] = dot8(av[i], xv[h], acc[i][h]);
   }
-  // The 16 sums over the lanes: four exchanges that halve the values a lane holds leave one in each of 16 lanes.
+  // The 16 sums over the lanes.  A swap of two registers' halves (odd rows of 16 with even ones) and an addition fold two
+  // values into one register; the rows' sums are rotations.  Row p of 16 lanes holds values 4 p + 0..3.
   float v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = acc[i / kPrepTokens][i % kPrepTokens];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const bool upper = (lane >> e) & 1;
+  for (int i = 0; i < 8; ++i) v[i] = fold<32>(v[i], v[i + 8]);
 #pragma unroll
-    for (int i = 0; i < (8 >> e); ++i) {
-      const float keep = upper ? v[i + (8 >> e)] : v[i], give = upper ? v[i] : v[i + (8 >> e)];
-      v[i] = keep + __shfl_xor(give, 1 << e);
-    }
+  for (int i = 0; i < 4; ++i) {
+    v[i] = fold<16>(v[i], v[i + 4]);
+    v[i] += rotated<8>(v[i]);
+    v[i] += rotated<4>(v[i]);
+    v[i] += rotated<2>(v[i]);
+    v[i] += rotated<1>(v[i]);
   }
-  v[0] += __shfl_xor(v[0], 16);
-  v[0] += __shfl_xor(v[0], 32);
-  // lane l < 16 holds value 8 l0 + 4 l1 + 2 l2 + l3 of its bits
-  if (lane < 16) red[wave][((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | (lane >> 3)] = v[0];
+  if ((lane & 15) == 0) *(f32x4 *)&red[wave][4 * (lane >> 4)] = f32x4{v[0], v[1], v[2], v[3]};
   __syncthreads();
   const int i = threadIdx.x / kPrepTokens, h = threadIdx.x % kPrepTokens;
   if (i >= kPrepRows || t0 + h >= T || r0 + i >= rows) return;
