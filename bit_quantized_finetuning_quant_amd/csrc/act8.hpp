@@ -12,9 +12,9 @@ typedef uint32_t act8_u32x2 __attribute__((ext_vector_type(2)));
 
 // max over the 8 lanes of a block
 __device__ __forceinline__ uint32_t block_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-  return v;
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));      // lane ^ 1
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));      // lane ^ 2
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));  // 7 - lane
 }
 
 // The codes of 8 values of a block with the largest magnitude c1 (finite, > 0): the quotients Q = 127 x / c1

@@ -173,6 +173,29 @@ __device__ __forceinline__ void dma16(const char *sbase, uint32_t voff, uint32_t
 }
 #pragma clang diagnostic pop
 
+// Sums over lanes without LDS.
+// Lanes 0..31 (or even rows of 16) the sum of a and its other half (row), the others that of b.
+template <int kLanes>
+__device__ __forceinline__ float fold(float a, float b) {
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  const auto r = kLanes == 32 ? __builtin_amdgcn_permlane32_swap(x, y, false, false)
+                              : __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// The value kBy lanes away in the row of 16.
+template <int kBy>
+__device__ __forceinline__ float rotated(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + kBy, 0xF, 0xF, true));
+}
+
+// The sum of the row of 16, in all of its lanes.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += rotated<8>(v);
+  v += rotated<4>(v);
+  v += rotated<2>(v);
+  return v + rotated<1>(v);
+}
+
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 }  // namespace qlora

@@ -124,10 +124,11 @@ __device__ __forceinline__ void finish8(const GatedOut &out, int64_t to, const f
 template <Activation kAct>
 __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ part, int parts, int64_t T, int64_t N,
                                                         GatedOut out) {
-  const int64_t runs = T * N / 8, zs = 2 * T * N;
-  for (int64_t i = (int64_t)blockIdx.x * kWide + threadIdx.x; i < runs; i += (int64_t)gridDim.x * kWide) {
-    const int64_t row = 8 * i / N, col = 8 * i - row * N;
-    const float *p = part + row * (2 * N) + col;
+  const int64_t zs = 2 * T * N;
+  const uint32_t row_runs = (uint32_t)(N / 8), runs = (uint32_t)T * row_runs;  // at most 2^26
+  for (uint32_t i = blockIdx.x * kWide + threadIdx.x; i < runs; i += gridDim.x * kWide) {
+    const uint32_t row = i / row_runs;
+    const float *p = part + row * (2 * N) + 8 * (i - row * row_runs);
     f32x4 v[4] = {};
 #pragma unroll 4
     for (int z = 0; z < parts; ++z)
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ 
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[k][q] += a[q];
       }
-    finish8<kAct>(out, 8 * i, v);
+    finish8<kAct>(out, 8 * (int64_t)i, v);
   }
 }
 
@@ -165,11 +166,12 @@ struct GatedPrep {
 
 __device__ __forceinline__ void prep_pack(const GatedPrep &a) {
   const int per = a.pad / 8;
-  const int64_t i = (int64_t)blockIdx.x * kWide + threadIdx.x, row = i / per;
+  const uint32_t i = blockIdx.x * kWide + threadIdx.x;  // (rows and tokens below 2^24, per at most 64)
+  const int64_t row = i / (uint32_t)per;
   if (row >= 2 * a.N + (a.up ? a.T : 0)) return;
   const bool token = row >= 2 * a.N;
   const int member = !token && row >= a.N ? 1 : 0;
-  const int c = (int)(i - row * per) * 8, width = token ? 2 * a.r : a.r, first = c - member * a.r;
+  const int c = (int)(i - (uint32_t)row * per) * 8, width = token ? 2 * a.r : a.r, first = c - member * a.r;
   const uint16_t *src = token ? a.u + (row - 2 * a.N) * width : a.B[member] + (row - member * a.N) * a.r;
   u32x4 v = {0u, 0u, 0u, 0u};
   if (first >= 0 && first + 8 <= width) {

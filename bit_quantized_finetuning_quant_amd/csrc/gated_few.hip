@@ -66,20 +66,6 @@ __device__ __forceinline__ float dot8(const u32x4 &a, const u32x4 &b, float c) {
   return c;
 }
 
-// Lanes 0..31 (or even rows of 16) the sum of a and its other half (row), the others that of b.
-template <int kLanes>
-__device__ __forceinline__ float fold(float a, float b) {
-  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-  const auto r = kLanes == 32 ? __builtin_amdgcn_permlane32_swap(x, y, false, false)
-                              : __builtin_amdgcn_permlane16_swap(x, y, false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-// The value kBy lanes away in the row of 16.
-template <int kBy>
-__device__ __forceinline__ float rotated(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + kBy, 0xF, 0xF, true));
-}
-
 // Workgroups below `utiles`: kPrepRows rows of A_set by kPrepTokens tokens of u, the lanes along n_in (a matrix
 // instruction's operand would take rows from neighbouring lanes: 64 accesses a load).  The others: x [T][K] into xp, 8
 // values a thread, zero past n_in.
@@ -135,10 +121,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gated_few_prep(const uint16_t
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[i] = fold<16>(v[i], v[i + 4]);
-    v[i] += rotated<8>(v[i]);
-    v[i] += rotated<4>(v[i]);
-    v[i] += rotated<2>(v[i]);
-    v[i] += rotated<1>(v[i]);
+    v[i] = row16_sum(v[i]);
   }
   if ((lane & 15) == 0) *(f32x4 *)&red[wave][4 * (lane >> 4)] = f32x4{v[0], v[1], v[2], v[3]};
   __syncthreads();

@@ -63,9 +63,11 @@ __device__ __forceinline__ void unpack8(const u32x4 &v, float (&out)[8]) {
 template <int kRow, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[N]) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], d);
+  for (int k = 0; k < N; ++k) {
+    v[k] = row16_sum(v[k]);
+    v[k] = fold<16>(v[k], v[k]);
+    v[k] = fold<32>(v[k], v[k]);
+  }
   if constexpr (kRow > 64) {
     constexpr int kWaves = kRow / 64;
     const int wave = threadIdx.x >> 6;
