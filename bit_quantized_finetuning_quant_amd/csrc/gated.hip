@@ -474,7 +474,7 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   size_t off = 256;
   p.off_u = off;
   off += align256((size_t)T * 2 * r * 2);
-  p.own_u = p.few && gated_few_own_u(T, r);
+  p.own_u = p.few && gated_few_own_u(T, K, r);
   p.off_part = off;
   off += p.own_u ? 0 : align256(lora_part_floats(T, 2 * r, K) * 4);
   p.off_xp = off;

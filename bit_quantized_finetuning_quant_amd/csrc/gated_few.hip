@@ -464,14 +464,12 @@ int gated_few_parts(int64_t T, int64_t N, int64_t K) {
 }
 
 // Tiles of u.  Each reads its rows and tokens whole, so from some number on the two launches of the adapters' product are
-// faster (two 11008 x 4096 weights: 128 tokens at rank 16, 256 tiles, 58 against 63 us; at rank 64, 1024 tiles, 71
-// against 66; 64 tokens at rank 64, 512 tiles, even).
+// faster: 128 tokens of two 8192 x 8192 weights at rank 64 (1024 tiles) 65 us against 69 with them, at rank 128 75 both, at
+// rank 200 85 against 81; of 11008 x 4096 at rank 200 (3200 tiles) 77 both.
 static int64_t u_tiles(int64_t T, int r) {
   return (2 * r + kPrepRows - 1) / kPrepRows * ((T + kPrepTokens - 1) / kPrepTokens);
 }
-bool gated_few_own_u(int64_t T, int r) {
-  return u_tiles(T, r) <= 512;
-}
+bool gated_few_own_u(int64_t T, int64_t K, int r) { return u_tiles(T, r) * K <= (int64_t)1 << 24; }
 
 size_t gated_few_xp_values(int64_t T, int64_t K) { return (size_t)(chunk_count(K) * kChunk * ((T + 3) / 4 * 4)); }
 
@@ -479,7 +477,7 @@ hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, cons
                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
                             float *part, const Codebook &cb, hipStream_t st) {
   const int64_t N = w[0].n_out, K = w[0].n_in;
-  const int utiles = gated_few_own_u(T, r) ? (int)u_tiles(T, r) : 0;
+  const int utiles = gated_few_own_u(T, K, r) ? (int)u_tiles(T, r) : 0;
   const int ld = (int)(T + 3) / 4 * 4;
   const int64_t runs = chunk_count(K) * (kChunk / 8) * T;
   gated_few_prep<<<(unsigned)(utiles + (runs + 64 * kPrepWaves - 1) / (64 * kPrepWaves)), 64 * kPrepWaves, 0, st>>>(

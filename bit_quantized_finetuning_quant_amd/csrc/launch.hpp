@@ -334,7 +334,7 @@ hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x,
 // many ranges of n_in are written, part[range][T][2 n_out] (gate before up).
 constexpr int64_t kGatedFewTokens = 128;
 int gated_few_parts(int64_t T, int64_t N, int64_t K);
-bool gated_few_own_u(int64_t T, int r);  // u is written here; otherwise it is there
+bool gated_few_own_u(int64_t T, int64_t K, int r);  // u is written here; otherwise it is there
 size_t gated_few_xp_values(int64_t T, int64_t K);
 hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
