@@ -11,10 +11,11 @@
 //                    added by a launch more
 //
 // What bounds them: the decode's vector instructions and, next to them, HBM.  Two 11008 x 4096 weights (46.5 MB), 1 token:
-// prep 7.0 us, gated_few 17.1 (2.7 TB/s; 12.9 with the decode's lookups left out), two 22016 x 8192 (186 MB) 53.7 (3.5
-// TB/s; 39); the decode is 23 instructions for 8 codes of a lane and 5 for their share of the table, 38 us of the 53.7 on
-// all SIMDs.  Codes or x a chunk further ahead cost a wave a SIMD and more than they gain (with prep 62 -> 65 us).  gated_split, 64
-// tokens of 22016 x 8192: 85 us, of which 43 are the decode's instructions and 21 the products.
+// prep 3.4 us, gated_few 16.5 (2.8 TB/s; 12.5 with the decode's lookups left out), two 22016 x 8192 (186 MB) 52.5 (3.5
+// TB/s; 39); the decode is 23 instructions for 8 codes of a lane and 5 for their share of the table, 38 us of the 52.5 on
+// all SIMDs.  Codes or x a chunk further ahead cost a wave a SIMD and more than they gain (with prep 62 -> 65 us).  gated_split,
+// 64 tokens of 22016 x 8192: 85 us, of which 43 are the decode's instructions and 21 the products.  The adapter's operands
+// are all asked for at once and before the first codes (one after the other they were 6 us of 33 tokens of 11008 x 4096).
 //
 // v_mfma_f32_16x16x32_bf16: A lane l holds A[l % 16][8 (l / 16) + 0..7], B lane l holds B[8 (l / 16) + 0..7][l % 16],
 // D register i of lane l is D[4 (l / 16) + i][l % 16].  Which 32 values of the contraction a product takes, and in what
@@ -183,6 +184,12 @@ __device__ __forceinline__ void build_table(const Pieces &b, float mu, const Cod
   }
 }
 
+// The operands of 32 ranks from j on: a lane's eight of a row of each B and of each of its tokens' u.
+template <int TT>
+struct Ranks {
+  u32x4 b[2], u[2][TT];
+};
+
 struct GatedFewArgs {
   const uint16_t *xp, *u;
   QWeight w[2];
@@ -191,9 +198,46 @@ struct GatedFewArgs {
   float scale;
 };
 
-// TT tiles of 16 tokens.  Four of them fit three waves a SIMD, so that the 2.7 that 11008 x 4096 has run at once (64
-// tokens: 38.6 -> 32.1 us); with fewer tiles the compiler's own choice is faster (48 tokens of 22016 x 8192: 102
-// against 129 us).
+// All loads are on their way before one is waited for (with ranks of whole eights; otherwise value by value).
+template <int TT>
+__device__ __forceinline__ void load_ranks(const GatedFewArgs &a, int64_t row, const int (&token)[TT], int j,
+                                           Ranks<TT> &o) {
+  if ((a.r & 7) == 0) {
+    const int at = min(j, a.r - 8);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      o.b[m] = load8(a.B[m] + row * a.r + at);
+#pragma unroll
+      for (int h = 0; h < TT; ++h) o.u[m][h] = load8(a.u + (int64_t)token[h] * (2 * a.r) + m * a.r + at);
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      o.b[m] = ranks8(a.B[m] + row * a.r, j, a.r);
+#pragma unroll
+      for (int h = 0; h < TT; ++h) o.u[m][h] = ranks8(a.u + (int64_t)token[h] * (2 * a.r) + m * a.r, j, a.r);
+    }
+  }
+}
+
+// acc += u B^T of them, D's rows the tokens', or with kSwap the weight's.
+template <bool kSwap, int TT>
+__device__ __forceinline__ void add_ranks(const GatedFewArgs &a, int j, Ranks<TT> &o, f32x4 (&acc)[2][TT]) {
+  const u32x4 none = {0u, 0u, 0u, 0u};
+  const bool in = j < a.r;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const u32x4 b = in ? o.b[m] : none;
+#pragma unroll
+    for (int h = 0; h < TT; ++h) {
+      const u32x4 u = in ? o.u[m][h] : none;
+      acc[m][h] = kSwap ? mfma16(b, u, acc[m][h]) : mfma16(u, b, acc[m][h]);
+    }
+  }
+}
+
+// TT tiles of 16 tokens.  Four of them are held to three waves a SIMD, so that the 2.7 that 11008 x 4096 has run at once
+// (64 tokens: 37.3 -> 34.9 us); with three the compiler's own choice is faster (33 tokens of 5504 x 2048: 16.4 against 18.8).
 template <int TT, bool kDQ>
 __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedFewArgs a, Codebook cb, GatedOut out) {
   __shared__ float red[kWaves][16 * TT][17];
@@ -219,27 +263,25 @@ __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedF
       b[m].s2 = a.w[m].s2[constant];
     }
   };
-  Pieces next[2];
-  load(wave, next);
-  const float mu0 = kDQ ? *a.w[0].mu : 0.f, mu1 = kDQ ? *a.w[1].mu : 0.f;
   int token[TT];
 #pragma unroll
   for (int h = 0; h < TT; ++h) token[h] = min(16 * h + n, a.T - 1);
 
-  // the adapter term first: 32 ranks a product, the waves in turn
+  // the adapter term first, 32 ranks a product, the waves in turn; its first loads go out before those of the codes
+  Ranks<TT> ranks;
+  if (32 * wave < a.r) load_ranks(a, row, token, 32 * wave + 8 * g, ranks);
+  Pieces next[2];
+  load(wave, next);
+  const float mu0 = kDQ ? *a.w[0].mu : 0.f, mu1 = kDQ ? *a.w[1].mu : 0.f;
   f32x4 acc[2][TT];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int h = 0; h < TT; ++h) acc[m][h] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int j = 32 * wave; j < a.r; j += 32 * kWaves)
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const u32x4 b = ranks8(a.B[m] + row * a.r, j + 8 * g, a.r);
-#pragma unroll
-      for (int h = 0; h < TT; ++h)
-        acc[m][h] = mfma16(ranks8(a.u + (int64_t)token[h] * (2 * a.r) + m * a.r, j + 8 * g, a.r), b, acc[m][h]);
-    }
+  for (int j = 32 * wave; j < a.r; j += 32 * kWaves) {
+    if (j > 32 * wave) load_ranks(a, row, token, j + 8 * g, ranks);
+    add_ranks<false>(a, j + 8 * g, ranks, acc);
+  }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -366,26 +408,27 @@ __global__ __launch_bounds__(64 * kWaves, TT <= 4 ? 3 : 2) void gated_split(Gate
     const char *src = xp + (int64_t)h * 256 * a.ld;
     for (int p = wave; p < a.ld / 4; p += kWaves) dma16(src + 1024 * p, x_from, lds_addr(xs[buf] + 1024 * p));
   };
+  int token[TT];
+#pragma unroll
+  for (int h = 0; h < TT; ++h) token[h] = min(16 * h + n, a.T - 1);
+  const int splits = (int)gridDim.x / tiles;
+  Ranks<TT> ranks;
+  if (32 * z < a.r) load_ranks(a, row0 + n, token, 32 * z + 8 * g, ranks);
   place(0);
   load(c0);
   load_x(2 * c0, 0);
   const float mu0 = kDQ ? *a.w[0].mu : 0.f, mu1 = kDQ ? *a.w[1].mu : 0.f;
-  // the adapter term, 32 ranks a product, the ranges in turn; D's rows are the weight's here: a lane holds four
-  // neighbouring columns of one token
+  // the adapter term, 32 ranks a product, the ranges in turn (its first loads are out already); D's rows are the weight's
+  // here: a lane holds four neighbouring columns of one token
   f32x4 acc[2][TT];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int h = 0; h < TT; ++h) acc[m][h] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int j = 32 * z; j < a.r; j += 32 * (int)(gridDim.x / tiles))
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const u32x4 b = ranks8(a.B[m] + (row0 + n) * a.r, j + 8 * g, a.r);
-#pragma unroll
-      for (int h = 0; h < TT; ++h)
-        acc[m][h] = mfma16(
-            b, ranks8(a.u + (int64_t)min(16 * h + n, a.T - 1) * (2 * a.r) + m * a.r, j + 8 * g, a.r), acc[m][h]);
-    }
+  for (int j = 32 * z; j < a.r; j += 32 * splits) {
+    if (j > 32 * z) load_ranks(a, row0 + n, token, j + 8 * g, ranks);
+    add_ranks<true>(a, j + 8 * g, ranks, acc);
+  }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -455,10 +498,10 @@ static int64_t range_chunks(int64_t T, int64_t N, int64_t K) {
 }
 
 // In ranges where x in registers costs more than the launch that adds them.  One pass against ranges, us: 17 tokens of
-// two 11008 x 4096 weights 30 and 34, 64 tokens 38 and 40; 33 tokens of 14336 x 4096 42 and 40, 64 tokens 54 and 44; 20 tokens of
-// 22016 x 8192 83 and 77, 33 tokens 102 and 84.
+// two 11008 x 4096 weights 23 and 30, 64 tokens 35 and 37; 33 tokens of 14336 x 4096 34 both, 64 tokens 43 and 40; 33 tokens of
+// 13824 x 5120 42 and 41, of 22016 x 8192 95 and 81.
 int gated_few_parts(int64_t T, int64_t N, int64_t K) {
-  if (T <= 16 || (T <= 64 && N * K < (int64_t)48 << 20)) return 0;
+  if (T <= 16 || (T <= 64 && N * K < (int64_t)(T <= 48 ? 64 : 48) << 20)) return 0;
   const int64_t range = range_chunks(T, N, K);
   return (int)((chunk_count(K) + range - 1) / range);
 }
@@ -485,10 +528,11 @@ hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, cons
   const GatedFewArgs a{xp, u, {w[0], w[1]}, {B[0], B[1]}, (int)T, ld, (int)N, (int)K, r, scale};
   const int parts = gated_few_parts(T, N, K), range = (int)range_chunks(T, N, K);
   auto run = [&](auto tiles, auto dq) {
-    if (tiles() > 4 || parts) {
-      gated_split<tiles(), dq()><<<(unsigned)(N / 64 * parts), 64 * kWaves, 0, st>>>(a, cb, range, part);
-      return;
-    }
+    if constexpr (tiles() > 1)
+      if (parts) {
+        gated_split<tiles(), dq()><<<(unsigned)(N / 64 * parts), 64 * kWaves, 0, st>>>(a, cb, range, part);
+        return;
+      }
     if constexpr (tiles() <= 4) gated_few<tiles(), dq()><<<(unsigned)(N / 16), 64 * kWaves, 0, st>>>(a, cb, out);
   };
   auto with_tiles = [&](auto dq) {
