@@ -14,8 +14,8 @@
 // Sums and statistics are fp32; s, y and grad_s round once.
 //
 // What bounds it is HBM, and for few rows the launch.  On this card's 5.35 TB/s of a 512 MB copy: forward 2048 x 4096 with
-// the residual (67 MB) 11.8 us, 5.7 TB/s, 4096 x 8192 in 8 bits too (305 MB) 51; backward 4096 x 8192 with the residual's
-// gradient (268 MB) 46 us, 5.8 TB/s, with the weight's 57 (the launch that adds it 5).  One row of 4096: 3.2 us.
+// the residual (67 MB) 11.4 us, 5.9 TB/s, 4096 x 8192 in 8 bits too (305 MB) 50; backward 4096 x 8192 with the residual's
+// gradient (268 MB) 46 us, 5.8 TB/s, with the weight's 55 (the launch that adds it 5).  One row of 4096: 3.0 us.
 //
 // Squares past fp32 (a row with |s| > 1.8e19) make the sum infinite; the row is
 // then summed again with s scaled by 2^-96, which is exact.
