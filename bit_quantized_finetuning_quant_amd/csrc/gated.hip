@@ -474,7 +474,7 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   size_t off = 256;
   p.off_u = off;
   off += align256((size_t)T * 2 * r * 2);
-  p.own_u = p.few && gated_few_own_u(T, K, r);
+  p.own_u = gated_own_u(T, K, r);
   p.off_part = off;
   off += p.own_u ? 0 : align256(lora_part_floats(T, 2 * r, K) * 4);
   p.off_xp = off;
@@ -500,11 +500,12 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
                                    char *ws, const Codebook &cb, hipStream_t st) {
   uint16_t *u = u_out ? u_out : (uint16_t *)(ws + p.off_u);
   float *part = (float *)(ws + p.off_part), *qpart = (float *)(ws + p.off_qpart);
-  hipError_t e;
-  if (!p.own_u) {
+  hipError_t e = hipSuccess;
+  if (!p.own_u)
     e = launch_lora(LoraKind::kU, x, p.K, A_set, p.K, p.T, 2 * p.r, p.K, 1.0f, u, part, st);
-    if (e != hipSuccess) return e;
-  }
+  else if (!p.few)
+    e = launch_gated_u(p.T, x, A_set, p.K, p.r, u, st);
+  if (e != hipSuccess) return e;
   if (p.few) {
     GatedOut first = out;
     if (!p.parts) {

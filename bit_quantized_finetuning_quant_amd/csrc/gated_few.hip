@@ -506,21 +506,32 @@ int gated_few_parts(int64_t T, int64_t N, int64_t K) {
   return (int)((chunk_count(K) + range - 1) / range);
 }
 
-// Tiles of u.  Each reads its rows and tokens whole, so from some number on the two launches of the adapters' product are
-// faster: 128 tokens of two 8192 x 8192 weights at rank 64 (1024 tiles) 65 us against 69 with them, at rank 128 75 both, at
-// rank 200 85 against 81; of 11008 x 4096 at rank 200 (3200 tiles) 77 both.
+// Tiles of u, each of which reads its rows of A_set and its tokens whole.
 static int64_t u_tiles(int64_t T, int r) {
   return (2 * r + kPrepRows - 1) / kPrepRows * ((T + kPrepTokens - 1) / kPrepTokens);
 }
-bool gated_few_own_u(int64_t T, int64_t K, int r) { return u_tiles(T, r) * K <= (int64_t)1 << 24; }
+// So from some number of values on the two launches of the adapters' product are faster.  In the launch that lays out x,
+// past 2^24: 128 tokens of two 8192 x 8192 weights at rank 64 (2^23) 65 us against 69 with them, at rank 128 75 both, at rank
+// 200 85 against 81.  By itself, past 128 tokens, from 5 2^20: 256 tokens of 11008 x 4096 at rank 16 (2^21) 64.5 against 68.3, 129
+// at rank 64 (2^22) 65 and 67, 1024 at rank 16 (2^23) 207 and 205.
+bool gated_own_u(int64_t T, int64_t K, int r) {
+  return u_tiles(T, r) * K <= (T <= kGatedFewTokens ? (int64_t)1 << 24 : (int64_t)5 << 20);
+}
 
 size_t gated_few_xp_values(int64_t T, int64_t K) { return (size_t)(chunk_count(K) * kChunk * ((T + 3) / 4 * 4)); }
+
+hipError_t launch_gated_u(int64_t T, const uint16_t *x, const uint16_t *A_set, int64_t K, int r, uint16_t *u,
+                          hipStream_t st) {
+  const int utiles = (int)u_tiles(T, r);
+  gated_few_prep<<<(unsigned)utiles, 64 * kPrepWaves, 0, st>>>(x, A_set, (int)T, (int)K, 0, 2 * r, utiles, u, nullptr);
+  return hipGetLastError();
+}
 
 hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
                             float *part, const Codebook &cb, hipStream_t st) {
   const int64_t N = w[0].n_out, K = w[0].n_in;
-  const int utiles = gated_few_own_u(T, K, r) ? (int)u_tiles(T, r) : 0;
+  const int utiles = gated_own_u(T, K, r) ? (int)u_tiles(T, r) : 0;
   const int ld = (int)(T + 3) / 4 * 4;
   const int64_t runs = chunk_count(K) * (kChunk / 8) * T;
   gated_few_prep<<<(unsigned)(utiles + (runs + 64 * kPrepWaves - 1) / (64 * kPrepWaves)), 64 * kPrepWaves, 0, st>>>(

@@ -329,12 +329,16 @@ struct GatedRounds {
 hipError_t launch_qgemm_gated(const QgemmSet &set, int64_t M, const uint16_t *x, const uint16_t *la, int r, float scale,
                               const GatedRounds &rounds, const GatedOut &out, float *part, const Codebook &cb,
                               hipStream_t st);
-// Up to kGatedFewTokens tokens (gated_few.hip): u [T x 2 r] is written, xp holds x laid out for the products.
+// u = x A_set^T [T x 2 r] where gated_own_u, which is faster there than the adapters' product.
+bool gated_own_u(int64_t T, int64_t K, int r);
+hipError_t launch_gated_u(int64_t T, const uint16_t *x, const uint16_t *A_set, int64_t K, int r, uint16_t *u,
+                          hipStream_t st);
+// Up to kGatedFewTokens tokens (gated_few.hip): u is written where gated_own_u and read otherwise, xp holds x laid out
+// for the products.
 // gated_few_parts = 0: in one pass, out.h is given and out.codes is not.  Otherwise only the fp32 results of that
 // many ranges of n_in are written, part[range][T][2 n_out] (gate before up).
 constexpr int64_t kGatedFewTokens = 128;
 int gated_few_parts(int64_t T, int64_t N, int64_t K);
-bool gated_few_own_u(int64_t T, int64_t K, int r);  // u is written here; otherwise it is there
 size_t gated_few_xp_values(int64_t T, int64_t K);
 hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, const uint16_t *A_set,
                             const uint16_t *const *B, int r, float scale, const GatedOut &out, uint16_t *u, uint16_t *xp,
@@ -344,7 +348,7 @@ struct GatedPlan {
   int r;
   bool few;            // the few-token form
   int parts;           // its fp32 results of all tokens (0: it writes the product itself)
-  bool own_u;          // it writes u
+  bool own_u;          // gated_own_u
   bool decode;         // decoded weights on plain tiles
   GatedRounds rounds;  // of the 256-row tiles of either form
   size_t off_u, off_xp, off_part, off_qpart, off_w, off_b, off_up, off_h, total;
