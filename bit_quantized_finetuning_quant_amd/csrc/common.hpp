@@ -146,6 +146,10 @@ __device__ __forceinline__ u32x4 load_run(const uint16_t *p) {
 // of 361 MB: 100.6 -> 80.6 us, of 90 MB even.)
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
 
+// s_waitcnt immediate (gfx9 encoding): vmcnt in bits 3:0 and 15:14, expcnt in
+// 6:4 (left at its maximum), lgkmcnt in 11:8.
+constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 15) | (7 << 4) | ((lgkm & 15) << 8) | ((vm >> 4) << 14); }
+
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 // The LDS byte address of a pointer into LDS.

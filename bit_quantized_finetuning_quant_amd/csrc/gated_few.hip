@@ -362,7 +362,9 @@ __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedF
 //        refilled
 // A wave's waits: at a chunk's start for all of its copies, in its middle for those of x, all but the four copies of
 // codes issued after them; each before the barrier behind which other waves read what it has copied, and with
-// lgkmcnt(0), so that what it has read is in registers before others overwrite it.
+// lgkmcnt(0), so that what it has read is in registers before others overwrite it.  They are asm, which the compiler
+// neither drops nor counts; the builtin beside the first tells it that nothing is on its way, or its own wait for what
+// is loaded before the loop stands behind every chunk's copies.
 template <int TT, bool kDQ>
 __global__ __launch_bounds__(64 * kWaves, TT <= 4 ? 3 : 2) void gated_split(GatedFewArgs a, Codebook cb, int range,
                                                                             float *__restrict__ part) {
@@ -438,6 +440,7 @@ __global__ __launch_bounds__(64 * kWaves, TT <= 4 ? 3 : 2) void gated_split(Gate
 
   for (int c = c0; c < c1; ++c) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::"v"(from[0]), "v"(from[1]), "v"(x_from) : "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
     barrier();
     load_x(2 * c + 1, 1);
     u32x4 w[2][2];
