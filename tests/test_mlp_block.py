@@ -153,3 +153,49 @@ def test_a_buffer_named_for_two_results_is_refused():
             call()
     torch.cuda.synchronize()
     assert bool((t == 0).all())
+
+
+def test_trusted_calls_give_the_same():
+    torch = torch_mod()
+    announce("feed-forward block, trusted calls")
+    p = _layer(70, 256, 704, 8, 9)
+    want = _step(p, "gelu_tanh")
+    with qlora.trusted_calls():
+        got = _step(p, "gelu_tanh")
+    for k in ("z", "s", "h", "ds", "gw", "gA", "gAd"):
+        assert torch.equal(got[k], want[k]), k
+    assert torch.equal(got["a"].codes, want["a"].codes) and torch.equal(got["h8"].scale, want["h8"].scale)
+
+
+def test_more_than_2_31_values():
+    """Rows past 2^31 values: the last ones are those of a call on them alone (rows are independent of each other)."""
+    torch = torch_mod()
+    T, N = 200_001, 11008
+    announce(f"feed-forward operators, {T} x {N}")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    gate, up = (torch.empty(T, N, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    last = slice(T - 37, T)
+    h, a = qlora.gated_act_fwd(gate, up, need_act8=True)
+    h2, a2 = qlora.gated_act_fwd(gate[last], up[last], need_act8=True)
+    assert torch.equal(h[last], h2) and torch.equal(a.codes[last], a2.codes) and torch.equal(a.scale[last], a2.scale)
+    del a, a2
+    for b, c in zip(qlora.gated_act_bwd(h, gate, up), qlora.gated_act_bwd(h[last], gate[last], up[last])):
+        assert torch.equal(b[last], c)
+    w = torch.randn(N, device="cuda")
+    y, s, _ = qlora.rms_norm_fwd(gate, w, EPS, residual=up)
+    y2, s2, _ = qlora.rms_norm_fwd(gate[last], w, EPS, residual=up[last])
+    assert torch.equal(y[last], y2) and torch.equal(s[last], s2)
+    ds = qlora.rms_norm_bwd(h, s, w, EPS, dres=up)[0]
+    assert torch.equal(ds[last], qlora.rms_norm_bwd(h[last], s2, w, EPS, dres=up[last])[0])
+    del y, s, ds, h, gate, up
+    # behind the projections: 300 rows take the tiles that the whole takes, or tiles whose sums differ in their order
+    K, r = 64, 8
+    qs = [qlora.quantize(torch.randn(N, K, generator=g, device="cuda")) for _ in range(2)]
+    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    A, Bs = torch.randn(2 * r, K, generator=g, device="cuda").bfloat16(), [torch.randn(N, r, generator=g, device="cuda").bfloat16()
+                                                                        for _ in range(2)]
+    out = qlora.linear_gated_fwd(x, qs, A, Bs, 0.25)
+    few = qlora.linear_gated_fwd(x[-300:], qs, A, Bs, 0.25)
+    for k in ("h", "gate", "up", "u"):
+        a, b = getattr(out, k)[-300:].double(), getattr(few, k).double()
+        assert float((a - b).norm() / b.norm()) <= NORMWISE_TOL, k
