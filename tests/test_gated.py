@@ -180,7 +180,8 @@ BLOCKS = [(1, 64, 64, 1), (1, 4096, 1024, 16), (2, 192, 320, 7), (3, 128, 192, 6
           (64, 704, 1024, 32), (65, 256, 320, 7), (100, 4096, 256, 128), (128, 512, 832, 256), (129, 320, 576, 8),
           (255, 192, 64, 1), (256, 128, 128, 16), (300, 4096, 320, 64), (511, 64, 1088, 8), (513, 2112, 192, 100),
           (1000, 256, 704, 64), (1024, 512, 1024, 8), (2049, 320, 448, 16), (4096, 128, 192, 200), (2, 262208, 64, 8),
-          (40, 131136, 128, 16), (40, 65600, 832, 200), (23, 16448, 3264, 16), (64, 8192, 6208, 7)]
+          (40, 131136, 128, 16), (40, 65600, 832, 200), (23, 16448, 3264, 16), (64, 8192, 6208, 7),
+          (3, 64, 4194240, 8), (70, 64, 1048640, 8), (1, 4194240, 64, 8), (200, 65600, 64, 1)]
 
 
 @gpu
