@@ -417,13 +417,18 @@ double plain_us(int64_t T, int64_t N, int64_t K, GatedRounds *rounds) {
   return 20.0 + us + 5.0 * (double)N * K / 5.1e6;
 }
 
+// The columns of the decoded form's adapter operands: the ranks of both members, in whole steps.
+int64_t padded_ranks(int r) { return cdiv(2 * r, kStep) * kStep; }
+
 // Whether the decoded form is taken.
-bool decode_pays(int64_t T, int64_t N, int64_t K) {
-  // offsets within a tile, from its first row of gate to its last of up, stay below 2^32, and the threads of the
-  // launches; the decoded weights below 2 GB
+bool decode_pays(int64_t T, int64_t N, int64_t K, int r) {
+  // offsets within a tile, from its first row of gate to its last of up, stay below 2^32 in the weights and in the
+  // adapter's operands (of 512 columns they would not at the largest n_ff), and the threads of the launches; the
+  // decoded weights below 2 GB
   if (N * K > (int64_t)1 << 29 || K > 65536 || T > (int64_t)1 << 22) return false;
-  GatedRounds r;
-  return 1.03 * plain_us(T, N, K, &r) < fused_us(T, N, K, &r);
+  if ((N + kTileV / 2) * padded_ranks(r) * 2 > (int64_t)1 << 32) return false;
+  GatedRounds rounds;
+  return 1.03 * plain_us(T, N, K, &rounds) < fused_us(T, N, K, &rounds);
 }
 
 // One pass of a workgroup each, up to 2^22 of them.
@@ -465,7 +470,7 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   p.r = r;
   p.few = T <= kGatedFewTokens;
   p.parts = p.few ? gated_few_parts(T, N, K) : 0;
-  p.decode = !p.few && decode_pays(T, N, K);
+  p.decode = !p.few && decode_pays(T, N, K, r);
   size_t tail = 0;
   if (!p.few) {
     p.decode ? plain_us(T, N, K, &p.rounds) : fused_us(T, N, K, &p.rounds);
@@ -484,7 +489,7 @@ GatedPlan plan_linear_gated(int64_t T, int64_t N, int64_t K, int r) {
   p.off_qpart = off;
   off += align256(std::max((size_t)p.parts * T * 2 * N * 4, tail));
   // the decoded form: both weights, the adapter's operands (u as it is where its ranks need no padding)
-  const size_t pad = (size_t)(2 * r + 63) / 64 * 64;
+  const size_t pad = (size_t)padded_ranks(r);
   p.off_w = off;
   off += p.decode ? align256((size_t)2 * N * K * 2) : 0;
   p.off_b = off;
@@ -524,7 +529,7 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
     return out.codes ? launch_act8_encode(first.h, p.T, p.N, out.codes, out.scale, st) : hipSuccess;
   }
   if (p.decode) {
-    const int pad = (2 * p.r + 63) / 64 * 64;
+    const int pad = (int)padded_ranks(p.r);
     GatedPrep g{};
     g.u = u;
     for (int i = 0; i < 2; ++i) {

@@ -1,0 +1,85 @@
+"""The gated product behind its projections, where fp32 sums leave nothing to their order: gate, up and u bit for bit.
+
+The inputs are chosen so that every partial sum, in whatever order, is a multiple of 2^-q below 2^(23 - q) in magnitude, and
+so exact in fp32 (`_exact` checks it): x is -1, 0 or 1; the decoded weights are bf16 values, multiples of 2^-q for a q
+that their smallest one gives; A is 0 or +-1/8, so that u is a multiple of 1/8 of a few bits, exact in bf16; B is a
+multiple of 2^-8 of 7 bits and the scale 1/2.  Then gate and up are exact, their bf16 results are those values rounded
+once, and h is off by its activation's error and one rounding: for silu and tanh-gelu as `test_gated.py` derives."""
+
+import pytest
+
+from bit_quantized_finetuning_quant_amd import qlora
+from helpers import announce, torch_mod
+from test_gated import E, HALF, TINY, _act, _close
+
+gpu = pytest.mark.gpu
+
+
+def _case(T, K, N, r, seed, dq):
+    torch = torch_mod()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.rand(*s, generator=g, device="cuda")  # noqa: E731
+    x = torch.where(rand(T, K) < min(1.0, 768 / K), torch.where(rand(T, K) < 0.5, 1.0, -1.0), 0.0).bfloat16()
+    A = torch.where(rand(2 * r, K) < min(1.0, 128 / K), torch.where(rand(2 * r, K) < 0.5, 0.125, -0.125), 0.0).bfloat16()
+    Bs = [torch.randint(-127, 128, (N, r), generator=g, device="cuda", dtype=torch.int8).bfloat16().mul_(2.0**-8) for _ in range(2)]
+    qs = []
+    for _ in range(2):
+        qs.append(qlora.quantize(torch.randn(N, K, generator=g, device="cuda").mul_(K**-0.5), double_quant=dq))
+    return x, qs, A, Bs, 0.5
+
+
+def _exact(x, qs, A, Bs, scale, cols):
+    """(u, gate, up) of these rows of x at the columns `cols` in 64 bits, after a check that fp32 sums are exact."""
+    torch = torch_mod()
+    mm = lambda a, b: torch.mm(a, b.t().contiguous())  # noqa: E731
+    x, r = x.double(), A.shape[0] // 2
+    u = mm(x, A.double())
+    assert bool((u.bfloat16().double() == u).all())
+    out = [u]
+    for i, (q, B) in enumerate(zip(qs, Bs)):
+        W, B, ui = qlora.dequantize(q)[cols].double(), B[cols].double(), u[:, i * r:(i + 1) * r].contiguous()
+        grid = next(k for k in range(60) if bool((W * 2.0**k == (W * 2.0**k).round()).all()))
+        assert grid >= 12  # the adapter's products are multiples of 2^-12
+        most = mm(x.abs(), W.abs()) + scale * mm(ui.abs(), B.abs())
+        # (the adapter's sum comes before its scale, which is 1/2)
+        assert float(most.max()) < 2.0**(23 - grid) and float(mm(ui.abs(), B.abs()).max()) < 2.0**(23 - 11)
+        out.append(mm(x, W) + scale * mm(ui, B))
+    return out
+
+
+def _check(p, out, act, rows=slice(None), cols=slice(None)):
+    torch = torch_mod()
+    u, gate, up = _exact(p[0][rows], *p[1:], cols)
+    assert torch.equal(out.u[rows].double(), u)
+    for name, want in (("gate", gate), ("up", up)):
+        got = getattr(out, name)[rows][:, cols]
+        assert torch.equal(got, want.bfloat16()), (name, int((got != want.bfloat16()).sum()))
+    value, _, _, _, _, sg = _act(act, gate)
+    want = value * up
+    _close(out.h[rows][:, cols], want, (HALF + sg + 4 * E) * want.abs() + 2.0**-126 * (gate * up).abs() + TINY)
+
+
+LARGEST = (1 << 22) - 64  # n_ff
+
+
+def test_the_decoded_form_at_the_largest_n_ff():
+    """Offsets of the decoded form's tiles from their first row of gate to their last of up are 32 bits: at the
+    largest n_ff with padded ranks of 512 they would pass them, and another form is taken."""
+    need = qlora.linear_gated_workspace_bytes
+    for T in (129, 200, 256, 1000, 4000):
+        for r in (225, 256):
+            assert need(T, LARGEST, 64, r) < 4 * LARGEST * 512, (T, r)  # (the decoded form holds B in 512 columns twice)
+    # its adapter's operands are still held one row below
+    assert need(256, LARGEST, 64, 224) > 4 * LARGEST * 448 and need(256, LARGEST - 64, 64, 256) > 4 * (LARGEST - 64) * 512
+
+
+@gpu
+def test_every_column_of_the_largest_n_ff():
+    torch = torch_mod()
+    T, K, r = 129, 64, 256
+    announce(f"gated block of the largest n_ff, T={T} r={r}")
+    p = _case(T, K, LARGEST, r, 7, True)
+    out = qlora.linear_gated_fwd(*p)
+    torch.cuda.synchronize()
+    for first in (0, LARGEST // 2 // 128 * 128, LARGEST - 4096):
+        _check(p, out, "silu", cols=slice(first, first + 4096))
