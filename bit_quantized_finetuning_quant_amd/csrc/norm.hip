@@ -18,7 +18,9 @@
 // gradient (268 MB) 46 us, 5.8 TB/s, with the weight's 55 (the launch that adds it 5).  One row of 4096: 3.0 us.
 //
 // Squares past fp32 (a row with |s| > 1.8e19) make the sum infinite; the row is
-// then summed again with s scaled by 2^-96, which is exact.
+// then summed again with s scaled by 2^-96.  Only the sums take scaled values (those below 2^-30 lose bits there, which
+// are nothing beside 2^128); xhat is s times 2^-96 rstd, which is at least 2^-128 and off by 2^-22 of itself at most, where it
+// is subnormal.
 
 #include <algorithm>
 
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_fwd(NormFwd p)
         if (i < runs) *(u32x4 *)(p.sum + row + 8 * i) = s[v];
       }
     }
-    float lift = 1.0f, rstd;
+    float lift = 1.0f, rstd;  // rstd of s lift
     for (;;) {
       float sq[1] = {0.f};
 #pragma unroll
@@ -154,6 +156,7 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_fwd(NormFwd p)
       if (lift != 1.0f || sq[0] < __builtin_inff()) break;  // (a NaN's sum is summed again, to the same)
       lift = kLift;
     }
+    const float outer = rstd * lift;  // 1 / the root of the mean square
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = lane + v * kRow;
@@ -164,7 +167,7 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_fwd(NormFwd p)
       u32x4 y;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        y[j] = pack_bf16x2(w[2 * j] * (a[2 * j] * lift * rstd), w[2 * j + 1] * (a[2 * j + 1] * lift * rstd));
+        y[j] = pack_bf16x2(w[2 * j] * (a[2 * j] * outer), w[2 * j + 1] * (a[2 * j + 1] * outer));
       if (p.y) *(u32x4 *)(p.y + row + 8 * i) = y;
       if (p.codes) {
         float block;
@@ -272,7 +275,7 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_bwd(NormBwd p)
       weight(v, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xhat = a[j] * lift * rstd;
+        const float xhat = a[j] * outer;
         o[j] = outer * (w[j] * b[j] - xhat * c);
         if (p.dres) o[j] += past[j];
         if constexpr (kWeight) gw[v][j] = __builtin_fmaf(b[j], xhat, gw[v][j]);
