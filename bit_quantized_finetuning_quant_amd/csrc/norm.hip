@@ -190,7 +190,8 @@ struct NormBwd {
   float *part;  // with the weight's gradient: [workgroup][D]
 };
 
-// One row: rstd (of s lifted) and c from the sums of s^2 and w dy s.  false: the squares pass fp32.
+// One row: rstd (of s lifted) and c from the sums of s^2 and w dy s.  false: the squares pass fp32.  (c may do so where its
+// value does not: it is not finite then, and norm_mean forms it.)
 template <int kRow, int V, bool kLifted, typename W>
 __device__ __forceinline__ bool norm_sums(const NormBwd &p, const u32x4 (&s)[V], const u32x4 (&g)[V], const W &weight,
                                           float (*red)[2], float &rstd, float &c) {
@@ -213,6 +214,26 @@ __device__ __forceinline__ bool norm_sums(const NormBwd &p, const u32x4 (&s)[V],
   rstd = 1.0f / sqrtf(sum[0] / (float)p.D + p.eps * lift * lift);
   c = sum[1] * rstd / (float)p.D;
   return sum[0] < __builtin_inff();
+}
+
+// c as the sum of w dy xhat / D, whose partial sums are at most the largest |w dy| (a second reduction, for rows whose
+// products w dy s pass fp32 before rstd brings them back).
+template <int kRow, int V, typename W>
+__device__ __forceinline__ float norm_mean(const u32x4 (&s)[V], const u32x4 (&g)[V], const W &weight, float (*red)[2],
+                                           float outer, int D) {
+  const float part = 1.0f / (float)D;
+  float sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float a[8], b[8], w[8];
+    unpack8(s[v], a);
+    unpack8(g[v], b);
+    weight(v, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(w[j] * b[j], a[j] * outer * part, sum[0]);
+  }
+  row_sum<kRow>(sum, red);
+  return sum[0];
 }
 
 // The weight stays in registers over a workgroup's rows where it has room there.
@@ -265,6 +286,7 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_bwd(NormBwd p)
       norm_sums<kRow, V, true>(p, s, g, weight, red, rstd, c);
     }
     const float outer = rstd * lift;  // 1 / the root of the mean square
+    if (!(__builtin_fabsf(c) < __builtin_inff())) c = norm_mean<kRow, V>(s, g, weight, red, outer, p.D);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = lane + v * kRow;

@@ -450,6 +450,8 @@ qlora_status qlora_rms_norm_fwd(const uint16_t *x, const uint16_t *residual, int
  *   xhat        = s rstd,   c_t = mean_d( weight_d dy_td xhat_td )
  *   grad_s      = bf16( dres + rstd (weight dy - xhat c) )     [T x D]
  *   grad_weight = sum_t dy_td xhat_td                          [D] fp32
+ * Finite rows with |weight_d dy_td| < 2^119 give finite gradients, where these fit
+ * their types (products weight dy s below 2^-126 lose bits in c).
  * grad_s is the gradient of x and of residual alike.  dres (the gradient that
  * reaches s past the norm; bf16) may be NULL, and grad_s may be dres or dy.
  * grad_weight may be NULL (a frozen weight); only with it a workspace is needed

@@ -34,3 +34,26 @@ def test_small_values_beside_huge_ones(D):
         _close(got, gs, ts)
         # (the bound of `_grads` ends in a constant that these values lie below)
         _close(gotw, gw, 141 * E * gw.abs())
+
+
+@gpu
+@pytest.mark.parametrize("D", DIMS)
+def test_large_gradients_of_large_rows(D):
+    """|w dy s| past fp32, where c = mean(w dy xhat) and the gradients are not: rows whose squares fit fp32 and rows whose
+    squares do not."""
+    torch = torch_mod()
+    announce(f"norm backward, large gradients D={D}")
+    eps = 1e-6
+    p = _inputs(5, D, D + 5, True)
+    s, dy = p["res"].double(), p["dy"].double()
+    for row, (of_s, of_dy) in enumerate([(1e15, 1e25), (1e17, 1e34), (1e33, 1e34), (1.0, 1.0), (1e36, 1e34)]):
+        s[row] *= of_s
+        dy[row] *= of_dy
+    s, dy = s.bfloat16(), dy.bfloat16()
+    assert bool(s.isfinite().all()) and float((p["w"].double() * dy.double()).abs().max()) < 2.0**119
+    for rows in ([0, 1, 2, 3, 4], [0], [1], [2], [4]):
+        a, b = dy[rows], s[rows]
+        (gs, ts), (gw, tw) = _grads(a, b, p["w"], eps, None)
+        got, gotw = qlora.rms_norm_bwd(a, b, p["w"], eps, need_grad_weight=True)
+        _close(got, gs, ts)
+        _close(gotw, gw, tw)
