@@ -17,7 +17,7 @@
 // the residual (67 MB) 11.4 us, 5.9 TB/s, 4096 x 8192 in 8 bits too (305 MB) 50; backward 4096 x 8192 with the residual's
 // gradient (268 MB) 46 us, 5.8 TB/s, with the weight's 55 (the launch that adds it 5).  One row of 4096: 3.0 us.
 //
-// Squares past fp32 (a row with |s| > 1.8e19) make the sum infinite; the row is
+// Squares past fp32 (a row with |s| > 1.8e19) make the sum infinite, or an eps near fp32's end the mean; the row is
 // then summed again with s scaled by 2^-96.  Only the sums take scaled values (those below 2^-30 lose bits there, which
 // are nothing beside 2^128); xhat is s times 2^-96 rstd, which is at least 2^-128 and off by 2^-22 of itself at most, where it
 // is subnormal.
@@ -152,8 +152,9 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_fwd(NormFwd p)
         }
       }
       row_sum<kRow>(sq, red);
-      rstd = 1.0f / sqrtf(sq[0] / (float)p.D + p.eps * lift * lift);
-      if (lift != 1.0f || sq[0] < __builtin_inff()) break;  // (a NaN's sum is summed again, to the same)
+      const float mean = sq[0] / (float)p.D + p.eps * lift * lift;
+      rstd = 1.0f / sqrtf(mean);
+      if (lift != 1.0f || mean < __builtin_inff()) break;  // (a NaN's sum is summed again, to the same)
       lift = kLift;
     }
     const float outer = rstd * lift;  // 1 / the root of the mean square
@@ -190,7 +191,7 @@ struct NormBwd {
   float *part;  // with the weight's gradient: [workgroup][D]
 };
 
-// One row: rstd (of s lifted) and c from the sums of s^2 and w dy s.  false: the squares pass fp32.  (c may do so where its
+// One row: rstd (of s lifted) and c from the sums of s^2 and w dy s.  false: mean s^2 + eps passes fp32.  (c may do so where its
 // value does not: it is not finite then, and norm_mean forms it.)
 template <int kRow, int V, bool kLifted, typename W>
 __device__ __forceinline__ bool norm_sums(const NormBwd &p, const u32x4 (&s)[V], const u32x4 (&g)[V], const W &weight,
@@ -211,9 +212,10 @@ __device__ __forceinline__ bool norm_sums(const NormBwd &p, const u32x4 (&s)[V],
     }
   }
   row_sum<kRow>(sum, red);
-  rstd = 1.0f / sqrtf(sum[0] / (float)p.D + p.eps * lift * lift);
+  const float mean = sum[0] / (float)p.D + p.eps * lift * lift;
+  rstd = 1.0f / sqrtf(mean);
   c = sum[1] * rstd / (float)p.D;
-  return sum[0] < __builtin_inff();
+  return mean < __builtin_inff();
 }
 
 // c as the sum of w dy xhat / D, whose partial sums are at most the largest |w dy| (a second reduction, for rows whose

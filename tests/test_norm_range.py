@@ -57,3 +57,21 @@ def test_large_gradients_of_large_rows(D):
         got, gotw = qlora.rms_norm_bwd(a, b, p["w"], eps, need_grad_weight=True)
         _close(got, gs, ts)
         _close(gotw, gw, tw)
+
+
+@gpu
+def test_the_largest_eps():
+    """mean + eps past fp32, where the root is not."""
+    torch = torch_mod()
+    announce("norm, the largest eps")
+    eps, D = float(torch.finfo(torch.float32).max), 64
+    p = _inputs(4, D, 4, True)
+    s = (1.7e18 * (1 + 0.01 * p["x"].double().clamp(-3, 3))).bfloat16()
+    assert float(s.float().square().sum(1).max()) < eps  # the squares' sum fits
+    y = qlora.rms_norm_fwd(s, p["w"], eps)[0]
+    want = _y(s, p["w"], eps)
+    _close(y, want, (HALF + 68 * E) * want.abs() + TINY)
+    (gs, ts), (gw, tw) = _grads(p["dy"], s, p["w"], eps, None)
+    got, gotw = qlora.rms_norm_bwd(p["dy"], s, p["w"], eps, need_grad_weight=True)
+    _close(got, gs, ts)
+    _close(gotw, gw, tw)
