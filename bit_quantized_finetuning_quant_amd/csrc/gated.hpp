@@ -3,8 +3,9 @@
 //   silu         act(g) = g sigma(g)
 //   gelu (tanh)  act(g) = g (1 + tanh(k (g + c g^3))) / 2 = g sigma(2 k (g + c g^3)),  k = sqrt(2 / pi), c = 0.044715
 //
-// Both are g sigma(z) with z odd in g.  sigma = 1 / (1 + e^-z) keeps its relative precision on both sides
-// (e^-z overflows, and sigma is 0, only where it is below 2^-127); 1 - sigma is the same of -z.
+// Both are g sigma(z) with z odd in g.  With t = e^-|z| and r = 1 / (1 + t), sigma and 1 - sigma are r and t r, or t r and r
+// where z < 0: both keep their relative precision on both sides (silu: 9 half steps of fp32 with the products; tanh-gelu as
+// much and those of its z, which weigh |z| times).
 #pragma once
 
 #include <type_traits>
@@ -16,32 +17,46 @@
 namespace qlora {
 namespace {
 
-constexpr float kLog2e = 1.44269504f;
+constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f;  // their sum is log2 e to 2^-50
 constexpr float kGeluTwoK = 1.59576912f, kGeluC = 0.044715f;
 
 template <Activation kAct>
 __device__ __forceinline__ float gate_z(float g) {
   return kAct == Activation::kSilu ? g : kGeluTwoK * g * __builtin_fmaf(kGeluC * g, g, 1.0f);
 }
-__device__ __forceinline__ float sigma(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+
+// sigma(z) and 1 - sigma(z).  v_exp takes the remainder of |z| log2 e, at most 1/2 (of the product itself it would lose |z|
+// half steps), and e^-160 is 0 in fp32.  A NaN is dropped.
+__device__ __forceinline__ void sigma(float z, float &s, float &other) {
+  const float a = __builtin_fminf(__builtin_fabsf(z), 160.0f), n = __builtin_rintf(a * kLog2e);
+  const float f = __builtin_fmaf(a, kLog2eLow, __builtin_fmaf(a, kLog2e, -n));
+  const float t = __builtin_ldexpf(__builtin_amdgcn_exp2f(-f), -(int)n);
+  const float r = __builtin_amdgcn_rcpf(1.0f + t), q = t * r;
+  s = z < 0.f ? q : r;
+  other = z < 0.f ? r : q;
 }
 
-// act(g); a gate of -inf gives the limit, 0 (the clamp drops a NaN, sigma carries it)
+// g, which carries a NaN, and for -inf the lowest finite value: times sigma it has the limit, 0
+__device__ __forceinline__ float bounded(float g) { return g < -0x1.fffffep127f ? -0x1.fffffep127f : g; }
+
+// act(g)
 template <Activation kAct>
 __device__ __forceinline__ float gate_act(float g) {
-  return __builtin_fmaxf(g, -0x1.fffffep127f) * sigma(gate_z<kAct>(g));
+  float s, other;
+  sigma(gate_z<kAct>(g), s, other);
+  return bounded(g) * s;
 }
 
 // act(g) and act'(g) = s + g s (1 - s) z'(g); past |g| = 128 s is 0 or 1 - s is, in fp32, and with it the
 // second term, so g is clamped there and z' cannot overflow
 template <Activation kAct>
 __device__ __forceinline__ void gate_act_slope(float g, float &value, float &slope) {
-  const float z = gate_z<kAct>(g), s = sigma(z), t = sigma(-z);
-  value = __builtin_fmaxf(g, -0x1.fffffep127f) * s;
-  const float c = __builtin_fminf(__builtin_fmaxf(g, -128.f), 128.f);
+  float s, other;
+  sigma(gate_z<kAct>(g), s, other);
+  value = bounded(g) * s;
+  const float c = g > 128.f ? 128.f : g < -128.f ? -128.f : g;  // (a NaN stays)
   const float dz = kAct == Activation::kSilu ? 1.0f : kGeluTwoK * __builtin_fmaf(3.0f * kGeluC * c, c, 1.0f);
-  slope = __builtin_fmaf(c * t * dz, s, s);
+  slope = __builtin_fmaf(c * other * dz, s, s);
 }
 
 // f(activation) with the activation as a constant

@@ -83,3 +83,27 @@ def test_every_column_of_the_largest_n_ff():
     torch.cuda.synchronize()
     for first in (0, LARGEST // 2 // 128 * 128, LARGEST - 4096):
         _check(p, out, "silu", cols=slice(first, first + 4096))
+
+
+@gpu
+def test_silu_to_a_few_steps_of_fp32():
+    """Every finite gate by every significand of up.  sigma = 1 / (1 + t) or t / (1 + t) with t = e^-|g|: t is exp2 of a
+    remainder below 1/2 that is off by e (fma, its constant's low part), with e = 2^-24 half a step of fp32, an
+    instruction of one step (2 e) and an exact power of two: 3 e.  The sum 1 e (of t's error at most all), the reciprocal 2 e, their product 1 e, and
+    the two products of g and up 1 e each: 9 e in all, and half a step of bf16.  Where t is subnormal (g < -87) it is off by
+    2^-150 at most, twice that with the product that follows."""
+    torch = torch_mod()
+    announce("silu to a few steps")
+    gate = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).cuda()
+    gate = gate[gate.isfinite() & (gate.abs() > 2.0**-100)]  # (below, products are subnormal)
+    gate = gate[: gate.numel() // 8 * 8].view(-1, 1).expand(-1, 128).contiguous()
+    for size in (1.0, 2.0**10):
+        up = ((1 + torch.arange(128, device="cuda") / 128) * size).bfloat16().expand_as(gate).contiguous()
+        want = gate.double() * torch.special.expit(gate.double()) * up.double()
+        small = 2.0**-149 * (gate.double() * up.double()).abs() * (gate.double() < -87)
+        tol = (HALF + 9 * E * (1 + HALF)) * want.abs() + small + TINY
+        fits = want.abs() < 3.38e38
+        h, _ = qlora.gated_act_fwd(gate, up)
+        _close(h[fits][None], want[fits][None], tol[fits][None])
+        _, dup = qlora.gated_act_bwd(up, gate, up)
+        _close(dup[fits][None], want[fits][None], tol[fits][None])
