@@ -113,7 +113,7 @@ __device__ __forceinline__ void finish8(const GatedOut &out, int64_t to, const f
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const float g0 = v[k][2 * q], g1 = v[k][2 * q + 1], u0 = v[2 + k][2 * q], u1 = v[2 + k][2 * q + 1];
-      h[2 * k + q] = pack_bf16x2(gate_act<kAct>(g0) * u0, gate_act<kAct>(g1) * u1);
+      h[2 * k + q] = pack_bf16x2(gate_act_of_sum<kAct>(g0) * u0, gate_act_of_sum<kAct>(g1) * u1);
       g[2 * k + q] = pack_bf16x2(g0, g1);
       u[2 * k + q] = pack_bf16x2(u0, u1);
     }
@@ -310,8 +310,8 @@ __global__ __launch_bounds__(kThreads, 2) void gated_tiles(GatedTilesArgs a, Gat
   };
   with_activation(out.act, [&](auto act) {
     put([&](int j, int n, int q) {
-      return pack_bf16x2(gate_act<act()>(acc[2 * j][n][q]) * acc[2 * j + 1][n][q],
-                         gate_act<act()>(acc[2 * j][n][q + 1]) * acc[2 * j + 1][n][q + 1]);
+      return pack_bf16x2(gate_act_of_sum<act()>(acc[2 * j][n][q]) * acc[2 * j + 1][n][q],
+                         gate_act_of_sum<act()>(acc[2 * j][n][q + 1]) * acc[2 * j + 1][n][q + 1]);
     });
   });
   each_row([&](int64_t to, const u32x4 &v) {

@@ -343,7 +343,7 @@ __global__ __launch_bounds__(64 * kWaves, TT == 4 ? 3 : 0) void gated_few(GatedF
       } else if (t < a.T) {
         const int64_t to = (int64_t)t * a.N + 16 * (int64_t)blockIdx.x + c;
         with_activation(out.act, [&](auto act) {
-          out.h[to] = __builtin_bit_cast(uint16_t, (__bf16)(gate_act<act()>(gate[h]) * sum));
+          out.h[to] = __builtin_bit_cast(uint16_t, (__bf16)(gate_act_of_sum<act()>(gate[h]) * sum));
         });
         if (out.gate) {
           out.gate[to] = __builtin_bit_cast(uint16_t, (__bf16)gate[h]);

@@ -1061,7 +1061,7 @@ __global__ __launch_bounds__(512) void qgemm_ws(QgemmSet set, int64_t M, const u
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const int at = (wm * 128 + i * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3)) * GLD + wn * 32 + l32;
-          ht[at] = __builtin_bit_cast(uint16_t, (__bf16)(gate_act<act()>(acc[i][0][q]) * acc[i][1][q]));
+          ht[at] = __builtin_bit_cast(uint16_t, (__bf16)(gate_act_of_sum<act()>(acc[i][0][q]) * acc[i][1][q]));
         }
     });
     if (kept) {
