@@ -289,6 +289,10 @@ __global__ __launch_bounds__(block_threads<kRow>()) void rms_norm_bwd(NormBwd p)
     }
     const float outer = rstd * lift;  // 1 / the root of the mean square
     if (!(__builtin_fabsf(c) < __builtin_inff())) c = norm_mean<kRow, V>(s, g, weight, red, outer, p.D);
+    // long rows are unpacked again below: unpacked over the sums they would take twice the registers, and spill
+    if constexpr (V > 2)
+#pragma unroll
+      for (int v = 0; v < V; ++v) asm("" : "+v"(s[v]), "+v"(g[v]));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = lane + v * kRow;
