@@ -546,6 +546,8 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
     g.wd = (uint16_t *)(ws + p.off_w);
     g.packs = (int)cdiv((2 * p.N + (g.up ? p.T : 0)) * (pad / 8), kWide);
     const unsigned blocks = (unsigned)(g.packs + std::min<int64_t>(cdiv(2 * g.chunks, 4 * kWide), 4096));
+    TimedLaunch tl;  // the decode and the product
+    const bool timed = timing_begin(st, tl, kTimedQgemmFwd);
     if (w[0].dq)
       gated_prep<true><<<blocks, kWide, 0, st>>>(g, cb);
     else
@@ -555,6 +557,7 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
     const GatedTilesArgs a{x,     g.up ? g.up : u, g.wd,   g.bp,   p.T,          p.N,   p.K,  pad,
                            nleft, ntoken,          n.full, n.tail, (int)n.steps, scale, qpart};
     gated_tiles<<<(unsigned)(n.full + n.tail * n.splits), kThreads, 0, st>>>(a, out);
+    if (timed) timing_end(st, tl);
     if (n.tail) launch_tail<true>(qpart, n, nleft, ntoken, p.T, p.N, out, st);
     return hipGetLastError();
   }
@@ -563,7 +566,10 @@ hipError_t launch_linear_gated_fwd(const GatedPlan &p, const uint16_t *x, const 
     s.m[i].w = w[i];
     s.m[i].lb = B[i];
   }
+  TimedLaunch tl;
+  const bool timed = timing_begin(st, tl, kTimedQgemmFwd);
   e = launch_qgemm_gated(s, p.T, x, u, p.r, scale, p.rounds, out, qpart, cb, st);
+  if (timed) timing_end(st, tl);
   if (e != hipSuccess) return e;
   if (p.rounds.tail) launch_tail<false>(qpart, p.rounds, (int)(p.N / 64), (int)cdiv(p.T, 256), p.T, p.N, out, st);
   return hipGetLastError();

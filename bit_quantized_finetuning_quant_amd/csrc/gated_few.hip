@@ -563,10 +563,13 @@ hipError_t launch_gated_few(int64_t T, const uint16_t *x, const QWeight *w, cons
     else
       run(std::integral_constant<int, 8>(), dq);
   };
+  TimedLaunch tl;
+  const bool timed = timing_begin(st, tl, kTimedGemvFwd);
   if (w[0].dq)
     with_tiles(std::true_type());
   else
     with_tiles(std::false_type());
+  if (timed) timing_end(st, tl);
   return hipGetLastError();
 }
 

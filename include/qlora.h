@@ -510,9 +510,10 @@ qlora_status qlora_linear_gated_fwd(const uint16_t *x, int64_t T, const qlora_nf
  * on the call's stream.  The events are created by the library (no device
  * memory is allocated).  Not thread-safe: one host thread at a time.        */
 enum {
-  QLORA_TIMED_QGEMM_FWD = 0, /* dequant-fused GEMM, forward: x W_hat^T (+ LoRA)       */
+  QLORA_TIMED_QGEMM_FWD = 0, /* dequant-fused GEMM, forward: x W_hat^T (+ LoRA); gated product T > 128, with the
+                                decode where the weights are decoded first            */
   QLORA_TIMED_QGEMM_DX = 1,  /* dequant-fused GEMM, grad_x: dy W_hat (+ LoRA)         */
-  QLORA_TIMED_GEMV_FWD = 2,  /* few-token forward, weight pass (T <= 16, to 64 by shape) */
+  QLORA_TIMED_GEMV_FWD = 2,  /* few-token forward, weight pass (T <= 16, to 64 by shape; gated product T <= 128) */
   QLORA_TIMED_GEMV_BWD = 3,  /* few-token backward, weight and adapter pass (T <= 2, or 4 by shape; sets T <= 4) */
   QLORA_TIMED_ADAMW = 4,     /* adapter AdamW update, whole 4096-element tiles          */
   QLORA_TIMED_KINDS = 5

@@ -107,3 +107,23 @@ def test_silu_to_a_few_steps_of_fp32():
         _close(h[fits][None], want[fits][None], tol[fits][None])
         _, dup = qlora.gated_act_bwd(up, gate, up)
         _close(dup[fits][None], want[fits][None], tol[fits][None])
+
+
+@gpu
+@pytest.mark.parametrize("T,K,N,kind", [(1, 512, 704, "gemv_fwd"), (40, 512, 704, "gemv_fwd"), (128, 512, 704, "gemv_fwd"),
+                                        (300, 512, 704, "qgemm_fwd"), (129, 2048, 5504, "qgemm_fwd")])
+def test_kernel_timing_sees_the_gated_product(T, K, N, kind):
+    """The product of every form is bracketed, once a call (300 tokens of this size decode first, 129 of 5504 x 2048 do not)."""
+    torch = torch_mod()
+    announce(f"kernel timing of the gated product T={T}")
+    p = _case(T, K, N, 16, T, True)
+    qlora.kernel_timing_read()
+    qlora.kernel_timing_enable(True)
+    try:
+        for _ in range(3):
+            qlora.linear_gated_fwd(*p)
+    finally:
+        qlora.kernel_timing_enable(False)
+        torch.cuda.synchronize()
+        got = qlora.kernel_timing_read()
+    assert {k: n for k, (n, _) in got.items() if n} == {kind: 3} and got[kind][1] > 0
