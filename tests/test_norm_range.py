@@ -75,3 +75,28 @@ def test_the_largest_eps():
     got, gotw = qlora.rms_norm_bwd(p["dy"], s, p["w"], eps, need_grad_weight=True)
     _close(got, gs, ts)
     _close(gotw, gw, tw)
+
+
+@gpu
+@pytest.mark.parametrize("T,D", [(1300, 2048), (1100, 4096), (700, 8192), (520, 16384), (300, 20480), (2500, 1024),
+                                 (4097, 8192)])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_backward_of_several_rows_a_workgroup(T, D, fp32):
+    """More rows than workgroups, some with one row more than others; 4097 x 8192 with dres reads 201 MB, past the
+    caches.  (The rows' order does not change their own gradient: the launch without grad_weight has a workgroup a row.)"""
+    torch = torch_mod()
+    announce(f"norm backward, several rows a workgroup T={T} D={D} fp32={fp32}")
+    p = _inputs(T, D, T + D, fp32)
+    for dres in (p["dres"], None):
+        (gs, ts), (gw, tw) = _grads(p["dy"], p["res"], p["w"], 1e-5, dres)
+        got, gotw = qlora.rms_norm_bwd(p["dy"], p["res"], p["w"], 1e-5, dres=dres, need_grad_weight=True)
+        _close(got, gs, ts)
+        _close(gotw, gw, tw)
+        assert torch.equal(qlora.rms_norm_bwd(p["dy"], p["res"], p["w"], 1e-5, dres=dres)[0], got)
+        assert torch.equal(qlora.rms_norm_bwd(p["dy"], p["res"], p["w"], 1e-5, dres=dres, need_grad_weight=True)[1], gotw)
+
+
+@pytest.mark.parametrize("D", [64, 1024, 1088, 4096, 4160, 8192, 65536])
+def test_workspace_is_at_most_512_rows_of_sums(D):
+    for T in (1, 3, 511, 512, 513, 2047, 2049, 1 << 20, (1 << 37) // D):
+        assert 0 < qlora.rms_norm_bwd_workspace_bytes(T, D) <= 512 * D * 4
