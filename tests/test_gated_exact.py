@@ -6,11 +6,13 @@ that their smallest one gives; A is 0 or +-1/8, so that u is a multiple of 1/8 o
 multiple of 2^-8 of 7 bits and the scale 1/2.  Then gate and up are exact, their bf16 results are those values rounded
 once, and h is off by its activation's error and one rounding: for silu and tanh-gelu as `test_gated.py` derives."""
 
+import numpy as np
 import pytest
 
-from bit_quantized_finetuning_quant_amd import qlora
-from helpers import announce, torch_mod
-from test_gated import E, HALF, TINY, _act, _close
+import oracle
+from bit_quantized_finetuning_quant_amd import qlora, workloads
+from helpers import announce, dev_bf16, dev_f32, host_bits, torch_mod
+from test_gated import ACTS, E, HALF, TINY, _act, _check_product, _close
 
 gpu = pytest.mark.gpu
 
@@ -127,3 +129,92 @@ def test_kernel_timing_sees_the_gated_product(T, K, N, kind):
         torch.cuda.synchronize()
         got = qlora.kernel_timing_read()
     assert {k: n for k, (n, _) in got.items() if n} == {kind: 3} and got[kind][1] > 0
+
+
+# 1 to 64 tokens with x in registers (tiles of 16 tokens: one to four), ranges of n_in (two to eight), the fused tiles,
+# whole and with a last round in ranges, and decoded weights, likewise; ranks with and without padding
+WIDE = [(1, 4096, 11008, 16), (16, 8192, 22016, 16), (20, 4096, 11008, 7), (33, 4096, 11008, 64), (64, 4096, 11008, 16),
+        (20, 8192, 22016, 16), (33, 8192, 22016, 64), (64, 8192, 22016, 16), (90, 4096, 11008, 16), (100, 4096, 11008, 100),
+        (128, 8192, 22016, 64), (129, 4096, 11008, 16), (300, 4096, 11008, 100), (509, 4096, 11008, 64),
+        (700, 8192, 22016, 16), (2048, 4096, 11008, 64), (2047, 4096, 11008, 7), (1500, 8192, 22016, 64)]
+
+
+@gpu
+@pytest.mark.parametrize("T,K,N,r", WIDE)
+def test_model_widths_bit_for_bit(T, K, N, r):
+    torch = torch_mod()
+    act, dq = ACTS[T % 2], T % 3 != 0
+    announce(f"gated block bit for bit T={T} K={K} N={N} r={r} {act} dq={dq}")
+    p = _case(T, K, N, r, T + r, dq)
+    out = qlora.linear_gated_fwd(*p, act, need_act8=True)
+    torch.cuda.synchronize()
+    rows = torch.arange(T) if T <= 128 else torch.cat([torch.arange(64), torch.randperm(T - 128)[:64] + 64, torch.arange(T - 64, T)])
+    _check(p, out, act, rows=rows.cuda())
+    b = qlora.act8_write(out.h)
+    assert torch.equal(out.act8.codes, b.codes) and torch.equal(out.act8.scale, b.scale)
+
+
+@gpu
+@pytest.mark.parametrize("T,K,N", [(1, 8192, 1024), (40, 8192, 1024), (64, 2048, 22016), (16, 65600, 320), (70, 16448, 2112),
+                                   (300, 2112, 576), (513, 1024, 2112), (3000, 1024, 5568), (2049, 2048, 4160)])
+def test_other_sizes_bit_for_bit(T, K, N):
+    torch = torch_mod()
+    r, act, dq = (31, 100, 8)[T % 3], ACTS[T % 2], T % 4 != 0
+    announce(f"gated block bit for bit T={T} K={K} N={N} r={r} {act} dq={dq}")
+    p = _case(T, K, N, r, T + K, dq)
+    out = qlora.linear_gated_fwd(*p, act)
+    torch.cuda.synchronize()
+    rows = torch.arange(T) if T <= 600 else torch.cat([torch.arange(100), torch.arange(T - 100, T)])
+    _check(p, out, act, rows=rows.cuda())
+
+
+def _one_hot(T, width, idx):
+    a = np.zeros((T, width), np.float32)
+    a[np.arange(T), idx] = 1.0
+    return dev_bf16(workloads.to_bf16_bits(a))
+
+
+@gpu
+@pytest.mark.parametrize("double_quant", [True, False])
+@pytest.mark.parametrize("T", [1, 16, 32, 48, 64, 96, 128, 256, 511])
+def test_decoders_every_element(T, double_quant):
+    """Rows of x with a single 1 and A = 0 make gate and up columns of the decoded weights: the oracle's, bit for bit, and h the
+    product of the two.  (T = 1 takes every 16th column.)"""
+    torch = torch_mod()
+    n_out, n_in, r = 512, 1024, 16
+    announce(f"gated block one-hot {n_out}x{n_in} T={T} double_quant={double_quant}")
+    rng = np.random.default_rng(500 + T + double_quant)
+    ws = [(rng.standard_normal((n_out, n_in)) * 0.02).astype(np.float32) for _ in range(2)]
+    qs = [qlora.quantize(dev_f32(w), double_quant=double_quant) for w in ws]
+    whs = [oracle.dequantize(oracle.quantize(w, n_out, n_in, double_quant=double_quant)) for w in ws]
+    Bs = [dev_bf16(workloads.to_bf16_bits((rng.standard_normal((n_out, r)) * 0.1).astype(np.float32))) for _ in range(2)]
+    A = torch.zeros(2 * r, n_in, dtype=torch.bfloat16, device="cuda")
+    cols = rng.permutation(n_in)[:64 if T == 1 else n_in]
+    for part in range(-(-cols.size // T)):
+        ks = cols[part * T:][:T]
+        ks = np.concatenate([ks, cols[:T - ks.size]])
+        out = qlora.linear_gated_fwd(_one_hot(T, n_in, ks), qs, A, Bs, 0.5)
+        assert np.array_equal(host_bits(out.gate), whs[0][:, ks].T), ("gate", part)
+        assert np.array_equal(host_bits(out.up), whs[1][:, ks].T), ("up", part)
+        _check_product(out.h, out.gate, out.up, "silu")
+
+
+@gpu
+@pytest.mark.parametrize("double_quant", [True, False])
+def test_decoder_of_many_tokens_every_element(double_quant):
+    """The form that decodes both weights into the workspace first."""
+    torch = torch_mod()
+    T, K, N, r = 3000, 1024, 5568, 31
+    announce(f"gated block one-hot {N}x{K} T={T} double_quant={double_quant}")
+    assert qlora.linear_gated_workspace_bytes(T, N, K, r) > 4 * N * K
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qs = [qlora.quantize(torch.randn(N, K, generator=g, device="cuda") * 0.02, double_quant=double_quant) for _ in range(2)]
+    ks = torch.randperm(T, device="cuda", generator=g) % K
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    x[torch.arange(T, device="cuda"), ks] = 1.0
+    A = torch.zeros(2 * r, K, dtype=torch.bfloat16, device="cuda")
+    Bs = [torch.randn(N, r, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    out = qlora.linear_gated_fwd(x, qs, A, Bs, 0.5)
+    for q, got in zip(qs, (out.gate, out.up)):
+        assert torch.equal(got, qlora.dequantize(q).t()[ks])
+    _check_product(out.h, out.gate, out.up, "silu")
