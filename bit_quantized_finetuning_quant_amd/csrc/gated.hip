@@ -402,8 +402,11 @@ GatedRounds gated_rounds(int64_t tiles, int64_t steps, double round_us, double s
 }
 
 // The two forms' times in us, fitted to 509 to 4096 tokens of n_ff x n_in = 5504 x 2048, 11008 x 4096 and 22016 x 8192:
-// within 10%, and the faster form everywhere.  (The plain tiles run at the card's power limit: a round of fewer is faster.)  Fused and decoded: 5504 x 2048 1024 tokens 76 and 62, 2048 tokens 123 and 110;
-// 11008 x 4096 509 tokens 124 and 127, 1024 tokens 210 and 199; 22016 x 8192 509 tokens 386 and 488, 1024 tokens 740 and 722.
+// within 10%, and the faster form at these sizes.  The adapter's ranks do not enter (a step for 32 of
+// them in either form, and the decoded form's packed operands), so where they outweigh n_in the other form may be faster.
+// (The plain tiles run at the card's power limit: a round of fewer is faster.)  Fused and decoded: 5504 x 2048 1024 tokens 76
+// and 62, 2048 tokens 123 and 110; 11008 x 4096 509 tokens 124 and 127, 1024 tokens 210 and 199; 22016 x 8192 509 tokens 386 and
+// 488, 1024 tokens 740 and 722.
 constexpr double kFusedRound = 5.0, kFusedStep = 0.98, kPlainRound = 7.0, kPlainStep = 1.235;
 constexpr int64_t kFusedTile = 256 * 128 * 4, kPlainTile = 256 * 256 * 4;
 double fused_us(int64_t T, int64_t N, int64_t K, GatedRounds *rounds) {

@@ -1211,9 +1211,10 @@ def linear_gated_fwd(x, qs, A_set, Bs, scale: float, activation: str = "silu", k
                      act8: Act8 = None, need_act8=False, gate=None, up=None, u_out=None, workspace=None,
                      stream=None) -> Gated:
     """The gated product of a feed-forward block behind its projections: h = bf16(act(gate) up) with gate and up the
-    linear_set_fwd of qs = [gate, up] (both [n_ff x n_in], n_ff % 64 == 0), taken in fp32.  keep: gate, up and u,
-    which the backward pass reads (gated_act_bwd, then linear_set_bwd or linear_set_bwd_act8), are returned too.
-    act8: h's 8-bit checkpoint, where it is given or need_act8; need_h=False leaves out h itself."""
+    linear_set_fwd of qs = [gate, up] (both [n_ff x n_in], n_ff % 64 == 0), taken in fp32; u = x A_set^T is rounded to
+    bf16, as it is returned, before it meets B.  keep: gate, up and u, which the backward pass reads (gated_act_bwd, then
+    linear_set_bwd or linear_set_bwd_act8), are returned too.  act8: h's 8-bit
+    checkpoint, where it is given or need_act8; need_h=False leaves out h itself."""
     torch = _torch()
     code = _activation(activation)
     if len(qs) != 2:

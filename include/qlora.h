@@ -484,19 +484,24 @@ qlora_status qlora_gated_act_bwd(const uint16_t *dh, const uint16_t *gate, const
 /* The gated product behind its projections, for T tokens: the projection set
  * q[0] (gate), q[1] (up) of qlora_linear_set_fwd, with the product formed from
  * the fp32 sums inside it:
- *   u_set = x A_set^T
+ *   u_set = bf16( x A_set^T )
  *   gate  = x W_hat_0^T + scale u_0 B_0^T,   up = x W_hat_1^T + scale u_1 B_1^T
  *   h     = bf16( act(gate) up )             [T x n_ff] and / or its checkpoint *h8
- * gate and up [T x n_ff] are also written, in bf16, where they are given (both
- * or neither): the backward pass, qlora_gated_act_bwd, reads them.  (h is formed
+ * u_set meets B in bf16, as in every linear call here (the backward passes take the
+ * same u).  gate and up [T x n_ff] are also written, in bf16, where they are given
+ * (both or neither): the backward pass, qlora_gated_act_bwd, reads them.  (h is formed
  * before they are rounded, so qlora_gated_act_fwd on them differs from h by
- * their roundings.)  Both weights are [n_ff x n_in] and of one storage form,
- * n_ff % 64 == 0, n_ff and n_in < 2^22, (T / 256 + 1) n_ff / 64 <= 2^22; the rest
- * as qlora_linear_set_fwd with two members.  x, h, gate, up and u_out are buffers
- * of their own (two the same: QLORA_ERR_VALUE).
+ * their roundings.)  A token whose u_set holds an Inf or NaN may have NaN in both
+ * gate and up, whichever member's ranks hold it; other tokens are not touched.
+ * Both weights are [n_ff x n_in] and of one storage form, n_ff % 64 == 0, n_ff and
+ * n_in < 2^22, (T / 256 + 1) n_ff / 64 <= 2^22; the rest as qlora_linear_set_fwd
+ * with two members.  x, h, gate, up and u_out are buffers of their own (two the
+ * same: QLORA_ERR_VALUE).
  * ws: qlora_linear_gated_workspace_bytes, for these sizes (fewer tokens may take
- * another form and need more).  From about a thousand tokens on it holds both
- * decoded weights (4 n_ff n_in bytes, at most 2 GB; longer ones stay packed).  */
+ * another form and need more).  From 129 tokens on, by the sizes (769 of
+ * 11008 x 4096), both weights may be decoded first: then it holds them (4 n_ff n_in
+ * bytes, at most 2 GB; longer ones stay packed) and B in as many columns as both
+ * members' ranks in whole 64s (4 n_ff bytes a column, 8.6 GB at most).          */
 size_t qlora_linear_gated_workspace_bytes(int64_t T, int64_t n_ff, int64_t n_in, int r);
 qlora_status qlora_linear_gated_fwd(const uint16_t *x, int64_t T, const qlora_nf4_weight *q, const uint16_t *A_set,
                                     const uint16_t *const *B, int r, float scale, qlora_activation act, uint16_t *h,

@@ -218,3 +218,27 @@ def test_decoder_of_many_tokens_every_element(double_quant):
     for q, got in zip(qs, (out.gate, out.up)):
         assert torch.equal(got, qlora.dequantize(q).t()[ks])
     _check_product(out.h, out.gate, out.up, "silu")
+
+
+@gpu
+@pytest.mark.parametrize("T,K,N,r", [(3, 256, 320, 16), (40, 256, 320, 16), (100, 256, 320, 16), (300, 256, 320, 16), (300, 256, 320, 100),
+                                     (4096, 64, 5568, 32), (3000, 1024, 5568, 31)])
+def test_an_overflow_in_u_stays_in_its_token(T, K, N, r):
+    """A rank of gate whose u passes bf16's range in one token: gate is not finite there, up is as without it or NaN,
+    and the other tokens are as without it."""
+    torch = torch_mod()
+    announce(f"gated block, u past its range T={T} r={r}")
+    x, qs, A, Bs, k = _case(T, K, N, r, T + r, True)
+    x[:, 0] = 0
+    base = qlora.linear_gated_fwd(x, qs, A, Bs, k)
+    A[3, 0], x[1, 0] = 3e38, 2.0
+    out = qlora.linear_gated_fwd(x, qs, A, Bs, k)
+    x[1, 0] = 2.0
+    A[3, 0] = 0
+    up = qlora.linear_gated_fwd(x, qs, A, Bs, k).up[1]
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[1] = False
+    for name in ("h", "gate", "up", "u"):
+        assert torch.equal(getattr(out, name)[rest], getattr(base, name)[rest]), name
+    assert float(out.u[1, 3]) == float("inf") and not bool(out.gate[1].isfinite().any())
+    assert torch.equal(out.up[1], up) or bool(out.up[1].isnan().all())
