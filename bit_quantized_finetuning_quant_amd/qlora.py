@@ -108,6 +108,10 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m bit_quantized_finetuning_quant_amd.build`")
+        try:
+            _torch()  # first: loaded before it, the library would bring in a HIP runtime beside torch's own
+        except ImportError:
+            pass
         l = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in _SIGNATURES.items():
             f = getattr(l, name)
