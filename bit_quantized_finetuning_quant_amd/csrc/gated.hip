@@ -8,12 +8,13 @@
 // Behind the projections the product takes gate and up in fp32; the bf16 copies
 // of both are what the backward pass reads, and need not be written.
 //
-// The product alone and its backward pass are bound by HBM: 2048 x 11008 with h and its codes written (158 MB) 25 us,
-// 6.3 TB/s (part of it from the last-level cache); the gradients of 4096 x 22016 (902 MB) 135 us, 6.7 TB/s.
+// The product alone and its backward pass are bound by HBM: 2048 x 11008 with h and its codes written (158 MB) 28 us
+// with inputs in turn, 5.6 TB/s (24 at best, part of it from the last-level cache); the gradients of 4096 x 22016 (902 MB) 152
+// us, 5.9 TB/s.
 //
 // Behind the projections there are three forms.  Up to 128 tokens the decode is the work (gated_few.hip).  Then the fused
 // GEMM (qgemm.hip) decodes a weight tile for 256 tokens beside the matrix instructions: 509 tokens of two 11008 x 4096
-// weights 115 us, 0.80 PFLOP/s, bound by the two roles of its waves.  From where that costs less (the forms' times are
+// weights 123 us, 0.75 PFLOP/s, bound by the two roles of its waves.  From where that costs less (the forms' times are
 // estimated in plan_linear_gated) the weights are decoded first.
 
 #include <algorithm>
@@ -143,10 +144,10 @@ __global__ __launch_bounds__(kWide) void gated_reduce(const float *__restrict__ 
 }
 
 // ---- many tokens: decoded weights in the workspace, plain tiles ------------------------------------------------
-// The fused GEMM decodes a weight tile once for every 256 tokens; from some thousand tokens on, decoding each
-// weight once (2.5 bytes a weight at HBM speed) and multiplying on plain 256 x 256 tiles is faster: 2048 tokens of two
-// 11008 x 4096 weights 312 us (the decode 42, 5.4 TB/s), fused 407; 4096 tokens of 22016 x 8192 2.13 ms (164 us; the tiles
-// 2.06 ms at best, 1.43 PFLOP/s), fused 2.98.  Matrix instructions bound the tiles, at the clock that the card's
+// The fused GEMM decodes a weight tile once for every 256 tokens; from some hundred tokens on (769 of two 11008 x 4096 weights),
+// decoding each weight once (2.5 bytes a weight at HBM speed) and multiplying on plain 256 x 256 tiles is faster: 2048 of two
+// 11008 x 4096 weights 342 us (the decode 40, 5.6 TB/s; the tiles 303; u 15), fused 407; 4096 tokens of 22016 x 8192 2.25 ms (the
+// decode 163 us; the tiles 2.05 ms, 1.45 PFLOP/s), fused 2.98.  Matrix instructions bound the tiles, at the clock that the card's
 // power leaves them (a library product of 4096 x 8192 x 44032 runs at 1.5 PFLOP/s).
 
 // What the tiles need beside x, in one launch, whose workgroups take one of two parts:

@@ -7,7 +7,7 @@
 // and r = 1 / (1 + t), sigma and 1 - sigma are r and t r, or t r and r where z < 0: both keep their relative precision on
 // both sides (silu: 9 half steps of fp32 with the products; tanh-gelu as much and those of its z, which weigh |z| times).
 // A gate that is an fp32 sum is itself off by half a step and more, which moves sigma by |z| of them.  There
-// sigma = 1 / (1 + exp2(-z log2 e)), whose rounded argument does as much, in 4 instructions in place of 12: with the others 2048
+// sigma = 1 / (1 + exp2(-z log2 e)), whose rounded argument does as much, in 4 instructions in place of 13: with the others 2048
 // tokens of two 11008 x 4096 weights take 356 us for 350, 512 with their codes 129 for 127.5.
 #pragma once
 

@@ -14,8 +14,9 @@
 // Sums and statistics are fp32; s, y and grad_s round once.
 //
 // What bounds it is HBM, and for few rows the launch.  On this card's 5.35 TB/s of a 512 MB copy: forward 2048 x 4096 with
-// the residual (67 MB) 11.4 us, 5.9 TB/s, 4096 x 8192 in 8 bits too (305 MB) 50; backward 4096 x 8192 with the residual's
-// gradient (268 MB) 46 us, 5.8 TB/s, with the weight's 55 (the launch that adds it 5).  One row of 4096: 3.0 us.
+// the residual (67 MB) 14.0 us with inputs in turn, 4.8 TB/s, and 11.3 where they lie in the last-level cache; 4096 x 8192 in
+// 8 bits too (305 MB) 51; backward 4096 x 8192 with the residual's gradient (268 MB) 51 us, 5.2 TB/s, with the weight's 55 and
+// the launch that adds it 5.  One row of 4096: 2.9 us.
 //
 // Squares past fp32 (a row with |s| > 1.8e19) make the sum infinite, or an eps near fp32's end the mean; the row is
 // then summed again with s scaled by 2^-96.  Only the sums take scaled values (those below 2^-30 lose bits there, which
