@@ -13,9 +13,10 @@
 // What bounds them: the decode's vector instructions and, next to them, HBM.  Two 11008 x 4096 weights (46.5 MB), 1 token:
 // prep 3.6 us, gated_few 16.9 (2.7 TB/s; 4 less with the decode's lookups left out), two 22016 x 8192 (186 MB) 54 at best, 60
 // in the mean (3.1 to 3.4 TB/s; 13 less); the decode is 23 instructions for 8 codes of a lane and 5 for their share of the
-// table, 38 us of the 54 on all SIMDs.  Codes or x a chunk further ahead cost a wave a SIMD and more than they gain (with prep 62 -> 65 us).  gated_split,
-// 64 tokens of 22016 x 8192: 82 us at best, 92 in the mean, of which 43 are the decode's instructions and 21 the products.  The adapter's operands
-// are all asked for at once and before the first codes (one after the other they were 6 us of 33 tokens of 11008 x 4096).
+// table, 38 us of the 54 on all SIMDs.  Codes or x a chunk further ahead cost a wave a SIMD and more than they gain (with
+// prep 62 -> 65 us).  gated_split, 64 tokens of 22016 x 8192: 82 us at best, 92 in the mean, of which 43 are the decode's
+// instructions and 21 the products.  The adapter's operands are all asked for at once and before the first codes (one after
+// the other they were 6 us of 33 tokens of 11008 x 4096).
 //
 // v_mfma_f32_16x16x32_bf16: A lane l holds A[l % 16][8 (l / 16) + 0..7], B lane l holds B[8 (l / 16) + 0..7][l % 16],
 // D register i of lane l is D[4 (l / 16) + i][l % 16].  Which 32 values of the contraction a product takes, and in what

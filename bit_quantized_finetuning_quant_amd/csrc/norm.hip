@@ -192,8 +192,8 @@ struct NormBwd {
   float *part;  // with the weight's gradient: [workgroup][D]
 };
 
-// One row: rstd (of s lifted) and c from the sums of s^2 and w dy s.  false: mean s^2 + eps passes fp32.  (c may do so where its
-// value does not: it is not finite then, and norm_mean forms it.)
+// One row: rstd (of s lifted) and c from the sums of s^2 and w dy s.  false: mean s^2 + eps passes fp32.  (c may do so where
+// its value does not: it is not finite then, and norm_mean forms it.)
 template <int kRow, int V, bool kLifted, typename W>
 __device__ __forceinline__ bool norm_sums(const NormBwd &p, const u32x4 (&s)[V], const u32x4 (&g)[V], const W &weight,
                                           float (*red)[2], float &rstd, float &c) {

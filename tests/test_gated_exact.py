@@ -91,8 +91,8 @@ def test_every_column_of_the_largest_n_ff():
 def test_silu_to_a_few_steps_of_fp32():
     """Every finite gate by every significand of up.  sigma = 1 / (1 + t) or t / (1 + t) with t = e^-|g|: t is exp2 of a
     remainder below 1/2 that is off by e (fma, its constant's low part), with e = 2^-24 half a step of fp32, an
-    instruction of one step (2 e) and an exact power of two: 3 e.  The sum 1 e (of t's error at most all), the reciprocal 2 e, their product 1 e, and
-    the two products of g and up 1 e each: 9 e in all, and half a step of bf16.  Where t is subnormal (g < -87) it is off by
+    instruction of one step (2 e) and an exact power of two: 3 e.  The sum 1 e (of t's error at most all), the reciprocal
+    2 e, their product 1 e, and the two products of g and up 1 e each: 9 e in all, and half a step of bf16.  Where t is subnormal (g < -87) it is off by
     2^-150 at most, twice that with the product that follows."""
     torch = torch_mod()
     announce("silu to a few steps")
@@ -221,8 +221,8 @@ def test_decoder_of_many_tokens_every_element(double_quant):
 
 
 @gpu
-@pytest.mark.parametrize("T,K,N,r", [(3, 256, 320, 16), (40, 256, 320, 16), (100, 256, 320, 16), (300, 256, 320, 16), (300, 256, 320, 100),
-                                     (4096, 64, 5568, 32), (3000, 1024, 5568, 31)])
+@pytest.mark.parametrize("T,K,N,r", [(3, 256, 320, 16), (40, 256, 320, 16), (100, 256, 320, 16), (300, 256, 320, 16),
+                                     (300, 256, 320, 100), (4096, 64, 5568, 32), (3000, 1024, 5568, 31)])
 def test_an_overflow_in_u_stays_in_its_token(T, K, N, r):
     """A rank of gate whose u passes bf16's range in one token: gate is not finite there, up is as without it or NaN,
     and the other tokens are as without it."""
